@@ -183,7 +183,7 @@ def prepare(case, seed):
     else:  # laid out once, as a program that serves 4-bit experts keeps them
         # (16 experts at a time: the intermediate values are in 32 bits)
         parts = [_mx_quantize(p) for p in w.split(16)]
-        s["w"] = torch.cat([p[0] for p in parts])
+        s["w"] = torch.cat([p[0] for p in parts]).to(torch.uint8)
         s["w_scales"] = _tile_scales(torch.cat([p[1] for p in parts]), case["op"] == "up")
     return s
 
