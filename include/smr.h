@@ -166,6 +166,65 @@ typedef struct smr_expert_gemm_args {
                                       t * width + s; 16-byte aligned */
 } smr_expert_gemm_args;
 
+/* MXFP4 (OCP microscaling, E2M1 codes): blocks of 32 consecutive values along
+ * K share a scale 2^(byte - 127) (E8M0, 255 = NaN); a code is sign, then 0,
+ * 0.5, 1, 1.5, 2, 3, 4 or 6, two to a byte, the even value in the low half.
+ * Row-major codes are uint8 [rows, K / 2], row-major scales uint8 [rows, K /
+ * 32]. The scales of a WEIGHT are laid out once by smr_tile_mxfp4_scales:
+ * uint8 [num_experts, tiles, K / 128, 512]; a tile holds 128 weight rows (of a
+ * gated weight 64 features: tile row 32 g + 16 u + i = row u * I + 64 * tile +
+ * 16 g + i, u = 0 gate, 1 up), byte (r % 32) * 16 + (r / 32) * 4 + q of piece
+ * c = scale of block 4 c + q of tile row r; rows past the end hold 0. */
+
+/* The experts' gated product, behind the align: for every routed slot i =
+ * t * width + s with expert e, act[i, f] = silu(g) * u, g = x[t] . w[e, f],
+ * u = x[t] . w[e, I + f] (fp32 accumulation, one rounding to bf16). */
+typedef struct smr_expert_up_args {
+    int32_t num_tokens;            /* T >= 0 */
+    int32_t width;                 /* slots per token (the align's width), >= 1 */
+    int32_t H;                     /* hidden size: multiple of 16 (MXFP4: 128), <= 16384 */
+    int32_t I;                     /* features of the gated product, multiple of 16, <= 16384 */
+    int32_t num_experts;           /* the align's num_experts (or num_physical), 1..1025 */
+    int32_t block_size;            /* A used by the align: 64 or 128 */
+    const void *x;                 /* bf16 [T, ld_x], or MXFP4 codes uint8 [T, H / 2]; 16-byte aligned */
+    int64_t ld_x;                  /* bf16: row stride in elements, >= H, multiple of 8; MXFP4: ignored */
+    const uint8_t *x_scales;       /* MXFP4: uint8 [T, H / 32], 4-byte aligned; NULL: x and w are bf16 */
+    const void *w;                 /* bf16 [num_experts, 2 I, H] (I gate rows, then I up rows), or
+                                      MXFP4 codes uint8 [num_experts, 2 I, H / 2]; 16-byte aligned */
+    const uint8_t *w_scales;       /* MXFP4: tiled scales of the gated weight, 16-byte aligned */
+    const int32_t *sorted_token_ids;  /* the align's outputs (device) */
+    int64_t sorted_cap;            /* length of sorted_token_ids */
+    const int32_t *expert_ids;     /* length >= ceil(sorted_cap / A) */
+    const int32_t *num_tokens_post_padded;
+    void *act;                     /* out: bf16 [T * width, I], 16-byte aligned */
+} smr_expert_up_args;
+
+/* The experts' second product and the weighted sum over a token's slots:
+ * y[i] = x[i] . w[e(i)]^T (fp32 accumulation), out[t] = sum over s, in order,
+ * of topk_weights[t, s] * y[t * width + s], in fp32, rounded to bf16 once (y
+ * is rounded to bf16 in between). A slot whose topk_ids entry is outside [0,
+ * num_logical) contributes nothing. */
+typedef struct smr_expert_down_args {
+    int32_t num_tokens;            /* T >= 0 */
+    int32_t width;                 /* >= 1 */
+    int32_t H;                     /* output features, multiple of 16, <= 16384 */
+    int32_t I;                     /* contraction: multiple of 16 (MXFP4: 128), <= 16384 */
+    int32_t num_experts;           /* 1..1025 */
+    int32_t block_size;            /* 64 or 128 */
+    const void *x;                 /* bf16 [T * width, I], or MXFP4 codes uint8 [T * width, I / 2]; 16-byte aligned */
+    const uint8_t *x_scales;       /* MXFP4: uint8 [T * width, I / 32], 4-byte aligned; NULL: bf16 */
+    const void *w;                 /* bf16 [num_experts, H, I], or MXFP4 codes [num_experts, H, I / 2] */
+    const uint8_t *w_scales;       /* MXFP4: tiled scales of the (plain) weight, 16-byte aligned */
+    const int32_t *topk_ids;       /* int32 [T, width]: the ids that were aligned (logical ones) */
+    const float *topk_weights;     /* fp32 [T, width] */
+    int32_t num_logical;           /* the align's num_experts: ids in [0, num_logical) have a row */
+    const int32_t *sorted_token_ids;
+    int64_t sorted_cap;
+    const int32_t *expert_ids;
+    const int32_t *num_tokens_post_padded;
+    void *out;                     /* out: bf16 [T, H], 16-byte aligned */
+} smr_expert_down_args;
+
 /* M-aware alignment tier (host, no device work): 64 if
  * num_tokens * topk < 128 * num_experts (fewer than one full 128-row block of
  * routed rows per expert), else 128. Returns -1 on non-positive topk or
@@ -254,6 +313,48 @@ SMR_API smr_status smr_route_align_static(const smr_route_args *route, const smr
 SMR_API smr_status smr_expert_gemm(const smr_expert_gemm_args *args, void *workspace, size_t workspace_bytes,
                                    void *stream);
 
+/* The experts' feed-forward behind the align, in bf16 or MXFP4 (see the
+ * argument structs): the gated product, then the second product summed per
+ * token. Both read the align's outputs as smr_expert_gemm does, blocks at or
+ * past num_tokens_post_padded cost nothing, and a block costs its own rows,
+ * not its padding. A slot that the align skipped (an id out of range) gets no
+ * row: its row of act is left as it was, and smr_expert_down leaves it out.
+ * Results do not depend on the launch or on other rows of the batch.
+ * smr_expert_up is one launch, workspace >= 256 bytes; smr_expert_down is two
+ * (the product into the workspace, then the sum), workspace as its _size says.
+ * The first 256 bytes are zeroed once by the caller, as for every workspace;
+ * error bits as for smr_expert_gemm. num_tokens == 0 launches nothing. */
+SMR_API size_t smr_expert_up_workspace_size(const smr_expert_up_args *args);
+SMR_API size_t smr_expert_down_workspace_size(const smr_expert_down_args *args);
+SMR_API smr_status smr_expert_up(const smr_expert_up_args *args, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+SMR_API smr_status smr_expert_down(const smr_expert_down_args *args, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* bf16 [rows, ld_x] to MXFP4 (row-major codes and scales), one launch. The
+ * scale of a block is the smallest power of two with amax <= 6 * scale (2^-127
+ * at the least; byte 0 for a block of zeros), codes are value / scale to the
+ * nearest, ties to the even code; no value saturates ("vLLM #60833
+ * --monokernel decode", Details). A block with a NaN or an infinity gets
+ * scale byte 255 and zero codes. K: multiple of 32, rows * K <= 2^34; ld_x >=
+ * K, multiple of 8; x 16-byte, codes 4-byte aligned. rows == 0: no launch. */
+SMR_API smr_status smr_quantize_mxfp4(const void *x, int64_t rows, int32_t K, int64_t ld_x, uint8_t *codes,
+                                      uint8_t *scales, void *stream);
+/* The bf16 [rows, K] values of row-major codes and scales (exact; a block
+ * with scale byte 255 becomes NaN). codes 4-byte, out 16-byte aligned. A
+ * value that bf16 cannot hold (scale byte 253 or more can exceed it) becomes
+ * infinite. */
+SMR_API smr_status smr_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t K,
+                                        void *out, void *stream);
+/* Row-major scales [num_experts, N, K / 32] of a weight to the tiled layout
+ * (gated: N = 2 I, I gate rows then I up rows; N / 2 a multiple of 16). K:
+ * multiple of 128. Run once per weight. smr_mxfp4_tiled_scale_bytes: its size
+ * (0 on invalid arguments). Both pointers 4-byte aligned (the products ask
+ * 16-byte alignment of the tiled scales). */
+SMR_API size_t smr_mxfp4_tiled_scale_bytes(int32_t num_experts, int32_t N, int32_t K, int32_t gated);
+SMR_API smr_status smr_tile_mxfp4_scales(const uint8_t *scales, int32_t num_experts, int32_t N, int32_t K,
+                                         int32_t gated, uint8_t *tiled, void *stream);
+
 /* Sticky device error word of a workspace: synchronises `stream`, then copies
  * the word to *code_out (0 = no error; bit 0 = an id out of range in align,
  * bit 1 = a bounded wait inside a kernel gave up, bit 2 = an align output
@@ -299,7 +400,8 @@ SMR_API const char *smr_last_error(void);
 SMR_API int32_t smr_version(void);
 
 /* Number of kernels the most recent successful smr_route / smr_align /
- * smr_route_align call on this thread enqueued (0 after a refusal). */
+ * smr_route_align call on this thread enqueued (0 after a refusal); the same for the expert
+ * and MXFP4 entry points. */
 SMR_API int32_t smr_last_launch_count(void);
 
 #ifdef __cplusplus

@@ -1,5 +1,6 @@
 """GB300-native MoE routing front-end: route (gate GEMM, bf16 logits, top-k,
-renormalised softmax, shared slot) and moe_align_block_size.
+renormalised softmax, shared slot), moe_align_block_size and, behind it, the
+experts' feed-forward in bf16 or MXFP4.
 
 Python names mirror the C ABI of include/smr.h; this layer only turns torch
 tensors into pointers, allocates outputs with torch when the caller does not
@@ -9,16 +10,18 @@ raise :class:`SmrUnsupported`, so a caller can take its own fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
 
 from . import _lib
-from ._lib import AlignArgs, ExpertGemmArgs, RouteArgs
+from ._lib import AlignArgs, ExpertDownArgs, ExpertGemmArgs, ExpertUpArgs, RouteArgs
 
 __all__ = [
     "SmrError", "SmrUnsupported", "Workspace", "route", "align", "route_align",
-    "route_align_static", "expert_gemm",
+    "route_align_static", "expert_gemm", "expert_up", "expert_down", "quantize_mxfp4",
+    "dequantize_mxfp4", "tile_mxfp4_scales",
     "select_block_size", "align_capacity", "route_workspace_size", "align_workspace_size",
     "route_align_workspace_size", "get_device_error", "clear_device_error",
     "get_static_device_error", "clear_static_device_error", "test_force_wait_timeout",
@@ -357,6 +360,239 @@ def expert_gemm(hidden, expert_w, sorted_token_ids, expert_ids, num_tokens_post_
     a.out = _ptr(out)
     wp, wn = _workspace(workspace, 256, hidden.device)
     _check(lib.smr_expert_gemm(ctypes.byref(a), wp, wn, _stream_ptr(stream)))
+    return out
+
+
+def _check_cuda(first, *others) -> None:
+    """Every tensor on the first one's CUDA device."""
+    if first.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors must be on one device (got {first.device} and {t.device})")
+
+
+def _stream_of(device, stream):
+    """The stream to launch on, and the context in which to allocate and
+    launch (nothing to enter for the current stream of the current device)."""
+    torch = _torch()
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+        if device.index == torch.cuda.current_device():
+            return s, contextlib.nullcontext()
+    else:
+        s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    return s, torch.cuda.stream(s)
+
+
+_stream_ws = {}
+
+
+def _ffn_workspace(ws, nbytes: int, device, s):
+    """Workspace of the feed-forward entry points: the caller's, or one per
+    device and stream (calls on two streams may overlap). A call that is being
+    captured gets one of its own, which the graph keeps and zeroes itself."""
+    torch = _torch()
+    if ws is None and torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:256].zero_()
+        return ws
+    if ws is None:
+        key = (device.index, s.cuda_stream)
+        ws = _stream_ws.get(key)
+        if ws is None:
+            ws = _stream_ws[key] = Workspace(0, device)
+    return ws.ensure(nbytes) if isinstance(ws, Workspace) else ws
+
+
+def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated):
+    """Checks of a product's operands in either format."""
+    torch = _torch()
+    mx = x_scales is not None
+    if mx != (w_scales is not None):
+        raise ValueError("x_scales and w_scales must both be given (MXFP4) or both be None (bfloat16)")
+    dtype, kdim = (torch.uint8, K // 2) if mx else (torch.bfloat16, K)
+    kind = "uint8 (MXFP4 codes)" if mx else "bfloat16"
+    if x.dtype != dtype or x.dim() != 2 or tuple(x.shape) != (rows, kdim) or (kdim > 1 and x.stride(1) != 1):
+        raise ValueError(f"x must be a {kind} [{rows}, {kdim}] tensor with unit stride along its rows")
+    if w.dtype != dtype or w.dim() != 3 or tuple(w.shape[1:]) != (w_rows, kdim) or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous {kind} [num_experts, {w_rows}, {kdim}] tensor")
+    if mx:
+        if not x.is_contiguous():
+            raise ValueError("MXFP4 codes x must be contiguous")
+        if (x_scales.dtype != torch.uint8 or tuple(x_scales.shape) != (rows, K // 32)
+                or not x_scales.is_contiguous()):
+            raise ValueError(f"x_scales must be a contiguous uint8 [{rows}, {K // 32}] tensor")
+        need = _lib.load().smr_mxfp4_tiled_scale_bytes(w.shape[0], w_rows, K, 1 if gated else 0)
+        if w_scales.dtype != torch.uint8 or not w_scales.is_contiguous() or w_scales.numel() != need:
+            raise ValueError(f"w_scales must be the {need} bytes that tile_mxfp4_scales gives for this weight")
+
+
+def _aligned_inputs(sorted_token_ids, expert_ids, npp, block_size):
+    torch = _torch()
+    for t in (sorted_token_ids, expert_ids, npp):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("sorted_token_ids, expert_ids and num_tokens_post_padded must be contiguous int32 tensors")
+    if block_size > 0 and expert_ids.numel() * block_size < sorted_token_ids.numel():
+        raise ValueError("expert_ids must hold an entry for every block of sorted_token_ids")
+    if npp.numel() < 1:
+        raise ValueError("num_tokens_post_padded must hold one entry")
+
+
+def _output(out, shape, device):
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    if out.dtype != torch.bfloat16 or tuple(out.shape) != tuple(shape) or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous bfloat16 tensor of shape {tuple(shape)}")
+    return out
+
+
+def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, width: int, block_size: int,
+              x_scales=None, w_scales=None, out=None, workspace=None, stream=None):
+    """The experts' gated product behind the align: returns act bf16
+    [num_tokens * width, I], row t * width + s = silu(g) * u with g and u the
+    products of x[t] (bf16 [num_tokens, H]) with the gate rows w[e, :I] and the
+    up rows w[e, I:] (bf16 [num_experts, 2 I, H]) of the slot's expert e.
+    With x_scales and w_scales, x and w are MXFP4 codes (quantize_mxfp4;
+    w_scales laid out by tile_mxfp4_scales(..., gated=True)). Rows of slots
+    that the align skipped are left as they are in `out`."""
+    _disabled()
+    lib = _lib.load()
+    if w.dim() != 3 or w.shape[1] % 2 or x.dim() != 2:
+        raise ValueError("x must be [num_tokens, H] and w [num_experts, 2 I, H]")
+    T, H, I = x.shape[0], x.shape[1] * (1 if x_scales is None else 2), w.shape[1] // 2
+    _product_inputs(x, w, x_scales, w_scales, T, H, 2 * I, True)
+    _aligned_inputs(sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
+    _check_cuda(x, w, x_scales, w_scales, sorted_token_ids, expert_ids, num_tokens_post_padded, out)
+    s, ctx = _stream_of(x.device, stream)
+    with ctx:
+        out = _output(out, (T * int(width), I), x.device)
+        a = ExpertUpArgs()
+        a.num_tokens, a.width, a.H, a.I = T, int(width), H, I
+        a.num_experts, a.block_size = w.shape[0], int(block_size)
+        a.x, a.ld_x, a.x_scales = _ptr(x), (x.stride(0) if T > 1 else H), _ptr(x_scales)
+        a.w, a.w_scales = _ptr(w), _ptr(w_scales)
+        a.sorted_token_ids, a.sorted_cap = _ptr(sorted_token_ids), sorted_token_ids.numel()
+        a.expert_ids, a.num_tokens_post_padded = _ptr(expert_ids), _ptr(num_tokens_post_padded)
+        a.act = _ptr(out)
+        buf = _ffn_workspace(workspace, lib.smr_expert_up_workspace_size(ctypes.byref(a)), x.device, s)
+        _check(lib.smr_expert_up(ctypes.byref(a), buf.data_ptr(), buf.numel() * buf.element_size(), s.cuda_stream))
+    return out
+
+
+def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_tokens_post_padded, *,
+                block_size: int, num_logical: int = 0, x_scales=None, w_scales=None, out=None,
+                workspace=None, stream=None):
+    """The experts' second product, summed per token: returns out bf16
+    [num_tokens, H], out[t] = sum over s of topk_weights[t, s] * (x[t * width +
+    s] . w[e]^T) for the slots' experts e; x bf16 [num_tokens * width, I] (the
+    rows of expert_up), w bf16 [num_experts, H, I], topk_ids and topk_weights
+    [num_tokens, width] as routed. With x_scales and w_scales, x and w are
+    MXFP4 codes. A slot whose id is outside [0, num_logical) contributes
+    nothing (num_logical: the experts that were aligned; num_experts if 0)."""
+    _disabled()
+    torch = _torch()
+    lib = _lib.load()
+    if topk_ids.dtype != torch.int32 or topk_ids.dim() != 2 or not topk_ids.is_contiguous():
+        raise ValueError("topk_ids must be a contiguous int32 [num_tokens, width] tensor")
+    if topk_weights.dtype != torch.float32 or topk_weights.shape != topk_ids.shape or not topk_weights.is_contiguous():
+        raise ValueError("topk_weights must be a contiguous float32 tensor of topk_ids' shape")
+    if w.dim() != 3 or x.dim() != 2:
+        raise ValueError("x must be [num_tokens * width, I] and w [num_experts, H, I]")
+    T, width = topk_ids.shape
+    I, H = x.shape[1] * (1 if x_scales is None else 2), w.shape[1]
+    _product_inputs(x, w, x_scales, w_scales, T * width, I, H, False)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _aligned_inputs(sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
+    _check_cuda(x, w, topk_ids, topk_weights, x_scales, w_scales, sorted_token_ids, expert_ids,
+                num_tokens_post_padded, out)
+    s, ctx = _stream_of(x.device, stream)
+    with ctx:
+        out = _output(out, (T, H), x.device)
+        a = ExpertDownArgs()
+        a.num_tokens, a.width, a.H, a.I = T, width, H, I
+        a.num_experts, a.block_size = w.shape[0], int(block_size)
+        a.x, a.x_scales, a.w, a.w_scales = _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales)
+        a.topk_ids, a.topk_weights = _ptr(topk_ids), _ptr(topk_weights)
+        a.num_logical = int(num_logical) if num_logical else w.shape[0]
+        a.sorted_token_ids, a.sorted_cap = _ptr(sorted_token_ids), sorted_token_ids.numel()
+        a.expert_ids, a.num_tokens_post_padded = _ptr(expert_ids), _ptr(num_tokens_post_padded)
+        a.out = _ptr(out)
+        buf = _ffn_workspace(workspace, lib.smr_expert_down_workspace_size(ctypes.byref(a)), x.device, s)
+        _check(lib.smr_expert_down(ctypes.byref(a), buf.data_ptr(), buf.numel() * buf.element_size(),
+                                   s.cuda_stream))
+    return out
+
+
+def quantize_mxfp4(x, *, codes=None, scales=None, stream=None) -> Tuple:
+    """bf16 x [..., K] to MXFP4: returns (codes uint8 [..., K / 2], scales
+    uint8 [..., K / 32]); see smr_quantize_mxfp4 in include/smr.h. x is
+    contiguous, or 2-D with unit stride along K."""
+    _disabled()
+    torch = _torch()
+    if x.dtype != torch.bfloat16 or x.dim() < 1 or not (x.is_contiguous() or (x.dim() == 2 and x.stride(1) == 1)):
+        raise ValueError("x must be a bfloat16 tensor, contiguous or 2-D with unit stride along its rows")
+    lead, K = tuple(x.shape[:-1]), x.shape[-1]
+    if K < 32 or K % 32:
+        raise ValueError(f"x's last dimension must be a positive multiple of 32 (got {K})")
+    for t, n, name in ((codes, K // 2, "codes"), (scales, K // 32, "scales")):
+        if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != lead + (n,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {lead + (n,)}")
+    _check_cuda(x, codes, scales)
+    rows = x.numel() // K
+    s, ctx = _stream_of(x.device, stream)
+    with ctx:
+        if codes is None:
+            codes = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
+        ld = x.stride(0) if not x.is_contiguous() and rows > 1 else K
+        _check(_lib.load().smr_quantize_mxfp4(_ptr(x), rows, K, ld, _ptr(codes), _ptr(scales), s.cuda_stream))
+    return codes, scales
+
+
+def dequantize_mxfp4(codes, scales, *, out=None, stream=None):
+    """The bf16 values [..., K] of MXFP4 codes [..., K / 2] and row-major
+    scales [..., K / 32] (exact; NaN where the scale byte is 255)."""
+    _disabled()
+    torch = _torch()
+    if codes.dtype != torch.uint8 or codes.dim() < 1 or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous uint8 tensor")
+    lead, K = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
+    if K < 32 or K % 32:
+        raise ValueError(f"codes' last dimension must be a positive multiple of 16 (got {K // 2})")
+    if scales.dtype != torch.uint8 or tuple(scales.shape) != lead + (K // 32,) or not scales.is_contiguous():
+        raise ValueError(f"scales must be a contiguous uint8 tensor of shape {lead + (K // 32,)}")
+    _check_cuda(codes, scales, out)
+    s, ctx = _stream_of(codes.device, stream)
+    with ctx:
+        out = _output(out, lead + (K,), codes.device)
+        _check(_lib.load().smr_dequantize_mxfp4(_ptr(codes), _ptr(scales), codes.numel() * 2 // K, K, _ptr(out),
+                                                s.cuda_stream))
+    return out
+
+
+def tile_mxfp4_scales(scales, *, gated: bool = False, out=None, stream=None):
+    """A weight's row-major scales uint8 [num_experts, N, K / 32] laid out once
+    for expert_up (gated=True: N = 2 I) or expert_down: uint8 [num_experts,
+    tiles, K / 128, 512]."""
+    _disabled()
+    torch = _torch()
+    lib = _lib.load()
+    if scales.dtype != torch.uint8 or scales.dim() != 3 or not scales.is_contiguous():
+        raise ValueError("scales must be a contiguous uint8 [num_experts, N, K / 32] tensor")
+    E, N, K = scales.shape[0], scales.shape[1], 32 * scales.shape[2]
+    shape = (E, -(-N // 128) if not gated else -(-(N // 2) // 64), K // 128, 512)
+    if out is not None and (out.dtype != torch.uint8 or tuple(out.shape) != shape or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous uint8 tensor of shape {shape}")
+    _check_cuda(scales, out)
+    s, ctx = _stream_of(scales.device, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.uint8, device=scales.device)
+        _check(lib.smr_tile_mxfp4_scales(_ptr(scales), E, N, K, 1 if gated else 0, _ptr(out), s.cuda_stream))
     return out
 
 

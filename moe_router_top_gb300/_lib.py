@@ -27,7 +27,9 @@ EXPORTED = (
     "smr_route_align", "smr_get_device_error", "smr_clear_device_error", "smr_status_string",
     "smr_last_error", "smr_version", "smr_last_launch_count", "smr_route_align_static",
     "smr_get_static_device_error", "smr_clear_static_device_error", "smr_test_force_wait_timeout",
-    "smr_expert_gemm",
+    "smr_expert_gemm", "smr_expert_up", "smr_expert_up_workspace_size", "smr_expert_down",
+    "smr_expert_down_workspace_size", "smr_quantize_mxfp4", "smr_dequantize_mxfp4",
+    "smr_mxfp4_tiled_scale_bytes", "smr_tile_mxfp4_scales",
 )
 
 SMR_STALL_NONE = 0
@@ -73,6 +75,32 @@ class ExpertGemmArgs(ctypes.Structure):
     ]
 
 
+class ExpertUpArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32), ("width", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("I", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("x_scales", ctypes.c_void_p),
+        ("w", ctypes.c_void_p), ("w_scales", ctypes.c_void_p),
+        ("sorted_token_ids", ctypes.c_void_p), ("sorted_cap", ctypes.c_int64),
+        ("expert_ids", ctypes.c_void_p), ("num_tokens_post_padded", ctypes.c_void_p),
+        ("act", ctypes.c_void_p),
+    ]
+
+
+class ExpertDownArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32), ("width", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("I", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("x_scales", ctypes.c_void_p),
+        ("w", ctypes.c_void_p), ("w_scales", ctypes.c_void_p),
+        ("topk_ids", ctypes.c_void_p), ("topk_weights", ctypes.c_void_p),
+        ("num_logical", ctypes.c_int32),
+        ("sorted_token_ids", ctypes.c_void_p), ("sorted_cap", ctypes.c_int64),
+        ("expert_ids", ctypes.c_void_p), ("num_tokens_post_padded", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -110,6 +138,17 @@ def load(path: str = LIB_PATH):
             "smr_test_force_wait_timeout": ([i32, i64], ctypes.c_int),
             "smr_expert_gemm": ([ctypes.POINTER(ExpertGemmArgs), P, sz, P], ctypes.c_int),
         }
+        UA, DA = ctypes.POINTER(ExpertUpArgs), ctypes.POINTER(ExpertDownArgs)
+        sigs.update({
+            "smr_expert_up_workspace_size": ([UA], sz),
+            "smr_expert_down_workspace_size": ([DA], sz),
+            "smr_expert_up": ([UA, P, sz, P], ctypes.c_int),
+            "smr_expert_down": ([DA, P, sz, P], ctypes.c_int),
+            "smr_quantize_mxfp4": ([P, i64, i32, i64, P, P, P], ctypes.c_int),
+            "smr_dequantize_mxfp4": ([P, P, i64, i32, P, P], ctypes.c_int),
+            "smr_mxfp4_tiled_scale_bytes": ([i32, i32, i32, i32], sz),
+            "smr_tile_mxfp4_scales": ([P, i32, i32, i32, i32, P, P], ctypes.c_int),
+        })
         for name, (argtypes, restype) in sigs.items():
             fn = getattr(lib, name)
             fn.argtypes = argtypes

@@ -382,6 +382,104 @@ smr_status run_route(const smr_route_args *a, void *ws, cudaStream_t stream,
     return SMR_OK;
 }
 
+// --- the experts' feed-forward ------------------------------------------------
+
+// smr_expert_down keeps its rows behind the part of a workspace where a small
+// route keeps its tagged keys (at most 16 tokens x 1024 experts): that route
+// takes a word there for its own once the tag matches, so no other data may
+// land on it when calls of both share a workspace.
+constexpr size_t kDownRowsOffset = kHeaderBytes + (size_t)smr::kSmallMaxM * kMaxExperts * 8;
+
+// What both products' arguments have in common.
+struct FfnCheck {
+    int num_tokens, width, K, feat, num_experts, block_size;
+    const char *k_name, *feat_name;
+    const void *x, *w;
+    const uint8_t *x_scales, *w_scales;
+    const int32_t *sorted, *eids, *npp;
+    int64_t sorted_cap;
+    const void *out;
+    const char *out_name;
+    bool gated;
+};
+
+void check_ffn(const FfnCheck &c, Reasons &r) {
+    const bool mx = c.x_scales != nullptr;
+    if (c.num_tokens < 0) r.bad("num_tokens must be >= 0 (got " + std::to_string(c.num_tokens) + ")");
+    if (c.width < 1) r.bad("width must be >= 1 (got " + std::to_string(c.width) + ")");
+    const int step = mx ? 128 : 16;
+    if (c.K < step || c.K > kMaxH || c.K % step != 0)
+        r.bad(std::string(c.k_name) + " must be a multiple of " + std::to_string(step) + " in [" +
+              std::to_string(step) + ", 16384] (got " + std::to_string(c.K) + ")");
+    if (c.feat < 16 || c.feat > kMaxH || c.feat % 16 != 0)
+        r.bad(std::string(c.feat_name) + " must be a multiple of 16 in [16, 16384] (got " + std::to_string(c.feat) + ")");
+    if (c.num_experts < 1 || c.num_experts > kMaxExperts + 1)
+        r.bad("num_experts must be in [1, 1025] (got " + std::to_string(c.num_experts) + ")");
+    if (c.block_size != 64 && c.block_size != 128)
+        r.unsup("block_size must be 64 or 128 (got " + std::to_string(c.block_size) + ")");
+    if ((c.x_scales == nullptr) != (c.w_scales == nullptr))
+        r.bad("x_scales and w_scales must both be set (MXFP4) or both be NULL (bf16)");
+    if (c.num_tokens < 1 || !r.invalid.empty()) return;
+    const int64_t numel = (int64_t)c.num_tokens * c.width;
+    if (!c.x || !aligned(c.x, 16)) r.bad("x must be a 16-byte aligned pointer");
+    if (!c.w || !aligned(c.w, 16)) r.bad("w must be a 16-byte aligned pointer");
+    if (c.x_scales && !aligned(c.x_scales, 4)) r.bad("x_scales must be 4-byte aligned");
+    if (c.w_scales && !aligned(c.w_scales, 16)) r.bad("w_scales must be 16-byte aligned");
+    if (!c.sorted || !c.eids || !c.npp)
+        r.bad("sorted_token_ids, expert_ids and num_tokens_post_padded must be set");
+    else if (!aligned(c.sorted, 4) || !aligned(c.eids, 4) || !aligned(c.npp, 4))
+        r.bad("sorted_token_ids, expert_ids and num_tokens_post_padded must be 4-byte aligned");
+    if (!c.out || !aligned(c.out, 16)) r.bad(std::string(c.out_name) + " must be a 16-byte aligned pointer");
+    if (c.sorted_cap < 1) r.bad("sorted_cap must be >= 1");
+    if (numel > (int64_t)1 << 30) r.unsup("num_tokens * width must be <= 2^30");
+    if (c.sorted_cap > INT32_MAX) r.unsup("sorted_cap exceeds int32 indexing");
+    else if (r.ok()) {
+        const int64_t tiles = c.gated ? (c.feat + 63) / 64 : (c.feat + 127) / 128;
+        if ((c.sorted_cap + c.block_size - 1) / c.block_size * tiles > (int64_t)1 << 30)
+            r.unsup("blocks x weight tiles must be <= 2^30");
+    }
+}
+
+FfnCheck up_check(const smr_expert_up_args *a) {
+    return FfnCheck{a->num_tokens, a->width, a->H, a->I, a->num_experts, a->block_size, "H", "I", a->x, a->w,
+                    a->x_scales, a->w_scales, a->sorted_token_ids, a->expert_ids, a->num_tokens_post_padded,
+                    a->sorted_cap, a->act, "act", true};
+}
+FfnCheck down_check(const smr_expert_down_args *a) {
+    return FfnCheck{a->num_tokens, a->width, a->I, a->H, a->num_experts, a->block_size, "I", "H", a->x, a->w,
+                    a->x_scales, a->w_scales, a->sorted_token_ids, a->expert_ids, a->num_tokens_post_padded,
+                    a->sorted_cap, a->out, "out", false};
+}
+
+smr::FfnLaunch ffn_launch(const FfnCheck &c, void *ws) {
+    smr::FfnLaunch L{};
+    L.x = c.x;
+    L.x_scales = c.x_scales;
+    L.w = c.w;
+    L.w_scales = c.w_scales;
+    L.gated = c.gated;
+    L.width = c.width;
+    L.K = c.K;
+    L.feat = c.feat;
+    L.A = c.block_size;
+    L.num_experts = c.num_experts;
+    L.numel = (int64_t)c.num_tokens * c.width;
+    L.ld_x = c.K;
+    L.sorted = c.sorted;
+    L.sorted_cap = c.sorted_cap;
+    L.eids = c.eids;
+    L.npp = c.npp;
+    L.hdr = ws;
+    return L;
+}
+
+// Rows and columns of an MXFP4 matrix.
+void check_mx_shape(int64_t rows, int32_t K, Reasons &r) {
+    if (rows < 0) r.bad("rows must be >= 0 (got " + std::to_string(rows) + ")");
+    if (K < 32 || K % 32 != 0) r.bad("K must be a positive multiple of 32 (got " + std::to_string(K) + ")");
+    else if (rows > ((int64_t)1 << 34) / K) r.unsup("rows * K must be <= 2^34");
+}
+
 }  // namespace
 
 namespace smr {
@@ -611,6 +709,146 @@ SMR_API smr_status smr_expert_gemm(const smr_expert_gemm_args *a, void *workspac
     L.hdr = workspace;
     cudaError_t e = smr::launch_expert_gemm(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("expert GEMM launch", e);
+    g_last_launches = 1;
+    return SMR_OK;
+}
+
+SMR_API size_t smr_expert_up_workspace_size(const smr_expert_up_args *args) { return args ? kHeaderBytes : 0; }
+
+SMR_API size_t smr_expert_down_workspace_size(const smr_expert_down_args *args) {
+    if (!args) return 0;
+    if (args->num_tokens < 1 || args->width < 1 || args->H < 1) return kHeaderBytes;
+    return kDownRowsOffset + round_up((size_t)args->num_tokens * (size_t)args->width * (size_t)args->H * 2, kWsAlign);
+}
+
+SMR_API smr_status smr_expert_up(const smr_expert_up_args *a, void *workspace, size_t workspace_bytes, void *stream) {
+    g_last_launches = 0;
+    if (!a) {
+        g_last_error = "smr_expert_up: args is NULL";
+        return SMR_ERR_INVALID_ARG;
+    }
+    Reasons r;
+    const FfnCheck c = up_check(a);
+    check_ffn(c, r);
+    if (!a->x_scales && a->num_tokens > 0 && (a->ld_x < a->H || a->ld_x % 8 != 0))
+        r.bad("ld_x must be >= H and a multiple of 8 (got " + std::to_string(a->ld_x) + ")");
+    if (!r.ok()) return r.finish("smr_expert_up");
+    if (a->num_tokens == 0) return SMR_OK;
+    smr_status st = check_ws(workspace, workspace_bytes, kHeaderBytes, "smr_expert_up");
+    if (st != SMR_OK) return st;
+    if ((st = check_device()) != SMR_OK) return st;
+    smr::FfnLaunch L = ffn_launch(c, workspace);
+    if (!a->x_scales) L.ld_x = a->ld_x;
+    L.out = static_cast<uint16_t *>(a->act);
+    const cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("expert up launch", e);
+    g_last_launches = 1;
+    return SMR_OK;
+}
+
+SMR_API smr_status smr_expert_down(const smr_expert_down_args *a, void *workspace, size_t workspace_bytes,
+                                   void *stream) {
+    g_last_launches = 0;
+    if (!a) {
+        g_last_error = "smr_expert_down: args is NULL";
+        return SMR_ERR_INVALID_ARG;
+    }
+    Reasons r;
+    const FfnCheck c = down_check(a);
+    check_ffn(c, r);
+    if (a->num_logical < 1 || a->num_logical > kMaxExperts + 1)
+        r.bad("num_logical must be in [1, 1025] (got " + std::to_string(a->num_logical) + ")");
+    if (a->num_tokens > 0) {
+        if (!a->topk_ids || !aligned(a->topk_ids, 4)) r.bad("topk_ids must be a 4-byte aligned pointer");
+        if (!a->topk_weights || !aligned(a->topk_weights, 4)) r.bad("topk_weights must be a 4-byte aligned pointer");
+        if ((int64_t)a->num_tokens * a->H > (int64_t)1 << 33) r.unsup("num_tokens * H must be <= 2^33");
+    }
+    if (!r.ok()) return r.finish("smr_expert_down");
+    if (a->num_tokens == 0) return SMR_OK;
+    smr_status st = check_ws(workspace, workspace_bytes, smr_expert_down_workspace_size(a), "smr_expert_down");
+    if (st != SMR_OK) return st;
+    if ((st = check_device()) != SMR_OK) return st;
+    smr::FfnLaunch L = ffn_launch(c, workspace);
+    L.out = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(workspace) + kDownRowsOffset);
+    cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("expert down launch", e);
+    const smr::CombineLaunch cl{L.out, a->topk_ids, a->topk_weights, static_cast<uint16_t *>(a->out), a->num_tokens,
+                                a->width, a->H, a->num_logical};
+    e = smr::launch_expert_combine(cl, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("expert combine launch", e);
+    g_last_launches = 2;
+    return SMR_OK;
+}
+
+SMR_API smr_status smr_quantize_mxfp4(const void *x, int64_t rows, int32_t K, int64_t ld_x, uint8_t *codes,
+                                      uint8_t *scales, void *stream) {
+    g_last_launches = 0;
+    Reasons r;
+    check_mx_shape(rows, K, r);
+    if (ld_x < K || ld_x % 8 != 0)
+        r.bad("ld_x must be >= K and a multiple of 8 (got " + std::to_string(ld_x) + ")");
+    if (rows > 0) {
+        if (!x || !aligned(x, 16)) r.bad("x must be a 16-byte aligned pointer");
+        if (!codes || !aligned(codes, 4)) r.bad("codes must be a 4-byte aligned pointer");
+        if (!scales) r.bad("scales is NULL");
+    }
+    if (!r.ok()) return r.finish("smr_quantize_mxfp4");
+    if (rows == 0) return SMR_OK;
+    const smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    const cudaError_t e = smr::launch_quantize_mxfp4(static_cast<const uint16_t *>(x), rows, K, ld_x, codes, scales,
+                                                     static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("MXFP4 quantise launch", e);
+    g_last_launches = 1;
+    return SMR_OK;
+}
+
+SMR_API smr_status smr_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int32_t K,
+                                        void *out, void *stream) {
+    g_last_launches = 0;
+    Reasons r;
+    check_mx_shape(rows, K, r);
+    if (rows > 0) {
+        if (!codes || !aligned(codes, 4)) r.bad("codes must be a 4-byte aligned pointer");
+        if (!scales) r.bad("scales is NULL");
+        if (!out || !aligned(out, 16)) r.bad("out must be a 16-byte aligned pointer");
+    }
+    if (!r.ok()) return r.finish("smr_dequantize_mxfp4");
+    if (rows == 0) return SMR_OK;
+    const smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    const cudaError_t e = smr::launch_dequantize_mxfp4(codes, scales, rows, K, static_cast<uint16_t *>(out),
+                                                       static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("MXFP4 dequantise launch", e);
+    g_last_launches = 1;
+    return SMR_OK;
+}
+
+SMR_API size_t smr_mxfp4_tiled_scale_bytes(int32_t num_experts, int32_t N, int32_t K, int32_t gated) {
+    if (num_experts < 1 || N < 1 || K < 128 || K % 128 != 0 || (gated != 0 && gated != 1) || (gated && N % 32 != 0))
+        return 0;
+    return (size_t)num_experts * (size_t)smr::mxfp4_weight_tiles(N, gated != 0) * (size_t)(K / 128) * 512;
+}
+
+SMR_API smr_status smr_tile_mxfp4_scales(const uint8_t *scales, int32_t num_experts, int32_t N, int32_t K,
+                                         int32_t gated, uint8_t *tiled, void *stream) {
+    g_last_launches = 0;
+    Reasons r;
+    if (num_experts < 1 || num_experts > kMaxExperts + 1)
+        r.bad("num_experts must be in [1, 1025] (got " + std::to_string(num_experts) + ")");
+    if (K < 128 || K > kMaxH || K % 128 != 0)
+        r.bad("K must be a multiple of 128 in [128, 16384] (got " + std::to_string(K) + ")");
+    if (gated != 0 && gated != 1) r.bad("gated must be 0 or 1 (got " + std::to_string(gated) + ")");
+    if (N < 1 || N > 2 * kMaxH || (gated == 1 && N % 32 != 0))
+        r.bad("N must be in [1, 32768], of a gated weight a multiple of 32 (got " + std::to_string(N) + ")");
+    if (!scales || !aligned(scales, 4)) r.bad("scales must be a 4-byte aligned pointer");
+    if (!tiled || !aligned(tiled, 4)) r.bad("tiled must be a 4-byte aligned pointer");
+    if (!r.ok()) return r.finish("smr_tile_mxfp4_scales");
+    const smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    const cudaError_t e = smr::launch_tile_mxfp4_scales(scales, num_experts, N, K, gated != 0, tiled,
+                                                        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("MXFP4 scale layout launch", e);
     g_last_launches = 1;
     return SMR_OK;
 }

@@ -1,0 +1,649 @@
+// smr_ffn.cu -- the experts' feed-forward behind the align: the gated product
+// (act = silu(x Wg^T) * (x Wu^T)) and the product that follows it, whose rows
+// are summed per token with the router's weights; operands in bf16 or MXFP4.
+//
+// The products are computed transposed: the tensor core's M rows are 128 rows
+// of an expert's weights and its N columns are the routed rows of one aligned
+// block (16 to 128, only as many as the block holds, in steps of 16). From one
+// token to a couple of thousand the time is the touched experts' weights out
+// of HBM, whatever the tile; this orientation streams each weight tile once
+// per block at full MMA width, and a block with three rows costs N = 16
+// columns instead of A padded rows. The ragged dimension has the fine step.
+//
+// GB300 design: one persistent CTA per SM over (block, weight tile) items,
+// tiles of one block next to each other (its rows stay in L2; blocks of one
+// expert follow each other, so its weights do too). Warp roles: 0 loads the
+// weights by TMA, 1 issues the MMAs, 2-5 load the routed rows (and their block
+// scales) with asynchronous 16-byte copies, 6-9 drain TMEM. (A TMA gather
+// takes 4 rows an instruction and about 70 cycles each: 128 rows took 2300
+// cycles a k-block, 3300 us for 16384 tokens.) The stage ring runs across
+// items; accumulators are double-buffered in TMEM, so the epilogue of one item
+// runs under the loads and MMAs of the next.
+// Every wait is bounded; a wait that gives up sets the workspace's error bit.
+#include <cudaTypedefs.h>
+
+#include "smr_device.cuh"
+#include "smr_launch.h"
+
+namespace smr {
+
+constexpr int kFfLoaders = 4;                    // warps that load the routed rows
+constexpr int kFfThreads = 32 * (2 + kFfLoaders + 4);
+constexpr int kFfRows = 128;                     // weight rows of a tile (the MMA's M)
+constexpr int kFfRowBytes = 128;                 // one k-block of a row: 64 bf16 or 256 MXFP4
+constexpr int kFfWBytes = kFfRows * kFfRowBytes;  // weight tile of a stage
+constexpr int kFfMaxStages = 9;
+constexpr int kFfInfos = 3;                      // items whose rows are known ahead of the epilogue
+constexpr int kSfAtom = 512;                     // scales of 128 rows x 4 blocks (128 values of K)
+
+// What the producer tells the other warps about an item.
+struct FfInfo {
+    int n;       // MMA columns (16..128), 0: nothing to do
+    int nt;      // weight tile
+    int pad[2];
+    int slot[128];  // flat slot of every column, -1: none
+};
+constexpr int kFfBars = 2 * kFfMaxStages + 4 + 2 * kFfInfos + 1;
+constexpr int kFfMiscBytes = (kFfBars * 8 + 8 + 15) / 16 * 16 + kFfInfos * (int)sizeof(FfInfo);
+
+struct FfParams {
+    int num_kb, last_steps;  // k-blocks; MMA steps of the last one (4 in the others)
+    int feat, ntiles;        // output features; weight tiles
+    const uint8_t *x;
+    int64_t x_row_bytes;     // between rows of x
+    int x_bytes;             // of a row of x
+    int div;                 // row of x = slot / div (the width for the gated product, else 1)
+    int num_experts, A, stages, tmem_cols;
+    int64_t sorted_cap;
+    int numel, max_blocks;
+    const int32_t *sorted, *eids, *npp;
+    uint16_t *out;           // bf16 [numel, feat]
+    const uint8_t *x_scales, *w_scales;  // MXFP4
+    int num_chunks;          // MXFP4: K / 128
+    uint32_t *err;
+    uint32_t stage_bytes, b_bytes;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int c0, int c3, int c4,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(0), "r"(c3), "r"(c4), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on the barrier once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// MXFP4 instruction descriptor (kind::mxf4): A and B E2M1 (bits 7-9, 10-11 =
+// 1), scales UE8M0 (bit 23), N >> 3 in bits 17-22, M >> 7 in bits 27-28; the
+// byte of a scale column where the step's two scales start (0 or 2) in bits
+// 4-5 (B) and 29-30 (A).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27);
+}
+// D[tmem] (+)= (A * scale_A) (B * scale_B)^T, 4-bit operands, one scale per 32
+// values of K, fp32 accumulation.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+}
+// 512 bytes of scales (32 rows of 16 bytes) into 4 TMEM columns, the same in
+// every quarter of the lanes. Ordered before the MMAs that this thread issues
+// next, and behind those that it issued.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t saddr) {
+    // no swizzle, 8-row groups 128 bytes apart (stride byte offset >> 4 in
+    // bits 32-45), descriptor version 1
+    const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1 << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// silu(g) * u in fp32, rounded to bf16 once. The fast exponential and
+// division are within a few 2^-23 of the exact value, far below the rounding.
+__device__ __forceinline__ uint16_t swiglu_bf16(float g, float u) {
+    const float a = __fdividef(g, 1.0f + __expf(-g)) * u;
+    return __bfloat16_as_ushort(__float2bfloat16_rn(a));
+}
+
+// Position in a ring of barriers: index and the parity of its current use.
+struct RingPos {
+    int i = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+// MX: MXFP4 operands, else bf16. UP: the gated product (a tile holds 64
+// features: 16 gate rows and their 16 up rows in turn, so that both halves of
+// a feature are in one warp's TMEM lanes), else 128 plain rows.
+template <bool MX, bool UP>
+__global__ void __launch_bounds__(kFfThreads, 1)
+expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const int ST = p.stages;
+    uint8_t *misc = smem + (size_t)ST * p.stage_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // the stage's operands landed
+    uint64_t *empty = full + kFfMaxStages;                 // the MMAs are done with the stage
+    uint64_t *acc_full = empty + kFfMaxStages;             // an item's accumulator is complete
+    uint64_t *acc_empty = acc_full + 2;                    // it has been read
+    uint64_t *info_full = acc_empty + 2;
+    uint64_t *info_empty = info_full + kFfInfos;
+    uint64_t *last = info_empty + kFfInfos;                // every MMA issued is done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(last + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    FfInfo *info = reinterpret_cast<FfInfo *>(misc + (kFfBars * 8 + 8 + 15) / 16 * 16);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(smem_u32(&full[s]), 1 + 32 * kFfLoaders);  // the weights' bytes, the row loaders
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&acc_full[s]), 1);
+            mbar_init(smem_u32(&acc_empty[s]), 4);
+        }
+        for (int s = 0; s < kFfInfos; ++s) {
+            mbar_init(smem_u32(&info_full[s]), 1);
+            mbar_init(smem_u32(&info_empty[s]), 1 + kFfLoaders + 4);  // issuer, row loaders, epilogue
+        }
+        mbar_init(smem_u32(last), 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+        prefetch_tensormap(&tm_w);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), (uint32_t)p.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_launch_dependents();
+    griddep_wait();  // the align's outputs and x come from previous kernels
+
+    const int nblk = min(__ldcg(p.npp) / p.A, p.max_blocks);
+    const int items = nblk > 0 ? nblk * p.ntiles : 0;
+    const uint32_t ring = smem_u32(smem);
+    int issued = 0;  // stages whose loads were issued (producer warp)
+
+    if (warp == 0) {
+        // ---------------------------------------------------- weights ----
+        const int A = p.A;
+        int ent[4], e = -1;
+        // the item's expert and this lane's 4 entries of its block, requested
+        // an item ahead
+        auto fetch = [&](int it) {
+            if (it >= items) return;
+            const int b = it / p.ntiles;
+            e = __ldcg(p.eids + b);
+            if (4 * lane < A) {
+                const int64_t at = (int64_t)b * A + 4 * lane;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ent[j] = at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
+            }
+        };
+        RingPos st, iq;
+        fetch(blockIdx.x);
+        for (int it = blockIdx.x; it < items; it += gridDim.x) {
+            const int nt = it % p.ntiles;
+            const int ex = e;
+            int slot[4], top = 0;
+            if (4 * lane < A) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = ent[j];
+                    const bool real = (uint32_t)i < (uint32_t)p.numel;
+                    // neither a slot nor the sentinel: a corrupted align output
+                    if (!real && i != p.numel) set_error(p.err, kErrBadSlot);
+                    slot[j] = real ? i : -1;
+                    if (real) top = 4 * lane + j + 1;
+                }
+            }
+            __syncwarp();
+            const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
+            int n = (rows + 15) & ~15;
+            if ((unsigned)ex >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
+                if (lane == 0) set_error(p.err, kErrBadId);
+                n = 0;
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&info_empty[iq.i]), iq.ph ^ 1u, abort_flag))) break;
+            FfInfo *inf = info + iq.i;
+            if (4 * lane < A) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) inf->slot[4 * lane + j] = slot[j];
+            }
+            if (lane == 0) {
+                inf->n = n;
+                inf->nt = nt;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&info_full[iq.i]));
+            iq.next(kFfInfos);
+            fetch(it + gridDim.x);
+            if (n == 0) continue;
+            bool ok = true;
+            if (lane == 0) {
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    if (!(ok = mbar_wait_bounded(smem_u32(&empty[st.i]), st.ph ^ 1u, abort_flag))) break;
+                    const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
+                    const uint32_t bar = smem_u32(&full[st.i]);
+                    const int xk = kb * (MX ? kFfRowBytes : kFfRowBytes / 2);
+                    if constexpr (MX) {
+                        const int c = 2 * kb;
+                        const uint32_t sbytes = (uint32_t)min(2, p.num_chunks - c) * kSfAtom;
+                        mbar_arrive_expect_tx(bar, kFfWBytes + sbytes);
+                        bulk_load(base + kFfWBytes + p.b_bytes,
+                                  p.w_scales + (((int64_t)ex * p.ntiles + nt) * p.num_chunks + c) * kSfAtom, sbytes, bar);
+                    } else {
+                        mbar_arrive_expect_tx(bar, kFfWBytes);
+                    }
+                    if constexpr (UP) tma_load_5d(base, &tm_w, xk, nt * 4, ex, bar);
+                    else tma_load_3d(base, &tm_w, xk, nt * kFfRows, ex, bar);
+                    ++issued;
+                    st.next(ST);
+                }
+            }
+            if (!__shfl_sync(0xffffffffu, (int)ok, 0)) break;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------- MMAs ----
+        if (lane == 0) {
+            RingPos st, iq, ac;
+            uint32_t sfbuf = 0;
+            bool ok = true;
+            for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+                if (!(ok = mbar_wait_bounded(smem_u32(&info_full[iq.i]), iq.ph, abort_flag))) break;
+                const int n = reinterpret_cast<volatile FfInfo *>(info)[iq.i].n;
+                mbar_arrive(smem_u32(&info_empty[iq.i]));
+                iq.next(kFfInfos);
+                if (n == 0) continue;
+                if (!(ok = mbar_wait_bounded(smem_u32(&acc_empty[ac.i]), ac.ph ^ 1u, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + (uint32_t)(ac.i * p.A);
+                const uint32_t idesc = MX ? idesc_mxf4(kFfRows, n) : idesc_bf16_f32(kFfRows, n);
+                for (int kb = 0; kb < p.num_kb; ++kb) {
+                    if (!(ok = mbar_wait_bounded(smem_u32(&full[st.i]), st.ph, abort_flag))) break;
+                    // the loaders' copies were written through the generic
+                    // proxy; the tensor core reads through the async one
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tc_fence_after();
+                    const uint32_t a = ring + (uint32_t)st.i * p.stage_bytes, b = a + kFfWBytes;
+                    const int steps = kb + 1 == p.num_kb ? p.last_steps : 4;
+                    if constexpr (MX) {
+                        // two sets of scale columns in turn: [A 8][B 8]
+                        const uint32_t sf = tmem + (uint32_t)(2 * p.A) + sfbuf * 16u;
+                        const uint32_t sa = b + p.b_bytes, sb = sa + 2 * kSfAtom;
+                        sfbuf ^= 1u;
+                        for (int c = 0; c < (steps + 1) / 2; ++c) {
+                            tc_cp_scales(sf + c * 4, sa + c * kSfAtom);
+                            tc_cp_scales(sf + 8 + c * 4, sb + c * kSfAtom);
+                        }
+                        for (int kk = 0; kk < steps; ++kk) {
+                            const uint32_t id = idesc | ((uint32_t)(kk & 1) << 30) | ((uint32_t)(kk & 1) << 5);
+                            tc_mma_mxf4(acc, smem_desc_sw<128>(a + kk * 32), smem_desc_sw<128>(b + kk * 32), id,
+                                        sf + (kk >> 1) * 4, sf + 8 + (kk >> 1) * 4, (kb | kk) != 0 ? 1u : 0u);
+                        }
+                    } else {
+                        for (int kk = 0; kk < steps; ++kk)
+                            tc_mma_bf16(acc, smem_desc_sw<128>(a + kk * 32), smem_desc_sw<128>(b + kk * 32), idesc,
+                                        (kb | kk) != 0 ? 1u : 0u);
+                    }
+                    tc_commit(smem_u32(&empty[st.i]));
+                    st.next(ST);
+                }
+                if (!ok) break;
+                tc_commit(smem_u32(&acc_full[ac.i]));
+                ac.next(2);
+            }
+            // every MMA issued is done before TMEM is freed, also after an abort
+            tc_commit(smem_u32(last));
+            volatile int never = 0;
+            if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
+        }
+        __syncwarp();
+    } else if (warp < 2 + kFfLoaders) {
+        // ------------------------------------------------ routed rows ----
+        // A row's k-block is eight 16-byte chunks; eight neighbouring threads
+        // copy a row's, chunk c of row r landing at r * 128 + ((c ^ (r & 7)) <<
+        // 4), the 128-byte swizzle. Each thread then leaves an arrival on the
+        // stage's barrier that fires when its copies have landed.
+        const int t = threadIdx.x - 64, c = t & 7, r0 = t >> 3;
+        constexpr int kStep = 32 * kFfLoaders / 8;  // rows that all loaders copy at once
+        constexpr int kRows = kFfRows / kStep;      // of a thread, at most
+        RingPos st, iq;
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&info_full[iq.i]), iq.ph, abort_flag));
+            if (!ok) break;
+            const volatile FfInfo *inf = info + iq.i;
+            const int n = inf->n;
+            const uint8_t *src[kRows], *ssrc = nullptr;
+            // a column without a slot reads row 0; it is not stored
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+                const int r = r0 + j * kStep, i = r < n ? inf->slot[r] : -1;
+                src[j] = p.x + (int64_t)(i < 0 ? 0 : i / p.div) * p.x_row_bytes + c * 16;
+            }
+            if constexpr (MX) {
+                const int i = t < n ? inf->slot[t] : -1;
+                ssrc = p.x_scales + (int64_t)(i < 0 ? 0 : i / p.div) * (p.num_chunks * 4);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
+            iq.next(kFfInfos);
+            if (n == 0) continue;
+            const uint32_t dst = ring + kFfWBytes + (uint32_t)(r0 * kFfRowBytes + ((c ^ (r0 & 7)) << 4));
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&empty[st.i]), st.ph ^ 1u, abort_flag));
+                if (!ok) break;
+                const uint32_t d = dst + (uint32_t)st.i * p.stage_bytes;
+                // (chunks past the row's end are not read by the last MMA steps)
+                if (kb * kFfRowBytes + c * 16 < p.x_bytes) {
+#pragma unroll
+                    for (int j = 0; j < kRows; ++j)
+                        if (r0 + j * kStep < n) cp_async_16(d + j * (kStep * kFfRowBytes), src[j] + kb * kFfRowBytes);
+                }
+                if constexpr (MX) {
+                    // scale of row r, block q of a 128-value piece: byte
+                    // (r % 32) * 16 + (r / 32) * 4 + q of its 512
+                    const uint32_t sd = ring + (uint32_t)st.i * p.stage_bytes + kFfWBytes + p.b_bytes + 2 * kSfAtom +
+                                        (t & 31) * 16 + (t >> 5) * 4;
+                    if (t < n) {
+                        cp_async_4(sd, ssrc + kb * 8);
+                        if (2 * kb + 1 < p.num_chunks) cp_async_4(sd + kSfAtom, ssrc + kb * 8 + 4);
+                    }
+                }
+                cp_async_arrive(smem_u32(&full[st.i]));
+                st.next(ST);
+            }
+        }
+        // nothing lands after the CTA has left
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+    } else {
+        // --------------------------------------------------- epilogue ----
+        const int q = warp & 3;
+        RingPos iq, ac;
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&info_full[iq.i]), iq.ph, abort_flag));
+            if (!ok) break;
+            const FfInfo *inf = info + iq.i;
+            const int n = inf->n;
+            if (n > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&acc_full[ac.i]), ac.ph, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.A);
+                const int hi = lane >> 4;
+                const int f = UP ? inf->nt * 64 + q * 16 + (lane & 15) : inf->nt * kFfRows + q * 32 + lane;
+                const bool f_ok = f < p.feat;
+                for (int c0 = 0; c0 < n; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_async(acc + (uint32_t)c0, v);
+                    tmem_wait_ld16(v);
+                    if constexpr (UP) {
+                        // lanes 0-15 hold gate rows, 16-31 the same features'
+                        // up rows: each half of the warp takes every other
+                        // column and gets its missing factor from the other
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? v[2 * j] : v[2 * j + 1], 16);
+                            const float g = __uint_as_float(hi ? got : v[2 * j]);
+                            const float u = __uint_as_float(hi ? v[2 * j + 1] : got);
+                            const int i = inf->slot[c0 + 2 * j + hi];
+                            if (i >= 0 && f_ok) p.out[(int64_t)i * p.feat + f] = swiglu_bf16(g, u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int i = inf->slot[c0 + j];
+                            if (i >= 0 && f_ok)
+                                p.out[(int64_t)i * p.feat + f] =
+                                    __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ac.i]));
+                ac.next(2);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
+            iq.next(kFfInfos);
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag && warp == 0 && lane == 0) {
+        // a wait gave up: the item's outputs are not written; weights still in
+        // flight land before the CTA leaves
+        set_error(p.err, kErrWaitTimeout);
+        for (int j = issued - ST > 0 ? issued - ST : 0; j < issued; ++j) {
+            volatile int drain = 0;
+            mbar_wait_bounded(smem_u32(&full[j % ST]), (uint32_t)(j / ST) & 1u, &drain);
+        }
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
+    }
+}
+
+// ------------------------------------------------------------- combine --
+//
+// out[t] = sum over the token's slots s, in order, of w[t, s] * y[t, s], in
+// fp32, rounded once. Bound by reading y (2 bytes per slot and feature); one
+// thread per 8 features. A slot whose id no expert has contributes nothing
+// (the align skipped it, so its row of y was not written).
+constexpr int kCombineThreads = 256;
+__global__ void __launch_bounds__(kCombineThreads)
+expert_combine_kernel(const uint16_t *__restrict__ y, const int32_t *__restrict__ ids,
+                      const float *__restrict__ wts, uint16_t *__restrict__ out, int T, int width, int H,
+                      int num_logical) {
+    griddep_launch_dependents();
+    const uint32_t vecs = (uint32_t)H / 8, at = blockIdx.x * kCombineThreads + threadIdx.x;
+    griddep_wait();
+    if (at >= (uint32_t)T * vecs) return;
+    const uint32_t t = at / vecs, v = at - t * vecs;
+    ids += (int64_t)t * width;
+    wts += (int64_t)t * width;
+    const uint16_t *row = y + (int64_t)t * width * H + v * 8;
+    float acc[8] = {};
+    for (int s0 = 0; s0 < width; s0 += 4) {
+        uint4 x[4];
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s = s0 + j;
+            const bool use = s < width && (uint32_t)__ldcg(ids + s) < (uint32_t)num_logical;
+            x[j] = use ? ld_stream_v4(row + (int64_t)s * H) : make_uint4(0u, 0u, 0u, 0u);
+            w[j] = use ? __ldcg(wts + s) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float f[8];
+            unpack8(x[j], f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) acc[u] = fmaf(w[j], f[u], acc[u]);
+        }
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * u], acc[2 * u + 1]);
+        o[u] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(out + (int64_t)at * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ---------------------------------------------------------------- host --
+
+static int sm_count() {
+    static std::atomic<int> cached[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// cuTensorMapEncodeTiled, looked up once (a function-local static).
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess || q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+static bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ptr, const cuuint64_t *dims,
+                   const cuuint64_t *strides, const cuuint32_t *box) {
+    const auto fn = tensor_map_encoder();
+    const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
+    return fn && fn(map, type, (cuuint32_t)rank, const_cast<void *>(ptr), dims, strides, box, unit,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool MX, bool UP>
+static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stream) {
+    FfParams p{};
+    const int per_block = MX ? 256 : 64, step = MX ? 64 : 16;  // values of K in a k-block, in an MMA
+    p.num_kb = (a.K + per_block - 1) / per_block;
+    p.last_steps = (a.K - (p.num_kb - 1) * per_block + step - 1) / step;
+    p.feat = a.feat;
+    p.ntiles = UP ? (a.feat + 63) / 64 : (a.feat + kFfRows - 1) / kFfRows;
+    p.div = UP ? a.width : 1;
+    p.num_experts = a.num_experts;
+    p.A = a.A;
+    p.numel = (int)a.numel;
+    p.sorted_cap = a.sorted_cap;
+    p.max_blocks = (int)((a.sorted_cap + a.A - 1) / a.A);
+    p.sorted = a.sorted;
+    p.eids = a.eids;
+    p.npp = a.npp;
+    p.out = a.out;
+    p.x_scales = a.x_scales;
+    p.w_scales = a.w_scales;
+    p.num_chunks = a.K / 128;
+    p.err = &reinterpret_cast<WsHeader *>(a.hdr)->error;
+    p.b_bytes = (uint32_t)a.A * kFfRowBytes;
+    p.stage_bytes = kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0);
+    constexpr uint32_t kSmemMax = 232448;
+    p.stages = (int)((kSmemMax - 1024 - kFfMiscBytes) / p.stage_bytes);
+    if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
+    const int cols = 2 * a.A + (MX ? 32 : 0);
+    p.tmem_cols = cols <= 128 ? 128 : (cols <= 256 ? 256 : 512);
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + kFfMiscBytes;
+
+    const CUtensorMapDataType type = MX ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t k_elems = (cuuint64_t)(MX ? a.K / 2 : a.K), k_bytes = MX ? k_elems : 2 * k_elems;
+    const cuuint32_t box_k = MX ? kFfRowBytes : kFfRowBytes / 2;
+    CUtensorMap mw;
+    bool ok;
+    if (UP) {
+        const cuuint64_t I = (cuuint64_t)a.feat;
+        const cuuint64_t dims[5] = {k_elems, 16, 2, I / 16, (cuuint64_t)a.num_experts};
+        const cuuint64_t strides[4] = {k_bytes, I * k_bytes, 16 * k_bytes, 2 * I * k_bytes};
+        const cuuint32_t box[5] = {box_k, 16, 2, 4, 1};
+        ok = encode(&mw, type, 5, a.w, dims, strides, box);
+    } else {
+        const cuuint64_t dims[3] = {k_elems, (cuuint64_t)a.feat, (cuuint64_t)a.num_experts};
+        const cuuint64_t strides[2] = {k_bytes, (cuuint64_t)a.feat * k_bytes};
+        const cuuint32_t box[3] = {box_k, kFfRows, 1};
+        ok = encode(&mw, type, 3, a.w, dims, strides, box);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    p.x = static_cast<const uint8_t *>(a.x);
+    p.x_bytes = (int)k_bytes;
+    p.x_row_bytes = MX ? (int64_t)k_bytes : a.ld_x * 2;
+
+    static std::atomic<bool> configured[kMaxDevices];
+    const cudaError_t e = once_per_device(configured, [](int) {
+        cudaError_t r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kSmemMax);
+        if (r == cudaSuccess)
+            r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+        return r;
+    });
+    if (e != cudaSuccess) return e;
+    const int most = p.max_blocks * p.ntiles;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms), 1, 1);
+    cfg.blockDim = dim3(kFfThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP>, mw, p);
+}
+
+cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream) {
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const bool mx = a.x_scales != nullptr;
+    if (a.gated) return mx ? launch_product<true, true>(a, sms, stream) : launch_product<false, true>(a, sms, stream);
+    return mx ? launch_product<true, false>(a, sms, stream) : launch_product<false, false>(a, sms, stream);
+}
+
+cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream) {
+    const int64_t threads = (int64_t)a.T * (a.H / 8);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((threads + kCombineThreads - 1) / kCombineThreads), 1, 1);
+    cfg.blockDim = dim3(kCombineThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, expert_combine_kernel, a.y, a.ids, a.wts, a.out, a.T, a.width, a.H,
+                              a.num_logical);
+}
+
+}  // namespace smr

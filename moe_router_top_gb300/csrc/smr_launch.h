@@ -174,6 +174,46 @@ struct ExpertGemmLaunch {
 };
 cudaError_t launch_expert_gemm(const ExpertGemmLaunch &a, cudaStream_t stream);
 
+// The experts' feed-forward: the gated product (gated: w [num_experts][2
+// feat][K], out = silu(gate) * up) or the plain one (w [num_experts][feat][K])
+// over the align's blocks; out bf16 [numel][feat], one row per routed slot.
+// x_scales != nullptr: x and w are MXFP4 codes.
+struct FfnLaunch {
+    const void *x;
+    int64_t ld_x;            // row stride (bf16 only, elements)
+    const uint8_t *x_scales; // E8M0, one row per row of x, [K / 32]
+    const void *w;
+    const uint8_t *w_scales; // E8M0, tiled (mxfp4_weight_tiles)
+    bool gated;
+    int width, K, feat, A, num_experts;
+    int64_t numel, sorted_cap;
+    const int32_t *sorted, *eids, *npp;
+    uint16_t *out;
+    void *hdr;               // workspace header (sticky error word)
+};
+cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream);
+
+// out[t] = sum over s of wts[t][s] * y[t * width + s], slots whose id is
+// outside [0, num_logical) left out.
+struct CombineLaunch {
+    const uint16_t *y;       // bf16 [T * width][H]
+    const int32_t *ids;      // [T][width]
+    const float *wts;
+    uint16_t *out;           // bf16 [T][H]
+    int T, width, H, num_logical;
+};
+cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream);
+
+// MXFP4. Tiles of 128 rows of a weight of N rows (gated: 64 of the N / 2
+// features, each with its gate and its up row).
+inline int mxfp4_weight_tiles(int N, bool gated) { return gated ? (N / 2 + 63) / 64 : (N + 127) / 128; }
+cudaError_t launch_quantize_mxfp4(const uint16_t *x, int64_t rows, int K, int64_t ld, uint8_t *codes, uint8_t *scales,
+                                  cudaStream_t stream);
+cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows, int K, uint16_t *out,
+                                    cudaStream_t stream);
+cudaError_t launch_tile_mxfp4_scales(const uint8_t *scales, int E, int N, int K, bool gated, uint8_t *tiled,
+                                     cudaStream_t stream);
+
 // moe_align_block_size.
 struct AlignLaunch {
     const int32_t *ids;
