@@ -33,6 +33,7 @@ constexpr int kFfRows = 128;                     // weight rows of a tile (the M
 constexpr int kFfRowBytes = 128;                 // one k-block of a row: 64 bf16 or 256 MXFP4
 constexpr int kFfWBytes = kFfRows * kFfRowBytes;  // weight tile of a stage
 constexpr int kFfMaxStages = 9;
+constexpr int kFfLag = 3;                        // stages of rows in flight a loader thread
 constexpr int kFfInfos = 3;                      // items whose rows are known ahead of the epilogue
 constexpr int kSfAtom = 512;                     // scales of 128 rows x 4 blocks (128 values of K)
 
@@ -88,10 +89,6 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// One arrival on the barrier once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
 
 // MXFP4 instruction descriptor (kind::mxf4): A and B E2M1 (bits 7-9, 10-11 =
 // 1), scales UE8M0 (bit 23), N >> 3 in bits 17-22, M >> 7 in bits 27-28; the
@@ -119,11 +116,37 @@ __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// silu(g) * u in fp32, rounded to bf16 once. The fast exponential and
-// division are within a few 2^-23 of the exact value, far below the rounding.
-__device__ __forceinline__ uint16_t swiglu_bf16(float g, float u) {
-    const float a = __fdividef(g, 1.0f + __expf(-g)) * u;
-    return __bfloat16_as_ushort(__float2bfloat16_rn(a));
+// silu(g) * u in fp32. The fast exponential and division are within a few
+// 2^-23 of the exact value, far below the rounding to bf16 that follows.
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+// Four lanes hold a feature each (a row of TMEM), c0..c3 its values in four
+// columns; each returns the four features, in bf16, of column (lane & 3): a
+// 4 x 4 transpose in three shuffles, so that results leave in 8-byte stores.
+// (One 2-byte store a value kept the epilogue at 12300 cycles an item of 128 x
+// 128, above the 12 k-blocks that it runs under.)
+__device__ __forceinline__ uint2 quad_pack(float c0, float c1, float c2, float c3, int lane) {
+    const bool odd = lane & 1, top = lane & 2;
+    const float x = __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1), y = __shfl_xor_sync(0xffffffffu, odd ? c2 : c3, 1);
+    const uint32_t p = odd ? pack_bf16x2(x, c1) : pack_bf16x2(c0, x);  // column (lane & 1)
+    const uint32_t q = odd ? pack_bf16x2(y, c3) : pack_bf16x2(c2, y);  // column 2 + (lane & 1)
+    const uint32_t z = __shfl_xor_sync(0xffffffffu, top ? p : q, 2);
+    return top ? make_uint2(z, q) : make_uint2(p, z);
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
+// A bounded wait of every lane of a warp, and one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), parity, abort));
 }
 
 // Position in a ring of barriers: index and the parity of its current use.
@@ -163,7 +186,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(smem_u32(&full[s]), 1 + 32 * kFfLoaders);  // the weights' bytes, the row loaders
+            mbar_init(smem_u32(&full[s]), 1 + kFfLoaders);  // the weights' bytes, the row loaders
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -235,7 +258,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (lane == 0) set_error(p.err, kErrBadId);
                 n = 0;
             }
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&info_empty[iq.i]), iq.ph ^ 1u, abort_flag))) break;
+            if (!warp_wait(&info_empty[iq.i], iq.ph ^ 1u, abort_flag)) break;
             FfInfo *inf = info + iq.i;
             if (4 * lane < A) {
 #pragma unroll
@@ -277,73 +300,89 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMAs ----
-        if (lane == 0) {
-            RingPos st, iq, ac;
-            uint32_t sfbuf = 0;
-            bool ok = true;
-            for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
-                if (!(ok = mbar_wait_bounded(smem_u32(&info_full[iq.i]), iq.ph, abort_flag))) break;
-                const int n = reinterpret_cast<volatile FfInfo *>(info)[iq.i].n;
-                mbar_arrive(smem_u32(&info_empty[iq.i]));
-                iq.next(kFfInfos);
-                if (n == 0) continue;
-                if (!(ok = mbar_wait_bounded(smem_u32(&acc_empty[ac.i]), ac.ph ^ 1u, abort_flag))) break;
+        // The whole warp runs the loop, so that descriptors and addresses stay
+        // in uniform registers; one elected lane issues.
+        const bool elected = elect_one();
+        RingPos st, iq, ac;
+        uint32_t sf = tmem + (uint32_t)(2 * p.A);  // two sets of scale columns in turn: [A 8][B 8]
+        bool ok = true;
+        for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+            if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+            const int n = __shfl_sync(0xffffffffu, reinterpret_cast<volatile FfInfo *>(info)[iq.i].n, 0);
+            __syncwarp();
+            if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
+            iq.next(kFfInfos);
+            if (n == 0) continue;
+            if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + (uint32_t)(ac.i * p.A);
+            const uint32_t idesc = MX ? idesc_mxf4(kFfRows, n) : idesc_bf16_f32(kFfRows, n);
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + (uint32_t)(ac.i * p.A);
-                const uint32_t idesc = MX ? idesc_mxf4(kFfRows, n) : idesc_bf16_f32(kFfRows, n);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!(ok = mbar_wait_bounded(smem_u32(&full[st.i]), st.ph, abort_flag))) break;
-                    // the loaders' copies were written through the generic
-                    // proxy; the tensor core reads through the async one
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    tc_fence_after();
-                    const uint32_t a = ring + (uint32_t)st.i * p.stage_bytes, b = a + kFfWBytes;
-                    const int steps = kb + 1 == p.num_kb ? p.last_steps : 4;
-                    if constexpr (MX) {
-                        // two sets of scale columns in turn: [A 8][B 8]
-                        const uint32_t sf = tmem + (uint32_t)(2 * p.A) + sfbuf * 16u;
-                        const uint32_t sa = b + p.b_bytes, sb = sa + 2 * kSfAtom;
-                        sfbuf ^= 1u;
-                        for (int c = 0; c < (steps + 1) / 2; ++c) {
-                            tc_cp_scales(sf + c * 4, sa + c * kSfAtom);
-                            tc_cp_scales(sf + 8 + c * 4, sb + c * kSfAtom);
+                const uint32_t a = ring + (uint32_t)st.i * p.stage_bytes, b = a + kFfWBytes;
+                const uint64_t da = smem_desc_sw<128>(a), db = smem_desc_sw<128>(b);  // + 2 per 32 bytes of K
+                const int steps = kb + 1 == p.num_kb ? p.last_steps : 4;
+                const uint32_t more = kb != 0 ? 1u : 0u;
+                if constexpr (MX) {
+                    const uint32_t sa = b + p.b_bytes, sb = sa + 2 * kSfAtom;
+                    if (elected) {
+                        tc_cp_scales(sf, sa);
+                        tc_cp_scales(sf + 8, sb);
+                        tc_mma_mxf4(acc, da, db, idesc, sf, sf + 8, more);
+                        tc_mma_mxf4(acc, da + 2, db + 2, idesc | (1u << 30) | (1u << 5), sf, sf + 8, 1u);
+                        if (steps == 4) {
+                            tc_cp_scales(sf + 4, sa + kSfAtom);
+                            tc_cp_scales(sf + 12, sb + kSfAtom);
+                            tc_mma_mxf4(acc, da + 4, db + 4, idesc, sf + 4, sf + 12, 1u);
+                            tc_mma_mxf4(acc, da + 6, db + 6, idesc | (1u << 30) | (1u << 5), sf + 4, sf + 12, 1u);
                         }
-                        for (int kk = 0; kk < steps; ++kk) {
-                            const uint32_t id = idesc | ((uint32_t)(kk & 1) << 30) | ((uint32_t)(kk & 1) << 5);
-                            tc_mma_mxf4(acc, smem_desc_sw<128>(a + kk * 32), smem_desc_sw<128>(b + kk * 32), id,
-                                        sf + (kk >> 1) * 4, sf + 8 + (kk >> 1) * 4, (kb | kk) != 0 ? 1u : 0u);
-                        }
+                    }
+                    sf ^= 16u;
+                } else if (elected) {
+                    if (steps == 4) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_bf16(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
                     } else {
                         for (int kk = 0; kk < steps; ++kk)
-                            tc_mma_bf16(acc, smem_desc_sw<128>(a + kk * 32), smem_desc_sw<128>(b + kk * 32), idesc,
-                                        (kb | kk) != 0 ? 1u : 0u);
+                            tc_mma_bf16(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
                     }
-                    tc_commit(smem_u32(&empty[st.i]));
-                    st.next(ST);
                 }
-                if (!ok) break;
-                tc_commit(smem_u32(&acc_full[ac.i]));
-                ac.next(2);
+                if (elected) tc_commit(smem_u32(&empty[st.i]));
+                st.next(ST);
             }
-            // every MMA issued is done before TMEM is freed, also after an abort
-            tc_commit(smem_u32(last));
-            volatile int never = 0;
-            if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
+            if (!ok) break;
+            if (elected) tc_commit(smem_u32(&acc_full[ac.i]));
+            ac.next(2);
         }
+        // every MMA issued is done before TMEM is freed, also after an abort
+        if (elected) tc_commit(smem_u32(last));
+        volatile int never = 0;
+        if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
         __syncwarp();
     } else if (warp < 2 + kFfLoaders) {
         // ------------------------------------------------ routed rows ----
         // A row's k-block is eight 16-byte chunks; eight neighbouring threads
         // copy a row's, chunk c of row r landing at r * 128 + ((c ^ (r & 7)) <<
-        // 4), the 128-byte swizzle. Each thread then leaves an arrival on the
-        // stage's barrier that fires when its copies have landed.
+        // 4), the 128-byte swizzle. A stage's copies are awaited kFfLag stages
+        // later, made visible to the tensor core (async proxy) and announced,
+        // one arrival a warp. (kFfLag < stages, or a stage would wait for
+        // itself to be freed.)
         const int t = threadIdx.x - 64, c = t & 7, r0 = t >> 3;
         constexpr int kStep = 32 * kFfLoaders / 8;  // rows that all loaders copy at once
         constexpr int kRows = kFfRows / kStep;      // of a thread, at most
-        RingPos st, iq;
+        RingPos st, iq, done;
+        int pending = 0;
+        auto announce = [&]() {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&full[done.i]));
+            done.next(ST);
+        };
         bool ok = true;
         for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&info_full[iq.i]), iq.ph, abort_flag));
+            ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
             if (!ok) break;
             const volatile FfInfo *inf = info + iq.i;
             const int n = inf->n;
@@ -364,7 +403,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             if (n == 0) continue;
             const uint32_t dst = ring + kFfWBytes + (uint32_t)(r0 * kFfRowBytes + ((c ^ (r0 & 7)) << 4));
             for (int kb = 0; kb < p.num_kb; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&empty[st.i]), st.ph ^ 1u, abort_flag));
+                ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag);
                 if (!ok) break;
                 const uint32_t d = dst + (uint32_t)st.i * p.stage_bytes;
                 // (chunks past the row's end are not read by the last MMA steps)
@@ -383,12 +422,17 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         if (2 * kb + 1 < p.num_chunks) cp_async_4(sd + kSfAtom, ssrc + kb * 8 + 4);
                     }
                 }
-                cp_async_arrive(smem_u32(&full[st.i]));
+                asm volatile("cp.async.commit_group;" ::: "memory");
                 st.next(ST);
+                if (++pending > kFfLag) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kFfLag) : "memory");
+                    announce();
+                    --pending;
+                }
             }
         }
-        // nothing lands after the CTA has left
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        for (; pending > 0; --pending) announce();
         __syncwarp();
     } else {
         // --------------------------------------------------- epilogue ----
@@ -396,42 +440,61 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         RingPos iq, ac;
         bool ok = true;
         for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&info_full[iq.i]), iq.ph, abort_flag));
+            ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
             if (!ok) break;
             const FfInfo *inf = info + iq.i;
             const int n = inf->n;
             if (n > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&acc_full[ac.i]), ac.ph, abort_flag));
+                ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.A);
-                const int hi = lane >> 4;
-                const int f = UP ? inf->nt * 64 + q * 16 + (lane & 15) : inf->nt * kFfRows + q * 32 + lane;
-                const bool f_ok = f < p.feat;
+                // this lane's store: 4 features from f of column (lane & 3) of
+                // every four
+                const int f = UP ? inf->nt * 64 + q * 16 + (lane & 12) : inf->nt * kFfRows + q * 32 + (lane & 28);
+                const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
+                uint16_t *out = p.out + f;
+                uint32_t v[16], next[16];
+                tmem_ld16_async(acc, v);
+                tmem_wait_ld16(v);
                 for (int c0 = 0; c0 < n; c0 += 16) {
-                    uint32_t v[16];
-                    tmem_ld16_async(acc + (uint32_t)c0, v);
-                    tmem_wait_ld16(v);
+                    if (c0 + 16 < n) tmem_ld16_async(acc + (uint32_t)(c0 + 16), next);
                     if constexpr (UP) {
                         // lanes 0-15 hold gate rows, 16-31 the same features'
                         // up rows: each half of the warp takes every other
                         // column and gets its missing factor from the other
+                        const bool hi = lane >= 16;
+                        const int *cols = inf->slot + c0 + 2 * (lane & 3) + (hi ? 1 : 0);
+                        const int i0 = cols[0], i1 = cols[8];
+                        float a[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? v[2 * j] : v[2 * j + 1], 16);
                             const float g = __uint_as_float(hi ? got : v[2 * j]);
                             const float u = __uint_as_float(hi ? v[2 * j + 1] : got);
-                            const int i = inf->slot[c0 + 2 * j + hi];
-                            if (i >= 0 && f_ok) p.out[(int64_t)i * p.feat + f] = swiglu_bf16(g, u);
+                            a[j] = swiglu(g, u);
                         }
+                        const uint2 s0 = quad_pack(a[0], a[1], a[2], a[3], lane);
+                        const uint2 s1 = quad_pack(a[4], a[5], a[6], a[7], lane);
+                        if (i0 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i0 * p.feat) = s0;
+                        if (i1 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i1 * p.feat) = s1;
                     } else {
+                        int i[4];
+                        uint2 s[4];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int i = inf->slot[c0 + j];
-                            if (i >= 0 && f_ok)
-                                p.out[(int64_t)i * p.feat + f] =
-                                    __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[j])));
-                        }
+                        for (int j = 0; j < 4; ++j) i[j] = inf->slot[c0 + 4 * j + (lane & 3)];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            s[j] = quad_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), lane);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (i[j] >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i[j] * p.feat) = s[j];
+                    }
+                    if (c0 + 16 < n) {
+                        tmem_wait_ld16(next);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = next[j];
                     }
                 }
                 tc_fence_before();
@@ -503,10 +566,7 @@ expert_combine_kernel(const uint16_t *__restrict__ y, const int32_t *__restrict_
     }
     uint32_t o[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * u], acc[2 * u + 1]);
-        o[u] = *reinterpret_cast<const uint32_t *>(&b);
-    }
+    for (int u = 0; u < 4; ++u) o[u] = pack_bf16x2(acc[2 * u], acc[2 * u + 1]);
     *reinterpret_cast<uint4 *>(out + (int64_t)at * 8) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
