@@ -10,7 +10,6 @@ raise :class:`SmrUnsupported`, so a caller can take its own fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -64,9 +63,20 @@ def _disabled() -> None:
         raise SmrUnsupported(_lib.SMR_ERR_UNSUPPORTED, "disabled by SMR_DISABLE")
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _raw_stream(dev: int) -> int:
+    """The current stream of a device, as the pointer that the library takes."""
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
 def _ptr(t) -> Optional[int]:
@@ -363,46 +373,48 @@ def expert_gemm(hidden, expert_w, sorted_token_ids, expert_ids, num_tokens_post_
     return out
 
 
-def _check_cuda(first, *others) -> None:
-    """Every tensor on the first one's CUDA device."""
-    if first.device.type != "cuda":
+def _check_cuda(first, *others) -> int:
+    """Index of the first tensor's CUDA device, which every other one must be on."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors must be on one device (got {first.device} and {t.device})")
+    return dev
 
 
-def _stream_of(device, stream):
-    """The stream to launch on, and the context in which to allocate and
-    launch (nothing to enter for the current stream of the current device)."""
+def _elsewhere(dev: int, stream):
+    """The context to allocate and launch in, or None for the current stream
+    of the current device."""
     torch = _torch()
     if stream is None:
-        s = torch.cuda.current_stream(device)
-        if device.index == torch.cuda.current_device():
-            return s, contextlib.nullcontext()
-    else:
-        s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-    return s, torch.cuda.stream(s)
+        return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    return torch.cuda.stream(stream)
 
 
 _stream_ws = {}
 
 
-def _ffn_workspace(ws, nbytes: int, device, s):
-    """Workspace of the feed-forward entry points: the caller's, or one per
-    device and stream (calls on two streams may overlap). A call that is being
-    captured gets one of its own, which the graph keeps and zeroes itself."""
+def _ffn_workspace(ws, nbytes: int, dev: int, s: int):
+    """(pointer, bytes) of a workspace of the feed-forward entry points: the
+    caller's, or one per device and stream (calls on two streams may overlap).
+    A call that is being captured gets one of its own, which its graph keeps
+    and zeroes itself."""
     torch = _torch()
-    if ws is None and torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        ws[:256].zero_()
-        return ws
     if ws is None:
-        key = (device.index, s.cuda_stream)
-        ws = _stream_ws.get(key)
+        if torch.cuda.is_current_stream_capturing():
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+            buf[:256].zero_()
+            return buf.data_ptr(), nbytes
+        ws = _stream_ws.get((dev, s))
         if ws is None:
-            ws = _stream_ws[key] = Workspace(0, device)
-    return ws.ensure(nbytes) if isinstance(ws, Workspace) else ws
+            ws = _stream_ws[(dev, s)] = Workspace(0, torch.device("cuda", dev))
+    if isinstance(ws, Workspace):
+        ws = ws.ensure(nbytes)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated):
@@ -412,39 +424,36 @@ def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated):
     if mx != (w_scales is not None):
         raise ValueError("x_scales and w_scales must both be given (MXFP4) or both be None (bfloat16)")
     dtype, kdim = (torch.uint8, K // 2) if mx else (torch.bfloat16, K)
-    kind = "uint8 (MXFP4 codes)" if mx else "bfloat16"
-    if x.dtype != dtype or x.dim() != 2 or tuple(x.shape) != (rows, kdim) or (kdim > 1 and x.stride(1) != 1):
-        raise ValueError(f"x must be a {kind} [{rows}, {kdim}] tensor with unit stride along its rows")
-    if w.dtype != dtype or w.dim() != 3 or tuple(w.shape[1:]) != (w_rows, kdim) or not w.is_contiguous():
-        raise ValueError(f"w must be a contiguous {kind} [num_experts, {w_rows}, {kdim}] tensor")
+    if x.dtype != dtype or x.shape != (rows, kdim) or (x.stride(1) != 1 and kdim > 1):
+        raise ValueError(f"x must be a {dtype} [{rows}, {kdim}] tensor with unit stride along its rows")
+    if w.dtype != dtype or w.shape[1:] != (w_rows, kdim) or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous {dtype} [num_experts, {w_rows}, {kdim}] tensor")
     if mx:
         if not x.is_contiguous():
             raise ValueError("MXFP4 codes x must be contiguous")
-        if (x_scales.dtype != torch.uint8 or tuple(x_scales.shape) != (rows, K // 32)
-                or not x_scales.is_contiguous()):
+        if x_scales.dtype != torch.uint8 or x_scales.shape != (rows, K // 32) or not x_scales.is_contiguous():
             raise ValueError(f"x_scales must be a contiguous uint8 [{rows}, {K // 32}] tensor")
         need = _lib.load().smr_mxfp4_tiled_scale_bytes(w.shape[0], w_rows, K, 1 if gated else 0)
-        if w_scales.dtype != torch.uint8 or not w_scales.is_contiguous() or w_scales.numel() != need:
+        if w_scales.dtype != torch.uint8 or w_scales.numel() != need or not w_scales.is_contiguous():
             raise ValueError(f"w_scales must be the {need} bytes that tile_mxfp4_scales gives for this weight")
 
 
 def _aligned_inputs(sorted_token_ids, expert_ids, npp, block_size):
-    torch = _torch()
-    for t in (sorted_token_ids, expert_ids, npp):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError("sorted_token_ids, expert_ids and num_tokens_post_padded must be contiguous int32 tensors")
-    if block_size > 0 and expert_ids.numel() * block_size < sorted_token_ids.numel():
+    int32 = _torch().int32
+    if (sorted_token_ids.dtype != int32 or expert_ids.dtype != int32 or npp.dtype != int32
+            or not sorted_token_ids.is_contiguous() or not expert_ids.is_contiguous()):
+        raise ValueError("sorted_token_ids, expert_ids and num_tokens_post_padded must be contiguous int32 tensors")
+    if expert_ids.numel() * block_size < sorted_token_ids.numel() and block_size > 0:
         raise ValueError("expert_ids must hold an entry for every block of sorted_token_ids")
     if npp.numel() < 1:
         raise ValueError("num_tokens_post_padded must hold one entry")
 
 
-def _output(out, shape, device):
-    torch = _torch()
+def _output(out, shape, dtype, device, name="out"):
     if out is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    if out.dtype != torch.bfloat16 or tuple(out.shape) != tuple(shape) or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous bfloat16 tensor of shape {tuple(shape)}")
+        return _torch().empty(shape, dtype=dtype, device=device)
+    if out.dtype != dtype or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return out
 
 
@@ -458,26 +467,31 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
     w_scales laid out by tile_mxfp4_scales(..., gated=True)). Rows of slots
     that the align skipped are left as they are in `out`."""
     _disabled()
+    torch = _torch()
     lib = _lib.load()
     if w.dim() != 3 or w.shape[1] % 2 or x.dim() != 2:
         raise ValueError("x must be [num_tokens, H] and w [num_experts, 2 I, H]")
-    T, H, I = x.shape[0], x.shape[1] * (1 if x_scales is None else 2), w.shape[1] // 2
+    T, H = x.shape
+    E, I = w.shape[0], w.shape[1] // 2
+    if x_scales is not None:
+        H *= 2
     _product_inputs(x, w, x_scales, w_scales, T, H, 2 * I, True)
     _aligned_inputs(sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
-    _check_cuda(x, w, x_scales, w_scales, sorted_token_ids, expert_ids, num_tokens_post_padded, out)
-    s, ctx = _stream_of(x.device, stream)
-    with ctx:
-        out = _output(out, (T * int(width), I), x.device)
-        a = ExpertUpArgs()
-        a.num_tokens, a.width, a.H, a.I = T, int(width), H, I
-        a.num_experts, a.block_size = w.shape[0], int(block_size)
-        a.x, a.ld_x, a.x_scales = _ptr(x), (x.stride(0) if T > 1 else H), _ptr(x_scales)
-        a.w, a.w_scales = _ptr(w), _ptr(w_scales)
-        a.sorted_token_ids, a.sorted_cap = _ptr(sorted_token_ids), sorted_token_ids.numel()
-        a.expert_ids, a.num_tokens_post_padded = _ptr(expert_ids), _ptr(num_tokens_post_padded)
-        a.act = _ptr(out)
-        buf = _ffn_workspace(workspace, lib.smr_expert_up_workspace_size(ctypes.byref(a)), x.device, s)
-        _check(lib.smr_expert_up(ctypes.byref(a), buf.data_ptr(), buf.numel() * buf.element_size(), s.cuda_stream))
+    dev = _check_cuda(x, w, x_scales, w_scales, sorted_token_ids, expert_ids, num_tokens_post_padded, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, width=width,
+                             block_size=block_size, x_scales=x_scales, w_scales=w_scales, out=out,
+                             workspace=workspace)
+    out = _output(out, (T * width, I), torch.bfloat16, x.device)
+    a = ExpertUpArgs(T, width, H, I, E, block_size, x.data_ptr(), x.stride(0) if T > 1 else H, _ptr(x_scales),
+                     w.data_ptr(), _ptr(w_scales), sorted_token_ids.data_ptr(), sorted_token_ids.numel(),
+                     expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), out.data_ptr())
+    ref = ctypes.byref(a)
+    s = _raw_stream(dev)
+    wp, wn = _ffn_workspace(workspace, lib.smr_expert_up_workspace_size(ref), dev, s)
+    _check(lib.smr_expert_up(ref, wp, wn, s))
     return out
 
 
@@ -501,28 +515,30 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     if w.dim() != 3 or x.dim() != 2:
         raise ValueError("x must be [num_tokens * width, I] and w [num_experts, H, I]")
     T, width = topk_ids.shape
-    I, H = x.shape[1] * (1 if x_scales is None else 2), w.shape[1]
+    E, H, I = w.shape
+    if x_scales is not None:
+        I *= 2
     _product_inputs(x, w, x_scales, w_scales, T * width, I, H, False)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     _aligned_inputs(sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
-    _check_cuda(x, w, topk_ids, topk_weights, x_scales, w_scales, sorted_token_ids, expert_ids,
-                num_tokens_post_padded, out)
-    s, ctx = _stream_of(x.device, stream)
-    with ctx:
-        out = _output(out, (T, H), x.device)
-        a = ExpertDownArgs()
-        a.num_tokens, a.width, a.H, a.I = T, width, H, I
-        a.num_experts, a.block_size = w.shape[0], int(block_size)
-        a.x, a.x_scales, a.w, a.w_scales = _ptr(x), _ptr(x_scales), _ptr(w), _ptr(w_scales)
-        a.topk_ids, a.topk_weights = _ptr(topk_ids), _ptr(topk_weights)
-        a.num_logical = int(num_logical) if num_logical else w.shape[0]
-        a.sorted_token_ids, a.sorted_cap = _ptr(sorted_token_ids), sorted_token_ids.numel()
-        a.expert_ids, a.num_tokens_post_padded = _ptr(expert_ids), _ptr(num_tokens_post_padded)
-        a.out = _ptr(out)
-        buf = _ffn_workspace(workspace, lib.smr_expert_down_workspace_size(ctypes.byref(a)), x.device, s)
-        _check(lib.smr_expert_down(ctypes.byref(a), buf.data_ptr(), buf.numel() * buf.element_size(),
-                                   s.cuda_stream))
+    dev = _check_cuda(x, w, topk_ids, topk_weights, x_scales, w_scales, sorted_token_ids, expert_ids,
+                      num_tokens_post_padded, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_tokens_post_padded,
+                               block_size=block_size, num_logical=num_logical, x_scales=x_scales,
+                               w_scales=w_scales, out=out, workspace=workspace)
+    out = _output(out, (T, H), torch.bfloat16, x.device)
+    a = ExpertDownArgs(T, width, H, I, E, block_size, x.data_ptr(), _ptr(x_scales), w.data_ptr(), _ptr(w_scales),
+                       topk_ids.data_ptr(), topk_weights.data_ptr(), num_logical if num_logical else E,
+                       sorted_token_ids.data_ptr(), sorted_token_ids.numel(), expert_ids.data_ptr(),
+                       num_tokens_post_padded.data_ptr(), out.data_ptr())
+    ref = ctypes.byref(a)
+    s = _raw_stream(dev)
+    wp, wn = _ffn_workspace(workspace, lib.smr_expert_down_workspace_size(ref), dev, s)
+    _check(lib.smr_expert_down(ref, wp, wn, s))
     return out
 
 
@@ -532,24 +548,25 @@ def quantize_mxfp4(x, *, codes=None, scales=None, stream=None) -> Tuple:
     contiguous, or 2-D with unit stride along K."""
     _disabled()
     torch = _torch()
-    if x.dtype != torch.bfloat16 or x.dim() < 1 or not (x.is_contiguous() or (x.dim() == 2 and x.stride(1) == 1)):
+    lib = _lib.load()
+    shape = x.shape
+    dense = x.is_contiguous()
+    if x.dtype != torch.bfloat16 or len(shape) < 1 or not (dense or (len(shape) == 2 and x.stride(1) == 1)):
         raise ValueError("x must be a bfloat16 tensor, contiguous or 2-D with unit stride along its rows")
-    lead, K = tuple(x.shape[:-1]), x.shape[-1]
+    K = shape[-1]
     if K < 32 or K % 32:
         raise ValueError(f"x's last dimension must be a positive multiple of 32 (got {K})")
-    for t, n, name in ((codes, K // 2, "codes"), (scales, K // 32, "scales")):
-        if t is not None and (t.dtype != torch.uint8 or tuple(t.shape) != lead + (n,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {lead + (n,)}")
-    _check_cuda(x, codes, scales)
+    dev = _check_cuda(x, codes, scales)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return quantize_mxfp4(x, codes=codes, scales=scales)
+    device, lead = x.device, shape[:-1]
+    codes = _output(codes, lead + (K // 2,), torch.uint8, device, "codes")
+    scales = _output(scales, lead + (K // 32,), torch.uint8, device, "scales")
     rows = x.numel() // K
-    s, ctx = _stream_of(x.device, stream)
-    with ctx:
-        if codes is None:
-            codes = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
-        ld = x.stride(0) if not x.is_contiguous() and rows > 1 else K
-        _check(_lib.load().smr_quantize_mxfp4(_ptr(x), rows, K, ld, _ptr(codes), _ptr(scales), s.cuda_stream))
+    _check(lib.smr_quantize_mxfp4(x.data_ptr(), rows, K, K if dense or rows < 2 else x.stride(0), codes.data_ptr(),
+                                  scales.data_ptr(), _raw_stream(dev)))
     return codes, scales
 
 
@@ -558,19 +575,23 @@ def dequantize_mxfp4(codes, scales, *, out=None, stream=None):
     scales [..., K / 32] (exact; NaN where the scale byte is 255)."""
     _disabled()
     torch = _torch()
-    if codes.dtype != torch.uint8 or codes.dim() < 1 or not codes.is_contiguous():
+    lib = _lib.load()
+    shape = codes.shape
+    if codes.dtype != torch.uint8 or len(shape) < 1 or not codes.is_contiguous():
         raise ValueError("codes must be a contiguous uint8 tensor")
-    lead, K = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
+    lead, K = shape[:-1], 2 * shape[-1]
     if K < 32 or K % 32:
         raise ValueError(f"codes' last dimension must be a positive multiple of 16 (got {K // 2})")
-    if scales.dtype != torch.uint8 or tuple(scales.shape) != lead + (K // 32,) or not scales.is_contiguous():
-        raise ValueError(f"scales must be a contiguous uint8 tensor of shape {lead + (K // 32,)}")
-    _check_cuda(codes, scales, out)
-    s, ctx = _stream_of(codes.device, stream)
-    with ctx:
-        out = _output(out, lead + (K,), codes.device)
-        _check(_lib.load().smr_dequantize_mxfp4(_ptr(codes), _ptr(scales), codes.numel() * 2 // K, K, _ptr(out),
-                                                s.cuda_stream))
+    if scales.dtype != torch.uint8 or scales.shape != lead + (K // 32,) or not scales.is_contiguous():
+        raise ValueError(f"scales must be a contiguous uint8 tensor of shape {tuple(lead) + (K // 32,)}")
+    dev = _check_cuda(codes, scales, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return dequantize_mxfp4(codes, scales, out=out)
+    out = _output(out, lead + (K,), torch.bfloat16, codes.device)
+    _check(lib.smr_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), codes.numel() * 2 // K, K, out.data_ptr(),
+                                    _raw_stream(dev)))
     return out
 
 
@@ -583,16 +604,16 @@ def tile_mxfp4_scales(scales, *, gated: bool = False, out=None, stream=None):
     lib = _lib.load()
     if scales.dtype != torch.uint8 or scales.dim() != 3 or not scales.is_contiguous():
         raise ValueError("scales must be a contiguous uint8 [num_experts, N, K / 32] tensor")
+    dev = _check_cuda(scales, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return tile_mxfp4_scales(scales, gated=gated, out=out)
     E, N, K = scales.shape[0], scales.shape[1], 32 * scales.shape[2]
-    shape = (E, -(-N // 128) if not gated else -(-(N // 2) // 64), K // 128, 512)
-    if out is not None and (out.dtype != torch.uint8 or tuple(out.shape) != shape or not out.is_contiguous()):
-        raise ValueError(f"out must be a contiguous uint8 tensor of shape {shape}")
-    _check_cuda(scales, out)
-    s, ctx = _stream_of(scales.device, stream)
-    with ctx:
-        if out is None:
-            out = torch.empty(shape, dtype=torch.uint8, device=scales.device)
-        _check(lib.smr_tile_mxfp4_scales(_ptr(scales), E, N, K, 1 if gated else 0, _ptr(out), s.cuda_stream))
+    shape = (E, -(-(N // 2) // 64) if gated else -(-N // 128), K // 128, 512)
+    out = _output(out, shape, torch.uint8, scales.device)
+    _check(lib.smr_tile_mxfp4_scales(scales.data_ptr(), E, N, K, 1 if gated else 0, out.data_ptr(),
+                                     _raw_stream(dev)))
     return out
 
 

@@ -108,6 +108,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load libsmr.so and declare its signatures (raises if it is not built)."""
     global _lib
+    if _lib is not None:  # set once, complete
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

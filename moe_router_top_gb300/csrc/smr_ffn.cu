@@ -33,19 +33,25 @@ constexpr int kFfRows = 128;                     // weight rows of a tile (the M
 constexpr int kFfRowBytes = 128;                 // one k-block of a row: 64 bf16 or 256 MXFP4
 constexpr int kFfWBytes = kFfRows * kFfRowBytes;  // weight tile of a stage
 constexpr int kFfMaxStages = 9;
-constexpr int kFfLag = 3;                        // stages of rows in flight a loader thread
-constexpr int kFfInfos = 3;                      // items whose rows are known ahead of the epilogue
+constexpr int kFfLag = 2;                        // stages that a row loader issues before it announces one
+constexpr int kFfInfos = 3;                      // pieces of work known ahead of the epilogue
 constexpr int kSfAtom = 512;                     // scales of 128 rows x 4 blocks (128 values of K)
 
-// What the producer tells the other warps about an item.
+// What the producer tells the other warps about a piece of work: one expert's
+// columns of an item.
+template <int COLS>
 struct FfInfo {
-    int n;       // MMA columns (16..128), 0: nothing to do
-    int nt;      // weight tile
+    int n;     // MMA columns (16..COLS, a multiple of 16); -1: no more work
+    int nt;    // weight tile of this CTA
     int pad[2];
-    int slot[128];  // flat slot of every column, -1: none
+    int slot[COLS];  // flat slot of every column, -1: none
 };
 constexpr int kFfBars = 2 * kFfMaxStages + 4 + 2 * kFfInfos + 1;
-constexpr int kFfMiscBytes = (kFfBars * 8 + 8 + 15) / 16 * 16 + kFfInfos * (int)sizeof(FfInfo);
+constexpr int kFfBarBytes = (kFfBars * 8 + 8 + 15) / 16 * 16;
+template <bool PAIR>
+constexpr int kFfCols = PAIR ? 256 : 128;  // columns of a piece, at most
+template <bool PAIR>
+constexpr int kFfMiscBytes = kFfBarBytes + kFfInfos * (int)sizeof(FfInfo<kFfCols<PAIR>>);
 
 struct FfParams {
     int num_kb, last_steps;  // k-blocks; MMA steps of the last one (4 in the others)
@@ -54,7 +60,8 @@ struct FfParams {
     int64_t x_row_bytes;     // between rows of x
     int x_bytes;             // of a row of x
     int div;                 // row of x = slot / div (the width for the gated product, else 1)
-    int num_experts, A, stages, tmem_cols;
+    int num_experts, A, stages;
+    int acc_cols, tmem_cols; // TMEM columns of an accumulator, of the allocation
     int64_t sorted_cap;
     int numel, max_blocks;
     const int32_t *sorted, *eids, *npp;
@@ -78,6 +85,41 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
         "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(map), "r"(c0), "r"(0), "r"(c3), "r"(c4), "r"(bar) : "memory");
+}
+// The same loads by a CTA of a pair; bar may be the other CTA's barrier.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c3, int c4,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(c0), "r"(0), "r"(c3), "r"(c4), "r"(bar) : "memory");
+}
+// Arrive on a barrier of either CTA of a pair (address from cluster_addr).
+// What is handed over is in this CTA's own shared memory (made visible to the
+// tensor core by a proxy fence before) or TMEM (read, and fenced), never in
+// global memory, so the arrival needs no release beyond the CTA: with
+// .release.cluster every one waited for the device-wide visibility of the
+// thread's earlier writes (2146 us against 886 without pairs, 16384 tokens).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void ff_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (PAIR) tc_mma_bf16_pair(d, a, b, idesc, accumulate);
+    else tc_mma_bf16(d, a, b, idesc, accumulate);
+}
+// Arrival (in both CTAs of a pair) once the MMAs issued so far are done.
+template <bool PAIR>
+__device__ __forceinline__ void ff_commit(uint64_t *bar) {
+    if constexpr (PAIR) tc_commit_pair(smem_u32(bar), 0x3);
+    else tc_commit(smem_u32(bar));
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -148,7 +190,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), parity, abort));
 }
-
 // Position in a ring of barriers: index and the parity of its current use.
 struct RingPos {
     int i = 0;
@@ -163,35 +204,42 @@ struct RingPos {
 
 // MX: MXFP4 operands, else bf16. UP: the gated product (a tile holds 64
 // features: 16 gate rows and their 16 up rows in turn, so that both halves of
-// a feature are in one warp's TMEM lanes), else 128 plain rows.
-template <bool MX, bool UP>
+// a feature are in one warp's TMEM lanes), else 128 plain rows. PAIR: two CTAs
+// on one 256-row tile and up to 256 columns (blocks of one expert next to each
+// other together); each holds its own 128 weight rows and half of the routed
+// rows, and drains its own lanes.
+template <bool MX, bool UP, bool PAIR>
 __global__ void __launch_bounds__(kFfThreads, 1)
 expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
+    using Info = FfInfo<kFfCols<PAIR>>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     const int ST = p.stages;
     uint8_t *misc = smem + (size_t)ST * p.stage_bytes;
+    // full and acc_empty of a pair are the leader's, the others each CTA's own
     uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // the stage's operands landed
     uint64_t *empty = full + kFfMaxStages;                 // the MMAs are done with the stage
-    uint64_t *acc_full = empty + kFfMaxStages;             // an item's accumulator is complete
+    uint64_t *acc_full = empty + kFfMaxStages;             // a piece's accumulator is complete
     uint64_t *acc_empty = acc_full + 2;                    // it has been read
     uint64_t *info_full = acc_empty + 2;
     uint64_t *info_empty = info_full + kFfInfos;
     uint64_t *last = info_empty + kFfInfos;                // every MMA issued is done
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(last + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    FfInfo *info = reinterpret_cast<FfInfo *>(misc + (kFfBars * 8 + 8 + 15) / 16 * 16);
+    Info *info = reinterpret_cast<Info *>(misc + kFfBarBytes);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(smem_u32(&full[s]), 1 + kFfLoaders);  // the weights' bytes, the row loaders
+            // the weights' bytes, and the row loaders' arrivals
+            mbar_init(smem_u32(&full[s]), 1 + (PAIR ? 2 : 1) * kFfLoaders);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
-            mbar_init(smem_u32(&acc_empty[s]), 4);
+            mbar_init(smem_u32(&acc_empty[s]), PAIR ? 8 : 4);  // epilogue warps
         }
         for (int s = 0; s < kFfInfos; ++s) {
             mbar_init(smem_u32(&info_full[s]), 1);
@@ -203,66 +251,56 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         prefetch_tensormap(&tm_w);
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), (uint32_t)p.tmem_cols);
-        tmem_relinquish();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(smem_u32(tmem_slot), (uint32_t)p.tmem_cols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), (uint32_t)p.tmem_cols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_launch_dependents();
     griddep_wait();  // the align's outputs and x come from previous kernels
 
-    const int nblk = min(__ldcg(p.npp) / p.A, p.max_blocks);
-    const int items = nblk > 0 ? nblk * p.ntiles : 0;
     const uint32_t ring = smem_u32(smem);
-    int issued = 0;  // stages whose loads were issued (producer warp)
+    int issued = 0;  // stages whose weights were requested (producer lane 0)
 
     if (warp == 0) {
         // ---------------------------------------------------- weights ----
-        const int A = p.A;
-        int ent[4], e = -1;
-        // the item's expert and this lane's 4 entries of its block, requested
-        // an item ahead
+        // An item is a group of 1 (PAIR: 256 / A) aligned blocks and a weight
+        // tile (PAIR: two). Blocks of a group that share an expert make one
+        // piece of work. Both CTAs of a pair walk the same pieces.
+        const int A = p.A, G = PAIR ? 256 / A : 1;
+        const int nblk = max(0, min(__ldcg(p.npp) / A, p.max_blocks));
+        const int tiles = PAIR ? (p.ntiles + 1) / 2 : p.ntiles;
+        const int items = (nblk + G - 1) / G * tiles;
+        const int stride = PAIR ? gridDim.x >> 1 : gridDim.x;
+        int ent[8], e = -1;  // this lane's 8 entries of the group, their block's expert
+        // requested an item ahead
         auto fetch = [&](int it) {
-            if (it >= items) return;
-            const int b = it / p.ntiles;
-            e = __ldcg(p.eids + b);
-            if (4 * lane < A) {
-                const int64_t at = (int64_t)b * A + 4 * lane;
+            const int in = 8 * lane, b = it / tiles * G + in / A;
+            if (it >= items || in >= G * A) return;
+            const int64_t at = (int64_t)b * A + in % A;
+            e = b < nblk ? __ldcg(p.eids + b) : -1;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) ent[j] = at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
-            }
+            for (int j = 0; j < 8; ++j)
+                ent[j] = b < nblk && at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
         };
         RingPos st, iq;
-        fetch(blockIdx.x);
-        for (int it = blockIdx.x; it < items; it += gridDim.x) {
-            const int nt = it % p.ntiles;
-            const int ex = e;
-            int slot[4], top = 0;
-            if (4 * lane < A) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = ent[j];
-                    const bool real = (uint32_t)i < (uint32_t)p.numel;
-                    // neither a slot nor the sentinel: a corrupted align output
-                    if (!real && i != p.numel) set_error(p.err, kErrBadSlot);
-                    slot[j] = real ? i : -1;
-                    if (real) top = 4 * lane + j + 1;
-                }
-            }
-            __syncwarp();
-            const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
-            int n = (rows + 15) & ~15;
-            if ((unsigned)ex >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
-                if (lane == 0) set_error(p.err, kErrBadId);
-                n = 0;
-            }
-            if (!warp_wait(&info_empty[iq.i], iq.ph ^ 1u, abort_flag)) break;
-            FfInfo *inf = info + iq.i;
-            if (4 * lane < A) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) inf->slot[4 * lane + j] = slot[j];
+        bool ok = true;
+        auto post = [&](int n, int nt, int first, int count, const int (&slot)[8]) {
+            // columns [first, first + count) of the group
+            if (!(ok = warp_wait(&info_empty[iq.i], iq.ph ^ 1u, abort_flag))) return;
+            Info *inf = info + iq.i;
+            const int c = 8 * lane - first;
+            if (c >= 0 && c < count) {
+                reinterpret_cast<int4 *>(inf->slot + c)[0] = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                reinterpret_cast<int4 *>(inf->slot + c)[1] = make_int4(slot[4], slot[5], slot[6], slot[7]);
             }
             if (lane == 0) {
                 inf->n = n;
@@ -271,52 +309,96 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&info_full[iq.i]));
             iq.next(kFfInfos);
-            fetch(it + gridDim.x);
-            if (n == 0) continue;
-            bool ok = true;
-            if (lane == 0) {
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!(ok = mbar_wait_bounded(smem_u32(&empty[st.i]), st.ph ^ 1u, abort_flag))) break;
-                    const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
-                    const uint32_t bar = smem_u32(&full[st.i]);
-                    const int xk = kb * (MX ? kFfRowBytes : kFfRowBytes / 2);
-                    if constexpr (MX) {
-                        const int c = 2 * kb;
-                        const uint32_t sbytes = (uint32_t)min(2, p.num_chunks - c) * kSfAtom;
-                        mbar_arrive_expect_tx(bar, kFfWBytes + sbytes);
-                        bulk_load(base + kFfWBytes + p.b_bytes,
-                                  p.w_scales + (((int64_t)ex * p.ntiles + nt) * p.num_chunks + c) * kSfAtom, sbytes, bar);
-                    } else {
-                        mbar_arrive_expect_tx(bar, kFfWBytes);
-                    }
-                    if constexpr (UP) tma_load_5d(base, &tm_w, xk, nt * 4, ex, bar);
-                    else tma_load_3d(base, &tm_w, xk, nt * kFfRows, ex, bar);
-                    ++issued;
-                    st.next(ST);
+        };
+        int it = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+        fetch(it);
+        for (; ok && it < items; it += stride) {
+            const int nt = PAIR ? it % tiles * 2 + (int)rank : it % tiles;
+            int slot[8], top = 0;
+            const int ex = e;
+            if (8 * lane < G * A) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = ent[j];
+                    const bool real = (uint32_t)i < (uint32_t)p.numel;
+                    // neither a slot nor the sentinel: a corrupted align output
+                    if (!real && i != p.numel) set_error(p.err, kErrBadSlot);
+                    slot[j] = real ? i : -1;
+                    if (real) top = j + 1;
                 }
+                if (top) top += 8 * lane;
             }
-            if (!__shfl_sync(0xffffffffu, (int)ok, 0)) break;
+            __syncwarp();
+            fetch(it + stride);
+            for (int g = 0; ok && g < G;) {
+                const int eg = __shfl_sync(0xffffffffu, ex, g * A / 8);
+                int h = g + 1;
+                while (h < G && __shfl_sync(0xffffffffu, ex, h * A / 8) == eg) ++h;
+                const int first = g * A, count = (h - g) * A;
+                const bool mine = 8 * lane >= first && 8 * lane < first + count;
+                const int rows = (int)__reduce_max_sync(0xffffffffu, mine ? (unsigned)top : 0u) - first;
+                g = h;
+                if (rows <= 0) continue;
+                if ((unsigned)eg >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
+                    if (lane == 0) set_error(p.err, kErrBadId);
+                    continue;
+                }
+                post((rows + 15) & ~15, nt, first, count, slot);
+                if (!ok) break;
+                if (lane == 0) {
+                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                        if (!(ok = mbar_wait_bounded(smem_u32(&empty[st.i]), st.ph ^ 1u, abort_flag))) break;
+                        const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
+                        const uint32_t bar = smem_u32(&full[st.i]);
+                        const int xk = kb * (MX ? kFfRowBytes : kFfRowBytes / 2);
+                        if constexpr (PAIR) {
+                            // both CTAs' bytes complete the leader's barrier
+                            if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
+                            const uint32_t fb = cluster_addr(bar, 0u);
+                            if constexpr (UP) tma_load_5d_pair(base, &tm_w, xk, nt * 4, eg, fb);
+                            else tma_load_3d_pair(base, &tm_w, xk, nt * kFfRows, eg, fb);
+                        } else {
+                            uint32_t sbytes = 0;
+                            const int c = 2 * kb;
+                            if constexpr (MX) sbytes = (uint32_t)min(2, p.num_chunks - c) * kSfAtom;
+                            mbar_arrive_expect_tx(bar, kFfWBytes + sbytes);
+                            if constexpr (MX)
+                                bulk_load(base + kFfWBytes + p.b_bytes,
+                                          p.w_scales + (((int64_t)eg * p.ntiles + nt) * p.num_chunks + c) * kSfAtom,
+                                          sbytes, bar);
+                            if constexpr (UP) tma_load_5d(base, &tm_w, xk, nt * 4, eg, bar);
+                            else tma_load_3d(base, &tm_w, xk, nt * kFfRows, eg, bar);
+                        }
+                        ++issued;
+                        st.next(ST);
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            }
         }
+        if (ok) post(-1, 0, 0, 0, ent);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMAs ----
         // The whole warp runs the loop, so that descriptors and addresses stay
-        // in uniform registers; one elected lane issues.
+        // in uniform registers; one elected lane issues (a pair's leader; its
+        // peer only keeps up with the pieces).
         const bool elected = elect_one();
         RingPos st, iq, ac;
-        uint32_t sf = tmem + (uint32_t)(2 * p.A);  // two sets of scale columns in turn: [A 8][B 8]
+        uint32_t sf = tmem + (uint32_t)(2 * p.acc_cols);  // MXFP4: two sets of scale columns in turn: [A 8][B 8]
         bool ok = true;
-        for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        while (ok) {
             if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
-            const int n = __shfl_sync(0xffffffffu, reinterpret_cast<volatile FfInfo *>(info)[iq.i].n, 0);
+            const int n = __shfl_sync(0xffffffffu, reinterpret_cast<volatile Info *>(info)[iq.i].n, 0);
             __syncwarp();
             if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
             iq.next(kFfInfos);
-            if (n == 0) continue;
+            if (n < 0) break;
+            if (rank != 0) continue;
             if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
             tc_fence_after();
-            const uint32_t acc = tmem + (uint32_t)(ac.i * p.A);
-            const uint32_t idesc = MX ? idesc_mxf4(kFfRows, n) : idesc_bf16_f32(kFfRows, n);
+            const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols);
+            const uint32_t idesc = MX ? idesc_mxf4(kFfRows, n) : idesc_bf16_f32(PAIR ? 2 * kFfRows : kFfRows, n);
             for (int kb = 0; kb < p.num_kb; ++kb) {
                 if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
                 tc_fence_after();
@@ -342,24 +424,28 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 } else if (elected) {
                     if (steps == 4) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_bf16(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
+                        for (int kk = 0; kk < 4; ++kk) ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
                     } else {
                         for (int kk = 0; kk < steps; ++kk)
-                            tc_mma_bf16(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
+                            ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
                     }
                 }
-                if (elected) tc_commit(smem_u32(&empty[st.i]));
+                if (elected) ff_commit<PAIR>(&empty[st.i]);
                 st.next(ST);
             }
             if (!ok) break;
-            if (elected) tc_commit(smem_u32(&acc_full[ac.i]));
+            if (elected) ff_commit<PAIR>(&acc_full[ac.i]);
             ac.next(2);
         }
         // every MMA issued is done before TMEM is freed, also after an abort
-        if (elected) tc_commit(smem_u32(last));
-        volatile int never = 0;
-        if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
+        if (rank == 0) {
+            if (elected) {
+                if constexpr (PAIR) tc_commit_pair(smem_u32(last), 0x1);
+                else tc_commit(smem_u32(last));
+            }
+            volatile int never = 0;
+            if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
+        }
         __syncwarp();
     } else if (warp < 2 + kFfLoaders) {
         // ------------------------------------------------ routed rows ----
@@ -367,8 +453,10 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         // copy a row's, chunk c of row r landing at r * 128 + ((c ^ (r & 7)) <<
         // 4), the 128-byte swizzle. A stage's copies are awaited kFfLag stages
         // later, made visible to the tensor core (async proxy) and announced,
-        // one arrival a warp. (kFfLag < stages, or a stage would wait for
-        // itself to be freed.)
+        // one arrival a warp. Stage j is announced after stage j + kFfLag was
+        // issued, at the furthest kFfLag pieces on: that piece's info needs
+        // the slot of one before j's piece, and its stage one before j.
+        static_assert(kFfInfos > kFfLag, "a piece would wait for its own info slot to be freed");
         const int t = threadIdx.x - 64, c = t & 7, r0 = t >> 3;
         constexpr int kStep = 32 * kFfLoaders / 8;  // rows that all loaders copy at once
         constexpr int kRows = kFfRows / kStep;      // of a thread, at most
@@ -377,20 +465,23 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         auto announce = [&]() {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[done.i]));
+            if (lane == 0) {
+                if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&full[done.i]), 0u));
+                else mbar_arrive(smem_u32(&full[done.i]));
+            }
             done.next(ST);
         };
         bool ok = true;
-        for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
-            ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
-            if (!ok) break;
-            const volatile FfInfo *inf = info + iq.i;
-            const int n = inf->n;
+        while (ok) {
+            if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+            const volatile Info *inf = info + iq.i;
+            // this CTA's rows are columns [col0, col0 + n)
+            const int all = inf->n, n = PAIR ? all / 2 : all, col0 = (int)rank * n;
             const uint8_t *src[kRows], *ssrc = nullptr;
             // a column without a slot reads row 0; it is not stored
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
-                const int r = r0 + j * kStep, i = r < n ? inf->slot[r] : -1;
+                const int r = r0 + j * kStep, i = r < n ? inf->slot[col0 + r] : -1;
                 src[j] = p.x + (int64_t)(i < 0 ? 0 : i / p.div) * p.x_row_bytes + c * 16;
             }
             if constexpr (MX) {
@@ -400,11 +491,10 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
             iq.next(kFfInfos);
-            if (n == 0) continue;
+            if (all < 0) break;
             const uint32_t dst = ring + kFfWBytes + (uint32_t)(r0 * kFfRowBytes + ((c ^ (r0 & 7)) << 4));
             for (int kb = 0; kb < p.num_kb; ++kb) {
-                ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag);
-                if (!ok) break;
+                if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
                 const uint32_t d = dst + (uint32_t)st.i * p.stage_bytes;
                 // (chunks past the row's end are not read by the last MMA steps)
                 if (kb * kFfRowBytes + c * 16 < p.x_bytes) {
@@ -439,71 +529,70 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         const int q = warp & 3;
         RingPos iq, ac;
         bool ok = true;
-        for (int it = blockIdx.x; ok && it < items; it += gridDim.x) {
-            ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
-            if (!ok) break;
-            const FfInfo *inf = info + iq.i;
+        while (ok) {
+            if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+            const Info *inf = info + iq.i;
             const int n = inf->n;
-            if (n > 0) {
-                ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.A);
-                // this lane's store: 4 features from f of column (lane & 3) of
-                // every four
-                const int f = UP ? inf->nt * 64 + q * 16 + (lane & 12) : inf->nt * kFfRows + q * 32 + (lane & 28);
-                const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
-                uint16_t *out = p.out + f;
-                uint32_t v[16], next[16];
-                tmem_ld16_async(acc, v);
-                tmem_wait_ld16(v);
-                for (int c0 = 0; c0 < n; c0 += 16) {
-                    if (c0 + 16 < n) tmem_ld16_async(acc + (uint32_t)(c0 + 16), next);
-                    if constexpr (UP) {
-                        // lanes 0-15 hold gate rows, 16-31 the same features'
-                        // up rows: each half of the warp takes every other
-                        // column and gets its missing factor from the other
-                        const bool hi = lane >= 16;
-                        const int *cols = inf->slot + c0 + 2 * (lane & 3) + (hi ? 1 : 0);
-                        const int i0 = cols[0], i1 = cols[8];
-                        float a[8];
+            if (n < 0) break;
+            if (!(ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.acc_cols);
+            // this lane's store: 4 features from f of column (lane & 3) of
+            // every four
+            const int f = UP ? inf->nt * 64 + q * 16 + (lane & 12) : inf->nt * kFfRows + q * 32 + (lane & 28);
+            const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
+            uint16_t *out = p.out + f;
+            uint32_t v[16], next[16];
+            tmem_ld16_async(acc, v);
+            tmem_wait_ld16(v);
+            for (int c0 = 0; c0 < n; c0 += 16) {
+                if (c0 + 16 < n) tmem_ld16_async(acc + (uint32_t)(c0 + 16), next);
+                if constexpr (UP) {
+                    // lanes 0-15 hold gate rows, 16-31 the same features' up
+                    // rows: each half of the warp takes every other column
+                    // and gets its missing factor from the other
+                    const bool hi = lane >= 16;
+                    const int *cols = inf->slot + c0 + 2 * (lane & 3) + (hi ? 1 : 0);
+                    const int i0 = cols[0], i1 = cols[8];
+                    float a[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? v[2 * j] : v[2 * j + 1], 16);
-                            const float g = __uint_as_float(hi ? got : v[2 * j]);
-                            const float u = __uint_as_float(hi ? v[2 * j + 1] : got);
-                            a[j] = swiglu(g, u);
-                        }
-                        const uint2 s0 = quad_pack(a[0], a[1], a[2], a[3], lane);
-                        const uint2 s1 = quad_pack(a[4], a[5], a[6], a[7], lane);
-                        if (i0 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i0 * p.feat) = s0;
-                        if (i1 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i1 * p.feat) = s1;
-                    } else {
-                        int i[4];
-                        uint2 s[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) i[j] = inf->slot[c0 + 4 * j + (lane & 3)];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            s[j] = quad_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), lane);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (i[j] >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i[j] * p.feat) = s[j];
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? v[2 * j] : v[2 * j + 1], 16);
+                        const float g = __uint_as_float(hi ? got : v[2 * j]);
+                        const float u = __uint_as_float(hi ? v[2 * j + 1] : got);
+                        a[j] = swiglu(g, u);
                     }
-                    if (c0 + 16 < n) {
-                        tmem_wait_ld16(next);
+                    const uint2 s0 = quad_pack(a[0], a[1], a[2], a[3], lane);
+                    const uint2 s1 = quad_pack(a[4], a[5], a[6], a[7], lane);
+                    if (i0 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i0 * p.feat) = s0;
+                    if (i1 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i1 * p.feat) = s1;
+                } else {
+                    int i[4];
+                    uint2 s[4];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = next[j];
-                    }
+                    for (int j = 0; j < 4; ++j) i[j] = inf->slot[c0 + 4 * j + (lane & 3)];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[j] = quad_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                         __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), lane);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (i[j] >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i[j] * p.feat) = s[j];
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&acc_empty[ac.i]));
-                ac.next(2);
+                if (c0 + 16 < n) {
+                    tmem_wait_ld16(next);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = next[j];
+                }
             }
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
+            if (lane == 0) {
+                if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[ac.i]), 0u));
+                else mbar_arrive(smem_u32(&acc_empty[ac.i]));
+                mbar_arrive(smem_u32(&info_empty[iq.i]));
+            }
+            ac.next(2);
             iq.next(kFfInfos);
         }
         __syncwarp();
@@ -512,15 +601,24 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     tc_fence_before();
     __syncthreads();
     if (*abort_flag && warp == 0 && lane == 0) {
-        // a wait gave up: the item's outputs are not written; weights still in
+        // a wait gave up: the piece's outputs are not written; weights still in
         // flight land before the CTA leaves
         set_error(p.err, kErrWaitTimeout);
-        for (int j = issued - ST > 0 ? issued - ST : 0; j < issued; ++j) {
-            volatile int drain = 0;
-            mbar_wait_bounded(smem_u32(&full[j % ST]), (uint32_t)(j / ST) & 1u, &drain);
-        }
+        if (rank == 0)
+            for (int j = issued - ST > 0 ? issued - ST : 0; j < issued; ++j) {
+                volatile int drain = 0;
+                mbar_wait_bounded(smem_u32(&full[j % ST]), (uint32_t)(j / ST) & 1u, &drain);
+            }
     }
-    if (warp == 1) {
+    if constexpr (PAIR) {
+        // no barrier of either CTA can still be signalled, both are done with TMEM
+        __syncwarp();
+        cluster_sync();
+        if (warp == 1) {
+            tc_fence_after();
+            tmem_dealloc_pair(tmem, (uint32_t)p.tmem_cols);
+        }
+    } else if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, (uint32_t)p.tmem_cols);
     }
@@ -572,6 +670,9 @@ expert_combine_kernel(const uint16_t *__restrict__ y, const int32_t *__restrict_
 
 // ---------------------------------------------------------------- host --
 
+// CTA pairs from this many rows an expert, on average.
+constexpr int kPairRows = 96;
+
 static int sm_count() {
     static std::atomic<int> cached[kMaxDevices];
     int dev = 0;
@@ -606,7 +707,7 @@ static bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const v
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool MX, bool UP>
+template <bool MX, bool UP, bool PAIR>
 static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stream) {
     FfParams p{};
     const int per_block = MX ? 256 : 64, step = MX ? 64 : 16;  // values of K in a k-block, in an MMA
@@ -628,14 +729,15 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.w_scales = a.w_scales;
     p.num_chunks = a.K / 128;
     p.err = &reinterpret_cast<WsHeader *>(a.hdr)->error;
-    p.b_bytes = (uint32_t)a.A * kFfRowBytes;
+    p.b_bytes = (uint32_t)(PAIR ? kFfRows : a.A) * kFfRowBytes;
     p.stage_bytes = kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0);
     constexpr uint32_t kSmemMax = 232448;
-    p.stages = (int)((kSmemMax - 1024 - kFfMiscBytes) / p.stage_bytes);
-    if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
-    const int cols = 2 * a.A + (MX ? 32 : 0);
+    p.stages = (int)((kSmemMax - 1024 - kFfMiscBytes<PAIR>) / p.stage_bytes);
+    if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;  // (6 at the least, above kFfLag)
+    p.acc_cols = PAIR ? kFfCols<PAIR> : a.A;
+    const int cols = 2 * p.acc_cols + (MX ? 32 : 0);
     p.tmem_cols = cols <= 128 ? 128 : (cols <= 256 ? 256 : 512);
-    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + kFfMiscBytes;
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + kFfMiscBytes<PAIR>;
 
     const CUtensorMapDataType type = MX ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const cuuint64_t k_elems = (cuuint64_t)(MX ? a.K / 2 : a.K), k_bytes = MX ? k_elems : 2 * k_elems;
@@ -661,34 +763,46 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
 
     static std::atomic<bool> configured[kMaxDevices];
     const cudaError_t e = once_per_device(configured, [](int) {
-        cudaError_t r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kSmemMax);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP>, cudaFuncAttributePreferredSharedMemoryCarveout,
+            r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         return r;
     });
     if (e != cudaSuccess) return e;
-    const int most = p.max_blocks * p.ntiles;
+    // one CTA (pair) per item, at most one CTA per SM
+    const int G = 256 / a.A;
+    const int most = PAIR ? (p.max_blocks + G - 1) / G * ((p.ntiles + 1) / 2) * 2 : p.max_blocks * p.ntiles;
+    const int room = PAIR ? sms / 2 * 2 : sms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms), 1, 1);
+    cfg.gridDim = dim3((unsigned)(most < room ? most : room), 1, 1);
     cfg.blockDim = dim3(kFfThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP>, mw, p);
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP, PAIR>, mw, p);
 }
 
 cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream) {
     const int sms = sm_count();
-    if (sms < 1) return cudaErrorInvalidDevice;
-    const bool mx = a.x_scales != nullptr;
-    if (a.gated) return mx ? launch_product<true, true>(a, sms, stream) : launch_product<false, true>(a, sms, stream);
-    return mx ? launch_product<true, false>(a, sms, stream) : launch_product<false, false>(a, sms, stream);
+    if (sms < 2) return cudaErrorInvalidDevice;
+    if (a.x_scales != nullptr)
+        return a.gated ? launch_product<true, true, false>(a, sms, stream)
+                       : launch_product<true, false, false>(a, sms, stream);
+    if (a.numel >= (int64_t)kPairRows * a.num_experts)
+        return a.gated ? launch_product<false, true, true>(a, sms, stream)
+                       : launch_product<false, false, true>(a, sms, stream);
+    return a.gated ? launch_product<false, true, false>(a, sms, stream)
+                   : launch_product<false, false, false>(a, sms, stream);
 }
 
 cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream) {
