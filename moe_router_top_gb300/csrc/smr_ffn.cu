@@ -34,7 +34,9 @@ constexpr int kFfRowBytes = 128;                 // one k-block of a row: 64 bf1
 constexpr int kFfWBytes = kFfRows * kFfRowBytes;  // weight tile of a stage
 constexpr int kFfMaxStages = 9;
 constexpr int kFfLag = 2;                        // stages that a row loader issues before it announces one
-constexpr int kFfInfos = 3;                      // pieces of work known ahead of the epilogue
+// Pieces of work known ahead of the epilogue: with a short contraction (MXFP4,
+// K = 512: two k-blocks a piece) these bound the weights in flight.
+constexpr int kFfInfos = 8;
 constexpr int kSfAtom = 512;                     // scales of 128 rows x 4 blocks (128 values of K)
 
 // What the producer tells the other warps about a piece of work: one expert's
@@ -45,6 +47,7 @@ struct FfInfo {
     int nt;    // weight tile of this CTA
     int pad[2];
     int slot[COLS];  // flat slot of every column, -1: none
+    int row[COLS];   // its row of x (0 for a column without a slot, which is not stored)
 };
 constexpr int kFfBars = 2 * kFfMaxStages + 4 + 2 * kFfInfos + 1;
 constexpr int kFfBarBytes = (kFfBars * 8 + 8 + 15) / 16 * 16;
@@ -59,7 +62,9 @@ struct FfParams {
     const uint8_t *x;
     int64_t x_row_bytes;     // between rows of x
     int x_bytes;             // of a row of x
-    int div;                 // row of x = slot / div (the width for the gated product, else 1)
+    // row of x = slot / width (gated product), exact for slots below 2^30 as
+    // slot * div_mul >> div_shift
+    uint32_t div_mul, div_shift;
     int num_experts, A, stages;
     int acc_cols, tmem_cols; // TMEM columns of an accumulator, of the allocation
     int64_t sorted_cap;
@@ -299,8 +304,17 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             Info *inf = info + iq.i;
             const int c = 8 * lane - first;
             if (c >= 0 && c < count) {
-                reinterpret_cast<int4 *>(inf->slot + c)[0] = make_int4(slot[0], slot[1], slot[2], slot[3]);
-                reinterpret_cast<int4 *>(inf->slot + c)[1] = make_int4(slot[4], slot[5], slot[6], slot[7]);
+                int row[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t i = slot[j] < 0 ? 0u : (uint32_t)slot[j];
+                    row[j] = UP ? (int)((uint64_t)i * p.div_mul >> p.div_shift) : (int)i;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    *reinterpret_cast<int4 *>(inf->slot + c + j) = make_int4(slot[j], slot[j + 1], slot[j + 2], slot[j + 3]);
+                    *reinterpret_cast<int4 *>(inf->row + c + j) = make_int4(row[j], row[j + 1], row[j + 2], row[j + 3]);
+                }
             }
             if (lane == 0) {
                 inf->n = n;
@@ -478,16 +492,13 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             // this CTA's rows are columns [col0, col0 + n)
             const int all = inf->n, n = PAIR ? all / 2 : all, col0 = (int)rank * n;
             const uint8_t *src[kRows], *ssrc = nullptr;
-            // a column without a slot reads row 0; it is not stored
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
-                const int r = r0 + j * kStep, i = r < n ? inf->slot[col0 + r] : -1;
-                src[j] = p.x + (int64_t)(i < 0 ? 0 : i / p.div) * p.x_row_bytes + c * 16;
+                const int r = r0 + j * kStep;
+                if (r < n) src[j] = p.x + (int64_t)inf->row[col0 + r] * p.x_row_bytes + c * 16;
             }
-            if constexpr (MX) {
-                const int i = t < n ? inf->slot[t] : -1;
-                ssrc = p.x_scales + (int64_t)(i < 0 ? 0 : i / p.div) * (p.num_chunks * 4);
-            }
+            if constexpr (MX)
+                if (t < n) ssrc = p.x_scales + (int64_t)inf->row[t] * (p.num_chunks * 4);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
             iq.next(kFfInfos);
@@ -715,7 +726,9 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.last_steps = (a.K - (p.num_kb - 1) * per_block + step - 1) / step;
     p.feat = a.feat;
     p.ntiles = UP ? (a.feat + 63) / 64 : (a.feat + kFfRows - 1) / kFfRows;
-    p.div = UP ? a.width : 1;
+    p.div_shift = 30;
+    while ((1ll << (p.div_shift - 30)) < a.width) ++p.div_shift;
+    p.div_mul = (uint32_t)(((1ull << p.div_shift) + (uint64_t)a.width - 1) / (uint64_t)a.width);
     p.num_experts = a.num_experts;
     p.A = a.A;
     p.numel = (int)a.numel;
