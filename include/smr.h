@@ -187,7 +187,8 @@ typedef struct smr_expert_up_args {
     int32_t num_experts;           /* the align's num_experts (or num_physical), 1..1025 */
     int32_t block_size;            /* A used by the align: 64 or 128 */
     const void *x;                 /* bf16 [T, ld_x], or MXFP4 codes uint8 [T, H / 2]; 16-byte aligned */
-    int64_t ld_x;                  /* bf16: row stride in elements, >= H, multiple of 8; MXFP4: ignored */
+    int64_t ld_x;                  /* bf16: row stride in elements, >= H, multiple of 8, <= 2^30; MXFP4:
+                                      ignored */
     const uint8_t *x_scales;       /* MXFP4: uint8 [T, H / 32], 4-byte aligned; NULL: x and w are bf16 */
     const void *w;                 /* bf16 [num_experts, 2 I, H] (I gate rows, then I up rows), or
                                       MXFP4 codes uint8 [num_experts, 2 I, H / 2]; 16-byte aligned */

@@ -732,6 +732,7 @@ SMR_API smr_status smr_expert_up(const smr_expert_up_args *a, void *workspace, s
     check_ffn(c, r);
     if (!a->x_scales && a->num_tokens > 0 && (a->ld_x < a->H || a->ld_x % 8 != 0))
         r.bad("ld_x must be >= H and a multiple of 8 (got " + std::to_string(a->ld_x) + ")");
+    else if (!a->x_scales && a->num_tokens > 0 && a->ld_x > (int64_t)1 << 30) r.unsup("ld_x must be <= 2^30");
     if (!r.ok()) return r.finish("smr_expert_up");
     if (a->num_tokens == 0) return SMR_OK;
     smr_status st = check_ws(workspace, workspace_bytes, kHeaderBytes, "smr_expert_up");

@@ -13,8 +13,9 @@
 // GB300 design: one persistent CTA per SM over (block, weight tile) items,
 // tiles of one block next to each other (its rows stay in L2; blocks of one
 // expert follow each other, so its weights do too). Warp roles: 0 loads the
-// weights by TMA, 1 issues the MMAs, 2-5 load the routed rows (and their block
-// scales) with asynchronous 16-byte copies, 6-9 drain TMEM. (A TMA gather
+// weights by TMA, 1 issues the MMAs, 2 reads the align's outputs ahead and
+// hands out the work, 3-8 load the routed rows (and their block scales) with
+// asynchronous 16-byte copies, 9-12 drain TMEM. (A TMA gather
 // takes 4 rows an instruction and about 70 cycles each: 128 rows took 2300
 // cycles a k-block, 3300 us for 16384 tokens.) The stage ring runs across
 // items; accumulators are double-buffered in TMEM, so the epilogue of one item
@@ -27,13 +28,12 @@
 
 namespace smr {
 
-constexpr int kFfLoaders = 4;                    // warps that load the routed rows
-constexpr int kFfThreads = 32 * (2 + kFfLoaders + 4);
+constexpr int kFfLoaders = 6;                    // warps that load the routed rows; at most the stages
+constexpr int kFfThreads = 32 * (3 + kFfLoaders + 4);
 constexpr int kFfRows = 128;                     // weight rows of a tile (the MMA's M)
 constexpr int kFfRowBytes = 128;                 // one k-block of a row: 64 bf16 or 256 MXFP4
 constexpr int kFfWBytes = kFfRows * kFfRowBytes;  // weight tile of a stage
 constexpr int kFfMaxStages = 9;
-constexpr int kFfLag = 2;                        // stages that a row loader issues before it announces one
 // Pieces of work known ahead of the epilogue: with a short contraction (MXFP4,
 // K = 512: two k-blocks a piece) these bound the weights in flight.
 constexpr int kFfInfos = 8;
@@ -45,7 +45,8 @@ template <int COLS>
 struct FfInfo {
     int n;     // MMA columns (16..COLS, a multiple of 16); -1: no more work
     int nt;    // weight tile of this CTA
-    int pad[2];
+    int e;     // expert
+    int pad;
     int slot[COLS];  // flat slot of every column, -1: none
     int row[COLS];   // its row of x (0 for a column without a slot, which is not stored)
 };
@@ -60,7 +61,7 @@ struct FfParams {
     int num_kb, last_steps;  // k-blocks; MMA steps of the last one (4 in the others)
     int feat, ntiles;        // output features; weight tiles
     const uint8_t *x;
-    int64_t x_row_bytes;     // between rows of x
+    uint32_t x_row_bytes;    // between rows of x
     int x_bytes;             // of a row of x
     // row of x = slot / width (gated product), exact for slots below 2^30 as
     // slot * div_mul >> div_shift
@@ -205,6 +206,9 @@ struct RingPos {
             ph ^= 1u;
         }
     }
+    __device__ __forceinline__ void skip(int by, int n) {
+        for (i += by; i >= n; i -= n) ph ^= 1u;
+    }
 };
 
 // MX: MXFP4 operands, else bf16. UP: the gated product (a tile holds 64
@@ -238,8 +242,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            // the weights' bytes, and the row loaders' arrivals
-            mbar_init(smem_u32(&full[s]), 1 + (PAIR ? 2 : 1) * kFfLoaders);
+            mbar_init(smem_u32(&full[s]), PAIR ? 3 : 2);  // the weights' bytes, the row loader (of each CTA)
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -248,7 +251,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         }
         for (int s = 0; s < kFfInfos; ++s) {
             mbar_init(smem_u32(&info_full[s]), 1);
-            mbar_init(smem_u32(&info_empty[s]), 1 + kFfLoaders + 4);  // issuer, row loaders, epilogue
+            mbar_init(smem_u32(&info_empty[s]), 2 + kFfLoaders + 4);  // every warp but the scout
         }
         mbar_init(smem_u32(last), 1);
         *abort_flag = 0;
@@ -273,32 +276,93 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     griddep_wait();  // the align's outputs and x come from previous kernels
 
     const uint32_t ring = smem_u32(smem);
-    int issued = 0;  // stages whose weights were requested (producer lane 0)
+    int issued = 0;  // stages whose weights were requested (warp 0)
 
     if (warp == 0) {
         // ---------------------------------------------------- weights ----
-        // An item is a group of 1 (PAIR: 256 / A) aligned blocks and a weight
-        // tile (PAIR: two). Blocks of a group that share an expert make one
-        // piece of work. Both CTAs of a pair walk the same pieces.
-        const int A = p.A, G = PAIR ? 256 / A : 1;
-        const int nblk = max(0, min(__ldcg(p.npp) / A, p.max_blocks));
-        const int tiles = PAIR ? (p.ntiles + 1) / 2 : p.ntiles;
-        const int items = (nblk + G - 1) / G * tiles;
-        const int stride = PAIR ? gridDim.x >> 1 : gridDim.x;
-        int ent[8], e = -1;  // this lane's 8 entries of the group, their block's expert
-        // requested an item ahead
-        auto fetch = [&](int it) {
-            const int in = 8 * lane, b = it / tiles * G + in / A;
-            if (it >= items || in >= G * A) return;
-            const int64_t at = (int64_t)b * A + in % A;
-            e = b < nblk ? __ldcg(p.eids + b) : -1;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                ent[j] = b < nblk && at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
-        };
+        const bool elected = elect_one();
         RingPos st, iq;
         bool ok = true;
-        auto post = [&](int n, int nt, int first, int count, const int (&slot)[8]) {
+        while (ok) {
+            if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+            const volatile Info *inf = info + iq.i;
+            const int n = inf->n, nt = inf->nt, e = inf->e;
+            __syncwarp();
+            if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
+            iq.next(kFfInfos);
+            if (n < 0) break;
+            const uint8_t *scales = nullptr;
+            if constexpr (MX) scales = p.w_scales + ((int64_t)e * p.ntiles + nt) * p.num_chunks * kSfAtom;
+            for (int kb = 0; kb < p.num_kb; ++kb) {
+                if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
+                const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
+                const uint32_t bar = smem_u32(&full[st.i]);
+                const int xk = kb * (MX ? kFfRowBytes : kFfRowBytes / 2);
+                if (elected) {
+                    if constexpr (PAIR) {
+                        // both CTAs' bytes complete the leader's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
+                        const uint32_t fb = cluster_addr(bar, 0u);
+                        if constexpr (UP) tma_load_5d_pair(base, &tm_w, xk, nt * 4, e, fb);
+                        else tma_load_3d_pair(base, &tm_w, xk, nt * kFfRows, e, fb);
+                    } else {
+                        uint32_t sbytes = 0;
+                        if constexpr (MX) sbytes = (uint32_t)min(2, p.num_chunks - 2 * kb) * kSfAtom;
+                        mbar_arrive_expect_tx(bar, kFfWBytes + sbytes);
+                        if constexpr (UP) tma_load_5d(base, &tm_w, xk, nt * 4, e, bar);
+                        else tma_load_3d(base, &tm_w, xk, nt * kFfRows, e, bar);
+                        if constexpr (MX)
+                            bulk_load(base + kFfWBytes + p.b_bytes, scales + 2 * kb * kSfAtom, sbytes, bar);
+                    }
+                }
+                ++issued;
+                st.next(ST);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------ scout ----
+        // An item is a group of 1 (PAIR: 256 / A) aligned blocks and a weight
+        // tile (PAIR: two). Blocks of a group that share an expert make one
+        // piece of work. Both CTAs of a pair walk the same pieces. CTAs take
+        // every gridDim-th item: a block's tiles run next to each other in
+        // time (its rows stay in L2), blocks of one expert too (its weights).
+        const int A = p.A, G = PAIR ? 256 / A : 1;
+        const int tiles = PAIR ? (p.ntiles + 1) / 2 : p.ntiles;
+        const int ctas = PAIR ? gridDim.x >> 1 : gridDim.x, cta = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+        const int dgrp = ctas / tiles, dtile = ctas % tiles;
+        int grp = cta / tiles, tile = cta % tiles;  // the item
+        const int bo = 8 * lane / A, po = 8 * lane % A;  // this lane's 8 entries: block of the group, place in it
+        const bool in = bo < G;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.sorted) & 15) == 0;
+        // the entries and the block's expert, requested two items ahead (a
+        // round trip to L2 is longer than a short item)
+        auto fetch = [&](int g, int (&ent)[8], int &e) {
+            const int b = g * G + bo;
+            if (!in || b >= p.max_blocks) return;
+            const int64_t at = (int64_t)b * A + po;
+            e = __ldcg(p.eids + b);
+            if (wide && at + 8 <= p.sorted_cap) {
+                const int4 lo = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at));
+                const int4 hi = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at) + 1);
+                ent[0] = lo.x; ent[1] = lo.y; ent[2] = lo.z; ent[3] = lo.w;
+                ent[4] = hi.x; ent[5] = hi.y; ent[6] = hi.z; ent[7] = hi.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ent[j] = at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
+            }
+        };
+        auto step = [&](int &g, int &t) {
+            g += dgrp;
+            t += dtile;
+            if (t >= tiles) {
+                t -= tiles;
+                ++g;
+            }
+        };
+        RingPos iq;
+        bool ok = true;
+        auto post = [&](int n, int nt, int e, int first, int count, const int (&slot)[8]) {
             // columns [first, first + count) of the group
             if (!(ok = warp_wait(&info_empty[iq.i], iq.ph ^ 1u, abort_flag))) return;
             Info *inf = info + iq.i;
@@ -316,34 +380,38 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     *reinterpret_cast<int4 *>(inf->row + c + j) = make_int4(row[j], row[j + 1], row[j + 2], row[j + 3]);
                 }
             }
-            if (lane == 0) {
-                inf->n = n;
-                inf->nt = nt;
-            }
+            if (lane == 0) *reinterpret_cast<int4 *>(inf) = make_int4(n, nt, e, 0);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&info_full[iq.i]));
             iq.next(kFfInfos);
         };
-        int it = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-        fetch(it);
-        for (; ok && it < items; it += stride) {
-            const int nt = PAIR ? it % tiles * 2 + (int)rank : it % tiles;
-            int slot[8], top = 0;
-            const int ex = e;
-            if (8 * lane < G * A) {
+        int ent0[8], ent1[8], e0 = -1, e1 = -1, slot[8];
+        int grp1 = grp, tile1 = tile;
+        step(grp1, tile1);
+        const int npp = __ldcg(p.npp);
+        fetch(grp, ent0, e0);
+        fetch(grp1, ent1, e1);
+        const int nblk = max(0, min(npp / A, p.max_blocks)), groups = (nblk + G - 1) / G;
+        auto run = [&](int (&ent)[8], int &e) {
+            // the item (grp, tile), whose entries are ent; then moves on
+            int top = 0;
+            const bool mine_in = in && grp * G + bo < nblk;
+            const int ex = mine_in ? e : -1;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int i = ent[j];
-                    const bool real = (uint32_t)i < (uint32_t)p.numel;
-                    // neither a slot nor the sentinel: a corrupted align output
-                    if (!real && i != p.numel) set_error(p.err, kErrBadSlot);
-                    slot[j] = real ? i : -1;
-                    if (real) top = j + 1;
-                }
-                if (top) top += 8 * lane;
+            for (int j = 0; j < 8; ++j) {
+                const int i = mine_in ? ent[j] : p.numel;
+                const bool real = (uint32_t)i < (uint32_t)p.numel;
+                // neither a slot nor the sentinel: a corrupted align output
+                if (!real && i != p.numel) set_error(p.err, kErrBadSlot);
+                slot[j] = real ? i : -1;
+                if (real) top = 8 * lane + j + 1;
             }
             __syncwarp();
-            fetch(it + stride);
+            const int nt = PAIR ? 2 * tile + (int)rank : tile;
+            step(grp, tile);
+            int grp2 = grp, tile2 = tile;
+            step(grp2, tile2);
+            if (grp2 < groups) fetch(grp2, ent, e);
             for (int g = 0; ok && g < G;) {
                 const int eg = __shfl_sync(0xffffffffu, ex, g * A / 8);
                 int h = g + 1;
@@ -355,42 +423,17 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (rows <= 0) continue;
                 if ((unsigned)eg >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
                     if (lane == 0) set_error(p.err, kErrBadId);
+                    __syncwarp();
                     continue;
                 }
-                post((rows + 15) & ~15, nt, first, count, slot);
-                if (!ok) break;
-                if (lane == 0) {
-                    for (int kb = 0; kb < p.num_kb; ++kb) {
-                        if (!(ok = mbar_wait_bounded(smem_u32(&empty[st.i]), st.ph ^ 1u, abort_flag))) break;
-                        const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
-                        const uint32_t bar = smem_u32(&full[st.i]);
-                        const int xk = kb * (MX ? kFfRowBytes : kFfRowBytes / 2);
-                        if constexpr (PAIR) {
-                            // both CTAs' bytes complete the leader's barrier
-                            if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
-                            const uint32_t fb = cluster_addr(bar, 0u);
-                            if constexpr (UP) tma_load_5d_pair(base, &tm_w, xk, nt * 4, eg, fb);
-                            else tma_load_3d_pair(base, &tm_w, xk, nt * kFfRows, eg, fb);
-                        } else {
-                            uint32_t sbytes = 0;
-                            const int c = 2 * kb;
-                            if constexpr (MX) sbytes = (uint32_t)min(2, p.num_chunks - c) * kSfAtom;
-                            mbar_arrive_expect_tx(bar, kFfWBytes + sbytes);
-                            if constexpr (MX)
-                                bulk_load(base + kFfWBytes + p.b_bytes,
-                                          p.w_scales + (((int64_t)eg * p.ntiles + nt) * p.num_chunks + c) * kSfAtom,
-                                          sbytes, bar);
-                            if constexpr (UP) tma_load_5d(base, &tm_w, xk, nt * 4, eg, bar);
-                            else tma_load_3d(base, &tm_w, xk, nt * kFfRows, eg, bar);
-                        }
-                        ++issued;
-                        st.next(ST);
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                post((rows + 15) & ~15, nt, eg, first, count, slot);
             }
+        };
+        while (ok && grp < groups) {
+            run(ent0, e0);
+            if (ok && grp < groups) run(ent1, e1);
         }
-        if (ok) post(-1, 0, 0, 0, ent);
+        if (ok) post(-1, 0, 0, 0, 0, slot);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMAs ----
@@ -461,79 +504,69 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
         }
         __syncwarp();
-    } else if (warp < 2 + kFfLoaders) {
+    } else if (warp < 3 + kFfLoaders) {
         // ------------------------------------------------ routed rows ----
-        // A row's k-block is eight 16-byte chunks; eight neighbouring threads
+        // Each loader warp fills every kFfLoaders-th stage, so that a stage is
+        // waited for, copied, made visible to the tensor core (async proxy)
+        // and announced by one warp, while the others' copies are in flight.
+        // A row's k-block is eight 16-byte chunks; eight neighbouring lanes
         // copy a row's, chunk c of row r landing at r * 128 + ((c ^ (r & 7)) <<
-        // 4), the 128-byte swizzle. A stage's copies are awaited kFfLag stages
-        // later, made visible to the tensor core (async proxy) and announced,
-        // one arrival a warp. Stage j is announced after stage j + kFfLag was
-        // issued, at the furthest kFfLag pieces on: that piece's info needs
-        // the slot of one before j's piece, and its stage one before j.
-        static_assert(kFfInfos > kFfLag, "a piece would wait for its own info slot to be freed");
-        const int t = threadIdx.x - 64, c = t & 7, r0 = t >> 3;
-        constexpr int kStep = 32 * kFfLoaders / 8;  // rows that all loaders copy at once
-        constexpr int kRows = kFfRows / kStep;      // of a thread, at most
-        RingPos st, iq, done;
-        int pending = 0;
-        auto announce = [&]() {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&full[done.i]), 0u));
-                else mbar_arrive(smem_u32(&full[done.i]));
-            }
-            done.next(ST);
-        };
+        // 4), the 128-byte swizzle.
+        // A parity wait tells a stage's last use from the one before only: a
+        // warp that waits for stage j (counted over all uses) must know that
+        // j - 2 * ST was consumed. It waited for j - kFfLoaders, so everything
+        // up to j - kFfLoaders - ST was: hence kFfLoaders <= ST.
+        const int c = lane & 7;
+        RingPos st, iq;
+        int next = warp - 3;  // this warp's next stage, counted from the piece's first
+        st.skip(next, ST);
         bool ok = true;
         while (ok) {
             if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
             const volatile Info *inf = info + iq.i;
+            const int all = inf->n;
             // this CTA's rows are columns [col0, col0 + n)
-            const int all = inf->n, n = PAIR ? all / 2 : all, col0 = (int)rank * n;
-            const uint8_t *src[kRows], *ssrc = nullptr;
-#pragma unroll
-            for (int j = 0; j < kRows; ++j) {
-                const int r = r0 + j * kStep;
-                if (r < n) src[j] = p.x + (int64_t)inf->row[col0 + r] * p.x_row_bytes + c * 16;
+            const int n = PAIR ? all / 2 : all, col0 = (int)rank * n;
+            if (all >= 0) {
+                for (; next < p.num_kb; next += kFfLoaders) {
+                    if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
+                    const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes + kFfWBytes;
+                    const int off = next * kFfRowBytes + c * 16;
+                    // (chunks past the row's end are not read by the last MMA steps)
+                    if (off < p.x_bytes) {
+                        const uint8_t *x = p.x + off;
+#pragma unroll 4
+                        for (int r = lane >> 3; r < n; r += 4)
+                            cp_async_16(base + (uint32_t)(r * kFfRowBytes + ((c ^ (r & 7)) << 4)),
+                                        x + (uint64_t)(uint32_t)inf->row[col0 + r] * p.x_row_bytes);
+                    }
+                    if constexpr (MX) {
+                        // scale of row r, block q of a 128-value piece: byte
+                        // (r % 32) * 16 + (r / 32) * 4 + q of its 512
+                        const uint32_t sd = base + p.b_bytes + 2 * kSfAtom + lane * 16;
+                        const bool two = 2 * next + 1 < p.num_chunks;
+                        for (int r = lane; r < n; r += 32) {
+                            const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)inf->row[r] * (uint32_t)p.num_chunks + 2 * next) * 4;
+                            cp_async_4(sd + (r >> 5) * 4, src);
+                            if (two) cp_async_4(sd + kSfAtom + (r >> 5) * 4, src + 4);
+                        }
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&full[st.i]), 0u));
+                        else mbar_arrive(smem_u32(&full[st.i]));
+                    }
+                    st.skip(kFfLoaders, ST);
+                }
+                next -= p.num_kb;
             }
-            if constexpr (MX)
-                if (t < n) ssrc = p.x_scales + (int64_t)inf->row[t] * (p.num_chunks * 4);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
             iq.next(kFfInfos);
             if (all < 0) break;
-            const uint32_t dst = ring + kFfWBytes + (uint32_t)(r0 * kFfRowBytes + ((c ^ (r0 & 7)) << 4));
-            for (int kb = 0; kb < p.num_kb; ++kb) {
-                if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
-                const uint32_t d = dst + (uint32_t)st.i * p.stage_bytes;
-                // (chunks past the row's end are not read by the last MMA steps)
-                if (kb * kFfRowBytes + c * 16 < p.x_bytes) {
-#pragma unroll
-                    for (int j = 0; j < kRows; ++j)
-                        if (r0 + j * kStep < n) cp_async_16(d + j * (kStep * kFfRowBytes), src[j] + kb * kFfRowBytes);
-                }
-                if constexpr (MX) {
-                    // scale of row r, block q of a 128-value piece: byte
-                    // (r % 32) * 16 + (r / 32) * 4 + q of its 512
-                    const uint32_t sd = ring + (uint32_t)st.i * p.stage_bytes + kFfWBytes + p.b_bytes + 2 * kSfAtom +
-                                        (t & 31) * 16 + (t >> 5) * 4;
-                    if (t < n) {
-                        cp_async_4(sd, ssrc + kb * 8);
-                        if (2 * kb + 1 < p.num_chunks) cp_async_4(sd + kSfAtom, ssrc + kb * 8 + 4);
-                    }
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                st.next(ST);
-                if (++pending > kFfLag) {
-                    asm volatile("cp.async.wait_group %0;" ::"n"(kFfLag) : "memory");
-                    announce();
-                    --pending;
-                }
-            }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        for (; pending > 0; --pending) announce();
         __syncwarp();
     } else {
         // --------------------------------------------------- epilogue ----
@@ -746,7 +779,8 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.stage_bytes = kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0);
     constexpr uint32_t kSmemMax = 232448;
     p.stages = (int)((kSmemMax - 1024 - kFfMiscBytes<PAIR>) / p.stage_bytes);
-    if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;  // (6 at the least, above kFfLag)
+    if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
+    if (p.stages < kFfLoaders) return cudaErrorNotSupported;  // (see the row loaders; 6 at the least)
     p.acc_cols = PAIR ? kFfCols<PAIR> : a.A;
     const int cols = 2 * p.acc_cols + (MX ? 32 : 0);
     p.tmem_cols = cols <= 128 ? 128 : (cols <= 256 ? 256 : 512);
@@ -772,7 +806,7 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     if (!ok) return cudaErrorInvalidValue;
     p.x = static_cast<const uint8_t *>(a.x);
     p.x_bytes = (int)k_bytes;
-    p.x_row_bytes = MX ? (int64_t)k_bytes : a.ld_x * 2;
+    p.x_row_bytes = MX ? (uint32_t)k_bytes : (uint32_t)(a.ld_x * 2);
 
     static std::atomic<bool> configured[kMaxDevices];
     const cudaError_t e = once_per_device(configured, [](int) {
