@@ -15,7 +15,7 @@
 // expert follow each other, so its weights do too). Warp roles: 0 loads the
 // weights by TMA, 1 issues the MMAs, 2 reads the align's outputs ahead and
 // hands out the work, 3-8 load the routed rows (and their block scales) with
-// asynchronous 16-byte copies, 9-12 drain TMEM. (A TMA gather
+// asynchronous 16-byte copies, 9-16 drain TMEM. (A TMA gather
 // takes 4 rows an instruction and about 70 cycles each: 128 rows took 2300
 // cycles a k-block, 3300 us for 16384 tokens.) The stage ring runs across
 // items; accumulators are double-buffered in TMEM, so the epilogue of one item
@@ -29,7 +29,8 @@
 namespace smr {
 
 constexpr int kFfLoaders = 6;                    // warps that load the routed rows; at most the stages
-constexpr int kFfThreads = 32 * (3 + kFfLoaders + 4);
+constexpr int kFfDrains = 8;                     // warps of the epilogue, two for each quarter of TMEM's lanes
+constexpr int kFfThreads = 32 * (3 + kFfLoaders + kFfDrains);
 constexpr int kFfRows = 128;                     // weight rows of a tile (the MMA's M)
 constexpr int kFfRowBytes = 128;                 // one k-block of a row: 64 bf16 or 256 MXFP4
 constexpr int kFfWBytes = kFfRows * kFfRowBytes;  // weight tile of a stage
@@ -247,11 +248,11 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
-            mbar_init(smem_u32(&acc_empty[s]), PAIR ? 8 : 4);  // epilogue warps
+            mbar_init(smem_u32(&acc_empty[s]), (PAIR ? 2 : 1) * kFfDrains);
         }
         for (int s = 0; s < kFfInfos; ++s) {
             mbar_init(smem_u32(&info_full[s]), 1);
-            mbar_init(smem_u32(&info_empty[s]), 2 + kFfLoaders + 4);  // every warp but the scout
+            mbar_init(smem_u32(&info_empty[s]), 2 + kFfLoaders + kFfDrains);  // every warp but the scout
         }
         mbar_init(smem_u32(last), 1);
         *abort_flag = 0;
@@ -392,6 +393,10 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         fetch(grp, ent0, e0);
         fetch(grp1, ent1, e1);
         const int nblk = max(0, min(npp / A, p.max_blocks)), groups = (nblk + G - 1) / G;
+        // every block's entries into L2, each line by one CTA
+        for (int64_t i = ((int64_t)blockIdx.x * 32 + lane) * 32; i < min((int64_t)nblk * A, p.sorted_cap);
+             i += (int64_t)gridDim.x * 32 * 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sorted + i));
         auto run = [&](int (&ent)[8], int &e) {
             // the item (grp, tile), whose entries are ent; then moves on
             int top = 0;
@@ -523,7 +528,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         bool ok = true;
         while (ok) {
             if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
-            const volatile Info *inf = info + iq.i;
+            const Info *inf = info + iq.i;
             const int all = inf->n;
             // this CTA's rows are columns [col0, col0 + n)
             const int n = PAIR ? all / 2 : all, col0 = (int)rank * n;
@@ -534,21 +539,33 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     const int off = next * kFfRowBytes + c * 16;
                     // (chunks past the row's end are not read by the last MMA steps)
                     if (off < p.x_bytes) {
+                        // 4 rows a step and group of eight lanes, their places
+                        // read before the copies (which order memory accesses)
                         const uint8_t *x = p.x + off;
-#pragma unroll 4
-                        for (int r = lane >> 3; r < n; r += 4)
-                            cp_async_16(base + (uint32_t)(r * kFfRowBytes + ((c ^ (r & 7)) << 4)),
-                                        x + (uint64_t)(uint32_t)inf->row[col0 + r] * p.x_row_bytes);
+#pragma unroll 2
+                        for (int r = 4 * (lane >> 3); r < n; r += 16) {
+                            const int4 at = *reinterpret_cast<const int4 *>(inf->row + col0 + r);
+                            const int row[4] = {at.x, at.y, at.z, at.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                cp_async_16(base + (uint32_t)((r + j) * kFfRowBytes + ((c ^ ((r + j) & 7)) << 4)),
+                                            x + (uint64_t)(uint32_t)row[j] * p.x_row_bytes);
+                        }
                     }
                     if constexpr (MX) {
                         // scale of row r, block q of a 128-value piece: byte
                         // (r % 32) * 16 + (r / 32) * 4 + q of its 512
                         const uint32_t sd = base + p.b_bytes + 2 * kSfAtom + lane * 16;
                         const bool two = 2 * next + 1 < p.num_chunks;
-                        for (int r = lane; r < n; r += 32) {
-                            const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)inf->row[r] * (uint32_t)p.num_chunks + 2 * next) * 4;
-                            cp_async_4(sd + (r >> 5) * 4, src);
-                            if (two) cp_async_4(sd + kSfAtom + (r >> 5) * 4, src + 4);
+                        int row[kFfRows / 32];
+#pragma unroll
+                        for (int j = 0; j < kFfRows / 32; ++j) row[j] = inf->row[lane + 32 * j];
+#pragma unroll
+                        for (int j = 0; j < kFfRows / 32; ++j) {
+                            if (lane + 32 * j >= n) continue;
+                            const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)row[j] * (uint32_t)p.num_chunks + 2 * next) * 4;
+                            cp_async_4(sd + j * 4, src);
+                            if (two) cp_async_4(sd + kSfAtom + j * 4, src + 4);
                         }
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -570,7 +587,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         __syncwarp();
     } else {
         // --------------------------------------------------- epilogue ----
-        const int q = warp & 3;
+        // two warps share a quarter's lanes, every other 16 columns each
+        const int q = warp & 3, c_beg = warp < 3 + kFfLoaders + 4 ? 0 : 16;
         RingPos iq, ac;
         bool ok = true;
         while (ok) {
@@ -587,10 +605,12 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
             uint16_t *out = p.out + f;
             uint32_t v[16], next[16];
-            tmem_ld16_async(acc, v);
-            tmem_wait_ld16(v);
-            for (int c0 = 0; c0 < n; c0 += 16) {
-                if (c0 + 16 < n) tmem_ld16_async(acc + (uint32_t)(c0 + 16), next);
+            if (c_beg < n) {
+                tmem_ld16_async(acc + (uint32_t)c_beg, v);
+                tmem_wait_ld16(v);
+            }
+            for (int c0 = c_beg; c0 < n; c0 += 32) {
+                if (c0 + 32 < n) tmem_ld16_async(acc + (uint32_t)(c0 + 32), next);
                 if constexpr (UP) {
                     // lanes 0-15 hold gate rows, 16-31 the same features' up
                     // rows: each half of the warp takes every other column
@@ -623,7 +643,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     for (int j = 0; j < 4; ++j)
                         if (i[j] >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i[j] * p.feat) = s[j];
                 }
-                if (c0 + 16 < n) {
+                if (c0 + 32 < n) {
                     tmem_wait_ld16(next);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] = next[j];
