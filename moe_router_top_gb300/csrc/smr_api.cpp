@@ -762,7 +762,7 @@ SMR_API smr_status smr_expert_down(const smr_expert_down_args *a, void *workspac
     if (a->num_tokens > 0) {
         if (!a->topk_ids || !aligned(a->topk_ids, 4)) r.bad("topk_ids must be a 4-byte aligned pointer");
         if (!a->topk_weights || !aligned(a->topk_weights, 4)) r.bad("topk_weights must be a 4-byte aligned pointer");
-        if ((int64_t)a->num_tokens * a->H > (int64_t)1 << 33) r.unsup("num_tokens * H must be <= 2^33");
+        if ((int64_t)a->num_tokens * a->H > (int64_t)1 << 34) r.unsup("num_tokens * H must be <= 2^34");
     }
     if (!r.ok()) return r.finish("smr_expert_down");
     if (a->num_tokens == 0) return SMR_OK;

@@ -273,8 +273,9 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     if constexpr (PAIR) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    griddep_launch_dependents();
     griddep_wait();  // the align's outputs and x come from previous kernels
+    // (only now: a kernel that follows may read what those wrote at once)
+    griddep_launch_dependents();
 
     const uint32_t ring = smem_u32(smem);
     int issued = 0;  // stages whose weights were requested (warp 0)
@@ -691,45 +692,56 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
 // ------------------------------------------------------------- combine --
 //
 // out[t] = sum over the token's slots s, in order, of w[t, s] * y[t, s], in
-// fp32, rounded once. Bound by reading y (2 bytes per slot and feature); one
-// thread per 8 features. A slot whose id no expert has contributes nothing
-// (the align skipped it, so its row of y was not written).
+// fp32, rounded once. Bound by reading y (2 bytes per slot and feature). One
+// thread per 8 features of one token, its slots' rows requested 8 at a time.
+// A slot whose id no expert has contributes nothing (the align skipped it, so
+// its row of y was not written). The ids and weights come from kernels before
+// the product, which lets this grid start only after it waited for them: they
+// are read while the product still runs.
 constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads)
 expert_combine_kernel(const uint16_t *__restrict__ y, const int32_t *__restrict__ ids,
-                      const float *__restrict__ wts, uint16_t *__restrict__ out, int T, int width, int H,
+                      const float *__restrict__ wts, uint16_t *__restrict__ out, int parts, int width, int H,
                       int num_logical) {
     griddep_launch_dependents();
-    const uint32_t vecs = (uint32_t)H / 8, at = blockIdx.x * kCombineThreads + threadIdx.x;
-    griddep_wait();
-    if (at >= (uint32_t)T * vecs) return;
-    const uint32_t t = at / vecs, v = at - t * vecs;
-    ids += (int64_t)t * width;
-    wts += (int64_t)t * width;
-    const uint16_t *row = y + (int64_t)t * width * H + v * 8;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = blockIdx.x / (unsigned)parts;
+    const int f = ((int)(blockIdx.x % (unsigned)parts) * (int)blockDim.x + (int)threadIdx.x) * 8;
+    ids += t * width;
+    wts += t * width;
+    const uint16_t *row = y + t * width * H + f;
     float acc[8] = {};
-    for (int s0 = 0; s0 < width; s0 += 4) {
-        uint4 x[4];
-        float w[4];
+    for (int s0 = 0; s0 < width; s0 += 32) {
+        const int s = s0 + lane;
+        const bool use = s < width && (uint32_t)__ldcg(ids + s) < (uint32_t)num_logical;
+        const float w = use ? __ldcg(wts + s) : 0.0f;
+        uint32_t left = __ballot_sync(0xffffffffu, use);
+        if (s0 == 0) griddep_wait();
+        while (left != 0u) {
+            uint4 x[8];
+            float wx[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int s = s0 + j;
-            const bool use = s < width && (uint32_t)__ldcg(ids + s) < (uint32_t)num_logical;
-            x[j] = use ? ld_stream_v4(row + (int64_t)s * H) : make_uint4(0u, 0u, 0u, 0u);
-            w[j] = use ? __ldcg(wts + s) : 0.0f;
-        }
+            for (int j = 0; j < 8; ++j) {
+                const int at = left != 0u ? __ffs(left) - 1 : -1;
+                wx[j] = __shfl_sync(0xffffffffu, w, at < 0 ? 0 : at);
+                x[j] = at >= 0 && f < H ? ld_stream_v4(row + (int64_t)(s0 + at) * H) : make_uint4(0u, 0u, 0u, 0u);
+                if (at < 0) wx[j] = 0.0f;
+                left &= left - 1u;
+            }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float f[8];
-            unpack8(x[j], f);
+            for (int j = 0; j < 8; ++j) {
+                float v[8];
+                unpack8(x[j], v);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) acc[u] = fmaf(w[j], f[u], acc[u]);
+                for (int u = 0; u < 8; ++u) acc[u] = fmaf(wx[j], v[u], acc[u]);
+            }
         }
     }
+    if (f >= H) return;
     uint32_t o[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) o[u] = pack_bf16x2(acc[2 * u], acc[2 * u + 1]);
-    *reinterpret_cast<uint4 *>(out + (int64_t)at * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4 *>(out + t * H + f) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // ---------------------------------------------------------------- host --
@@ -873,17 +885,18 @@ cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream) {
-    const int64_t threads = (int64_t)a.T * (a.H / 8);
+    const int vecs = a.H / 8, threads = vecs < kCombineThreads ? (vecs + 31) / 32 * 32 : kCombineThreads;
+    const int parts = (vecs + threads - 1) / threads;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((threads + kCombineThreads - 1) / kCombineThreads), 1, 1);
-    cfg.blockDim = dim3(kCombineThreads, 1, 1);
+    cfg.gridDim = dim3((unsigned)a.T * (unsigned)parts, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, expert_combine_kernel, a.y, a.ids, a.wts, a.out, a.T, a.width, a.H,
+    return cudaLaunchKernelEx(&cfg, expert_combine_kernel, a.y, a.ids, a.wts, a.out, parts, a.width, a.H,
                               a.num_logical);
 }
 
