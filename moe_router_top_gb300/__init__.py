@@ -417,43 +417,41 @@ def _ffn_workspace(ws, nbytes: int, dev: int, s: int):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated):
-    """Checks of a product's operands in either format."""
+def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated, sorted_token_ids, expert_ids, npp, block_size):
+    """Checks of a product's operands in either format and of the align's outputs."""
     torch = _torch()
     mx = x_scales is not None
     if mx != (w_scales is not None):
         raise ValueError("x_scales and w_scales must both be given (MXFP4) or both be None (bfloat16)")
     dtype, kdim = (torch.uint8, K // 2) if mx else (torch.bfloat16, K)
-    if x.dtype != dtype or x.shape != (rows, kdim) or (x.stride(1) != 1 and kdim > 1):
+    if x.dtype is not dtype or x.shape != (rows, kdim) or (x.stride(1) != 1 and kdim > 1):
         raise ValueError(f"x must be a {dtype} [{rows}, {kdim}] tensor with unit stride along its rows")
-    if w.dtype != dtype or w.shape[1:] != (w_rows, kdim) or not w.is_contiguous():
+    if w.dtype is not dtype or w.shape[1:] != (w_rows, kdim) or not w.is_contiguous():
         raise ValueError(f"w must be a contiguous {dtype} [num_experts, {w_rows}, {kdim}] tensor")
     if mx:
         if not x.is_contiguous():
             raise ValueError("MXFP4 codes x must be contiguous")
-        if x_scales.dtype != torch.uint8 or x_scales.shape != (rows, K // 32) or not x_scales.is_contiguous():
+        if x_scales.dtype is not torch.uint8 or x_scales.shape != (rows, K // 32) or not x_scales.is_contiguous():
             raise ValueError(f"x_scales must be a contiguous uint8 [{rows}, {K // 32}] tensor")
         need = _lib.load().smr_mxfp4_tiled_scale_bytes(w.shape[0], w_rows, K, 1 if gated else 0)
-        if w_scales.dtype != torch.uint8 or w_scales.numel() != need or not w_scales.is_contiguous():
+        if w_scales.dtype is not torch.uint8 or w_scales.numel() != need or not w_scales.is_contiguous():
             raise ValueError(f"w_scales must be the {need} bytes that tile_mxfp4_scales gives for this weight")
-
-
-def _aligned_inputs(sorted_token_ids, expert_ids, npp, block_size):
-    int32 = _torch().int32
-    if (sorted_token_ids.dtype != int32 or expert_ids.dtype != int32 or npp.dtype != int32
+    int32 = torch.int32
+    if (sorted_token_ids.dtype is not int32 or expert_ids.dtype is not int32 or npp.dtype is not int32
             or not sorted_token_ids.is_contiguous() or not expert_ids.is_contiguous()):
         raise ValueError("sorted_token_ids, expert_ids and num_tokens_post_padded must be contiguous int32 tensors")
-    if expert_ids.numel() * block_size < sorted_token_ids.numel() and block_size > 0:
+    if block_size > 0 and expert_ids.numel() * block_size < sorted_token_ids.numel():
         raise ValueError("expert_ids must hold an entry for every block of sorted_token_ids")
     if npp.numel() < 1:
         raise ValueError("num_tokens_post_padded must hold one entry")
 
 
-def _output(out, shape, dtype, device, name="out"):
+def _output(out, lead, n, dtype, like, name="out"):
+    """The caller's output of shape [*lead, n], checked, or a new one on like's device."""
     if out is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    if out.dtype != dtype or out.shape != shape or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+        return _torch().empty((*lead, n), dtype=dtype, device=like.device)
+    if out.dtype != dtype or out.shape != (*lead, n) or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {(*lead, n)}")
     return out
 
 
@@ -475,8 +473,8 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
     E, I = w.shape[0], w.shape[1] // 2
     if x_scales is not None:
         H *= 2
-    _product_inputs(x, w, x_scales, w_scales, T, H, 2 * I, True)
-    _aligned_inputs(sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
+    _product_inputs(x, w, x_scales, w_scales, T, H, 2 * I, True, sorted_token_ids, expert_ids,
+                    num_tokens_post_padded, block_size)
     dev = _check_cuda(x, w, x_scales, w_scales, sorted_token_ids, expert_ids, num_tokens_post_padded, out)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -484,7 +482,7 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
             return expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, width=width,
                              block_size=block_size, x_scales=x_scales, w_scales=w_scales, out=out,
                              workspace=workspace)
-    out = _output(out, (T * width, I), torch.bfloat16, x.device)
+    out = _output(out, (T * width,), I, torch.bfloat16, x)
     a = ExpertUpArgs(T, width, H, I, E, block_size, x.data_ptr(), x.stride(0) if T > 1 else H, _ptr(x_scales),
                      w.data_ptr(), _ptr(w_scales), sorted_token_ids.data_ptr(), sorted_token_ids.numel(),
                      expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), out.data_ptr())
@@ -518,10 +516,10 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     E, H, I = w.shape
     if x_scales is not None:
         I *= 2
-    _product_inputs(x, w, x_scales, w_scales, T * width, I, H, False)
+    _product_inputs(x, w, x_scales, w_scales, T * width, I, H, False, sorted_token_ids, expert_ids,
+                    num_tokens_post_padded, block_size)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    _aligned_inputs(sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
     dev = _check_cuda(x, w, topk_ids, topk_weights, x_scales, w_scales, sorted_token_ids, expert_ids,
                       num_tokens_post_padded, out)
     ctx = _elsewhere(dev, stream)
@@ -530,7 +528,7 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
             return expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_tokens_post_padded,
                                block_size=block_size, num_logical=num_logical, x_scales=x_scales,
                                w_scales=w_scales, out=out, workspace=workspace)
-    out = _output(out, (T, H), torch.bfloat16, x.device)
+    out = _output(out, (T,), H, torch.bfloat16, x)
     a = ExpertDownArgs(T, width, H, I, E, block_size, x.data_ptr(), _ptr(x_scales), w.data_ptr(), _ptr(w_scales),
                        topk_ids.data_ptr(), topk_weights.data_ptr(), num_logical if num_logical else E,
                        sorted_token_ids.data_ptr(), sorted_token_ids.numel(), expert_ids.data_ptr(),
@@ -561,9 +559,9 @@ def quantize_mxfp4(x, *, codes=None, scales=None, stream=None) -> Tuple:
     if ctx is not None:
         with ctx:
             return quantize_mxfp4(x, codes=codes, scales=scales)
-    device, lead = x.device, shape[:-1]
-    codes = _output(codes, lead + (K // 2,), torch.uint8, device, "codes")
-    scales = _output(scales, lead + (K // 32,), torch.uint8, device, "scales")
+    lead = shape[:-1]
+    codes = _output(codes, lead, K // 2, torch.uint8, x, "codes")
+    scales = _output(scales, lead, K // 32, torch.uint8, x, "scales")
     rows = x.numel() // K
     _check(lib.smr_quantize_mxfp4(x.data_ptr(), rows, K, K if dense or rows < 2 else x.stride(0), codes.data_ptr(),
                                   scales.data_ptr(), _raw_stream(dev)))
@@ -589,7 +587,7 @@ def dequantize_mxfp4(codes, scales, *, out=None, stream=None):
     if ctx is not None:
         with ctx:
             return dequantize_mxfp4(codes, scales, out=out)
-    out = _output(out, lead + (K,), torch.bfloat16, codes.device)
+    out = _output(out, lead, K, torch.bfloat16, codes)
     _check(lib.smr_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), codes.numel() * 2 // K, K, out.data_ptr(),
                                     _raw_stream(dev)))
     return out
@@ -610,8 +608,8 @@ def tile_mxfp4_scales(scales, *, gated: bool = False, out=None, stream=None):
         with ctx:
             return tile_mxfp4_scales(scales, gated=gated, out=out)
     E, N, K = scales.shape[0], scales.shape[1], 32 * scales.shape[2]
-    shape = (E, -(-(N // 2) // 64) if gated else -(-N // 128), K // 128, 512)
-    out = _output(out, shape, torch.uint8, scales.device)
+    tiles = -(-(N // 2) // 64) if gated else -(-N // 128)
+    out = _output(out, (E, tiles, K // 128), 512, torch.uint8, scales)
     _check(lib.smr_tile_mxfp4_scales(scales.data_ptr(), E, N, K, 1 if gated else 0, out.data_ptr(),
                                      _raw_stream(dev)))
     return out

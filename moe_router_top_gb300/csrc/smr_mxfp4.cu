@@ -33,8 +33,8 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
 __global__ void __launch_bounds__(kMxThreads)
 quantize_mxfp4_kernel(const uint16_t *__restrict__ x, int64_t ld, uint32_t vecs_per_row, uint32_t vecs,
                       uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const uint32_t first = blockIdx.x * (kMxThreads * kMxVecs) + threadIdx.x;
     uint4 v[kMxVecs];
 #pragma unroll
@@ -77,22 +77,30 @@ quantize_mxfp4_kernel(const uint16_t *__restrict__ x, int64_t ld, uint32_t vecs_
     }
 }
 
-// E2M1 code (4 bits) times 2^(byte - 127) as bf16 bits. Exact: two
-// significant bits, and 2^-128 is still a (subnormal) bf16; byte 255 is NaN.
-__device__ __forceinline__ uint32_t mx_value_bf16(uint32_t code, float s) {
-    const uint32_t mag = code & 7u, ex = mag >> 1, fr = mag & 1u;
-    // 0, 0.5; (1 + fr / 2) * 2^(ex - 1)
-    const float g = ex == 0u ? 0.5f * (float)fr : __uint_as_float(((126u + ex) << 23) | (fr << 22));
-    return __float_as_uint((code & 8u) ? -(g * s) : g * s) >> 16;
+// Four E2M1 codes (16 bits) as two pairs of bf16: the eight magnitudes' high
+// and low bytes are picked from tables by the codes' low three bits, the sign
+// is moved over.
+__device__ __forceinline__ uint2 e2m1x4_bf16(uint32_t c) {
+    const uint32_t m = c & 0x7777u;
+    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, m), lo = __byte_perm(0xC0800000u, 0xC0804000u, m);
+    const uint32_t s01 = (c << 12 & 0x8000u) | (c << 24 & 0x80000000u), s23 = (c << 4 & 0x8000u) | (c << 16 & 0x80000000u);
+    return make_uint2(__byte_perm(lo, hi, 0x5140) | s01, __byte_perm(lo, hi, 0x7362) | s23);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // Bound by memory like the quantisation: 4 bytes of codes to 8 bf16 values a
-// step.
+// step, times the scale in bf16 (exact: a value has two significant bits, and
+// the smallest, 2^-128, is still a subnormal bf16; byte 255 is NaN). Table
+// look-ups and paired products: with one fp32 product a value the arithmetic
+// took longer than the memory (41 us for 16384 x 4096).
 __global__ void __launch_bounds__(kMxThreads)
 dequantize_mxfp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, uint32_t vecs,
                         uint16_t *__restrict__ out) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const uint32_t first = blockIdx.x * (kMxThreads * kMxVecs) + threadIdx.x;
     uint32_t c[kMxVecs], b[kMxVecs];
 #pragma unroll
@@ -105,13 +113,10 @@ dequantize_mxfp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__rest
     for (int j = 0; j < kMxVecs; ++j) {
         const uint32_t i = first + j * kMxThreads;
         if (i >= vecs) continue;
-        const float s = b[j] == 255u ? __uint_as_float(0x7FC00000u)
-                                     : __uint_as_float(b[j] == 0u ? 0x00400000u : b[j] << 23);
-        uint32_t o[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            o[u] = mx_value_bf16(c[j] >> (8 * u), s) | (mx_value_bf16(c[j] >> (8 * u + 4), s) << 16);
-        reinterpret_cast<uint4 *>(out)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        const uint32_t h = b[j] == 255u ? 0x7FC0u : (b[j] == 0u ? 0x0040u : b[j] << 7), s = h | (h << 16);
+        const uint2 lo = e2m1x4_bf16(c[j] & 0xFFFFu), hi = e2m1x4_bf16(c[j] >> 16);
+        reinterpret_cast<uint4 *>(out)[i] =
+            make_uint4(mul_bf16x2(lo.x, s), mul_bf16x2(lo.y, s), mul_bf16x2(hi.x, s), mul_bf16x2(hi.y, s));
     }
 }
 
@@ -125,8 +130,8 @@ dequantize_mxfp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__rest
 __global__ void __launch_bounds__(kMxThreads)
 tile_mxfp4_scales_kernel(const uint32_t *__restrict__ scales, int N, int chunks, int ntiles, int gated,
                          int64_t words, uint32_t *__restrict__ tiled) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int64_t at = (int64_t)blockIdx.x * kMxThreads + threadIdx.x;
     if (at >= words) return;
     const int in = (int)(at & 127), r = (in & 3) * 32 + (in >> 2);
