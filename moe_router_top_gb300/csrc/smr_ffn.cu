@@ -14,8 +14,8 @@
 // tiles of one block next to each other (its rows stay in L2; blocks of one
 // expert follow each other, so its weights do too). Warp roles: 0 loads the
 // weights by TMA, 1 issues the MMAs, 2 reads the align's outputs ahead and
-// hands out the work, 3-8 load the routed rows (and their block scales) with
-// asynchronous 16-byte copies, 9-16 drain TMEM. (A TMA gather
+// hands out the work, from 3 on load the routed rows (and their block scales) with
+// asynchronous 16-byte copies, the last eight drain TMEM. (A TMA gather
 // takes 4 rows an instruction and about 70 cycles each: 128 rows took 2300
 // cycles a k-block, 3300 us for 16384 tokens.) The stage ring runs across
 // items; accumulators are double-buffered in TMEM, so the epilogue of one item
@@ -28,13 +28,19 @@
 
 namespace smr {
 
-constexpr int kFfLoaders = 6;                    // warps that load the routed rows; at most the stages
+// k-blocks a stage: two for blocks of 64 rows. A stage costs every role a few
+// hundred cycles of barrier round trips whatever its size (550 a stage of one
+// k-block, 30 bytes a cycle: too few where a single token leaves an SM's share
+// of the memory rate to a few CTAs).
+template <int SUB>
+constexpr int kFfLoaders = SUB == 2 ? 4 : 6;     // warps that load the routed rows; at most the stages
 constexpr int kFfDrains = 8;                     // warps of the epilogue, two for each quarter of TMEM's lanes
-constexpr int kFfThreads = 32 * (3 + kFfLoaders + kFfDrains);
+template <int SUB>
+constexpr int kFfThreads = 32 * (3 + kFfLoaders<SUB> + kFfDrains);
 constexpr int kFfRows = 128;                     // weight rows of a tile (the MMA's M)
 constexpr int kFfRowBytes = 128;                 // one k-block of a row: 64 bf16 or 256 MXFP4
 constexpr int kFfWBytes = kFfRows * kFfRowBytes;  // weight tile of a stage
-constexpr int kFfMaxStages = 9;
+constexpr int kFfMaxStages = 6;
 // Pieces of work known ahead of the epilogue: with a short contraction (MXFP4,
 // K = 512: two k-blocks a piece) these bound the weights in flight.
 constexpr int kFfInfos = 8;
@@ -218,10 +224,11 @@ struct RingPos {
 // on one 256-row tile and up to 256 columns (blocks of one expert next to each
 // other together); each holds its own 128 weight rows and half of the routed
 // rows, and drains its own lanes.
-template <bool MX, bool UP, bool PAIR>
-__global__ void __launch_bounds__(kFfThreads, 1)
+template <bool MX, bool UP, bool PAIR, int SUB>
+__global__ void __launch_bounds__(kFfThreads<SUB>, 1)
 expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     using Info = FfInfo<kFfCols<PAIR>>;
+    constexpr int kLoaders = kFfLoaders<SUB>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -252,7 +259,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         }
         for (int s = 0; s < kFfInfos; ++s) {
             mbar_init(smem_u32(&info_full[s]), 1);
-            mbar_init(smem_u32(&info_empty[s]), 2 + kFfLoaders + kFfDrains);  // every warp but the scout
+            mbar_init(smem_u32(&info_empty[s]), 2 + kLoaders + kFfDrains);  // every warp but the scout
         }
         mbar_init(smem_u32(last), 1);
         *abort_flag = 0;
@@ -277,7 +284,9 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     // (only now: a kernel that follows may read what those wrote at once)
     griddep_launch_dependents();
 
+    // a stage: [weights SUB][rows SUB][MXFP4: weights' scales 2 SUB][rows' scales 2 SUB]
     const uint32_t ring = smem_u32(smem);
+    const uint32_t x_off = SUB * kFfWBytes, ws_off = x_off + SUB * p.b_bytes, xs_off = ws_off + 2 * SUB * kSfAtom;
     int issued = 0;  // stages whose weights were requested (warp 0)
 
     if (warp == 0) {
@@ -295,26 +304,31 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             if (n < 0) break;
             const uint8_t *scales = nullptr;
             if constexpr (MX) scales = p.w_scales + ((int64_t)e * p.ntiles + nt) * p.num_chunks * kSfAtom;
-            for (int kb = 0; kb < p.num_kb; ++kb) {
+            for (int kb = 0; kb < p.num_kb; kb += SUB) {
                 if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
                 const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
                 const uint32_t bar = smem_u32(&full[st.i]);
-                const int xk = kb * (MX ? kFfRowBytes : kFfRowBytes / 2);
+                const int subs = SUB == 1 ? 1 : min(SUB, p.num_kb - kb);
                 if (elected) {
                     if constexpr (PAIR) {
                         // both CTAs' bytes complete the leader's barrier
                         if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
                         const uint32_t fb = cluster_addr(bar, 0u);
+                        const int xk = kb * (kFfRowBytes / 2);
                         if constexpr (UP) tma_load_5d_pair(base, &tm_w, xk, nt * 4, e, fb);
                         else tma_load_3d_pair(base, &tm_w, xk, nt * kFfRows, e, fb);
                     } else {
                         uint32_t sbytes = 0;
-                        if constexpr (MX) sbytes = (uint32_t)min(2, p.num_chunks - 2 * kb) * kSfAtom;
-                        mbar_arrive_expect_tx(bar, kFfWBytes + sbytes);
-                        if constexpr (UP) tma_load_5d(base, &tm_w, xk, nt * 4, e, bar);
-                        else tma_load_3d(base, &tm_w, xk, nt * kFfRows, e, bar);
-                        if constexpr (MX)
-                            bulk_load(base + kFfWBytes + p.b_bytes, scales + 2 * kb * kSfAtom, sbytes, bar);
+                        if constexpr (MX) sbytes = (uint32_t)min(2 * SUB, p.num_chunks - 2 * kb) * kSfAtom;
+                        mbar_arrive_expect_tx(bar, subs * kFfWBytes + sbytes);
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            if (u >= subs) break;
+                            const int xk = (kb + u) * (MX ? kFfRowBytes : kFfRowBytes / 2);
+                            if constexpr (UP) tma_load_5d(base + u * kFfWBytes, &tm_w, xk, nt * 4, e, bar);
+                            else tma_load_3d(base + u * kFfWBytes, &tm_w, xk, nt * kFfRows, e, bar);
+                        }
+                        if constexpr (MX) bulk_load(base + ws_off, scales + 2 * kb * kSfAtom, sbytes, bar);
                     }
                 }
                 ++issued;
@@ -462,35 +476,42 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             tc_fence_after();
             const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols);
             const uint32_t idesc = MX ? idesc_mxf4(kFfRows, n) : idesc_bf16_f32(PAIR ? 2 * kFfRows : kFfRows, n);
-            for (int kb = 0; kb < p.num_kb; ++kb) {
+            for (int kb = 0; kb < p.num_kb; kb += SUB) {
                 if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
                 tc_fence_after();
-                const uint32_t a = ring + (uint32_t)st.i * p.stage_bytes, b = a + kFfWBytes;
-                const uint64_t da = smem_desc_sw<128>(a), db = smem_desc_sw<128>(b);  // + 2 per 32 bytes of K
-                const int steps = kb + 1 == p.num_kb ? p.last_steps : 4;
-                const uint32_t more = kb != 0 ? 1u : 0u;
-                if constexpr (MX) {
-                    const uint32_t sa = b + p.b_bytes, sb = sa + 2 * kSfAtom;
-                    if (elected) {
-                        tc_cp_scales(sf, sa);
-                        tc_cp_scales(sf + 8, sb);
-                        tc_mma_mxf4(acc, da, db, idesc, sf, sf + 8, more);
-                        tc_mma_mxf4(acc, da + 2, db + 2, idesc | (1u << 30) | (1u << 5), sf, sf + 8, 1u);
-                        if (steps == 4) {
-                            tc_cp_scales(sf + 4, sa + kSfAtom);
-                            tc_cp_scales(sf + 12, sb + kSfAtom);
-                            tc_mma_mxf4(acc, da + 4, db + 4, idesc, sf + 4, sf + 12, 1u);
-                            tc_mma_mxf4(acc, da + 6, db + 6, idesc | (1u << 30) | (1u << 5), sf + 4, sf + 12, 1u);
-                        }
-                    }
-                    sf ^= 16u;
-                } else if (elected) {
-                    if (steps == 4) {
+                const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
-                    } else {
-                        for (int kk = 0; kk < steps; ++kk)
-                            ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
+                for (int u = 0; u < SUB; ++u) {
+                    if (SUB > 1 && kb + u >= p.num_kb) break;
+                    // descriptors: + 2 per 32 bytes of K
+                    const uint64_t da = smem_desc_sw<128>(base + u * kFfWBytes),
+                                   db = smem_desc_sw<128>(base + x_off + u * p.b_bytes);
+                    const int steps = kb + u + 1 == p.num_kb ? p.last_steps : 4;
+                    const uint32_t more = kb + u != 0 ? 1u : 0u;
+                    if constexpr (MX) {
+                        const uint32_t sa = base + ws_off + 2 * u * kSfAtom, sb = base + xs_off + 2 * u * kSfAtom;
+                        if (elected) {
+                            tc_cp_scales(sf, sa);
+                            tc_cp_scales(sf + 8, sb);
+                            tc_mma_mxf4(acc, da, db, idesc, sf, sf + 8, more);
+                            tc_mma_mxf4(acc, da + 2, db + 2, idesc | (1u << 30) | (1u << 5), sf, sf + 8, 1u);
+                            if (steps == 4) {
+                                tc_cp_scales(sf + 4, sa + kSfAtom);
+                                tc_cp_scales(sf + 12, sb + kSfAtom);
+                                tc_mma_mxf4(acc, da + 4, db + 4, idesc, sf + 4, sf + 12, 1u);
+                                tc_mma_mxf4(acc, da + 6, db + 6, idesc | (1u << 30) | (1u << 5), sf + 4, sf + 12, 1u);
+                            }
+                        }
+                        sf ^= 16u;
+                    } else if (elected) {
+                        if (steps == 4) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
+                        } else {
+                            for (int kk = 0; kk < steps; ++kk)
+                                ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
+                        }
                     }
                 }
                 if (elected) ff_commit<PAIR>(&empty[st.i]);
@@ -510,9 +531,9 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
         }
         __syncwarp();
-    } else if (warp < 3 + kFfLoaders) {
+    } else if (warp < 3 + kLoaders) {
         // ------------------------------------------------ routed rows ----
-        // Each loader warp fills every kFfLoaders-th stage, so that a stage is
+        // Each loader warp fills every kLoaders-th stage, so that a stage is
         // waited for, copied, made visible to the tensor core (async proxy)
         // and announced by one warp, while the others' copies are in flight.
         // A row's k-block is eight 16-byte chunks; eight neighbouring lanes
@@ -520,8 +541,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         // 4), the 128-byte swizzle.
         // A parity wait tells a stage's last use from the one before only: a
         // warp that waits for stage j (counted over all uses) must know that
-        // j - 2 * ST was consumed. It waited for j - kFfLoaders, so everything
-        // up to j - kFfLoaders - ST was: hence kFfLoaders <= ST.
+        // j - 2 * ST was consumed. It waited for j - kLoaders, so everything
+        // up to j - kLoaders - ST was: hence kLoaders <= ST.
         const int c = lane & 7;
         RingPos st, iq;
         int next = warp - 3;  // this warp's next stage, counted from the piece's first
@@ -534,39 +555,44 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             // this CTA's rows are columns [col0, col0 + n)
             const int n = PAIR ? all / 2 : all, col0 = (int)rank * n;
             if (all >= 0) {
-                for (; next < p.num_kb; next += kFfLoaders) {
+                const int count = (p.num_kb + SUB - 1) / SUB;
+                for (; next < count; next += kLoaders) {
                     if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
-                    const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes + kFfWBytes;
-                    const int off = next * kFfRowBytes + c * 16;
+                    const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
+                    const int kb = next * SUB;
                     // (chunks past the row's end are not read by the last MMA steps)
-                    if (off < p.x_bytes) {
-                        // 4 rows a step and group of eight lanes, their places
-                        // read before the copies (which order memory accesses)
-                        const uint8_t *x = p.x + off;
+                    const int off = kb * kFfRowBytes + c * 16, ends = p.x_bytes;
+                    const uint8_t *x = p.x + off;
+                    // 4 rows a step and group of eight lanes, their places
+                    // read before the copies (which order memory accesses)
 #pragma unroll 2
-                        for (int r = 4 * (lane >> 3); r < n; r += 16) {
-                            const int4 at = *reinterpret_cast<const int4 *>(inf->row + col0 + r);
-                            const int row[4] = {at.x, at.y, at.z, at.w};
+                    for (int r = 4 * (lane >> 3); r < n; r += 16) {
+                        const int4 at = *reinterpret_cast<const int4 *>(inf->row + col0 + r);
+                        const int row[4] = {at.x, at.y, at.z, at.w};
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                cp_async_16(base + (uint32_t)((r + j) * kFfRowBytes + ((c ^ ((r + j) & 7)) << 4)),
-                                            x + (uint64_t)(uint32_t)row[j] * p.x_row_bytes);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint8_t *from = x + (uint64_t)(uint32_t)row[j] * p.x_row_bytes;
+                            const uint32_t to = base + x_off + (uint32_t)((r + j) * kFfRowBytes + ((c ^ ((r + j) & 7)) << 4));
+#pragma unroll
+                            for (int u = 0; u < SUB; ++u)
+                                if (off + u * kFfRowBytes < ends) cp_async_16(to + u * p.b_bytes, from + u * kFfRowBytes);
                         }
                     }
                     if constexpr (MX) {
                         // scale of row r, block q of a 128-value piece: byte
                         // (r % 32) * 16 + (r / 32) * 4 + q of its 512
-                        const uint32_t sd = base + p.b_bytes + 2 * kSfAtom + lane * 16;
-                        const bool two = 2 * next + 1 < p.num_chunks;
+                        const uint32_t sd = base + xs_off + lane * 16;
+                        const int pieces = min(2 * SUB, p.num_chunks - 2 * kb);
                         int row[kFfRows / 32];
 #pragma unroll
                         for (int j = 0; j < kFfRows / 32; ++j) row[j] = inf->row[lane + 32 * j];
 #pragma unroll
                         for (int j = 0; j < kFfRows / 32; ++j) {
                             if (lane + 32 * j >= n) continue;
-                            const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)row[j] * (uint32_t)p.num_chunks + 2 * next) * 4;
-                            cp_async_4(sd + j * 4, src);
-                            if (two) cp_async_4(sd + kSfAtom + j * 4, src + 4);
+                            const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)row[j] * (uint32_t)p.num_chunks + 2 * kb) * 4;
+#pragma unroll
+                            for (int q = 0; q < 2 * SUB; ++q)
+                                if (q < pieces) cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q);
                         }
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -576,9 +602,9 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&full[st.i]), 0u));
                         else mbar_arrive(smem_u32(&full[st.i]));
                     }
-                    st.skip(kFfLoaders, ST);
+                    st.skip(kLoaders, ST);
                 }
-                next -= p.num_kb;
+                next -= count;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
@@ -589,7 +615,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     } else {
         // --------------------------------------------------- epilogue ----
         // two warps share a quarter's lanes, every other 16 columns each
-        const int q = warp & 3, c_beg = warp < 3 + kFfLoaders + 4 ? 0 : 16;
+        const int q = warp & 3, c_beg = warp < 3 + kLoaders + 4 ? 0 : 16;
         RingPos iq, ac;
         bool ok = true;
         while (ok) {
@@ -783,7 +809,7 @@ static bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const v
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool MX, bool UP, bool PAIR>
+template <bool MX, bool UP, bool PAIR, int SUB>
 static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stream) {
     FfParams p{};
     const int per_block = MX ? 256 : 64, step = MX ? 64 : 16;  // values of K in a k-block, in an MMA
@@ -808,11 +834,11 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.num_chunks = a.K / 128;
     p.err = &reinterpret_cast<WsHeader *>(a.hdr)->error;
     p.b_bytes = (uint32_t)(PAIR ? kFfRows : a.A) * kFfRowBytes;
-    p.stage_bytes = kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0);
+    p.stage_bytes = SUB * (kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0));
     constexpr uint32_t kSmemMax = 232448;
     p.stages = (int)((kSmemMax - 1024 - kFfMiscBytes<PAIR>) / p.stage_bytes);
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
-    if (p.stages < kFfLoaders) return cudaErrorNotSupported;  // (see the row loaders; 6 at the least)
+    if (p.stages < kFfLoaders<SUB>) return cudaErrorNotSupported;  // (see the row loaders; never with these sizes)
     p.acc_cols = PAIR ? kFfCols<PAIR> : a.A;
     const int cols = 2 * p.acc_cols + (MX ? 32 : 0);
     p.tmem_cols = cols <= 128 ? 128 : (cols <= 256 ? 256 : 512);
@@ -842,10 +868,10 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
 
     static std::atomic<bool> configured[kMaxDevices];
     const cudaError_t e = once_per_device(configured, [](int) {
-        cudaError_t r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR, SUB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kSmemMax);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR>, cudaFuncAttributePreferredSharedMemoryCarveout,
+            r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR, SUB>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         return r;
     });
@@ -856,7 +882,7 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     const int room = PAIR ? sms / 2 * 2 : sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(most < room ? most : room), 1, 1);
-    cfg.blockDim = dim3(kFfThreads, 1, 1);
+    cfg.blockDim = dim3(kFfThreads<SUB>, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -868,20 +894,23 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP, PAIR>, mw, p);
+    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP, PAIR, SUB>, mw, p);
+}
+
+template <bool MX, bool UP>
+static cudaError_t launch_single(const FfnLaunch &a, int sms, cudaStream_t stream) {
+    return a.A == 64 ? launch_product<MX, UP, false, 2>(a, sms, stream) : launch_product<MX, UP, false, 1>(a, sms, stream);
 }
 
 cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
     if (a.x_scales != nullptr)
-        return a.gated ? launch_product<true, true, false>(a, sms, stream)
-                       : launch_product<true, false, false>(a, sms, stream);
+        return a.gated ? launch_single<true, true>(a, sms, stream) : launch_single<true, false>(a, sms, stream);
     if (a.numel >= (int64_t)kPairRows * a.num_experts)
-        return a.gated ? launch_product<false, true, true>(a, sms, stream)
-                       : launch_product<false, false, true>(a, sms, stream);
-    return a.gated ? launch_product<false, true, false>(a, sms, stream)
-                   : launch_product<false, false, false>(a, sms, stream);
+        return a.gated ? launch_product<false, true, true, 1>(a, sms, stream)
+                       : launch_product<false, false, true, 1>(a, sms, stream);
+    return a.gated ? launch_single<false, true>(a, sms, stream) : launch_single<false, false>(a, sms, stream);
 }
 
 cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream) {
