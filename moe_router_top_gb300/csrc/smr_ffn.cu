@@ -55,7 +55,11 @@ struct FfInfo {
     int e;     // expert
     int pad;
     int slot[COLS];  // flat slot of every column, -1: none
-    int row[COLS];   // its row of x (0 for a column without a slot, which is not stored)
+    // its row of x, -1: none. Such a column is neither loaded nor stored: what
+    // the MMAs make of the old contents of shared memory stays in its column.
+    // (Loading row 0 for it, 15 times a block in every CTA, queued the whole
+    // GPU up on one line of L2: 2500 cycles a stage with a single token.)
+    int row[COLS];
 };
 constexpr int kFfBars = 2 * kFfMaxStages + 4 + 2 * kFfInfos + 1;
 constexpr int kFfBarBytes = (kFfBars * 8 + 8 + 15) / 16 * 16;
@@ -138,11 +142,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// Copies that happen where row >= 0 (predicated: a branch a row cost the
+// large batches 15%).
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, int row) {
+    asm volatile("{\n .reg .pred q;\n setp.ge.s32 q, %2, 0;\n @q cp.async.ca.shared.global [%0], [%1], 4;\n}"
+                 ::"r"(dst), "l"(src), "r"(row) : "memory");
 }
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, int row) {
+    asm volatile("{\n .reg .pred q;\n setp.ge.s32 q, %2, 0;\n @q cp.async.cg.shared.global [%0], [%1], 16;\n}"
+                 ::"r"(dst), "l"(src), "r"(row) : "memory");
 }
 
 // MXFP4 instruction descriptor (kind::mxf4): A and B E2M1 (bits 7-9, 10-11 =
@@ -387,8 +395,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 int row[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const uint32_t i = slot[j] < 0 ? 0u : (uint32_t)slot[j];
-                    row[j] = UP ? (int)((uint64_t)i * p.div_mul >> p.div_shift) : (int)i;
+                    row[j] = slot[j];
+                    if (UP && slot[j] >= 0) row[j] = (int)((uint64_t)(uint32_t)slot[j] * p.div_mul >> p.div_shift);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; j += 4) {
@@ -575,7 +583,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                             const uint32_t to = base + x_off + (uint32_t)((r + j) * kFfRowBytes + ((c ^ ((r + j) & 7)) << 4));
 #pragma unroll
                             for (int u = 0; u < SUB; ++u)
-                                if (off + u * kFfRowBytes < ends) cp_async_16(to + u * p.b_bytes, from + u * kFfRowBytes);
+                                cp_async_16(to + u * p.b_bytes, from + u * kFfRowBytes, off + u * kFfRowBytes < ends ? row[j] : -1);
                         }
                     }
                     if constexpr (MX) {
@@ -585,14 +593,13 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         const int pieces = min(2 * SUB, p.num_chunks - 2 * kb);
                         int row[kFfRows / 32];
 #pragma unroll
-                        for (int j = 0; j < kFfRows / 32; ++j) row[j] = inf->row[lane + 32 * j];
+                        for (int j = 0; j < kFfRows / 32; ++j) row[j] = lane + 32 * j < n ? inf->row[lane + 32 * j] : -1;
 #pragma unroll
                         for (int j = 0; j < kFfRows / 32; ++j) {
-                            if (lane + 32 * j >= n) continue;
                             const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)row[j] * (uint32_t)p.num_chunks + 2 * kb) * 4;
 #pragma unroll
                             for (int q = 0; q < 2 * SUB; ++q)
-                                if (q < pieces) cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q);
+                                cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q, q < pieces ? row[j] : -1);
                         }
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
