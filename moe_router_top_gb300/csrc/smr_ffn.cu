@@ -346,11 +346,11 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------ scout ----
-        // An item is a group of 1 (PAIR: 256 / A) aligned blocks and a weight
-        // tile (PAIR: two). Blocks of a group that share an expert make one
-        // piece of work. Both CTAs of a pair walk the same pieces. CTAs take
-        // every gridDim-th item: a block's tiles run next to each other in
-        // time (its rows stay in L2), blocks of one expert too (its weights).
+        // An item is a group of blocks of one expert (one block; PAIR: up to
+        // 256 / A, counted from the expert's first) and a weight tile (PAIR:
+        // two). Both CTAs of a pair walk the same items. CTAs take every
+        // gridDim-th item: a block's tiles run next to each other in time
+        // (its rows stay in L2), blocks of one expert too (its weights).
         const int A = p.A, G = PAIR ? 256 / A : 1;
         const int tiles = PAIR ? (p.ntiles + 1) / 2 : p.ntiles;
         const int ctas = PAIR ? gridDim.x >> 1 : gridDim.x, cta = PAIR ? blockIdx.x >> 1 : blockIdx.x;
@@ -359,11 +359,38 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         const int bo = 8 * lane / A, po = 8 * lane % A;  // this lane's 8 entries: block of the group, place in it
         const bool in = bo < G;
         const bool wide = (reinterpret_cast<uintptr_t>(p.sorted) & 15) == 0;
+        const int nblk = max(0, min(__ldcg(p.npp) / A, p.max_blocks));
+        // First block of group g (asked for in ascending order), -1 past the
+        // last: 32 blocks at a time, a bit for every block that starts one,
+        // which is every G-th block of an expert's segment.
+        int scan_at = -32, scan_base = 0, last_e = 0, run = 0;  // (run: blocks of the segment before the 32)
+        uint32_t starts = 0u;
+        auto locate = [&](int g) {
+            if constexpr (PAIR) {
+                while (g - scan_base >= __popc(starts)) {
+                    if (scan_at + 32 >= nblk) return -1;
+                    scan_base += __popc(starts);
+                    scan_at += 32;
+                    const int b = scan_at + lane, eb = b < nblk ? __ldcg(p.eids + b) : 0;
+                    int before = __shfl_up_sync(0xffffffffu, eb, 1);
+                    if (lane == 0) before = last_e;
+                    const uint32_t first = __ballot_sync(0xffffffffu, b == 0 || eb != before);
+                    const uint32_t upto = first & (0xffffffffu >> (31 - lane));
+                    const int place = upto != 0u ? lane - (31 - __clz(upto)) : run + lane;
+                    starts = __ballot_sync(0xffffffffu, b < nblk && place % G == 0);
+                    last_e = __shfl_sync(0xffffffffu, eb, 31);
+                    run = __shfl_sync(0xffffffffu, place, 31) + 1;
+                }
+                return scan_at + (int)__fns(starts, 0, g - scan_base + 1);
+            } else {
+                return g < nblk ? g : -1;
+            }
+        };
         // the entries and the block's expert, requested two items ahead (a
         // round trip to L2 is longer than a short item)
-        auto fetch = [&](int g, int (&ent)[8], int &e) {
-            const int b = g * G + bo;
-            if (!in || b >= p.max_blocks) return;
+        auto fetch = [&](int b0, int (&ent)[8], int &e) {
+            const int b = b0 + bo;
+            if (!in || b0 < 0 || b >= nblk) return;
             const int64_t at = (int64_t)b * A + po;
             e = __ldcg(p.eids + b);
             if (wide && at + 8 <= p.sorted_cap) {
@@ -386,12 +413,11 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         };
         RingPos iq;
         bool ok = true;
-        auto post = [&](int n, int nt, int e, int first, int count, const int (&slot)[8]) {
-            // columns [first, first + count) of the group
+        auto post = [&](int n, int nt, int e, const int (&slot)[8]) {
             if (!(ok = warp_wait(&info_empty[iq.i], iq.ph ^ 1u, abort_flag))) return;
             Info *inf = info + iq.i;
-            const int c = 8 * lane - first;
-            if (c >= 0 && c < count) {
+            const int c = 8 * lane;
+            if (c < n) {
                 int row[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -409,25 +435,30 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             if (lane == 0) mbar_arrive(smem_u32(&info_full[iq.i]));
             iq.next(kFfInfos);
         };
-        int ent0[8], ent1[8], e0 = -1, e1 = -1, slot[8];
-        int grp1 = grp, tile1 = tile;
-        step(grp1, tile1);
-        const int npp = __ldcg(p.npp);
-        fetch(grp, ent0, e0);
-        fetch(grp1, ent1, e1);
-        const int nblk = max(0, min(npp / A, p.max_blocks)), groups = (nblk + G - 1) / G;
         // every block's entries into L2, each line by one CTA
         for (int64_t i = ((int64_t)blockIdx.x * 32 + lane) * 32; i < min((int64_t)nblk * A, p.sorted_cap);
              i += (int64_t)gridDim.x * 32 * 32)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sorted + i));
-        auto run = [&](int (&ent)[8], int &e) {
-            // the item (grp, tile), whose entries are ent; then moves on
+        int ent0[8], ent1[8], e0 = -1, e1 = -1, slot[8];
+        int grp2 = grp, tile2 = tile;  // the item after the next
+        int at0 = locate(grp);         // first blocks of this item's and the next one's groups
+        fetch(at0, ent0, e0);
+        step(grp2, tile2);
+        int at1 = locate(grp2);
+        fetch(at1, ent1, e1);
+        step(grp2, tile2);
+        auto take = [&](int &at, int (&ent)[8], int &e) {
+            // the item whose first block is `at`; then the one after the next is requested
             int top = 0;
-            const bool mine_in = in && grp * G + bo < nblk;
-            const int ex = mine_in ? e : -1;
+            const bool here = in && at + bo < nblk;
+            const int ex = here ? e : -1;
+            const int eg = __shfl_sync(0xffffffffu, ex, 0);
+            int h = 1;  // blocks of the group
+            while (h < G && at + h < nblk && __shfl_sync(0xffffffffu, ex, h * A / 8) == eg) ++h;
+            const bool mine = here && bo < h;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int i = mine_in ? ent[j] : p.numel;
+                const int i = mine ? ent[j] : p.numel;
                 const bool real = (uint32_t)i < (uint32_t)p.numel;
                 // neither a slot nor the sentinel: a corrupted align output
                 if (!real && i != p.numel) set_error(p.err, kErrBadSlot);
@@ -435,33 +466,26 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (real) top = 8 * lane + j + 1;
             }
             __syncwarp();
+            const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
             const int nt = PAIR ? 2 * tile + (int)rank : tile;
+            at = locate(grp2);
+            fetch(at, ent, e);
             step(grp, tile);
-            int grp2 = grp, tile2 = tile;
             step(grp2, tile2);
-            if (grp2 < groups) fetch(grp2, ent, e);
-            for (int g = 0; ok && g < G;) {
-                const int eg = __shfl_sync(0xffffffffu, ex, g * A / 8);
-                int h = g + 1;
-                while (h < G && __shfl_sync(0xffffffffu, ex, h * A / 8) == eg) ++h;
-                const int first = g * A, count = (h - g) * A;
-                const bool mine = 8 * lane >= first && 8 * lane < first + count;
-                const int rows = (int)__reduce_max_sync(0xffffffffu, mine ? (unsigned)top : 0u) - first;
-                g = h;
-                if (rows <= 0) continue;
-                if ((unsigned)eg >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
-                    if (lane == 0) set_error(p.err, kErrBadId);
-                    __syncwarp();
-                    continue;
-                }
-                post((rows + 15) & ~15, nt, eg, first, count, slot);
+            if (rows == 0) return;
+            if ((unsigned)eg >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
+                if (lane == 0) set_error(p.err, kErrBadId);
+                __syncwarp();
+                return;
             }
+            post((rows + 15) & ~15, nt, eg, slot);
         };
-        while (ok && grp < groups) {
-            run(ent0, e0);
-            if (ok && grp < groups) run(ent1, e1);
+        while (ok && at0 >= 0) {
+            take(at0, ent0, e0);
+            if (ok && at1 >= 0) take(at1, ent1, e1);
+            else if (at1 < 0) break;
         }
-        if (ok) post(-1, 0, 0, 0, 0, slot);
+        if (ok) post(-1, 0, 0, slot);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------- MMAs ----
@@ -884,8 +908,7 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     });
     if (e != cudaSuccess) return e;
     // one CTA (pair) per item, at most one CTA per SM
-    const int G = 256 / a.A;
-    const int most = PAIR ? (p.max_blocks + G - 1) / G * ((p.ntiles + 1) / 2) * 2 : p.max_blocks * p.ntiles;
+    const int64_t most = (int64_t)p.max_blocks * (PAIR ? (p.ntiles + 1) / 2 * 2 : p.ntiles);
     const int room = PAIR ? sms / 2 * 2 : sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(most < room ? most : room), 1, 1);
