@@ -1,0 +1,235 @@
+"""Host-side checks of the expert feed-forward and MXFP4 entry points (no GPU
+needed): refusals with every reason before any device work, workspace sizes,
+the calls that launch nothing, and the Python layer's argument checks."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+from moe_router_top_gb300 import _lib
+from moe_router_top_gb300._lib import ExpertDownArgs, ExpertUpArgs
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from moe_router_top_gb300 import build
+    build.build()
+    return _lib.load()
+
+
+@pytest.fixture(scope="module")
+def smr(lib):
+    import moe_router_top_gb300
+    return moe_router_top_gb300
+
+
+P = 0x10000
+
+
+def _up(**over):
+    a = ExpertUpArgs(4, 11, 256, 128, 65, 64, P, 256, None, P, None, P, 44 + 65 * 63, P, P, P)
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+def _down(**over):
+    a = ExpertDownArgs(4, 11, 256, 128, 65, 64, P, None, P, None, P, P, 65, P, 44 + 65 * 63, P, P, P)
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+def _refused(lib, fn, a, status, *frags):
+    assert fn(ctypes.byref(a), P, 1 << 40, None) == status
+    msg = lib.smr_last_error().decode()
+    for f in frags:
+        assert f in msg, msg
+    assert lib.smr_last_launch_count() == 0
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(ExpertUpArgs) == 6 * 4 + 10 * 8 and ExpertUpArgs.x.offset == 24
+    assert ctypes.sizeof(ExpertDownArgs) == 6 * 4 + 12 * 8 and ExpertDownArgs.num_logical.offset == 72
+
+
+INVALID, UNSUP, WORKSPACE = _lib.SMR_ERR_INVALID_ARG, _lib.SMR_ERR_UNSUPPORTED, _lib.SMR_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("over,status,frag", [
+    (dict(num_tokens=-1), INVALID, "num_tokens must be >= 0"),
+    (dict(width=0), INVALID, "width must be >= 1"),
+    (dict(H=250), INVALID, "multiple of 16"),
+    (dict(H=16400), INVALID, "16384"),
+    (dict(I=8), INVALID, "multiple of 16"),
+    (dict(num_experts=0), INVALID, "num_experts must be in [1, 1025]"),
+    (dict(num_experts=1026), INVALID, "num_experts must be in [1, 1025]"),
+    (dict(block_size=32), UNSUP, "block_size must be 64 or 128"),
+    (dict(x=None), INVALID, "x must be"),
+    (dict(x=P + 8), INVALID, "x must be"),
+    (dict(w=P + 4), INVALID, "w must be"),
+    (dict(x_scales=P), INVALID, "both be set"),
+    (dict(w_scales=P), INVALID, "both be set"),
+    (dict(sorted_token_ids=None), INVALID, "must be set"),
+    (dict(expert_ids=P + 2), INVALID, "4-byte aligned"),
+    (dict(num_tokens_post_padded=None), INVALID, "must be set"),
+    (dict(sorted_cap=0), INVALID, "sorted_cap must be >= 1"),
+    (dict(sorted_cap=1 << 31), UNSUP, "int32 indexing"),
+    (dict(num_tokens=1 << 27), UNSUP, "2^30"),
+])
+def test_product_refusals(lib, over, status, frag):
+    _refused(lib, lib.smr_expert_up, _up(**over), status, "smr_expert_up", frag)
+    _refused(lib, lib.smr_expert_down, _down(**over), status, "smr_expert_down", frag)
+
+
+def test_own_refusals(lib):
+    _refused(lib, lib.smr_expert_up, _up(ld_x=248), INVALID, "ld_x must be >= H")
+    _refused(lib, lib.smr_expert_up, _up(ld_x=260), INVALID, "multiple of 8")
+    _refused(lib, lib.smr_expert_up, _up(ld_x=1 << 31), UNSUP, "2^30")
+    _refused(lib, lib.smr_expert_up, _up(act=None), INVALID, "act must be")
+    _refused(lib, lib.smr_expert_down, _down(out=P + 8), INVALID, "out must be")
+    _refused(lib, lib.smr_expert_down, _down(topk_ids=None), INVALID, "topk_ids must be")
+    _refused(lib, lib.smr_expert_down, _down(topk_weights=P + 1), INVALID, "topk_weights must be")
+    _refused(lib, lib.smr_expert_down, _down(num_logical=0), INVALID, "num_logical must be in")
+    # every reason in one message
+    _refused(lib, lib.smr_expert_up, _up(width=0, H=7, I=0), INVALID, "width must", "H must", "I must")
+    # blocks x weight tiles
+    _refused(lib, lib.smr_expert_up, _up(I=16384, sorted_cap=(1 << 31) - 1), UNSUP, "blocks x weight tiles")
+
+
+def test_mxfp4_products_ask_for_whole_scale_groups(lib):
+    mx = dict(x_scales=P, w_scales=P)
+    _refused(lib, lib.smr_expert_up, _up(H=192, ld_x=192, **mx), INVALID, "H must be a multiple of 128")
+    _refused(lib, lib.smr_expert_down, _down(I=160, **mx), INVALID, "I must be a multiple of 128")
+    _refused(lib, lib.smr_expert_up, _up(x_scales=P + 2, w_scales=P), INVALID, "x_scales must be 4-byte")
+    _refused(lib, lib.smr_expert_up, _up(x_scales=P, w_scales=P + 8), INVALID, "w_scales must be 16-byte")
+
+
+def test_workspaces(lib):
+    up, down = _up(), _down()
+    assert lib.smr_expert_up_workspace_size(ctypes.byref(up)) == 256
+    # the rows sit behind a small route's keys (16 tokens x 1024 experts x 8 bytes)
+    need = 256 + 16 * 1024 * 8 + 44 * 256 * 2
+    assert lib.smr_expert_down_workspace_size(ctypes.byref(down)) == need
+    assert lib.smr_expert_up(ctypes.byref(up), None, 0, None) == WORKSPACE
+    assert lib.smr_expert_down(ctypes.byref(down), P, need - 1, None) == WORKSPACE
+    assert lib.smr_expert_down(ctypes.byref(down), P + 128, need, None) == WORKSPACE
+    assert lib.smr_expert_up(None, P, 256, None) == INVALID
+    assert lib.smr_expert_down(None, P, 256, None) == INVALID
+    assert lib.smr_expert_down_workspace_size(None) == 0
+
+
+def test_nothing_to_do(lib):
+    for fn, a in ((lib.smr_expert_up, ExpertUpArgs(0, 1, 16, 16, 1, 64)),
+                  (lib.smr_expert_down, ExpertDownArgs(0, 1, 16, 16, 1, 64, num_logical=1))):
+        assert fn(ctypes.byref(a), None, 0, None) == _lib.SMR_OK
+        assert lib.smr_last_launch_count() == 0
+    assert lib.smr_quantize_mxfp4(None, 0, 32, 32, None, None, None) == _lib.SMR_OK
+    assert lib.smr_dequantize_mxfp4(None, None, 0, 32, None, None) == _lib.SMR_OK
+
+
+@pytest.mark.parametrize("args,frag", [
+    ((P, -1, 32, 32, P, P), "rows must be >= 0"),
+    ((P, 4, 48, 48, P, P), "multiple of 32"),
+    ((P, 4, 0, 32, P, P), "multiple of 32"),
+    ((P, 4, 64, 32, P, P), "ld_x must be >= K"),
+    ((P, 4, 64, 68, P, P), "multiple of 8"),
+    ((P + 2, 4, 64, 64, P, P), "x must be a 16-byte"),
+    ((P, 4, 64, 64, P + 2, P), "codes must be a 4-byte"),
+    ((P, 4, 64, 64, P, None), "scales is NULL"),
+    ((P, 1 << 40, 64, 64, P, P), "2^34"),
+])
+def test_quantize_refusals(lib, args, frag):
+    assert lib.smr_quantize_mxfp4(*args, None) in (INVALID, UNSUP)
+    assert frag in lib.smr_last_error().decode()
+
+
+def test_dequantize_and_layout_refusals(lib):
+    assert lib.smr_dequantize_mxfp4(P, P, 4, 64, P + 8, None) == INVALID
+    assert "out must be a 16-byte" in lib.smr_last_error().decode()
+    assert lib.smr_tile_mxfp4_scales(P, 2, 48, 128, 1, P, None) == INVALID
+    assert "multiple of 32" in lib.smr_last_error().decode()
+    assert lib.smr_tile_mxfp4_scales(P, 2, 64, 96, 0, P, None) == INVALID
+    assert lib.smr_tile_mxfp4_scales(P + 1, 2, 64, 128, 2, None, None) == INVALID
+    msg = lib.smr_last_error().decode()
+    assert "gated must" in msg and "scales must" in msg and "tiled must" in msg
+    assert lib.smr_mxfp4_tiled_scale_bytes(3, 160, 256, 0) == 3 * 2 * 2 * 512
+    assert lib.smr_mxfp4_tiled_scale_bytes(3, 160, 256, 1) == 3 * 2 * 2 * 512  # 80 features: two tiles of 64
+    assert lib.smr_mxfp4_tiled_scale_bytes(3, 160, 96, 0) == 0
+
+
+def _align_outputs(T, width, E, A):
+    cap = T * width + E * (A - 1)
+    return (torch.zeros(cap, dtype=torch.int32), torch.zeros((cap + A - 1) // A, dtype=torch.int32),
+            torch.zeros(1, dtype=torch.int32))
+
+
+def test_python_checks(smr):
+    T, width, E, H, I, A = 3, 2, 4, 64, 32, 64
+    x, w = torch.zeros(T, H, dtype=torch.bfloat16), torch.zeros(E, 2 * I, H, dtype=torch.bfloat16)
+    al = _align_outputs(T, width, E, A)
+    kw = dict(width=width, block_size=A)
+    with pytest.raises(ValueError, match="CUDA device"):
+        smr.expert_up(x, w, *al, **kw)
+    for bad, frag in ((dict(x=x.float()), "x must be"), (dict(x=x[:, ::2]), "x must be"), (dict(x=x[0]), "x must be"),
+                      (dict(w=w[:, :, :32]), "w must be"), (dict(w=w.transpose(1, 2)), "must be"),
+                      (dict(w=w[:, :33]), "2 I")):
+        with pytest.raises(ValueError, match=frag):
+            smr.expert_up(bad.get("x", x), bad.get("w", w), *al, **kw)
+    with pytest.raises(ValueError, match="int32"):
+        smr.expert_up(x, w, al[0].long(), al[1], al[2], **kw)
+    with pytest.raises(ValueError, match="entry for every block"):
+        smr.expert_up(x, w, al[0], al[1][:1], al[2], **kw)
+    with pytest.raises(ValueError, match="both be given"):
+        smr.expert_up(x, w, *al, x_scales=x, **kw)
+    ids, wts = torch.zeros(T, width, dtype=torch.int32), torch.zeros(T, width)
+    act, w2 = torch.zeros(T * width, I, dtype=torch.bfloat16), torch.zeros(E, H, I, dtype=torch.bfloat16)
+    for bad, frag in ((dict(ids=ids.long()), "topk_ids"), (dict(wts=wts.double()), "topk_weights"),
+                      (dict(act=act[:-1]), "x must be"), (dict(wts=wts[:2]), "topk_weights")):
+        with pytest.raises(ValueError, match=frag):
+            smr.expert_down(bad.get("act", act), w2, bad.get("ids", ids), bad.get("wts", wts), *al, block_size=A)
+    with pytest.raises(ValueError, match="CUDA device"):
+        smr.expert_down(act, w2, ids, wts, *al, block_size=A)
+
+
+def test_python_mxfp4_checks(smr):
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        smr.quantize_mxfp4(x)
+    with pytest.raises(ValueError, match="multiple of 32"):
+        smr.quantize_mxfp4(x[:, :48])
+    with pytest.raises(ValueError, match="bfloat16"):
+        smr.quantize_mxfp4(x.float())
+    with pytest.raises(ValueError, match="contiguous"):
+        smr.quantize_mxfp4(x.t())
+    c, s = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="scales must be"):
+        smr.dequantize_mxfp4(c, s[:, :1])
+    with pytest.raises(ValueError, match="CUDA device"):
+        smr.dequantize_mxfp4(c, s)
+    with pytest.raises(ValueError, match="scales must be"):
+        smr.tile_mxfp4_scales(c)
+    # MXFP4 operands of a product: types, scale shapes
+    al = _align_outputs(4, 1, 2, 64)
+    codes, sc = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8)
+    w = torch.zeros(2, 64, 64, dtype=torch.uint8)
+    ws = torch.zeros(2, 1, 1, 512, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="x_scales must be"):
+        smr.expert_up(codes, w, *al, width=1, block_size=64, x_scales=sc[:, :2], w_scales=ws)
+    with pytest.raises(ValueError, match="w_scales must be"):
+        smr.expert_up(codes, w, *al, width=1, block_size=64, x_scales=sc, w_scales=ws[:1])
+    with pytest.raises(ValueError, match="CUDA device"):
+        smr.expert_up(codes, w, *al, width=1, block_size=64, x_scales=sc, w_scales=ws)
+
+
+def test_disabled(smr, monkeypatch):
+    monkeypatch.setenv("SMR_DISABLE", "1")
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (lambda: smr.quantize_mxfp4(x), lambda: smr.dequantize_mxfp4(x, x), lambda: smr.tile_mxfp4_scales(x),
+                 lambda: smr.expert_up(x, x, x, x, x, width=1, block_size=64),
+                 lambda: smr.expert_down(x, x, x, x, x, x, x, block_size=64)):
+        with pytest.raises(smr.SmrUnsupported):
+            call()

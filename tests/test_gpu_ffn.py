@@ -122,9 +122,13 @@ def _close(got, ref, tol):
     assert (err <= tol).all(), f"max error / bound {(err / tol).max().item():.3g}"
 
 
+def _laid_out(smr, w, gated, **kw):
+    codes, scales = smr.quantize_mxfp4(w, **kw)
+    return codes, smr.tile_mxfp4_scales(scales, gated=gated, **kw)
+
+
 def _weights_mx(smr, w, gated):
-    codes, scales = smr.quantize_mxfp4(w)
-    return codes, smr.tile_mxfp4_scales(scales, gated=gated), _mx_exact(w)[2]
+    return *_laid_out(smr, w, gated), _mx_exact(w)[2]
 
 
 def _values(smr, x, mx):
@@ -146,6 +150,8 @@ SHAPES = [
     (300, 512, 192, 64, 1, 8, 64, 1.1),
     (1000, 256, 128, 16, 0, 4, 128, 2.0),  # hot experts over many blocks
     (2500, 128, 80, 6, 1, 3, 64, 0.0),
+    (4000, 400, 208, 5, 0, 2, 128, 0.0),  # pairs of CTAs: whole and partial tiles and k-blocks
+    (3000, 272, 336, 4, 1, 1, 64, 1.1),   # pairs, an odd number of weight tiles, groups of four blocks
 ]
 SHAPES_MX = [
     (1, 128, 128, 1, 0, 1, 64, 0.0),
@@ -268,3 +274,298 @@ def test_tiled_scales_layout(smr, E, N, K, gated):
             for q in range(K // 32):
                 got = t[:, tile, q // 4, (r % 32) * 16 + (r // 32) * 4 + q % 4]
                 assert torch.equal(got, s[:, row, q] if row is not None else torch.zeros(E, dtype=torch.uint8))
+
+
+def _case(smr, T=37, H=256, I=128, E=6, S=1, k=2, A=64, seed=3, mx=False):
+    ids, wts, g = _routing(T, E, k, S, 0.0, seed)
+    al = smr.align(ids, E + S, A)
+    x, w13, w2 = _normal(g, T, H), _normal(g, E + S, 2 * I, H, std=1.5 * H ** -0.5), _normal(g, E + S, H, I, std=I ** -0.5)
+    return ids, wts, al, x, w13, w2
+
+
+def _ffn(smr, c, mx=False, **kw):
+    ids, wts, al, x, w13, w2 = c
+    ku, kd = {}, {}
+    s = {"stream": kw["stream"]} if "stream" in kw else {}
+    if mx:
+        x, ku["x_scales"] = smr.quantize_mxfp4(x, **s)
+        w13, ku["w_scales"] = _laid_out(smr, w13, True, **s)
+    act = smr.expert_up(x, w13, *al, width=ids.shape[1], block_size=64, **ku, **kw)
+    y = act
+    if mx:
+        y, kd["x_scales"] = smr.quantize_mxfp4(act, **s)
+        w2, kd["w_scales"] = _laid_out(smr, w2, False, **s)
+    return act, smr.expert_down(y, w2, ids, wts, *al, block_size=64, **kd, **kw)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,E,k,S", [(4, 64, 4, 1), (200, 32, 4, 0), (600, 4, 2, 1)])
+def test_route_then_experts(smr, mx, T, E, k, S):
+    """The whole layer as it is used: route and align, the gated product, the
+    second product, each stage against 64 bits on the stage before it."""
+    H, I = 512, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + E)
+    x, gate = _normal(g, T, H), _normal(g, E, H, std=0.05)
+    shared = _normal(g, 1, H, std=0.05) if S else None
+    w13, w2 = _normal(g, E + S, 2 * I, H, std=H ** -0.5), _normal(g, E + S, H, I, std=I ** -0.5)
+    ids, wts, *al = smr.route_align(x, gate, shared, topk=k, block_size=64)
+    xa, kw, xv = _values(smr, x, mx)
+    wa, wv = w13, w13.double()
+    if mx:
+        wa, kw["w_scales"], wv = _weights_mx(smr, w13, True)
+    act = smr.expert_up(xa, wa, *al, width=k + S, block_size=64, **kw)
+    _close(act, *_ref_up(xv, wv, ids, k + S))
+    ya, kw, yv = _values(smr, act, mx)
+    wa, wv = w2, w2.double()
+    if mx:
+        wa, kw["w_scales"], wv = _weights_mx(smr, w2, False)
+    out = smr.expert_down(ya, wa, ids, wts, *al, block_size=64, **kw)
+    _close(out, *_ref_down(yv, wv, ids, wts))
+
+
+def test_strided_rows(smr):
+    ids, wts, al, x, w13, w2 = _case(smr)
+    wide = torch.full((x.shape[0], x.shape[1] + 72), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:8 + x.shape[1]] = x
+    part = wide[:, 8:8 + x.shape[1]]
+    a = smr.expert_up(part, w13, *al, width=ids.shape[1], block_size=64)
+    assert torch.equal(a, smr.expert_up(x, w13, *al, width=ids.shape[1], block_size=64))
+    one = smr.expert_up(part[:1], w13, *smr.align(ids[:1].contiguous(), 7, 64), width=ids.shape[1], block_size=64)
+    assert torch.equal(one, a[: ids.shape[1]])
+
+
+def test_skipped_slots(smr):
+    """Ids that no expert has (another rank's, say): their rows of act stay as
+    they were and they add nothing, also where a whole token has none."""
+    ids, wts, al, x, w13, w2 = _case(smr, T=50)
+    ids = ids.clone()
+    ids[3, 1], ids[7, 0], ids[20] = -1, 100, 7
+    ws = smr.Workspace(256)
+    al = smr.align(ids, 7, 64, workspace=ws)
+    assert smr.get_device_error(ws) == 1
+    out = torch.full((150, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    smr.expert_up(x, w13, *al, width=3, block_size=64, out=out)
+    gone = ((ids < 0) | (ids >= 7)).reshape(-1)
+    assert (out[gone] == 5.0).all() and gone.sum() == 5
+    ref, tol = _ref_up(x.double(), w13.double(), ids, 3)
+    _close(out[~gone], ref[~gone], tol[~gone])
+    out[gone] = float("nan")
+    y = smr.expert_down(out, w2, ids, wts, *al, block_size=64)
+    clean = torch.where(gone[:, None], torch.zeros_like(out), out)
+    _close(y, *_ref_down(clean.double(), w2.double(), ids, wts))
+    assert (y[20] == 0).all()
+
+
+def test_no_slot_at_all(smr):
+    ids, wts, al, x, w13, w2 = _case(smr, T=5)
+    ids = torch.full_like(ids, -1)
+    al = smr.align(ids, 7, 64, workspace=smr.Workspace(256))
+    assert int(al[2]) == 0
+    act = torch.full((15, 128), 2.0, dtype=torch.bfloat16, device="cuda")
+    smr.expert_up(x, w13, *al, width=3, block_size=64, out=act)
+    assert (act == 2.0).all()
+    assert (smr.expert_down(act, w2, ids, wts, *al, block_size=64) == 0).all()
+
+
+def test_remapped_experts(smr):
+    """Behind an EPLB remap: the weights are the physical experts', the ids the logical ones'."""
+    ids, wts, _, x, w13, w2 = _case(smr, T=90, E=6, S=0)
+    phys = torch.tensor([[0, 7], [1, 1], [2, 8], [3, 3], [4, 4], [5, 6]], dtype=torch.int32, device="cuda")
+    count = torch.tensor([2, 1, 2, 1, 1, 2], dtype=torch.int32, device="cuda")
+    al = smr.align(ids, 6, 64, eplb_map=phys, eplb_count=count, num_physical=9)
+    logical = torch.tensor([0, 1, 2, 3, 4, 5, 5, 0, 2], device="cuda")
+    act = smr.expert_up(x, w13[logical].contiguous(), *al, width=2, block_size=64)
+    _close(act, *_ref_up(x.double(), w13.double(), ids, 2))
+    out = smr.expert_down(act, w2[logical].contiguous(), ids, wts, *al, block_size=64, num_logical=6)
+    _close(out, *_ref_down(act.double(), w2.double(), ids, wts))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_captured_and_replayed(smr, mx):
+    """Two graphs captured without a workspace of their own, replayed on two
+    streams at once with new inputs between replays, next to eager calls."""
+    cases = [_case(smr, T=40, seed=s) for s in (5, 6)]
+    eager = [_ffn(smr, c, mx) for c in cases]
+    graphs, outs = [], []
+    for c in cases:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(_ffn(smr, c, mx))
+        graphs.append(gr)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for gr, s in zip(graphs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                gr.replay()
+        again = _ffn(smr, cases[0], mx)
+        assert torch.equal(again[1], eager[0][1])
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+    for got, ref in zip(outs, eager):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    cases[0][3].neg_()  # the first graph's hidden states
+    graphs[0].replay()
+    ref = _ffn(smr, cases[0], mx)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], ref[0]) and torch.equal(outs[0][1], ref[1])
+    assert not torch.equal(ref[0], eager[0][0])
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_streams(smr, mx):
+    c = _case(smr, T=300)
+    ref = _ffn(smr, c, mx)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [_ffn(smr, c, mx, stream=s) for s in streams for _ in range(4)]
+    outs.append(_ffn(smr, c, mx, stream=streams[0].cuda_stream))
+    with torch.cuda.stream(streams[1]):
+        outs.append(_ffn(smr, c, mx))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o[0], ref[0]) and torch.equal(o[1], ref[1])
+
+
+def test_one_workspace_for_every_call(smr):
+    """Route, align and both products in turn on one workspace: what one leaves
+    behind means nothing to the next."""
+    ws = smr.Workspace(64 << 20)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    refs = {}
+    for turn in range(3):
+        for T, E in ((4, 512), (16, 64), (300, 64)):
+            g.manual_seed(T)
+            x, gate = _normal(g, T, 256), _normal(g, E, 256, std=0.1)
+            w13, w2 = _normal(g, E, 128, 256, std=0.1), _normal(g, E, 256, 64, std=0.2)
+            ids, wts, *al = smr.route_align(x, gate, topk=4, block_size=64, workspace=ws)
+            act = smr.expert_up(x, w13, *al, width=4, block_size=64, workspace=ws)
+            out = smr.expert_down(act, w2, ids, wts, *al, block_size=64, workspace=ws)
+            got = (ids, wts, act, out)
+            ref = refs.setdefault(T, got)
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert smr.get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("A,T", [(64, 60), (128, 60), (128, 2000)])
+def test_bad_values_stay_in_their_rows(smr, A, T):
+    ids, wts, _, x, w13, w2 = _case(smr, T=T)
+    al = smr.align(ids, 7, A)
+    good = smr.expert_up(x, w13, *al, width=3, block_size=A)
+    x = x.clone()
+    x[11, 5], x[12, 3] = float("nan"), float("inf")
+    act = smr.expert_up(x, w13, *al, width=3, block_size=A)
+    tok = torch.arange(T * 3, device="cuda") // 3
+    keep = (tok != 11) & (tok != 12)
+    assert torch.equal(act[keep], good[keep]) and torch.isnan(act[tok == 11]).all()
+    assert not torch.isfinite(act[tok == 12]).any()
+    out = smr.expert_down(act, w2, ids, wts, *al, block_size=A)
+    assert torch.isfinite(out).all(1).logical_not().nonzero().flatten().tolist() == [11, 12]
+
+
+def test_not_a_number_blocks(smr):
+    ids, wts, al, x, w13, w2 = _case(smr, T=60)
+    x = x.clone()
+    x[9, 40] = float("nan")
+    codes, xs = smr.quantize_mxfp4(x)
+    w, ws, wv = _weights_mx(smr, w13, True)
+    act = smr.expert_up(codes, w, *al, width=3, block_size=64, x_scales=xs, w_scales=ws)
+    tok = torch.arange(180, device="cuda") // 3
+    assert torch.isnan(act[tok == 9]).all() and torch.isfinite(act[tok != 9]).all()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [3, 500, 3000])
+def test_same_bits_twice_and_tail_ignored(smr, T, mx):
+    c = _case(smr, T=T)
+    a = _ffn(smr, c, mx)
+    n = int(c[2][2])
+    c[2][0][n:] = torch.randint(0, T * 3, (c[2][0].numel() - n,), device="cuda", dtype=torch.int32)
+    c[2][1][n // 64:] = 3
+    b = _ffn(smr, c, mx)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_corrupted_align_outputs(smr):
+    """Entries that are neither slots nor the sentinel, experts that do not
+    exist and lengths past the arrays are flagged and skipped."""
+    ids, wts, al, x, w13, w2 = _case(smr, T=100)
+    good = smr.expert_up(x, w13, *al, width=3, block_size=64)
+    srt, eids, npp = (t.clone() for t in al)
+    bad_slot = int(srt[1])
+    srt[1] = 1 << 29
+    ws = smr.Workspace(256)
+    out = torch.zeros_like(good)
+    smr.expert_up(x, w13, srt, eids, npp, width=3, block_size=64, out=out, workspace=ws)
+    assert smr.get_device_error(ws) == 4
+    keep = torch.arange(300, device="cuda") != bad_slot
+    assert torch.equal(out[keep], good[keep]) and (out[bad_slot] == 0).all()
+    srt = al[0].clone()
+    srt[2] = -5
+    eids[0] = 7
+    ws = smr.Workspace(256)
+    smr.expert_up(x, w13, srt, eids, npp, width=3, block_size=64, workspace=ws)
+    assert smr.get_device_error(ws) == 5
+    for n in (1 << 30, -64):
+        ws = smr.Workspace(256)
+        npp.fill_(n)
+        srt, eids = al[0].clone(), al[1].clone()
+        srt[int(al[2]):] = 300
+        eids[int(al[2]) // 64:] = 0
+        out = torch.zeros_like(good)
+        smr.expert_up(x, w13, srt, eids, npp, width=3, block_size=64, out=out, workspace=ws)
+        assert smr.get_device_error(ws) == 0
+        assert torch.equal(out, good if n > 0 else torch.zeros_like(good))
+
+
+def test_offsets_past_32_bits(smr):
+    """Outputs and rows of more than 2^31 elements (and 2^32 bytes)."""
+    T, I, H = 140000, 16384, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    wts = torch.rand(T, 1, device="cuda", generator=g)
+    al = smr.align(ids, 1, 128)
+    x, w = _normal(g, T, H), _normal(g, 1, 2 * I, H, std=0.5)
+    act = smr.expert_up(x, w, *al, width=1, block_size=128)
+    rows = torch.tensor([0, 1, 65536, 131071, 131072, 131073, T - 1], device="cuda")
+    one = torch.zeros(rows.numel(), 1, dtype=torch.int32, device="cuda")
+    _close(act[rows], *_ref_up(x[rows].double(), w.double(), one, 1))
+    w2 = _normal(g, 1, H, I, std=I ** -0.5)
+    out = smr.expert_down(act, w2, ids, wts, *al, block_size=128)
+    _close(out[rows], *_ref_down(act[rows].double(), w2.double(), one, wts[rows]))
+    del act, out
+    w2 = _normal(g, 1, I, H, std=0.25)  # the rows before the sum: T * 16384
+    out = smr.expert_down(x, w2, ids, wts, *al, block_size=128)
+    _close(out[rows], *_ref_down(x[rows].double(), w2.double(), one, wts[rows]))
+
+
+def test_empty_batch(smr):
+    al = smr.align(torch.zeros(0, 2, dtype=torch.int32, device="cuda"), 4, 64)
+    w13 = torch.zeros(4, 32, 64, dtype=torch.bfloat16, device="cuda")
+    act = smr.expert_up(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), w13, *al, width=2, block_size=64)
+    assert act.shape == (0, 16) and smr.last_launch_count() == 0
+    out = smr.expert_down(act, torch.zeros(4, 64, 16, dtype=torch.bfloat16, device="cuda"),
+                          torch.zeros(0, 2, dtype=torch.int32, device="cuda"), torch.zeros(0, 2, device="cuda"),
+                          *al, block_size=64)
+    assert out.shape == (0, 64) and smr.last_launch_count() == 0
+
+
+def test_given_outputs_and_launches(smr):
+    c = _case(smr, T=9)
+    ids, wts, al, x, w13, w2 = c
+    ref = _ffn(smr, c)
+    act, out = torch.empty_like(ref[0]), torch.empty_like(ref[1])
+    assert smr.expert_up(x, w13, *al, width=3, block_size=64, out=act) is act and smr.last_launch_count() == 1
+    assert smr.expert_down(act, w2, ids, wts, *al, block_size=64, out=out) is out and smr.last_launch_count() == 2
+    assert torch.equal(act, ref[0]) and torch.equal(out, ref[1])
+    with pytest.raises(ValueError, match="out must be"):
+        smr.expert_up(x, w13, *al, width=3, block_size=64, out=act[:-1])
+    with pytest.raises(ValueError, match="one device"):
+        smr.expert_up(x, w13.cpu(), *al, width=3, block_size=64)
+    with pytest.raises(smr.SmrUnsupported, match="64 or 128"):
+        smr.expert_up(x, w13, *al, width=3, block_size=256)
+    with pytest.raises(smr.SmrError, match="16-byte aligned"):
+        smr.expert_up(torch.zeros(9, 264, dtype=torch.bfloat16, device="cuda")[:, 4:260], w13, *al, width=3, block_size=64)
