@@ -359,7 +359,41 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         const int bo = 8 * lane / A, po = 8 * lane % A;  // this lane's 8 entries: block of the group, place in it
         const bool in = bo < G;
         const bool wide = (reinterpret_cast<uintptr_t>(p.sorted) & 15) == 0;
-        const int nblk = max(0, min(__ldcg(p.npp) / A, p.max_blocks));
+        // the entries and the block's expert (of blocks below `limit`),
+        // requested two items ahead (a round trip to L2 is longer than a short
+        // item)
+        auto fetch = [&](int b0, int limit, int (&ent)[8], int &e) {
+            const int b = b0 + bo;
+            if (!in || b0 < 0 || b >= limit) return;
+            const int64_t at = (int64_t)b * A + po;
+            e = __ldcg(p.eids + b);
+            if (wide && at + 8 <= p.sorted_cap) {
+                const int4 lo = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at));
+                const int4 hi = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at) + 1);
+                ent[0] = lo.x; ent[1] = lo.y; ent[2] = lo.z; ent[3] = lo.w;
+                ent[4] = hi.x; ent[5] = hi.y; ent[6] = hi.z; ent[7] = hi.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ent[j] = at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
+            }
+        };
+        auto step = [&](int &g, int &t) {
+            g += dgrp;
+            t += dtile;
+            if (t >= tiles) {
+                t -= tiles;
+                ++g;
+            }
+        };
+        int ent0[8], ent1[8], e0 = -1, e1 = -1, slot[8];
+        int grp2 = grp, tile2 = tile;  // the item after the next
+        const int npp = __ldcg(p.npp);
+        if constexpr (!PAIR) {  // the first two at once with npp: what lies past it is left out below
+            fetch(grp, p.max_blocks, ent0, e0);
+            step(grp2, tile2);
+            fetch(grp2, p.max_blocks, ent1, e1);
+        }
+        const int nblk = max(0, min(npp / A, p.max_blocks));
         // First block of group g (asked for in ascending order), -1 past the
         // last: 32 blocks at a time, a bit for every block that starts one,
         // which is every G-th block of an expert's segment.
@@ -384,31 +418,6 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 return scan_at + (int)__fns(starts, 0, g - scan_base + 1);
             } else {
                 return g < nblk ? g : -1;
-            }
-        };
-        // the entries and the block's expert, requested two items ahead (a
-        // round trip to L2 is longer than a short item)
-        auto fetch = [&](int b0, int (&ent)[8], int &e) {
-            const int b = b0 + bo;
-            if (!in || b0 < 0 || b >= nblk) return;
-            const int64_t at = (int64_t)b * A + po;
-            e = __ldcg(p.eids + b);
-            if (wide && at + 8 <= p.sorted_cap) {
-                const int4 lo = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at));
-                const int4 hi = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at) + 1);
-                ent[0] = lo.x; ent[1] = lo.y; ent[2] = lo.z; ent[3] = lo.w;
-                ent[4] = hi.x; ent[5] = hi.y; ent[6] = hi.z; ent[7] = hi.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ent[j] = at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
-            }
-        };
-        auto step = [&](int &g, int &t) {
-            g += dgrp;
-            t += dtile;
-            if (t >= tiles) {
-                t -= tiles;
-                ++g;
             }
         };
         RingPos iq;
@@ -439,13 +448,13 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         for (int64_t i = ((int64_t)blockIdx.x * 32 + lane) * 32; i < min((int64_t)nblk * A, p.sorted_cap);
              i += (int64_t)gridDim.x * 32 * 32)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sorted + i));
-        int ent0[8], ent1[8], e0 = -1, e1 = -1, slot[8];
-        int grp2 = grp, tile2 = tile;  // the item after the next
-        int at0 = locate(grp);         // first blocks of this item's and the next one's groups
-        fetch(at0, ent0, e0);
-        step(grp2, tile2);
+        int at0 = locate(grp);  // first blocks of this item's and the next one's groups
+        if constexpr (PAIR) {
+            fetch(at0, nblk, ent0, e0);
+            step(grp2, tile2);
+        }
         int at1 = locate(grp2);
-        fetch(at1, ent1, e1);
+        if constexpr (PAIR) fetch(at1, nblk, ent1, e1);
         step(grp2, tile2);
         auto take = [&](int &at, int (&ent)[8], int &e) {
             // the item whose first block is `at`; then the one after the next is requested
@@ -469,7 +478,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
             const int nt = PAIR ? 2 * tile + (int)rank : tile;
             at = locate(grp2);
-            fetch(at, ent, e);
+            fetch(at, nblk, ent, e);
             step(grp, tile);
             step(grp2, tile2);
             if (rows == 0) return;
