@@ -176,7 +176,8 @@ cudaError_t launch_expert_gemm(const ExpertGemmLaunch &a, cudaStream_t stream);
 
 // The experts' feed-forward: the gated product (gated: w [num_experts][2
 // feat][K], out = silu(gate) * up) or the plain one (w [num_experts][feat][K])
-// over the align's blocks; out bf16 [numel][feat], one row per routed slot.
+// over the align's blocks; out bf16 (or fp32) [numel][feat], one row per
+// routed slot.
 // x_scales != nullptr: x and w are MXFP4 codes.
 struct FfnLaunch {
     const void *x;
@@ -188,7 +189,8 @@ struct FfnLaunch {
     int width, K, feat, A, num_experts;
     int64_t numel, sorted_cap;
     const int32_t *sorted, *eids, *npp;
-    uint16_t *out;
+    void *out;
+    bool out32;              // (not gated) out is fp32
     void *hdr;               // workspace header (sticky error word)
 };
 cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream);
@@ -196,7 +198,8 @@ cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream);
 // out[t] = sum over s of wts[t][s] * y[t * width + s], slots whose id is
 // outside [0, num_logical) left out.
 struct CombineLaunch {
-    const uint16_t *y;       // bf16 [T * width][H]
+    const void *y;           // [T * width][H], fp32 where y32, else bf16
+    bool y32;
     const int32_t *ids;      // [T][width]
     const float *wts;
     uint16_t *out;           // bf16 [T][H]

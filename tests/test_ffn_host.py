@@ -112,8 +112,10 @@ def test_workspaces(lib):
     up, down = _up(), _down()
     assert lib.smr_expert_up_workspace_size(ctypes.byref(up)) == 256
     # the rows sit behind a small route's keys (16 tokens x 1024 experts x 8 bytes)
-    need = 256 + 16 * 1024 * 8 + 44 * 256 * 2
+    need = 256 + 16 * 1024 * 8 + 44 * 256 * 4  # fp32 rows
     assert lib.smr_expert_down_workspace_size(ctypes.byref(down)) == need
+    many = _down(num_tokens=4096)  # above 2^23 values: bf16 rows
+    assert lib.smr_expert_down_workspace_size(ctypes.byref(many)) == 256 + 16 * 1024 * 8 + 4096 * 11 * 256 * 2
     assert lib.smr_expert_up(ctypes.byref(up), None, 0, None) == WORKSPACE
     assert lib.smr_expert_down(ctypes.byref(down), P, need - 1, None) == WORKSPACE
     assert lib.smr_expert_down(ctypes.byref(down), P + 128, need, None) == WORKSPACE
