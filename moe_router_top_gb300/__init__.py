@@ -373,14 +373,15 @@ def expert_gemm(hidden, expert_w, sorted_token_ids, expert_ids, num_tokens_post_
     return out
 
 
-def _check_cuda(first, *others) -> int:
-    """Index of the first tensor's CUDA device, which every other one must be on."""
-    dev = first.get_device()
+def _check_cuda(*tensors) -> int:
+    """Index of the CUDA device that every tensor (None is left out) is on."""
+    devices = {t.get_device() for t in tensors if t is not None}
+    dev = devices.pop()
+    if devices:
+        raise ValueError("tensors must be on one device (got "
+                         + ", ".join(sorted({str(t.device) for t in tensors if t is not None})) + ")")
     if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on one device (got {first.device} and {t.device})")
     return dev
 
 
@@ -389,7 +390,7 @@ def _elsewhere(dev: int, stream):
     of the current device."""
     torch = _torch()
     if stream is None:
-        return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+        return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev)
     return torch.cuda.stream(stream)
@@ -405,7 +406,7 @@ def _ffn_workspace(ws, nbytes: int, dev: int, s: int):
     and zeroes itself."""
     torch = _torch()
     if ws is None:
-        if torch.cuda.is_current_stream_capturing():
+        if torch._C._cuda_isCurrentStreamCapturing():
             buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
             buf[:256].zero_()
             return buf.data_ptr(), nbytes
@@ -414,7 +415,7 @@ def _ffn_workspace(ws, nbytes: int, dev: int, s: int):
             ws = _stream_ws[(dev, s)] = Workspace(0, torch.device("cuda", dev))
     if isinstance(ws, Workspace):
         ws = ws.ensure(nbytes)
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated, sorted_token_ids, expert_ids, npp, block_size):
