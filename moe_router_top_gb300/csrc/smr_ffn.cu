@@ -40,7 +40,7 @@ constexpr int kFfThreads = 32 * (3 + kFfLoaders<SUB> + kFfDrains);
 constexpr int kFfRows = 128;                     // weight rows of a tile (the MMA's M)
 constexpr int kFfRowBytes = 128;                 // one k-block of a row: 64 bf16 or 256 MXFP4
 constexpr int kFfWBytes = kFfRows * kFfRowBytes;  // weight tile of a stage
-constexpr int kFfMaxStages = 6;
+constexpr int kFfMaxStages = 8;
 // Pieces of work known ahead of the epilogue: with a short contraction (MXFP4,
 // K = 512: two k-blocks a piece) these bound the weights in flight.
 constexpr int kFfInfos = 8;
@@ -63,10 +63,12 @@ struct FfInfo {
 };
 constexpr int kFfBars = 2 * kFfMaxStages + 4 + 2 * kFfInfos + 1;
 constexpr int kFfBarBytes = (kFfBars * 8 + 8 + 15) / 16 * 16;
-template <bool PAIR>
-constexpr int kFfCols = PAIR ? 256 : 128;  // columns of a piece, at most
-template <bool PAIR>
-constexpr int kFfMiscBytes = kFfBarBytes + kFfInfos * (int)sizeof(FfInfo<kFfCols<PAIR>>);
+// Columns of a piece, at most. (A pair of MXFP4: 128, as two accumulators of
+// 256 columns would leave no room in TMEM for the scales.)
+template <bool MX, bool PAIR>
+constexpr int kFfCols = PAIR && !MX ? 256 : 128;
+template <bool MX, bool PAIR>
+constexpr int kFfMiscBytes = kFfBarBytes + kFfInfos * (int)sizeof(FfInfo<kFfCols<MX, PAIR>>);
 
 struct FfParams {
     int num_kb, last_steps;  // k-blocks; MMA steps of the last one (4 in the others)
@@ -163,21 +165,31 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n) {
 }
 // D[tmem] (+)= (A * scale_A) (B * scale_B)^T, 4-bit operands, one scale per 32
 // values of K, fp32 accumulation.
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+            ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
 }
 // 512 bytes of scales (32 rows of 16 bytes) into 4 TMEM columns, the same in
-// every quarter of the lanes. Ordered before the MMAs that this thread issues
-// next, and behind those that it issued.
+// every quarter of the lanes (of a pair: in each CTA from its own shared
+// memory). Ordered before the MMAs that this thread issues next, and behind
+// those that it issued.
+template <bool PAIR>
 __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t saddr) {
     // no swizzle, 8-row groups 128 bytes apart (stride byte offset >> 4 in
     // bits 32-45), descriptor version 1
     const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128u >> 4) << 32) | ((uint64_t)1 << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 // silu(g) * u in fp32. The fast exponential and division are within a few
@@ -239,13 +251,15 @@ struct RingPos {
 // MX: MXFP4 operands, else bf16. UP: the gated product (a tile holds 64
 // features: 16 gate rows and their 16 up rows in turn, so that both halves of
 // a feature are in one warp's TMEM lanes), else 128 plain rows. PAIR: two CTAs
-// on one 256-row tile and up to 256 columns (blocks of one expert next to each
-// other together); each holds its own 128 weight rows and half of the routed
-// rows, and drains its own lanes.
+// on one 256-row tile and up to kCols columns (blocks of one expert next to
+// each other together); each holds its own 128 weight rows (and their scales),
+// half of the routed rows and all of these rows' scales, and drains its own
+// lanes.
 template <bool MX, bool UP, bool PAIR, int SUB>
 __global__ void __launch_bounds__(kFfThreads<SUB>, 1)
 expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
-    using Info = FfInfo<kFfCols<PAIR>>;
+    constexpr int kCols = kFfCols<MX, PAIR>;
+    using Info = FfInfo<kCols>;
     constexpr int kLoaders = kFfLoaders<SUB>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -330,11 +344,15 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (elected) {
                     if constexpr (PAIR) {
                         // both CTAs' bytes complete the leader's barrier
-                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
+                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * subs * kFfWBytes);
                         const uint32_t fb = cluster_addr(bar, 0u);
-                        const int xk = kb * (kFfRowBytes / 2);
-                        if constexpr (UP) tma_load_5d_pair(base, &tm_w, xk, nt * 4, e, fb);
-                        else tma_load_3d_pair(base, &tm_w, xk, nt * kFfRows, e, fb);
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            if (u >= subs) break;
+                            const int xk = (kb + u) * (MX ? kFfRowBytes : kFfRowBytes / 2);
+                            if constexpr (UP) tma_load_5d_pair(base + u * kFfWBytes, &tm_w, xk, nt * 4, e, fb);
+                            else tma_load_3d_pair(base + u * kFfWBytes, &tm_w, xk, nt * kFfRows, e, fb);
+                        }
                     } else {
                         uint32_t sbytes = 0;
                         if constexpr (MX) sbytes = (uint32_t)min(2 * SUB, p.num_chunks - 2 * kb) * kSfAtom;
@@ -357,11 +375,11 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     } else if (warp == 2) {
         // ------------------------------------------------------ scout ----
         // An item is a group of blocks of one expert (one block; PAIR: up to
-        // 256 / A, counted from the expert's first) and a weight tile (PAIR:
+        // kCols / A, counted from the expert's first) and a weight tile (PAIR:
         // two). Both CTAs of a pair walk the same items. CTAs take every
         // gridDim-th item: a block's tiles run next to each other in time
         // (its rows stay in L2), blocks of one expert too (its weights).
-        const int A = p.A, G = PAIR ? 256 / A : 1;
+        const int A = p.A, G = PAIR ? kCols / A : 1;
         const int tiles = PAIR ? (p.ntiles + 1) / 2 : p.ntiles;
         const int ctas = PAIR ? gridDim.x >> 1 : gridDim.x, cta = PAIR ? blockIdx.x >> 1 : blockIdx.x;
         const int dgrp = ctas / tiles, dtile = ctas % tiles;
@@ -526,7 +544,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
             tc_fence_after();
             const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols);
-            const uint32_t idesc = MX ? idesc_mxf4(kFfRows, n) : idesc_bf16_f32(PAIR ? 2 * kFfRows : kFfRows, n);
+            constexpr int kM = PAIR ? 2 * kFfRows : kFfRows;
+            const uint32_t idesc = MX ? idesc_mxf4(kM, n) : idesc_bf16_f32(kM, n);
             for (int kb = 0; kb < p.num_kb; kb += SUB) {
                 if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
                 tc_fence_after();
@@ -542,15 +561,15 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     if constexpr (MX) {
                         const uint32_t sa = base + ws_off + 2 * u * kSfAtom, sb = base + xs_off + 2 * u * kSfAtom;
                         if (elected) {
-                            tc_cp_scales(sf, sa);
-                            tc_cp_scales(sf + 8, sb);
-                            tc_mma_mxf4(acc, da, db, idesc, sf, sf + 8, more);
-                            tc_mma_mxf4(acc, da + 2, db + 2, idesc | (1u << 30) | (1u << 5), sf, sf + 8, 1u);
+                            tc_cp_scales<PAIR>(sf, sa);
+                            tc_cp_scales<PAIR>(sf + 8, sb);
+                            tc_mma_mxf4<PAIR>(acc, da, db, idesc, sf, sf + 8, more);
+                            tc_mma_mxf4<PAIR>(acc, da + 2, db + 2, idesc | (1u << 30) | (1u << 5), sf, sf + 8, 1u);
                             if (steps == 4) {
-                                tc_cp_scales(sf + 4, sa + kSfAtom);
-                                tc_cp_scales(sf + 12, sb + kSfAtom);
-                                tc_mma_mxf4(acc, da + 4, db + 4, idesc, sf + 4, sf + 12, 1u);
-                                tc_mma_mxf4(acc, da + 6, db + 6, idesc | (1u << 30) | (1u << 5), sf + 4, sf + 12, 1u);
+                                tc_cp_scales<PAIR>(sf + 4, sa + kSfAtom);
+                                tc_cp_scales<PAIR>(sf + 12, sb + kSfAtom);
+                                tc_mma_mxf4<PAIR>(acc, da + 4, db + 4, idesc, sf + 4, sf + 12, 1u);
+                                tc_mma_mxf4<PAIR>(acc, da + 6, db + 6, idesc | (1u << 30) | (1u << 5), sf + 4, sf + 12, 1u);
                             }
                         }
                         sf ^= 16u;
@@ -630,19 +649,29 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         }
                     }
                     if constexpr (MX) {
-                        // scale of row r, block q of a 128-value piece: byte
+                        // scale of column r, block q of a 128-value piece: byte
                         // (r % 32) * 16 + (r / 32) * 4 + q of its 512
                         const uint32_t sd = base + xs_off + lane * 16;
                         const int pieces = min(2 * SUB, p.num_chunks - 2 * kb);
                         int row[kFfRows / 32];
 #pragma unroll
-                        for (int j = 0; j < kFfRows / 32; ++j) row[j] = lane + 32 * j < n ? inf->row[lane + 32 * j] : -1;
+                        for (int j = 0; j < kFfRows / 32; ++j) row[j] = lane + 32 * j < all ? inf->row[lane + 32 * j] : -1;
 #pragma unroll
                         for (int j = 0; j < kFfRows / 32; ++j) {
                             const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)row[j] * (uint32_t)p.num_chunks + 2 * kb) * 4;
 #pragma unroll
                             for (int q = 0; q < 2 * SUB; ++q)
                                 cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q, q < pieces ? row[j] : -1);
+                        }
+                        // (of a pair: the weights' scales too, as a plain bulk
+                        // copy cannot complete the other CTA's barrier)
+                        if constexpr (PAIR) {
+                            const uint8_t *src = p.w_scales +
+                                (((int64_t)inf->e * p.ntiles + min(inf->nt, p.ntiles - 1)) * p.num_chunks + 2 * kb) * kSfAtom;
+#pragma unroll
+                            for (int i = 0; i < 2 * SUB; ++i)
+                                cp_async_16(base + ws_off + i * kSfAtom + lane * 16, src + i * kSfAtom + lane * 16,
+                                            i < pieces ? 0 : -1);
                         }
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -856,7 +885,12 @@ expert_combine_kernel(const void *__restrict__ y, const int32_t *__restrict__ id
 
 // ---------------------------------------------------------------- host --
 
-// CTA pairs from this many rows an expert, on average.
+// CTA pairs from this many rows an expert, on average: a pair halves the rows
+// that each CTA loads and that its MMAs read (16384 tokens, 1024 rows an
+// expert: bf16 588 us with pairs, 847 without; MXFP4 266 and 314; 2047 skewed
+// tokens, 128 rows: down 103 and 114), but below a block an expert it only
+// leaves half as many items to share out (512 skewed tokens, 32 rows: 143 and
+// 134).
 constexpr int kPairRows = 96;
 
 static int sm_count() {
@@ -918,16 +952,17 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.w_scales = a.w_scales;
     p.num_chunks = a.K / 128;
     p.err = &reinterpret_cast<WsHeader *>(a.hdr)->error;
-    p.b_bytes = (uint32_t)(PAIR ? kFfRows : a.A) * kFfRowBytes;
+    constexpr int kCols = kFfCols<MX, PAIR>;
+    p.b_bytes = (uint32_t)(PAIR ? kCols / 2 : a.A) * kFfRowBytes;
     p.stage_bytes = SUB * (kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0));
     constexpr uint32_t kSmemMax = 232448;
-    p.stages = (int)((kSmemMax - 1024 - kFfMiscBytes<PAIR>) / p.stage_bytes);
+    p.stages = (int)((kSmemMax - 1024 - kFfMiscBytes<MX, PAIR>) / p.stage_bytes);
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
     if (p.stages < kFfLoaders<SUB>) return cudaErrorNotSupported;  // (see the row loaders; never with these sizes)
-    p.acc_cols = PAIR ? kFfCols<PAIR> : a.A;
+    p.acc_cols = PAIR ? kCols : a.A;
     const int cols = 2 * p.acc_cols + (MX ? 32 : 0);
     p.tmem_cols = cols <= 128 ? 128 : (cols <= 256 ? 256 : 512);
-    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + kFfMiscBytes<PAIR>;
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + kFfMiscBytes<MX, PAIR>;
 
     const CUtensorMapDataType type = MX ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const cuuint64_t k_elems = (cuuint64_t)(MX ? a.K / 2 : a.K), k_bytes = MX ? k_elems : 2 * k_elems;
@@ -982,7 +1017,8 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
 }
 
 template <bool MX, bool UP>
-static cudaError_t launch_single(const FfnLaunch &a, int sms, cudaStream_t stream) {
+static cudaError_t launch_format(const FfnLaunch &a, int sms, cudaStream_t stream) {
+    if (a.numel >= (int64_t)kPairRows * a.num_experts) return launch_product<MX, UP, true, MX ? 2 : 1>(a, sms, stream);
     return a.A == 64 ? launch_product<MX, UP, false, 2>(a, sms, stream) : launch_product<MX, UP, false, 1>(a, sms, stream);
 }
 
@@ -990,11 +1026,8 @@ cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms < 2) return cudaErrorInvalidDevice;
     if (a.x_scales != nullptr)
-        return a.gated ? launch_single<true, true>(a, sms, stream) : launch_single<true, false>(a, sms, stream);
-    if (a.numel >= (int64_t)kPairRows * a.num_experts)
-        return a.gated ? launch_product<false, true, true, 1>(a, sms, stream)
-                       : launch_product<false, false, true, 1>(a, sms, stream);
-    return a.gated ? launch_single<false, true>(a, sms, stream) : launch_single<false, false>(a, sms, stream);
+        return a.gated ? launch_format<true, true>(a, sms, stream) : launch_format<true, false>(a, sms, stream);
+    return a.gated ? launch_format<false, true>(a, sms, stream) : launch_format<false, false>(a, sms, stream);
 }
 
 cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream) {

@@ -160,10 +160,15 @@ SHAPES_MX = [
     (40, 256, 128, 3, 0, 2, 128, 0.0),
     (300, 512, 256, 64, 1, 8, 64, 1.1),
     (1000, 256, 640, 16, 0, 4, 128, 2.0),
+    (2000, 384, 384, 5, 1, 2, 64, 0.0),   # pairs of CTAs, half a k-block
+    (1500, 640, 256, 4, 0, 2, 128, 1.1),
 ]
+# output features in partial tiles (only the contraction is in whole scale groups)
+UP_MX = SHAPES_MX + [(20, 256, 80, 3, 0, 2, 64, 0.0), (600, 256, 208, 3, 0, 2, 64, 0.0), (700, 128, 176, 4, 1, 1, 128, 0.0)]
+DOWN_MX = SHAPES_MX + [(20, 80, 256, 3, 0, 2, 64, 0.0), (600, 272, 256, 3, 0, 2, 64, 0.0), (700, 400, 128, 4, 1, 1, 128, 0.0)]
 
 
-@pytest.mark.parametrize("mx,shape", [(False, s) for s in SHAPES] + [(True, s) for s in SHAPES_MX])
+@pytest.mark.parametrize("mx,shape", [(False, s) for s in SHAPES] + [(True, s) for s in UP_MX])
 def test_up_matches_64_bits(smr, mx, shape):
     T, H, I, E, S, k, A, zipf = shape
     ids, _, g = _routing(T, E, k, S, zipf, 11 + T)
@@ -181,7 +186,7 @@ def test_up_matches_64_bits(smr, mx, shape):
     _close(out, *_ref_up(xv, wv, ids, k + S))
 
 
-@pytest.mark.parametrize("mx,shape", [(False, s) for s in SHAPES] + [(True, s) for s in SHAPES_MX])
+@pytest.mark.parametrize("mx,shape", [(False, s) for s in SHAPES] + [(True, s) for s in DOWN_MX])
 def test_down_matches_64_bits(smr, mx, shape):
     T, H, I, E, S, k, A, zipf = shape
     ids, wts, g = _routing(T, E, k, S, zipf, 31 + T)
