@@ -28,10 +28,11 @@
 
 namespace smr {
 
-// k-blocks a stage: two for blocks of 64 rows. A stage costs every role a few
-// hundred cycles of barrier round trips whatever its size (550 a stage of one
-// k-block, 30 bytes a cycle: too few where a single token leaves an SM's share
-// of the memory rate to a few CTAs).
+// k-blocks a stage: two for blocks of 64 rows and for pairs in MXFP4, else one
+// (a stage would be too large for a ring of them). A stage costs every role a
+// few hundred cycles of barrier round trips whatever its size: 550 a stage of
+// one k-block, 430 a k-block in stages of two (one token, 96 items; MXFP4 up,
+// 16384 tokens: 261 us in stages of one, 240 in stages of two).
 template <int SUB>
 constexpr int kFfLoaders = SUB == 2 ? 4 : 6;     // warps that load the routed rows; at most the stages
 constexpr int kFfDrains = 8;                     // warps of the epilogue, two for each quarter of TMEM's lanes
@@ -88,6 +89,7 @@ struct FfParams {
     int out32;
     const uint8_t *x_scales, *w_scales;  // MXFP4
     int num_chunks;          // MXFP4: K / 128
+    int scale_bytes;         // MXFP4: rows of x_scales can be read 16, 8 or 4 bytes at a time
     uint32_t *err;
     uint32_t stage_bytes, b_bytes;
 };
@@ -144,6 +146,15 @@ __device__ __forceinline__ void ff_commit(uint64_t *bar) {
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+// Loads of 16 or 8 bytes where row >= 0, else the registers stay as they are.
+__device__ __forceinline__ void ld_cg_16(uint32_t *v, const void *src, int row) {
+    asm volatile("{\n .reg .pred q;\n setp.ge.s32 q, %5, 0;\n @q ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]) : "l"(src), "r"(row));
+}
+__device__ __forceinline__ void ld_cg_8(uint32_t *v, const void *src, int row) {
+    asm volatile("{\n .reg .pred q;\n setp.ge.s32 q, %3, 0;\n @q ld.global.cg.v2.u32 {%0, %1}, [%2];\n}"
+                 : "+r"(v[0]), "+r"(v[1]) : "l"(src), "r"(row));
 }
 // Copies that happen where row >= 0 (predicated: a branch a row cost the
 // large batches 15%).
@@ -630,6 +641,38 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
                     const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
                     const int kb = next * SUB;
+                    // MXFP4: this lane's columns' scales of the stage. Where rows
+                    // can be read in wider pieces they pass through registers,
+                    // requested before the rows are copied and stored after:
+                    // a gather of 32 rows costs the load unit 32 cycles
+                    // whatever its width, and 4-byte copies take four for the
+                    // 16 bytes of a stage (MXFP4 up, 16384 tokens: 266 us
+                    // with those, 240 with 16-byte loads).
+                    constexpr int kSets = MX ? kCols / 32 : 1, kWords = 2 * SUB;
+                    uint32_t scale[kSets][kWords];
+                    int srow[kSets];
+                    if constexpr (MX) {
+#pragma unroll
+                        for (int j = 0; j < kSets; ++j) {
+                            srow[j] = lane + 32 * j < all ? inf->row[lane + 32 * j] : -1;
+#pragma unroll
+                            for (int q = 0; q < kWords; ++q) scale[j][q] = 0u;
+                        }
+                        if (p.scale_bytes > 4) {
+#pragma unroll
+                            for (int j = 0; j < kSets; ++j) {
+                                const uint32_t *src = reinterpret_cast<const uint32_t *>(p.x_scales) +
+                                                      (uint64_t)(uint32_t)srow[j] * (uint32_t)p.num_chunks + 2 * kb;
+                                if (kWords == 4 && p.scale_bytes == 16) {
+                                    ld_cg_16(scale[j], src, srow[j]);
+                                } else {
+#pragma unroll
+                                    for (int q = 0; q < kWords; q += 2)
+                                        ld_cg_8(scale[j] + q, src + q, 2 * kb + q < p.num_chunks ? srow[j] : -1);
+                                }
+                            }
+                        }
+                    }
                     // (chunks past the row's end are not read by the last MMA steps)
                     const int off = kb * kFfRowBytes + c * 16, ends = p.x_bytes;
                     const uint8_t *x = p.x + off;
@@ -652,16 +695,22 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         // scale of column r, block q of a 128-value piece: byte
                         // (r % 32) * 16 + (r / 32) * 4 + q of its 512
                         const uint32_t sd = base + xs_off + lane * 16;
-                        const int pieces = min(2 * SUB, p.num_chunks - 2 * kb);
-                        int row[kFfRows / 32];
+                        const int pieces = min(kWords, p.num_chunks - 2 * kb);
+                        if (p.scale_bytes > 4) {
 #pragma unroll
-                        for (int j = 0; j < kFfRows / 32; ++j) row[j] = lane + 32 * j < all ? inf->row[lane + 32 * j] : -1;
+                            for (int j = 0; j < kSets; ++j)
 #pragma unroll
-                        for (int j = 0; j < kFfRows / 32; ++j) {
-                            const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)row[j] * (uint32_t)p.num_chunks + 2 * kb) * 4;
+                                for (int q = 0; q < kWords; ++q)
+                                    asm volatile("st.shared.b32 [%0], %1;"
+                                                 ::"r"(sd + q * kSfAtom + j * 4), "r"(scale[j][q]) : "memory");
+                        } else {
 #pragma unroll
-                            for (int q = 0; q < 2 * SUB; ++q)
-                                cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q, q < pieces ? row[j] : -1);
+                            for (int j = 0; j < kSets; ++j) {
+                                const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)srow[j] * (uint32_t)p.num_chunks + 2 * kb) * 4;
+#pragma unroll
+                                for (int q = 0; q < kWords; ++q)
+                                    cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q, q < pieces ? srow[j] : -1);
+                            }
                         }
                         // (of a pair: the weights' scales too, as a plain bulk
                         // copy cannot complete the other CTA's barrier)
@@ -951,6 +1000,8 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.x_scales = a.x_scales;
     p.w_scales = a.w_scales;
     p.num_chunks = a.K / 128;
+    const uintptr_t scales_at = reinterpret_cast<uintptr_t>(a.x_scales) | (uintptr_t)(4 * p.num_chunks);
+    p.scale_bytes = scales_at % 16 == 0 ? 16 : (scales_at % 8 == 0 ? 8 : 4);
     p.err = &reinterpret_cast<WsHeader *>(a.hdr)->error;
     constexpr int kCols = kFfCols<MX, PAIR>;
     p.b_bytes = (uint32_t)(PAIR ? kCols / 2 : a.A) * kFfRowBytes;

@@ -574,3 +574,20 @@ def test_given_outputs_and_launches(smr):
         smr.expert_up(x, w13, *al, width=3, block_size=256)
     with pytest.raises(smr.SmrError, match="16-byte aligned"):
         smr.expert_up(torch.zeros(9, 264, dtype=torch.bfloat16, device="cuda")[:, 4:260], w13, *al, width=3, block_size=64)
+
+
+@pytest.mark.parametrize("K", [128, 256, 512])
+@pytest.mark.parametrize("shift", [0, 4, 8])
+@pytest.mark.parametrize("T", [20, 600])
+def test_scale_rows_of_any_alignment(smr, K, shift, T):
+    """Rows of scales that can be read 16, 8 or only 4 bytes at a time."""
+    ids, _, al, x, w13, _ = _case(smr, T=T, H=K)
+    w, ws = _laid_out(smr, w13, True)
+    codes, xs = smr.quantize_mxfp4(x)
+    ref = smr.expert_up(codes, w, *al, width=3, block_size=64, x_scales=xs, w_scales=ws)
+    buf = torch.full((xs.numel() + shift,), 255, dtype=torch.uint8, device="cuda")
+    moved = buf[shift:].view_as(xs)
+    moved.copy_(xs)
+    assert torch.equal(smr.expert_up(codes, w, *al, width=3, block_size=64, x_scales=moved, w_scales=ws), ref)
+    xv, wv = smr.dequantize_mxfp4(codes, xs).double(), _mx_exact(w13)[2]
+    _close(ref, *_ref_up(xv, wv, ids, 3))
