@@ -470,6 +470,9 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
     lib = _lib.load()
     if w.dim() != 3 or w.shape[1] % 2 or x.dim() != 2:
         raise ValueError("x must be [num_tokens, H] and w [num_experts, 2 I, H]")
+    width, block_size = int(width), int(block_size)
+    if width < 1:
+        raise ValueError(f"width must be >= 1 (got {width})")
     T, H = x.shape
     E, I = w.shape[0], w.shape[1] // 2
     if x_scales is not None:
@@ -513,6 +516,7 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
         raise ValueError("topk_weights must be a contiguous float32 tensor of topk_ids' shape")
     if w.dim() != 3 or x.dim() != 2:
         raise ValueError("x must be [num_tokens * width, I] and w [num_experts, H, I]")
+    block_size, num_logical = int(block_size), int(num_logical)
     T, width = topk_ids.shape
     E, H, I = w.shape
     if x_scales is not None:

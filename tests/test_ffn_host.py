@@ -187,6 +187,8 @@ def test_python_checks(smr):
         smr.expert_up(x, w, al[0], al[1][:1], al[2], **kw)
     with pytest.raises(ValueError, match="both be given"):
         smr.expert_up(x, w, *al, x_scales=x, **kw)
+    with pytest.raises(ValueError, match="width must be"):
+        smr.expert_up(x, w, *al, width=0, block_size=A)
     ids, wts = torch.zeros(T, width, dtype=torch.int32), torch.zeros(T, width)
     act, w2 = torch.zeros(T * width, I, dtype=torch.bfloat16), torch.zeros(E, H, I, dtype=torch.bfloat16)
     for bad, frag in ((dict(ids=ids.long()), "topk_ids"), (dict(wts=wts.double()), "topk_weights"),
