@@ -399,23 +399,33 @@ def _elsewhere(dev: int, stream):
 _stream_ws = {}
 
 
-def _ffn_workspace(ws, nbytes: int, dev: int, s: int):
-    """(pointer, bytes) of a workspace of the feed-forward entry points: the
-    caller's, or one per device and stream (calls on two streams may overlap).
-    A call that is being captured gets one of its own, which its graph keeps
-    and zeroes itself."""
+def _run_product(fn, size_fn, args, ws, dev: int) -> None:
+    """Calls a product with the caller's workspace, or with one per device and
+    stream (calls on two streams may overlap). A Workspace that turns out too
+    small grows and the call is made again (it was refused before any launch).
+    A call that is being captured gets a workspace of its own, which its graph
+    keeps and zeroes itself."""
     torch = _torch()
+    ref = ctypes.byref(args)
+    s = torch._C._cuda_getCurrentRawStream(dev)
     if ws is None:
         if torch._C._cuda_isCurrentStreamCapturing():
-            buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
-            buf[:256].zero_()
-            return buf.data_ptr(), nbytes
-        ws = _stream_ws.get((dev, s))
-        if ws is None:
-            ws = _stream_ws[(dev, s)] = Workspace(0, torch.device("cuda", dev))
+            ws = torch.empty(size_fn(ref), dtype=torch.uint8, device=torch.device("cuda", dev))
+            ws[:256].zero_()
+        else:
+            ws = _stream_ws.get((dev, s))
+            if ws is None:
+                ws = _stream_ws[(dev, s)] = Workspace(0, torch.device("cuda", dev))
     if isinstance(ws, Workspace):
-        ws = ws.ensure(nbytes)
-    return ws.data_ptr(), ws.nbytes
+        buf = ws.buf
+        status = _lib.SMR_ERR_WORKSPACE if buf is None else fn(ref, buf.data_ptr(), buf.numel(), s)
+        if status == _lib.SMR_ERR_WORKSPACE:
+            buf = ws.ensure(size_fn(ref))
+            status = fn(ref, buf.data_ptr(), buf.numel(), s)
+    else:
+        status = fn(ref, ws.data_ptr(), ws.nbytes, s)
+    if status:
+        _check(status)
 
 
 def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated, sorted_token_ids, expert_ids, npp, block_size):
@@ -490,10 +500,7 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
     a = ExpertUpArgs(T, width, H, I, E, block_size, x.data_ptr(), x.stride(0) if T > 1 else H, _ptr(x_scales),
                      w.data_ptr(), _ptr(w_scales), sorted_token_ids.data_ptr(), sorted_token_ids.numel(),
                      expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), out.data_ptr())
-    ref = ctypes.byref(a)
-    s = _raw_stream(dev)
-    wp, wn = _ffn_workspace(workspace, lib.smr_expert_up_workspace_size(ref), dev, s)
-    _check(lib.smr_expert_up(ref, wp, wn, s))
+    _run_product(lib.smr_expert_up, lib.smr_expert_up_workspace_size, a, workspace, dev)
     return out
 
 
@@ -538,10 +545,7 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
                        topk_ids.data_ptr(), topk_weights.data_ptr(), num_logical if num_logical else E,
                        sorted_token_ids.data_ptr(), sorted_token_ids.numel(), expert_ids.data_ptr(),
                        num_tokens_post_padded.data_ptr(), out.data_ptr())
-    ref = ctypes.byref(a)
-    s = _raw_stream(dev)
-    wp, wn = _ffn_workspace(workspace, lib.smr_expert_down_workspace_size(ref), dev, s)
-    _check(lib.smr_expert_down(ref, wp, wn, s))
+    _run_product(lib.smr_expert_down, lib.smr_expert_down_workspace_size, a, workspace, dev)
     return out
 
 
