@@ -591,3 +591,36 @@ def test_scale_rows_of_any_alignment(smr, K, shift, T):
     assert torch.equal(smr.expert_up(codes, w, *al, width=3, block_size=64, x_scales=moved, w_scales=ws), ref)
     xv, wv = smr.dequantize_mxfp4(codes, xs).double(), _mx_exact(w13)[2]
     _close(ref, *_ref_up(xv, wv, ids, 3))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,E,width,H", [
+    (1, 1, 1, 16),        # one slot, one partial tile
+    (2, 3, 6, 272),       # a token's slots on the same expert several times
+    (16, 2, 40, 640),     # more than 32 slots a token
+    (16, 300, 11, 4096),
+    (7, 40, 4, 16384),    # 128 weight tiles
+])
+def test_down_of_few_tokens(smr, mx, T, E, width, H):
+    I = 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + H)
+    ids = torch.randint(0, E, (T, width), generator=g, device="cuda").int()
+    if E > 2 and T > 1:
+        ids[1, 0], ids[0] = -1, E  # a slot, and a whole token, that no expert has
+    wts = torch.rand(T, width, generator=g, device="cuda") - 0.3
+    al = smr.align(ids, E, 64, workspace=smr.Workspace(256))
+    x, w = _normal(g, T * width, I), _normal(g, E, H, I, std=I ** -0.5)
+    skipped = ((ids < 0) | (ids >= E)).reshape(-1)
+    xa, kw, xv = _values(smr, x, mx)
+    if mx:
+        wa, kw["w_scales"], wv = _weights_mx(smr, w, False)
+    else:
+        wa, wv = w, w.double()
+        xa = xa.clone()
+        xa[skipped] = float("nan")  # never read
+    ws = smr.Workspace(256)
+    out = smr.expert_down(xa, wa, ids, wts, *al, block_size=64, workspace=ws, **kw)
+    assert smr.get_device_error(ws) == 0
+    _close(out, *_ref_down(torch.where(skipped[:, None], 0.0, xv), wv, ids, wts))
+    assert torch.equal(out, smr.expert_down(xa, wa, ids, wts, *al, block_size=64, workspace=ws, **kw))
