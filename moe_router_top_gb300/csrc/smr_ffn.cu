@@ -935,12 +935,13 @@ expert_combine_kernel(const void *__restrict__ y, const int32_t *__restrict__ id
 // ---------------------------------------------------------------- host --
 
 // CTA pairs from this many rows an expert, on average: a pair halves the rows
-// that each CTA loads and that its MMAs read (16384 tokens, 1024 rows an
-// expert: bf16 588 us with pairs, 847 without; MXFP4 266 and 314; 2047 skewed
-// tokens, 128 rows: down 103 and 114), but below a block an expert it only
-// leaves half as many items to share out (512 skewed tokens, 32 rows: 143 and
-// 134).
-constexpr int kPairRows = 96;
+// that each CTA loads and that its MMAs read, but has only half as many items
+// to share out. With pairs and without (us, 128 experts, gated product): bf16
+// 16384 tokens of 8 slots 588 and 847, 1024 skewed tokens (64 rows an expert)
+// 135 and 157, evenly spread 136 and 135, 512 tokens (32 rows) 133 and 127;
+// MXFP4 16384 tokens 240 and 314, 1024 tokens 44 and 49 skewed, 42 and 41
+// evenly spread, 512 tokens 40 and 38.
+constexpr int kPairRows = 48;
 
 static int sm_count() {
     static std::atomic<int> cached[kMaxDevices];
