@@ -213,16 +213,37 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 }
 // Four lanes hold a feature each (a row of TMEM), c0..c3 its values in four
 // columns; each returns the four features, in bf16, of column (lane & 3): a
-// 4 x 4 transpose in three shuffles, so that results leave in 8-byte stores.
-// (One 2-byte store a value kept the epilogue at 12300 cycles an item of 128 x
-// 128, above the 12 k-blocks that it runs under.)
-__device__ __forceinline__ uint2 quad_pack(float c0, float c1, float c2, float c3, int lane) {
+// 4 x 4 transpose of 16-bit values in two shuffles, so that results leave in
+// 8-byte stores. (One 2-byte store a value kept the epilogue at 12300 cycles an
+// item of 128 x 128, above the 12 k-blocks that it runs under.) First the lanes
+// two apart exchange a pair of columns, then neighbours a column of both
+// features that they hold by then; the byte selectors depend on the lane only.
+struct QuadSel {
+    uint32_t keep, send, w0, w1;
+    bool top;
+    __device__ __forceinline__ explicit QuadSel(int lane) : top((lane & 2) != 0) {
+        const bool odd = lane & 1;
+        keep = odd ? 0x7632u : 0x5410u;  // the column that stays: high or low halves
+        send = odd ? 0x5410u : 0x7632u;
+        const uint32_t own = odd ? 0x1054u : 0x5410u, other = odd ? 0x3276u : 0x7632u;  // lower feature first
+        w0 = top ? other : own;
+        w1 = top ? own : other;
+    }
+};
+__device__ __forceinline__ uint2 quad_pack(float c0, float c1, float c2, float c3, const QuadSel &s) {
+    const uint32_t a = pack_bf16x2(c0, c1), b = pack_bf16x2(c2, c3);
+    const uint32_t p = s.top ? b : a, q = __shfl_xor_sync(0xffffffffu, s.top ? a : b, 2);
+    const uint32_t own = __byte_perm(p, q, s.keep), got = __shfl_xor_sync(0xffffffffu, __byte_perm(p, q, s.send), 1);
+    return make_uint2(__byte_perm(own, got, s.w0), __byte_perm(own, got, s.w1));
+}
+
+// The same in fp32.
+__device__ __forceinline__ float4 quad_turn(float c0, float c1, float c2, float c3, int lane) {
     const bool odd = lane & 1, top = lane & 2;
     const float x = __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1), y = __shfl_xor_sync(0xffffffffu, odd ? c2 : c3, 1);
-    const uint32_t p = odd ? pack_bf16x2(x, c1) : pack_bf16x2(c0, x);  // column (lane & 1)
-    const uint32_t q = odd ? pack_bf16x2(y, c3) : pack_bf16x2(c2, y);  // column 2 + (lane & 1)
-    const uint32_t z = __shfl_xor_sync(0xffffffffu, top ? p : q, 2);
-    return top ? make_uint2(z, q) : make_uint2(p, z);
+    const float2 p = odd ? make_float2(x, c1) : make_float2(c0, x), q = odd ? make_float2(y, c3) : make_float2(c2, y);
+    const float z0 = __shfl_xor_sync(0xffffffffu, top ? p.x : q.x, 2), z1 = __shfl_xor_sync(0xffffffffu, top ? p.y : q.y, 2);
+    return top ? make_float4(z0, z1, q.x, q.y) : make_float4(p.x, p.y, z0, z1);
 }
 
 // One lane of a converged warp.
@@ -235,15 +256,6 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), parity, abort));
 }
-// The same in fp32.
-__device__ __forceinline__ float4 quad_turn(float c0, float c1, float c2, float c3, int lane) {
-    const bool odd = lane & 1, top = lane & 2;
-    const float x = __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1), y = __shfl_xor_sync(0xffffffffu, odd ? c2 : c3, 1);
-    const float2 p = odd ? make_float2(x, c1) : make_float2(c0, x), q = odd ? make_float2(y, c3) : make_float2(c2, y);
-    const float z0 = __shfl_xor_sync(0xffffffffu, top ? p.x : q.x, 2), z1 = __shfl_xor_sync(0xffffffffu, top ? p.y : q.y, 2);
-    return top ? make_float4(z0, z1, q.x, q.y) : make_float4(p.x, p.y, z0, z1);
-}
-
 // Position in a ring of barriers: index and the parity of its current use.
 struct RingPos {
     int i = 0;
@@ -744,6 +756,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         // --------------------------------------------------- epilogue ----
         // two warps share a quarter's lanes, every other 16 columns each
         const int q = warp & 3, c_beg = warp < 3 + kLoaders + 4 ? 0 : 16;
+        const QuadSel quad(lane);
         RingPos iq, ac;
         bool ok = true;
         while (ok) {
@@ -781,8 +794,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         const float u = __uint_as_float(hi ? v[2 * j + 1] : got);
                         a[j] = swiglu(g, u);
                     }
-                    const uint2 s0 = quad_pack(a[0], a[1], a[2], a[3], lane);
-                    const uint2 s1 = quad_pack(a[4], a[5], a[6], a[7], lane);
+                    const uint2 s0 = quad_pack(a[0], a[1], a[2], a[3], quad);
+                    const uint2 s1 = quad_pack(a[4], a[5], a[6], a[7], quad);
                     if (i0 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i0 * p.feat) = s0;
                     if (i1 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i1 * p.feat) = s1;
                 } else {
@@ -804,7 +817,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             s[j] = quad_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), lane);
+                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), quad);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (i[j] >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i[j] * p.feat) = s[j];
