@@ -203,8 +203,8 @@ typedef struct smr_expert_up_args {
 /* The experts' second product and the weighted sum over a token's slots:
  * y[i] = x[i] . w[e(i)]^T (fp32 accumulation), out[t] = sum over s, in order,
  * of topk_weights[t, s] * y[t * width + s], in fp32, rounded to bf16 once (y
- * waits in the workspace, in fp32 up to 2^23 values, else rounded to bf16). A
- * slot whose topk_ids entry is outside [0,
+ * waits in the workspace, in fp32 up to 2^23 values and 48 rows an expert,
+ * else rounded to bf16). A slot whose topk_ids entry is outside [0,
  * num_logical) contributes nothing. */
 typedef struct smr_expert_down_args {
     int32_t num_tokens;            /* T >= 0 */

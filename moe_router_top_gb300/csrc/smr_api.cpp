@@ -716,11 +716,11 @@ SMR_API smr_status smr_expert_gemm(const smr_expert_gemm_args *a, void *workspac
 SMR_API size_t smr_expert_up_workspace_size(const smr_expert_up_args *args) { return args ? kHeaderBytes : 0; }
 
 // The rows between the product and the sum are fp32 as long as they are few
-// (32 MB stay in L2, and rounding them would only cost precision), else bf16:
+// (they stay in L2, and rounding them would only cost precision), else bf16:
 // at 16384 tokens of 2048 features and 8 slots fp32 rows would be 1.07 GB more
 // to move, 160 us on top of 410.
 static bool down_rows_fp32(const smr_expert_down_args *a) {
-    return (int64_t)a->num_tokens * a->width * a->H <= (int64_t)1 << 23;
+    return smr::expert_rows_fp32((int64_t)a->num_tokens * a->width, a->num_experts, a->H);
 }
 
 SMR_API size_t smr_expert_down_workspace_size(const smr_expert_down_args *args) {

@@ -85,8 +85,7 @@ struct FfParams {
     int64_t sorted_cap;
     int numel, max_blocks;
     const int32_t *sorted, *eids, *npp;
-    void *out;               // bf16 [numel, feat]; fp32 where out32
-    int out32;
+    void *out;               // [numel, feat], fp32 or bf16
     const uint8_t *x_scales, *w_scales;  // MXFP4
     int num_chunks;          // MXFP4: K / 128
     int scale_bytes;         // MXFP4: rows of x_scales can be read 16, 8 or 4 bytes at a time
@@ -278,7 +277,9 @@ struct RingPos {
 // each other together); each holds its own 128 weight rows (and their scales),
 // half of the routed rows and all of these rows' scales, and drains its own
 // lanes.
-template <bool MX, bool UP, bool PAIR, int SUB>
+// F32: the outputs are fp32, else bf16 (a variant of its own: with both in one
+// kernel the code of 17 short items a CTA took 25.1 us instead of 21.0).
+template <bool MX, bool UP, bool PAIR, int SUB, bool F32>
 __global__ void __launch_bounds__(kFfThreads<SUB>, 1)
 expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     constexpr int kCols = kFfCols<MX, PAIR>;
@@ -802,7 +803,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     int i[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) i[j] = inf->slot[c0 + 4 * j + (lane & 3)];
-                    if (p.out32) {
+                    if constexpr (F32) {
                         float4 s[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -955,6 +956,12 @@ expert_combine_kernel(const void *__restrict__ y, const int32_t *__restrict__ id
 // MXFP4 16384 tokens 240 and 314, 1024 tokens 44 and 49 skewed, 42 and 41
 // evenly spread, 512 tokens 40 and 38.
 constexpr int kPairRows = 48;
+static bool use_pairs(int64_t numel, int num_experts) { return numel >= (int64_t)kPairRows * num_experts; }
+
+// Few enough to stay in L2 (32 MB); pairs of CTAs write bf16 rows only.
+bool expert_rows_fp32(int64_t numel, int num_experts, int H) {
+    return numel * H <= (int64_t)1 << 23 && !use_pairs(numel, num_experts);
+}
 
 static int sm_count() {
     static std::atomic<int> cached[kMaxDevices];
@@ -990,7 +997,7 @@ static bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const v
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool MX, bool UP, bool PAIR, int SUB>
+template <bool MX, bool UP, bool PAIR, int SUB, bool F32 = false>
 static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stream) {
     FfParams p{};
     const int per_block = MX ? 256 : 64, step = MX ? 64 : 16;  // values of K in a k-block, in an MMA
@@ -1010,7 +1017,6 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.eids = a.eids;
     p.npp = a.npp;
     p.out = a.out;
-    p.out32 = a.out32 ? 1 : 0;
     p.x_scales = a.x_scales;
     p.w_scales = a.w_scales;
     p.num_chunks = a.K / 128;
@@ -1053,10 +1059,10 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
 
     static std::atomic<bool> configured[kMaxDevices];
     const cudaError_t e = once_per_device(configured, [](int) {
-        cudaError_t r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR, SUB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR, SUB, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kSmemMax);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR, SUB>, cudaFuncAttributePreferredSharedMemoryCarveout,
+            r = cudaFuncSetAttribute(expert_ffn_kernel<MX, UP, PAIR, SUB, F32>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         return r;
     });
@@ -1078,12 +1084,16 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP, PAIR, SUB>, mw, p);
+    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP, PAIR, SUB, F32>, mw, p);
 }
 
 template <bool MX, bool UP>
 static cudaError_t launch_format(const FfnLaunch &a, int sms, cudaStream_t stream) {
-    if (a.numel >= (int64_t)kPairRows * a.num_experts) return launch_product<MX, UP, true, MX ? 2 : 1>(a, sms, stream);
+    if (use_pairs(a.numel, a.num_experts)) return launch_product<MX, UP, true, MX ? 2 : 1>(a, sms, stream);
+    if constexpr (!UP)
+        if (a.out32)
+            return a.A == 64 ? launch_product<MX, UP, false, 2, true>(a, sms, stream)
+                             : launch_product<MX, UP, false, 1, true>(a, sms, stream);
     return a.A == 64 ? launch_product<MX, UP, false, 2>(a, sms, stream) : launch_product<MX, UP, false, 1>(a, sms, stream);
 }
 
