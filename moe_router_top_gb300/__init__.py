@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional, Tuple
 
 from . import _lib
@@ -397,32 +398,55 @@ def _elsewhere(dev: int, stream):
 
 
 _stream_ws = {}
+_stream_lock = threading.RLock()
+
+
+def _check_buffer(ws, dev: int) -> None:
+    """Refuses a workspace that kernels on device `dev` could not write to."""
+    if ws.get_device() != dev:
+        raise ValueError(f"workspace must be on the operands' device, cuda:{dev} (got {ws.device})")
+    if not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
+def _call_product(fn, size_fn, ref, ws, dev: int, s: int) -> int:
+    """One call on a Workspace. One that is too small is refused before any
+    launch; it grows and the call is made again."""
+    buf = ws.buf
+    status = _lib.SMR_ERR_WORKSPACE
+    if buf is not None:
+        _check_buffer(buf, dev)
+        status = fn(ref, buf.data_ptr(), buf.numel(), s)
+    if status == _lib.SMR_ERR_WORKSPACE:
+        buf = ws.ensure(size_fn(ref))
+        _check_buffer(buf, dev)
+        status = fn(ref, buf.data_ptr(), buf.numel(), s)
+    return status
 
 
 def _run_product(fn, size_fn, args, ws, dev: int) -> None:
     """Calls a product with the caller's workspace, or with one per device and
-    stream (calls on two streams may overlap). A Workspace that turns out too
-    small grows and the call is made again (it was refused before any launch).
-    A call that is being captured gets a workspace of its own, which its graph
-    keeps and zeroes itself."""
+    stream (calls on two streams may overlap). Threads may call on one stream:
+    the launches of a call that shares such a workspace stay together. A call
+    that is being captured gets a workspace of its own, which its graph keeps
+    and zeroes itself."""
     torch = _torch()
     ref = ctypes.byref(args)
     s = torch._C._cuda_getCurrentRawStream(dev)
-    if ws is None:
-        if torch._C._cuda_isCurrentStreamCapturing():
-            ws = torch.empty(size_fn(ref), dtype=torch.uint8, device=torch.device("cuda", dev))
-            ws[:256].zero_()
-        else:
+    if isinstance(ws, Workspace):
+        status = _call_product(fn, size_fn, ref, ws, dev, s)
+    elif ws is None and not torch._C._cuda_isCurrentStreamCapturing():
+        with _stream_lock:
             ws = _stream_ws.get((dev, s))
             if ws is None:
                 ws = _stream_ws[(dev, s)] = Workspace(0, torch.device("cuda", dev))
-    if isinstance(ws, Workspace):
-        buf = ws.buf
-        status = _lib.SMR_ERR_WORKSPACE if buf is None else fn(ref, buf.data_ptr(), buf.numel(), s)
-        if status == _lib.SMR_ERR_WORKSPACE:
-            buf = ws.ensure(size_fn(ref))
-            status = fn(ref, buf.data_ptr(), buf.numel(), s)
+            status = _call_product(fn, size_fn, ref, ws, dev, s)
     else:
+        if ws is None:
+            ws = torch.empty(size_fn(ref), dtype=torch.uint8, device=torch.device("cuda", dev))
+            ws[:256].zero_()
+        else:
+            _check_buffer(ws, dev)
         status = fn(ref, ws.data_ptr(), ws.nbytes, s)
     if status:
         _check(status)

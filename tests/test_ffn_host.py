@@ -4,6 +4,9 @@ the calls that launch nothing, and the Python layer's argument checks."""
 from __future__ import annotations
 
 import ctypes
+import threading
+import time
+import types
 
 import pytest
 
@@ -237,3 +240,76 @@ def test_disabled(smr, monkeypatch):
                  lambda: smr.expert_down(x, x, x, x, x, x, x, block_size=64)):
         with pytest.raises(smr.SmrUnsupported):
             call()
+
+
+class _Buffer:
+    """Stands in for device memory."""
+    device = "cuda:0"
+
+    def __init__(self, n, dev=0, dense=True):
+        self.n, self.nbytes, self.dev, self.dense = n, n, dev, dense
+
+    def get_device(self):
+        return self.dev
+
+    def is_contiguous(self):
+        return self.dense
+
+    def numel(self):
+        return self.n
+
+    def data_ptr(self):
+        return P
+
+
+@pytest.fixture
+def fake_device(smr, monkeypatch):
+    """A device that the Python layer can 'launch' on: memory and streams are stand-ins."""
+    c = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda dev: 7, _cuda_isCurrentStreamCapturing=lambda: False)
+    monkeypatch.setattr(smr, "_torch_module", types.SimpleNamespace(
+        _C=c, device=torch.device, uint8=torch.uint8, zeros=lambda n, dtype, device: _Buffer(n)))
+    monkeypatch.setattr(smr, "_stream_ws", {})
+    return smr
+
+
+def test_workspace_must_be_writable_there(fake_device):
+    smr, args, calls = fake_device, ExpertUpArgs(), []
+
+    def fn(*a):
+        calls.append(a)
+        return _lib.SMR_OK
+
+    for bad, frag in ((torch.zeros(256, dtype=torch.uint8), "device"), (_Buffer(256, dev=1), "device"),
+                      (_Buffer(256, dense=False), "contiguous")):
+        holder = smr.Workspace(0, torch.device("cuda", 0))
+        holder.buf = bad
+        for ws in (bad, holder):
+            with pytest.raises(ValueError, match=frag):
+                smr._run_product(fn, lambda ref: 256, args, ws, 0)
+    assert not calls
+    smr._run_product(fn, lambda ref: 256, args, _Buffer(512), 0)
+    smr._run_product(fn, lambda ref: 256, args, smr.Workspace(0, torch.device("cuda", 0)), 0)
+    assert [a[1:] for a in calls] == [(P, 512, 7), (P, 256, 7)]
+
+
+def test_threads_on_one_stream_take_turns(fake_device):
+    """Calls of several threads on one stream share a workspace: the product
+    and the sum of one call are launched with no other call's between them."""
+    smr, busy, mixed = fake_device, [], []
+
+    def fn(ref, ptr, n, s):
+        if n < 1024:
+            return WORKSPACE
+        busy.append(1)
+        mixed.append(len(busy) > 1)
+        time.sleep(0.002)
+        busy.pop()
+        return _lib.SMR_OK
+
+    threads = [threading.Thread(target=lambda: [smr._run_product(fn, lambda ref: 1024, ExpertDownArgs(), None, 0)
+                                                for _ in range(10)]) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(mixed) == 40 and not any(mixed) and len(smr._stream_ws) == 1
