@@ -205,7 +205,10 @@ typedef struct smr_expert_up_args {
  * of topk_weights[t, s] * y[t * width + s], in fp32, rounded to bf16 once (y
  * waits in the workspace, in fp32 up to 2^23 values and 48 rows an expert,
  * else rounded to bf16). A slot whose topk_ids entry is outside [0,
- * num_logical) contributes nothing. */
+ * num_logical) contributes nothing; every other slot must have been aligned
+ * (behind an EPLB remap that sends a logical expert to no physical one, which
+ * the align flags, set its topk_ids entries to -1: without a row of y they
+ * would add whatever the workspace holds). */
 typedef struct smr_expert_down_args {
     int32_t num_tokens;            /* T >= 0 */
     int32_t width;                 /* >= 1 */
@@ -321,7 +324,9 @@ SMR_API smr_status smr_expert_gemm(const smr_expert_gemm_args *args, void *works
  * past num_tokens_post_padded cost nothing, and a block costs its own rows,
  * not its padding. A slot that the align skipped (an id out of range) gets no
  * row: its row of act is left as it was, and smr_expert_down leaves it out.
- * Results do not depend on the launch or on other rows of the batch.
+ * The same call gives the same bits, and a row that holds a NaN or an infinity
+ * reaches its own token only. A row's bits may differ between batches of
+ * other sizes (tiles, and the type that y waits in, follow the sizes).
  * smr_expert_up is one launch, workspace >= 256 bytes; smr_expert_down is two
  * (the product into the workspace, then the sum), workspace as its _size says.
  * The first 256 bytes are zeroed once by the caller, as for every workspace;

@@ -401,6 +401,12 @@ _stream_ws = {}
 _stream_lock = threading.RLock()
 
 
+def _check_sizes(*sizes: int) -> None:
+    """Refuses sizes that the library's 32-bit arguments would cut off."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"sizes must be below 2^31 (got {max(sizes)})")
+
+
 def _check_buffer(ws, dev: int) -> None:
     """Refuses a workspace that kernels on device `dev` could not write to."""
     if ws.get_device() != dev:
@@ -455,6 +461,7 @@ def _run_product(fn, size_fn, args, ws, dev: int) -> None:
 def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated, sorted_token_ids, expert_ids, npp, block_size):
     """Checks of a product's operands in either format and of the align's outputs."""
     torch = _torch()
+    _check_sizes(rows, K, w_rows, w.shape[0], block_size)
     mx = x_scales is not None
     if mx != (w_scales is not None):
         raise ValueError("x_scales and w_scales must both be given (MXFP4) or both be None (bfloat16)")
@@ -507,6 +514,7 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
     width, block_size = int(width), int(block_size)
     if width < 1:
         raise ValueError(f"width must be >= 1 (got {width})")
+    _check_sizes(width)
     T, H = x.shape
     E, I = w.shape[0], w.shape[1] // 2
     if x_scales is not None:
@@ -537,7 +545,8 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     rows of expert_up), w bf16 [num_experts, H, I], topk_ids and topk_weights
     [num_tokens, width] as routed. With x_scales and w_scales, x and w are
     MXFP4 codes. A slot whose id is outside [0, num_logical) contributes
-    nothing (num_logical: the experts that were aligned; num_experts if 0)."""
+    nothing (num_logical: the experts that were aligned; num_experts if 0);
+    every other slot must have been aligned."""
     _disabled()
     torch = _torch()
     lib = _lib.load()
@@ -548,6 +557,7 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     if w.dim() != 3 or x.dim() != 2:
         raise ValueError("x must be [num_tokens * width, I] and w [num_experts, H, I]")
     block_size, num_logical = int(block_size), int(num_logical)
+    _check_sizes(num_logical)
     T, width = topk_ids.shape
     E, H, I = w.shape
     if x_scales is not None:
@@ -587,6 +597,7 @@ def quantize_mxfp4(x, *, codes=None, scales=None, stream=None) -> Tuple:
     K = shape[-1]
     if K < 32 or K % 32:
         raise ValueError(f"x's last dimension must be a positive multiple of 32 (got {K})")
+    _check_sizes(K)
     dev = _check_cuda(x, codes, scales)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -613,6 +624,7 @@ def dequantize_mxfp4(codes, scales, *, out=None, stream=None):
     lead, K = shape[:-1], 2 * shape[-1]
     if K < 32 or K % 32:
         raise ValueError(f"codes' last dimension must be a positive multiple of 16 (got {K // 2})")
+    _check_sizes(K)
     if scales.dtype != torch.uint8 or scales.shape != lead + (K // 32,) or not scales.is_contiguous():
         raise ValueError(f"scales must be a contiguous uint8 tensor of shape {tuple(lead) + (K // 32,)}")
     dev = _check_cuda(codes, scales, out)
@@ -635,12 +647,13 @@ def tile_mxfp4_scales(scales, *, gated: bool = False, out=None, stream=None):
     lib = _lib.load()
     if scales.dtype != torch.uint8 or scales.dim() != 3 or not scales.is_contiguous():
         raise ValueError("scales must be a contiguous uint8 [num_experts, N, K / 32] tensor")
+    E, N, K = scales.shape[0], scales.shape[1], 32 * scales.shape[2]
+    _check_sizes(E, N, K)
     dev = _check_cuda(scales, out)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return tile_mxfp4_scales(scales, gated=gated, out=out)
-    E, N, K = scales.shape[0], scales.shape[1], 32 * scales.shape[2]
     tiles = -(-(N // 2) // 64) if gated else -(-N // 128)
     out = _output(out, (E, tiles, K // 128), 512, torch.uint8, scales)
     _check(lib.smr_tile_mxfp4_scales(scales.data_ptr(), E, N, K, 1 if gated else 0, out.data_ptr(),

@@ -313,3 +313,24 @@ def test_threads_on_one_stream_take_turns(fake_device):
     for t in threads:
         t.join()
     assert len(mixed) == 40 and not any(mixed) and len(smr._stream_ws) == 1
+
+
+def test_sizes_past_32_bits_are_refused(smr):
+    """They would be cut off on the way into the library."""
+    big = 1 << 32
+    al = _align_outputs(3, 2, 4, 64)
+    x, w = torch.zeros(3, 64, dtype=torch.bfloat16), torch.zeros(4, 64, 64, dtype=torch.bfloat16)
+    for width, block_size in ((big + 2, 64), (2, big + 64)):
+        with pytest.raises(ValueError, match="below 2"):
+            smr.expert_up(x, w, *al, width=width, block_size=block_size)
+    ids, wts, w2 = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2), torch.zeros(4, 64, 32, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="below 2"):
+        smr.expert_down(torch.zeros(6, 32, dtype=torch.bfloat16), w2, ids, wts, *al, block_size=64, num_logical=big + 4)
+    # (meta tensors: shapes without memory)
+    with pytest.raises(ValueError, match="below 2"):
+        smr.quantize_mxfp4(torch.empty(1, big + 32, dtype=torch.bfloat16, device="meta"))
+    with pytest.raises(ValueError, match="below 2"):
+        smr.dequantize_mxfp4(torch.empty(1, big // 2 + 16, dtype=torch.uint8, device="meta"),
+                             torch.empty(1, big // 32 + 1, dtype=torch.uint8, device="meta"))
+    with pytest.raises(ValueError, match="below 2"):
+        smr.tile_mxfp4_scales(torch.empty(1, 1, big // 32 + 4, dtype=torch.uint8, device="meta"))
