@@ -156,14 +156,15 @@ __device__ __forceinline__ void ld_cg_8(uint32_t *v, const void *src, int row) {
                  : "+r"(v[0]), "+r"(v[1]) : "l"(src), "r"(row));
 }
 // Copies that happen where row >= 0 (predicated: a branch a row cost the
-// large batches 15%).
+// large batches 15%). No memory clobber: what they write is read only behind
+// the wait for them, and loads of row numbers may move ahead of them.
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src, int row) {
     asm volatile("{\n .reg .pred q;\n setp.ge.s32 q, %2, 0;\n @q cp.async.ca.shared.global [%0], [%1], 4;\n}"
-                 ::"r"(dst), "l"(src), "r"(row) : "memory");
+                 ::"r"(dst), "l"(src), "r"(row));
 }
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, int row) {
     asm volatile("{\n .reg .pred q;\n setp.ge.s32 q, %2, 0;\n @q cp.async.cg.shared.global [%0], [%1], 16;\n}"
-                 ::"r"(dst), "l"(src), "r"(row) : "memory");
+                 ::"r"(dst), "l"(src), "r"(row));
 }
 
 // MXFP4 instruction descriptor (kind::mxf4): A and B E2M1 (bits 7-9, 10-11 =
@@ -412,8 +413,9 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         const bool in = bo < G;
         const bool wide = (reinterpret_cast<uintptr_t>(p.sorted) & 15) == 0;
         // the entries and the block's expert (of blocks below `limit`),
-        // requested two items ahead (a round trip to L2 is longer than a short
-        // item)
+        // requested kAhead items ahead (a round trip to L2 is longer than two
+        // short items; with two, this warp took 1300 cycles an item and set
+        // the pace of 8 tokens' second product in MXFP4)
         auto fetch = [&](int b0, int limit, int (&ent)[8], int &e) {
             const int b = b0 + bo;
             if (!in || b0 < 0 || b >= limit) return;
@@ -437,13 +439,15 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 ++g;
             }
         };
-        int ent0[8], ent1[8], e0 = -1, e1 = -1, slot[8];
-        int grp2 = grp, tile2 = tile;  // the item after the next
+        constexpr int kAhead = 4;
+        int ent[kAhead][8], e[kAhead], at[kAhead], slot[8];  // (at: first block of the item's group)
+        int grp2 = grp, tile2 = tile;  // the item that is requested next
         const int npp = __ldcg(p.npp);
         if constexpr (!PAIR) {  // the first two at once with npp: what lies past it is left out below
-            fetch(grp, p.max_blocks, ent0, e0);
-            step(grp2, tile2);
-            fetch(grp2, p.max_blocks, ent1, e1);
+            int g = grp, t = tile;
+            fetch(g, p.max_blocks, ent[0], e[0]);
+            step(g, t);
+            fetch(g, p.max_blocks, ent[1], e[1]);
         }
         const int nblk = max(0, min(npp / A, p.max_blocks));
         // First block of group g (asked for in ascending order), -1 past the
@@ -467,7 +471,9 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     last_e = __shfl_sync(0xffffffffu, eb, 31);
                     run = __shfl_sync(0xffffffffu, place, 31) + 1;
                 }
-                return scan_at + (int)__fns(starts, 0, g - scan_base + 1);
+                // the bit with g - scan_base others below it
+                const bool hit = (starts >> lane & 1u) && __popc(starts & ((1u << lane) - 1u)) == g - scan_base;
+                return scan_at + __ffs(__ballot_sync(0xffffffffu, hit)) - 1;
             } else {
                 return g < nblk ? g : -1;
             }
@@ -500,17 +506,16 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         for (int64_t i = ((int64_t)blockIdx.x * 32 + lane) * 32; i < min((int64_t)nblk * A, p.sorted_cap);
              i += (int64_t)gridDim.x * 32 * 32)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sorted + i));
-        int at0 = locate(grp);  // first blocks of this item's and the next one's groups
-        if constexpr (PAIR) {
-            fetch(at0, nblk, ent0, e0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            at[u] = locate(grp2);
+            if (PAIR || u >= 2) fetch(at[u], nblk, ent[u], e[u]);
             step(grp2, tile2);
         }
-        int at1 = locate(grp2);
-        if constexpr (PAIR) fetch(at1, nblk, ent1, e1);
-        step(grp2, tile2);
         auto take = [&](int &at, int (&ent)[8], int &e) {
-            // the item whose first block is `at`; then the one after the next is requested
+            // the item whose first block is `at`; then the one kAhead later is requested
             int top = 0;
+            bool bad = false;
             const bool here = in && at + bo < nblk;
             const int ex = here ? e : -1;
             const int eg = __shfl_sync(0xffffffffu, ex, 0);
@@ -521,11 +526,12 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             for (int j = 0; j < 8; ++j) {
                 const int i = mine ? ent[j] : p.numel;
                 const bool real = (uint32_t)i < (uint32_t)p.numel;
-                // neither a slot nor the sentinel: a corrupted align output
-                if (!real && i != p.numel) set_error(p.err, kErrBadSlot);
+                bad |= !real && i != p.numel;
                 slot[j] = real ? i : -1;
                 if (real) top = 8 * lane + j + 1;
             }
+            // neither a slot nor the sentinel: a corrupted align output
+            if (bad) set_error(p.err, kErrBadSlot);
             __syncwarp();
             const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
             const int nt = PAIR ? 2 * tile + (int)rank : tile;
@@ -541,10 +547,10 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             }
             post((rows + 15) & ~15, nt, eg, slot);
         };
-        while (ok && at0 >= 0) {
-            take(at0, ent0, e0);
-            if (ok && at1 >= 0) take(at1, ent1, e1);
-            else if (at1 < 0) break;
+        while (ok && at[0] >= 0) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (ok && at[u] >= 0) take(at[u], ent[u], e[u]);
         }
         if (ok) post(-1, 0, 0, slot);
         __syncwarp();
@@ -689,9 +695,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     // (chunks past the row's end are not read by the last MMA steps)
                     const int off = kb * kFfRowBytes + c * 16, ends = p.x_bytes;
                     const uint8_t *x = p.x + off;
-                    // 4 rows a step and group of eight lanes, their places
-                    // read before the copies (which order memory accesses)
-#pragma unroll 2
+                    // 4 rows a step and group of eight lanes
+#pragma unroll 4
                     for (int r = 4 * (lane >> 3); r < n; r += 16) {
                         const int4 at = *reinterpret_cast<const int4 *>(inf->row + col0 + r);
                         const int row[4] = {at.x, at.y, at.z, at.w};
@@ -711,11 +716,10 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         const int pieces = min(kWords, p.num_chunks - 2 * kb);
                         if (p.scale_bytes > 4) {
 #pragma unroll
-                            for (int j = 0; j < kSets; ++j)
-#pragma unroll
-                                for (int q = 0; q < kWords; ++q)
-                                    asm volatile("st.shared.b32 [%0], %1;"
-                                                 ::"r"(sd + q * kSfAtom + j * 4), "r"(scale[j][q]) : "memory");
+                            for (int q = 0; q < kWords; ++q)  // (kSets = 4)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                             ::"r"(sd + q * kSfAtom), "r"(scale[0][q]), "r"(scale[1][q]),
+                                               "r"(scale[2][q]), "r"(scale[3][q]) : "memory");
                         } else {
 #pragma unroll
                             for (int j = 0; j < kSets; ++j) {
