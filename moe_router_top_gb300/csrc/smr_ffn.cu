@@ -4,8 +4,9 @@
 //
 // The products are computed transposed: the tensor core's M rows are 128 rows
 // of an expert's weights and its N columns are the routed rows of one aligned
-// block (16 to 128, only as many as the block holds, in steps of 16). From one
-// token to a couple of thousand the time is the touched experts' weights out
+// block (16 to 128, only as many as the block holds, in steps of 16; a pair of
+// CTAs takes 256 weight rows and up to 256 columns from several blocks of an
+// expert). From one token to a couple of thousand the time is the touched experts' weights out
 // of HBM, whatever the tile; this orientation streams each weight tile once
 // per block at full MMA width, and a block with three rows costs N = 16
 // columns instead of A padded rows. The ragged dimension has the fine step.
@@ -14,8 +15,8 @@
 // tiles of one block next to each other (its rows stay in L2; blocks of one
 // expert follow each other, so its weights do too). Warp roles: 0 loads the
 // weights by TMA, 1 issues the MMAs, 2 reads the align's outputs ahead and
-// hands out the work, from 3 on load the routed rows (and their block scales) with
-// asynchronous 16-byte copies, the last eight drain TMEM. (A TMA gather
+// hands out the work, from 3 on load the routed rows (and their block scales)
+// with asynchronous 16-byte copies, the last eight drain TMEM. (A TMA gather
 // takes 4 rows an instruction and about 70 cycles each: 128 rows took 2300
 // cycles a k-block, 3300 us for 16384 tokens.) The stage ring runs across
 // items; accumulators are double-buffered in TMEM, so the epilogue of one item
@@ -885,6 +886,11 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
 // still runs.
 // Y32: y is fp32, else bf16 (half the bytes, one more rounding of each term:
 // the error against 64 bits grows from 0.0017 to 0.0024 of the result).
+// Threads of a block: 128 where a block of 256 would not fit beside a CTA of
+// the product (pairs leave 12000 registers free) and for fp32 rows (few tokens:
+// more blocks), else 256: the whole second product in us with 128 and 256, one
+// token 9.95 and 10.4, 8 tokens in MXFP4 20.1 and 20.6, 2048 tokens 91.2 and
+// 92.0 (128 experts), 512 tokens 80.9 and 79.8.
 constexpr int kCombineThreads = 256;
 template <bool Y32>
 __global__ void __launch_bounds__(kCombineThreads)
@@ -1110,7 +1116,9 @@ cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream) {
-    const int vecs = a.H / 8, threads = vecs < kCombineThreads ? (vecs + 31) / 32 * 32 : kCombineThreads;
+    const bool narrow = a.y32 || use_pairs((int64_t)a.T * a.width, a.num_experts);
+    const int most = narrow ? kCombineThreads / 2 : kCombineThreads;
+    const int vecs = a.H / 8, threads = vecs < most ? (vecs + 31) / 32 * 32 : most;
     const int parts = (vecs + threads - 1) / threads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.T * (unsigned)parts, 1, 1);

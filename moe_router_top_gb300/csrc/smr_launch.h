@@ -205,7 +205,7 @@ struct CombineLaunch {
     const int32_t *ids;      // [T][width]
     const float *wts;
     uint16_t *out;           // bf16 [T][H]
-    int T, width, H, num_logical;
+    int T, width, H, num_logical, num_experts;
 };
 cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream);
 
