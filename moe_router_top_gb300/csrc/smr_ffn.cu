@@ -212,33 +212,54 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&b);
 }
-// Four lanes hold a feature each (a row of TMEM), c0..c3 its values in four
-// columns; each returns the four features, in bf16, of column (lane & 3): a
-// 4 x 4 transpose of 16-bit values in two shuffles, so that results leave in
-// 8-byte stores. (One 2-byte store a value kept the epilogue at 12300 cycles an
-// item of 128 x 128, above the 12 k-blocks that it runs under.) First the lanes
-// two apart exchange a pair of columns, then neighbours a column of both
-// features that they hold by then; the byte selectors depend on the lane only.
-struct QuadSel {
-    uint32_t keep, send, w0, w1;
-    bool top;
-    __device__ __forceinline__ explicit QuadSel(int lane) : top((lane & 2) != 0) {
-        const bool odd = lane & 1;
-        keep = odd ? 0x7632u : 0x5410u;  // the column that stays: high or low halves
-        send = odd ? 0x5410u : 0x7632u;
-        const uint32_t own = odd ? 0x1054u : 0x5410u, other = odd ? 0x3276u : 0x7632u;  // lower feature first
-        w0 = top ? other : own;
-        w1 = top ? own : other;
-    }
-};
-__device__ __forceinline__ uint2 quad_pack(float c0, float c1, float c2, float c3, const QuadSel &s) {
-    const uint32_t a = pack_bf16x2(c0, c1), b = pack_bf16x2(c2, c3);
-    const uint32_t p = s.top ? b : a, q = __shfl_xor_sync(0xffffffffu, s.top ? a : b, 2);
-    const uint32_t own = __byte_perm(p, q, s.keep), got = __shfl_xor_sync(0xffffffffu, __byte_perm(p, q, s.send), 1);
-    return make_uint2(__byte_perm(own, got, s.w0), __byte_perm(own, got, s.w1));
-}
+// Outputs in bf16 leave through shared memory, 16 columns at a time, in whole
+// lines. (Stored from registers, a warp reaches 64 bytes of a line at most:
+// 131072 scattered rows of 4096 bytes took 164 us that way, 313 us in pieces of
+// 32 bytes, 83 us in lines.) TMEM is read in the matrix-fragment shape, whose
+// transposing store puts neighbouring features next to each other without a
+// shuffle, and which gives a thread the gate and the up value of the same
+// places.
+template <bool UP>
+constexpr int kOutBytes = UP ? 128 : 256;        // of a column: 64 or 128 features
+template <bool UP>
+constexpr int kOutPitch = kOutBytes<UP> + 16;    // 8 rows of a store in different banks
+// Blocks of 16 columns for each half of the epilogue's warps: two, so that one
+// is filled while the other is read, but one where shared memory has no room
+// left (MXFP4, plain product).
+template <bool MX, bool UP>
+constexpr int kOutBufs = MX && !UP ? 1 : 2;
+template <bool MX, bool UP, bool F32>
+constexpr int kFfOutBytes = F32 ? 0 : 2 * kOutBufs<MX, UP> * 16 * kOutPitch<UP>;
 
-// The same in fp32.
+// 32 lanes x 16 columns as two fragments of 16 x 16: v[8 h + 4 u + 2 r + b] is
+// lane 16 h + 8 r + (thread / 4), column 8 u + 2 (thread % 4) + b.
+__device__ __forceinline__ void tmem_ld_frags_async(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                 : "r"(taddr + (16u << 16)));
+}
+// A 16 x 16 fragment in bf16, transposed: row c of shared memory (of 16, one
+// address a thread) gets column c's 16 features.
+__device__ __forceinline__ void put_frag(uint32_t dst, const float (&a)[8]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(dst), "r"(pack_bf16x2(a[0], a[1])), "r"(pack_bf16x2(a[2], a[3])),
+                   "r"(pack_bf16x2(a[4], a[5])), "r"(pack_bf16x2(a[6], a[7])) : "memory");
+}
+// Four warps meet; every one gets whether all of them came with ok.
+__device__ __forceinline__ bool meet_if(int id, bool ok) {
+    uint32_t all;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n barrier.cta.red.and.pred p, %2, 128, q;\n"
+                 " selp.u32 %0, 1, 0, p;\n}" : "=r"(all) : "r"((uint32_t)ok), "r"(id) : "memory");
+    return all != 0;
+}
+__device__ __forceinline__ void meet(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// Four lanes hold a feature each (a row of TMEM), c0..c3 its values in four
+// columns; each returns the four features of column (lane & 3), so that fp32
+// outputs leave in whole lines of 8 lanes.
 __device__ __forceinline__ float4 quad_turn(float c0, float c1, float c2, float c3, int lane) {
     const bool odd = lane & 1, top = lane & 2;
     const float x = __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 1), y = __shfl_xor_sync(0xffffffffu, odd ? c2 : c3, 1);
@@ -303,6 +324,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(last + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Info *info = reinterpret_cast<Info *>(misc + kFfBarBytes);
+    uint8_t *out_rows = misc + kFfMiscBytes<MX, PAIR>;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -760,74 +782,79 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         __syncwarp();
     } else {
         // --------------------------------------------------- epilogue ----
-        // two warps share a quarter's lanes, every other 16 columns each
-        const int q = warp & 3, c_beg = warp < 3 + kLoaders + 4 ? 0 : 16;
-        const QuadSel quad(lane);
+        // four warps, one a quarter of TMEM's lanes, take every other 16
+        // columns, the other four the rest
+        const int q = warp & 3, half = warp < 3 + kLoaders + 4 ? 0 : 1;
         RingPos iq, ac;
-        bool ok = true;
-        while (ok) {
-            if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+        // blocks of 16 columns: this half's, and this thread's row of a 16 x 16
+        // fragment's four 8 x 8 matrices
+        const uint32_t blocks = smem_u32(out_rows) + (uint32_t)(half * kOutBufs<MX, UP> * 16 * kOutPitch<UP>);
+        const uint32_t put = (uint32_t)((8 * (lane >> 4) + (lane & 7)) * kOutPitch<UP> + q * (UP ? 32 : 64) + ((lane >> 3) & 1) * 16);
+        uint32_t buf = 0;
+        while (true) {
+            bool ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
             const Info *inf = info + iq.i;
-            const int n = inf->n;
-            if (n < 0) break;
-            if (!(ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag))) break;
+            const int n = ok ? inf->n : -1;
+            if (n >= 0) ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag);
+            // the four warps go on together, or none does
+            if constexpr (!F32) ok = meet_if(1 + half, ok);
+            if (!ok || n < 0) break;
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.acc_cols);
-            // this lane's store: 4 features from f of column (lane & 3) of
-            // every four
-            const int f = UP ? inf->nt * 64 + q * 16 + (lane & 12) : inf->nt * kFfRows + q * 32 + (lane & 28);
-            const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
-            uint16_t *out = static_cast<uint16_t *>(p.out) + f;
             uint32_t v[16], next[16];
-            if (c_beg < n) {
-                tmem_ld16_async(acc + (uint32_t)c_beg, v);
+            const auto load = [&](int c, uint32_t (&to)[16]) {
+                if constexpr (F32) tmem_ld16_async(acc + (uint32_t)c, to);
+                else tmem_ld_frags_async(acc + (uint32_t)c, to);
+            };
+            if (16 * half < n) {
+                load(16 * half, v);
                 tmem_wait_ld16(v);
             }
-            for (int c0 = c_beg; c0 < n; c0 += 32) {
-                if (c0 + 32 < n) tmem_ld16_async(acc + (uint32_t)(c0 + 32), next);
-                if constexpr (UP) {
-                    // lanes 0-15 hold gate rows, 16-31 the same features' up
-                    // rows: each half of the warp takes every other column
-                    // and gets its missing factor from the other
-                    const bool hi = lane >= 16;
-                    const int *cols = inf->slot + c0 + 2 * (lane & 3) + (hi ? 1 : 0);
-                    const int i0 = cols[0], i1 = cols[8];
-                    float a[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? v[2 * j] : v[2 * j + 1], 16);
-                        const float g = __uint_as_float(hi ? got : v[2 * j]);
-                        const float u = __uint_as_float(hi ? v[2 * j + 1] : got);
-                        a[j] = swiglu(g, u);
-                    }
-                    const uint2 s0 = quad_pack(a[0], a[1], a[2], a[3], quad);
-                    const uint2 s1 = quad_pack(a[4], a[5], a[6], a[7], quad);
-                    if (i0 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i0 * p.feat) = s0;
-                    if (i1 >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i1 * p.feat) = s1;
-                } else {
+            for (int c0 = 16 * half; c0 < n; c0 += 32) {
+                if (c0 + 32 < n) load(c0 + 32, next);
+                if constexpr (F32) {
+                    // this lane's store: 4 features from f of column (lane & 3) of every four
+                    const int f = inf->nt * kFfRows + q * 32 + (lane & 28);
+                    const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
                     int i[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) i[j] = inf->slot[c0 + 4 * j + (lane & 3)];
-                    if constexpr (F32) {
-                        float4 s[4];
+                    float4 s[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            s[j] = quad_turn(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), lane);
+                    for (int j = 0; j < 4; ++j)
+                        s[j] = quad_turn(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                         __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), lane);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (i[j] >= 0 && f_ok)
-                                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + f + (int64_t)i[j] * p.feat) = s[j];
-                    } else {
-                        uint2 s[4];
+                    for (int j = 0; j < 4; ++j)
+                        if (i[j] >= 0 && f_ok)
+                            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + f + (int64_t)i[j] * p.feat) = s[j];
+                } else {
+                    const uint32_t at = blocks + buf * (16 * kOutPitch<UP>);
+                    float lo[8], hi[8];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            s[j] = quad_pack(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                             __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]), quad);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (i[j] >= 0 && f_ok) *reinterpret_cast<uint2 *>(out + (int64_t)i[j] * p.feat) = s[j];
+                    for (int j = 0; j < 8; ++j) {
+                        lo[j] = __uint_as_float(v[j]);
+                        hi[j] = __uint_as_float(v[8 + j]);
+                        if (UP) lo[j] = swiglu(lo[j], hi[j]);  // (gate rows, up rows)
                     }
+                    if constexpr (kOutBufs<MX, UP> == 1) meet(1 + half);  // the block before has been read
+                    put_frag(at + put, lo);
+                    if constexpr (!UP) put_frag(at + put + 32, hi);
+                    meet(1 + half);
+                    // 16 bytes a lane: 4 columns of 128 bytes or 2 of 256 a time
+                    constexpr int kLanes = kOutBytes<UP> / 16, kAtOnce = 32 / kLanes;
+                    const int f = inf->nt * (kOutBytes<UP> / 2) + lane % kLanes * 8;
+#pragma unroll
+                    for (int c = 4 * q; c < 4 * q + 4; c += kAtOnce) {
+                        const int col = c + lane / kLanes, i = inf->slot[c0 + col];
+                        uint4 w;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(at + (uint32_t)(col * kOutPitch<UP> + lane % kLanes * 16)) : "memory");
+                        if (i >= 0 && f < p.feat)  // (feat is a multiple of 16)
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (int64_t)i * p.feat + f) = w;
+                    }
+                    if constexpr (kOutBufs<MX, UP> == 2) buf ^= 1u;
                 }
                 if (c0 + 32 < n) {
                     tmem_wait_ld16(next);
@@ -1037,13 +1064,14 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.b_bytes = (uint32_t)(PAIR ? kCols / 2 : a.A) * kFfRowBytes;
     p.stage_bytes = SUB * (kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0));
     constexpr uint32_t kSmemMax = 232448;
-    p.stages = (int)((kSmemMax - 1024 - kFfMiscBytes<MX, PAIR>) / p.stage_bytes);
+    constexpr int kMisc = kFfMiscBytes<MX, PAIR> + kFfOutBytes<MX, UP, F32>;
+    p.stages = (int)((kSmemMax - 1024 - kMisc) / p.stage_bytes);
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
     if (p.stages < kFfLoaders<SUB>) return cudaErrorNotSupported;  // (see the row loaders; never with these sizes)
     p.acc_cols = PAIR ? kCols : a.A;
     const int cols = 2 * p.acc_cols + (MX ? 32 : 0);
     p.tmem_cols = cols <= 128 ? 128 : (cols <= 256 ? 256 : 512);
-    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + kFfMiscBytes<MX, PAIR>;
+    const size_t smem = 1024 + (size_t)p.stages * p.stage_bytes + kMisc;
 
     const CUtensorMapDataType type = MX ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const cuuint64_t k_elems = (cuuint64_t)(MX ? a.K / 2 : a.K), k_bytes = MX ? k_elems : 2 * k_elems;
