@@ -304,7 +304,7 @@ struct RingPos {
 // kernel the code of 17 short items a CTA took 25.1 us instead of 21.0).
 template <bool MX, bool UP, bool PAIR, int SUB, bool F32>
 __global__ void __launch_bounds__(kFfThreads<SUB>, 1)
-expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
+expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const FfParams p) {
     constexpr int kCols = kFfCols<MX, PAIR>;
     using Info = FfInfo<kCols>;
     constexpr int kLoaders = kFfLoaders<SUB>;
@@ -345,6 +345,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         *abort_flag = 0;
         mbar_fence_init();
         prefetch_tensormap(&tm_w);
+        if constexpr (MX && PAIR) prefetch_tensormap(&tm_s);
     }
     if (warp == 1) {
         if constexpr (PAIR) {
@@ -392,8 +393,11 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (elected) {
                     if constexpr (PAIR) {
                         // both CTAs' bytes complete the leader's barrier
-                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * subs * kFfWBytes);
+                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * (subs * kFfWBytes + (MX ? 2 * SUB * kSfAtom : 0)));
                         const uint32_t fb = cluster_addr(bar, 0u);
+                        // (the last stage's box may reach into the next tile's scales; they are not used)
+                        if constexpr (MX)
+                            tma_load_2d_pair(base + ws_off, &tm_s, 0, (e * p.ntiles + min(nt, p.ntiles - 1)) * p.num_chunks + 2 * kb, fb);
 #pragma unroll
                         for (int u = 0; u < SUB; ++u) {
                             if (u >= subs) break;
@@ -466,6 +470,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         int ent[kAhead][8], e[kAhead], at[kAhead], slot[8];  // (at: first block of the item's group)
         int grp2 = grp, tile2 = tile;  // the item that is requested next
         const int npp = __ldcg(p.npp);
+        // (requested with npp: of blocks past it, left out below)
+        const int first_e = PAIR && lane < p.max_blocks ? __ldcg(p.eids + lane) : 0;
         if constexpr (!PAIR) {  // the first two at once with npp: what lies past it is left out below
             int g = grp, t = tile;
             fetch(g, p.max_blocks, ent[0], e[0]);
@@ -484,7 +490,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     if (scan_at + 32 >= nblk) return -1;
                     scan_base += __popc(starts);
                     scan_at += 32;
-                    const int b = scan_at + lane, eb = b < nblk ? __ldcg(p.eids + b) : 0;
+                    const int b = scan_at + lane, eb = scan_at == 0 ? first_e : (b < nblk ? __ldcg(p.eids + b) : 0);
                     int before = __shfl_up_sync(0xffffffffu, eb, 1);
                     if (lane == 0) before = last_e;
                     const uint32_t first = __ballot_sync(0xffffffffu, b == 0 || eb != before);
@@ -752,16 +758,6 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                                     cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q, q < pieces ? srow[j] : -1);
                             }
                         }
-                        // (of a pair: the weights' scales too, as a plain bulk
-                        // copy cannot complete the other CTA's barrier)
-                        if constexpr (PAIR) {
-                            const uint8_t *src = p.w_scales +
-                                (((int64_t)inf->e * p.ntiles + min(inf->nt, p.ntiles - 1)) * p.num_chunks + 2 * kb) * kSfAtom;
-#pragma unroll
-                            for (int i = 0; i < 2 * SUB; ++i)
-                                cp_async_16(base + ws_off + i * kSfAtom + lane * 16, src + i * kSfAtom + lane * 16,
-                                            i < pieces ? 0 : -1);
-                        }
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1026,11 +1022,11 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 static bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ptr, const cuuint64_t *dims,
-                   const cuuint64_t *strides, const cuuint32_t *box) {
+                   const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     const auto fn = tensor_map_encoder();
     const cuuint32_t unit[5] = {1, 1, 1, 1, 1};
     return fn && fn(map, type, (cuuint32_t)rank, const_cast<void *>(ptr), dims, strides, box, unit,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1090,6 +1086,14 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
         const cuuint32_t box[3] = {box_k, kFfRows, 1};
         ok = encode(&mw, type, 3, a.w, dims, strides, box);
     }
+    // a weight's tiled scales: pieces of 512 bytes
+    CUtensorMap ms{};
+    if (MX && PAIR && ok) {
+        const cuuint64_t dims[2] = {kSfAtom / 4, (cuuint64_t)a.num_experts * p.ntiles * p.num_chunks};
+        const cuuint64_t strides[1] = {kSfAtom};
+        const cuuint32_t box[2] = {kSfAtom / 4, 2 * SUB};
+        ok = encode(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, a.w_scales, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+    }
     if (!ok) return cudaErrorInvalidValue;
     p.x = static_cast<const uint8_t *>(a.x);
     p.x_bytes = (int)k_bytes;
@@ -1122,7 +1126,7 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP, PAIR, SUB, F32>, mw, p);
+    return cudaLaunchKernelEx(&cfg, expert_ffn_kernel<MX, UP, PAIR, SUB, F32>, mw, ms, p);
 }
 
 template <bool MX, bool UP>
