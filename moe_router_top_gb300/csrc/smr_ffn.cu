@@ -212,8 +212,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&b);
 }
-// Outputs in bf16 leave through shared memory, 16 columns at a time, in whole
-// lines. (Stored from registers, a warp reaches 64 bytes of a line at most:
+// Outputs in bf16 leave through shared memory, in whole lines. (Stored from registers, a warp reaches 64 bytes of a line at most:
 // 131072 scattered rows of 4096 bytes took 164 us that way, 313 us in pieces of
 // 32 bytes, 83 us in lines.) TMEM is read in the matrix-fragment shape, whose
 // transposing store puts neighbouring features next to each other without a
@@ -223,13 +222,12 @@ template <bool UP>
 constexpr int kOutBytes = UP ? 128 : 256;        // of a column: 64 or 128 features
 template <bool UP>
 constexpr int kOutPitch = kOutBytes<UP> + 16;    // 8 rows of a store in different banks
-// Blocks of 16 columns for each half of the epilogue's warps: two, so that one
-// is filled while the other is read, but one where shared memory has no room
-// left (MXFP4, plain product).
-template <bool MX, bool UP>
-constexpr int kOutBufs = MX && !UP ? 1 : 2;
-template <bool MX, bool UP, bool F32>
-constexpr int kFfOutBytes = F32 ? 0 : 2 * kOutBufs<MX, UP> * 16 * kOutPitch<UP>;
+template <bool UP>
+constexpr int kOutCols = UP ? 16 : 8;            // columns of a block: one matrix store of each warp
+// Two blocks for each half of the epilogue's warps: one is filled while the
+// other is read.
+template <bool UP, bool F32>
+constexpr int kFfOutBytes = F32 ? 0 : 2 * 2 * kOutCols<UP> * kOutPitch<UP>;
 
 // 32 lanes x 16 columns as two fragments of 16 x 16: v[8 h + 4 u + 2 r + b] is
 // lane 16 h + 8 r + (thread / 4), column 8 u + 2 (thread % 4) + b.
@@ -241,12 +239,14 @@ __device__ __forceinline__ void tmem_ld_frags_async(uint32_t taddr, uint32_t (&v
                  : "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
                  : "r"(taddr + (16u << 16)));
 }
-// A 16 x 16 fragment in bf16, transposed: row c of shared memory (of 16, one
-// address a thread) gets column c's 16 features.
-__device__ __forceinline__ void put_frag(uint32_t dst, const float (&a)[8]) {
+// Four 8 x 8 matrices in bf16, transposed: the address is that of the row
+// (thread % 8) of matrix (thread / 8) in shared memory, which gets a column's 8
+// features.
+__device__ __forceinline__ void put_frags(uint32_t dst, float a0, float a1, float a2, float a3, float a4, float a5,
+                                          float a6, float a7) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};"
-                 ::"r"(dst), "r"(pack_bf16x2(a[0], a[1])), "r"(pack_bf16x2(a[2], a[3])),
-                   "r"(pack_bf16x2(a[4], a[5])), "r"(pack_bf16x2(a[6], a[7])) : "memory");
+                 ::"r"(dst), "r"(pack_bf16x2(a0, a1)), "r"(pack_bf16x2(a2, a3)), "r"(pack_bf16x2(a4, a5)),
+                   "r"(pack_bf16x2(a6, a7)) : "memory");
 }
 // Four warps meet; every one gets whether all of them came with ok.
 __device__ __forceinline__ bool meet_if(int id, bool ok) {
@@ -782,10 +782,11 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         // columns, the other four the rest
         const int q = warp & 3, half = warp < 3 + kLoaders + 4 ? 0 : 1;
         RingPos iq, ac;
-        // blocks of 16 columns: this half's, and this thread's row of a 16 x 16
-        // fragment's four 8 x 8 matrices
-        const uint32_t blocks = smem_u32(out_rows) + (uint32_t)(half * kOutBufs<MX, UP> * 16 * kOutPitch<UP>);
-        const uint32_t put = (uint32_t)((8 * (lane >> 4) + (lane & 7)) * kOutPitch<UP> + q * (UP ? 32 : 64) + ((lane >> 3) & 1) * 16);
+        // this half's blocks, and this thread's place in one for the four
+        // matrices of a store: 16 features x 16 columns, or 32 x 8
+        const uint32_t blocks = smem_u32(out_rows) + (uint32_t)(half * 2 * kOutCols<UP> * kOutPitch<UP>);
+        const uint32_t put = UP ? (uint32_t)((8 * (lane >> 4) + (lane & 7)) * kOutPitch<UP> + q * 32 + ((lane >> 3) & 1) * 16)
+                                : (uint32_t)((lane & 7) * kOutPitch<UP> + q * 64 + (lane >> 3) * 16);
         uint32_t buf = 0;
         while (true) {
             bool ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
@@ -825,32 +826,33 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                         if (i[j] >= 0 && f_ok)
                             *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + f + (int64_t)i[j] * p.feat) = s[j];
                 } else {
-                    const uint32_t at = blocks + buf * (16 * kOutPitch<UP>);
-                    float lo[8], hi[8];
+                    float a[16];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        lo[j] = __uint_as_float(v[j]);
-                        hi[j] = __uint_as_float(v[8 + j]);
-                        if (UP) lo[j] = swiglu(lo[j], hi[j]);  // (gate rows, up rows)
-                    }
-                    if constexpr (kOutBufs<MX, UP> == 1) meet(1 + half);  // the block before has been read
-                    put_frag(at + put, lo);
-                    if constexpr (!UP) put_frag(at + put + 32, hi);
-                    meet(1 + half);
-                    // 16 bytes a lane: 4 columns of 128 bytes or 2 of 256 a time
-                    constexpr int kLanes = kOutBytes<UP> / 16, kAtOnce = 32 / kLanes;
-                    const int f = inf->nt * (kOutBytes<UP> / 2) + lane % kLanes * 8;
+                    for (int j = 0; j < 16; ++j) a[j] = __uint_as_float(v[j]);
 #pragma unroll
-                    for (int c = 4 * q; c < 4 * q + 4; c += kAtOnce) {
-                        const int col = c + lane / kLanes, i = inf->slot[c0 + col];
+                    for (int b = 0; b < 16; b += kOutCols<UP>) {  // a block: columns c0 + b on
+                        const uint32_t at = blocks + buf * (kOutCols<UP> * kOutPitch<UP>);
+                        const int k = b / 2;
+                        if constexpr (UP)  // (gate rows, then up rows)
+                            put_frags(at + put, swiglu(a[0], a[8]), swiglu(a[1], a[9]), swiglu(a[2], a[10]),
+                                      swiglu(a[3], a[11]), swiglu(a[4], a[12]), swiglu(a[5], a[13]),
+                                      swiglu(a[6], a[14]), swiglu(a[7], a[15]));
+                        else
+                            put_frags(at + put, a[k], a[k + 1], a[k + 2], a[k + 3], a[8 + k], a[9 + k], a[10 + k], a[11 + k]);
+                        // (they have also read the block before the last one)
+                        meet(1 + half);
+                        // 16 bytes a lane: 4 columns of 128 bytes or 2 of 256
+                        constexpr int kLanes = kOutBytes<UP> / 16;
+                        const int col = 32 / kLanes * q + lane / kLanes, i = inf->slot[c0 + b + col];
+                        const int f = inf->nt * (kOutBytes<UP> / 2) + lane % kLanes * 8;
                         uint4 w;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                                      : "r"(at + (uint32_t)(col * kOutPitch<UP> + lane % kLanes * 16)) : "memory");
                         if (i >= 0 && f < p.feat)  // (feat is a multiple of 16)
                             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (int64_t)i * p.feat + f) = w;
+                        buf ^= 1u;
                     }
-                    if constexpr (kOutBufs<MX, UP> == 2) buf ^= 1u;
                 }
                 if (c0 + 32 < n) {
                     tmem_wait_ld16(next);
@@ -1060,7 +1062,7 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.b_bytes = (uint32_t)(PAIR ? kCols / 2 : a.A) * kFfRowBytes;
     p.stage_bytes = SUB * (kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0));
     constexpr uint32_t kSmemMax = 232448;
-    constexpr int kMisc = kFfMiscBytes<MX, PAIR> + kFfOutBytes<MX, UP, F32>;
+    constexpr int kMisc = kFfMiscBytes<MX, PAIR> + kFfOutBytes<UP, F32>;
     p.stages = (int)((kSmemMax - 1024 - kMisc) / p.stage_bytes);
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
     if (p.stages < kFfLoaders<SUB>) return cudaErrorNotSupported;  // (see the row loaders; never with these sizes)
