@@ -401,10 +401,11 @@ _stream_ws = {}
 _stream_lock = threading.RLock()
 
 
-def _check_sizes(*sizes: int) -> None:
-    """Refuses sizes that the library's 32-bit arguments would cut off."""
-    if max(sizes) >= 1 << 31:
-        raise ValueError(f"sizes must be below 2^31 (got {max(sizes)})")
+def _check_sizes(bits: int) -> None:
+    """Refuses sizes that the library's 32-bit arguments would cut off (bits:
+    the sizes or-ed together)."""
+    if bits & ~0x7FFFFFFF:
+        raise ValueError("sizes must be at least 0 and below 2^31")
 
 
 def _check_buffer(ws, dev: int) -> None:
@@ -458,10 +459,12 @@ def _run_product(fn, size_fn, args, ws, dev: int) -> None:
         _check(status)
 
 
-def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated, sorted_token_ids, expert_ids, npp, block_size):
-    """Checks of a product's operands in either format and of the align's outputs."""
+def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated, sorted_token_ids, expert_ids, npp, block_size,
+                    extra):
+    """Checks of a product's operands in either format and of the align's outputs
+    (extra: one more size)."""
     torch = _torch()
-    _check_sizes(rows, K, w_rows, w.shape[0], block_size)
+    _check_sizes(rows | K | w_rows | w.shape[0] | block_size | extra)
     mx = x_scales is not None
     if mx != (w_scales is not None):
         raise ValueError("x_scales and w_scales must both be given (MXFP4) or both be None (bfloat16)")
@@ -514,13 +517,12 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
     width, block_size = int(width), int(block_size)
     if width < 1:
         raise ValueError(f"width must be >= 1 (got {width})")
-    _check_sizes(width)
     T, H = x.shape
     E, I = w.shape[0], w.shape[1] // 2
     if x_scales is not None:
         H *= 2
     _product_inputs(x, w, x_scales, w_scales, T, H, 2 * I, True, sorted_token_ids, expert_ids,
-                    num_tokens_post_padded, block_size)
+                    num_tokens_post_padded, block_size, width)
     dev = _check_cuda(x, w, x_scales, w_scales, sorted_token_ids, expert_ids, num_tokens_post_padded, out)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -557,13 +559,12 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     if w.dim() != 3 or x.dim() != 2:
         raise ValueError("x must be [num_tokens * width, I] and w [num_experts, H, I]")
     block_size, num_logical = int(block_size), int(num_logical)
-    _check_sizes(num_logical)
     T, width = topk_ids.shape
     E, H, I = w.shape
     if x_scales is not None:
         I *= 2
     _product_inputs(x, w, x_scales, w_scales, T * width, I, H, False, sorted_token_ids, expert_ids,
-                    num_tokens_post_padded, block_size)
+                    num_tokens_post_padded, block_size, num_logical)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     dev = _check_cuda(x, w, topk_ids, topk_weights, x_scales, w_scales, sorted_token_ids, expert_ids,
@@ -648,7 +649,7 @@ def tile_mxfp4_scales(scales, *, gated: bool = False, out=None, stream=None):
     if scales.dtype != torch.uint8 or scales.dim() != 3 or not scales.is_contiguous():
         raise ValueError("scales must be a contiguous uint8 [num_experts, N, K / 32] tensor")
     E, N, K = scales.shape[0], scales.shape[1], 32 * scales.shape[2]
-    _check_sizes(E, N, K)
+    _check_sizes(E | N | K)
     dev = _check_cuda(scales, out)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
