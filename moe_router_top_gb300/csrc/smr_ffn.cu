@@ -33,7 +33,7 @@ namespace smr {
 // (a stage would be too large for a ring of them). A stage costs every role a
 // few hundred cycles of barrier round trips whatever its size: 550 a stage of
 // one k-block, 430 a k-block in stages of two (one token, 96 items; MXFP4 up,
-// 16384 tokens: 261 us in stages of one, 240 in stages of two).
+// 16384 tokens: 210 us in stages of one, 187 in stages of two).
 template <int SUB>
 constexpr int kFfLoaders = SUB == 2 ? 4 : 6;     // warps that load the routed rows; at most the stages
 constexpr int kFfDrains = 8;                     // warps of the epilogue, two for each quarter of TMEM's lanes
@@ -300,8 +300,9 @@ struct RingPos {
 // each other together); each holds its own 128 weight rows (and their scales),
 // half of the routed rows and all of these rows' scales, and drains its own
 // lanes.
-// F32: the outputs are fp32, else bf16 (a variant of its own: with both in one
-// kernel the code of 17 short items a CTA took 25.1 us instead of 21.0).
+// F32: the outputs are fp32, else bf16 (a variant of its own that stays within
+// 96 registers a thread: with both in one kernel blocks of the sum no longer
+// fitted beside a CTA, and 8 tokens in MXFP4 took 25.1 us instead of 21.0).
 template <bool MX, bool UP, bool PAIR, int SUB, bool F32>
 __global__ void __launch_bounds__(kFfThreads<SUB>, 1)
 expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const FfParams p) {
@@ -441,8 +442,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         const bool wide = (reinterpret_cast<uintptr_t>(p.sorted) & 15) == 0;
         // the entries and the block's expert (of blocks below `limit`),
         // requested kAhead items ahead (a round trip to L2 is longer than two
-        // short items; with two, this warp took 1300 cycles an item and set
-        // the pace of 8 tokens' second product in MXFP4)
+        // short items: with two ahead this warp took 1300 cycles an item)
         auto fetch = [&](int b0, int limit, int (&ent)[8], int &e) {
             const int b = b0 + bo;
             if (!in || b0 < 0 || b >= limit) return;
@@ -694,8 +694,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                     // requested before the rows are copied and stored after:
                     // a gather of 32 rows costs the load unit 32 cycles
                     // whatever its width, and 4-byte copies take four for the
-                    // 16 bytes of a stage (MXFP4 up, 16384 tokens: 266 us
-                    // with those, 240 with 16-byte loads).
+                    // 16 bytes of a stage (MXFP4 up, 16384 tokens: a
+                    // tenth longer with those than with 16-byte loads).
                     constexpr int kSets = MX ? kCols / 32 : 1, kWords = 2 * SUB;
                     uint32_t scale[kSets][kWords];
                     int srow[kSets];
@@ -985,11 +985,11 @@ expert_combine_kernel(const void *__restrict__ y, const int32_t *__restrict__ id
 
 // CTA pairs from this many rows an expert, on average: a pair halves the rows
 // that each CTA loads and that its MMAs read, but has only half as many items
-// to share out. With pairs and without (us, 128 experts, gated product): bf16
-// 16384 tokens of 8 slots 588 and 847, 1024 skewed tokens (64 rows an expert)
-// 135 and 157, evenly spread 136 and 135, 512 tokens (32 rows) 133 and 127;
-// MXFP4 16384 tokens 240 and 314, 1024 tokens 44 and 49 skewed, 42 and 41
-// evenly spread, 512 tokens 40 and 38.
+// to share out. With pairs and without (us on the device, 128 experts, gated
+// product): bf16 16384 tokens of 8 slots 494 and 777, 1024 skewed tokens (64
+// rows an expert) 134 and 156, evenly spread 134 and 133, 768 tokens (48 rows)
+// 131 and 145, evenly spread 132 and 126; MXFP4 16384 tokens 187 and 258, 1024
+// tokens 44.5 and 48.8 skewed, 40.6 and 40.4 evenly spread.
 constexpr int kPairRows = 48;
 static bool use_pairs(int64_t numel, int num_experts) { return numel >= (int64_t)kPairRows * num_experts; }
 
