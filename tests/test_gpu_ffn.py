@@ -624,3 +624,39 @@ def test_down_of_few_tokens(smr, mx, T, E, width, H):
     assert smr.get_device_error(ws) == 0
     _close(out, *_ref_down(torch.where(skipped[:, None], 0.0, xv), wv, ids, wts))
     assert torch.equal(out, smr.expert_down(xa, wa, ids, wts, *al, block_size=64, workspace=ws, **kw))
+
+
+def test_threads_on_one_stream(smr):
+    """Calls of four threads on the default stream share its workspace."""
+    import threading
+    cases = [_case(smr, T=T, seed=T) for T in (3, 40, 300, 600)]
+    refs = [_ffn(smr, c) for c in cases]
+    torch.cuda.synchronize()
+    outs = [[] for _ in cases]
+
+    def work(k):
+        outs[k] += [_ffn(smr, cases[k])[1] for _ in range(25)]
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, refs):
+        assert len(got) == 25 and all(torch.equal(o, ref[1]) for o in got)
+
+
+def test_default_stream_by_its_pointer(smr):
+    c = _case(smr, T=20)
+    ref = _ffn(smr, c)
+    got = _ffn(smr, c, stream=torch.cuda.default_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_workspace_on_the_host_is_refused(smr):
+    ids, wts, al, x, w13, w2 = _case(smr, T=5)
+    for ws in (torch.zeros(4096, dtype=torch.uint8), smr.Workspace(4096, "cpu")):
+        with pytest.raises(ValueError, match="workspace must be on"):
+            smr.expert_up(x, w13, *al, width=3, block_size=64, workspace=ws)
