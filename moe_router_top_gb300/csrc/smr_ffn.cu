@@ -239,14 +239,25 @@ __device__ __forceinline__ void tmem_ld_frags_async(uint32_t taddr, uint32_t (&v
                  : "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
                  : "r"(taddr + (16u << 16)));
 }
-// Four 8 x 8 matrices in bf16, transposed: the address is that of the row
-// (thread % 8) of matrix (thread / 8) in shared memory, which gets a column's 8
-// features.
-__device__ __forceinline__ void put_frags(uint32_t dst, float a0, float a1, float a2, float a3, float a4, float a5,
-                                          float a6, float a7) {
+// The fragments' values in bf16, in the order of put_frags: the gated product's
+// features of 16 columns, or twice 32 features of 8 columns.
+template <bool UP>
+__device__ __forceinline__ void pack_frags(const uint32_t (&v)[16], uint32_t (&o)[UP ? 4 : 8]) {
+    float a[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) a[j] = __uint_as_float(v[j]);
+#pragma unroll
+    for (int j = 0; j < (UP ? 4 : 8); ++j) {
+        const int k = UP ? 2 * j : 4 * (j >> 2) + 2 * (j & 1) + 8 * (j >> 1 & 1);
+        o[j] = UP ? pack_bf16x2(swiglu(a[k], a[(k + 8) & 15]), swiglu(a[k + 1], a[(k + 9) & 15]))  // (gate, up rows)
+                  : pack_bf16x2(a[k], a[k + 1]);
+    }
+}
+// Four 8 x 8 matrices, transposed: the address is that of the row (thread % 8)
+// of matrix (thread / 8) in shared memory, which gets a column's 8 features.
+__device__ __forceinline__ void put_frags(uint32_t dst, const uint32_t *o) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared::cta.b16 [%0], {%1, %2, %3, %4};"
-                 ::"r"(dst), "r"(pack_bf16x2(a0, a1)), "r"(pack_bf16x2(a2, a3)), "r"(pack_bf16x2(a4, a5)),
-                   "r"(pack_bf16x2(a6, a7)) : "memory");
+                 ::"r"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
 }
 // Four warps meet; every one gets whether all of them came with ok.
 __device__ __forceinline__ bool meet_if(int id, bool ok) {
@@ -799,20 +810,16 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.acc_cols);
             uint32_t v[16], next[16];
-            const auto load = [&](int c, uint32_t (&to)[16]) {
-                if constexpr (F32) tmem_ld16_async(acc + (uint32_t)c, to);
-                else tmem_ld_frags_async(acc + (uint32_t)c, to);
-            };
-            if (16 * half < n) {
-                load(16 * half, v);
-                tmem_wait_ld16(v);
-            }
-            for (int c0 = 16 * half; c0 < n; c0 += 32) {
-                if (c0 + 32 < n) load(c0 + 32, next);
-                if constexpr (F32) {
-                    // this lane's store: 4 features from f of column (lane & 3) of every four
-                    const int f = inf->nt * kFfRows + q * 32 + (lane & 28);
-                    const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
+            if constexpr (F32) {
+                if (16 * half < n) {
+                    tmem_ld16_async(acc + (uint32_t)(16 * half), v);
+                    tmem_wait_ld16(v);
+                }
+                // this lane's store: 4 features from f of column (lane & 3) of every four
+                const int f = inf->nt * kFfRows + q * 32 + (lane & 28);
+                const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
+                for (int c0 = 16 * half; c0 < n; c0 += 32) {
+                    if (c0 + 32 < n) tmem_ld16_async(acc + (uint32_t)(c0 + 32), next);
                     int i[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) i[j] = inf->slot[c0 + 4 * j + (lane & 3)];
@@ -825,39 +832,49 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                     for (int j = 0; j < 4; ++j)
                         if (i[j] >= 0 && f_ok)
                             *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + f + (int64_t)i[j] * p.feat) = s[j];
-                } else {
-                    float a[16];
+                    if (c0 + 32 < n) {
+                        tmem_wait_ld16(next);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) a[j] = __uint_as_float(v[j]);
-#pragma unroll
-                    for (int b = 0; b < 16; b += kOutCols<UP>) {  // a block: columns c0 + b on
-                        const uint32_t at = blocks + buf * (kOutCols<UP> * kOutPitch<UP>);
-                        const int k = b / 2;
-                        if constexpr (UP)  // (gate rows, then up rows)
-                            put_frags(at + put, swiglu(a[0], a[8]), swiglu(a[1], a[9]), swiglu(a[2], a[10]),
-                                      swiglu(a[3], a[11]), swiglu(a[4], a[12]), swiglu(a[5], a[13]),
-                                      swiglu(a[6], a[14]), swiglu(a[7], a[15]));
-                        else
-                            put_frags(at + put, a[k], a[k + 1], a[k + 2], a[k + 3], a[8 + k], a[9 + k], a[10 + k], a[11 + k]);
-                        // (they have also read the block before the last one)
-                        meet(1 + half);
-                        // 16 bytes a lane: 4 columns of 128 bytes or 2 of 256
-                        constexpr int kLanes = kOutBytes<UP> / 16;
-                        const int col = 32 / kLanes * q + lane / kLanes, i = inf->slot[c0 + b + col];
-                        const int f = inf->nt * (kOutBytes<UP> / 2) + lane % kLanes * 8;
-                        uint4 w;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                     : "r"(at + (uint32_t)(col * kOutPitch<UP> + lane % kLanes * 16)) : "memory");
-                        if (i >= 0 && f < p.feat)  // (feat is a multiple of 16)
-                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + (int64_t)i * p.feat + f) = w;
-                        buf ^= 1u;
+                        for (int j = 0; j < 16; ++j) v[j] = next[j];
                     }
                 }
-                if (c0 + 32 < n) {
-                    tmem_wait_ld16(next);
+            } else {
+                constexpr int kSteps = 16 / kOutCols<UP>;
+                uint32_t o[UP ? 4 : 8];
+                if (16 * half < n) {
+                    tmem_ld_frags_async(acc + (uint32_t)(16 * half), v);
+                    tmem_wait_ld16(v);
+                    pack_frags<UP>(v, o);
+                }
+                // 16 bytes a lane: 4 columns of 128 bytes or 2 of 256
+                constexpr int kLanes = kOutBytes<UP> / 16;
+                const int col = 32 / kLanes * q + lane / kLanes;
+                const int f = inf->nt * (kOutBytes<UP> / 2) + lane % kLanes * 8;
+                const bool f_ok = f < p.feat;  // (feat is a multiple of 16)
+                uint16_t *out = static_cast<uint16_t *>(p.out) + f;
+                for (int c0 = 16 * half; c0 < n; c0 += 32) {
+                    if (c0 + 32 < n) tmem_ld_frags_async(acc + (uint32_t)(c0 + 32), next);
+                    uint4 w[kSteps];
+                    int i[kSteps];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = next[j];
+                    for (int b = 0; b < kSteps; ++b) {
+                        const uint32_t at = blocks + buf * (kOutCols<UP> * kOutPitch<UP>);
+                        put_frags(at + put, o + 4 * b);
+                        meet(1 + half);  // (the four have also read the block before the last one)
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[b].x), "=r"(w[b].y), "=r"(w[b].z), "=r"(w[b].w)
+                                     : "r"(at + (uint32_t)(col * kOutPitch<UP> + lane % kLanes * 16)) : "memory");
+                        i[b] = inf->slot[c0 + b * kOutCols<UP> + col];
+                        buf ^= 1u;
+                    }
+                    // the next columns are computed while these are on their way from shared memory
+                    if (c0 + 32 < n) {
+                        tmem_wait_ld16(next);
+                        pack_frags<UP>(next, o);
+                    }
+#pragma unroll
+                    for (int b = 0; b < kSteps; ++b)
+                        if (i[b] >= 0 && f_ok) *reinterpret_cast<uint4 *>(out + (int64_t)i[b] * p.feat) = w[b];
                 }
             }
             tc_fence_before();
