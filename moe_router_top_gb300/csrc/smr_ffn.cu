@@ -204,9 +204,21 @@ __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t saddr) {
     else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// silu(g) * u in fp32. The fast exponential and division are within a few
-// 2^-23 of the exact value, far below the rounding to bf16 that follows.
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) * u in fp32: with h = exp(-|g| / 2) = 2^(-|g| log2(e) / 2), silu(g) =
+// g / (1 + h^2) for g >= 0 and g h^2 / (1 + h^2) below, one factor h going to g
+// and one to u. The denominator stays in [1, 2] and h is a normal number down
+// to g = -174, so that a small sigmoid beside a large u keeps its value (1 / (1
+// + exp(-g)) overflows at g = -88); from there on the product is below 2^-115
+// for every finite u and comes out as 0. Off by at most 4 + 1.2 |g| units of
+// 2^-23 from the two powers (the rounding of their argument, 2 units each) and
+// 5 from the rest.
+__device__ __forceinline__ float swiglu(float g, float u) {
+    float h, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fabsf(g) * -0.72134752f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.0f)));
+    const float t = g < 0.0f ? h : 1.0f;
+    return g * t * r * (u * t);
+}
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);

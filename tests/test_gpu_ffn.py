@@ -660,3 +660,31 @@ def test_workspace_on_the_host_is_refused(smr):
     for ws in (torch.zeros(4096, dtype=torch.uint8), smr.Workspace(4096, "cpu")):
         with pytest.raises(ValueError, match="workspace must be on"):
             smr.expert_up(x, w13, *al, width=3, block_size=64, workspace=ws)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [4, 200])  # single CTAs and pairs
+def test_strongly_negative_gates(smr, mx, T):
+    """Gates far outside the exponential's range beside large up values, whose
+    product is an ordinary number. One value of K is not zero, so the products
+    are exact and only silu(g) * u is rounded: half a step of bf16, and by the
+    bounds of the intrinsics 4 + 1.2 |g| + 5 units of 2^-23 (two exponentials of
+    half the argument, the quotient, the sums and products)."""
+    gates = torch.tensor([0.0, -0.5, 3.0, 12.0, 90.0, 200.0, -20.0, -60.0, -87.0, -87.5, -88.5, -90.0, -95.0, -100.0,
+                          -120.0, -192.0] * 2, device="cuda").to(torch.bfloat16)
+    ups = torch.cat([torch.full((16,), 2.0 ** 100, device="cuda"), torch.full((16,), -1.5, device="cuda")]).to(torch.bfloat16)
+    I, H = 32, 128
+    w = torch.zeros(1, 2 * I, H, dtype=torch.bfloat16, device="cuda")
+    w[0, :I, 0], w[0, I:, 0] = gates, ups
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    al = smr.align(ids, 1, 64)
+    xa, kw, _ = _values(smr, x, mx)
+    wv = w.double()
+    if mx:
+        w, kw["w_scales"], wv = _weights_mx(smr, w, True)
+    out = smr.expert_up(xa, w, *al, width=1, block_size=64, **kw)
+    g, u = wv[0, :I, 0], wv[0, I:, 0]
+    ref = (g / (1 + torch.exp(-g)) * u).expand(T, I)
+    _close(out, ref, (U + (9 + 1.2 * g.abs()) * 2.0 ** -23) * ref.abs() + TINY)
