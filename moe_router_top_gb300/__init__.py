@@ -10,6 +10,7 @@ raise :class:`SmrUnsupported`, so a caller can take its own fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -93,6 +94,17 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _stream_context(stream, device):
+    """The context of a call's stream (a torch stream or a pointer; None: the current one)."""
+    torch = _torch()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+_ERROR_WORD = slice(4, 8)  # bytes of a workspace's header
+
+
 class Workspace:
     """A zero-initialised device buffer that grows on demand.
 
@@ -110,9 +122,19 @@ class Workspace:
             self.ensure(nbytes)
 
     def ensure(self, nbytes: int):
+        """Grows to nbytes, in order on the current stream; the sticky error
+        bits go over to the new memory."""
         torch = _torch()
         if self.buf is None or self.buf.numel() < nbytes:
+            error = None
+            if self.buf is not None:
+                error = self.buf[_ERROR_WORD].clone()
+                if self.buf.is_cuda:  # (calls so far may have run on another stream than its own)
+                    self.buf.record_stream(torch.cuda.current_stream(self.device))
+                self.buf = None
             self.buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
+            if error is not None:
+                self.buf[_ERROR_WORD].copy_(error)
         return self.buf
 
     @property
@@ -127,14 +149,16 @@ class Workspace:
 _default_ws = {}
 
 
-def _workspace(ws, nbytes: int, device):
+def _workspace(ws, nbytes: int, device, stream):
     if ws is None:
         key = (device.type, device.index)
         ws = _default_ws.get(key)
         if ws is None:
             ws = _default_ws[key] = Workspace(0, device)
     if isinstance(ws, Workspace):
-        ws.ensure(nbytes)
+        if ws.buf is None or ws.nbytes < nbytes:
+            with _stream_context(stream, device):
+                ws.ensure(nbytes)
         return ws.ptr, ws.nbytes
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -208,7 +232,7 @@ def route(hidden, gate_w, shared_w=None, bias=None, *, topk: int, shared_scale: 
     a = _route_args(hidden, gate_w, shared_w, bias, topk, shared_scale, renormalize, topk_ids,
                     topk_weights, logits_out, shared_logit_bf16, hidden_fp8, hidden_scales)
     need = lib.smr_route_workspace_size(ctypes.byref(a))
-    wp, wn = _workspace(workspace, need, hidden.device)
+    wp, wn = _workspace(workspace, need, hidden.device, stream)
     _check(lib.smr_route(ctypes.byref(a), wp, wn, _stream_ptr(stream)))
     return topk_ids, topk_weights
 
@@ -283,7 +307,7 @@ def align(topk_ids, num_experts: int, block_size: int = 0, *, routed_topk: int =
     a = _align_args(topk_ids, T, W, num_experts, block_size, routed_topk, routed_experts, *outs,
                     eplb=eplb)
     need = lib.smr_align_workspace_size(ctypes.byref(a))
-    wp, wn = _workspace(workspace, need, topk_ids.device)
+    wp, wn = _workspace(workspace, need, topk_ids.device, stream)
     _check(lib.smr_align(ctypes.byref(a), wp, wn, _stream_ptr(stream)))
     return outs
 
@@ -311,7 +335,7 @@ def route_align(hidden, gate_w, shared_w=None, bias=None, *, topk: int, block_si
                           sorted_token_ids, expert_ids, num_tokens_post_padded)
     aa = _align_args(topk_ids, M, topk + S, E + S, block_size, topk, E, *outs, eplb=eplb)
     need = lib.smr_route_align_workspace_size(ctypes.byref(ra), ctypes.byref(aa))
-    wp, wn = _workspace(workspace, need, hidden.device)
+    wp, wn = _workspace(workspace, need, hidden.device, stream)
     _check(lib.smr_route_align(ctypes.byref(ra), ctypes.byref(aa), wp, wn, _stream_ptr(stream)))
     return (topk_ids, topk_weights) + tuple(outs)
 
@@ -369,7 +393,7 @@ def expert_gemm(hidden, expert_w, sorted_token_ids, expert_ids, num_tokens_post_
     a.sorted_token_ids, a.sorted_cap = _ptr(sorted_token_ids), sorted_token_ids.numel()
     a.expert_ids, a.num_tokens_post_padded = _ptr(expert_ids), _ptr(num_tokens_post_padded)
     a.out = _ptr(out)
-    wp, wn = _workspace(workspace, 256, hidden.device)
+    wp, wn = _workspace(workspace, 256, hidden.device, stream)
     _check(lib.smr_expert_gemm(ctypes.byref(a), wp, wn, _stream_ptr(stream)))
     return out
 

@@ -334,3 +334,43 @@ def test_sizes_past_32_bits_are_refused(smr):
                              torch.empty(1, big // 32 + 1, dtype=torch.uint8, device="meta"))
     with pytest.raises(ValueError, match="below 2"):
         smr.tile_mxfp4_scales(torch.empty(1, 1, big // 32 + 4, dtype=torch.uint8, device="meta"))
+
+
+def test_growing_keeps_the_error_bits(smr):
+    ws = smr.Workspace(256, "cpu")
+    ws.buf[4], ws.buf[8] = 5, 9  # error bits; another word of the header
+    ws.ensure(4096)
+    assert ws.nbytes == 4096 and ws.buf.nonzero().flatten().tolist() == [4] and ws.buf[4] == 5
+    ws.ensure(100)
+    assert ws.nbytes == 4096
+
+
+def test_growing_is_ordered_on_the_calls_stream(smr, monkeypatch):
+    """A route on another stream than the current one zeroes its workspace there."""
+    seen = []
+
+    class Stream:
+        cuda_stream = 7
+
+    class Context:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            seen.append(self.s)
+
+        def __exit__(self, *a):
+            seen.append(None)
+
+    def zeros(n, dtype, device):
+        seen.append("zeros")
+        return torch.zeros(n, dtype=dtype)
+
+    monkeypatch.setattr(smr, "_torch_module", types.SimpleNamespace(
+        cuda=types.SimpleNamespace(stream=Context), device=torch.device, uint8=torch.uint8, zeros=zeros,
+        _C=types.SimpleNamespace(_cuda_isCurrentStreamCapturing=lambda: False)))
+    ws, s = smr.Workspace(0, "cuda:0"), Stream()
+    smr._workspace(ws, 512, torch.device("cuda", 0), s)
+    assert seen == [s, "zeros", None] and ws.nbytes == 512
+    smr._workspace(ws, 512, torch.device("cuda", 0), s)
+    assert len(seen) == 3

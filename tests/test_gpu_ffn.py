@@ -688,3 +688,18 @@ def test_strongly_negative_gates(smr, mx, T):
     g, u = wv[0, :I, 0], wv[0, I:, 0]
     ref = (g / (1 + torch.exp(-g)) * u).expand(T, I)
     _close(out, ref, (U + (9 + 1.2 * g.abs()) * 2.0 ** -23) * ref.abs() + TINY)
+
+
+def test_error_bits_survive_a_growing_workspace(smr):
+    """An align's flag is still there when a later call on the workspace needs more room."""
+    ids, wts, _, x, w13, w2 = _case(smr, T=50)
+    ids = ids.clone()
+    ids[3, 1] = -1
+    ws = smr.Workspace(256)
+    al = smr.align(ids, 7, 64, workspace=ws)
+    act = smr.expert_up(x, w13, *al, width=3, block_size=64, workspace=ws)
+    out = smr.expert_down(act, w2, ids, wts, *al, block_size=64, workspace=ws)
+    assert ws.nbytes > 256 and smr.get_device_error(ws) == 1
+    assert torch.isfinite(out).all()
+    smr.clear_device_error(ws)
+    assert smr.get_device_error(ws) == 0
