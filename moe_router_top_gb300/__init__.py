@@ -112,12 +112,19 @@ class Workspace:
     zero, a call tag that only advances), so a workspace is zeroed once (on
     allocation) and can be reused by later calls and CUDA graph replays.
     Calls sharing one workspace must not overlap on the GPU.
+
+    It does not grow while its stream is being captured (the zeroing would
+    only be recorded, and repeated by every replay): a call that needs more is
+    refused then, so make it once, or call ensure, before the capture. Memory
+    that a capture has used stays with the workspace when it grows later.
     """
 
     def __init__(self, nbytes: int = 0, device=None):
         torch = _torch()
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf = None
+        self._captured = False  # whether a capture has used buf
+        self._kept = []         # what captures used before
         if nbytes:
             self.ensure(nbytes)
 
@@ -125,16 +132,25 @@ class Workspace:
         """Grows to nbytes, in order on the current stream; the sticky error
         bits go over to the new memory."""
         torch = _torch()
+        capturing = self.device.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing()
         if self.buf is None or self.buf.numel() < nbytes:
+            if capturing:
+                raise SmrError(_lib.SMR_ERR_WORKSPACE, f"a workspace cannot grow (to {nbytes} bytes) while its stream "
+                               "is being captured: make the call once, or call ensure, before the capture")
             error = None
             if self.buf is not None:
                 error = self.buf[_ERROR_WORD].clone()
-                if self.buf.is_cuda:  # (calls so far may have run on another stream than its own)
+                if self._captured:
+                    self._kept.append(self.buf)
+                    self._captured = False
+                elif self.buf.is_cuda:  # (calls so far may have run on another stream than its own)
                     self.buf.record_stream(torch.cuda.current_stream(self.device))
                 self.buf = None
             self.buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
             if error is not None:
                 self.buf[_ERROR_WORD].copy_(error)
+        elif capturing:
+            self._captured = True
         return self.buf
 
     @property
@@ -155,8 +171,16 @@ def _workspace(ws, nbytes: int, device, stream):
         ws = _default_ws.get(key)
         if ws is None:
             ws = _default_ws[key] = Workspace(0, device)
-    if isinstance(ws, Workspace):
         if ws.buf is None or ws.nbytes < nbytes:
+            torch = _torch()
+            if device.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing():
+                # memory of the graph's own, which it zeroes at every replay
+                own = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+                return own.data_ptr(), nbytes
+    if isinstance(ws, Workspace):
+        if stream is None or (ws.buf is not None and ws.nbytes >= nbytes):
+            ws.ensure(nbytes)
+        else:
             with _stream_context(stream, device):
                 ws.ensure(nbytes)
         return ws.ptr, ws.nbytes
@@ -447,6 +471,7 @@ def _call_product(fn, size_fn, ref, ws, dev: int, s: int) -> int:
     status = _lib.SMR_ERR_WORKSPACE
     if buf is not None:
         _check_buffer(buf, dev)
+        ws.ensure(0)  # (marks what a capture uses)
         status = fn(ref, buf.data_ptr(), buf.numel(), s)
     if status == _lib.SMR_ERR_WORKSPACE:
         buf = ws.ensure(size_fn(ref))

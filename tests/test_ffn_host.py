@@ -7,6 +7,7 @@ import ctypes
 import threading
 import time
 import types
+import weakref
 
 import pytest
 
@@ -374,3 +375,66 @@ def test_growing_is_ordered_on_the_calls_stream(smr, monkeypatch):
     assert seen == [s, "zeros", None] and ws.nbytes == 512
     smr._workspace(ws, 512, torch.device("cuda", 0), s)
     assert len(seen) == 3
+
+
+@pytest.fixture
+def captured_device(smr, monkeypatch):
+    """A stand-in device whose stream can be put under capture; memory is the host's."""
+    state = types.SimpleNamespace(capturing=False)
+    c = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda dev: 7,
+                              _cuda_isCurrentStreamCapturing=lambda: state.capturing)
+    monkeypatch.setattr(smr, "_torch_module", types.SimpleNamespace(
+        _C=c, device=torch.device, uint8=torch.uint8, zeros=lambda n, dtype, device: torch.zeros(n, dtype=dtype)))
+    monkeypatch.setattr(smr, "_default_ws", {})
+    monkeypatch.setattr(smr, "_check_buffer", lambda ws, dev: None)
+    return state
+
+
+def test_no_growth_under_capture(smr, captured_device):
+    calls = []
+
+    def fn(ref, ptr, n, s):
+        calls.append(n)
+        return _lib.SMR_OK if n >= 1024 else WORKSPACE
+
+    captured_device.capturing = True
+    dev = torch.device("cuda", 0)
+    for ws in (smr.Workspace(0, dev), smr.Workspace(0, dev)):
+        captured_device.capturing = False
+        ws.ensure(512)
+        captured_device.capturing = True
+        before = ws.buf
+        with pytest.raises(smr.SmrError, match="being captured"):
+            smr._run_product(fn, lambda ref: 1024, ExpertDownArgs(), ws, 0)
+        with pytest.raises(smr.SmrError, match="being captured"):
+            smr._workspace(ws, 1024, dev, None)
+        assert ws.buf is before
+    with pytest.raises(smr.SmrError, match="being captured"):
+        smr.Workspace(256, dev)
+    assert calls == [512, 512]
+    # a route without a workspace: the capture gets memory of its own, the shared one is left alone
+    ptr, n = smr._workspace(None, 2048, dev, None)
+    assert ptr and n == 2048 and smr._default_ws["cuda", 0].buf is None
+    captured_device.capturing = False
+    smr._workspace(None, 2048, dev, None)
+    assert smr._default_ws["cuda", 0].nbytes == 2048
+
+
+def test_memory_of_a_capture_is_kept(smr, captured_device):
+    """A graph goes on writing to the memory that it was captured with."""
+    ws = smr.Workspace(1024, torch.device("cuda", 0))
+    captured_device.capturing = True
+    smr._run_product(lambda *a: _lib.SMR_OK, lambda ref: 1024, ExpertDownArgs(), ws, 0)
+    captured_device.capturing = False
+    old = weakref.ref(ws.buf)
+    ws.ensure(4096)
+    assert old() is not None and old() is not ws.buf
+    free = weakref.ref(ws.buf)
+    ws.ensure(8192)  # no capture has used these
+    assert free() is None and old() is not None
+    captured_device.capturing = True
+    smr._workspace(ws, 8192, torch.device("cuda", 0), None)
+    captured_device.capturing = False
+    used = weakref.ref(ws.buf)
+    ws.ensure(16384)
+    assert used() is not None

@@ -703,3 +703,31 @@ def test_error_bits_survive_a_growing_workspace(smr):
     assert torch.isfinite(out).all()
     smr.clear_device_error(ws)
     assert smr.get_device_error(ws) == 0
+
+
+def test_workspace_of_a_graph(smr):
+    """A caller's workspace under capture: refused where it is too small, and
+    still the graph's after an eager call made it grow."""
+    small, big = _case(smr, T=30, seed=4), _case(smr, T=700, seed=5)
+    ref = [t.clone() for t in _ffn(smr, small)]
+    ids, wts, al, x, w13, w2 = small
+    ws = smr.Workspace(256)
+    with pytest.raises(smr.SmrError, match="being captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            smr.expert_down(ref[0], w2, ids, wts, *al, block_size=64, workspace=ws)
+    torch.cuda.synchronize()
+    assert ws.nbytes == 256
+    _ffn(smr, small, workspace=ws)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        outs = _ffn(smr, small, workspace=ws)
+    before = ws.nbytes
+    _ffn(smr, big, workspace=ws)
+    assert ws.nbytes > before
+    others = [torch.full((before,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]  # memory that was given back would be theirs
+    for t in outs:
+        t.zero_()
+    gr.replay()
+    torch.cuda.synchronize()
+    assert all((o == 7).all() for o in others)
+    assert torch.equal(outs[0], ref[0]) and torch.equal(outs[1], ref[1]) and smr.get_device_error(ws) == 0
