@@ -330,7 +330,8 @@ SMR_API smr_status smr_expert_gemm(const smr_expert_gemm_args *args, void *works
  * smr_expert_up is one launch, workspace >= 256 bytes; smr_expert_down is two
  * (the product into the workspace, then the sum), workspace as its _size says.
  * The first 256 bytes are zeroed once by the caller, as for every workspace;
- * error bits as for smr_expert_gemm. num_tokens == 0 launches nothing. */
+ * error bits as for smr_expert_gemm, also in the device's own word
+ * (smr_get_expert_error). num_tokens == 0 launches nothing. */
 SMR_API size_t smr_expert_up_workspace_size(const smr_expert_up_args *args);
 SMR_API size_t smr_expert_down_workspace_size(const smr_expert_down_args *args);
 SMR_API smr_status smr_expert_up(const smr_expert_up_args *args, void *workspace, size_t workspace_bytes,
@@ -371,6 +372,14 @@ SMR_API smr_status smr_get_device_error(const void *workspace, void *stream, int
 
 /* Clears the sticky device error word (stream-ordered memset). */
 SMR_API smr_status smr_clear_device_error(void *workspace, void *stream);
+
+/* One more sticky word per device: it gets the bits of every smr_expert_up
+ * and smr_expert_down launch on the device, whatever workspace the call had,
+ * also from graph replays and after the workspace is gone. Reads (after
+ * synchronising `stream`) or clears (stream-ordered) that of the current
+ * device. Not for launch paths. */
+SMR_API smr_status smr_get_expert_error(void *stream, int32_t *code_out);
+SMR_API smr_status smr_clear_expert_error(void *stream);
 
 /* The sticky device error word of smr_route_align_static's fixed scratch
  * array on the current device (same bits and synchronisation as

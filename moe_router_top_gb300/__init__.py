@@ -732,17 +732,39 @@ def route_align_workspace_size(route_args: RouteArgs, align_args: AlignArgs) -> 
                                                           ctypes.byref(align_args)))
 
 
-def get_device_error(workspace, stream=None) -> int:
-    """Sticky error bits of a workspace (synchronises the stream)."""
+def _shared_default_ws():
+    """The workspace that route, align and expert_gemm share on the current device, None if there is none yet."""
+    ws = _default_ws.get(("cuda", _torch().cuda.current_device()))
+    return None if ws is None or ws.buf is None else ws
+
+
+def get_device_error(workspace=None, stream=None) -> int:
+    """Sticky error bits of a workspace (synchronises the stream). Without one:
+    those of the calls on the current device that were given none, and of every
+    expert_up and expert_down there, replayed ones included. (A route or align
+    captured without a workspace before any such eager call keeps its bits in
+    its graph's memory.)"""
     lib = _lib.load()
-    ptr = workspace.ptr if isinstance(workspace, Workspace) else workspace.data_ptr()
     code = ctypes.c_int32(0)
+    bits = 0
+    if workspace is None:
+        _check(lib.smr_get_expert_error(_stream_ptr(stream), ctypes.byref(code)))
+        bits, workspace = code.value, _shared_default_ws()
+        if workspace is None:
+            return bits
+    ptr = workspace.ptr if isinstance(workspace, Workspace) else workspace.data_ptr()
     _check(lib.smr_get_device_error(ptr, _stream_ptr(stream), ctypes.byref(code)))
-    return code.value
+    return bits | code.value
 
 
-def clear_device_error(workspace, stream=None) -> None:
+def clear_device_error(workspace=None, stream=None) -> None:
+    """Clears what get_device_error reads with the same arguments."""
     lib = _lib.load()
+    if workspace is None:
+        _check(lib.smr_clear_expert_error(_stream_ptr(stream)))
+        workspace = _shared_default_ws()
+        if workspace is None:
+            return
     ptr = workspace.ptr if isinstance(workspace, Workspace) else workspace.data_ptr()
     _check(lib.smr_clear_device_error(ptr, _stream_ptr(stream)))
 

@@ -30,6 +30,7 @@ EXPORTED = (
     "smr_expert_gemm", "smr_expert_up", "smr_expert_up_workspace_size", "smr_expert_down",
     "smr_expert_down_workspace_size", "smr_quantize_mxfp4", "smr_dequantize_mxfp4",
     "smr_mxfp4_tiled_scale_bytes", "smr_tile_mxfp4_scales",
+    "smr_get_expert_error", "smr_clear_expert_error",
 )
 
 SMR_STALL_NONE = 0
@@ -149,6 +150,8 @@ def load(path: str = LIB_PATH):
             "smr_quantize_mxfp4": ([P, i64, i32, i64, P, P, P], ctypes.c_int),
             "smr_dequantize_mxfp4": ([P, P, i64, i32, P, P], ctypes.c_int),
             "smr_mxfp4_tiled_scale_bytes": ([i32, i32, i32, i32], sz),
+            "smr_get_expert_error": ([P, ctypes.POINTER(i32)], ctypes.c_int),
+            "smr_clear_expert_error": ([P], ctypes.c_int),
             "smr_tile_mxfp4_scales": ([P, i32, i32, i32, i32, P, P], ctypes.c_int),
         })
         for name, (argtypes, restype) in sigs.items():

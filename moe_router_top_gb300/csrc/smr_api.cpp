@@ -473,6 +473,17 @@ smr::FfnLaunch ffn_launch(const FfnCheck &c, void *ws) {
     return L;
 }
 
+// A sticky error word on the device.
+smr_status read_word(const void *word, void *stream, int32_t *code_out, const char *what) {
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = cudaMemcpy(code_out, word, 4, cudaMemcpyDeviceToHost);
+    return e == cudaSuccess ? SMR_OK : cuda_fail(what, e);
+}
+smr_status clear_word(void *word, void *stream, const char *what) {
+    const cudaError_t e = cudaMemsetAsync(word, 0, 4, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SMR_OK : cuda_fail(what, e);
+}
+
 // Rows and columns of an MXFP4 matrix.
 void check_mx_shape(int64_t rows, int32_t K, Reasons &r) {
     if (rows < 0) r.bad("rows must be >= 0 (got " + std::to_string(rows) + ")");
@@ -869,13 +880,7 @@ SMR_API smr_status smr_get_device_error(const void *workspace, void *stream, int
         g_last_error = "smr_get_device_error: workspace or code_out is NULL";
         return SMR_ERR_INVALID_ARG;
     }
-    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail("smr_get_device_error", e);
-    uint32_t word = 0;
-    e = cudaMemcpy(&word, static_cast<const uint8_t *>(workspace) + 4, 4, cudaMemcpyDeviceToHost);
-    if (e != cudaSuccess) return cuda_fail("smr_get_device_error", e);
-    *code_out = (int32_t)word;
-    return SMR_OK;
+    return read_word(static_cast<const uint8_t *>(workspace) + 4, stream, code_out, "smr_get_device_error");
 }
 
 SMR_API smr_status smr_clear_device_error(void *workspace, void *stream) {
@@ -883,10 +888,29 @@ SMR_API smr_status smr_clear_device_error(void *workspace, void *stream) {
         g_last_error = "smr_clear_device_error: workspace is NULL";
         return SMR_ERR_INVALID_ARG;
     }
-    cudaError_t e = cudaMemsetAsync(static_cast<uint8_t *>(workspace) + 4, 0, 4,
-                                    static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail("smr_clear_device_error", e);
-    return SMR_OK;
+    return clear_word(static_cast<uint8_t *>(workspace) + 4, stream, "smr_clear_device_error");
+}
+
+SMR_API smr_status smr_get_expert_error(void *stream, int32_t *code_out) {
+    if (!code_out) {
+        g_last_error = "smr_get_expert_error: code_out is NULL";
+        return SMR_ERR_INVALID_ARG;
+    }
+    smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    void *word = nullptr;
+    const cudaError_t e = smr::expert_error_word(&word);
+    if (e != cudaSuccess) return cuda_fail("smr_get_expert_error", e);
+    return read_word(word, stream, code_out, "smr_get_expert_error");
+}
+
+SMR_API smr_status smr_clear_expert_error(void *stream) {
+    smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    void *word = nullptr;
+    const cudaError_t e = smr::expert_error_word(&word);
+    if (e != cudaSuccess) return cuda_fail("smr_clear_expert_error", e);
+    return clear_word(word, stream, "smr_clear_expert_error");
 }
 
 SMR_API smr_status smr_get_static_device_error(void *stream, int32_t *code_out) {

@@ -316,6 +316,14 @@ struct RingPos {
     }
 };
 
+// Every error goes to the workspace's header and to one word per device, which
+// outlives workspaces and which a caller without one can read.
+static __device__ uint32_t g_expert_error;
+__device__ __forceinline__ void ffn_error(uint32_t *err, uint32_t bits) {
+    set_error(err, bits);
+    set_error(&g_expert_error, bits);
+}
+
 // MX: MXFP4 operands, else bf16. UP: the gated product (a tile holds 64
 // features: 16 gate rows and their 16 up rows in turn, so that both halves of
 // a feature are in one warp's TMEM lanes), else 128 plain rows. PAIR: two CTAs
@@ -583,7 +591,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 if (real) top = 8 * lane + j + 1;
             }
             // neither a slot nor the sentinel: a corrupted align output
-            if (bad) set_error(p.err, kErrBadSlot);
+            if (bad) ffn_error(p.err, kErrBadSlot);
             __syncwarp();
             const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
             const int nt = PAIR ? 2 * tile + (int)rank : tile;
@@ -593,7 +601,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
             step(grp2, tile2);
             if (rows == 0) return;
             if ((unsigned)eg >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
-                if (lane == 0) set_error(p.err, kErrBadId);
+                if (lane == 0) ffn_error(p.err, kErrBadId);
                 __syncwarp();
                 return;
             }
@@ -907,7 +915,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     if (*abort_flag && warp == 0 && lane == 0) {
         // a wait gave up: the piece's outputs are not written; weights still in
         // flight land before the CTA leaves
-        set_error(p.err, kErrWaitTimeout);
+        ffn_error(p.err, kErrWaitTimeout);
         if (rank == 0)
             for (int j = issued - ST > 0 ? issued - ST : 0; j < issued; ++j) {
                 volatile int drain = 0;
@@ -1038,6 +1046,8 @@ static int sm_count() {
     }
     return n;
 }
+
+cudaError_t expert_error_word(void **ptr) { return cudaGetSymbolAddress(ptr, g_expert_error); }
 
 // cuTensorMapEncodeTiled, looked up once (a function-local static).
 static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {

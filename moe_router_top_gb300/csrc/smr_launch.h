@@ -196,6 +196,8 @@ struct FfnLaunch {
 // Whether the rows between the second product and the sum are fp32 (out32).
 bool expert_rows_fp32(int64_t numel, int num_experts, int H);
 cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream);
+// The word on the current device that gets every product's error bits.
+cudaError_t expert_error_word(void **ptr);
 
 // out[t] = sum over s of wts[t][s] * y[t * width + s], slots whose id is
 // outside [0, num_logical) left out.

@@ -438,3 +438,8 @@ def test_memory_of_a_capture_is_kept(smr, captured_device):
     used = weakref.ref(ws.buf)
     ws.ensure(16384)
     assert used() is not None
+
+
+def test_expert_error_word_refusals(lib):
+    assert lib.smr_get_expert_error(None, None) == INVALID
+    assert "code_out is NULL" in lib.smr_last_error().decode()

@@ -731,3 +731,41 @@ def test_workspace_of_a_graph(smr):
     torch.cuda.synchronize()
     assert all((o == 7).all() for o in others)
     assert torch.equal(outs[0], ref[0]) and torch.equal(outs[1], ref[1]) and smr.get_device_error(ws) == 0
+
+
+def test_errors_without_a_workspace(smr):
+    """The bits of calls that were given no workspace can be read: eager ones,
+    replayed ones, and after the memory of a call is gone."""
+    ids, wts, al, x, w13, w2 = _case(smr, T=40)
+    smr.clear_device_error()
+    act, out = _ffn(smr, (ids, wts, al, x, w13, w2))
+    assert smr.get_device_error() == 0
+    srt = al[0].clone()
+    srt[1] = 1 << 29  # neither a slot nor the sentinel
+    smr.expert_up(x, w13, srt, *al[1:], width=3, block_size=64, out=act)
+    assert smr.get_device_error() == 4 == smr.get_device_error(None)
+    smr.clear_device_error()
+    assert smr.get_device_error() == 0
+    eids = al[1].clone()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        smr.expert_down(act, w2, ids, wts, al[0], eids, al[2], block_size=64, out=out)
+    gr.replay()
+    assert smr.get_device_error() == 0
+    eids[0] = 99  # an expert that does not exist
+    gr.replay()
+    assert smr.get_device_error() == 1
+    eids[0] = al[1][0]
+    gr.replay()
+    assert smr.get_device_error() == 1  # (sticky)
+    smr.clear_device_error()
+    ws = smr.Workspace(256)
+    smr.expert_up(x, w13, srt, *al[1:], width=3, block_size=64, out=act, workspace=ws)
+    assert smr.get_device_error(ws) == 4 and smr.get_device_error() == 4
+    smr.clear_device_error()
+    bad = ids.clone()
+    bad[0, 0] = -1
+    smr.align(bad, 7, 64)  # (the workspace that these calls share)
+    assert smr.get_device_error() == 1
+    smr.clear_device_error()
+    assert smr.get_device_error() == 0 and smr.get_device_error(ws) == 4
