@@ -36,7 +36,9 @@
  *    the buffer ready for the next one (counters back at zero, a call tag
  *    that only advances), so it can be reused by later calls and graph
  *    replays without clearing. Calls that share a workspace must not run
- *    concurrently.
+ *    concurrently on the GPU: they go to one stream, or are ordered by events.
+ *    Host threads may make them on one stream at once (a call's launches stay
+ *    together).
  *  - Kernels are launched with programmatic stream serialization: a launch
  *    may start while the preceding kernel on the stream is finishing. It
  *    reads hidden states, ids and the workspace, and writes every output,

@@ -111,7 +111,8 @@ class Workspace:
     The library leaves a workspace ready for its next call (counters back at
     zero, a call tag that only advances), so a workspace is zeroed once (on
     allocation) and can be reused by later calls and CUDA graph replays.
-    Calls sharing one workspace must not overlap on the GPU.
+    Calls sharing one workspace must not overlap on the GPU. Threads may call
+    with it on one stream: the launches of a call stay together.
 
     It does not grow while its stream is being captured (the zeroing would
     only be recorded, and repeated by every replay): a call that needs more is
@@ -123,6 +124,7 @@ class Workspace:
         torch = _torch()
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf = None
+        self.lock = threading.RLock()  # held from reading buf until the launches are made
         self._captured = False  # whether a capture has used buf
         self._kept = []         # what captures used before
         if nbytes:
@@ -165,12 +167,24 @@ class Workspace:
 _default_ws = {}
 
 
+_no_lock = contextlib.nullcontext()
+
+
+def _default_workspace(device):
+    key = (device.type, device.index)
+    return _default_ws.get(key) or _default_ws.setdefault(key, Workspace(0, device))
+
+
+def _hold(ws, device):
+    """The lock under which a call takes its workspace's memory and launches."""
+    if ws is None:
+        ws = _default_workspace(device)
+    return ws.lock if isinstance(ws, Workspace) else _no_lock
+
+
 def _workspace(ws, nbytes: int, device, stream):
     if ws is None:
-        key = (device.type, device.index)
-        ws = _default_ws.get(key)
-        if ws is None:
-            ws = _default_ws[key] = Workspace(0, device)
+        ws = _default_workspace(device)
         if ws.buf is None or ws.nbytes < nbytes:
             torch = _torch()
             if device.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing():
@@ -256,8 +270,10 @@ def route(hidden, gate_w, shared_w=None, bias=None, *, topk: int, shared_scale: 
     a = _route_args(hidden, gate_w, shared_w, bias, topk, shared_scale, renormalize, topk_ids,
                     topk_weights, logits_out, shared_logit_bf16, hidden_fp8, hidden_scales)
     need = lib.smr_route_workspace_size(ctypes.byref(a))
-    wp, wn = _workspace(workspace, need, hidden.device, stream)
-    _check(lib.smr_route(ctypes.byref(a), wp, wn, _stream_ptr(stream)))
+    with _hold(workspace, hidden.device):
+        wp, wn = _workspace(workspace, need, hidden.device, stream)
+        status = lib.smr_route(ctypes.byref(a), wp, wn, _stream_ptr(stream))
+    _check(status)
     return topk_ids, topk_weights
 
 
@@ -331,8 +347,10 @@ def align(topk_ids, num_experts: int, block_size: int = 0, *, routed_topk: int =
     a = _align_args(topk_ids, T, W, num_experts, block_size, routed_topk, routed_experts, *outs,
                     eplb=eplb)
     need = lib.smr_align_workspace_size(ctypes.byref(a))
-    wp, wn = _workspace(workspace, need, topk_ids.device, stream)
-    _check(lib.smr_align(ctypes.byref(a), wp, wn, _stream_ptr(stream)))
+    with _hold(workspace, topk_ids.device):
+        wp, wn = _workspace(workspace, need, topk_ids.device, stream)
+        status = lib.smr_align(ctypes.byref(a), wp, wn, _stream_ptr(stream))
+    _check(status)
     return outs
 
 
@@ -359,8 +377,10 @@ def route_align(hidden, gate_w, shared_w=None, bias=None, *, topk: int, block_si
                           sorted_token_ids, expert_ids, num_tokens_post_padded)
     aa = _align_args(topk_ids, M, topk + S, E + S, block_size, topk, E, *outs, eplb=eplb)
     need = lib.smr_route_align_workspace_size(ctypes.byref(ra), ctypes.byref(aa))
-    wp, wn = _workspace(workspace, need, hidden.device, stream)
-    _check(lib.smr_route_align(ctypes.byref(ra), ctypes.byref(aa), wp, wn, _stream_ptr(stream)))
+    with _hold(workspace, hidden.device):
+        wp, wn = _workspace(workspace, need, hidden.device, stream)
+        status = lib.smr_route_align(ctypes.byref(ra), ctypes.byref(aa), wp, wn, _stream_ptr(stream))
+    _check(status)
     return (topk_ids, topk_weights) + tuple(outs)
 
 
@@ -417,8 +437,10 @@ def expert_gemm(hidden, expert_w, sorted_token_ids, expert_ids, num_tokens_post_
     a.sorted_token_ids, a.sorted_cap = _ptr(sorted_token_ids), sorted_token_ids.numel()
     a.expert_ids, a.num_tokens_post_padded = _ptr(expert_ids), _ptr(num_tokens_post_padded)
     a.out = _ptr(out)
-    wp, wn = _workspace(workspace, 256, hidden.device, stream)
-    _check(lib.smr_expert_gemm(ctypes.byref(a), wp, wn, _stream_ptr(stream)))
+    with _hold(workspace, hidden.device):
+        wp, wn = _workspace(workspace, 256, hidden.device, stream)
+        status = lib.smr_expert_gemm(ctypes.byref(a), wp, wn, _stream_ptr(stream))
+    _check(status)
     return out
 
 
@@ -446,7 +468,6 @@ def _elsewhere(dev: int, stream):
 
 
 _stream_ws = {}
-_stream_lock = threading.RLock()
 
 
 def _check_sizes(bits: int) -> None:
@@ -467,36 +488,32 @@ def _check_buffer(ws, dev: int) -> None:
 def _call_product(fn, size_fn, ref, ws, dev: int, s: int) -> int:
     """One call on a Workspace. One that is too small is refused before any
     launch; it grows and the call is made again."""
-    buf = ws.buf
-    status = _lib.SMR_ERR_WORKSPACE
-    if buf is not None:
-        _check_buffer(buf, dev)
-        ws.ensure(0)  # (marks what a capture uses)
-        status = fn(ref, buf.data_ptr(), buf.numel(), s)
-    if status == _lib.SMR_ERR_WORKSPACE:
-        buf = ws.ensure(size_fn(ref))
-        _check_buffer(buf, dev)
-        status = fn(ref, buf.data_ptr(), buf.numel(), s)
+    with ws.lock:
+        buf = ws.buf
+        status = _lib.SMR_ERR_WORKSPACE
+        if buf is not None:
+            _check_buffer(buf, dev)
+            ws.ensure(0)  # (marks what a capture uses)
+            status = fn(ref, buf.data_ptr(), buf.numel(), s)
+        if status == _lib.SMR_ERR_WORKSPACE:
+            buf = ws.ensure(size_fn(ref))
+            _check_buffer(buf, dev)
+            status = fn(ref, buf.data_ptr(), buf.numel(), s)
     return status
 
 
 def _run_product(fn, size_fn, args, ws, dev: int) -> None:
     """Calls a product with the caller's workspace, or with one per device and
-    stream (calls on two streams may overlap). Threads may call on one stream:
-    the launches of a call that shares such a workspace stay together. A call
-    that is being captured gets a workspace of its own, which its graph keeps
-    and zeroes itself."""
+    stream (calls on two streams may overlap). A call that is being captured
+    gets a workspace of its own, which its graph keeps and zeroes itself."""
     torch = _torch()
     ref = ctypes.byref(args)
     s = torch._C._cuda_getCurrentRawStream(dev)
     if isinstance(ws, Workspace):
         status = _call_product(fn, size_fn, ref, ws, dev, s)
     elif ws is None and not torch._C._cuda_isCurrentStreamCapturing():
-        with _stream_lock:
-            ws = _stream_ws.get((dev, s))
-            if ws is None:
-                ws = _stream_ws[(dev, s)] = Workspace(0, torch.device("cuda", dev))
-            status = _call_product(fn, size_fn, ref, ws, dev, s)
+        ws = _stream_ws.get((dev, s)) or _stream_ws.setdefault((dev, s), Workspace(0, torch.device("cuda", dev)))
+        status = _call_product(fn, size_fn, ref, ws, dev, s)
     else:
         if ws is None:
             ws = torch.empty(size_fn(ref), dtype=torch.uint8, device=torch.device("cuda", dev))
@@ -752,8 +769,8 @@ def get_device_error(workspace=None, stream=None) -> int:
         bits, workspace = code.value, _shared_default_ws()
         if workspace is None:
             return bits
-    ptr = workspace.ptr if isinstance(workspace, Workspace) else workspace.data_ptr()
-    _check(lib.smr_get_device_error(ptr, _stream_ptr(stream), ctypes.byref(code)))
+    buf = workspace.buf if isinstance(workspace, Workspace) else workspace
+    _check(lib.smr_get_device_error(buf.data_ptr(), _stream_ptr(stream), ctypes.byref(code)))
     return bits | code.value
 
 
@@ -765,8 +782,8 @@ def clear_device_error(workspace=None, stream=None) -> None:
         workspace = _shared_default_ws()
         if workspace is None:
             return
-    ptr = workspace.ptr if isinstance(workspace, Workspace) else workspace.data_ptr()
-    _check(lib.smr_clear_device_error(ptr, _stream_ptr(stream)))
+    buf = workspace.buf if isinstance(workspace, Workspace) else workspace
+    _check(lib.smr_clear_device_error(buf.data_ptr(), _stream_ptr(stream)))
 
 
 def get_static_device_error(stream=None) -> int:

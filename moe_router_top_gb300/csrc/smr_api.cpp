@@ -18,6 +18,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -80,6 +81,14 @@ smr_status check_device() {
         return SMR_ERR_DEVICE;
     }
     return SMR_OK;
+}
+
+// Held while a call makes its launches: a call of another thread with the same
+// workspace and stream must not land between them (it would write over what
+// the first launch left for the second). Workspaces share 64 locks.
+std::mutex &launch_lock(const void *workspace) {
+    static std::mutex locks[64];
+    return locks[(reinterpret_cast<uintptr_t>(workspace) / kWsAlign) * 0x9E3779B97F4A7C15ull >> 58];
 }
 
 // Failure-injection hook (smr_test_force_wait_timeout), process-wide.
@@ -549,6 +558,7 @@ SMR_API smr_status smr_route(const smr_route_args *args, void *workspace, size_t
     smr_status st = check_ws(workspace, workspace_bytes, smr_route_workspace_size(args), "smr_route");
     if (st != SMR_OK) return st;
     if ((st = check_device()) != SMR_OK) return st;
+    const std::lock_guard<std::mutex> together(launch_lock(workspace));
     int launches = 0;
     st = run_route(args, workspace, static_cast<cudaStream_t>(stream), nullptr, &launches);
     if (st == SMR_OK) g_last_launches = launches;
@@ -568,6 +578,7 @@ SMR_API smr_status smr_align(const smr_align_args *args, void *workspace, size_t
     smr_status st = check_ws(workspace, workspace_bytes, smr_align_workspace_size(args), "smr_align");
     if (st != SMR_OK) return st;
     if ((st = check_device()) != SMR_OK) return st;
+    const std::lock_guard<std::mutex> together(launch_lock(workspace));
     smr::AlignLaunch L = make_align_launch(args, args->topk_ids, workspace, kHeaderBytes);
     cudaError_t e = smr::launch_align(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("align launch", e);
@@ -599,6 +610,7 @@ SMR_API smr_status smr_route_align(const smr_route_args *route, const smr_align_
     if (st != SMR_OK) return st;
     if ((st = check_device()) != SMR_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const std::lock_guard<std::mutex> together(launch_lock(workspace));
     int launches = 0;
     if (route->M >= 1 && route->M <= smr::kSmallMaxM && !has_eplb(&al)) {
         st = run_route(route, workspace, s, &al, &launches);
@@ -792,6 +804,7 @@ SMR_API smr_status smr_expert_down(const smr_expert_down_args *a, void *workspac
     smr::FfnLaunch L = ffn_launch(c, workspace);
     L.out = static_cast<uint8_t *>(workspace) + kDownRowsOffset;
     L.out32 = down_rows_fp32(a);
+    const std::lock_guard<std::mutex> together(launch_lock(workspace));
     cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("expert down launch", e);
     const smr::CombineLaunch cl{L.out, L.out32, a->topk_ids, a->topk_weights, static_cast<uint16_t *>(a->out),

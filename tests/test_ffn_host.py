@@ -4,6 +4,8 @@ the calls that launch nothing, and the Python layer's argument checks."""
 from __future__ import annotations
 
 import ctypes
+import os
+import subprocess
 import threading
 import time
 import types
@@ -443,3 +445,45 @@ def test_memory_of_a_capture_is_kept(smr, captured_device):
 def test_expert_error_word_refusals(lib):
     assert lib.smr_get_expert_error(None, None) == INVALID
     assert "code_out is NULL" in lib.smr_last_error().decode()
+
+
+def test_launches_of_a_call_stay_together(tmp_path):
+    """Through the C interface, two threads, one workspace: every product is
+    followed by its own sum."""
+    from moe_router_top_gb300 import build
+    exe, here = tmp_path / "launch_order", os.path.dirname(__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(build.nvcc())), "include")
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-I" + build.INCLUDE, "-I" + build.CSRC, "-I" + cuda, "-o", str(exe),
+                           os.path.join(here, "launch_order.cpp"), os.path.join(build.CSRC, "smr_api.cpp"),
+                           "-Wl,--unresolved-symbols=ignore-all", "-lpthread"])
+    lines = subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout.split("\n")[:-1]
+    assert [ln.split()[0] for ln in lines] == ["product", "sum"] * 20
+    assert len({ln.split()[1] for ln in lines}) == 1
+
+
+def test_threads_on_one_workspace_take_turns(fake_device):
+    """A caller's workspace, like the ones that the layer keeps: no call's
+    launches between another's, and none on memory that has been replaced."""
+    smr, busy, bad = fake_device, [], []
+    ws = smr.Workspace(0, torch.device("cuda", 0))
+
+    def fn(ref, ptr, n, s):
+        busy.append(1)
+        bad.append(len(busy) > 1 or n != ws.buf.numel())
+        time.sleep(0.002)
+        bad.append(len(busy) > 1 or n != ws.buf.numel())
+        busy.pop()
+        return _lib.SMR_OK
+
+    def work(k):
+        for _ in range(10):
+            smr._run_product(fn, lambda ref: 1024, ExpertDownArgs(), ws, 0)
+            with smr._hold(ws, ws.device):
+                fn(None, *[smr._workspace(ws, 1024, ws.device, None)[i] for i in (0, 1)], 7)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(bad) == 160 and not any(bad)

@@ -769,3 +769,33 @@ def test_errors_without_a_workspace(smr):
     assert smr.get_device_error() == 1
     smr.clear_device_error()
     assert smr.get_device_error() == 0 and smr.get_device_error(ws) == 4
+
+
+def test_threads_with_one_workspace(smr):
+    """Four threads on the default stream with a workspace of the caller's that
+    has to grow; two of them route and align on it in between."""
+    import threading
+    cases = [_case(smr, T=T, seed=T) for T in (40, 300, 600, 900)]
+    refs = [_ffn(smr, c) for c in cases]
+    als = [tuple(t.clone() for t in smr.align(c[0], 7, 64)) for c in cases]
+    torch.cuda.synchronize()
+    ws, outs = smr.Workspace(256), [[] for _ in cases]
+
+    def work(k):
+        for _ in range(25):
+            al = smr.align(cases[k][0], 7, 64, workspace=ws) if k % 2 else cases[k][2]
+            outs[k].append((_ffn(smr, cases[k], workspace=ws)[1], al))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for got, ref, al in zip(outs, refs, als):
+        assert len(got) == 25
+        n = int(al[2])
+        for out, a in got:
+            assert torch.equal(out, ref[1])
+            assert int(a[2]) == n and torch.equal(a[0][:n], al[0][:n]) and torch.equal(a[1][: n // 64], al[1][: n // 64])
+    assert smr.get_device_error(ws) == 0
