@@ -86,6 +86,16 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void *p) {
     return r;
 }
 
+// The same for data that a kernel before this one may still be writing when
+// this one starts (a programmatic launch): not through the read-only path,
+// which promises that nobody writes while the kernel runs.
+__device__ __forceinline__ uint4 ld_stream_rows_v4(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+
 __device__ __forceinline__ void set_error(uint32_t *err, uint32_t bits) {
     if (err) atomicOr(err, bits);
 }

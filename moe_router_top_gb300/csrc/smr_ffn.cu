@@ -985,10 +985,10 @@ expert_combine_kernel(const void *__restrict__ y, const int32_t *__restrict__ id
                 const uint8_t *from = row + (int64_t)(s0 + at) * next;
                 if (at >= 0 && f < H) {
                     if constexpr (Y32) {
-                        x[2 * j] = ld_stream_v4(from);
-                        x[2 * j + 1] = ld_stream_v4(from + 16);
+                        x[2 * j] = ld_stream_rows_v4(from);
+                        x[2 * j + 1] = ld_stream_rows_v4(from + 16);
                     } else {
-                        x[j] = ld_stream_v4(from);
+                        x[j] = ld_stream_rows_v4(from);
                     }
                 }
                 n += at >= 0;

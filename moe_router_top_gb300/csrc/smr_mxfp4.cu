@@ -42,7 +42,7 @@ quantize_mxfp4_kernel(const uint16_t *__restrict__ x, int64_t ld, uint32_t vecs_
         const uint32_t i = first + j * kMxThreads;
         // rows without a gap between them are one long row
         const uint32_t row = vecs_per_row ? i / vecs_per_row : 0u;
-        v[j] = i < vecs ? ld_stream_v4(x + (int64_t)row * ld + (int64_t)(i - row * vecs_per_row) * 8)
+        v[j] = i < vecs ? ld_stream_rows_v4(x + (int64_t)row * ld + (int64_t)(i - row * vecs_per_row) * 8)
                         : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
@@ -128,7 +128,7 @@ dequantize_mxfp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__rest
 // u * I + 64 * tile + 16 g + i. Rows past the end: zero bytes (their weights
 // are read as zeros). Run once per weight; one thread per 4 bytes.
 __global__ void __launch_bounds__(kMxThreads)
-tile_mxfp4_scales_kernel(const uint32_t *__restrict__ scales, int N, int chunks, int ntiles, int gated,
+tile_mxfp4_scales_kernel(const uint32_t *scales, int N, int chunks, int ntiles, int gated,
                          int64_t words, uint32_t *__restrict__ tiled) {
     griddep_wait();
     griddep_launch_dependents();
@@ -150,7 +150,7 @@ tile_mxfp4_scales_kernel(const uint32_t *__restrict__ scales, int N, int chunks,
         row = (int64_t)t * 128 + r;
         ok = row < N;
     }
-    tiled[at] = ok ? scales[(e * N + row) * chunks + c] : 0u;
+    tiled[at] = ok ? __ldcg(scales + (e * N + row) * chunks + c) : 0u;  // (may come from the kernel before)
 }
 
 template <typename... P, typename... Q>

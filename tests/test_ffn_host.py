@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import re
 import subprocess
 import threading
 import time
@@ -487,3 +488,22 @@ def test_threads_on_one_workspace_take_turns(fake_device):
     for t in threads:
         t.join()
     assert len(bad) == 160 and not any(bad)
+
+
+def test_no_read_only_loads_behind_a_programmatic_launch():
+    """The experts' and MXFP4 kernels start while the kernel before them may
+    still write what they read (the product's rows, the values to quantise,
+    fresh scales): none of it may come through the read-only path."""
+    from moe_router_top_gb300 import build
+    for name in ("smr_ffn.cu", "smr_mxfp4.cu"):
+        text = open(os.path.join(build.CSRC, name)).read()
+        code = re.sub(r"//[^\n]*", "", text)
+        for bad in (".nc", "ld_stream_v4", "__ldg"):
+            assert bad not in code, (name, bad)
+        # a plain load through a const restrict pointer may become one as well
+        kernels = re.findall(r"__global__.*?\n}\n", code, re.S)
+        assert kernels
+        for kernel in kernels:
+            head, body = kernel.split("{", 1)
+            for ptr in re.findall(r"const (?:uint\w+|int\w+|float) \*__restrict__ (\w+)", head):
+                assert not re.search(rf"\b{ptr}\[", body), (name, ptr)
