@@ -808,7 +808,7 @@ SMR_API smr_status smr_expert_down(const smr_expert_down_args *a, void *workspac
     cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("expert down launch", e);
     const smr::CombineLaunch cl{L.out, L.out32, a->topk_ids, a->topk_weights, static_cast<uint16_t *>(a->out),
-                                a->num_tokens, a->width, a->H, a->num_logical, a->num_experts};
+                                a->num_tokens, a->width, a->H, a->num_logical};
     e = smr::launch_expert_combine(cl, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("expert combine launch", e);
     g_last_launches = 2;

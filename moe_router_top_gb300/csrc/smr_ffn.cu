@@ -948,14 +948,18 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
 // still runs.
 // Y32: y is fp32, else bf16 (half the bytes, one more rounding of each term:
 // the error against 64 bits grows from 0.0017 to 0.0024 of the result).
-// Threads of a block: 128 where a block of 256 would not fit beside a CTA of
-// the product (pairs leave 12000 registers free) and for fp32 rows (few tokens:
-// more blocks), else 256: the whole second product in us with 128 and 256, one
-// token 9.95 and 10.4, 8 tokens in MXFP4 20.1 and 20.6, 2048 tokens 91.2 and
-// 92.0 (128 experts), 512 tokens 80.9 and 79.8.
-constexpr int kCombineThreads = 256;
+// Blocks of 128 threads fit beside a CTA of every variant of the product, so
+// that they are resident before it ends (pairs in MXFP4 leave 11776 of 65536
+// registers, blocks of 128 rows and pairs in bf16 13312: 256 threads of 64 do
+// not fit there). The whole second product in us with 128 and 256: one token
+// 9.95 and 10.4, 8 tokens in MXFP4 20.1 and 20.6, 700 tokens in blocks of 64
+// rows 74.8 and 75.3, of 128 rows 74.3 and 74.6 (MXFP4 28.3 and 28.6), 2000
+// tokens over 512 experts of 4096 features 422 and 424 (MXFP4 171 and 172).
+// (The kernel is compiled for 256 threads: for 128 the compiler keeps fewer of
+// the fp32 rows' loads ahead, 512 tokens 88.0 us instead of 86.4.)
+constexpr int kCombineThreads = 128;
 template <bool Y32>
-__global__ void __launch_bounds__(kCombineThreads)
+__global__ void __launch_bounds__(2 * kCombineThreads)
 expert_combine_kernel(const void *__restrict__ y, const int32_t *__restrict__ ids, const float *__restrict__ wts,
                       uint16_t *__restrict__ out, int parts, int width, int H, int num_logical) {
     griddep_launch_dependents();
@@ -1189,9 +1193,7 @@ cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream) {
-    const bool narrow = a.y32 || use_pairs((int64_t)a.T * a.width, a.num_experts);
-    const int most = narrow ? kCombineThreads / 2 : kCombineThreads;
-    const int vecs = a.H / 8, threads = vecs < most ? (vecs + 31) / 32 * 32 : most;
+    const int vecs = a.H / 8, threads = vecs < kCombineThreads ? (vecs + 31) / 32 * 32 : kCombineThreads;
     const int parts = (vecs + threads - 1) / threads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.T * (unsigned)parts, 1, 1);

@@ -207,7 +207,7 @@ struct CombineLaunch {
     const int32_t *ids;      // [T][width]
     const float *wts;
     uint16_t *out;           // bf16 [T][H]
-    int T, width, H, num_logical, num_experts;
+    int T, width, H, num_logical;
 };
 cudaError_t launch_expert_combine(const CombineLaunch &a, cudaStream_t stream);
 

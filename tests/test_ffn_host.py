@@ -507,3 +507,29 @@ def test_no_read_only_loads_behind_a_programmatic_launch():
             head, body = kernel.split("{", 1)
             for ptr in re.findall(r"const (?:uint\w+|int\w+|float) \*__restrict__ (\w+)", head):
                 assert not re.search(rf"\b{ptr}\[", body), (name, ptr)
+
+
+def test_blocks_of_the_sum_fit_beside_the_product(tmp_path):
+    """By the compiler's register counts: a block of the sum fits on an SM
+    that holds a CTA of the product whose rows it waits for, in every variant."""
+    from moe_router_top_gb300 import build
+    out = subprocess.run([build.nvcc()] + build.ARCH + build.FLAGS + ["-Xptxas", "-v", "-c", os.path.join(build.CSRC, "smr_ffn.cu"),
+                         "-o", str(tmp_path / "ffn.o")], check=True, capture_output=True, text=True)
+    used = dict(re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", out.stdout + out.stderr, re.S))
+    source = open(os.path.join(build.CSRC, "smr_ffn.cu")).read()
+    threads = int(re.search(r"kCombineThreads = (\d+);", source).group(1))
+
+    def alloc(name, threads):  # registers are handed out to warps in units of 8 a thread
+        return -(-int(used[name]) // 8) * 8 * threads
+
+    combine = {f: next(n for n in used if f"expert_combine_kernelILb{f}" in n) for f in (0, 1)}
+    seen = 0
+    for name in used:
+        m = re.search(r"expert_ffn_kernelILb(\d)ELb0ELb(\d)ELi(\d)ELb(\d)E", name)  # (MX, not gated, PAIR, SUB, F32)
+        if not m:
+            continue
+        mx, pair, sub, f32 = map(int, m.groups())
+        seen += 1
+        product, block = alloc(name, 480 if sub == 2 else 544), alloc(combine[f32], threads)
+        assert product + block <= 65536, (name, product, block)
+    assert seen >= 10
