@@ -464,6 +464,8 @@ def _elsewhere(dev: int, stream):
         return None if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"stream must be on the operands' device, cuda:{dev} (got {stream.device})")
     return torch.cuda.stream(stream)
 
 

@@ -533,3 +533,15 @@ def test_blocks_of_the_sum_fit_beside_the_product(tmp_path):
         product, block = alloc(name, 480 if sub == 2 else 544), alloc(combine[f32], threads)
         assert product + block <= 65536, (name, product, block)
     assert seen >= 10
+
+
+def test_streams_of_another_device_are_refused(smr, monkeypatch):
+    """Not taken for the operands' device's current stream."""
+    entered = []
+    cuda = types.SimpleNamespace(stream=lambda s: entered.append(s) or "context", ExternalStream=lambda p, device: (p, device))
+    monkeypatch.setattr(smr, "_torch_module", types.SimpleNamespace(cuda=cuda))
+    other, same = (types.SimpleNamespace(device=torch.device("cuda", i)) for i in (1, 0))
+    with pytest.raises(ValueError, match="stream must be on the operands' device, cuda:0"):
+        smr._elsewhere(0, other)
+    assert entered == []
+    assert smr._elsewhere(0, same) == "context" and smr._elsewhere(0, 7) == "context" and entered == [same, (7, 0)]
