@@ -470,6 +470,13 @@ def _elsewhere(dev: int, stream):
 
 
 _stream_ws = {}
+_PER_THREAD_STREAM = 2  # the handle by which every thread names a default stream of its own
+
+
+def _stream_workspace(dev: int, s: int) -> Workspace:
+    """The workspace of calls on a stream that were given none."""
+    key = (dev, s) if s != _PER_THREAD_STREAM else (dev, s, threading.get_ident())
+    return _stream_ws.get(key) or _stream_ws.setdefault(key, Workspace(0, _torch().device("cuda", dev)))
 
 
 def _check_sizes(bits: int) -> None:
@@ -514,8 +521,7 @@ def _run_product(fn, size_fn, args, ws, dev: int) -> None:
     if isinstance(ws, Workspace):
         status = _call_product(fn, size_fn, ref, ws, dev, s)
     elif ws is None and not torch._C._cuda_isCurrentStreamCapturing():
-        ws = _stream_ws.get((dev, s)) or _stream_ws.setdefault((dev, s), Workspace(0, torch.device("cuda", dev)))
-        status = _call_product(fn, size_fn, ref, ws, dev, s)
+        status = _call_product(fn, size_fn, ref, _stream_workspace(dev, s), dev, s)
     else:
         if ws is None:
             ws = torch.empty(size_fn(ref), dtype=torch.uint8, device=torch.device("cuda", dev))

@@ -545,3 +545,32 @@ def test_streams_of_another_device_are_refused(smr, monkeypatch):
         smr._elsewhere(0, other)
     assert entered == []
     assert smr._elsewhere(0, same) == "context" and smr._elsewhere(0, 7) == "context" and entered == [same, (7, 0)]
+
+
+def test_every_stream_has_a_workspace_of_its_own(fake_device, monkeypatch):
+    """Also where threads name different streams by one handle, their own default streams."""
+    smr, stream = fake_device, []
+    monkeypatch.setattr(smr._torch_module._C, "_cuda_getCurrentRawStream", lambda dev: stream[-1])
+
+    def call():
+        smr._run_product(lambda *a: _lib.SMR_OK, lambda ref: 1024, ExpertDownArgs(), None, 0)
+
+    for s in (7, 9, 7, 0):
+        stream.append(s)
+        call()
+    assert len(smr._stream_ws) == 3 and len({id(w.buf) for w in smr._stream_ws.values()}) == 3
+    stream.append(2)
+    gate = threading.Barrier(3)
+
+    def work():
+        gate.wait()  # (three threads at a time: idents are not reused)
+        call()
+        call()
+        gate.wait()
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(smr._stream_ws) == 6
