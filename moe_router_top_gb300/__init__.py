@@ -25,7 +25,7 @@ __all__ = [
     "dequantize_mxfp4", "tile_mxfp4_scales",
     "select_block_size", "align_capacity", "route_workspace_size", "align_workspace_size",
     "route_align_workspace_size", "get_device_error", "clear_device_error",
-    "get_static_device_error", "clear_static_device_error", "test_force_wait_timeout",
+    "get_static_device_error", "clear_static_device_error", "release_workspaces", "test_force_wait_timeout",
     "last_launch_count", "version",
 ]
 
@@ -477,6 +477,15 @@ def _stream_workspace(dev: int, s: int) -> Workspace:
     """The workspace of calls on a stream that were given none."""
     key = (dev, s) if s != _PER_THREAD_STREAM else (dev, s, threading.get_ident())
     return _stream_ws.get(key) or _stream_ws.setdefault(key, Workspace(0, _torch().device("cuda", dev)))
+
+
+def release_workspaces() -> None:
+    """Gives back the memory that expert_up and expert_down keep, per stream,
+    for calls without a workspace (as much as the largest such call took; work
+    that is queued on it is not disturbed). Later calls take new memory. To be
+    called, too, before a stream that torch did not make is destroyed and once
+    its work is done: another one may get its handle."""
+    _stream_ws.clear()
 
 
 def _check_sizes(bits: int) -> None:

@@ -574,3 +574,15 @@ def test_every_stream_has_a_workspace_of_its_own(fake_device, monkeypatch):
     for t in threads:
         t.join()
     assert len(smr._stream_ws) == 6
+
+
+def test_kept_workspaces_can_be_released(fake_device):
+    smr = fake_device
+    sizes = []
+    for need in (4096, 512):
+        smr._run_product(lambda ref, ptr, n, s: sizes.append(n) or _lib.SMR_OK, lambda ref: need, ExpertDownArgs(), None, 0)
+        kept = weakref.ref(next(iter(smr._stream_ws.values())).buf)
+        assert kept() is not None
+        smr.release_workspaces()
+        assert kept() is None and smr._stream_ws == {}
+    assert sizes == [4096, 512]

@@ -799,3 +799,24 @@ def test_threads_with_one_workspace(smr):
             assert torch.equal(out, ref[1])
             assert int(a[2]) == n and torch.equal(a[0][:n], al[0][:n]) and torch.equal(a[1][: n // 64], al[1][: n // 64])
     assert smr.get_device_error(ws) == 0
+
+
+def test_released_workspaces(smr):
+    """The memory goes back, and what was queued on it still comes out right."""
+    c = _case(smr, T=5000, H=1024, I=128)
+    ref = _ffn(smr, c)
+    smr.release_workspaces()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    for _ in range(5):
+        out = _ffn(smr, c)
+        smr.release_workspaces()
+        torch.full((32 << 20,), 7, dtype=torch.uint8, device="cuda")  # (may take the memory over, in order)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+    del out
+    assert torch.cuda.memory_allocated() == before
+    assert smr.expert_down(ref[0], c[5], c[0], c[1], *c[2], block_size=64).shape == ref[1].shape
+    assert torch.cuda.memory_allocated() - before > 5000 * 3 * 1024 * 2
+    smr.release_workspaces()
