@@ -503,7 +503,7 @@ def _check_buffer(ws, dev: int) -> None:
         raise ValueError("workspace must be contiguous")
 
 
-def _call_product(fn, size_fn, ref, ws, dev: int, s: int) -> int:
+def _call_product(fn, size_fn, ref, ws, dev: int, s: int, capturing: bool) -> int:
     """One call on a Workspace. One that is too small is refused before any
     launch; it grows and the call is made again."""
     with ws.lock:
@@ -511,7 +511,7 @@ def _call_product(fn, size_fn, ref, ws, dev: int, s: int) -> int:
         status = _lib.SMR_ERR_WORKSPACE
         if buf is not None:
             _check_buffer(buf, dev)
-            ws.ensure(0)  # (marks what a capture uses)
+            ws._captured |= capturing
             status = fn(ref, buf.data_ptr(), buf.numel(), s)
         if status == _lib.SMR_ERR_WORKSPACE:
             buf = ws.ensure(size_fn(ref))
@@ -526,11 +526,11 @@ def _run_product(fn, size_fn, args, ws, dev: int) -> None:
     gets a workspace of its own, which its graph keeps and zeroes itself."""
     torch = _torch()
     ref = ctypes.byref(args)
-    s = torch._C._cuda_getCurrentRawStream(dev)
+    s, capturing = torch._C._cuda_getCurrentRawStream(dev), torch._C._cuda_isCurrentStreamCapturing()
     if isinstance(ws, Workspace):
-        status = _call_product(fn, size_fn, ref, ws, dev, s)
-    elif ws is None and not torch._C._cuda_isCurrentStreamCapturing():
-        status = _call_product(fn, size_fn, ref, _stream_workspace(dev, s), dev, s)
+        status = _call_product(fn, size_fn, ref, ws, dev, s, capturing)
+    elif ws is None and not capturing:
+        status = _call_product(fn, size_fn, ref, _stream_workspace(dev, s), dev, s, False)
     else:
         if ws is None:
             ws = torch.empty(size_fn(ref), dtype=torch.uint8, device=torch.device("cuda", dev))
