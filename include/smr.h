@@ -204,9 +204,10 @@ typedef struct smr_expert_up_args {
 
 /* The experts' second product and the weighted sum over a token's slots:
  * y[i] = x[i] . w[e(i)]^T (fp32 accumulation), out[t] = sum over s, in order,
- * of topk_weights[t, s] * y[t * width + s], in fp32, rounded to bf16 once (y
- * waits in the workspace, in fp32 up to 2^23 values and 48 rows an expert,
- * else rounded to bf16). A slot whose topk_ids entry is outside [0,
+ * of topk_weights[t, s] * y[t * width + s], in fp32, rounded to bf16 once. y
+ * waits in the workspace: in fp32 up to 2^23 values and below 48 rows an expert
+ * on average, else rounded to bf16; smr_expert_down_fp32 keeps it in fp32
+ * whatever the batch, for a workspace and a traffic of y twice as large. A slot whose topk_ids entry is outside [0,
  * num_logical) contributes nothing; every other slot must have been aligned
  * (behind an EPLB remap that sends a logical expert to no physical one, which
  * the align flags, set its topk_ids entries to -1: without a row of y they
@@ -340,6 +341,9 @@ SMR_API smr_status smr_expert_up(const smr_expert_up_args *args, void *workspace
                                  void *stream);
 SMR_API smr_status smr_expert_down(const smr_expert_down_args *args, void *workspace, size_t workspace_bytes,
                                    void *stream);
+SMR_API size_t smr_expert_down_fp32_workspace_size(const smr_expert_down_args *args);
+SMR_API smr_status smr_expert_down_fp32(const smr_expert_down_args *args, void *workspace, size_t workspace_bytes,
+                                        void *stream);
 
 /* bf16 [rows, ld_x] to MXFP4 (row-major codes and scales), one launch. The
  * scale of a block is the smallest power of two with amax <= 6 * scale (2^-127

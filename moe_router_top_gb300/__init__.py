@@ -622,8 +622,8 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
 
 
 def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_tokens_post_padded, *,
-                block_size: int, num_logical: int = 0, x_scales=None, w_scales=None, out=None,
-                workspace=None, stream=None):
+                block_size: int, num_logical: int = 0, fp32_rows: bool = False, x_scales=None,
+                w_scales=None, out=None, workspace=None, stream=None):
     """The experts' second product, summed per token: returns out bf16
     [num_tokens, H], out[t] = sum over s of topk_weights[t, s] * (x[t * width +
     s] . w[e]^T) for the slots' experts e; x bf16 [num_tokens * width, I] (the
@@ -631,7 +631,9 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     [num_tokens, width] as routed. With x_scales and w_scales, x and w are
     MXFP4 codes. A slot whose id is outside [0, num_logical) contributes
     nothing (num_logical: the experts that were aligned; num_experts if 0);
-    every other slot must have been aligned."""
+    every other slot must have been aligned. The products wait for the sum in
+    fp32 while they are few, else in bf16; fp32_rows=True keeps them in fp32
+    whatever the batch (smr_expert_down_fp32 in include/smr.h)."""
     _disabled()
     torch = _torch()
     lib = _lib.load()
@@ -656,14 +658,17 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     if ctx is not None:
         with ctx:
             return expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_tokens_post_padded,
-                               block_size=block_size, num_logical=num_logical, x_scales=x_scales,
-                               w_scales=w_scales, out=out, workspace=workspace)
+                               block_size=block_size, num_logical=num_logical, fp32_rows=fp32_rows,
+                               x_scales=x_scales, w_scales=w_scales, out=out, workspace=workspace)
     out = _output(out, (T,), H, torch.bfloat16, x)
     a = ExpertDownArgs(T, width, H, I, E, block_size, x.data_ptr(), _ptr(x_scales), w.data_ptr(), _ptr(w_scales),
                        topk_ids.data_ptr(), topk_weights.data_ptr(), num_logical if num_logical else E,
                        sorted_token_ids.data_ptr(), sorted_token_ids.numel(), expert_ids.data_ptr(),
                        num_tokens_post_padded.data_ptr(), out.data_ptr())
-    _run_product(lib.smr_expert_down, lib.smr_expert_down_workspace_size, a, workspace, dev)
+    if fp32_rows:
+        _run_product(lib.smr_expert_down_fp32, lib.smr_expert_down_fp32_workspace_size, a, workspace, dev)
+    else:
+        _run_product(lib.smr_expert_down, lib.smr_expert_down_workspace_size, a, workspace, dev)
     return out
 
 

@@ -30,7 +30,7 @@ EXPORTED = (
     "smr_expert_gemm", "smr_expert_up", "smr_expert_up_workspace_size", "smr_expert_down",
     "smr_expert_down_workspace_size", "smr_quantize_mxfp4", "smr_dequantize_mxfp4",
     "smr_mxfp4_tiled_scale_bytes", "smr_tile_mxfp4_scales",
-    "smr_get_expert_error", "smr_clear_expert_error",
+    "smr_expert_down_fp32", "smr_expert_down_fp32_workspace_size", "smr_get_expert_error", "smr_clear_expert_error",
 )
 
 SMR_STALL_NONE = 0
@@ -147,6 +147,8 @@ def load(path: str = LIB_PATH):
             "smr_expert_down_workspace_size": ([DA], sz),
             "smr_expert_up": ([UA, P, sz, P], ctypes.c_int),
             "smr_expert_down": ([DA, P, sz, P], ctypes.c_int),
+            "smr_expert_down_fp32": ([DA, P, sz, P], ctypes.c_int),
+            "smr_expert_down_fp32_workspace_size": ([DA], sz),
             "smr_quantize_mxfp4": ([P, i64, i32, i64, P, P, P], ctypes.c_int),
             "smr_dequantize_mxfp4": ([P, P, i64, i32, P, P], ctypes.c_int),
             "smr_mxfp4_tiled_scale_bytes": ([i32, i32, i32, i32], sz),

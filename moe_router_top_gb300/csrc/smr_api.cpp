@@ -739,18 +739,26 @@ SMR_API smr_status smr_expert_gemm(const smr_expert_gemm_args *a, void *workspac
 SMR_API size_t smr_expert_up_workspace_size(const smr_expert_up_args *args) { return args ? kHeaderBytes : 0; }
 
 // The rows between the product and the sum are fp32 as long as they are few
-// (they stay in L2, and rounding them would only cost precision), else bf16:
-// at 16384 tokens of 2048 features and 8 slots fp32 rows would be 1.07 GB more
-// to move, 160 us on top of 410.
+// (they stay in L2, and rounding them would only cost precision), else bf16
+// unless the caller asks for fp32: at 16384 tokens of 2048 features and 8 slots
+// fp32 rows are 1.07 GB more to move, 632 us instead of 391 (MXFP4 615 and 340;
+// 700 tokens 75 and 85, MXFP4 28 and 37).
 static bool down_rows_fp32(const smr_expert_down_args *a) {
     return smr::expert_rows_fp32((int64_t)a->num_tokens * a->width, a->num_experts, a->H);
 }
 
-SMR_API size_t smr_expert_down_workspace_size(const smr_expert_down_args *args) {
-    if (!args) return 0;
+static size_t down_workspace_size(const smr_expert_down_args *args, bool rows32) {
     if (args->num_tokens < 1 || args->width < 1 || args->H < 1) return kHeaderBytes;
     const size_t rows = (size_t)args->num_tokens * (size_t)args->width * (size_t)args->H;
-    return kDownRowsOffset + round_up(rows * (down_rows_fp32(args) ? 4 : 2), kWsAlign);
+    return kDownRowsOffset + round_up(rows * (rows32 ? 4 : 2), kWsAlign);
+}
+
+SMR_API size_t smr_expert_down_workspace_size(const smr_expert_down_args *args) {
+    return args ? down_workspace_size(args, down_rows_fp32(args)) : 0;
+}
+
+SMR_API size_t smr_expert_down_fp32_workspace_size(const smr_expert_down_args *args) {
+    return args ? down_workspace_size(args, true) : 0;
 }
 
 SMR_API smr_status smr_expert_up(const smr_expert_up_args *a, void *workspace, size_t workspace_bytes, void *stream) {
@@ -779,11 +787,11 @@ SMR_API smr_status smr_expert_up(const smr_expert_up_args *a, void *workspace, s
     return SMR_OK;
 }
 
-SMR_API smr_status smr_expert_down(const smr_expert_down_args *a, void *workspace, size_t workspace_bytes,
-                                   void *stream) {
+static smr_status run_expert_down(const char *what, const smr_expert_down_args *a, bool always_fp32, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
     g_last_launches = 0;
     if (!a) {
-        g_last_error = "smr_expert_down: args is NULL";
+        g_last_error = std::string(what) + ": args is NULL";
         return SMR_ERR_INVALID_ARG;
     }
     Reasons r;
@@ -796,14 +804,15 @@ SMR_API smr_status smr_expert_down(const smr_expert_down_args *a, void *workspac
         if (!a->topk_weights || !aligned(a->topk_weights, 4)) r.bad("topk_weights must be a 4-byte aligned pointer");
         if ((int64_t)a->num_tokens * a->H > (int64_t)1 << 34) r.unsup("num_tokens * H must be <= 2^34");
     }
-    if (!r.ok()) return r.finish("smr_expert_down");
+    if (!r.ok()) return r.finish(what);
     if (a->num_tokens == 0) return SMR_OK;
-    smr_status st = check_ws(workspace, workspace_bytes, smr_expert_down_workspace_size(a), "smr_expert_down");
+    const bool rows32 = always_fp32 || down_rows_fp32(a);
+    smr_status st = check_ws(workspace, workspace_bytes, down_workspace_size(a, rows32), what);
     if (st != SMR_OK) return st;
     if ((st = check_device()) != SMR_OK) return st;
     smr::FfnLaunch L = ffn_launch(c, workspace);
     L.out = static_cast<uint8_t *>(workspace) + kDownRowsOffset;
-    L.out32 = down_rows_fp32(a);
+    L.out32 = rows32;
     const std::lock_guard<std::mutex> together(launch_lock(workspace));
     cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("expert down launch", e);
@@ -813,6 +822,16 @@ SMR_API smr_status smr_expert_down(const smr_expert_down_args *a, void *workspac
     if (e != cudaSuccess) return cuda_fail("expert combine launch", e);
     g_last_launches = 2;
     return SMR_OK;
+}
+
+SMR_API smr_status smr_expert_down(const smr_expert_down_args *args, void *workspace, size_t workspace_bytes,
+                                   void *stream) {
+    return run_expert_down("smr_expert_down", args, false, workspace, workspace_bytes, stream);
+}
+
+SMR_API smr_status smr_expert_down_fp32(const smr_expert_down_args *args, void *workspace, size_t workspace_bytes,
+                                        void *stream) {
+    return run_expert_down("smr_expert_down_fp32", args, true, workspace, workspace_bytes, stream);
 }
 
 SMR_API smr_status smr_quantize_mxfp4(const void *x, int64_t rows, int32_t K, int64_t ld_x, uint8_t *codes,

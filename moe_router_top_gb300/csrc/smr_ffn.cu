@@ -947,7 +947,8 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
 // grid start only after it waited for them: they are read while the product
 // still runs.
 // Y32: y is fp32, else bf16 (half the bytes, one more rounding of each term:
-// the error against 64 bits grows from 0.0017 to 0.0024 of the result).
+// the error against 64 bits grows from 0.0017 to 0.0024 of the result; a caller
+// can have fp32 rows at any number of them).
 // Blocks of 128 threads fit beside a CTA of every variant of the product, so
 // that they are resident before it ends (pairs in MXFP4 leave 11776 of 65536
 // registers, blocks of 128 rows and pairs in bf16 13312: 256 threads of 64 do
@@ -1034,7 +1035,8 @@ expert_combine_kernel(const void *__restrict__ y, const int32_t *__restrict__ id
 constexpr int kPairRows = 48;
 static bool use_pairs(int64_t numel, int num_experts) { return numel >= (int64_t)kPairRows * num_experts; }
 
-// Few enough to stay in L2 (32 MB); pairs of CTAs write bf16 rows only.
+// Few enough to stay in L2 (32 MB), and no more than a pair's worth of rows an
+// expert (see smr_expert_down_workspace_size for what more of them cost).
 bool expert_rows_fp32(int64_t numel, int num_experts, int H) {
     return numel * H <= (int64_t)1 << 23 && !use_pairs(numel, num_experts);
 }
@@ -1176,7 +1178,10 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
 
 template <bool MX, bool UP>
 static cudaError_t launch_format(const FfnLaunch &a, int sms, cudaStream_t stream) {
-    if (use_pairs(a.numel, a.num_experts)) return launch_product<MX, UP, true, MX ? 2 : 1>(a, sms, stream);
+    const bool pairs = use_pairs(a.numel, a.num_experts);
+    if constexpr (!UP)
+        if (a.out32 && pairs) return launch_product<MX, UP, true, MX ? 2 : 1, true>(a, sms, stream);
+    if (pairs) return launch_product<MX, UP, true, MX ? 2 : 1>(a, sms, stream);
     if constexpr (!UP)
         if (a.out32)
             return a.A == 64 ? launch_product<MX, UP, false, 2, true>(a, sms, stream)

@@ -190,10 +190,11 @@ struct FfnLaunch {
     int64_t numel, sorted_cap;
     const int32_t *sorted, *eids, *npp;
     void *out;
-    bool out32;              // (not gated, as expert_rows_fp32 says) out is fp32
+    bool out32;              // (not gated) out is fp32
     void *hdr;               // workspace header (sticky error word)
 };
-// Whether the rows between the second product and the sum are fp32 (out32).
+// Whether the rows between the second product and the sum are fp32 (out32)
+// where the caller leaves it open.
 bool expert_rows_fp32(int64_t numel, int num_experts, int H);
 cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream);
 // The word on the current device that gets every product's error bits.

@@ -586,3 +586,17 @@ def test_kept_workspaces_can_be_released(fake_device):
         smr.release_workspaces()
         assert kept() is None and smr._stream_ws == {}
     assert sizes == [4096, 512]
+
+
+def test_fp32_rows(lib):
+    size, size32 = lib.smr_expert_down_workspace_size, lib.smr_expert_down_fp32_workspace_size
+    few, many = _down(), _down(num_tokens=4096)
+    assert size32(ctypes.byref(few)) == size(ctypes.byref(few))  # fp32 anyway
+    need = 256 + 16 * 1024 * 8 + 4096 * 11 * 256 * 4
+    assert size32(ctypes.byref(many)) == need
+    assert lib.smr_expert_down_fp32(ctypes.byref(many), P, need - 1, None) == WORKSPACE
+    assert "smr_expert_down_fp32" in lib.smr_last_error().decode()
+    assert lib.smr_expert_down_fp32(None, P, need, None) == INVALID and size32(None) == 0
+    _refused(lib, lib.smr_expert_down_fp32, _down(num_logical=0), INVALID, "smr_expert_down_fp32", "num_logical must be in")
+    empty = ExpertDownArgs(0, 1, 16, 16, 1, 64, num_logical=1)
+    assert lib.smr_expert_down_fp32(ctypes.byref(empty), None, 0, None) == _lib.SMR_OK

@@ -820,3 +820,47 @@ def test_released_workspaces(smr):
     assert smr.expert_down(ref[0], c[5], c[0], c[1], *c[2], block_size=64).shape == ref[1].shape
     assert torch.cuda.memory_allocated() - before > 5000 * 3 * 1024 * 2
     smr.release_workspaces()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T,H,I,E,S,k,A,zipf", [
+    (20, 272, 256, 3, 0, 2, 64, 0.0),       # fp32 rows anyway
+    (700, 4096, 128, 64, 0, 4, 64, 0.0),    # single CTAs, above 2^23 values
+    (700, 4096, 128, 64, 0, 4, 128, 1.1),
+    (2000, 384, 384, 5, 1, 2, 64, 0.0),     # pairs
+    (1500, 640, 256, 4, 0, 2, 128, 1.1),
+    (3000, 400, 128, 4, 1, 1, 64, 1.1),     # pairs, partial tiles, an odd number of them
+])
+def test_down_with_fp32_rows(smr, mx, T, H, I, E, S, k, A, zipf):
+    """Without the rounding of the rows: |do| <= sum_s |w_s| c ad_s (1 + u) +
+    width 2^-24 sum_s |w_s y_s| + u |o| + 2^-134."""
+    ids, wts, g = _routing(T, E, k, S, zipf, 71 + T)
+    al = smr.align(ids, E + S, A)
+    x, w = _normal(g, T * (k + S), I), _normal(g, E + S, H, I, std=I ** -0.5)
+    xa, kw, xv = _values(smr, x, mx)
+    wa, wv = w, w.double()
+    if mx:
+        wa, kw["w_scales"], wv = _weights_mx(smr, w, False)
+    ws = smr.Workspace(256)
+    out = smr.expert_down(xa, wa, ids, wts, *al, block_size=A, fp32_rows=True, workspace=ws, **kw)
+    assert smr.get_device_error(ws) == 0 and smr.last_launch_count() == 2
+    assert ws.nbytes >= 4 * T * (k + S) * H
+    ref, _ = _ref_down(xv, wv, ids, wts)
+    c = 2.0 * (I // 16 + 32) * 2.0 ** -24
+    y, ad = torch.zeros(T * (k + S), H, dtype=torch.float64, device="cuda"), torch.zeros(T * (k + S), H, dtype=torch.float64, device="cuda")
+    flat = ids.reshape(-1)
+    for e in torch.unique(flat).tolist():
+        i = torch.nonzero(flat == e).squeeze(1)
+        y[i], ad[i] = xv[i] @ wv[e].T, xv[i].abs() @ wv[e].abs().T
+    wt = wts.double()[:, :, None].abs()
+    tol = (wt * c * ad.view(T, k + S, H)).sum(1) * (1 + U) + (k + S) * 2.0 ** -24 * (wt * y.abs().view(T, k + S, H)).sum(1)
+    _close(out, ref, tol + U * ref.abs() + TINY)
+    again = smr.expert_down(xa, wa, ids, wts, *al, block_size=A, fp32_rows=True, workspace=ws, **kw)
+    assert torch.equal(out, again)
+    if T == 20:
+        assert torch.equal(out, smr.expert_down(xa, wa, ids, wts, *al, block_size=A, **kw))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    there = smr.expert_down(xa, wa, ids, wts, *al, block_size=A, fp32_rows=True, stream=s, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out, there)
