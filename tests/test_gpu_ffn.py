@@ -864,3 +864,179 @@ def test_down_with_fp32_rows(smr, mx, T, H, I, E, S, k, A, zipf):
     there = smr.expert_down(xa, wa, ids, wts, *al, block_size=A, fp32_rows=True, stream=s, **kw)
     torch.cuda.synchronize()
     assert torch.equal(out, there)
+
+
+def _operands(smr, x, w13, mx):
+    """expert_up's operands and their 64-bit values."""
+    xa, kw, xv = _values(smr, x, mx)
+    if not mx:
+        return xa, w13, kw, xv, w13.double()
+    w, kw["w_scales"], wv = _weights_mx(smr, w13, True)
+    return xa, w, kw, xv, wv
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("A", [64, 128])
+def test_pairs_skipped_slots(smr, A, mx):
+    """As test_skipped_slots, with enough rows an expert for CTA pairs."""
+    ids, wts, _, x, w13, w2 = _case(smr, T=700)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(A)
+    ids = torch.where(torch.rand(ids.shape, device="cuda", generator=g) < 0.1, torch.full_like(ids, -1), ids)
+    ids[20], ids[31, 0], ids[ids == 4] = 7, 1 << 20, -3  # a token without any, an expert without a row
+    ws = smr.Workspace(256)
+    al = smr.align(ids, 7, A, workspace=ws)
+    assert smr.get_device_error(ws) == 1
+    smr.clear_device_error(ws)
+    xa, w, kw, xv, wv = _operands(smr, x, w13, mx)
+    out = torch.full((2100, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    smr.expert_up(xa, w, *al, width=3, block_size=A, out=out, workspace=ws, **kw)
+    gone = ((ids < 0) | (ids >= 7)).reshape(-1)
+    assert (out[gone] == 5.0).all() and int((~gone).sum()) >= 48 * 7
+    ref, tol = _ref_up(xv, wv, ids, 3)
+    _close(out[~gone], ref[~gone], tol[~gone])
+    y, kd, yv = _values(smr, torch.where(gone[:, None], torch.zeros_like(out), out), mx)
+    wd, wdv = w2, w2.double()
+    if mx:
+        wd, kd["w_scales"], wdv = _weights_mx(smr, w2, False)
+    ref, tol = _ref_down(yv, wdv, ids, wts)
+    for fp32_rows in (False, True):
+        z = smr.expert_down(y, wd, ids, wts, *al, block_size=A, fp32_rows=fp32_rows, workspace=ws, **kd)
+        _close(z, ref, tol)
+        assert (z[20] == 0).all()
+    assert smr.get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("A", [64, 128])
+def test_pairs_remapped_experts(smr, A, mx):
+    ids, wts, _, x, w13, w2 = _case(smr, T=1200, E=6, S=0)
+    phys = torch.tensor([[0, 7], [1, 1], [2, 8], [3, 3], [4, 4], [5, 6]], dtype=torch.int32, device="cuda")
+    count = torch.tensor([2, 1, 2, 1, 1, 2], dtype=torch.int32, device="cuda")
+    al = smr.align(ids, 6, A, eplb_map=phys, eplb_count=count, num_physical=9)
+    logical = torch.tensor([0, 1, 2, 3, 4, 5, 5, 0, 2], device="cuda")
+    xa, w, kw, xv, _ = _operands(smr, x, w13[logical].contiguous(), mx)
+    act = smr.expert_up(xa, w, *al, width=2, block_size=A, **kw)
+    _close(act, *_ref_up(xv, _mx_exact(w13)[2] if mx else w13.double(), ids, 2))
+    y, kd, yv = _values(smr, act, mx)
+    wd, wdv = w2[logical].contiguous(), w2.double()
+    if mx:
+        wd, kd["w_scales"] = _laid_out(smr, wd, False)
+        wdv = _mx_exact(w2)[2]
+    out = smr.expert_down(y, wd, ids, wts, *al, block_size=A, num_logical=6, **kd)
+    _close(out, *_ref_down(yv, wdv, ids, wts))
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("A", [64, 128])
+def test_pairs_corrupted_align_outputs(smr, A, mx):
+    """As test_corrupted_align_outputs, with CTA pairs: a bad entry or owner
+    costs its own row or block, also in the middle of a group of blocks."""
+    ids, wts, _, x, w13, w2 = _case(smr, T=900)
+    al = smr.align(ids, 7, A)
+    n = int(al[2])
+    xa, w, kw, xv, wv = _operands(smr, x, w13, mx)
+    good = smr.expert_up(xa, w, *al, width=3, block_size=A, **kw)
+    _close(good, *_ref_up(xv, wv, ids, 3))
+    srt, eids, npp = (t.clone() for t in al)
+    real = torch.nonzero(al[0][:n] < 2700).flatten()
+    hit = real[torch.tensor([1, 700, 1300, 2699], device="cuda")]
+    lost = al[0][hit].long()
+    srt[hit] = torch.tensor([1 << 29, -5, 2701, -(1 << 31)], dtype=torch.int32, device="cuda")
+    ws = smr.Workspace(256)
+    out = torch.zeros_like(good)
+    smr.expert_up(xa, w, srt, eids, npp, width=3, block_size=A, out=out, workspace=ws, **kw)
+    assert smr.get_device_error(ws) == 4
+    keep = torch.ones(2700, dtype=torch.bool, device="cuda")
+    keep[lost] = False
+    assert torch.equal(out[keep], good[keep]) and (out[lost] == 0).all()
+    for block, owner in ((0, 7), (1, -1), (n // A - 1, 1 << 30)):
+        bad = eids.clone()
+        bad[block] = owner
+        ws = smr.Workspace(256)
+        out = torch.zeros_like(good)
+        smr.expert_up(xa, w, al[0], bad, npp, width=3, block_size=A, out=out, workspace=ws, **kw)
+        assert smr.get_device_error(ws) == 1
+        rows = al[0][block * A:(block + 1) * A].long()
+        keep = torch.ones(2701, dtype=torch.bool, device="cuda")
+        keep[rows] = False
+        keep = keep[:2700]
+        assert torch.equal(out[keep], good[keep]) and (out[~keep] == 0).all() and (~keep).any()
+    for length in (1 << 30, -64, 0):
+        ws = smr.Workspace(256)
+        npp.fill_(length)
+        srt, eids = al[0].clone(), al[1].clone()
+        srt[n:], eids[n // A:] = 2700, 0
+        out = torch.zeros_like(good)
+        smr.expert_up(xa, w, srt, eids, npp, width=3, block_size=A, out=out, workspace=ws, **kw)
+        assert smr.get_device_error(ws) == 0
+        assert torch.equal(out, good if length > 0 else torch.zeros_like(good))
+
+
+@pytest.mark.parametrize("A", [64, 128])
+def test_pairs_not_a_number_blocks(smr, A):
+    ids, wts, _, x, w13, w2 = _case(smr, T=800)
+    al = smr.align(ids, 7, A)
+    x = x.clone()
+    x[9, 40], x[700, 255] = float("nan"), float("inf")
+    codes, xs = smr.quantize_mxfp4(x)
+    w, ws, wv = _weights_mx(smr, w13, True)
+    act = smr.expert_up(codes, w, *al, width=3, block_size=A, x_scales=xs, w_scales=ws)
+    tok = torch.arange(2400, device="cuda") // 3
+    bad = (tok == 9) | (tok == 700)
+    assert torch.isnan(act[bad]).all()
+    ref, tol = _ref_up(_mx_exact(torch.where(torch.isfinite(x), x, torch.zeros_like(x)))[2], wv, ids, 3)
+    _close(act[~bad], ref[~bad], tol[~bad])
+    # a weight whose block is not a number: its expert's rows at its feature only
+    w13 = w13.clone()
+    w13[2, 128 + 17, 3] = float("nan")  # an up row
+    w, ws = _laid_out(smr, w13, True)
+    good = act
+    act = smr.expert_up(codes, w, *al, width=3, block_size=A, x_scales=xs, w_scales=ws)
+    of2 = (ids == 2).reshape(-1) & ~bad
+    assert torch.isnan(act[of2, 17]).all() and of2.any()
+    act[of2, 17] = good[of2, 17]
+    assert torch.equal(act[~bad], good[~bad])
+    y, yx = smr.quantize_mxfp4(good)
+    w, ws = _laid_out(smr, w2, False)
+    out = smr.expert_down(y, w, ids, wts, *al, block_size=A, x_scales=yx, w_scales=ws)
+    assert torch.isnan(out).all(1).nonzero().flatten().tolist() == [9, 700]
+    assert torch.isfinite(out).all(1).logical_not().nonzero().flatten().tolist() == [9, 700]
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_streams_with_their_own_inputs(smr, mx):
+    """Calls without a workspace on several streams at once, each stream with
+    other inputs and sizes: none reads another's rows."""
+    cases = [_case(smr, T=T, H=1024, seed=T) for T in (900, 1100, 1500, 2000)]
+    refs = [_ffn(smr, c, mx) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[] for _ in cases]
+    for _ in range(12):
+        for c, s, o in zip(cases, streams, outs):
+            o.append(_ffn(smr, c, mx, stream=s))
+    torch.cuda.synchronize()
+    for ref, o in zip(refs, outs):
+        assert all(torch.equal(a, ref[0]) and torch.equal(b, ref[1]) for a, b in o)
+
+
+@pytest.mark.parametrize("A,T", [(64, 40), (128, 40), (64, 1000), (128, 1000)])
+def test_align_outputs_of_any_alignment(smr, A, T):
+    """sorted_token_ids and expert_ids are asked to be 4-byte aligned only, and
+    may end with the last block's entries."""
+    ids, wts, _, x, w13, w2 = _case(smr, T=T)
+    al = smr.align(ids, 7, A)
+    ref = smr.expert_up(x, w13, *al, width=3, block_size=A)
+    n = int(al[2])
+    last = int((al[0][:n] < 3 * T).nonzero()[-1]) + 1  # (the sentinels behind the last slot may be missing)
+    for shift in (0, 1, 2, 3):
+        srt = torch.full((shift + last,), -1, dtype=torch.int32, device="cuda")[shift:]
+        eids = torch.full((shift + n // A,), -1, dtype=torch.int32, device="cuda")[shift:]
+        srt.copy_(al[0][:last])
+        eids.copy_(al[1][: n // A])
+        ws = smr.Workspace(256)
+        out = torch.full_like(ref, float("nan"))
+        smr.expert_up(x, w13, srt, eids, al[2], width=3, block_size=A, out=out, workspace=ws)
+        assert smr.get_device_error(ws) == 0 and torch.equal(out, ref)
+    _close(ref, *_ref_up(x.double(), w13.double(), ids, 3))
