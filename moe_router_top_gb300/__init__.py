@@ -130,6 +130,13 @@ class Workspace:
         if nbytes:
             self.ensure(nbytes)
 
+    def __getstate__(self):  # (locks cannot be copied, and graphs know the original's memory only)
+        return {"device": self.device, "buf": self.buf}
+
+    def __setstate__(self, state):
+        self.__init__(0, state["device"])
+        self.buf = state["buf"]
+
     def ensure(self, nbytes: int):
         """Grows to nbytes, in order on the current stream; the sticky error
         bits go over to the new memory."""

@@ -3,8 +3,10 @@ needed): refusals with every reason before any device work, workspace sizes,
 the calls that launch nothing, and the Python layer's argument checks."""
 from __future__ import annotations
 
+import copy
 import ctypes
 import os
+import pickle
 import re
 import subprocess
 import threading
@@ -600,3 +602,13 @@ def test_fp32_rows(lib):
     _refused(lib, lib.smr_expert_down_fp32, _down(num_logical=0), INVALID, "smr_expert_down_fp32", "num_logical must be in")
     empty = ExpertDownArgs(0, 1, 16, 16, 1, 64, num_logical=1)
     assert lib.smr_expert_down_fp32(ctypes.byref(empty), None, 0, None) == _lib.SMR_OK
+
+
+def test_workspaces_can_be_copied(smr):
+    """As part of a model that is copied or stored, say."""
+    ws = smr.Workspace(512, "cpu")
+    ws.buf[4] = 2
+    for other in (copy.deepcopy(ws), pickle.loads(pickle.dumps(ws))):
+        assert other.nbytes == 512 and other.buf[4] == 2 and other.buf is not ws.buf and other.lock is not ws.lock
+        other.ensure(1024)
+        assert other.nbytes == 1024 and ws.nbytes == 512
