@@ -123,6 +123,7 @@ class Workspace:
     def __init__(self, nbytes: int = 0, device=None):
         torch = _torch()
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self._on_cuda = self.device.type == "cuda"
         self.buf = None
         self.lock = threading.RLock()  # held from reading buf until the launches are made
         self._captured = False  # whether a capture has used buf
@@ -141,26 +142,27 @@ class Workspace:
         """Grows to nbytes, in order on the current stream; the sticky error
         bits go over to the new memory."""
         torch = _torch()
-        capturing = self.device.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing()
-        if self.buf is None or self.buf.numel() < nbytes:
+        buf = self.buf
+        capturing = self._on_cuda and torch._C._cuda_isCurrentStreamCapturing()
+        if buf is None or buf.numel() < nbytes:
             if capturing:
                 raise SmrError(_lib.SMR_ERR_WORKSPACE, f"a workspace cannot grow (to {nbytes} bytes) while its stream "
                                "is being captured: make the call once, or call ensure, before the capture")
             error = None
-            if self.buf is not None:
-                error = self.buf[_ERROR_WORD].clone()
+            if buf is not None:
+                error = buf[_ERROR_WORD].clone()
                 if self._captured:
-                    self._kept.append(self.buf)
+                    self._kept.append(buf)
                     self._captured = False
-                elif self.buf.is_cuda:  # (calls so far may have run on another stream than its own)
-                    self.buf.record_stream(torch.cuda.current_stream(self.device))
-                self.buf = None
-            self.buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
+                elif buf.is_cuda:  # (calls so far may have run on another stream than its own)
+                    buf.record_stream(torch.cuda.current_stream(self.device))
+                buf = self.buf = None
+            self.buf = buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
             if error is not None:
-                self.buf[_ERROR_WORD].copy_(error)
+                buf[_ERROR_WORD].copy_(error)
         elif capturing:
             self._captured = True
-        return self.buf
+        return buf
 
     @property
     def ptr(self) -> int:
@@ -200,11 +202,11 @@ def _workspace(ws, nbytes: int, device, stream):
                 return own.data_ptr(), nbytes
     if isinstance(ws, Workspace):
         if stream is None or (ws.buf is not None and ws.nbytes >= nbytes):
-            ws.ensure(nbytes)
+            buf = ws.ensure(nbytes)
         else:
             with _stream_context(stream, device):
-                ws.ensure(nbytes)
-        return ws.ptr, ws.nbytes
+                buf = ws.ensure(nbytes)
+        return buf.data_ptr(), buf.numel()
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
