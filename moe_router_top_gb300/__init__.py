@@ -176,38 +176,25 @@ class Workspace:
 _default_ws = {}
 
 
-_no_lock = contextlib.nullcontext()
-
-
-def _default_workspace(device):
-    key = (device.type, device.index)
-    return _default_ws.get(key) or _default_ws.setdefault(key, Workspace(0, device))
-
-
-def _hold(ws, device):
-    """The lock under which a call takes its workspace's memory and launches."""
+def _launch(fn, args, ws, nbytes: int, device, stream) -> int:
+    """Calls fn(*args, memory, its size, stream) with nbytes of the caller's
+    workspace, or of the one that such calls share on the device. The memory
+    stays the workspace's until the launches are made."""
     if ws is None:
-        ws = _default_workspace(device)
-    return ws.lock if isinstance(ws, Workspace) else _no_lock
-
-
-def _workspace(ws, nbytes: int, device, stream):
-    if ws is None:
-        ws = _default_workspace(device)
-        if ws.buf is None or ws.nbytes < nbytes:
-            torch = _torch()
-            if device.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing():
-                # memory of the graph's own, which it zeroes at every replay
-                own = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-                return own.data_ptr(), nbytes
-    if isinstance(ws, Workspace):
+        key = (device.type, device.index)
+        ws = _default_ws.get(key) or _default_ws.setdefault(key, Workspace(0, device))
+        if (ws.buf is None or ws.nbytes < nbytes) and ws._on_cuda and _torch()._C._cuda_isCurrentStreamCapturing():
+            # memory of the graph's own, which it zeroes at every replay
+            ws = _torch().zeros(nbytes, dtype=_torch().uint8, device=device)
+    if not isinstance(ws, Workspace):
+        return fn(*args, ws.data_ptr(), ws.numel() * ws.element_size(), _stream_ptr(stream))
+    with ws.lock:
         if stream is None or (ws.buf is not None and ws.nbytes >= nbytes):
             buf = ws.ensure(nbytes)
         else:
             with _stream_context(stream, device):
                 buf = ws.ensure(nbytes)
-        return buf.data_ptr(), buf.numel()
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+        return fn(*args, buf.data_ptr(), buf.numel(), _stream_ptr(stream))
 
 
 def _route_args(hidden, gate_w, shared_w, bias, topk, shared_scale, renormalize, ids, wts,
@@ -279,10 +266,7 @@ def route(hidden, gate_w, shared_w=None, bias=None, *, topk: int, shared_scale: 
     a = _route_args(hidden, gate_w, shared_w, bias, topk, shared_scale, renormalize, topk_ids,
                     topk_weights, logits_out, shared_logit_bf16, hidden_fp8, hidden_scales)
     need = lib.smr_route_workspace_size(ctypes.byref(a))
-    with _hold(workspace, hidden.device):
-        wp, wn = _workspace(workspace, need, hidden.device, stream)
-        status = lib.smr_route(ctypes.byref(a), wp, wn, _stream_ptr(stream))
-    _check(status)
+    _check(_launch(lib.smr_route, (ctypes.byref(a),), workspace, need, hidden.device, stream))
     return topk_ids, topk_weights
 
 
@@ -356,10 +340,7 @@ def align(topk_ids, num_experts: int, block_size: int = 0, *, routed_topk: int =
     a = _align_args(topk_ids, T, W, num_experts, block_size, routed_topk, routed_experts, *outs,
                     eplb=eplb)
     need = lib.smr_align_workspace_size(ctypes.byref(a))
-    with _hold(workspace, topk_ids.device):
-        wp, wn = _workspace(workspace, need, topk_ids.device, stream)
-        status = lib.smr_align(ctypes.byref(a), wp, wn, _stream_ptr(stream))
-    _check(status)
+    _check(_launch(lib.smr_align, (ctypes.byref(a),), workspace, need, topk_ids.device, stream))
     return outs
 
 
@@ -386,10 +367,7 @@ def route_align(hidden, gate_w, shared_w=None, bias=None, *, topk: int, block_si
                           sorted_token_ids, expert_ids, num_tokens_post_padded)
     aa = _align_args(topk_ids, M, topk + S, E + S, block_size, topk, E, *outs, eplb=eplb)
     need = lib.smr_route_align_workspace_size(ctypes.byref(ra), ctypes.byref(aa))
-    with _hold(workspace, hidden.device):
-        wp, wn = _workspace(workspace, need, hidden.device, stream)
-        status = lib.smr_route_align(ctypes.byref(ra), ctypes.byref(aa), wp, wn, _stream_ptr(stream))
-    _check(status)
+    _check(_launch(lib.smr_route_align, (ctypes.byref(ra), ctypes.byref(aa)), workspace, need, hidden.device, stream))
     return (topk_ids, topk_weights) + tuple(outs)
 
 
@@ -446,10 +424,7 @@ def expert_gemm(hidden, expert_w, sorted_token_ids, expert_ids, num_tokens_post_
     a.sorted_token_ids, a.sorted_cap = _ptr(sorted_token_ids), sorted_token_ids.numel()
     a.expert_ids, a.num_tokens_post_padded = _ptr(expert_ids), _ptr(num_tokens_post_padded)
     a.out = _ptr(out)
-    with _hold(workspace, hidden.device):
-        wp, wn = _workspace(workspace, 256, hidden.device, stream)
-        status = lib.smr_expert_gemm(ctypes.byref(a), wp, wn, _stream_ptr(stream))
-    _check(status)
+    _check(_launch(lib.smr_expert_gemm, (ctypes.byref(a),), workspace, 256, hidden.device, stream))
     return out
 
 

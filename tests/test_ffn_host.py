@@ -376,10 +376,16 @@ def test_growing_is_ordered_on_the_calls_stream(smr, monkeypatch):
         cuda=types.SimpleNamespace(stream=Context), device=torch.device, uint8=torch.uint8, zeros=zeros,
         _C=types.SimpleNamespace(_cuda_isCurrentStreamCapturing=lambda: False)))
     ws, s = smr.Workspace(0, "cuda:0"), Stream()
-    smr._workspace(ws, 512, torch.device("cuda", 0), s)
-    assert seen == [s, "zeros", None] and ws.nbytes == 512
-    smr._workspace(ws, 512, torch.device("cuda", 0), s)
-    assert len(seen) == 3
+    calls = []
+
+    def fn(*args):
+        calls.append(args)
+        return _lib.SMR_OK
+
+    smr._launch(fn, ("a",), ws, 512, torch.device("cuda", 0), s)
+    assert seen == [s, "zeros", None] and calls == [("a", ws.ptr, 512, 7)]
+    smr._launch(fn, (), ws, 512, torch.device("cuda", 0), s)
+    assert len(seen) == 3 and calls[1] == (ws.ptr, 512, 7)
 
 
 @pytest.fixture
@@ -389,7 +395,8 @@ def captured_device(smr, monkeypatch):
     c = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda dev: 7,
                               _cuda_isCurrentStreamCapturing=lambda: state.capturing)
     monkeypatch.setattr(smr, "_torch_module", types.SimpleNamespace(
-        _C=c, device=torch.device, uint8=torch.uint8, zeros=lambda n, dtype, device: torch.zeros(n, dtype=dtype)))
+        _C=c, device=torch.device, uint8=torch.uint8, zeros=lambda n, dtype, device: torch.zeros(n, dtype=dtype),
+        cuda=types.SimpleNamespace(current_stream=lambda: types.SimpleNamespace(cuda_stream=7))))
     monkeypatch.setattr(smr, "_default_ws", {})
     monkeypatch.setattr(smr, "_check_buffer", lambda ws, dev: None)
     return state
@@ -412,17 +419,17 @@ def test_no_growth_under_capture(smr, captured_device):
         with pytest.raises(smr.SmrError, match="being captured"):
             smr._run_product(fn, lambda ref: 1024, ExpertDownArgs(), ws, 0)
         with pytest.raises(smr.SmrError, match="being captured"):
-            smr._workspace(ws, 1024, dev, None)
+            smr._launch(fn, (None,), ws, 1024, dev, None)
         assert ws.buf is before
     with pytest.raises(smr.SmrError, match="being captured"):
         smr.Workspace(256, dev)
     assert calls == [512, 512]
     # a route without a workspace: the capture gets memory of its own, the shared one is left alone
-    ptr, n = smr._workspace(None, 2048, dev, None)
-    assert ptr and n == 2048 and smr._default_ws["cuda", 0].buf is None
+    assert smr._launch(fn, (None,), None, 2048, dev, 7) == _lib.SMR_OK
+    assert calls[2:] == [2048] and smr._default_ws["cuda", 0].buf is None
     captured_device.capturing = False
-    smr._workspace(None, 2048, dev, None)
-    assert smr._default_ws["cuda", 0].nbytes == 2048
+    smr._launch(fn, (None,), None, 2048, dev, None)
+    assert calls[3:] == [2048] and smr._default_ws["cuda", 0].nbytes == 2048
 
 
 def test_memory_of_a_capture_is_kept(smr, captured_device):
@@ -438,7 +445,7 @@ def test_memory_of_a_capture_is_kept(smr, captured_device):
     ws.ensure(8192)  # no capture has used these
     assert free() is None and old() is not None
     captured_device.capturing = True
-    smr._workspace(ws, 8192, torch.device("cuda", 0), None)
+    smr._launch(lambda *a: _lib.SMR_OK, (), ws, 8192, torch.device("cuda", 0), 7)
     captured_device.capturing = False
     used = weakref.ref(ws.buf)
     ws.ensure(16384)
@@ -481,8 +488,7 @@ def test_threads_on_one_workspace_take_turns(fake_device):
     def work(k):
         for _ in range(10):
             smr._run_product(fn, lambda ref: 1024, ExpertDownArgs(), ws, 0)
-            with smr._hold(ws, ws.device):
-                fn(None, *[smr._workspace(ws, 1024, ws.device, None)[i] for i in (0, 1)], 7)
+            smr._launch(fn, (None,), ws, 1024, ws.device, 7)
 
     threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
     for t in threads:
