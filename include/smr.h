@@ -381,7 +381,8 @@ SMR_API smr_status smr_clear_device_error(void *workspace, void *stream);
 
 /* One more sticky word per device: it gets the bits of every smr_expert_up
  * and smr_expert_down launch on the device, whatever workspace the call had,
- * also from graph replays and after the workspace is gone. Reads (after
+ * also from graph replays and after the workspace is gone (bit 1: a wait gave
+ * up; outputs made from the rows it left unwritten are not valid). Reads (after
  * synchronising `stream`) or clears (stream-ordered) that of the current
  * device. Not for launch paths. */
 SMR_API smr_status smr_get_expert_error(void *stream, int32_t *code_out);

@@ -16,9 +16,8 @@
 // expert follow each other, so its weights do too). Warp roles: 0 loads the
 // weights by TMA, 1 issues the MMAs, 2 reads the align's outputs ahead and
 // hands out the work, from 3 on load the routed rows (and their block scales)
-// with asynchronous 16-byte copies, the last eight drain TMEM. (A TMA gather
-// takes 4 rows an instruction and about 70 cycles each: 128 rows took 2300
-// cycles a k-block, 3300 us for 16384 tokens.) The stage ring runs across
+// with asynchronous 16-byte copies (a TMA gather takes 4 rows an instruction,
+// too slow for 128 rows a k-block), the last eight drain TMEM. The stage ring runs across
 // items; accumulators are double-buffered in TMEM, so the epilogue of one item
 // runs under the loads and MMAs of the next.
 // Every wait is bounded; a wait that gives up sets the workspace's error bit.
@@ -31,9 +30,8 @@ namespace smr {
 
 // k-blocks a stage: two for blocks of 64 rows and for pairs in MXFP4, else one
 // (a stage would be too large for a ring of them). A stage costs every role a
-// few hundred cycles of barrier round trips whatever its size: 550 a stage of
-// one k-block, 430 a k-block in stages of two (one token, 96 items; MXFP4 up,
-// 16384 tokens: 210 us in stages of one, 187 in stages of two).
+// few hundred cycles of barrier round trips whatever its size (MXFP4 up, 16384
+// tokens: 210 us in stages of one, 187 in stages of two).
 template <int SUB>
 constexpr int kFfLoaders = SUB == 2 ? 4 : 6;     // warps that load the routed rows; at most the stages
 constexpr int kFfDrains = 8;                     // warps of the epilogue, two for each quarter of TMEM's lanes
@@ -59,8 +57,8 @@ struct FfInfo {
     int slot[COLS];  // flat slot of every column, -1: none
     // its row of x, -1: none. Such a column is neither loaded nor stored: what
     // the MMAs make of the old contents of shared memory stays in its column.
-    // (Loading row 0 for it, 15 times a block in every CTA, queued the whole
-    // GPU up on one line of L2: 2500 cycles a stage with a single token.)
+    // (Loading row 0 for it, 15 times a block in every CTA, would queue the
+    // whole GPU up on one line of L2.)
     int row[COLS];
 };
 constexpr int kFfBars = 2 * kFfMaxStages + 4 + 2 * kFfInfos + 1;
@@ -127,8 +125,8 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
 // What is handed over is in this CTA's own shared memory (made visible to the
 // tensor core by a proxy fence before) or TMEM (read, and fenced), never in
 // global memory, so the arrival needs no release beyond the CTA: with
-// .release.cluster every one waited for the device-wide visibility of the
-// thread's earlier writes (2146 us against 886 without pairs, 16384 tokens).
+// .release.cluster every one waits for the device-wide visibility of the
+// thread's earlier writes, which costs more than pairs gain.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -224,9 +222,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&b);
 }
-// Outputs in bf16 leave through shared memory, in whole lines. (Stored from registers, a warp reaches 64 bytes of a line at most:
-// 131072 scattered rows of 4096 bytes took 164 us that way, 313 us in pieces of
-// 32 bytes, 83 us in lines.) TMEM is read in the matrix-fragment shape, whose
+// Outputs in bf16 leave through shared memory, in whole lines. (Stored from
+// registers, a warp reaches 64 bytes of a line at most, which halves the rate
+// of scattered rows.) TMEM is read in the matrix-fragment shape, whose
 // transposing store puts neighbouring features next to each other without a
 // shuffle, and which gives a thread the gate and the up value of the same
 // places.
@@ -331,9 +329,8 @@ __device__ __forceinline__ void ffn_error(uint32_t *err, uint32_t bits) {
 // each other together); each holds its own 128 weight rows (and their scales),
 // half of the routed rows and all of these rows' scales, and drains its own
 // lanes.
-// F32: the outputs are fp32, else bf16 (a variant of its own that stays within
-// 96 registers a thread: with both in one kernel blocks of the sum no longer
-// fitted beside a CTA, and 8 tokens in MXFP4 took 25.1 us instead of 21.0).
+// F32: the outputs are fp32, else bf16 (a variant of its own, without the other
+// epilogue's registers, so that blocks of the sum fit beside a CTA).
 template <bool MX, bool UP, bool PAIR, int SUB, bool F32>
 __global__ void __launch_bounds__(kFfThreads<SUB>, 1)
 expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const FfParams p) {
@@ -473,7 +470,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
         const bool wide = (reinterpret_cast<uintptr_t>(p.sorted) & 15) == 0;
         // the entries and the block's expert (of blocks below `limit`),
         // requested kAhead items ahead (a round trip to L2 is longer than two
-        // short items: with two ahead this warp took 1300 cycles an item)
+        // short items)
         auto fetch = [&](int b0, int limit, int (&ent)[8], int &e) {
             const int b = b0 + bo;
             if (!in || b0 < 0 || b >= limit) return;
@@ -1027,11 +1024,13 @@ expert_combine_kernel(const void *__restrict__ y, const int32_t *__restrict__ id
 
 // CTA pairs from this many rows an expert, on average: a pair halves the rows
 // that each CTA loads and that its MMAs read, but has only half as many items
-// to share out. With pairs and without (us on the device, 128 experts, gated
-// product): bf16 16384 tokens of 8 slots 494 and 777, 1024 skewed tokens (64
-// rows an expert) 134 and 156, evenly spread 134 and 133, 768 tokens (48 rows)
-// 131 and 145, evenly spread 132 and 126; MXFP4 16384 tokens 187 and 258, 1024
-// tokens 44.5 and 48.8 skewed, 40.6 and 40.4 evenly spread.
+// to share out. With pairs and without (us on the device, 128 experts, tokens
+// of 8 slots): gated product in bf16, 16384 tokens 500 and 799, 1024 skewed
+// tokens (64 rows an expert) 135 and 157, evenly spread 136 and 136, 768 tokens
+// (48 rows) 133 and 146, evenly spread 135 and 128; in MXFP4, 16384 tokens 187
+// and 262, 1024 tokens 44.8 and 48.9 skewed, 41.1 and 40.8 evenly spread. Second
+// product in bf16, 16384 tokens 395 and 560, 1024 skewed tokens 84.7 and 94.8;
+// in MXFP4 (K = 768, where the loaders bound both) 340 and 334, 38.9 and 40.1.
 constexpr int kPairRows = 48;
 static bool use_pairs(int64_t numel, int num_experts) { return numel >= (int64_t)kPairRows * num_experts; }
 

@@ -94,8 +94,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // Bound by memory like the quantisation: 4 bytes of codes to 8 bf16 values a
 // step, times the scale in bf16 (exact: a value has two significant bits, and
 // the smallest, 2^-128, is still a subnormal bf16; byte 255 is NaN). Table
-// look-ups and paired products: with one fp32 product a value the arithmetic
-// took longer than the memory (41 us for 16384 x 4096).
+// look-ups and paired products, as the arithmetic of one fp32 product a value
+// takes longer than the memory (16384 x 4096: 26.3 us, 6.4 TB/s).
 __global__ void __launch_bounds__(kMxThreads)
 dequantize_mxfp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, uint32_t vecs,
                         uint16_t *__restrict__ out) {
