@@ -5,8 +5,11 @@ experts' feed-forward in bf16 or MXFP4.
 Python names mirror the C ABI of include/smr.h; this layer only turns torch
 tensors into pointers, allocates outputs with torch when the caller does not
 pass them, and raises on a non-OK status. The work runs in libsmr.so's CUDA
-kernels on the caller's current stream. ``SMR_DISABLE=1`` makes every call
-raise :class:`SmrUnsupported`, so a caller can take its own fallback.
+kernels on the caller's current stream. Without a workspace route, align,
+route_align and expert_gemm share one per device, so such calls must not
+overlap on the GPU; expert_up and expert_down keep one per stream.
+``SMR_DISABLE=1`` makes every call raise :class:`SmrUnsupported`, so a caller
+can take its own fallback.
 """
 from __future__ import annotations
 
