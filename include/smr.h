@@ -115,6 +115,42 @@ typedef struct smr_route_args {
     float *hidden_scales;    /* out: fp32 [M, H / 128] */
 } smr_route_args;
 
+/* How logits become choices and weights (smr_select_experts, and a route's
+ * logits in smr_route_scored). For a row of logits x (NaN and -inf count as
+ * the lowest finite number, +inf as the largest) the scores are s = softmax(x)
+ * or sigmoid(x) and the choices c = s + balance_bias. A group (num_experts /
+ * num_groups consecutive experts) is worth the sum of its group_best largest
+ * c; the topk_groups best groups stay (equal ones: the lower index). The slots
+ * are the topk largest c of those groups, (c desc, id asc); a slot's weight is
+ * s, over the sum of the selected s if weights are renormalised, times
+ * routed_scale. Choices are taken as in 64 bits; without a balance bias c is
+ * compared as x, which has its order. */
+typedef struct smr_scoring {
+    int32_t sigmoid;            /* 1: sigmoid(x), 0: softmax(x) over all experts */
+    int32_t num_groups;         /* 1..32, divides the experts */
+    int32_t topk_groups;        /* 1..num_groups; topk <= topk_groups * (experts a group) */
+    int32_t group_best;         /* 1 or 2 */
+    float routed_scale;         /* multiplies the routed weights */
+    const float *balance_bias;  /* fp32 [experts], or NULL; NaN and infinities count as for x */
+} smr_scoring;
+
+/* Selection from logits that are in memory. */
+typedef struct smr_select_args {
+    const void *logits;      /* fp32 or bf16 [M, ld_logits] */
+    int32_t logits_fp32;     /* 1: fp32, 0: bf16 */
+    int32_t M;               /* tokens, >= 0 */
+    int64_t ld_logits;       /* row stride in elements, >= E */
+    int32_t E;               /* routed experts, 1..1024 */
+    int32_t topk;            /* 1..E, topk + has_shared <= 32 */
+    int32_t has_shared;      /* 1: slot topk = (E, shared weight) */
+    int32_t renormalize;     /* 1: weights over the sum of the selected scores */
+    const float *shared_logits;  /* fp32 [M]: the shared weight is shared_scale * sigmoid of it; NULL: shared_scale */
+    float shared_scale;
+    smr_scoring scoring;
+    int32_t *topk_ids;       /* out: int32 [M, topk + has_shared] */
+    float *topk_weights;     /* out: fp32 [M, topk + has_shared] */
+} smr_select_args;
+
 /* Align problem over a [num_tokens, width] id matrix. */
 typedef struct smr_align_args {
     const int32_t *topk_ids;      /* int32 [num_tokens, width], ids in [0, num_experts) */
@@ -232,6 +268,53 @@ typedef struct smr_expert_down_args {
     const int32_t *num_tokens_post_padded;
     void *out;                     /* out: bf16 [T, H], 16-byte aligned */
 } smr_expert_down_args;
+
+/* The same products on E4M3 codes, with the scales that smr_route
+ * (hidden_fp8), smr_quantize_fp8 and smr_quantize_fp8_weight give: one fp32
+ * scale per 128 values of a row of x, and per 128 x 128 block of each of an
+ * expert's weights (the gate rows' blocks, then the up rows'). A scale applies
+ * to its block's products, which are accumulated in fp32. */
+typedef struct smr_expert_up_fp8_args {
+    int32_t num_tokens;            /* T >= 0 */
+    int32_t width;                 /* slots per token (the align's width), >= 1 */
+    int32_t H;                     /* hidden size: multiple of 32, <= 16384 */
+    int32_t I;                     /* features of the gated product, multiple of 16 (act in E4M3: 32), <= 16384 */
+    int32_t num_experts;           /* 1..1025 */
+    int32_t block_size;            /* A used by the align: 64 or 128 */
+    const uint8_t *x;              /* E4M3 [T, H], 16-byte aligned */
+    const float *x_scales;         /* [T, ceil(H / 128)], 4-byte aligned */
+    const uint8_t *w;              /* E4M3 [num_experts, 2 I, H] (I gate rows, then I up rows), 16-byte aligned */
+    const float *w_scales;         /* [num_experts, 2 ceil(I / 128), ceil(H / 128)], 4-byte aligned */
+    const int32_t *sorted_token_ids;  /* the align's outputs (device) */
+    int64_t sorted_cap;
+    const int32_t *expert_ids;
+    const int32_t *num_tokens_post_padded;
+    void *act;                     /* out: bf16 [T * width, I]; with act_scales E4M3 [T * width, I]; 16-byte aligned */
+    float *act_scales;             /* out: [T * width, ceil(I / 128)], 4-byte aligned: act is quantised
+                                      (from its bf16 values, as smr_quantize_fp8 would); NULL: act is bf16 */
+} smr_expert_up_fp8_args;
+
+typedef struct smr_expert_down_fp8_args {
+    int32_t num_tokens;            /* T >= 0 */
+    int32_t width;                 /* >= 1 */
+    int32_t H;                     /* output features, multiple of 16, <= 16384 */
+    int32_t I;                     /* contraction: multiple of 32, <= 16384 */
+    int32_t num_experts;           /* 1..1025 */
+    int32_t block_size;            /* 64 or 128 */
+    const uint8_t *x;              /* E4M3 [T * width, I], 16-byte aligned */
+    const float *x_scales;         /* [T * width, ceil(I / 128)], 4-byte aligned */
+    const uint8_t *w;              /* E4M3 [num_experts, H, I], 16-byte aligned */
+    const float *w_scales;         /* [num_experts, ceil(H / 128), ceil(I / 128)], 4-byte aligned */
+    const int32_t *topk_ids;       /* as in smr_expert_down_args */
+    const float *topk_weights;
+    int32_t num_logical;
+    int32_t fp32_rows;             /* 1: the rows before the sum are fp32 whatever the batch (0: while they are few) */
+    const int32_t *sorted_token_ids;
+    int64_t sorted_cap;
+    const int32_t *expert_ids;
+    const int32_t *num_tokens_post_padded;
+    void *out;                     /* out: bf16 [T, H], 16-byte aligned */
+} smr_expert_down_fp8_args;
 
 /* M-aware alignment tier (host, no device work): 64 if
  * num_tokens * topk < 128 * num_experts (fewer than one full 128-row block of
@@ -368,6 +451,52 @@ SMR_API smr_status smr_dequantize_mxfp4(const uint8_t *codes, const uint8_t *sca
 SMR_API size_t smr_mxfp4_tiled_scale_bytes(int32_t num_experts, int32_t N, int32_t K, int32_t gated);
 SMR_API smr_status smr_tile_mxfp4_scales(const uint8_t *scales, int32_t num_experts, int32_t N, int32_t K,
                                          int32_t gated, uint8_t *tiled, void *stream);
+
+/* The experts' products in E4M3 (see the argument structs): what is said of
+ * smr_expert_up and smr_expert_down holds for them too. smr_expert_up_fp8
+ * without act_scales is one launch, workspace >= 256 bytes; with them the
+ * workspace is as its _size says. */
+SMR_API size_t smr_expert_up_fp8_workspace_size(const smr_expert_up_fp8_args *args);
+SMR_API size_t smr_expert_down_fp8_workspace_size(const smr_expert_down_fp8_args *args);
+SMR_API smr_status smr_expert_up_fp8(const smr_expert_up_fp8_args *args, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+SMR_API smr_status smr_expert_down_fp8(const smr_expert_down_fp8_args *args, void *workspace, size_t workspace_bytes,
+                                       void *stream);
+
+/* bf16 [rows, ld_x] to E4M3 codes [rows, K] with one fp32 scale per 128 values
+ * [rows, ceil(K / 128)], one launch, as the route's hidden_fp8: scale = amax /
+ * 448, codes = E4M3(x * (448 / amax)) rounded to nearest even, in fp32. amax
+ * counts as 2^-110 at the least; a block of zeros has scale 0 and zero codes,
+ * one with a NaN or an infinity a NaN scale and zero codes. K: multiple of 32,
+ * rows * K <= 2^34; ld_x >= K, multiple of 8; x and codes 16-byte, scales
+ * 4-byte aligned. rows == 0: no launch. */
+SMR_API smr_status smr_quantize_fp8(const void *x, int64_t rows, int32_t K, int64_t ld_x, uint8_t *codes,
+                                    float *scales, void *stream);
+/* The same of `matrices` weights [N, K] (of a gated weight: 2 num_experts
+ * matrices of I rows), one scale per 128 x 128 block [matrices, ceil(N / 128),
+ * ceil(K / 128)]; matrices * N * K <= 2^40. */
+SMR_API smr_status smr_quantize_fp8_weight(const void *w, int32_t matrices, int32_t N, int32_t K, uint8_t *codes,
+                                           float *scales, void *stream);
+/* The values [rows, K] of codes and row scales, rounded to bf16. */
+SMR_API smr_status smr_dequantize_fp8(const uint8_t *codes, const float *scales, int64_t rows, int32_t K, void *out,
+                                      void *stream);
+
+/* Scores, groups and top-k of logits in memory (see smr_scoring), one launch,
+ * no workspace. M == 0: no launch. */
+SMR_API smr_status smr_select_experts(const smr_select_args *args, void *stream);
+
+/* smr_route and smr_route_align with scores, groups and a balance bias: the
+ * gate's logits, rounded to bf16 (args->bias added before), are selected from
+ * as scoring says; args->renormalize, topk, shared_w, shared_scale and
+ * shared_logit_bf16 mean what they mean there. Two launches up to M = 16 and
+ * ceil(E / 512) + 1 above, then the align's (1 or 3). */
+SMR_API size_t smr_route_scored_workspace_size(const smr_route_args *args);
+SMR_API size_t smr_route_align_scored_workspace_size(const smr_route_args *route, const smr_align_args *align);
+SMR_API smr_status smr_route_scored(const smr_route_args *args, const smr_scoring *scoring, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+SMR_API smr_status smr_route_align_scored(const smr_route_args *route, const smr_scoring *scoring,
+                                          const smr_align_args *align, void *workspace, size_t workspace_bytes,
+                                          void *stream);
 
 /* Sticky device error word of a workspace: synchronises `stream`, then copies
  * the word to *code_out (0 = no error; bit 0 = an id out of range in align,

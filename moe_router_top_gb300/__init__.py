@@ -1,6 +1,6 @@
 """GB300-native MoE routing front-end: route (gate GEMM, bf16 logits, top-k,
 renormalised softmax, shared slot), moe_align_block_size and, behind it, the
-experts' feed-forward in bf16 or MXFP4.
+experts' feed-forward in bf16, E4M3 or MXFP4.
 
 Python names mirror the C ABI of include/smr.h; this layer only turns torch
 tensors into pointers, allocates outputs with torch when the caller does not
@@ -20,12 +20,14 @@ import threading
 from typing import Optional, Tuple
 
 from . import _lib
-from ._lib import AlignArgs, ExpertDownArgs, ExpertGemmArgs, ExpertUpArgs, RouteArgs
+from ._lib import (AlignArgs, ExpertDownArgs, ExpertDownFp8Args, ExpertGemmArgs, ExpertUpArgs, ExpertUpFp8Args,
+                   RouteArgs, Scoring, SelectArgs)
 
 __all__ = [
     "SmrError", "SmrUnsupported", "Workspace", "route", "align", "route_align",
     "route_align_static", "expert_gemm", "expert_up", "expert_down", "quantize_mxfp4",
-    "dequantize_mxfp4", "tile_mxfp4_scales",
+    "dequantize_mxfp4", "tile_mxfp4_scales", "select_experts", "quantize_fp8", "quantize_fp8_weight",
+    "dequantize_fp8",
     "select_block_size", "align_capacity", "route_workspace_size", "align_workspace_size",
     "route_align_workspace_size", "get_device_error", "clear_device_error",
     "get_static_device_error", "clear_static_device_error", "release_workspaces", "test_force_wait_timeout",
@@ -258,18 +260,98 @@ def _route_outputs(hidden, topk, has_shared, ids, wts):
 def route(hidden, gate_w, shared_w=None, bias=None, *, topk: int, shared_scale: float = 1.0,
           renormalize: bool = True, shared_logit_bf16: bool = False, topk_ids=None,
           topk_weights=None, logits_out=None, hidden_fp8=None, hidden_scales=None,
-          workspace=None, stream=None) -> Tuple:
+          workspace=None, stream=None, scoring: str = "softmax", balance_bias=None,
+          num_groups: int = 1, topk_groups: Optional[int] = None, group_best: int = 1,
+          routed_scale: float = 1.0) -> Tuple:
     """Route M tokens: returns (topk_ids int32 [M, k+S], topk_weights fp32 [M, k+S]).
     hidden_fp8 (uint8 [M, H]) and hidden_scales (float32 [M, H/128]), when
     given, receive the hidden states as e4m3 codes with one scale per 128
-    values, written by the same launch."""
+    values, written by the same launch. scoring, balance_bias, num_groups,
+    topk_groups, group_best and routed_scale: as for select_experts, applied to
+    the gate's logits (rounded to bf16, `bias` added before)."""
     _disabled()
     lib = _lib.load()
+    scored = _scoring(scoring, balance_bias, num_groups, topk_groups, group_best, routed_scale, gate_w.shape[0],
+                      hidden.device)
     topk_ids, topk_weights = _route_outputs(hidden, topk, shared_w is not None, topk_ids, topk_weights)
     a = _route_args(hidden, gate_w, shared_w, bias, topk, shared_scale, renormalize, topk_ids,
                     topk_weights, logits_out, shared_logit_bf16, hidden_fp8, hidden_scales)
+    if scored is not None:
+        need = lib.smr_route_scored_workspace_size(ctypes.byref(a))
+        _check(_launch(lib.smr_route_scored, (ctypes.byref(a), ctypes.byref(scored)), workspace, need, hidden.device,
+                       stream))
+        return topk_ids, topk_weights
     need = lib.smr_route_workspace_size(ctypes.byref(a))
     _check(_launch(lib.smr_route, (ctypes.byref(a),), workspace, need, hidden.device, stream))
+    return topk_ids, topk_weights
+
+
+def _scoring(scoring, balance_bias, num_groups, topk_groups, group_best, routed_scale, E, device):
+    """The library's scoring, or None where it is the route's own (softmax
+    scores, the top-k of them, weights as they are)."""
+    if (scoring == "softmax" and balance_bias is None and num_groups == 1 and topk_groups in (None, 1)
+            and group_best in (1, 2) and routed_scale == 1.0):
+        return None
+    torch = _torch()
+    if scoring not in ("softmax", "sigmoid"):
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid' (got {scoring!r})")
+    if balance_bias is not None:
+        if balance_bias.dtype != torch.float32 or balance_bias.shape != (E,) or not balance_bias.is_contiguous():
+            raise ValueError(f"balance_bias must be a contiguous float32 [{E}] tensor")
+        if balance_bias.device != device:
+            raise ValueError(f"tensors must be on one device (got {balance_bias.device}, {device})")
+    num_groups = int(num_groups)
+    topk_groups = num_groups if topk_groups is None else int(topk_groups)
+    _check_sizes(num_groups | topk_groups | int(group_best))
+    return Scoring(1 if scoring == "sigmoid" else 0, num_groups, topk_groups, int(group_best), float(routed_scale),
+                   _ptr(balance_bias))
+
+
+def select_experts(logits, *, topk: int, scoring: str = "softmax", balance_bias=None, num_groups: int = 1,
+                   topk_groups: Optional[int] = None, group_best: int = 1, renormalize: bool = True,
+                   routed_scale: float = 1.0, has_shared: bool = False, shared_logits=None,
+                   shared_scale: float = 1.0, topk_ids=None, topk_weights=None, stream=None) -> Tuple:
+    """Experts and weights of M tokens from their logits (float32 or bfloat16
+    [M, E], unit stride along E): returns (topk_ids int32 [M, k+S],
+    topk_weights fp32 [M, k+S]), S = 1 with has_shared.
+
+    Scores s are softmax(logits) or sigmoid(logits), choices s + balance_bias
+    (float32 [E]). The experts form num_groups groups of neighbours, worth the
+    sum of their group_best (1 or 2) largest choices; the topk_groups best
+    (all by default) stay, the lower index among equal ones. The topk largest
+    choices of those are selected, the lower id among equal ones; a slot's
+    weight is its score (over the sum of the selected ones with renormalize)
+    times routed_scale. Choices are taken as in 64 bits. NaN and -inf count as
+    the lowest finite number, +inf as the largest. The shared slot is (E,
+    shared_scale * sigmoid(shared_logits[t])), or (E, shared_scale) without
+    shared_logits (float32 [M])."""
+    _disabled()
+    torch = _torch()
+    lib = _lib.load()
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be a float32 or bfloat16 [M, E] tensor with unit stride along E")
+    M, E = logits.shape
+    topk = int(topk)
+    _check_sizes(M | E | topk)
+    if shared_logits is not None and (not has_shared or shared_logits.dtype != torch.float32
+                                      or shared_logits.numel() != M or not shared_logits.is_contiguous()):
+        raise ValueError(f"shared_logits must be a contiguous float32 [{M}] tensor, given with has_shared")
+    dev = _check_cuda(logits, balance_bias, shared_logits, topk_ids, topk_weights)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return select_experts(logits, topk=topk, scoring=scoring, balance_bias=balance_bias, num_groups=num_groups,
+                                  topk_groups=topk_groups, group_best=group_best, renormalize=renormalize,
+                                  routed_scale=routed_scale, has_shared=has_shared, shared_logits=shared_logits,
+                                  shared_scale=shared_scale, topk_ids=topk_ids, topk_weights=topk_weights)
+    scored = _scoring(scoring, balance_bias, num_groups, topk_groups, group_best, routed_scale, E, logits.device)
+    width = topk + (1 if has_shared else 0)
+    topk_ids = _output(topk_ids, (M,), width, torch.int32, logits, "topk_ids")
+    topk_weights = _output(topk_weights, (M,), width, torch.float32, logits, "topk_weights")
+    a = SelectArgs(logits.data_ptr(), 1 if logits.dtype is torch.float32 else 0, M, logits.stride(0) if M > 1 else E, E,
+                   topk, 1 if has_shared else 0, 1 if renormalize else 0, _ptr(shared_logits), float(shared_scale),
+                   scored or Scoring(0, 1, 1, 1, 1.0, None), topk_ids.data_ptr(), topk_weights.data_ptr())
+    _check(lib.smr_select_experts(ctypes.byref(a), _raw_stream(dev)))
     return topk_ids, topk_weights
 
 
@@ -353,12 +435,17 @@ def route_align(hidden, gate_w, shared_w=None, bias=None, *, topk: int, block_si
                 logits_out=None, sorted_token_ids=None, expert_ids=None,
                 num_tokens_post_padded=None, eplb_map=None, eplb_count=None,
                 num_physical: int = 0, hidden_fp8=None, hidden_scales=None, workspace=None,
-                stream=None) -> Tuple:
-    """Route then align (one launch for M <= 16 without an EPLB remap).
-    Returns (topk_ids, topk_weights, sorted_token_ids, expert_ids,
+                stream=None, scoring: str = "softmax", balance_bias=None, num_groups: int = 1,
+                topk_groups: Optional[int] = None, group_best: int = 1,
+                routed_scale: float = 1.0) -> Tuple:
+    """Route then align (one launch for M <= 16 without an EPLB remap; scoring
+    and what follows it as for route, in launches of their own). Returns
+    (topk_ids, topk_weights, sorted_token_ids, expert_ids,
     num_tokens_post_padded)."""
     _disabled()
     lib = _lib.load()
+    scored = _scoring(scoring, balance_bias, num_groups, topk_groups, group_best, routed_scale, gate_w.shape[0],
+                      hidden.device)
     S = 1 if shared_w is not None else 0
     topk_ids, topk_weights = _route_outputs(hidden, topk, S, topk_ids, topk_weights)
     ra = _route_args(hidden, gate_w, shared_w, bias, topk, shared_scale, renormalize, topk_ids,
@@ -369,6 +456,11 @@ def route_align(hidden, gate_w, shared_w=None, bias=None, *, topk: int, block_si
     outs = _align_outputs(hidden.device, M * (topk + S), num_physical if eplb else E + S, A,
                           sorted_token_ids, expert_ids, num_tokens_post_padded)
     aa = _align_args(topk_ids, M, topk + S, E + S, block_size, topk, E, *outs, eplb=eplb)
+    if scored is not None:
+        need = lib.smr_route_align_scored_workspace_size(ctypes.byref(ra), ctypes.byref(aa))
+        _check(_launch(lib.smr_route_align_scored, (ctypes.byref(ra), ctypes.byref(scored), ctypes.byref(aa)), workspace,
+                       need, hidden.device, stream))
+        return (topk_ids, topk_weights) + tuple(outs)
     need = lib.smr_route_align_workspace_size(ctypes.byref(ra), ctypes.byref(aa))
     _check(_launch(lib.smr_route_align, (ctypes.byref(ra), ctypes.byref(aa)), workspace, need, hidden.device, stream))
     return (topk_ids, topk_weights) + tuple(outs)
@@ -538,6 +630,9 @@ def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated, sorted_tok
     mx = x_scales is not None
     if mx != (w_scales is not None):
         raise ValueError("x_scales and w_scales must both be given (MXFP4) or both be None (bfloat16)")
+    if mx and x_scales.dtype is torch.float32:
+        _fp8_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated)
+        return _align_inputs(sorted_token_ids, expert_ids, npp, block_size)
     dtype, kdim = (torch.uint8, K // 2) if mx else (torch.bfloat16, K)
     if x.dtype is not dtype or x.shape != (rows, kdim) or (x.stride(1) != 1 and kdim > 1):
         raise ValueError(f"x must be a {dtype} [{rows}, {kdim}] tensor with unit stride along its rows")
@@ -551,7 +646,28 @@ def _product_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated, sorted_tok
         need = _lib.load().smr_mxfp4_tiled_scale_bytes(w.shape[0], w_rows, K, 1 if gated else 0)
         if w_scales.dtype is not torch.uint8 or w_scales.numel() != need or not w_scales.is_contiguous():
             raise ValueError(f"w_scales must be the {need} bytes that tile_mxfp4_scales gives for this weight")
-    int32 = torch.int32
+    _align_inputs(sorted_token_ids, expert_ids, npp, block_size)
+
+
+def _fp8_inputs(x, w, x_scales, w_scales, rows, K, w_rows, gated):
+    """Checks of a product's operands in E4M3."""
+    torch = _torch()
+    codes = (torch.uint8, torch.float8_e4m3fn)
+    if x.dtype not in codes or x.shape != (rows, K) or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous [{rows}, {K}] tensor of E4M3 codes (uint8 or float8_e4m3fn)")
+    if w.dtype not in codes or w.shape[1:] != (w_rows, K) or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous [num_experts, {w_rows}, {K}] tensor of E4M3 codes")
+    kb = -(-K // 128)
+    if x_scales.shape != (rows, kb) or not x_scales.is_contiguous():
+        raise ValueError(f"x_scales must be a contiguous float32 [{rows}, {kb}] tensor")
+    nb = 2 * -(-(w_rows // 2) // 128) if gated else -(-w_rows // 128)
+    if w_scales.dtype is not torch.float32 or w_scales.shape != (w.shape[0], nb, kb) or not w_scales.is_contiguous():
+        raise ValueError(f"w_scales must be a contiguous float32 [{w.shape[0]}, {nb}, {kb}] tensor")
+
+
+def _align_inputs(sorted_token_ids, expert_ids, npp, block_size):
+    """Checks of the align's outputs."""
+    int32 = _torch().int32
     if (sorted_token_ids.dtype is not int32 or expert_ids.dtype is not int32 or npp.dtype is not int32
             or not sorted_token_ids.is_contiguous() or not expert_ids.is_contiguous()):
         raise ValueError("sorted_token_ids, expert_ids and num_tokens_post_padded must be contiguous int32 tensors")
@@ -571,14 +687,21 @@ def _output(out, lead, n, dtype, like, name="out"):
 
 
 def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, width: int, block_size: int,
-              x_scales=None, w_scales=None, out=None, workspace=None, stream=None):
+              x_scales=None, w_scales=None, out=None, workspace=None, stream=None, quantize_act: bool = False,
+              act_scales=None):
     """The experts' gated product behind the align: returns act bf16
     [num_tokens * width, I], row t * width + s = silu(g) * u with g and u the
     products of x[t] (bf16 [num_tokens, H]) with the gate rows w[e, :I] and the
     up rows w[e, I:] (bf16 [num_experts, 2 I, H]) of the slot's expert e.
     With x_scales and w_scales, x and w are MXFP4 codes (quantize_mxfp4;
-    w_scales laid out by tile_mxfp4_scales(..., gated=True)). Rows of slots
-    that the align skipped are left as they are in `out`."""
+    w_scales laid out by tile_mxfp4_scales(..., gated=True)); with float32
+    scales they are E4M3 codes [num_tokens, H] and [num_experts, 2 I, H]
+    (uint8 or float8_e4m3fn; x_scales [num_tokens, ceil(H / 128)] as from
+    route's hidden_fp8 or quantize_fp8, w_scales [num_experts, 2 ceil(I / 128),
+    ceil(H / 128)] as from quantize_fp8_weight(..., gated=True)), and
+    quantize_act=True returns (codes uint8, scales), what quantize_fp8 gives of
+    act, for expert_down (into `out` and `act_scales` if they are given). Rows
+    of slots that the align skipped are left as they are in `out`."""
     _disabled()
     torch = _torch()
     lib = _lib.load()
@@ -589,17 +712,29 @@ def expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, *, wid
         raise ValueError(f"width must be >= 1 (got {width})")
     T, H = x.shape
     E, I = w.shape[0], w.shape[1] // 2
-    if x_scales is not None:
+    fp8 = x_scales is not None and x_scales.dtype is torch.float32
+    if x_scales is not None and not fp8:
         H *= 2
+    if (quantize_act and not fp8) or (act_scales is not None and not quantize_act):
+        raise ValueError("quantize_act needs E4M3 operands (float32 scales), and act_scales quantize_act")
     _product_inputs(x, w, x_scales, w_scales, T, H, 2 * I, True, sorted_token_ids, expert_ids,
                     num_tokens_post_padded, block_size, width)
-    dev = _check_cuda(x, w, x_scales, w_scales, sorted_token_ids, expert_ids, num_tokens_post_padded, out)
+    dev = _check_cuda(x, w, x_scales, w_scales, sorted_token_ids, expert_ids, num_tokens_post_padded, out, act_scales)
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
             return expert_up(x, w, sorted_token_ids, expert_ids, num_tokens_post_padded, width=width,
                              block_size=block_size, x_scales=x_scales, w_scales=w_scales, out=out,
-                             workspace=workspace)
+                             workspace=workspace, quantize_act=quantize_act, act_scales=act_scales)
+    if fp8:
+        out = _output(out, (T * width,), I, torch.uint8 if quantize_act else torch.bfloat16, x)
+        if quantize_act:
+            act_scales = _output(act_scales, (T * width,), -(-I // 128), torch.float32, x, "act_scales")
+        a = ExpertUpFp8Args(T, width, H, I, E, block_size, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(),
+                            w_scales.data_ptr(), sorted_token_ids.data_ptr(), sorted_token_ids.numel(),
+                            expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(), out.data_ptr(), _ptr(act_scales))
+        _run_product(lib.smr_expert_up_fp8, lib.smr_expert_up_fp8_workspace_size, a, workspace, dev)
+        return (out, act_scales) if quantize_act else out
     out = _output(out, (T * width,), I, torch.bfloat16, x)
     a = ExpertUpArgs(T, width, H, I, E, block_size, x.data_ptr(), x.stride(0) if T > 1 else H, _ptr(x_scales),
                      w.data_ptr(), _ptr(w_scales), sorted_token_ids.data_ptr(), sorted_token_ids.numel(),
@@ -616,7 +751,9 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     s] . w[e]^T) for the slots' experts e; x bf16 [num_tokens * width, I] (the
     rows of expert_up), w bf16 [num_experts, H, I], topk_ids and topk_weights
     [num_tokens, width] as routed. With x_scales and w_scales, x and w are
-    MXFP4 codes. A slot whose id is outside [0, num_logical) contributes
+    MXFP4 codes, or with float32 scales E4M3 codes [num_tokens * width, I] and
+    [num_experts, H, I] (x_scales [num_tokens * width, ceil(I / 128)], w_scales
+    [num_experts, ceil(H / 128), ceil(I / 128)]). A slot whose id is outside [0, num_logical) contributes
     nothing (num_logical: the experts that were aligned; num_experts if 0);
     every other slot must have been aligned. The products wait for the sum in
     fp32 while they are few, else in bf16; fp32_rows=True keeps them in fp32
@@ -633,7 +770,8 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
     block_size, num_logical = int(block_size), int(num_logical)
     T, width = topk_ids.shape
     E, H, I = w.shape
-    if x_scales is not None:
+    fp8 = x_scales is not None and x_scales.dtype is torch.float32
+    if x_scales is not None and not fp8:
         I *= 2
     _product_inputs(x, w, x_scales, w_scales, T * width, I, H, False, sorted_token_ids, expert_ids,
                     num_tokens_post_padded, block_size, num_logical)
@@ -648,6 +786,14 @@ def expert_down(x, w, topk_ids, topk_weights, sorted_token_ids, expert_ids, num_
                                block_size=block_size, num_logical=num_logical, fp32_rows=fp32_rows,
                                x_scales=x_scales, w_scales=w_scales, out=out, workspace=workspace)
     out = _output(out, (T,), H, torch.bfloat16, x)
+    if fp8:
+        a = ExpertDownFp8Args(T, width, H, I, E, block_size, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(),
+                              w_scales.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(),
+                              num_logical if num_logical else E, 1 if fp32_rows else 0, sorted_token_ids.data_ptr(),
+                              sorted_token_ids.numel(), expert_ids.data_ptr(), num_tokens_post_padded.data_ptr(),
+                              out.data_ptr())
+        _run_product(lib.smr_expert_down_fp8, lib.smr_expert_down_fp8_workspace_size, a, workspace, dev)
+        return out
     a = ExpertDownArgs(T, width, H, I, E, block_size, x.data_ptr(), _ptr(x_scales), w.data_ptr(), _ptr(w_scales),
                        topk_ids.data_ptr(), topk_weights.data_ptr(), num_logical if num_logical else E,
                        sorted_token_ids.data_ptr(), sorted_token_ids.numel(), expert_ids.data_ptr(),
@@ -734,6 +880,90 @@ def tile_mxfp4_scales(scales, *, gated: bool = False, out=None, stream=None):
     out = _output(out, (E, tiles, K // 128), 512, torch.uint8, scales)
     _check(lib.smr_tile_mxfp4_scales(scales.data_ptr(), E, N, K, 1 if gated else 0, out.data_ptr(),
                                      _raw_stream(dev)))
+    return out
+
+
+def quantize_fp8(x, *, codes=None, scales=None, stream=None) -> Tuple:
+    """bf16 x [..., K] to E4M3: returns (codes uint8 [..., K], scales float32
+    [..., ceil(K / 128)], one per 128 values), as the route's hidden_fp8; see
+    smr_quantize_fp8 in include/smr.h. x is contiguous, or 2-D with unit stride
+    along K; K a multiple of 32."""
+    _disabled()
+    torch = _torch()
+    lib = _lib.load()
+    shape = x.shape
+    dense = x.is_contiguous()
+    if x.dtype != torch.bfloat16 or len(shape) < 1 or not (dense or (len(shape) == 2 and x.stride(1) == 1)):
+        raise ValueError("x must be a bfloat16 tensor, contiguous or 2-D with unit stride along its rows")
+    K = shape[-1]
+    if K < 32 or K % 32:
+        raise ValueError(f"x's last dimension must be a positive multiple of 32 (got {K})")
+    _check_sizes(K)
+    dev = _check_cuda(x, codes, scales)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return quantize_fp8(x, codes=codes, scales=scales)
+    lead = shape[:-1]
+    codes = _output(codes, lead, K, torch.uint8, x, "codes")
+    scales = _output(scales, lead, -(-K // 128), torch.float32, x, "scales")
+    rows = x.numel() // K
+    _check(lib.smr_quantize_fp8(x.data_ptr(), rows, K, K if dense or rows < 2 else x.stride(0), codes.data_ptr(),
+                                scales.data_ptr(), _raw_stream(dev)))
+    return codes, scales
+
+
+def quantize_fp8_weight(w, *, gated: bool = False, codes=None, scales=None, stream=None) -> Tuple:
+    """A weight bf16 [num_experts, N, K] to E4M3, once, for expert_up
+    (gated=True: N = 2 I, the gate's and the up rows' blocks apart) or
+    expert_down: returns (codes uint8 [num_experts, N, K], scales float32
+    [num_experts, ceil(N / 128) (gated: 2 ceil(I / 128)), ceil(K / 128)], one
+    per 128 x 128 block). K is a multiple of 32."""
+    _disabled()
+    torch = _torch()
+    lib = _lib.load()
+    if w.dtype != torch.bfloat16 or w.dim() != 3 or not w.is_contiguous() or (gated and w.shape[1] % 2):
+        raise ValueError("w must be a contiguous bfloat16 [num_experts, N, K] tensor (N even for a gated weight)")
+    E, N, K = w.shape
+    if K < 32 or K % 32:
+        raise ValueError(f"w's last dimension must be a positive multiple of 32 (got {K})")
+    _check_sizes(2 * E | N | K)
+    dev = _check_cuda(w, codes, scales)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return quantize_fp8_weight(w, gated=gated, codes=codes, scales=scales)
+    parts = 2 if gated else 1
+    codes = _output(codes, (E, N), K, torch.uint8, w, "codes")
+    scales = _output(scales, (E, parts * -(-(N // parts) // 128)), -(-K // 128), torch.float32, w, "scales")
+    _check(lib.smr_quantize_fp8_weight(w.data_ptr(), E * parts, N // parts, K, codes.data_ptr(), scales.data_ptr(),
+                                       _raw_stream(dev)))
+    return codes, scales
+
+
+def dequantize_fp8(codes, scales, *, out=None, stream=None):
+    """The values [..., K] of E4M3 codes (uint8 or float8_e4m3fn) and row
+    scales [..., ceil(K / 128)], rounded to bf16 (NaN where the scale is)."""
+    _disabled()
+    torch = _torch()
+    lib = _lib.load()
+    shape = codes.shape
+    if codes.dtype not in (torch.uint8, torch.float8_e4m3fn) or len(shape) < 1 or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous uint8 or float8_e4m3fn tensor")
+    lead, K = shape[:-1], shape[-1]
+    if K < 32 or K % 32:
+        raise ValueError(f"codes' last dimension must be a positive multiple of 32 (got {K})")
+    _check_sizes(K)
+    if scales.dtype != torch.float32 or scales.shape != lead + (-(-K // 128),) or not scales.is_contiguous():
+        raise ValueError(f"scales must be a contiguous float32 tensor of shape {tuple(lead) + (-(-K // 128),)}")
+    dev = _check_cuda(codes, scales, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return dequantize_fp8(codes, scales, out=out)
+    out = _output(out, lead, K, torch.bfloat16, codes)
+    _check(lib.smr_dequantize_fp8(codes.data_ptr(), scales.data_ptr(), codes.numel() // K, K, out.data_ptr(),
+                                  _raw_stream(dev)))
     return out
 
 

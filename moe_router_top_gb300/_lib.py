@@ -31,6 +31,9 @@ EXPORTED = (
     "smr_expert_down_workspace_size", "smr_quantize_mxfp4", "smr_dequantize_mxfp4",
     "smr_mxfp4_tiled_scale_bytes", "smr_tile_mxfp4_scales",
     "smr_expert_down_fp32", "smr_expert_down_fp32_workspace_size", "smr_get_expert_error", "smr_clear_expert_error",
+    "smr_expert_up_fp8", "smr_expert_up_fp8_workspace_size", "smr_expert_down_fp8", "smr_expert_down_fp8_workspace_size",
+    "smr_quantize_fp8", "smr_quantize_fp8_weight", "smr_dequantize_fp8", "smr_select_experts", "smr_route_scored",
+    "smr_route_scored_workspace_size", "smr_route_align_scored", "smr_route_align_scored_workspace_size",
 )
 
 SMR_STALL_NONE = 0
@@ -102,6 +105,50 @@ class ExpertDownArgs(ctypes.Structure):
     ]
 
 
+class Scoring(ctypes.Structure):
+    _fields_ = [
+        ("sigmoid", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+        ("group_best", ctypes.c_int32), ("routed_scale", ctypes.c_float),
+        ("balance_bias", ctypes.c_void_p),
+    ]
+
+
+class SelectArgs(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("logits_fp32", ctypes.c_int32), ("M", ctypes.c_int32),
+        ("ld_logits", ctypes.c_int64), ("E", ctypes.c_int32), ("topk", ctypes.c_int32),
+        ("has_shared", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+        ("shared_logits", ctypes.c_void_p), ("shared_scale", ctypes.c_float),
+        ("scoring", Scoring), ("topk_ids", ctypes.c_void_p), ("topk_weights", ctypes.c_void_p),
+    ]
+
+
+class ExpertUpFp8Args(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32), ("width", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("I", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("x_scales", ctypes.c_void_p),
+        ("w", ctypes.c_void_p), ("w_scales", ctypes.c_void_p),
+        ("sorted_token_ids", ctypes.c_void_p), ("sorted_cap", ctypes.c_int64),
+        ("expert_ids", ctypes.c_void_p), ("num_tokens_post_padded", ctypes.c_void_p),
+        ("act", ctypes.c_void_p), ("act_scales", ctypes.c_void_p),
+    ]
+
+
+class ExpertDownFp8Args(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int32), ("width", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("I", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("block_size", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("x_scales", ctypes.c_void_p),
+        ("w", ctypes.c_void_p), ("w_scales", ctypes.c_void_p),
+        ("topk_ids", ctypes.c_void_p), ("topk_weights", ctypes.c_void_p),
+        ("num_logical", ctypes.c_int32), ("fp32_rows", ctypes.c_int32),
+        ("sorted_token_ids", ctypes.c_void_p), ("sorted_cap", ctypes.c_int64),
+        ("expert_ids", ctypes.c_void_p), ("num_tokens_post_padded", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -155,6 +202,21 @@ def load(path: str = LIB_PATH):
             "smr_get_expert_error": ([P, ctypes.POINTER(i32)], ctypes.c_int),
             "smr_clear_expert_error": ([P], ctypes.c_int),
             "smr_tile_mxfp4_scales": ([P, i32, i32, i32, i32, P, P], ctypes.c_int),
+        })
+        U8, D8, SC = ctypes.POINTER(ExpertUpFp8Args), ctypes.POINTER(ExpertDownFp8Args), ctypes.POINTER(Scoring)
+        sigs.update({
+            "smr_expert_up_fp8_workspace_size": ([U8], sz),
+            "smr_expert_down_fp8_workspace_size": ([D8], sz),
+            "smr_expert_up_fp8": ([U8, P, sz, P], ctypes.c_int),
+            "smr_expert_down_fp8": ([D8, P, sz, P], ctypes.c_int),
+            "smr_quantize_fp8": ([P, i64, i32, i64, P, P, P], ctypes.c_int),
+            "smr_quantize_fp8_weight": ([P, i32, i32, i32, P, P, P], ctypes.c_int),
+            "smr_dequantize_fp8": ([P, P, i64, i32, P, P], ctypes.c_int),
+            "smr_select_experts": ([ctypes.POINTER(SelectArgs), P], ctypes.c_int),
+            "smr_route_scored_workspace_size": ([RA], sz),
+            "smr_route_align_scored_workspace_size": ([RA, AA], sz),
+            "smr_route_scored": ([RA, SC, P, sz, P], ctypes.c_int),
+            "smr_route_align_scored": ([RA, SC, AA, P, sz, P], ctypes.c_int),
         })
         for name, (argtypes, restype) in sigs.items():
             fn = getattr(lib, name)

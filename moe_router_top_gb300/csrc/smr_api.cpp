@@ -214,6 +214,18 @@ void check_align(const smr_align_args *a, Reasons &r, bool ids_from_route) {
     if (cap > INT32_MAX) r.unsup("capacity exceeds int32 indexing");
 }
 
+// What an align behind a route has to agree on with it.
+void check_route_align(const smr_route_args *route, smr_align_args *al, Reasons &r) {
+    const int S = route->has_shared ? 1 : 0;
+    al->routed_topk = route->topk;
+    al->routed_experts = route->E;
+    if (al->topk_ids != route->topk_ids) r.bad("align.topk_ids must equal route.topk_ids");
+    if (al->num_tokens != route->M) r.bad("align.num_tokens must equal route.M");
+    if (al->width != route->topk + S) r.bad("align.width must equal route.topk + has_shared");
+    if (al->num_experts != route->E + S) r.bad("align.num_experts must equal route.E + has_shared");
+    check_align(al, r, true);
+}
+
 size_t align_scratch_bytes(const smr_align_args *a) {
     const int64_t numel = (int64_t)a->num_tokens * a->width;
     if (numel <= smr::kAlignSingleMax) return 0;
@@ -276,10 +288,57 @@ smr::AlignLaunch make_align_launch(const smr_align_args *a, const int32_t *ids, 
     return L;
 }
 
+// The products' rows and a scored route's logits lie behind the part of a
+// workspace where a small route keeps its tagged keys (at most 16 tokens x
+// 1024 experts): that route takes a word there for its own once the tag
+// matches, so no other data may land on it when calls of both share a
+// workspace.
+constexpr size_t kDownRowsOffset = kHeaderBytes + (size_t)smr::kSmallMaxM * kMaxExperts * 8;
+
+void check_scoring(const smr_scoring &c, int E, int topk, Reasons &r) {
+    if (c.sigmoid != 0 && c.sigmoid != 1) r.bad("sigmoid must be 0 or 1 (got " + std::to_string(c.sigmoid) + ")");
+    if (c.group_best != 1 && c.group_best != 2)
+        r.bad("group_best must be 1 or 2 (got " + std::to_string(c.group_best) + ")");
+    if (!std::isfinite(c.routed_scale)) r.bad("routed_scale must be finite");
+    if (c.balance_bias && !aligned(c.balance_bias, 4)) r.bad("balance_bias must be 4-byte aligned");
+    if (c.num_groups < 1 || c.num_groups > 32) {
+        r.bad("num_groups must be in [1, 32] (got " + std::to_string(c.num_groups) + ")");
+        return;
+    }
+    if (c.topk_groups < 1 || c.topk_groups > c.num_groups)
+        r.bad("topk_groups must be in [1, num_groups] (got " + std::to_string(c.topk_groups) + ")");
+    if (E < 1 || E > kMaxExperts) return;
+    if (E % c.num_groups != 0)
+        r.bad("num_groups must divide the experts (got " + std::to_string(c.num_groups) + " groups of " + std::to_string(E) + ")");
+    else if (topk > c.topk_groups * (E / c.num_groups))
+        r.bad("topk must be at most topk_groups * (experts a group)");
+    else if (smr::score_places(E, c.num_groups) > smr::kScoreMaxPlaces)
+        r.unsup("num_groups of that many experts are not supported: (experts a group) / (32 / groups rounded up to a "
+                "power of two) must be <= 32");
+}
+
+smr::ScoreLaunch score_launch(const smr_scoring &c) {
+    smr::ScoreLaunch L{};
+    L.bias = c.balance_bias;
+    L.sigmoid = c.sigmoid;
+    L.groups = c.num_groups;
+    L.kept = c.topk_groups;
+    L.best = c.group_best;
+    L.routed_scale = c.routed_scale;
+    return L;
+}
+
+size_t scored_scratch_bytes(const smr_route_args *a) {
+    if (a->M <= 0) return 0;
+    return kDownRowsOffset - kHeaderBytes + generic_logits_bytes(a) + round_up((size_t)a->M * 4, kWsAlign);
+}
+
+// scoring: the logits only, then the selection from them.
 smr_status run_route(const smr_route_args *a, void *ws, cudaStream_t stream,
                      const smr_align_args *fused_align, int *launches,
-                     int32_t *tile_counts = nullptr) {
+                     int32_t *tile_counts = nullptr, const smr_scoring *scoring = nullptr) {
     const int S = a->has_shared ? 1 : 0;
+    uint8_t *const logits_at = static_cast<uint8_t *>(ws) + (scoring ? kDownRowsOffset : kHeaderBytes);
     if (a->M <= smr::kSmallMaxM) {
         smr::SmallRouteLaunch L{};
         L.x = static_cast<const uint16_t *>(a->hidden);
@@ -309,17 +368,32 @@ smr_status run_route(const smr_route_args *a, void *ws, cudaStream_t stream,
         const smr::StallHook hook = smr::stall_hook();
         L.stall = hook.site == smr::kStallSmallTail;
         L.stall_limit = L.stall ? hook.limit : 0;
+        // (its own selection is written over; the shared slot stays)
+        if (scoring) L.logits_out = reinterpret_cast<uint16_t *>(logits_at);
         cudaError_t e = smr::launch_small_route(L, stream);
         if (e != cudaSuccess) return cuda_fail("small-M route launch", e);
         *launches += 1;
+        if (!scoring) return SMR_OK;
+        smr::ScoreLaunch C = score_launch(*scoring);
+        C.logits = logits_at;
+        C.ld = a->E;
+        C.M = a->M; C.E = a->E; C.S = S; C.k = a->topk;
+        C.renorm = a->renormalize;
+        C.shared_done = 1;
+        C.ids = a->topk_ids;
+        C.wts = a->topk_weights;
+        C.logits_out = a->logits_out;
+        e = smr::launch_select_experts(C, stream);
+        if (e != cudaSuccess) return cuda_fail("scored select launch", e);
+        *launches += 1;
         return SMR_OK;
     }
-    if (generic_route(a)) {
+    if (generic_route(a) || scoring) {
         // the logits of every 512-column range of the gate, then the top-k
         // over whole rows
         const int64_t ld = smr::generic_logits_ld(a->E);
-        uint16_t *lg = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + kHeaderBytes);
-        float *sv = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHeaderBytes + generic_logits_bytes(a));
+        uint16_t *lg = reinterpret_cast<uint16_t *>(logits_at);
+        float *sv = reinterpret_cast<float *>(logits_at + generic_logits_bytes(a));
         for (int c0 = 0; c0 < a->E; c0 += smr::kTcRangeCols) {
             smr::TcRouteLaunch L{};
             L.x = static_cast<const uint16_t *>(a->hidden);
@@ -340,6 +414,23 @@ smr_status run_route(const smr_route_args *a, void *ws, cudaStream_t stream,
             cudaError_t e = smr::launch_tc_route(L, stream);
             if (e != cudaSuccess) return cuda_fail("tcgen05 logits launch", e);
             *launches += 1;
+        }
+        if (scoring) {
+            smr::ScoreLaunch C = score_launch(*scoring);
+            C.logits = lg;
+            C.ld = ld;
+            C.shared = sv;
+            C.shared_scale = a->shared_scale;
+            C.shared_bf16 = a->shared_logit_bf16;
+            C.M = a->M; C.E = a->E; C.S = S; C.k = a->topk;
+            C.renorm = a->renormalize;
+            C.ids = a->topk_ids;
+            C.wts = a->topk_weights;
+            C.logits_out = a->logits_out;
+            const cudaError_t e = smr::launch_select_experts(C, stream);
+            if (e != cudaSuccess) return cuda_fail("scored select launch", e);
+            *launches += 1;
+            return SMR_OK;
         }
         smr::SelectLaunch L{};
         L.logits = lg;
@@ -393,30 +484,26 @@ smr_status run_route(const smr_route_args *a, void *ws, cudaStream_t stream,
 
 // --- the experts' feed-forward ------------------------------------------------
 
-// smr_expert_down keeps its rows behind the part of a workspace where a small
-// route keeps its tagged keys (at most 16 tokens x 1024 experts): that route
-// takes a word there for its own once the tag matches, so no other data may
-// land on it when calls of both share a workspace.
-constexpr size_t kDownRowsOffset = kHeaderBytes + (size_t)smr::kSmallMaxM * kMaxExperts * 8;
 
 // What both products' arguments have in common.
 struct FfnCheck {
     int num_tokens, width, K, feat, num_experts, block_size;
     const char *k_name, *feat_name;
     const void *x, *w;
-    const uint8_t *x_scales, *w_scales;
+    const void *x_scales, *w_scales;
     const int32_t *sorted, *eids, *npp;
     int64_t sorted_cap;
     const void *out;
     const char *out_name;
     bool gated;
+    bool fp8 = false;  // E4M3: scales are required
 };
 
 void check_ffn(const FfnCheck &c, Reasons &r) {
-    const bool mx = c.x_scales != nullptr;
+    const bool mx = c.x_scales != nullptr && !c.fp8;
     if (c.num_tokens < 0) r.bad("num_tokens must be >= 0 (got " + std::to_string(c.num_tokens) + ")");
     if (c.width < 1) r.bad("width must be >= 1 (got " + std::to_string(c.width) + ")");
-    const int step = mx ? 128 : 16;
+    const int step = c.fp8 ? 32 : (mx ? 128 : 16);
     if (c.K < step || c.K > kMaxH || c.K % step != 0)
         r.bad(std::string(c.k_name) + " must be a multiple of " + std::to_string(step) + " in [" +
               std::to_string(step) + ", 16384] (got " + std::to_string(c.K) + ")");
@@ -426,14 +513,17 @@ void check_ffn(const FfnCheck &c, Reasons &r) {
         r.bad("num_experts must be in [1, 1025] (got " + std::to_string(c.num_experts) + ")");
     if (c.block_size != 64 && c.block_size != 128)
         r.unsup("block_size must be 64 or 128 (got " + std::to_string(c.block_size) + ")");
-    if ((c.x_scales == nullptr) != (c.w_scales == nullptr))
+    if (c.fp8) {
+        if (c.num_tokens > 0 && (!c.x_scales || !c.w_scales)) r.bad("x_scales and w_scales must be set");
+    } else if ((c.x_scales == nullptr) != (c.w_scales == nullptr))
         r.bad("x_scales and w_scales must both be set (MXFP4) or both be NULL (bf16)");
     if (c.num_tokens < 1 || !r.invalid.empty()) return;
     const int64_t numel = (int64_t)c.num_tokens * c.width;
     if (!c.x || !aligned(c.x, 16)) r.bad("x must be a 16-byte aligned pointer");
     if (!c.w || !aligned(c.w, 16)) r.bad("w must be a 16-byte aligned pointer");
     if (c.x_scales && !aligned(c.x_scales, 4)) r.bad("x_scales must be 4-byte aligned");
-    if (c.w_scales && !aligned(c.w_scales, 16)) r.bad("w_scales must be 16-byte aligned");
+    if (c.w_scales && !c.fp8 && !aligned(c.w_scales, 16)) r.bad("w_scales must be 16-byte aligned");
+    if (c.w_scales && c.fp8 && !aligned(c.w_scales, 4)) r.bad("w_scales must be 4-byte aligned");
     if (!c.sorted || !c.eids || !c.npp)
         r.bad("sorted_token_ids, expert_ids and num_tokens_post_padded must be set");
     else if (!aligned(c.sorted, 4) || !aligned(c.eids, 4) || !aligned(c.npp, 4))
@@ -460,6 +550,17 @@ FfnCheck down_check(const smr_expert_down_args *a) {
                     a->sorted_cap, a->out, "out", false};
 }
 
+FfnCheck up_fp8_check(const smr_expert_up_fp8_args *a) {
+    return FfnCheck{a->num_tokens, a->width, a->H, a->I, a->num_experts, a->block_size, "H", "I", a->x, a->w,
+                    a->x_scales, a->w_scales, a->sorted_token_ids, a->expert_ids, a->num_tokens_post_padded,
+                    a->sorted_cap, a->act, "act", true, true};
+}
+FfnCheck down_fp8_check(const smr_expert_down_fp8_args *a) {
+    return FfnCheck{a->num_tokens, a->width, a->I, a->H, a->num_experts, a->block_size, "I", "H", a->x, a->w,
+                    a->x_scales, a->w_scales, a->sorted_token_ids, a->expert_ids, a->num_tokens_post_padded,
+                    a->sorted_cap, a->out, "out", false, true};
+}
+
 smr::FfnLaunch ffn_launch(const FfnCheck &c, void *ws) {
     smr::FfnLaunch L{};
     L.x = c.x;
@@ -467,6 +568,7 @@ smr::FfnLaunch ffn_launch(const FfnCheck &c, void *ws) {
     L.w = c.w;
     L.w_scales = c.w_scales;
     L.gated = c.gated;
+    L.fp8 = c.fp8;
     L.width = c.width;
     L.K = c.K;
     L.feat = c.feat;
@@ -480,6 +582,32 @@ smr::FfnLaunch ffn_launch(const FfnCheck &c, void *ws) {
     L.npp = c.npp;
     L.hdr = ws;
     return L;
+}
+
+// The sum behind a second product, its rows in the workspace.
+smr_status run_product_and_sum(const char *what, smr::FfnLaunch L, bool rows32, const int32_t *ids, const float *wts,
+                               int num_logical, void *out, int T, int H, void *workspace, void *stream) {
+    L.out = static_cast<uint8_t *>(workspace) + kDownRowsOffset;
+    L.out32 = rows32;
+    const std::lock_guard<std::mutex> together(launch_lock(workspace));
+    cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(what, e);
+    const smr::CombineLaunch cl{L.out, L.out32, ids, wts, static_cast<uint16_t *>(out), T, L.width, H, num_logical};
+    e = smr::launch_expert_combine(cl, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("expert combine launch", e);
+    g_last_launches = 2;
+    return SMR_OK;
+}
+
+// What both second products ask of their sum's arguments.
+void check_sum(int T, int H, const int32_t *ids, const float *wts, int num_logical, Reasons &r) {
+    if (num_logical < 1 || num_logical > kMaxExperts + 1)
+        r.bad("num_logical must be in [1, 1025] (got " + std::to_string(num_logical) + ")");
+    if (T > 0) {
+        if (!ids || !aligned(ids, 4)) r.bad("topk_ids must be a 4-byte aligned pointer");
+        if (!wts || !aligned(wts, 4)) r.bad("topk_weights must be a 4-byte aligned pointer");
+        if ((int64_t)T * H > (int64_t)1 << 34) r.unsup("num_tokens * H must be <= 2^34");
+    }
 }
 
 // A sticky error word on the device.
@@ -595,15 +723,8 @@ SMR_API smr_status smr_route_align(const smr_route_args *route, const smr_align_
     }
     Reasons r;
     check_route(route, r);
-    const int S = route->has_shared ? 1 : 0;
     smr_align_args al = *align;
-    al.routed_topk = route->topk;
-    al.routed_experts = route->E;
-    if (align->topk_ids != route->topk_ids) r.bad("align.topk_ids must equal route.topk_ids");
-    if (align->num_tokens != route->M) r.bad("align.num_tokens must equal route.M");
-    if (align->width != route->topk + S) r.bad("align.width must equal route.topk + has_shared");
-    if (align->num_experts != route->E + S) r.bad("align.num_experts must equal route.E + has_shared");
-    check_align(&al, r, true);
+    check_route_align(route, &al, r);
     if (!r.ok()) return r.finish("smr_route_align");
     smr_status st = check_ws(workspace, workspace_bytes, smr_route_align_workspace_size(route, &al),
                              "smr_route_align");
@@ -649,15 +770,8 @@ SMR_API smr_status smr_route_align_static(const smr_route_args *route, const smr
     }
     Reasons r;
     check_route(route, r);
-    const int S = route->has_shared ? 1 : 0;
     smr_align_args al = *align;
-    al.routed_topk = route->topk;
-    al.routed_experts = route->E;
-    if (align->topk_ids != route->topk_ids) r.bad("align.topk_ids must equal route.topk_ids");
-    if (align->num_tokens != route->M) r.bad("align.num_tokens must equal route.M");
-    if (align->width != route->topk + S) r.bad("align.width must equal route.topk + has_shared");
-    if (align->num_experts != route->E + S) r.bad("align.num_experts must equal route.E + has_shared");
-    check_align(&al, r, true);
+    check_route_align(route, &al, r);
     if (route->M < 1 || route->M > smr::kSmallMaxM)
         r.unsup("the fixed-scratch entry point covers 1 <= M <= 16 (got M=" +
                 std::to_string(route->M) + ")");
@@ -747,10 +861,13 @@ static bool down_rows_fp32(const smr_expert_down_args *a) {
     return smr::expert_rows_fp32((int64_t)a->num_tokens * a->width, a->num_experts, a->H);
 }
 
-static size_t down_workspace_size(const smr_expert_down_args *args, bool rows32) {
-    if (args->num_tokens < 1 || args->width < 1 || args->H < 1) return kHeaderBytes;
-    const size_t rows = (size_t)args->num_tokens * (size_t)args->width * (size_t)args->H;
+static size_t rows_workspace_size(int num_tokens, int width, int feat, bool rows32) {
+    if (num_tokens < 1 || width < 1 || feat < 1) return kHeaderBytes;
+    const size_t rows = (size_t)num_tokens * (size_t)width * (size_t)feat;
     return kDownRowsOffset + round_up(rows * (rows32 ? 4 : 2), kWsAlign);
+}
+static size_t down_workspace_size(const smr_expert_down_args *args, bool rows32) {
+    return rows_workspace_size(args->num_tokens, args->width, args->H, rows32);
 }
 
 SMR_API size_t smr_expert_down_workspace_size(const smr_expert_down_args *args) {
@@ -797,31 +914,15 @@ static smr_status run_expert_down(const char *what, const smr_expert_down_args *
     Reasons r;
     const FfnCheck c = down_check(a);
     check_ffn(c, r);
-    if (a->num_logical < 1 || a->num_logical > kMaxExperts + 1)
-        r.bad("num_logical must be in [1, 1025] (got " + std::to_string(a->num_logical) + ")");
-    if (a->num_tokens > 0) {
-        if (!a->topk_ids || !aligned(a->topk_ids, 4)) r.bad("topk_ids must be a 4-byte aligned pointer");
-        if (!a->topk_weights || !aligned(a->topk_weights, 4)) r.bad("topk_weights must be a 4-byte aligned pointer");
-        if ((int64_t)a->num_tokens * a->H > (int64_t)1 << 34) r.unsup("num_tokens * H must be <= 2^34");
-    }
+    check_sum(a->num_tokens, a->H, a->topk_ids, a->topk_weights, a->num_logical, r);
     if (!r.ok()) return r.finish(what);
     if (a->num_tokens == 0) return SMR_OK;
     const bool rows32 = always_fp32 || down_rows_fp32(a);
     smr_status st = check_ws(workspace, workspace_bytes, down_workspace_size(a, rows32), what);
     if (st != SMR_OK) return st;
     if ((st = check_device()) != SMR_OK) return st;
-    smr::FfnLaunch L = ffn_launch(c, workspace);
-    L.out = static_cast<uint8_t *>(workspace) + kDownRowsOffset;
-    L.out32 = rows32;
-    const std::lock_guard<std::mutex> together(launch_lock(workspace));
-    cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail("expert down launch", e);
-    const smr::CombineLaunch cl{L.out, L.out32, a->topk_ids, a->topk_weights, static_cast<uint16_t *>(a->out),
-                                a->num_tokens, a->width, a->H, a->num_logical};
-    e = smr::launch_expert_combine(cl, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail("expert combine launch", e);
-    g_last_launches = 2;
-    return SMR_OK;
+    return run_product_and_sum("expert down launch", ffn_launch(c, workspace), rows32, a->topk_ids, a->topk_weights,
+                               a->num_logical, a->out, a->num_tokens, a->H, workspace, stream);
 }
 
 SMR_API smr_status smr_expert_down(const smr_expert_down_args *args, void *workspace, size_t workspace_bytes,
@@ -832,6 +933,262 @@ SMR_API smr_status smr_expert_down(const smr_expert_down_args *args, void *works
 SMR_API smr_status smr_expert_down_fp32(const smr_expert_down_args *args, void *workspace, size_t workspace_bytes,
                                         void *stream) {
     return run_expert_down("smr_expert_down_fp32", args, true, workspace, workspace_bytes, stream);
+}
+
+// --- E4M3 ---------------------------------------------------------------------
+
+SMR_API size_t smr_expert_up_fp8_workspace_size(const smr_expert_up_fp8_args *args) {
+    if (!args) return 0;
+    return args->act_scales ? rows_workspace_size(args->num_tokens, args->width, args->I, false) : kHeaderBytes;
+}
+
+SMR_API smr_status smr_expert_up_fp8(const smr_expert_up_fp8_args *a, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+    g_last_launches = 0;
+    if (!a) {
+        g_last_error = "smr_expert_up_fp8: args is NULL";
+        return SMR_ERR_INVALID_ARG;
+    }
+    Reasons r;
+    const FfnCheck c = up_fp8_check(a);
+    check_ffn(c, r);
+    if (a->act_scales && a->I % 32 != 0) r.bad("I must be a multiple of 32 with act_scales (got " + std::to_string(a->I) + ")");
+    if (a->act_scales && !aligned(a->act_scales, 4)) r.bad("act_scales must be 4-byte aligned");
+    if (a->act_scales && r.ok() && a->sorted_cap * ((a->I + 127) / 128) > (int64_t)1 << 31)
+        r.unsup("sorted_cap * ceil(I / 128) must be <= 2^31 with act_scales");
+    if (!r.ok()) return r.finish("smr_expert_up_fp8");
+    if (a->num_tokens == 0) return SMR_OK;
+    smr_status st = check_ws(workspace, workspace_bytes, smr_expert_up_fp8_workspace_size(a), "smr_expert_up_fp8");
+    if (st != SMR_OK) return st;
+    if ((st = check_device()) != SMR_OK) return st;
+    smr::FfnLaunch L = ffn_launch(c, workspace);
+    L.out = a->act_scales ? static_cast<uint8_t *>(workspace) + kDownRowsOffset : a->act;
+    const std::lock_guard<std::mutex> together(launch_lock(workspace));
+    cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("expert up launch", e);
+    g_last_launches = 1;
+    if (a->act_scales) {
+        const smr::QuantizeRows q{static_cast<const uint16_t *>(L.out), a->sorted_token_ids, a->num_tokens_post_padded,
+                                  a->sorted_cap, L.numel, a->I, static_cast<uint8_t *>(a->act), a->act_scales};
+        e = smr::launch_quantize_fp8_slots(q, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail("E4M3 quantise launch", e);
+        g_last_launches = 2;
+    }
+    return SMR_OK;
+}
+
+static bool down_fp8_rows_fp32(const smr_expert_down_fp8_args *a) {
+    return a->fp32_rows != 0 || smr::expert_rows_fp32((int64_t)a->num_tokens * a->width, a->num_experts, a->H);
+}
+
+SMR_API size_t smr_expert_down_fp8_workspace_size(const smr_expert_down_fp8_args *a) {
+    return a ? rows_workspace_size(a->num_tokens, a->width, a->H, down_fp8_rows_fp32(a)) : 0;
+}
+
+SMR_API smr_status smr_expert_down_fp8(const smr_expert_down_fp8_args *a, void *workspace, size_t workspace_bytes,
+                                       void *stream) {
+    g_last_launches = 0;
+    if (!a) {
+        g_last_error = "smr_expert_down_fp8: args is NULL";
+        return SMR_ERR_INVALID_ARG;
+    }
+    Reasons r;
+    const FfnCheck c = down_fp8_check(a);
+    check_ffn(c, r);
+    check_sum(a->num_tokens, a->H, a->topk_ids, a->topk_weights, a->num_logical, r);
+    if (a->fp32_rows != 0 && a->fp32_rows != 1) r.bad("fp32_rows must be 0 or 1 (got " + std::to_string(a->fp32_rows) + ")");
+    if (!r.ok()) return r.finish("smr_expert_down_fp8");
+    if (a->num_tokens == 0) return SMR_OK;
+    smr_status st = check_ws(workspace, workspace_bytes, smr_expert_down_fp8_workspace_size(a), "smr_expert_down_fp8");
+    if (st != SMR_OK) return st;
+    if ((st = check_device()) != SMR_OK) return st;
+    return run_product_and_sum("expert down launch", ffn_launch(c, workspace), down_fp8_rows_fp32(a), a->topk_ids,
+                               a->topk_weights, a->num_logical, a->out, a->num_tokens, a->H, workspace, stream);
+}
+
+SMR_API smr_status smr_quantize_fp8(const void *x, int64_t rows, int32_t K, int64_t ld_x, uint8_t *codes,
+                                    float *scales, void *stream) {
+    g_last_launches = 0;
+    Reasons r;
+    check_mx_shape(rows, K, r);
+    if (ld_x < K || ld_x % 8 != 0)
+        r.bad("ld_x must be >= K and a multiple of 8 (got " + std::to_string(ld_x) + ")");
+    if (rows > 0) {
+        if (!x || !aligned(x, 16)) r.bad("x must be a 16-byte aligned pointer");
+        if (!codes || !aligned(codes, 16)) r.bad("codes must be a 16-byte aligned pointer");
+        if (!scales || !aligned(scales, 4)) r.bad("scales must be a 4-byte aligned pointer");
+    }
+    if (!r.ok()) return r.finish("smr_quantize_fp8");
+    if (rows == 0) return SMR_OK;
+    const smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    const cudaError_t e = smr::launch_quantize_fp8(static_cast<const uint16_t *>(x), rows, K, ld_x, codes, scales,
+                                                   static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("E4M3 quantise launch", e);
+    g_last_launches = 1;
+    return SMR_OK;
+}
+
+SMR_API smr_status smr_quantize_fp8_weight(const void *w, int32_t matrices, int32_t N, int32_t K, uint8_t *codes,
+                                           float *scales, void *stream) {
+    g_last_launches = 0;
+    Reasons r;
+    check_mx_shape(N, K, r);
+    if (matrices < 0) r.bad("matrices must be >= 0 (got " + std::to_string(matrices) + ")");
+    if (r.ok() && (int64_t)matrices * N > ((int64_t)1 << 40) / K) r.unsup("matrices * N * K must be <= 2^40");
+    if (r.ok() && (int64_t)matrices * ((N + 127) / 128) * ((K + 127) / 128) > INT32_MAX)
+        r.unsup("blocks of 128 x 128 must be < 2^31");
+    const bool some = matrices > 0 && N > 0;
+    if (some) {
+        if (!w || !aligned(w, 16)) r.bad("w must be a 16-byte aligned pointer");
+        if (!codes || !aligned(codes, 16)) r.bad("codes must be a 16-byte aligned pointer");
+        if (!scales || !aligned(scales, 4)) r.bad("scales must be a 4-byte aligned pointer");
+    }
+    if (!r.ok()) return r.finish("smr_quantize_fp8_weight");
+    if (!some) return SMR_OK;
+    const smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    const cudaError_t e = smr::launch_quantize_fp8_weight(static_cast<const uint16_t *>(w), matrices, N, K, codes, scales,
+                                                          static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("E4M3 weight quantise launch", e);
+    g_last_launches = 1;
+    return SMR_OK;
+}
+
+SMR_API smr_status smr_dequantize_fp8(const uint8_t *codes, const float *scales, int64_t rows, int32_t K, void *out,
+                                      void *stream) {
+    g_last_launches = 0;
+    Reasons r;
+    check_mx_shape(rows, K, r);
+    if (rows > 0) {
+        if (!codes || !aligned(codes, 16)) r.bad("codes must be a 16-byte aligned pointer");
+        if (!scales || !aligned(scales, 4)) r.bad("scales must be a 4-byte aligned pointer");
+        if (!out || !aligned(out, 16)) r.bad("out must be a 16-byte aligned pointer");
+    }
+    if (!r.ok()) return r.finish("smr_dequantize_fp8");
+    if (rows == 0) return SMR_OK;
+    const smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    const cudaError_t e = smr::launch_dequantize_fp8(codes, scales, rows, K, static_cast<uint16_t *>(out),
+                                                     static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("E4M3 dequantise launch", e);
+    g_last_launches = 1;
+    return SMR_OK;
+}
+
+// --- scores -------------------------------------------------------------------
+
+SMR_API smr_status smr_select_experts(const smr_select_args *a, void *stream) {
+    g_last_launches = 0;
+    if (!a) {
+        g_last_error = "smr_select_experts: args is NULL";
+        return SMR_ERR_INVALID_ARG;
+    }
+    Reasons r;
+    if (a->M < 0) r.bad("M must be >= 0 (got " + std::to_string(a->M) + ")");
+    if (a->E < 1 || a->E > kMaxExperts) r.bad("E must be in [1, 1024] (got " + std::to_string(a->E) + ")");
+    if (a->has_shared != 0 && a->has_shared != 1)
+        r.bad("has_shared must be 0 or 1 (got " + std::to_string(a->has_shared) + ")");
+    const int S = a->has_shared ? 1 : 0;
+    if (a->topk < 1 || a->topk > a->E) r.bad("topk must be in [1, E] (got " + std::to_string(a->topk) + ")");
+    else if (a->topk + S > 32) r.unsup("topk + has_shared must be <= 32 (got " + std::to_string(a->topk + S) + ")");
+    if (a->renormalize != 0 && a->renormalize != 1)
+        r.bad("renormalize must be 0 or 1 (got " + std::to_string(a->renormalize) + ")");
+    if (a->logits_fp32 != 0 && a->logits_fp32 != 1)
+        r.bad("logits_fp32 must be 0 or 1 (got " + std::to_string(a->logits_fp32) + ")");
+    if (!std::isfinite(a->shared_scale)) r.bad("shared_scale must be finite");
+    if (!S && a->shared_logits) r.bad("shared_logits must be NULL when has_shared == 0");
+    check_scoring(a->scoring, a->E, a->topk, r);
+    if (a->M > 0) {
+        if (!a->logits || !aligned(a->logits, a->logits_fp32 ? 4 : 2)) r.bad("logits must be an aligned pointer");
+        if (a->ld_logits < a->E || a->ld_logits > (int64_t)1 << 30)
+            r.bad("ld_logits must be in [E, 2^30] (got " + std::to_string(a->ld_logits) + ")");
+        if (a->shared_logits && !aligned(a->shared_logits, 4)) r.bad("shared_logits must be 4-byte aligned");
+        if (!a->topk_ids || !aligned(a->topk_ids, 4)) r.bad("topk_ids must be a 4-byte aligned pointer");
+        if (!a->topk_weights || !aligned(a->topk_weights, 4)) r.bad("topk_weights must be a 4-byte aligned pointer");
+    }
+    if (!r.ok()) return r.finish("smr_select_experts");
+    if (a->M == 0) return SMR_OK;
+    const smr_status st = check_device();
+    if (st != SMR_OK) return st;
+    smr::ScoreLaunch L = score_launch(a->scoring);
+    L.logits = a->logits;
+    L.f32 = a->logits_fp32 != 0;
+    L.ld = a->ld_logits;
+    L.shared = a->shared_logits;
+    L.shared_scale = a->shared_scale;
+    L.M = a->M; L.E = a->E; L.S = S; L.k = a->topk;
+    L.renorm = a->renormalize;
+    L.ids = a->topk_ids;
+    L.wts = a->topk_weights;
+    const cudaError_t e = smr::launch_select_experts(L, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail("select launch", e);
+    g_last_launches = 1;
+    return SMR_OK;
+}
+
+SMR_API size_t smr_route_scored_workspace_size(const smr_route_args *args) {
+    return args ? kHeaderBytes + scored_scratch_bytes(args) : 0;
+}
+
+SMR_API size_t smr_route_align_scored_workspace_size(const smr_route_args *route, const smr_align_args *align) {
+    if (!route || !align) return 0;
+    smr_align_args al = *align;
+    al.num_tokens = route->M;
+    al.width = route->topk + (route->has_shared ? 1 : 0);
+    al.num_experts = route->E + (route->has_shared ? 1 : 0);
+    return kHeaderBytes + scored_scratch_bytes(route) + align_scratch_bytes(&al);
+}
+
+SMR_API smr_status smr_route_scored(const smr_route_args *args, const smr_scoring *scoring, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+    g_last_launches = 0;
+    if (!args || !scoring) {
+        g_last_error = "smr_route_scored: args or scoring is NULL";
+        return SMR_ERR_INVALID_ARG;
+    }
+    Reasons r;
+    check_route(args, r);
+    check_scoring(*scoring, args->E, args->topk, r);
+    if (!r.ok()) return r.finish("smr_route_scored");
+    if (args->M == 0) return SMR_OK;
+    smr_status st = check_ws(workspace, workspace_bytes, smr_route_scored_workspace_size(args), "smr_route_scored");
+    if (st != SMR_OK) return st;
+    if ((st = check_device()) != SMR_OK) return st;
+    const std::lock_guard<std::mutex> together(launch_lock(workspace));
+    int launches = 0;
+    st = run_route(args, workspace, static_cast<cudaStream_t>(stream), nullptr, &launches, nullptr, scoring);
+    if (st == SMR_OK) g_last_launches = launches;
+    return st;
+}
+
+SMR_API smr_status smr_route_align_scored(const smr_route_args *route, const smr_scoring *scoring,
+                                          const smr_align_args *align, void *workspace, size_t workspace_bytes,
+                                          void *stream) {
+    g_last_launches = 0;
+    if (!route || !scoring || !align) {
+        g_last_error = "smr_route_align_scored: route, scoring or align args is NULL";
+        return SMR_ERR_INVALID_ARG;
+    }
+    Reasons r;
+    check_route(route, r);
+    check_scoring(*scoring, route->E, route->topk, r);
+    smr_align_args al = *align;
+    check_route_align(route, &al, r);
+    if (!r.ok()) return r.finish("smr_route_align_scored");
+    smr_status st = check_ws(workspace, workspace_bytes, smr_route_align_scored_workspace_size(route, &al),
+                             "smr_route_align_scored");
+    if (st != SMR_OK) return st;
+    if ((st = check_device()) != SMR_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const std::lock_guard<std::mutex> together(launch_lock(workspace));
+    int launches = 0;
+    if (route->M > 0 && (st = run_route(route, workspace, s, nullptr, &launches, nullptr, scoring)) != SMR_OK) return st;
+    smr::AlignLaunch L = make_align_launch(&al, route->topk_ids, workspace, kHeaderBytes + scored_scratch_bytes(route));
+    const cudaError_t e = smr::launch_align(L, s);
+    if (e != cudaSuccess) return cuda_fail("align launch", e);
+    g_last_launches = launches + smr::align_launches(L.numel, false);
+    return SMR_OK;
 }
 
 SMR_API smr_status smr_quantize_mxfp4(const void *x, int64_t rows, int32_t K, int64_t ld_x, uint8_t *codes,

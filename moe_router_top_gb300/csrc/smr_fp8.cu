@@ -1,0 +1,237 @@
+// smr_fp8.cu -- E4M3 with one fp32 scale per 128 values (activations: along a
+// row; weights: per 128 x 128 block): quantisation and its inverse, in the
+// format that the route's launch writes ("Netra Kernel ...", Fusing the
+// activation/quantization boundary).
+//
+// scale = amax / 448, codes = E4M3(x * (448 / amax)) rounded to nearest even,
+// the quotients and the product in fp32. amax counts as 2^-110 at the least
+// (448 / amax overflows below 2^-119 and every value would saturate); a block
+// of zeros has scale 0 and codes +0. A block with a NaN or an infinity gets a
+// NaN scale and codes +0.
+#include <cuda_fp16.h>
+
+#include "smr_device.cuh"
+#include "smr_launch.h"
+
+namespace smr {
+
+constexpr int kFp8Threads = 256;
+constexpr int kFp8Vecs = 4;  // 16-byte vectors (8 values) a thread has in flight
+
+// A block's scale and the factor for its values; m: the largest magnitude's
+// bf16 bits (as unsigned integers magnitudes order like their values, with
+// infinities and NaN above all). The factor is 0 for blocks of codes +0.
+__device__ __forceinline__ void block_scale_e4m3(uint32_t m, float &scale, float &factor) {
+    const float amax = fmaxf(__uint_as_float(m << 16), 0x1p-110f);
+    scale = m == 0u ? 0.0f : (m >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.0f));
+    factor = m == 0u || m >= 0x7F80u ? 0.0f : __fdiv_rn(448.0f, amax);
+}
+__device__ __forceinline__ uint32_t abs_max8(const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0u;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m = max(m, max(w[u] & 0x7FFFu, (w[u] >> 16) & 0x7FFFu));
+    return m;
+}
+// Eight values to codes (NaN times a factor of 0 is still NaN: those are cleared).
+__device__ __forceinline__ uint2 codes8(const uint4 &v, float factor) {
+    float f[8];
+    unpack8(v, f);
+    uint16_t h[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[u]) : "f"(f[2 * u + 1] * factor), "f"(f[2 * u] * factor));
+    if (factor == 0.0f) return make_uint2(0u, 0u);
+    return make_uint2((uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16);
+}
+
+// Bound by memory: 2 bytes read and 1 written per value. One 16-byte load per
+// 8 values, 16 neighbouring lanes share a block; kFp8Vecs independent loads a
+// thread cover the latency. A row's last block may be short (K / 8 vectors a
+// row, whole blocks of 16 counted).
+__global__ void __launch_bounds__(kFp8Threads)
+quantize_fp8_kernel(const uint16_t *__restrict__ x, int64_t ld, uint32_t row_vecs, uint32_t row_blocks, uint32_t blocks,
+                    uint8_t *__restrict__ codes, float *__restrict__ scales) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t first = blockIdx.x * (kFp8Threads / 16 * kFp8Vecs) + threadIdx.x / 16, in = threadIdx.x & 15;
+    uint4 v[kFp8Vecs];
+    int64_t at[kFp8Vecs];  // the vector among the codes, -1: none
+#pragma unroll
+    for (int j = 0; j < kFp8Vecs; ++j) {
+        const uint32_t b = first + j * (kFp8Threads / 16);
+        const uint32_t row = b / row_blocks, vec = (b - row * row_blocks) * 16 + in;
+        at[j] = b < blocks && vec < row_vecs ? (int64_t)row * row_vecs + vec : -1;
+        v[j] = at[j] >= 0 ? ld_stream_rows_v4(x + (int64_t)row * ld + vec * 8) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < kFp8Vecs; ++j) {
+        uint32_t m = abs_max8(v[j]);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float scale, factor;
+        block_scale_e4m3(m, scale, factor);
+        const uint2 c = codes8(v[j], factor);
+        if (at[j] >= 0) reinterpret_cast<uint2 *>(codes)[at[j]] = c;
+        const uint32_t b = first + j * (kFp8Threads / 16);
+        if (in == 0 && b < blocks) scales[b] = scale;
+    }
+}
+
+// The same for the rows of the slots that an align lists (no other row is
+// written): a 16-lane group takes a block of one listed row a step. The grid
+// covers the SMs; what lies past num_tokens_post_padded costs nothing.
+__global__ void __launch_bounds__(kFp8Threads)
+quantize_fp8_slots_kernel(const QuantizeRows p, uint32_t row_blocks) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t in = threadIdx.x & 15;
+    const int64_t rows = min((int64_t)max(__ldcg(p.npp), 0), p.sorted_cap);
+    const uint32_t blocks = (uint32_t)(rows * row_blocks), row_vecs = (uint32_t)p.K / 8;  // (blocks < 2^31)
+    const uint32_t step = gridDim.x * (kFp8Threads / 16);
+    for (uint32_t b0 = blockIdx.x * (kFp8Threads / 16); b0 < blocks; b0 += kFp8Vecs * step) {
+        uint4 v[kFp8Vecs];
+        int64_t at[kFp8Vecs];   // the vector among the codes, -1: none
+        int64_t sat[kFp8Vecs];  // the block among the scales, -1: none
+#pragma unroll
+        for (int j = 0; j < kFp8Vecs; ++j) {
+            const uint32_t b = b0 + j * step + threadIdx.x / 16;
+            const uint32_t r = b / row_blocks, kb = b - r * row_blocks, vec = kb * 16 + in;
+            const int slot = b < blocks ? __ldcg(p.sorted + r) : -1;
+            const bool real = slot >= 0 && slot < p.numel;
+            at[j] = real && vec < row_vecs ? (int64_t)slot * row_vecs + vec : -1;
+            sat[j] = real && in == 0 ? (int64_t)slot * row_blocks + kb : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kFp8Vecs; ++j)
+            v[j] = at[j] >= 0 ? ld_stream_rows_v4(p.x + at[j] * 8) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < kFp8Vecs; ++j) {
+            uint32_t m = abs_max8(v[j]);
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float scale, factor;
+            block_scale_e4m3(m, scale, factor);
+            const uint2 c = codes8(v[j], factor);
+            if (at[j] >= 0) reinterpret_cast<uint2 *>(p.codes)[at[j]] = c;
+            if (sat[j] >= 0) p.scales[sat[j]] = scale;
+        }
+    }
+}
+
+// Weights, once: a CTA per 128 x 128 block of one of the matrices [N][K].
+__global__ void __launch_bounds__(kFp8Threads)
+quantize_fp8_weight_kernel(const uint16_t *__restrict__ w, uint32_t N, uint32_t K, uint32_t row_blocks, uint32_t col_blocks,
+                           uint8_t *__restrict__ codes, float *__restrict__ scales) {
+    __shared__ uint32_t top[kFp8Threads / 32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t kb = blockIdx.x % col_blocks, rb = blockIdx.x / col_blocks % row_blocks, e = blockIdx.x / col_blocks / row_blocks;
+    const uint32_t k = kb * 128 + threadIdx.x % 16 * 8;
+    constexpr int kRows = 128 * 16 / kFp8Threads;
+    uint4 v[kRows];
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+        const uint32_t r = rb * 128 + threadIdx.x / 16 + j * (kFp8Threads / 16);
+        v[j] = r < N && k < K ? ld_stream_rows_v4(w + ((int64_t)e * N + r) * K + k) : make_uint4(0u, 0u, 0u, 0u);
+        m = max(m, abs_max8(v[j]));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (threadIdx.x % 32 == 0) top[threadIdx.x / 32] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFp8Threads / 32; ++i) m = max(m, top[i]);
+    float scale, factor;
+    block_scale_e4m3(m, scale, factor);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+        const uint32_t r = rb * 128 + threadIdx.x / 16 + j * (kFp8Threads / 16);
+        const uint2 c = codes8(v[j], factor);
+        if (r < N && k < K) *reinterpret_cast<uint2 *>(codes + ((int64_t)e * N + r) * K + k) = c;
+    }
+    if (threadIdx.x == 0) scales[blockIdx.x] = scale;
+}
+
+// Bound by memory: 8 codes to 8 bf16 values a step (E4M3 is exact in half
+// precision), times the scale in fp32, rounded once.
+__global__ void __launch_bounds__(kFp8Threads)
+dequantize_fp8_kernel(const uint8_t *__restrict__ codes, const float *__restrict__ scales, uint32_t row_vecs,
+                      uint32_t row_blocks, uint32_t vecs, uint16_t *__restrict__ out) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t first = blockIdx.x * (kFp8Threads * kFp8Vecs) + threadIdx.x;
+    uint2 c[kFp8Vecs];
+    float s[kFp8Vecs];
+#pragma unroll
+    for (int j = 0; j < kFp8Vecs; ++j) {
+        const uint32_t i = first + j * kFp8Threads, row = i / row_vecs;
+        c[j] = i < vecs ? __ldcg(reinterpret_cast<const uint2 *>(codes) + i) : make_uint2(0u, 0u);
+        s[j] = i < vecs ? __ldcg(scales + (int64_t)row * row_blocks + (i - row * row_vecs) / 16) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kFp8Vecs; ++j) {
+        const uint32_t i = first + j * kFp8Threads;
+        const uint16_t h[4] = {(uint16_t)c[j].x, (uint16_t)(c[j].x >> 16), (uint16_t)c[j].y, (uint16_t)(c[j].y >> 16)};
+        uint32_t o[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint32_t f16;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f16) : "h"(h[u]));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&f16));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * s[j], f.y * s[j]);
+            o[u] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        if (i < vecs) reinterpret_cast<uint4 *>(out)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+static cudaLaunchConfig_t fp8_config(int64_t ctas, cudaStream_t stream, cudaLaunchAttribute *attr) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(kFp8Threads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+cudaError_t launch_quantize_fp8(const uint16_t *x, int64_t rows, int K, int64_t ld, uint8_t *codes, float *scales,
+                                cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    const uint32_t row_blocks = (uint32_t)(K + 127) / 128, blocks = (uint32_t)(rows * row_blocks);
+    const int64_t per = kFp8Threads / 16 * kFp8Vecs;
+    const cudaLaunchConfig_t cfg = fp8_config((blocks + per - 1) / per, stream, attr);
+    return cudaLaunchKernelEx(&cfg, quantize_fp8_kernel, x, ld, (uint32_t)(K / 8), row_blocks, blocks, codes, scales);
+}
+
+cudaError_t launch_quantize_fp8_slots(const QuantizeRows &a, cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    const uint32_t row_blocks = (uint32_t)(a.K + 127) / 128;
+    const int64_t per = kFp8Threads / 16, need = (a.sorted_cap * row_blocks + per - 1) / per;
+    const int64_t room = 8 * (int64_t)sm_count();
+    const cudaLaunchConfig_t cfg = fp8_config(need < room ? need : room, stream, attr);
+    return cudaLaunchKernelEx(&cfg, quantize_fp8_slots_kernel, a, row_blocks);
+}
+
+cudaError_t launch_quantize_fp8_weight(const uint16_t *w, int matrices, int N, int K, uint8_t *codes, float *scales,
+                                       cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    const uint32_t row_blocks = (uint32_t)(N + 127) / 128, col_blocks = (uint32_t)(K + 127) / 128;
+    const cudaLaunchConfig_t cfg = fp8_config((int64_t)matrices * row_blocks * col_blocks, stream, attr);
+    return cudaLaunchKernelEx(&cfg, quantize_fp8_weight_kernel, w, (uint32_t)N, (uint32_t)K, row_blocks, col_blocks, codes,
+                              scales);
+}
+
+cudaError_t launch_dequantize_fp8(const uint8_t *codes, const float *scales, int64_t rows, int K, uint16_t *out,
+                                  cudaStream_t stream) {
+    cudaLaunchAttribute attr[1];
+    const uint32_t row_vecs = (uint32_t)(K / 8), vecs = (uint32_t)(rows * row_vecs);
+    const int64_t per = kFp8Threads * kFp8Vecs;
+    const cudaLaunchConfig_t cfg = fp8_config(((int64_t)vecs + per - 1) / per, stream, attr);
+    return cudaLaunchKernelEx(&cfg, dequantize_fp8_kernel, codes, scales, row_vecs, (uint32_t)(K + 127) / 128, vecs, out);
+}
+
+}  // namespace smr

@@ -153,6 +153,29 @@ struct SelectLaunch {
     uint16_t *logits_out;    // optional [M][E]
 };
 cudaError_t launch_select(const SelectLaunch &a, cudaStream_t stream);
+
+// Scores, groups and top-k of every token row from its logits.
+struct ScoreLaunch {
+    const void *logits;      // [M][ld], fp32 (f32) or bf16
+    bool f32;
+    int64_t ld;
+    const float *bias;       // [E] added to the scores for the choice alone, or nullptr
+    const float *shared;     // [M] shared logits, or nullptr: the slot's weight is shared_scale
+    int M, E, S, k;
+    int sigmoid, renorm;
+    int groups, kept, best;  // E / groups experts a group; kept of them stay, by the sum of their `best` largest
+    float routed_scale, shared_scale;
+    int shared_bf16;         // the shared logit is rounded to bf16 before the sigmoid
+    int shared_done;         // slot k was written by the kernel before
+    int32_t *ids;            // [M][k + S]
+    float *wts;
+    uint16_t *logits_out;    // optional [M][E] copy of bf16 logits
+    int nk, log_groups, group_size;  // set by the launcher
+};
+// Experts that a lane holds (score_places), at most.
+constexpr int kScoreMaxPlaces = 32;
+int score_places(int E, int groups, int *log_groups = nullptr);
+cudaError_t launch_select_experts(const ScoreLaunch &a, cudaStream_t stream);
 // A 2-D bf16 tensor map with the 128-byte swizzle (rows of row_bytes; boxes
 // of box_inner x box_outer elements); false if it cannot be encoded.
 bool make_tma_map_2d(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t outer,
@@ -178,14 +201,15 @@ cudaError_t launch_expert_gemm(const ExpertGemmLaunch &a, cudaStream_t stream);
 // feat][K], out = silu(gate) * up) or the plain one (w [num_experts][feat][K])
 // over the align's blocks; out bf16 (or fp32) [numel][feat], one row per
 // routed slot.
-// x_scales != nullptr: x and w are MXFP4 codes.
+// x_scales != nullptr: x and w are MXFP4 codes, or E4M3 codes (fp8).
 struct FfnLaunch {
     const void *x;
-    int64_t ld_x;            // row stride (bf16 only, elements)
-    const uint8_t *x_scales; // E8M0, one row per row of x, [K / 32]
+    int64_t ld_x;            // row stride (elements; not MXFP4)
+    const void *x_scales;    // E8M0, one row per row of x, [K / 32]; E4M3: fp32 [ceil(K / 128)]
     const void *w;
-    const uint8_t *w_scales; // E8M0, tiled (mxfp4_weight_tiles)
-    bool gated;
+    const void *w_scales;    // E8M0, tiled (mxfp4_weight_tiles); E4M3: fp32 [num_experts]
+                             // [ceil(feat / 128) (gated: twice)][ceil(K / 128)]
+    bool gated, fp8;
     int width, K, feat, A, num_experts;
     int64_t numel, sorted_cap;
     const int32_t *sorted, *eids, *npp;
@@ -197,6 +221,9 @@ struct FfnLaunch {
 // where the caller leaves it open.
 bool expert_rows_fp32(int64_t numel, int num_experts, int H);
 cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream);
+cudaError_t launch_expert_product_fp8(const FfnLaunch &a, int sms, cudaStream_t stream);
+// Whether a product of that many rows runs on CTA pairs.
+bool expert_pairs(int64_t numel, int num_experts);
 // The word on the current device that gets every product's error bits.
 cudaError_t expert_error_word(void **ptr);
 
@@ -221,6 +248,28 @@ cudaError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales,
                                     cudaStream_t stream);
 cudaError_t launch_tile_mxfp4_scales(const uint8_t *scales, int E, int N, int K, bool gated, uint8_t *tiled,
                                      cudaStream_t stream);
+
+// E4M3 codes with an fp32 scale per 128 values of a row, or per 128 x 128 block
+// of each of `matrices` weights [N][K]; at most 2^29 blocks, 2^31 vectors of 8.
+cudaError_t launch_quantize_fp8(const uint16_t *x, int64_t rows, int K, int64_t ld, uint8_t *codes, float *scales,
+                                cudaStream_t stream);
+// The rows of the slots that an align lists.
+struct QuantizeRows {
+    const uint16_t *x;       // bf16 [numel][K]
+    const int32_t *sorted, *npp;
+    int64_t sorted_cap, numel;
+    int K;
+    uint8_t *codes;          // [numel][K]
+    float *scales;           // [numel][ceil(K / 128)]
+};
+cudaError_t launch_quantize_fp8_slots(const QuantizeRows &a, cudaStream_t stream);
+cudaError_t launch_quantize_fp8_weight(const uint16_t *w, int matrices, int N, int K, uint8_t *codes, float *scales,
+                                       cudaStream_t stream);
+cudaError_t launch_dequantize_fp8(const uint8_t *codes, const float *scales, int64_t rows, int K, uint16_t *out,
+                                  cudaStream_t stream);
+
+// SMs of the current device (0: it cannot be asked).
+int sm_count();
 
 // moe_align_block_size.
 struct AlignLaunch {

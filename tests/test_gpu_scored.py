@@ -1,0 +1,215 @@
+"""Scores, balance bias, groups and top-k (select_experts and the scored route)
+against a greedy pick in 64 bits. Needs a GB300.
+
+Ids are equal; weights are off by a few roundings and by that of the
+exponential's argument, a difference of two logits: (8 + d) 2^-23 relative for
+logits that differ by d, and half the smallest subnormal number.
+"""
+from __future__ import annotations
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_ffn import smr  # noqa: E402, F401
+
+BIG = torch.finfo(torch.float32).max
+
+
+def _finite(x):
+    return torch.nan_to_num(x.double(), nan=-BIG, posinf=BIG, neginf=-BIG)
+
+
+def _reference(logits, k, scoring, bias, groups, kept, best, renorm, scale):
+    x = _finite(logits)
+    T, E = x.shape
+    top = x.amax(1, keepdim=True)
+    if scoring == "sigmoid":
+        score = torch.where(x < 0, torch.exp(x) / (1 + torch.exp(x)), 1 / (1 + torch.exp(-x)))
+    else:
+        score = torch.exp(x - top) / torch.exp(x - top).sum(1, keepdim=True)
+    choice = score if bias is None else score + _finite(bias)
+    row = torch.arange(T, device=x.device)
+    keep = torch.ones(T, groups, dtype=torch.bool, device=x.device)
+    if groups > 1:
+        value = choice.view(T, groups, -1).topk(min(best, E // groups), dim=-1).values.sum(-1)
+        keep[:] = False
+        for _ in range(kept):
+            g = (value == value.amax(1, keepdim=True)).int().argmax(1)
+            keep[row, g] = True
+            value[row, g] = -float("inf")
+    order = x if bias is None else choice
+    left = torch.where(keep.repeat_interleave(E // groups, 1), order, torch.full_like(order, -float("inf")))
+    ids = torch.empty(T, k, dtype=torch.long, device=x.device)
+    for j in range(k):
+        ids[:, j] = (left == left.amax(1, keepdim=True)).int().argmax(1)
+        left[row, ids[:, j]] = -float("inf")
+    xs = torch.gather(x, 1, ids)
+    if not renorm:
+        w = torch.gather(score, 1, ids)
+    elif scoring == "sigmoid":  # relative to the largest e^x, as far as that is below 1
+        shift = xs.amax(1, keepdim=True).clamp(max=0)
+        w = torch.where(xs < 0, torch.exp(xs - shift) / (1 + torch.exp(xs)), 1 / (1 + torch.exp(-xs)))
+        w = w / w.sum(1, keepdim=True)
+    else:
+        w = torch.exp(xs - xs.amax(1, keepdim=True))
+        w = w / w.sum(1, keepdim=True)
+    spread = ((top if scoring == "softmax" else xs.abs().amax(1, keepdim=True)) - xs).clamp(max=120)
+    tol = (8 + spread) * 2.0 ** -23 * (w * scale).abs() + 2.0 ** -150 * (1 + abs(scale))
+    return ids, w * scale, tol
+
+
+def _check(smr, logits, k, scoring="sigmoid", bias=None, groups=1, kept=None, best=1, renorm=True, scale=1.0):
+    kept = groups if kept is None else kept
+    E = logits.shape[1]
+    ids, w = smr.select_experts(logits, topk=k, scoring=scoring, balance_bias=bias, num_groups=groups, topk_groups=kept,
+                                group_best=best, renormalize=renorm, routed_scale=scale)
+    assert smr.last_launch_count() == (1 if logits.shape[0] else 0)
+    rid, rw, tol = _reference(logits, k, scoring, bias, groups, kept, best, renorm, scale)
+    assert ids.dtype == torch.int32 and torch.equal(ids.long(), rid)
+    assert ((w.double() - rw).abs() <= tol).all(), ((w.double() - rw).abs() / tol).max()
+
+
+def _logits(M, E, seed, std=1.5, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(M, E, device="cuda", generator=g) * std).to(dtype), g
+
+
+# M, E, k, groups, kept, best
+SHAPES = [
+    (1, 1, 1, 1, 1, 1),
+    (1, 8, 8, 1, 1, 1),
+    (4, 512, 10, 1, 1, 1),
+    (3, 60, 6, 4, 2, 2),       # 15 experts a group
+    (33, 20, 4, 5, 3, 2),      # groups that are no power of two
+    (100, 256, 8, 8, 4, 2),
+    (257, 128, 8, 16, 3, 1),
+    (50, 1024, 31, 1, 1, 1),
+    (50, 1024, 32, 32, 2, 2),
+    (9, 96, 7, 32, 5, 2),      # three experts a group
+    (9, 32, 5, 32, 5, 2),      # one expert a group
+    (2047, 160, 6, 8, 3, 1),
+    (5000, 384, 8, 1, 1, 1),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_select_matches_64_bits(smr, shape, scoring, dtype):
+    M, E, k, groups, kept, best = shape
+    logits, g = _logits(M, E, M + E, dtype=dtype)
+    bias = torch.randn(E, device="cuda", generator=g) * 0.1
+    for b in (None, bias, torch.zeros_like(bias)):
+        for renorm in (True, False):
+            _check(smr, logits, k, scoring, b, groups, kept, best, renorm, 2.5 if b is None else 1.0)
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_choices_next_to_each_other(smr, scoring):
+    """Choices that 32 bits do not tell apart: a bias that undoes the first row's scores, groups too."""
+    logits, g = _logits(16, 256, 5)
+    logits = logits[:1] + torch.randn(16, 256, device="cuda", generator=g) * 1e-7
+    s = torch.sigmoid(logits[0].double()) if scoring == "sigmoid" else torch.softmax(logits[0].double(), 0)
+    for target in (0.7, -3.0, 40.0):
+        bias = (target - s).float()
+        for groups, kept, best in ((1, 1, 1), (8, 4, 2), (8, 4, 1)):
+            _check(smr, logits, 8, scoring, bias, groups, kept, best)
+
+
+def test_equal_choices_take_the_lower_id(smr):
+    flat = torch.zeros(3, 256, device="cuda")
+    for scoring in ("sigmoid", "softmax"):
+        for groups, kept in ((1, 1), (8, 3)):
+            for bias in (None, torch.zeros(256, device="cuda"), torch.full((256,), -2.0, device="cuda")):
+                _check(smr, flat, 9, scoring, bias, groups, kept, 2)
+    few = torch.randint(-2, 3, (500, 256), device="cuda").float()
+    for bias in (None, torch.randint(0, 2, (256,), device="cuda").float()):
+        _check(smr, few, 9, "sigmoid", bias, 8, 4, 2)
+    signed = torch.where(torch.rand(64, 128, device="cuda") < 0.5, 0.0, -0.0)
+    _check(smr, signed.to(torch.bfloat16), 8)
+
+
+def test_large_logits(smr):
+    """Scores that saturate: the order is the logits' without a bias."""
+    logits, g = _logits(64, 256, 8, std=30.0)
+    for scoring in ("sigmoid", "softmax"):
+        for renorm in (True, False):
+            _check(smr, logits, 8, scoring, None, renorm=renorm)
+    _check(smr, logits - 200.0, 8, "sigmoid")  # e^-200: renormalised, the ratios stay
+    _check(smr, logits.clamp(max=30.0), 8, "sigmoid", torch.randn(256, device="cuda", generator=g))
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_not_finite(smr, scoring):
+    inf, nan = float("inf"), float("nan")
+    logits, _ = _logits(8, 64, 3)
+    logits[0] = -inf                 # a row that a mask leaves nothing of
+    logits[1, 5:] = -inf             # fewer than k left
+    logits[2, 7] = nan
+    logits[3] = nan
+    logits[4, [3, 9]] = inf
+    logits[5] = inf
+    logits[6, ::2] = torch.finfo(torch.float32).min
+    bias = torch.linspace(-0.5, 0.5, 64, device="cuda")
+    cut = bias.clone()
+    cut[10:20], cut[20], cut[21] = -inf, nan, inf
+    for b in (None, bias, cut):
+        for groups, kept, best in ((1, 1, 1), (4, 2, 1), (4, 2, 2)):
+            for renorm in (True, False):
+                _check(smr, logits, 6, scoring, b, groups, kept, best, renorm)
+
+
+def test_strides_and_outputs(smr):
+    wide, _ = _logits(70, 200, 6)
+    for dtype in (torch.float32, torch.bfloat16):
+        view = wide.to(dtype)[:, 3:131]
+        _check(smr, view, 8)
+        ids, w = smr.select_experts(view, topk=8, scoring="sigmoid")
+        again = smr.select_experts(view.contiguous(), topk=8, scoring="sigmoid")
+        assert torch.equal(ids, again[0]) and torch.equal(w, again[1])
+    out_i = torch.full((72, 9), -7, dtype=torch.int32, device="cuda")
+    out_w = torch.full((72, 9), -7.0, device="cuda")
+    smr.select_experts(view, topk=8, has_shared=True, shared_scale=0.5, topk_ids=out_i[1:71], topk_weights=out_w[1:71])
+    assert (out_i[[0, 71]] == -7).all() and (out_w[[0, 71]] == -7).all()
+    assert (out_i[1:71, 8] == 128).all() and (out_w[1:71, 8] == 0.5).all()
+    shared = torch.linspace(-120, 50, 70, device="cuda")
+    _, w = smr.select_experts(view, topk=8, has_shared=True, shared_scale=0.5, shared_logits=shared)
+    ref = 0.5 * torch.sigmoid(shared.double())
+    assert ((w[:, 8].double() - ref).abs() <= 2e-6 * ref + 2.0 ** -147).all()
+    empty_i, empty_w = smr.select_experts(wide[:0], topk=4)
+    assert empty_i.shape == (0, 4) and empty_w.shape == (0, 4) and smr.last_launch_count() == 0
+
+
+@pytest.mark.parametrize("M,E,S", [(1, 64, 0), (16, 512, 1), (17, 512, 1), (40, 96, 1), (300, 1000, 0)])
+def test_scored_route(smr, M, E, S):
+    """The route's logits, selected from as select_experts would, then the align."""
+    g = torch.Generator(device="cuda").manual_seed(M + E)
+    x = torch.randn(M, 256, device="cuda", generator=g).to(torch.bfloat16)
+    gate = (torch.randn(E, 256, device="cuda", generator=g) / 12).to(torch.bfloat16)
+    ws_ = (torch.randn(1, 256, device="cuda", generator=g) / 12).to(torch.bfloat16) if S else None
+    bias = torch.randn(E, device="cuda", generator=g) * 0.1
+    how = dict(topk=6, scoring="sigmoid", balance_bias=bias, num_groups=8, topk_groups=4, group_best=2)
+    logits = torch.empty(M, E, dtype=torch.bfloat16, device="cuda")
+    codes, scales = torch.empty(M, 256, dtype=torch.uint8, device="cuda"), torch.empty(M, 2, device="cuda")
+    ws = smr.Workspace()
+    ids, w = smr.route(x, gate, ws_, logits_out=logits, hidden_fp8=codes, hidden_scales=scales, shared_scale=0.75,
+                       routed_scale=2.0, workspace=ws, **how)
+    plain = torch.empty_like(logits)
+    pid, pw = smr.route(x, gate, ws_, topk=6, logits_out=plain, shared_scale=0.75, workspace=ws)
+    assert torch.equal(logits, plain)
+    sid, sw = smr.select_experts(logits, routed_scale=2.0, **how)
+    assert torch.equal(ids[:, :6], sid) and torch.equal(w[:, :6], sw)
+    if S:
+        assert (ids[:, 6] == E).all()
+        assert torch.allclose(w[:, 6], pw[:, 6], rtol=2e-6, atol=0)
+    c, s = smr.quantize_fp8(x)
+    assert torch.equal(c, codes) and torch.equal(s, scales)
+    got = smr.route_align(x, gate, ws_, block_size=64, shared_scale=0.75, routed_scale=2.0, workspace=ws, **how)
+    assert torch.equal(got[0], ids) and torch.equal(got[1], w)
+    al = smr.align(ids, E + S, 64)
+    n = int(al[2])
+    assert n == int(got[4]) and torch.equal(al[0][:n], got[2][:n]) and torch.equal(al[1][: n // 64], got[3][: n // 64])
+    assert smr.get_device_error(ws) == 0
