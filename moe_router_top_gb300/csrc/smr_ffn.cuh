@@ -72,19 +72,22 @@ struct FfInfo {
 template <bool FP8>
 constexpr int kFfAccs = FP8 ? 4 : 2;
 // E4M3: scales of a piece's columns for kFp8Group k-blocks, and of the weight
-// tile (of its gate and of its up rows), in a ring of their own.
+// tile's gate and up rows, in a ring of their own. (Of the second product: the
+// columns' times the tile's. Of the gated one both products would take as much
+// again to read, and reading them is what bounds the epilogue.)
 constexpr int kFp8Group = 4, kFp8Ring = 3;
 template <int COLS>
-constexpr int kFp8ScaleBytes = kFp8Group * (COLS + 2) * 4;
+constexpr int kFp8ScaleBytes = kFp8Group * (COLS + 4) * 4;
 template <bool FP8>
 constexpr int kFfBars = 2 * kFfMaxStages + 2 * kFfAccs<FP8> + 2 * kFfInfos + 1 + (FP8 ? 2 * kFp8Ring : 0);
 template <bool FP8>
 constexpr int kFfBarBytes = (kFfBars<FP8> * 8 + 8 + 15) / 16 * 16;
 // Columns of a piece, at most. (A pair of MXFP4: 128, as two accumulators of
-// 256 columns would leave no room in TMEM for the scales.)
+// 256 columns would leave no room in TMEM for the scales. A pair of E4M3: 128,
+// as the epilogue holds the columns' sums in registers.)
 template <bool MX, bool PAIR, bool FP8 = false>
 constexpr int kFfCols = PAIR && !MX && !FP8 ? 256 : 128;
-template <bool MX, bool PAIR, bool FP8 = false>
+template <bool MX, bool UP, bool PAIR, bool FP8 = false>
 constexpr int kFfMiscBytes = kFfBarBytes<FP8> + kFfInfos * (int)sizeof(FfInfo<kFfCols<MX, PAIR, FP8>>) +
                              (FP8 ? kFp8Ring * kFp8ScaleBytes<kFfCols<MX, PAIR, FP8>> : 0);
 
@@ -362,16 +365,168 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
             " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
             ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
-// Two fp32 values in one instruction.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
-        " mov.b64 {%0, %1}, d;\n}" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
-__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float2 b) {
-    asm("{\n .reg .b64 a, b, d;\n mov.b64 d, {%0, %1};\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-        " fma.rn.f32x2 d, a, b, d;\n mov.b64 {%0, %1}, d;\n}" : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(b.x), "f"(b.y));
+
+// The warp that reads the align's outputs ahead and hands out the work.
+// An item is a group of blocks of one expert (one block; PAIR: up to
+// COLS / A, counted from the expert's first) and a weight tile (PAIR:
+// two). Both CTAs of a pair walk the same items. CTAs take every
+// gridDim-th item: a block's tiles run next to each other in time
+// (its rows stay in L2), blocks of one expert too (its weights).
+// UP: rows of x by token, else by slot. AHEAD: items whose entries are under way.
+template <bool UP, bool PAIR, int COLS, int INFOS, int AHEAD>
+__device__ __forceinline__ void ff_scout(const FfParams &p, FfInfo<COLS> *info, uint64_t *info_full, uint64_t *info_empty,
+                                         volatile int *abort_flag, uint32_t rank) {
+    const int lane = threadIdx.x & 31;
+    const int A = p.A, G = PAIR ? COLS / A : 1;
+    const int tiles = PAIR ? (p.ntiles + 1) / 2 : p.ntiles;
+    const int ctas = PAIR ? gridDim.x >> 1 : gridDim.x, cta = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    const int dgrp = ctas / tiles, dtile = ctas % tiles;
+    int grp = cta / tiles, tile = cta % tiles;  // the item
+    const int bo = 8 * lane / A, po = 8 * lane % A;  // this lane's 8 entries: block of the group, place in it
+    const bool in = bo < G;
+    const bool wide = (reinterpret_cast<uintptr_t>(p.sorted) & 15) == 0;
+    // the entries and the block's expert (of blocks below `limit`),
+    // requested AHEAD items ahead (a round trip to L2 is longer than two
+    // short items)
+    auto fetch = [&](int b0, int limit, int (&ent)[8], int &e) {
+        const int b = b0 + bo;
+        if (!in || b0 < 0 || b >= limit) return;
+        const int64_t at = (int64_t)b * A + po;
+        e = __ldcg(p.eids + b);
+        if (wide && at + 8 <= p.sorted_cap) {
+            const int4 lo = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at));
+            const int4 hi = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at) + 1);
+            ent[0] = lo.x; ent[1] = lo.y; ent[2] = lo.z; ent[3] = lo.w;
+            ent[4] = hi.x; ent[5] = hi.y; ent[6] = hi.z; ent[7] = hi.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ent[j] = at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
+        }
+    };
+    auto step = [&](int &g, int &t) {
+        g += dgrp;
+        t += dtile;
+        if (t >= tiles) {
+            t -= tiles;
+            ++g;
+        }
+    };
+        int ent[AHEAD][8], e[AHEAD], at[AHEAD], slot[8];  // (at: first block of the item's group)
+    int grp2 = grp, tile2 = tile;  // the item that is requested next
+    const int npp = __ldcg(p.npp);
+    // (requested with npp: of blocks past it, left out below)
+    const int first_e = PAIR && lane < p.max_blocks ? __ldcg(p.eids + lane) : 0;
+    if constexpr (!PAIR) {  // the first two at once with npp: what lies past it is left out below
+        int g = grp, t = tile;
+        fetch(g, p.max_blocks, ent[0], e[0]);
+        step(g, t);
+        fetch(g, p.max_blocks, ent[1], e[1]);
+    }
+    const int nblk = max(0, min(npp / A, p.max_blocks));
+    // First block of group g (asked for in ascending order), -1 past the
+    // last: 32 blocks at a time, a bit for every block that starts one,
+    // which is every G-th block of an expert's segment.
+    int scan_at = -32, scan_base = 0, last_e = 0, run = 0;  // (run: blocks of the segment before the 32)
+    uint32_t starts = 0u;
+    auto locate = [&](int g) {
+        if constexpr (PAIR) {
+            while (g - scan_base >= __popc(starts)) {
+                if (scan_at + 32 >= nblk) return -1;
+                scan_base += __popc(starts);
+                scan_at += 32;
+                const int b = scan_at + lane, eb = scan_at == 0 ? first_e : (b < nblk ? __ldcg(p.eids + b) : 0);
+                int before = __shfl_up_sync(0xffffffffu, eb, 1);
+                if (lane == 0) before = last_e;
+                const uint32_t first = __ballot_sync(0xffffffffu, b == 0 || eb != before);
+                const uint32_t upto = first & (0xffffffffu >> (31 - lane));
+                const int place = upto != 0u ? lane - (31 - __clz(upto)) : run + lane;
+                starts = __ballot_sync(0xffffffffu, b < nblk && place % G == 0);
+                last_e = __shfl_sync(0xffffffffu, eb, 31);
+                run = __shfl_sync(0xffffffffu, place, 31) + 1;
+            }
+            // the bit with g - scan_base others below it
+            const bool hit = (starts >> lane & 1u) && __popc(starts & ((1u << lane) - 1u)) == g - scan_base;
+            return scan_at + __ffs(__ballot_sync(0xffffffffu, hit)) - 1;
+        } else {
+            return g < nblk ? g : -1;
+        }
+    };
+    RingPos iq;
+    bool ok = true;
+    auto post = [&](int n, int nt, int e, const int (&slot)[8]) {
+        if (!(ok = warp_wait(&info_empty[iq.i], iq.ph ^ 1u, abort_flag))) return;
+        FfInfo<COLS> *inf = info + iq.i;
+        const int c = 8 * lane;
+        if (c < n) {
+            int row[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                row[j] = slot[j];
+                if (UP && slot[j] >= 0) row[j] = (int)((uint64_t)(uint32_t)slot[j] * p.div_mul >> p.div_shift);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                *reinterpret_cast<int4 *>(inf->slot + c + j) = make_int4(slot[j], slot[j + 1], slot[j + 2], slot[j + 3]);
+                *reinterpret_cast<int4 *>(inf->row + c + j) = make_int4(row[j], row[j + 1], row[j + 2], row[j + 3]);
+            }
+        }
+        if (lane == 0) *reinterpret_cast<int4 *>(inf) = make_int4(n, nt, e, 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&info_full[iq.i]));
+        iq.next(INFOS);
+    };
+    // every block's entries into L2, each line by one CTA
+    for (int64_t i = ((int64_t)blockIdx.x * 32 + lane) * 32; i < min((int64_t)nblk * A, p.sorted_cap);
+         i += (int64_t)gridDim.x * 32 * 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sorted + i));
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+        at[u] = locate(grp2);
+        if (PAIR || u >= 2) fetch(at[u], nblk, ent[u], e[u]);
+        step(grp2, tile2);
+    }
+    auto take = [&](int &at, int (&ent)[8], int &e) {
+        // the item whose first block is `at`; then the one AHEAD later is requested
+        int top = 0;
+        bool bad = false;
+        const bool here = in && at + bo < nblk;
+        const int ex = here ? e : -1;
+        const int eg = __shfl_sync(0xffffffffu, ex, 0);
+        int h = 1;  // blocks of the group
+        while (h < G && at + h < nblk && __shfl_sync(0xffffffffu, ex, h * A / 8) == eg) ++h;
+        const bool mine = here && bo < h;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = mine ? ent[j] : p.numel;
+            const bool real = (uint32_t)i < (uint32_t)p.numel;
+            bad |= !real && i != p.numel;
+            slot[j] = real ? i : -1;
+            if (real) top = 8 * lane + j + 1;
+        }
+        // neither a slot nor the sentinel: a corrupted align output
+        if (bad) ffn_error(p, kErrBadSlot);
+        __syncwarp();
+        const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
+        const int nt = PAIR ? 2 * tile + (int)rank : tile;
+        at = locate(grp2);
+        fetch(at, nblk, ent, e);
+        step(grp, tile);
+        step(grp2, tile2);
+        if (rows == 0) return;
+        if ((unsigned)eg >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
+            if (lane == 0) ffn_error(p, kErrBadId);
+            __syncwarp();
+            return;
+        }
+        post((rows + 15) & ~15, nt, eg, slot);
+    };
+    while (ok && at[0] >= 0) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (ok && at[u] >= 0) take(at[u], ent[u], e[u]);
+    }
+    if (ok) post(-1, 0, 0, slot);
+    __syncwarp();
 }
 
 // MX: MXFP4 operands, else bf16. UP: the gated product (a tile holds 64
@@ -411,7 +566,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Info *info = reinterpret_cast<Info *>(misc + kFfBarBytes<FP8>);
     float *scale_ring = reinterpret_cast<float *>(misc + kFfBarBytes<FP8> + kFfInfos * sizeof(Info));
-    uint8_t *out_rows = misc + kFfMiscBytes<MX, PAIR, FP8>;
+    uint8_t *out_rows = misc + kFfMiscBytes<MX, UP, PAIR, FP8>;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -462,509 +617,364 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
     const uint32_t x_off = SUB * kFfWBytes, ws_off = x_off + SUB * p.b_bytes, xs_off = ws_off + 2 * SUB * kSfAtom;
     int issued = 0;  // stages whose weights were requested (warp 0)
 
-    if (warp == 0) {
-        // ---------------------------------------------------- weights ----
-        const bool elected = elect_one();
-        RingPos st, iq;
-        bool ok = true;
-        while (ok) {
-            if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
-            const volatile Info *inf = info + iq.i;
-            const int n = inf->n, nt = inf->nt, e = inf->e;
-            __syncwarp();
-            if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
-            iq.next(kFfInfos);
-            if (n < 0) break;
-            const uint8_t *scales = nullptr;
-            if constexpr (MX) scales = p.w_scales + ((int64_t)e * p.ntiles + nt) * p.num_chunks * kSfAtom;
-            for (int kb = 0; kb < p.num_kb; kb += SUB) {
-                if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
-                const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
-                const uint32_t bar = smem_u32(&full[st.i]);
-                const int subs = SUB == 1 ? 1 : min(SUB, p.num_kb - kb);
-                if (elected) {
-                    if constexpr (PAIR) {
-                        // both CTAs' bytes complete the leader's barrier
-                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * (subs * kFfWBytes + (MX ? 2 * SUB * kSfAtom : 0)));
-                        const uint32_t fb = cluster_addr(bar, 0u);
-                        // (the last stage's box may reach into the next tile's scales; they are not used)
-                        if constexpr (MX)
-                            tma_load_2d_pair(base + ws_off, &tm_s, 0, (e * p.ntiles + min(nt, p.ntiles - 1)) * p.num_chunks + 2 * kb, fb);
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u) {
-                            if (u >= subs) break;
-                            const int xk = (kb + u) * (MX || FP8 ? kFfRowBytes : kFfRowBytes / 2);
-                            if constexpr (UP) tma_load_5d_pair(base + u * kFfWBytes, &tm_w, xk, nt * 4, e, fb);
-                            else tma_load_3d_pair(base + u * kFfWBytes, &tm_w, xk, nt * kFfRows, e, fb);
-                        }
-                    } else {
-                        uint32_t sbytes = 0;
-                        if constexpr (MX) sbytes = (uint32_t)min(2 * SUB, p.num_chunks - 2 * kb) * kSfAtom;
-                        mbar_arrive_expect_tx(bar, subs * kFfWBytes + sbytes);
-#pragma unroll
-                        for (int u = 0; u < SUB; ++u) {
-                            if (u >= subs) break;
-                            const int xk = (kb + u) * (MX || FP8 ? kFfRowBytes : kFfRowBytes / 2);
-                            if constexpr (UP) tma_load_5d(base + u * kFfWBytes, &tm_w, xk, nt * 4, e, bar);
-                            else tma_load_3d(base + u * kFfWBytes, &tm_w, xk, nt * kFfRows, e, bar);
-                        }
-                        if constexpr (MX) bulk_load(base + ws_off, scales + 2 * kb * kSfAtom, sbytes, bar);
-                    }
-                }
-                ++issued;
-                st.next(ST);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------------ scout ----
-        // An item is a group of blocks of one expert (one block; PAIR: up to
-        // kCols / A, counted from the expert's first) and a weight tile (PAIR:
-        // two). Both CTAs of a pair walk the same items. CTAs take every
-        // gridDim-th item: a block's tiles run next to each other in time
-        // (its rows stay in L2), blocks of one expert too (its weights).
-        const int A = p.A, G = PAIR ? kCols / A : 1;
-        const int tiles = PAIR ? (p.ntiles + 1) / 2 : p.ntiles;
-        const int ctas = PAIR ? gridDim.x >> 1 : gridDim.x, cta = PAIR ? blockIdx.x >> 1 : blockIdx.x;
-        const int dgrp = ctas / tiles, dtile = ctas % tiles;
-        int grp = cta / tiles, tile = cta % tiles;  // the item
-        const int bo = 8 * lane / A, po = 8 * lane % A;  // this lane's 8 entries: block of the group, place in it
-        const bool in = bo < G;
-        const bool wide = (reinterpret_cast<uintptr_t>(p.sorted) & 15) == 0;
-        // the entries and the block's expert (of blocks below `limit`),
-        // requested kAhead items ahead (a round trip to L2 is longer than two
-        // short items)
-        auto fetch = [&](int b0, int limit, int (&ent)[8], int &e) {
-            const int b = b0 + bo;
-            if (!in || b0 < 0 || b >= limit) return;
-            const int64_t at = (int64_t)b * A + po;
-            e = __ldcg(p.eids + b);
-            if (wide && at + 8 <= p.sorted_cap) {
-                const int4 lo = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at));
-                const int4 hi = __ldcg(reinterpret_cast<const int4 *>(p.sorted + at) + 1);
-                ent[0] = lo.x; ent[1] = lo.y; ent[2] = lo.z; ent[3] = lo.w;
-                ent[4] = hi.x; ent[5] = hi.y; ent[6] = hi.z; ent[7] = hi.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ent[j] = at + j < p.sorted_cap ? __ldcg(p.sorted + at + j) : p.numel;
-            }
-        };
-        auto step = [&](int &g, int &t) {
-            g += dgrp;
-            t += dtile;
-            if (t >= tiles) {
-                t -= tiles;
-                ++g;
-            }
-        };
-        constexpr int kAhead = 4;
-        int ent[kAhead][8], e[kAhead], at[kAhead], slot[8];  // (at: first block of the item's group)
-        int grp2 = grp, tile2 = tile;  // the item that is requested next
-        const int npp = __ldcg(p.npp);
-        // (requested with npp: of blocks past it, left out below)
-        const int first_e = PAIR && lane < p.max_blocks ? __ldcg(p.eids + lane) : 0;
-        if constexpr (!PAIR) {  // the first two at once with npp: what lies past it is left out below
-            int g = grp, t = tile;
-            fetch(g, p.max_blocks, ent[0], e[0]);
-            step(g, t);
-            fetch(g, p.max_blocks, ent[1], e[1]);
-        }
-        const int nblk = max(0, min(npp / A, p.max_blocks));
-        // First block of group g (asked for in ascending order), -1 past the
-        // last: 32 blocks at a time, a bit for every block that starts one,
-        // which is every G-th block of an expert's segment.
-        int scan_at = -32, scan_base = 0, last_e = 0, run = 0;  // (run: blocks of the segment before the 32)
-        uint32_t starts = 0u;
-        auto locate = [&](int g) {
-            if constexpr (PAIR) {
-                while (g - scan_base >= __popc(starts)) {
-                    if (scan_at + 32 >= nblk) return -1;
-                    scan_base += __popc(starts);
-                    scan_at += 32;
-                    const int b = scan_at + lane, eb = scan_at == 0 ? first_e : (b < nblk ? __ldcg(p.eids + b) : 0);
-                    int before = __shfl_up_sync(0xffffffffu, eb, 1);
-                    if (lane == 0) before = last_e;
-                    const uint32_t first = __ballot_sync(0xffffffffu, b == 0 || eb != before);
-                    const uint32_t upto = first & (0xffffffffu >> (31 - lane));
-                    const int place = upto != 0u ? lane - (31 - __clz(upto)) : run + lane;
-                    starts = __ballot_sync(0xffffffffu, b < nblk && place % G == 0);
-                    last_e = __shfl_sync(0xffffffffu, eb, 31);
-                    run = __shfl_sync(0xffffffffu, place, 31) + 1;
-                }
-                // the bit with g - scan_base others below it
-                const bool hit = (starts >> lane & 1u) && __popc(starts & ((1u << lane) - 1u)) == g - scan_base;
-                return scan_at + __ffs(__ballot_sync(0xffffffffu, hit)) - 1;
-            } else {
-                return g < nblk ? g : -1;
-            }
-        };
-        RingPos iq;
-        bool ok = true;
-        auto post = [&](int n, int nt, int e, const int (&slot)[8]) {
-            if (!(ok = warp_wait(&info_empty[iq.i], iq.ph ^ 1u, abort_flag))) return;
-            Info *inf = info + iq.i;
-            const int c = 8 * lane;
-            if (c < n) {
-                int row[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    row[j] = slot[j];
-                    if (UP && slot[j] >= 0) row[j] = (int)((uint64_t)(uint32_t)slot[j] * p.div_mul >> p.div_shift);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    *reinterpret_cast<int4 *>(inf->slot + c + j) = make_int4(slot[j], slot[j + 1], slot[j + 2], slot[j + 3]);
-                    *reinterpret_cast<int4 *>(inf->row + c + j) = make_int4(row[j], row[j + 1], row[j + 2], row[j + 3]);
-                }
-            }
-            if (lane == 0) *reinterpret_cast<int4 *>(inf) = make_int4(n, nt, e, 0);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&info_full[iq.i]));
-            iq.next(kFfInfos);
-        };
-        // every block's entries into L2, each line by one CTA
-        for (int64_t i = ((int64_t)blockIdx.x * 32 + lane) * 32; i < min((int64_t)nblk * A, p.sorted_cap);
-             i += (int64_t)gridDim.x * 32 * 32)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sorted + i));
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            at[u] = locate(grp2);
-            if (PAIR || u >= 2) fetch(at[u], nblk, ent[u], e[u]);
-            step(grp2, tile2);
-        }
-        auto take = [&](int &at, int (&ent)[8], int &e) {
-            // the item whose first block is `at`; then the one kAhead later is requested
-            int top = 0;
-            bool bad = false;
-            const bool here = in && at + bo < nblk;
-            const int ex = here ? e : -1;
-            const int eg = __shfl_sync(0xffffffffu, ex, 0);
-            int h = 1;  // blocks of the group
-            while (h < G && at + h < nblk && __shfl_sync(0xffffffffu, ex, h * A / 8) == eg) ++h;
-            const bool mine = here && bo < h;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int i = mine ? ent[j] : p.numel;
-                const bool real = (uint32_t)i < (uint32_t)p.numel;
-                bad |= !real && i != p.numel;
-                slot[j] = real ? i : -1;
-                if (real) top = 8 * lane + j + 1;
-            }
-            // neither a slot nor the sentinel: a corrupted align output
-            if (bad) ffn_error(p, kErrBadSlot);
-            __syncwarp();
-            const int rows = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
-            const int nt = PAIR ? 2 * tile + (int)rank : tile;
-            at = locate(grp2);
-            fetch(at, nblk, ent, e);
-            step(grp, tile);
-            step(grp2, tile2);
-            if (rows == 0) return;
-            if ((unsigned)eg >= (unsigned)p.num_experts) {  // only a corrupted align output gets here
-                if (lane == 0) ffn_error(p, kErrBadId);
+    if (warp < kFirst + kLoaders) {
+        if (warp == 0) {
+            // ---------------------------------------------------- weights ----
+            const bool elected = elect_one();
+            RingPos st, iq;
+            bool ok = true;
+            while (ok) {
+                if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+                const volatile Info *inf = info + iq.i;
+                const int n = inf->n, nt = inf->nt, e = inf->e;
                 __syncwarp();
-                return;
-            }
-            post((rows + 15) & ~15, nt, eg, slot);
-        };
-        while (ok && at[0] >= 0) {
+                if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
+                iq.next(kFfInfos);
+                if (n < 0) break;
+                const uint8_t *scales = nullptr;
+                if constexpr (MX) scales = p.w_scales + ((int64_t)e * p.ntiles + nt) * p.num_chunks * kSfAtom;
+                for (int kb = 0; kb < p.num_kb; kb += SUB) {
+                    if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
+                    const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
+                    const uint32_t bar = smem_u32(&full[st.i]);
+                    const int subs = SUB == 1 ? 1 : min(SUB, p.num_kb - kb);
+                    if (elected) {
+                        if constexpr (PAIR) {
+                            // both CTAs' bytes complete the leader's barrier
+                            if (rank == 0) mbar_arrive_expect_tx(bar, 2 * (subs * kFfWBytes + (MX ? 2 * SUB * kSfAtom : 0)));
+                            const uint32_t fb = cluster_addr(bar, 0u);
+                            // (the last stage's box may reach into the next tile's scales; they are not used)
+                            if constexpr (MX)
+                                tma_load_2d_pair(base + ws_off, &tm_s, 0, (e * p.ntiles + min(nt, p.ntiles - 1)) * p.num_chunks + 2 * kb, fb);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (ok && at[u] >= 0) take(at[u], ent[u], e[u]);
-        }
-        if (ok) post(-1, 0, 0, slot);
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------- MMAs ----
-        // The whole warp runs the loop, so that descriptors and addresses stay
-        // in uniform registers; one elected lane issues (a pair's leader; its
-        // peer only keeps up with the pieces).
-        const bool elected = elect_one();
-        RingPos st, iq, ac;
-        uint32_t sf = tmem + (uint32_t)(2 * p.acc_cols);  // MXFP4: two sets of scale columns in turn: [A 8][B 8]
-        bool ok = true;
-        while (ok) {
-            if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
-            const int n = __shfl_sync(0xffffffffu, reinterpret_cast<volatile Info *>(info)[iq.i].n, 0);
+                            for (int u = 0; u < SUB; ++u) {
+                                if (u >= subs) break;
+                                const int xk = (kb + u) * (MX || FP8 ? kFfRowBytes : kFfRowBytes / 2);
+                                if constexpr (UP) tma_load_5d_pair(base + u * kFfWBytes, &tm_w, xk, nt * 4, e, fb);
+                                else tma_load_3d_pair(base + u * kFfWBytes, &tm_w, xk, nt * kFfRows, e, fb);
+                            }
+                        } else {
+                            uint32_t sbytes = 0;
+                            if constexpr (MX) sbytes = (uint32_t)min(2 * SUB, p.num_chunks - 2 * kb) * kSfAtom;
+                            mbar_arrive_expect_tx(bar, subs * kFfWBytes + sbytes);
+#pragma unroll
+                            for (int u = 0; u < SUB; ++u) {
+                                if (u >= subs) break;
+                                const int xk = (kb + u) * (MX || FP8 ? kFfRowBytes : kFfRowBytes / 2);
+                                if constexpr (UP) tma_load_5d(base + u * kFfWBytes, &tm_w, xk, nt * 4, e, bar);
+                                else tma_load_3d(base + u * kFfWBytes, &tm_w, xk, nt * kFfRows, e, bar);
+                            }
+                            if constexpr (MX) bulk_load(base + ws_off, scales + 2 * kb * kSfAtom, sbytes, bar);
+                        }
+                    }
+                    ++issued;
+                    st.next(ST);
+                }
+            }
             __syncwarp();
-            if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
-            iq.next(kFfInfos);
-            if (n < 0) break;
-            if (rank != 0) continue;
-            constexpr int kM = PAIR ? 2 * kFfRows : kFfRows;
-            if constexpr (FP8) {
-                const uint32_t idesc = idesc_e4m3(kM, n);
-                for (int kb = 0; ok && kb < p.num_kb; kb += SUB) {
+        } else if (warp == 2) {
+            ff_scout<UP, PAIR, kCols, kFfInfos, 4>(p, info, info_full, info_empty, abort_flag, rank);
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------- MMAs ----
+            // The whole warp runs the loop, so that descriptors and addresses stay
+            // in uniform registers; one elected lane issues (a pair's leader; its
+            // peer only keeps up with the pieces).
+            const bool elected = elect_one();
+            RingPos st, iq, ac;
+            uint32_t sf = tmem + (uint32_t)(2 * p.acc_cols);  // MXFP4: two sets of scale columns in turn: [A 8][B 8]
+            bool ok = true;
+            while (ok) {
+                if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+                const int n = __shfl_sync(0xffffffffu, reinterpret_cast<volatile Info *>(info)[iq.i].n, 0);
+                __syncwarp();
+                if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
+                iq.next(kFfInfos);
+                if (n < 0) break;
+                if (rank != 0) continue;
+                constexpr int kM = PAIR ? 2 * kFfRows : kFfRows;
+                if constexpr (FP8) {
+                    const uint32_t idesc = idesc_e4m3(kM, n);
+                    for (int kb = 0; ok && kb < p.num_kb; kb += SUB) {
+                        if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
+                        const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u) {
+                            if (SUB > 1 && kb + u >= p.num_kb) break;
+                            if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
+                            tc_fence_after();
+                            const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols);
+                            const uint64_t da = smem_desc_sw<128>(base + u * kFfWBytes),
+                                           db = smem_desc_sw<128>(base + x_off + u * p.b_bytes);
+                            const int steps = kb + u + 1 == p.num_kb ? p.last_steps : 4;
+                            if (elected) {
+                                if (steps == 4) {
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                                } else {
+                                    for (int kk = 0; kk < steps; ++kk)
+                                        tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                                }
+                                ff_commit<PAIR>(&acc_full[ac.i]);
+                            }
+                            ac.next(p.accs);
+                        }
+                        if (!ok) break;
+                        if (elected) ff_commit<PAIR>(&empty[st.i]);
+                        st.next(ST);
+                    }
+                    continue;
+                }
+                if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols);
+                const uint32_t idesc = MX ? idesc_mxf4(kM, n) : idesc_bf16_f32(kM, n);
+                for (int kb = 0; kb < p.num_kb; kb += SUB) {
                     if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
+                    tc_fence_after();
                     const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
                         if (SUB > 1 && kb + u >= p.num_kb) break;
-                        if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
-                        tc_fence_after();
-                        const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols);
+                        // descriptors: + 2 per 32 bytes of K
                         const uint64_t da = smem_desc_sw<128>(base + u * kFfWBytes),
                                        db = smem_desc_sw<128>(base + x_off + u * p.b_bytes);
                         const int steps = kb + u + 1 == p.num_kb ? p.last_steps : 4;
-                        if (elected) {
+                        const uint32_t more = kb + u != 0 ? 1u : 0u;
+                        if constexpr (MX) {
+                            const uint32_t sa = base + ws_off + 2 * u * kSfAtom, sb = base + xs_off + 2 * u * kSfAtom;
+                            if (elected) {
+                                tc_cp_scales<PAIR>(sf, sa);
+                                tc_cp_scales<PAIR>(sf + 8, sb);
+                                tc_mma_mxf4<PAIR>(acc, da, db, idesc, sf, sf + 8, more);
+                                tc_mma_mxf4<PAIR>(acc, da + 2, db + 2, idesc | (1u << 30) | (1u << 5), sf, sf + 8, 1u);
+                                if (steps == 4) {
+                                    tc_cp_scales<PAIR>(sf + 4, sa + kSfAtom);
+                                    tc_cp_scales<PAIR>(sf + 12, sb + kSfAtom);
+                                    tc_mma_mxf4<PAIR>(acc, da + 4, db + 4, idesc, sf + 4, sf + 12, 1u);
+                                    tc_mma_mxf4<PAIR>(acc, da + 6, db + 6, idesc | (1u << 30) | (1u << 5), sf + 4, sf + 12, 1u);
+                                }
+                            }
+                            sf ^= 16u;
+                        } else if (elected) {
                             if (steps == 4) {
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                                    ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
                             } else {
                                 for (int kk = 0; kk < steps; ++kk)
-                                    tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                                    ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
                             }
-                            ff_commit<PAIR>(&acc_full[ac.i]);
                         }
-                        ac.next(p.accs);
                     }
-                    if (!ok) break;
                     if (elected) ff_commit<PAIR>(&empty[st.i]);
                     st.next(ST);
                 }
-                continue;
+                if (!ok) break;
+                if (elected) ff_commit<PAIR>(&acc_full[ac.i]);
+                ac.next(2);
             }
-            if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols);
-            const uint32_t idesc = MX ? idesc_mxf4(kM, n) : idesc_bf16_f32(kM, n);
-            for (int kb = 0; kb < p.num_kb; kb += SUB) {
-                if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
-                tc_fence_after();
-                const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
+            // every MMA issued is done before TMEM is freed, also after an abort
+            if (rank == 0) {
+                if (elected) {
+                    if constexpr (PAIR) tc_commit_pair(smem_u32(last), 0x1);
+                    else tc_commit(smem_u32(last));
+                }
+                volatile int never = 0;
+                if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
+            }
+            __syncwarp();
+        } else if (FP8 && warp == 3) {
+            // ----------------------------------------------------- scales ----
+            // E4M3: for every kFp8Group k-blocks the scales of the piece's columns
+            // and of the weight tile. Of 16 columns those that a
+            // thread of the epilogue holds, 2 t, 2 t + 1, 8 + 2 t and 9 + 2 t, lie
+            // next to each other. A row's scales are requested before the wait
+            // for the ring.
+            if constexpr (FP8) {
+                constexpr int kSets = kCols / 32;
+                const int place = (lane & 16) + (lane & 6) * 2 + (lane & 8) / 4 + (lane & 1);
+                RingPos sc, iq;
+                bool ok = true;
+                while (ok) {
+                    if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+                    const Info *inf = info + iq.i;
+                    const int n = inf->n;
+                    if (n >= 0) {
+                        int row[kSets];
 #pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    if (SUB > 1 && kb + u >= p.num_kb) break;
-                    // descriptors: + 2 per 32 bytes of K
-                    const uint64_t da = smem_desc_sw<128>(base + u * kFfWBytes),
-                                   db = smem_desc_sw<128>(base + x_off + u * p.b_bytes);
-                    const int steps = kb + u + 1 == p.num_kb ? p.last_steps : 4;
-                    const uint32_t more = kb + u != 0 ? 1u : 0u;
-                    if constexpr (MX) {
-                        const uint32_t sa = base + ws_off + 2 * u * kSfAtom, sb = base + xs_off + 2 * u * kSfAtom;
-                        if (elected) {
-                            tc_cp_scales<PAIR>(sf, sa);
-                            tc_cp_scales<PAIR>(sf + 8, sb);
-                            tc_mma_mxf4<PAIR>(acc, da, db, idesc, sf, sf + 8, more);
-                            tc_mma_mxf4<PAIR>(acc, da + 2, db + 2, idesc | (1u << 30) | (1u << 5), sf, sf + 8, 1u);
-                            if (steps == 4) {
-                                tc_cp_scales<PAIR>(sf + 4, sa + kSfAtom);
-                                tc_cp_scales<PAIR>(sf + 12, sb + kSfAtom);
-                                tc_mma_mxf4<PAIR>(acc, da + 4, db + 4, idesc, sf + 4, sf + 12, 1u);
-                                tc_mma_mxf4<PAIR>(acc, da + 6, db + 6, idesc | (1u << 30) | (1u << 5), sf + 4, sf + 12, 1u);
+                        for (int j = 0; j < kSets; ++j) row[j] = lane + 32 * j < n ? inf->row[lane + 32 * j] : -1;
+                        const int tile = min(inf->nt, p.ntiles - 1);
+                        // lanes 0 to 3: the tile's scales, 4 to 7: those of its up rows
+                        const int wrow = UP ? (tile >> 1) + (lane & 4 ? p.scale_rows >> 1 : 0) : tile;
+                        const float *ws = reinterpret_cast<const float *>(p.w_scales) +
+                                          ((int64_t)inf->e * p.scale_rows + wrow) * p.num_kb + (lane & 3);
+                        for (int kb = 0; kb < p.num_kb; kb += kFp8Group) {
+                            uint32_t v[kSets][kFp8Group];
+                            float w = 0.0f;
+                            if (lane < 8 && kb + (lane & 3) < p.num_kb) w = __ldcg(ws + kb);
+#pragma unroll
+                            for (int j = 0; j < kSets; ++j) {
+                                const uint32_t *src = reinterpret_cast<const uint32_t *>(p.x_scales) +
+                                                      (uint64_t)(uint32_t)row[j] * (uint32_t)p.num_kb + kb;
+#pragma unroll
+                                for (int q = 0; q < kFp8Group; ++q) v[j][q] = 0u;
+                                if (p.scale_bytes == 16) {
+                                    ld_cg_16(v[j], src, row[j]);
+                                } else if (p.scale_bytes == 8) {
+#pragma unroll
+                                    for (int q = 0; q < kFp8Group; q += 2)
+                                        ld_cg_8(v[j] + q, src + q, kb + q < p.num_kb ? row[j] : -1);
+                                } else {
+#pragma unroll
+                                    for (int q = 0; q < kFp8Group; ++q)
+                                        if (row[j] >= 0 && kb + q < p.num_kb) v[j][q] = __ldcg(src + q);
+                                }
                             }
-                        }
-                        sf ^= 16u;
-                    } else if (elected) {
-                        if (steps == 4) {
+                            __syncwarp();
+                            if (!(ok = warp_wait(&scale_empty[sc.i], sc.ph ^ 1u, abort_flag))) break;
+                            float *to = scale_ring + sc.i * (kFp8ScaleBytes<kCols> / 4) + place;
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
-                        } else {
-                            for (int kk = 0; kk < steps; ++kk)
-                                ff_mma_bf16<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : more);
+                            for (int q = 0; q < kFp8Group; ++q) {
+                                const float wg = __shfl_sync(0xffffffffu, w, q), wu = __shfl_sync(0xffffffffu, w, 4 + q);
+#pragma unroll
+                                for (int j = 0; j < kSets; ++j) {
+                                    if (32 * j >= n) break;
+                                    const float x = __uint_as_float(v[j][q]);
+                                    to[q * (kCols + 4) + 32 * j] = UP ? x : x * wg;
+                                }
+                                if (UP && lane < 2) to[q * (kCols + 4) + kCols - place + lane] = lane == 0 ? wg : wu;
+                            }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&scale_full[sc.i]));
+                            sc.next(kFp8Ring);
                         }
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
+                    iq.next(kFfInfos);
+                    if (n < 0) break;
                 }
-                if (elected) ff_commit<PAIR>(&empty[st.i]);
-                st.next(ST);
+                __syncwarp();
             }
-            if (!ok) break;
-            if (elected) ff_commit<PAIR>(&acc_full[ac.i]);
-            ac.next(2);
-        }
-        // every MMA issued is done before TMEM is freed, also after an abort
-        if (rank == 0) {
-            if (elected) {
-                if constexpr (PAIR) tc_commit_pair(smem_u32(last), 0x1);
-                else tc_commit(smem_u32(last));
-            }
-            volatile int never = 0;
-            if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
-        }
-        __syncwarp();
-    } else if (FP8 && warp == 3) {
-        // ----------------------------------------------------- scales ----
-        // E4M3: for every kFp8Group k-blocks the scales of the piece's columns
-        // and of the weight tile, k-block by k-block, so that the epilogue
-        // reads those of neighbouring columns at once. A row's are next to
-        // each other; they are requested before the wait for the ring.
-        if constexpr (FP8) {
-            constexpr int kSets = kCols / 32;
-            RingPos sc, iq;
+        } else {
+            // ------------------------------------------------ routed rows ----
+            // Each loader warp fills every kLoaders-th stage, so that a stage is
+            // waited for, copied, made visible to the tensor core (async proxy)
+            // and announced by one warp, while the others' copies are in flight.
+            // A row's k-block is eight 16-byte chunks; eight neighbouring lanes
+            // copy a row's, chunk c of row r landing at r * 128 + ((c ^ (r & 7)) <<
+            // 4), the 128-byte swizzle.
+            // A parity wait tells a stage's last use from the one before only: a
+            // warp that waits for stage j (counted over all uses) must know that
+            // j - 2 * ST was consumed. It waited for j - kLoaders, so everything
+            // up to j - kLoaders - ST was: hence kLoaders <= ST.
+            const int c = lane & 7;
+            RingPos st, iq;
+            int next = warp - kFirst;  // this warp's next stage, counted from the piece's first
+            st.skip(next, ST);
             bool ok = true;
             while (ok) {
                 if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
                 const Info *inf = info + iq.i;
-                const int n = inf->n;
-                if (n >= 0) {
-                    int row[kSets];
+                const int all = inf->n;
+                // this CTA's rows are columns [col0, col0 + n)
+                const int n = PAIR ? all / 2 : all, col0 = (int)rank * n;
+                if (all >= 0) {
+                    const int count = (p.num_kb + SUB - 1) / SUB;
+                    for (; next < count; next += kLoaders) {
+                        if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
+                        const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
+                        const int kb = next * SUB;
+                        // MXFP4: this lane's columns' scales of the stage. Where rows
+                        // can be read in wider pieces they pass through registers,
+                        // requested before the rows are copied and stored after:
+                        // a gather of 32 rows costs the load unit 32 cycles
+                        // whatever its width, and 4-byte copies take four for the
+                        // 16 bytes of a stage (MXFP4 up, 16384 tokens: a
+                        // tenth longer with those than with 16-byte loads).
+                        constexpr int kSets = MX ? kCols / 32 : 1, kWords = 2 * SUB;
+                        uint32_t scale[kSets][kWords];
+                        int srow[kSets];
+                        if constexpr (MX) {
 #pragma unroll
-                    for (int j = 0; j < kSets; ++j) row[j] = lane + 32 * j < n ? inf->row[lane + 32 * j] : -1;
-                    const int tile = min(inf->nt, p.ntiles - 1);
-                    // lanes 0 to 3: the tile's scales, 4 to 7: those of its up rows
-                    const int wrow = UP ? (tile >> 1) + (lane & 4 ? p.scale_rows >> 1 : 0) : tile;
-                    const float *ws = reinterpret_cast<const float *>(p.w_scales) +
-                                      ((int64_t)inf->e * p.scale_rows + wrow) * p.num_kb + (lane & 3);
-                    for (int kb = 0; kb < p.num_kb; kb += kFp8Group) {
-                        uint32_t v[kSets][kFp8Group];
+                            for (int j = 0; j < kSets; ++j) {
+                                srow[j] = lane + 32 * j < all ? inf->row[lane + 32 * j] : -1;
 #pragma unroll
-                        for (int j = 0; j < kSets; ++j) {
-                            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.x_scales) +
-                                                  (uint64_t)(uint32_t)row[j] * (uint32_t)p.num_kb + kb;
+                                for (int q = 0; q < kWords; ++q) scale[j][q] = 0u;
+                            }
+                            if (p.scale_bytes > 4) {
 #pragma unroll
-                            for (int q = 0; q < kFp8Group; ++q) v[j][q] = 0u;
-                            if (p.scale_bytes == 16) {
-                                ld_cg_16(v[j], src, row[j]);
-                            } else if (p.scale_bytes == 8) {
+                                for (int j = 0; j < kSets; ++j) {
+                                    const uint32_t *src = reinterpret_cast<const uint32_t *>(p.x_scales) +
+                                                          (uint64_t)(uint32_t)srow[j] * (uint32_t)p.num_chunks + 2 * kb;
+                                    if (kWords == 4 && p.scale_bytes == 16) {
+                                        ld_cg_16(scale[j], src, srow[j]);
+                                    } else {
 #pragma unroll
-                                for (int q = 0; q < kFp8Group; q += 2)
-                                    ld_cg_8(v[j] + q, src + q, kb + q < p.num_kb ? row[j] : -1);
-                            } else {
-#pragma unroll
-                                for (int q = 0; q < kFp8Group; ++q)
-                                    if (row[j] >= 0 && kb + q < p.num_kb) v[j][q] = __ldcg(src + q);
+                                        for (int q = 0; q < kWords; q += 2)
+                                            ld_cg_8(scale[j] + q, src + q, 2 * kb + q < p.num_chunks ? srow[j] : -1);
+                                    }
+                                }
                             }
                         }
-                        float w = 0.0f;
-                        if (lane < 8 && kb + (lane & 3) < p.num_kb) w = __ldcg(ws + kb);
-                        __syncwarp();
-                        if (!(ok = warp_wait(&scale_empty[sc.i], sc.ph ^ 1u, abort_flag))) break;
-                        float *to = scale_ring + sc.i * (kFp8ScaleBytes<kCols> / 4);
+                        // (chunks past the row's end are not read by the last MMA steps)
+                        const int off = kb * kFfRowBytes + c * 16, ends = p.x_bytes;
+                        const uint8_t *x = p.x + off;
+                        // 4 rows a step and group of eight lanes
+#pragma unroll 4
+                        for (int r = 4 * (lane >> 3); r < n; r += 16) {
+                            const int4 at = *reinterpret_cast<const int4 *>(inf->row + col0 + r);
+                            const int row[4] = {at.x, at.y, at.z, at.w};
 #pragma unroll
-                        for (int q = 0; q < kFp8Group; ++q)
+                            for (int j = 0; j < 4; ++j) {
+                                const uint8_t *from = x + (uint64_t)(uint32_t)row[j] * p.x_row_bytes;
+                                const uint32_t to = base + x_off + (uint32_t)((r + j) * kFfRowBytes + ((c ^ ((r + j) & 7)) << 4));
 #pragma unroll
-                            for (int j = 0; j < kSets; ++j) to[q * kCols + lane + 32 * j] = __uint_as_float(v[j][q]);
-                        if (lane < 8) to[kFp8Group * kCols + 2 * (lane & 3) + (lane >> 2)] = w;
+                                for (int u = 0; u < SUB; ++u)
+                                    cp_async_16(to + u * p.b_bytes, from + u * kFfRowBytes, off + u * kFfRowBytes < ends ? row[j] : -1);
+                            }
+                        }
+                        if constexpr (MX) {
+                            // scale of column r, block q of a 128-value piece: byte
+                            // (r % 32) * 16 + (r / 32) * 4 + q of its 512
+                            const uint32_t sd = base + xs_off + lane * 16;
+                            const int pieces = min(kWords, p.num_chunks - 2 * kb);
+                            if (p.scale_bytes > 4) {
+#pragma unroll
+                                for (int q = 0; q < kWords; ++q)  // (kSets = 4)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                                 ::"r"(sd + q * kSfAtom), "r"(scale[0][q]), "r"(scale[1][q]),
+                                                   "r"(scale[2][q]), "r"(scale[3][q]) : "memory");
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < kSets; ++j) {
+                                    const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)srow[j] * (uint32_t)p.num_chunks + 2 * kb) * 4;
+#pragma unroll
+                                    for (int q = 0; q < kWords; ++q)
+                                        cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q, q < pieces ? srow[j] : -1);
+                                }
+                            }
+                        }
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&scale_full[sc.i]));
-                        sc.next(kFp8Ring);
+                        if (lane == 0) {
+                            if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&full[st.i]), 0u));
+                            else mbar_arrive(smem_u32(&full[st.i]));
+                        }
+                        st.skip(kLoaders, ST);
                     }
+                    next -= count;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
                 iq.next(kFfInfos);
-                if (n < 0) break;
+                if (all < 0) break;
             }
             __syncwarp();
         }
-    } else if (warp < kFirst + kLoaders) {
-        // ------------------------------------------------ routed rows ----
-        // Each loader warp fills every kLoaders-th stage, so that a stage is
-        // waited for, copied, made visible to the tensor core (async proxy)
-        // and announced by one warp, while the others' copies are in flight.
-        // A row's k-block is eight 16-byte chunks; eight neighbouring lanes
-        // copy a row's, chunk c of row r landing at r * 128 + ((c ^ (r & 7)) <<
-        // 4), the 128-byte swizzle.
-        // A parity wait tells a stage's last use from the one before only: a
-        // warp that waits for stage j (counted over all uses) must know that
-        // j - 2 * ST was consumed. It waited for j - kLoaders, so everything
-        // up to j - kLoaders - ST was: hence kLoaders <= ST.
-        const int c = lane & 7;
-        RingPos st, iq;
-        int next = warp - kFirst;  // this warp's next stage, counted from the piece's first
-        st.skip(next, ST);
-        bool ok = true;
-        while (ok) {
-            if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
-            const Info *inf = info + iq.i;
-            const int all = inf->n;
-            // this CTA's rows are columns [col0, col0 + n)
-            const int n = PAIR ? all / 2 : all, col0 = (int)rank * n;
-            if (all >= 0) {
-                const int count = (p.num_kb + SUB - 1) / SUB;
-                for (; next < count; next += kLoaders) {
-                    if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
-                    const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
-                    const int kb = next * SUB;
-                    // MXFP4: this lane's columns' scales of the stage. Where rows
-                    // can be read in wider pieces they pass through registers,
-                    // requested before the rows are copied and stored after:
-                    // a gather of 32 rows costs the load unit 32 cycles
-                    // whatever its width, and 4-byte copies take four for the
-                    // 16 bytes of a stage (MXFP4 up, 16384 tokens: a
-                    // tenth longer with those than with 16-byte loads).
-                    constexpr int kSets = MX ? kCols / 32 : 1, kWords = 2 * SUB;
-                    uint32_t scale[kSets][kWords];
-                    int srow[kSets];
-                    if constexpr (MX) {
-#pragma unroll
-                        for (int j = 0; j < kSets; ++j) {
-                            srow[j] = lane + 32 * j < all ? inf->row[lane + 32 * j] : -1;
-#pragma unroll
-                            for (int q = 0; q < kWords; ++q) scale[j][q] = 0u;
-                        }
-                        if (p.scale_bytes > 4) {
-#pragma unroll
-                            for (int j = 0; j < kSets; ++j) {
-                                const uint32_t *src = reinterpret_cast<const uint32_t *>(p.x_scales) +
-                                                      (uint64_t)(uint32_t)srow[j] * (uint32_t)p.num_chunks + 2 * kb;
-                                if (kWords == 4 && p.scale_bytes == 16) {
-                                    ld_cg_16(scale[j], src, srow[j]);
-                                } else {
-#pragma unroll
-                                    for (int q = 0; q < kWords; q += 2)
-                                        ld_cg_8(scale[j] + q, src + q, 2 * kb + q < p.num_chunks ? srow[j] : -1);
-                                }
-                            }
-                        }
-                    }
-                    // (chunks past the row's end are not read by the last MMA steps)
-                    const int off = kb * kFfRowBytes + c * 16, ends = p.x_bytes;
-                    const uint8_t *x = p.x + off;
-                    // 4 rows a step and group of eight lanes
-#pragma unroll 4
-                    for (int r = 4 * (lane >> 3); r < n; r += 16) {
-                        const int4 at = *reinterpret_cast<const int4 *>(inf->row + col0 + r);
-                        const int row[4] = {at.x, at.y, at.z, at.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint8_t *from = x + (uint64_t)(uint32_t)row[j] * p.x_row_bytes;
-                            const uint32_t to = base + x_off + (uint32_t)((r + j) * kFfRowBytes + ((c ^ ((r + j) & 7)) << 4));
-#pragma unroll
-                            for (int u = 0; u < SUB; ++u)
-                                cp_async_16(to + u * p.b_bytes, from + u * kFfRowBytes, off + u * kFfRowBytes < ends ? row[j] : -1);
-                        }
-                    }
-                    if constexpr (MX) {
-                        // scale of column r, block q of a 128-value piece: byte
-                        // (r % 32) * 16 + (r / 32) * 4 + q of its 512
-                        const uint32_t sd = base + xs_off + lane * 16;
-                        const int pieces = min(kWords, p.num_chunks - 2 * kb);
-                        if (p.scale_bytes > 4) {
-#pragma unroll
-                            for (int q = 0; q < kWords; ++q)  // (kSets = 4)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                             ::"r"(sd + q * kSfAtom), "r"(scale[0][q]), "r"(scale[1][q]),
-                                               "r"(scale[2][q]), "r"(scale[3][q]) : "memory");
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < kSets; ++j) {
-                                const uint8_t *src = p.x_scales + ((uint64_t)(uint32_t)srow[j] * (uint32_t)p.num_chunks + 2 * kb) * 4;
-#pragma unroll
-                                for (int q = 0; q < kWords; ++q)
-                                    cp_async_4(sd + q * kSfAtom + j * 4, src + 4 * q, q < pieces ? srow[j] : -1);
-                            }
-                        }
-                    }
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&full[st.i]), 0u));
-                        else mbar_arrive(smem_u32(&full[st.i]));
-                    }
-                    st.skip(kLoaders, ST);
-                }
-                next -= count;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
-            iq.next(kFfInfos);
-            if (all < 0) break;
-        }
-        __syncwarp();
     } else {
         // --------------------------------------------------- epilogue ----
         // four warps, one a quarter of TMEM's lanes, take every other 16
@@ -998,46 +1008,56 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                     if (in == 0 && !(ok = warp_wait(&scale_full[sc.i], sc.ph, abort_flag))) break;
                     if (!(ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag))) break;
                     tc_fence_after();
-                    const float *scales = scale_ring + sc.i * (kFp8ScaleBytes<kCols> / 4);
-                    const float wg = scales[kFp8Group * kCols + 2 * in];
-                    const float wu = UP ? scales[kFp8Group * kCols + 2 * in + 1] : wg;
-                    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.acc_cols);
+                    const float *scales = scale_ring + sc.i * (kFp8ScaleBytes<kCols> / 4) + in * (kCols + 4);
+                    const float2 w = UP ? *reinterpret_cast<const float2 *>(scales + kCols) : make_float2(1.0f, 1.0f);
+                    scales += 16 * half + (F32 ? 0 : 4 * (lane & 3));
+                    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.acc_cols + 16 * half);
+                    // twice 16 columns a wait: what a wait costs is the same for more
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const int c0 = 16 * half + 32 * g;
-                        if (c0 >= n) break;
-                        uint32_t v[16];
-                        if constexpr (F32) tmem_ld16_async(acc + (uint32_t)c0, v);
-                        else tmem_ld_frags_async(acc + (uint32_t)c0, v);
-                        const float *xs = scales + in * kCols + c0;
-                        if constexpr (F32) {
-                            float4 s[4];
+                    for (int g0 = 0; g0 < kGroups; g0 += 2) {
+                        if (16 * half + 32 * g0 >= n) break;
+                        uint32_t v[2][16];
+                        float4 f[2];
+                        const bool both = 16 * half + 32 * (g0 + 1) < n;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) s[j] = *reinterpret_cast<const float4 *>(xs + 4 * j);
-                            tmem_wait_ld16(v);
+                        for (int b = 0; b < 2; ++b) {
+                            if (b == 1 && !both) break;
+                            if constexpr (F32) tmem_ld16_async(acc + (uint32_t)(32 * (g0 + b)), v[b]);
+                            else tmem_ld_frags_async(acc + (uint32_t)(32 * (g0 + b)), v[b]);
+                        }
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) {
-                                const float4 f = s[j >> 2];
-                                const float2 f2 = mul2(j & 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y), make_float2(wg, wg));
-                                fma2(sum[g][j], sum[g][j + 1], __uint_as_float(v[j]), __uint_as_float(v[j + 1]), f2);
-                            }
-                        } else {
-                            float2 s[2];
+                        for (int b = 0; b < 2; ++b) {
+                            if (b == 1 && !both) break;
+                            const int g = g0 + b;
+                            if constexpr (F32) {
+                                tmem_wait_ld16(v[b]);
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) s[u] = *reinterpret_cast<const float2 *>(xs + 8 * u + 2 * (lane & 3));
-                            tmem_wait_ld16(v);
+                                for (int t = 0; t < 4; ++t) {
+                                    f[b] = *reinterpret_cast<const float4 *>(scales + 32 * g + 4 * t);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const float w = UP && h == 1 ? wu : wg;
-                                    const float2 f = mul2(s[u], make_float2(w, w));
-#pragma unroll
-                                    for (int r = 0; r < 2; ++r) {
-                                        const int j = 8 * h + 4 * u + 2 * r;
-                                        fma2(sum[g][j], sum[g][j + 1], __uint_as_float(v[j]), __uint_as_float(v[j + 1]), f);
+                                    for (int u = 0; u < 2; ++u) {
+                                        const int j = 8 * u + 2 * t;
+                                        sum[g][j] = fmaf(__uint_as_float(v[b][j]), u ? f[b].z : f[b].x, sum[g][j]);
+                                        sum[g][j + 1] = fmaf(__uint_as_float(v[b][j + 1]), u ? f[b].w : f[b].y, sum[g][j + 1]);
                                     }
                                 }
+                            } else {
+                                f[b] = *reinterpret_cast<const float4 *>(scales + 32 * g);
+                                tmem_wait_ld16(v[b]);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const float wh = h == 0 ? w.x : w.y;
+                                    const float4 s = UP ? make_float4(f[b].x * wh, f[b].y * wh, f[b].z * wh, f[b].w * wh) : f[b];
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) {
+                                        const int j = 8 * h + 2 * r;
+                                        sum[g][j] = fmaf(__uint_as_float(v[b][j]), s.x, sum[g][j]);
+                                        sum[g][j + 1] = fmaf(__uint_as_float(v[b][j + 1]), s.y, sum[g][j + 1]);
+                                        sum[g][j + 4] = fmaf(__uint_as_float(v[b][j + 4]), s.z, sum[g][j + 4]);
+                                        sum[g][j + 5] = fmaf(__uint_as_float(v[b][j + 5]), s.w, sum[g][j + 5]);
+                                    }
+                                }
+                            }
                         }
                     }
                     tc_fence_before();
@@ -1239,14 +1259,8 @@ static bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const v
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool MX, bool UP, bool PAIR, int SUB, bool F32 = false, bool FP8 = false>
-static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stream) {
-    FfParams p{};
-    const int per_block = MX ? 256 : (FP8 ? 128 : 64), step = MX ? 64 : (FP8 ? 32 : 16);  // values of K in a k-block, in an MMA
-    p.num_kb = (a.K + per_block - 1) / per_block;
-    p.last_steps = (a.K - (p.num_kb - 1) * per_block + step - 1) / step;
-    p.feat = a.feat;
-    p.ntiles = UP ? (a.feat + 63) / 64 : (a.feat + kFfRows - 1) / kFfRows;
+// What does not depend on the format.
+static cudaError_t common_params(const FfnLaunch &a, FfParams &p) {
     p.div_shift = 30;
     while ((1ll << (p.div_shift - 30)) < a.width) ++p.div_shift;
     p.div_mul = (uint32_t)(((1ull << p.div_shift) + (uint64_t)a.width - 1) / (uint64_t)a.width);
@@ -1261,21 +1275,49 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.out = a.out;
     p.x_scales = static_cast<const uint8_t *>(a.x_scales);
     p.w_scales = static_cast<const uint8_t *>(a.w_scales);
+    p.scale_rows = (a.gated ? 2 : 1) * ((a.feat + 127) / 128);
+    p.err = &reinterpret_cast<WsHeader *>(a.hdr)->error;
+    void *word = nullptr;
+    const cudaError_t found = expert_error_word(&word);
+    p.err_device = static_cast<uint32_t *>(word);
+    return found;
+}
+
+// The tensor map of a weight: tiles of 128 rows, of a gated one 16 gate rows
+// and their 16 up rows in turn.
+static bool encode_weight(CUtensorMap *map, const FfnLaunch &a, CUtensorMapDataType type, cuuint64_t k_elems, cuuint64_t k_bytes,
+                          cuuint32_t box_k) {
+    if (a.gated) {
+        const cuuint64_t I = (cuuint64_t)a.feat;
+        const cuuint64_t dims[5] = {k_elems, 16, 2, I / 16, (cuuint64_t)a.num_experts};
+        const cuuint64_t strides[4] = {k_bytes, I * k_bytes, 16 * k_bytes, 2 * I * k_bytes};
+        const cuuint32_t box[5] = {box_k, 16, 2, 4, 1};
+        return encode(map, type, 5, a.w, dims, strides, box);
+    }
+    const cuuint64_t dims[3] = {k_elems, (cuuint64_t)a.feat, (cuuint64_t)a.num_experts};
+    const cuuint64_t strides[2] = {k_bytes, (cuuint64_t)a.feat * k_bytes};
+    const cuuint32_t box[3] = {box_k, kFfRows, 1};
+    return encode(map, type, 3, a.w, dims, strides, box);
+}
+
+template <bool MX, bool UP, bool PAIR, int SUB, bool F32 = false, bool FP8 = false>
+static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stream) {
+    FfParams p{};
+    const int per_block = MX ? 256 : (FP8 ? 128 : 64), step = MX ? 64 : (FP8 ? 32 : 16);  // values of K in a k-block, in an MMA
+    p.num_kb = (a.K + per_block - 1) / per_block;
+    p.last_steps = (a.K - (p.num_kb - 1) * per_block + step - 1) / step;
+    p.feat = a.feat;
+    p.ntiles = UP ? (a.feat + 63) / 64 : (a.feat + kFfRows - 1) / kFfRows;
+    if (const cudaError_t e = common_params(a, p)) return e;
     p.num_chunks = a.K / 128;
     // (4 bytes of scales are 128 values of MXFP4 and of E4M3)
     const uintptr_t scales_at = reinterpret_cast<uintptr_t>(a.x_scales) | (uintptr_t)(4 * (FP8 ? p.num_kb : p.num_chunks));
     p.scale_bytes = scales_at % 16 == 0 ? 16 : (scales_at % 8 == 0 ? 8 : 4);
-    p.scale_rows = (UP ? 2 : 1) * ((a.feat + 127) / 128);
-    p.err = &reinterpret_cast<WsHeader *>(a.hdr)->error;
-    void *word = nullptr;
-    const cudaError_t found = expert_error_word(&word);
-    if (found != cudaSuccess) return found;
-    p.err_device = static_cast<uint32_t *>(word);
     constexpr int kCols = kFfCols<MX, PAIR, FP8>;
     p.b_bytes = (uint32_t)(PAIR ? kCols / 2 : a.A) * kFfRowBytes;
     p.stage_bytes = SUB * (kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0));
     constexpr uint32_t kSmemMax = 232448;
-    constexpr int kMisc = kFfMiscBytes<MX, PAIR, FP8> + kFfOutBytes<UP, F32>;
+    constexpr int kMisc = kFfMiscBytes<MX, UP, PAIR, FP8> + kFfOutBytes<UP, F32>;
     p.stages = (int)((kSmemMax - 1024 - kMisc) / p.stage_bytes);
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
     if (p.stages < kFfLoaders<SUB, FP8>) return cudaErrorNotSupported;  // (see the row loaders; never with these sizes)
@@ -1290,19 +1332,7 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     const cuuint64_t k_elems = (cuuint64_t)(MX ? a.K / 2 : a.K), k_bytes = MX || FP8 ? k_elems : 2 * k_elems;
     const cuuint32_t box_k = MX || FP8 ? kFfRowBytes : kFfRowBytes / 2;
     CUtensorMap mw;
-    bool ok;
-    if (UP) {
-        const cuuint64_t I = (cuuint64_t)a.feat;
-        const cuuint64_t dims[5] = {k_elems, 16, 2, I / 16, (cuuint64_t)a.num_experts};
-        const cuuint64_t strides[4] = {k_bytes, I * k_bytes, 16 * k_bytes, 2 * I * k_bytes};
-        const cuuint32_t box[5] = {box_k, 16, 2, 4, 1};
-        ok = encode(&mw, type, 5, a.w, dims, strides, box);
-    } else {
-        const cuuint64_t dims[3] = {k_elems, (cuuint64_t)a.feat, (cuuint64_t)a.num_experts};
-        const cuuint64_t strides[2] = {k_bytes, (cuuint64_t)a.feat * k_bytes};
-        const cuuint32_t box[3] = {box_k, kFfRows, 1};
-        ok = encode(&mw, type, 3, a.w, dims, strides, box);
-    }
+    bool ok = encode_weight(&mw, a, type, k_elems, k_bytes, box_k);
     // a weight's tiled scales: pieces of 512 bytes
     CUtensorMap ms{};
     if (MX && PAIR && ok) {
