@@ -19,7 +19,7 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libsmr.so")
 SOURCES = ["smr_api.cpp", "smr_small.cu", "smr_align.cu", "smr_tc.cu", "smr_select.cu", "smr_score.cu", "smr_expert.cu",
            "smr_ffn.cu", "smr_ffn8.cu", "smr_mxfp4.cu", "smr_fp8.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("smr_device.cuh", "smr_ffn.cuh", "smr_launch.h")] + [
+HEADERS = [os.path.join(CSRC, h) for h in ("smr_device.cuh", "smr_ffn.cuh", "smr_fp8.cuh", "smr_launch.h")] + [
     os.path.join(INCLUDE, "smr.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

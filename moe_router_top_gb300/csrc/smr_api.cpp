@@ -937,9 +937,15 @@ SMR_API smr_status smr_expert_down_fp32(const smr_expert_down_args *args, void *
 
 // --- E4M3 ---------------------------------------------------------------------
 
+// Whether quantised activations pass through the workspace in bf16: with few
+// rows an expert a block of 128 features is not one CTA's.
+static bool up_fp8_through_bf16(const smr_expert_up_fp8_args *a) {
+    return a->act_scales && !smr::expert_rows_fp8((int64_t)a->num_tokens * a->width, a->num_experts);
+}
+
 SMR_API size_t smr_expert_up_fp8_workspace_size(const smr_expert_up_fp8_args *args) {
     if (!args) return 0;
-    return args->act_scales ? rows_workspace_size(args->num_tokens, args->width, args->I, false) : kHeaderBytes;
+    return up_fp8_through_bf16(args) ? rows_workspace_size(args->num_tokens, args->width, args->I, false) : kHeaderBytes;
 }
 
 SMR_API smr_status smr_expert_up_fp8(const smr_expert_up_fp8_args *a, void *workspace, size_t workspace_bytes,
@@ -962,12 +968,14 @@ SMR_API smr_status smr_expert_up_fp8(const smr_expert_up_fp8_args *a, void *work
     if (st != SMR_OK) return st;
     if ((st = check_device()) != SMR_OK) return st;
     smr::FfnLaunch L = ffn_launch(c, workspace);
-    L.out = a->act_scales ? static_cast<uint8_t *>(workspace) + kDownRowsOffset : a->act;
+    const bool through_bf16 = up_fp8_through_bf16(a);
+    L.out = through_bf16 ? static_cast<uint8_t *>(workspace) + kDownRowsOffset : a->act;
+    L.out_scales = through_bf16 ? nullptr : a->act_scales;
     const std::lock_guard<std::mutex> together(launch_lock(workspace));
     cudaError_t e = smr::launch_expert_product(L, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("expert up launch", e);
     g_last_launches = 1;
-    if (a->act_scales) {
+    if (through_bf16) {
         const smr::QuantizeRows q{static_cast<const uint16_t *>(L.out), a->sorted_token_ids, a->num_tokens_post_padded,
                                   a->sorted_cap, L.numel, a->I, static_cast<uint8_t *>(a->act), a->act_scales};
         e = smr::launch_quantize_fp8_slots(q, static_cast<cudaStream_t>(stream));

@@ -106,7 +106,8 @@ struct FfParams {
     int64_t sorted_cap;
     int numel, max_blocks;
     const int32_t *sorted, *eids, *npp;
-    void *out;               // [numel, feat], fp32 or bf16
+    void *out;               // [numel, feat], fp32, bf16 or E4M3
+    float *out_scales;       // E4M3 outputs: [numel, ceil(feat / 128)]
     const uint8_t *x_scales, *w_scales;  // MXFP4; E4M3: fp32
     int num_chunks;          // MXFP4: K / 128
     int scale_bytes;         // rows of x_scales can be read 16, 8 or 4 bytes at a time
@@ -1283,20 +1284,20 @@ static cudaError_t common_params(const FfnLaunch &a, FfParams &p) {
     return found;
 }
 
-// The tensor map of a weight: tiles of 128 rows, of a gated one 16 gate rows
+// The tensor map of a weight: boxes of `rows` rows, of a gated one 16 gate rows
 // and their 16 up rows in turn.
 static bool encode_weight(CUtensorMap *map, const FfnLaunch &a, CUtensorMapDataType type, cuuint64_t k_elems, cuuint64_t k_bytes,
-                          cuuint32_t box_k) {
+                          cuuint32_t box_k, cuuint32_t rows = kFfRows) {
     if (a.gated) {
         const cuuint64_t I = (cuuint64_t)a.feat;
         const cuuint64_t dims[5] = {k_elems, 16, 2, I / 16, (cuuint64_t)a.num_experts};
         const cuuint64_t strides[4] = {k_bytes, I * k_bytes, 16 * k_bytes, 2 * I * k_bytes};
-        const cuuint32_t box[5] = {box_k, 16, 2, 4, 1};
+        const cuuint32_t box[5] = {box_k, 16, 2, rows / 32, 1};
         return encode(map, type, 5, a.w, dims, strides, box);
     }
     const cuuint64_t dims[3] = {k_elems, (cuuint64_t)a.feat, (cuuint64_t)a.num_experts};
     const cuuint64_t strides[2] = {k_bytes, (cuuint64_t)a.feat * k_bytes};
-    const cuuint32_t box[3] = {box_k, kFfRows, 1};
+    const cuuint32_t box[3] = {box_k, rows, 1};
     return encode(map, type, 3, a.w, dims, strides, box);
 }
 

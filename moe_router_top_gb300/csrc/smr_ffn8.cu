@@ -15,21 +15,25 @@
 // thread of the epilogue holds one row, its scale is one register, and a weight
 // tile's is the same for all.
 #include "smr_ffn.cuh"
+#include "smr_fp8.cuh"
 
 namespace smr {
 
-// Rows of K: 256 a CTA pair (blocks of one expert together), 256 weight rows,
-// 128 of each in either CTA. 16 warps: 0 weights, 1 MMAs, 2 scout, 4 to 7 load
-// the routed rows (32 each), the last 8 are the epilogue, two for each quarter
-// of TMEM's lanes (128 columns each).
-constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 2;
+// A piece of work: up to 256 routed rows (blocks of one expert together) and two
+// weight tiles for a CTA pair; either CTA holds half of the rows and half of
+// each tile. 16 warps: 0 weights, 1 MMAs, 2 scout, 3 scales, 4 to 7 load the
+// routed rows (32 each), the last 8 are the epilogue, two for each quarter of
+// TMEM's lanes, one of these for either tile.
+constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4, kRowScales = 3;
 constexpr int kRowStageBytes = 2 * kFfWBytes;
-constexpr int kRowBars = 2 * kFfMaxStages + 2 * kRowAccs + 2 * kRowInfos + 1;
+constexpr int kRowScaleBytes = kFp8Group * 128 * 8;  // [k-block][row] (two products of scales)
+constexpr int kRowBars = 2 * kFfMaxStages + 2 * kRowAccs + 2 * kRowInfos + 2 * kRowScales + 1;
 constexpr int kRowBarBytes = (kRowBars * 8 + 8 + 15) / 16 * 16;
 // The epilogue's outputs leave through shared memory, 128 bytes of 32 rows a
 // warp at a time, so that rows are written in whole lines.
 constexpr int kRowOutBytes = 8 * 32 * 128;
-constexpr int kRowMiscBytes = kRowBarBytes + kRowInfos * (int)sizeof(FfInfo<256>) + kRowOutBytes + 2 * 128 * 4;
+constexpr int kRowMiscBytes = kRowBarBytes + kRowInfos * (int)sizeof(FfInfo<256>) + kRowScales * kRowScaleBytes +
+                              kRowOutBytes + 2 * 128 * 4;
 
 enum RowOut : int { kRowBf16 = 0, kRowF32 = 1, kRowE4m3 = 2 };
 
@@ -65,6 +69,121 @@ __device__ __forceinline__ void put_row_lines(uint32_t buffer, const uint32_t (&
     __syncwarp();
 }
 
+// A row's 128 columns times g and u (16 and 16 in turn), added to d; the last
+// 32 are left in `last`, so that the accumulator can be handed back before they
+// are added. Bound by the loads' latency (77 cycles) and by the adds (one a
+// cycle for the two warps of a scheduler): while one load's values are added the
+// next is under way, 32 columns and 16 in turn, as many as there are registers
+// for. One statement, as the order in it is what counts.
+__device__ __forceinline__ void add_columns(float (&d)[128], float (&last)[32], uint32_t taddr, float g, float u) {
+    asm volatile(
+        "{\n .reg .f32 a<32>;\n .reg .f32 b<16>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x32.b32 {a0,a1,a2,a3,a4,a5,a6,a7,a8,a9,a10,a11,a12,a13,a14,a15,a16,a17,a18,a19,a20,a21,a22,a23,a24,a25,a26,a27,a28,a29,a30,a31}, [%160 + 0];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x16.b32 {b0,b1,b2,b3,b4,b5,b6,b7,b8,b9,b10,b11,b12,b13,b14,b15}, [%160 + 32];\n"
+        " fma.rn.f32 %0, a0, %161, %0;\n fma.rn.f32 %1, a1, %161, %1;\n"
+        " fma.rn.f32 %2, a2, %161, %2;\n fma.rn.f32 %3, a3, %161, %3;\n"
+        " fma.rn.f32 %4, a4, %161, %4;\n fma.rn.f32 %5, a5, %161, %5;\n"
+        " fma.rn.f32 %6, a6, %161, %6;\n fma.rn.f32 %7, a7, %161, %7;\n"
+        " fma.rn.f32 %8, a8, %161, %8;\n fma.rn.f32 %9, a9, %161, %9;\n"
+        " fma.rn.f32 %10, a10, %161, %10;\n fma.rn.f32 %11, a11, %161, %11;\n"
+        " fma.rn.f32 %12, a12, %161, %12;\n fma.rn.f32 %13, a13, %161, %13;\n"
+        " fma.rn.f32 %14, a14, %161, %14;\n fma.rn.f32 %15, a15, %161, %15;\n"
+        " fma.rn.f32 %16, a16, %162, %16;\n fma.rn.f32 %17, a17, %162, %17;\n"
+        " fma.rn.f32 %18, a18, %162, %18;\n fma.rn.f32 %19, a19, %162, %19;\n"
+        " fma.rn.f32 %20, a20, %162, %20;\n fma.rn.f32 %21, a21, %162, %21;\n"
+        " fma.rn.f32 %22, a22, %162, %22;\n fma.rn.f32 %23, a23, %162, %23;\n"
+        " fma.rn.f32 %24, a24, %162, %24;\n fma.rn.f32 %25, a25, %162, %25;\n"
+        " fma.rn.f32 %26, a26, %162, %26;\n fma.rn.f32 %27, a27, %162, %27;\n"
+        " fma.rn.f32 %28, a28, %162, %28;\n fma.rn.f32 %29, a29, %162, %29;\n"
+        " fma.rn.f32 %30, a30, %162, %30;\n fma.rn.f32 %31, a31, %162, %31;\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x32.b32 {a0,a1,a2,a3,a4,a5,a6,a7,a8,a9,a10,a11,a12,a13,a14,a15,a16,a17,a18,a19,a20,a21,a22,a23,a24,a25,a26,a27,a28,a29,a30,a31}, [%160 + 48];\n"
+        " fma.rn.f32 %32, b0, %161, %32;\n fma.rn.f32 %33, b1, %161, %33;\n"
+        " fma.rn.f32 %34, b2, %161, %34;\n fma.rn.f32 %35, b3, %161, %35;\n"
+        " fma.rn.f32 %36, b4, %161, %36;\n fma.rn.f32 %37, b5, %161, %37;\n"
+        " fma.rn.f32 %38, b6, %161, %38;\n fma.rn.f32 %39, b7, %161, %39;\n"
+        " fma.rn.f32 %40, b8, %161, %40;\n fma.rn.f32 %41, b9, %161, %41;\n"
+        " fma.rn.f32 %42, b10, %161, %42;\n fma.rn.f32 %43, b11, %161, %43;\n"
+        " fma.rn.f32 %44, b12, %161, %44;\n fma.rn.f32 %45, b13, %161, %45;\n"
+        " fma.rn.f32 %46, b14, %161, %46;\n fma.rn.f32 %47, b15, %161, %47;\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x16.b32 {b0,b1,b2,b3,b4,b5,b6,b7,b8,b9,b10,b11,b12,b13,b14,b15}, [%160 + 80];\n"
+        " fma.rn.f32 %48, a0, %162, %48;\n fma.rn.f32 %49, a1, %162, %49;\n"
+        " fma.rn.f32 %50, a2, %162, %50;\n fma.rn.f32 %51, a3, %162, %51;\n"
+        " fma.rn.f32 %52, a4, %162, %52;\n fma.rn.f32 %53, a5, %162, %53;\n"
+        " fma.rn.f32 %54, a6, %162, %54;\n fma.rn.f32 %55, a7, %162, %55;\n"
+        " fma.rn.f32 %56, a8, %162, %56;\n fma.rn.f32 %57, a9, %162, %57;\n"
+        " fma.rn.f32 %58, a10, %162, %58;\n fma.rn.f32 %59, a11, %162, %59;\n"
+        " fma.rn.f32 %60, a12, %162, %60;\n fma.rn.f32 %61, a13, %162, %61;\n"
+        " fma.rn.f32 %62, a14, %162, %62;\n fma.rn.f32 %63, a15, %162, %63;\n"
+        " fma.rn.f32 %64, a16, %161, %64;\n fma.rn.f32 %65, a17, %161, %65;\n"
+        " fma.rn.f32 %66, a18, %161, %66;\n fma.rn.f32 %67, a19, %161, %67;\n"
+        " fma.rn.f32 %68, a20, %161, %68;\n fma.rn.f32 %69, a21, %161, %69;\n"
+        " fma.rn.f32 %70, a22, %161, %70;\n fma.rn.f32 %71, a23, %161, %71;\n"
+        " fma.rn.f32 %72, a24, %161, %72;\n fma.rn.f32 %73, a25, %161, %73;\n"
+        " fma.rn.f32 %74, a26, %161, %74;\n fma.rn.f32 %75, a27, %161, %75;\n"
+        " fma.rn.f32 %76, a28, %161, %76;\n fma.rn.f32 %77, a29, %161, %77;\n"
+        " fma.rn.f32 %78, a30, %161, %78;\n fma.rn.f32 %79, a31, %161, %79;\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x32.b32 {%128,%129,%130,%131,%132,%133,%134,%135,%136,%137,%138,%139,%140,%141,%142,%143,%144,%145,%146,%147,%148,%149,%150,%151,%152,%153,%154,%155,%156,%157,%158,%159}, [%160 + 96];\n"
+        " fma.rn.f32 %80, b0, %162, %80;\n fma.rn.f32 %81, b1, %162, %81;\n"
+        " fma.rn.f32 %82, b2, %162, %82;\n fma.rn.f32 %83, b3, %162, %83;\n"
+        " fma.rn.f32 %84, b4, %162, %84;\n fma.rn.f32 %85, b5, %162, %85;\n"
+        " fma.rn.f32 %86, b6, %162, %86;\n fma.rn.f32 %87, b7, %162, %87;\n"
+        " fma.rn.f32 %88, b8, %162, %88;\n fma.rn.f32 %89, b9, %162, %89;\n"
+        " fma.rn.f32 %90, b10, %162, %90;\n fma.rn.f32 %91, b11, %162, %91;\n"
+        " fma.rn.f32 %92, b12, %162, %92;\n fma.rn.f32 %93, b13, %162, %93;\n"
+        " fma.rn.f32 %94, b14, %162, %94;\n fma.rn.f32 %95, b15, %162, %95;\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        "}"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]), "+f"(d[4]), "+f"(d[5]), "+f"(d[6]), "+f"(d[7]),
+          "+f"(d[8]), "+f"(d[9]), "+f"(d[10]), "+f"(d[11]), "+f"(d[12]), "+f"(d[13]), "+f"(d[14]), "+f"(d[15]),
+          "+f"(d[16]), "+f"(d[17]), "+f"(d[18]), "+f"(d[19]), "+f"(d[20]), "+f"(d[21]), "+f"(d[22]), "+f"(d[23]),
+          "+f"(d[24]), "+f"(d[25]), "+f"(d[26]), "+f"(d[27]), "+f"(d[28]), "+f"(d[29]), "+f"(d[30]), "+f"(d[31]),
+          "+f"(d[32]), "+f"(d[33]), "+f"(d[34]), "+f"(d[35]), "+f"(d[36]), "+f"(d[37]), "+f"(d[38]), "+f"(d[39]),
+          "+f"(d[40]), "+f"(d[41]), "+f"(d[42]), "+f"(d[43]), "+f"(d[44]), "+f"(d[45]), "+f"(d[46]), "+f"(d[47]),
+          "+f"(d[48]), "+f"(d[49]), "+f"(d[50]), "+f"(d[51]), "+f"(d[52]), "+f"(d[53]), "+f"(d[54]), "+f"(d[55]),
+          "+f"(d[56]), "+f"(d[57]), "+f"(d[58]), "+f"(d[59]), "+f"(d[60]), "+f"(d[61]), "+f"(d[62]), "+f"(d[63]),
+          "+f"(d[64]), "+f"(d[65]), "+f"(d[66]), "+f"(d[67]), "+f"(d[68]), "+f"(d[69]), "+f"(d[70]), "+f"(d[71]),
+          "+f"(d[72]), "+f"(d[73]), "+f"(d[74]), "+f"(d[75]), "+f"(d[76]), "+f"(d[77]), "+f"(d[78]), "+f"(d[79]),
+          "+f"(d[80]), "+f"(d[81]), "+f"(d[82]), "+f"(d[83]), "+f"(d[84]), "+f"(d[85]), "+f"(d[86]), "+f"(d[87]),
+          "+f"(d[88]), "+f"(d[89]), "+f"(d[90]), "+f"(d[91]), "+f"(d[92]), "+f"(d[93]), "+f"(d[94]), "+f"(d[95]),
+          "+f"(d[96]), "+f"(d[97]), "+f"(d[98]), "+f"(d[99]), "+f"(d[100]), "+f"(d[101]), "+f"(d[102]), "+f"(d[103]),
+          "+f"(d[104]), "+f"(d[105]), "+f"(d[106]), "+f"(d[107]), "+f"(d[108]), "+f"(d[109]), "+f"(d[110]), "+f"(d[111]),
+          "+f"(d[112]), "+f"(d[113]), "+f"(d[114]), "+f"(d[115]), "+f"(d[116]), "+f"(d[117]), "+f"(d[118]), "+f"(d[119]),
+          "+f"(d[120]), "+f"(d[121]), "+f"(d[122]), "+f"(d[123]), "+f"(d[124]), "+f"(d[125]), "+f"(d[126]), "+f"(d[127]),
+          "=&f"(last[0]), "=&f"(last[1]), "=&f"(last[2]), "=&f"(last[3]), "=&f"(last[4]), "=&f"(last[5]), "=&f"(last[6]), "=&f"(last[7]),
+          "=&f"(last[8]), "=&f"(last[9]), "=&f"(last[10]), "=&f"(last[11]), "=&f"(last[12]), "=&f"(last[13]), "=&f"(last[14]), "=&f"(last[15]),
+          "=&f"(last[16]), "=&f"(last[17]), "=&f"(last[18]), "=&f"(last[19]), "=&f"(last[20]), "=&f"(last[21]), "=&f"(last[22]), "=&f"(last[23]),
+          "=&f"(last[24]), "=&f"(last[25]), "=&f"(last[26]), "=&f"(last[27]), "=&f"(last[28]), "=&f"(last[29]), "=&f"(last[30]), "=&f"(last[31])
+        : "r"(taddr), "f"(g), "f"(u) : "memory");
+}
+
+// silu(g) * u of four pairs, as swiglu, with one reciprocal for the four
+// denominators (each in [1, 2]): the special functions' unit is what bounds
+// these, an exponential and a quarter of a reciprocal take it 10 cycles a warp.
+__device__ __forceinline__ void swiglu4(const float (&g)[4], const float (&u)[4], float (&a)[4]) {
+    float d[4], n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float h;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fabsf(g[i]) * -0.72134752f));
+        d[i] = fmaf(h, h, 1.0f);
+        const float t = g[i] < 0.0f ? h : 1.0f;
+        n[i] = g[i] * t;
+        a[i] = u[i] * t;
+    }
+    const float d01 = d[0] * d[1], d23 = d[2] * d[3];
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d01 * d23));
+    const float r01 = r * d23, r23 = r * d01;
+    a[0] *= n[0] * (r01 * d[1]);
+    a[1] *= n[1] * (r01 * d[0]);
+    a[2] *= n[2] * (r23 * d[3]);
+    a[3] *= n[3] * (r23 * d[2]);
+}
+
 template <bool UP, int OUT>
 __global__ void __launch_bounds__(kRowThreads, 1)
 expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
@@ -81,12 +200,15 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     uint64_t *acc_empty = acc_full + kRowAccs;
     uint64_t *info_full = acc_empty + kRowAccs;
     uint64_t *info_empty = info_full + kRowInfos;
-    uint64_t *last = info_empty + kRowInfos;
+    uint64_t *scale_full = info_empty + kRowInfos;
+    uint64_t *scale_empty = scale_full + kRowScales;
+    uint64_t *last = scale_empty + kRowScales;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(last + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Info *info = reinterpret_cast<Info *>(misc + kRowBarBytes);
-    uint8_t *out_rows = misc + kRowBarBytes + kRowInfos * sizeof(Info);
-    float *amax_ex = reinterpret_cast<float *>(out_rows + kRowOutBytes);  // [2][128]
+    float2 *scale_ring = reinterpret_cast<float2 *>(misc + kRowBarBytes + kRowInfos * sizeof(Info));
+    uint8_t *out_rows = misc + kRowBarBytes + kRowInfos * sizeof(Info) + kRowScales * kRowScaleBytes;
+    uint32_t *amax_ex = reinterpret_cast<uint32_t *>(out_rows + kRowOutBytes);  // [2][128]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -97,11 +219,15 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         }
         for (int s = 0; s < kRowAccs; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
-            mbar_init(smem_u32(&acc_empty[s]), 2 * kFfDrains);
+            mbar_init(smem_u32(&acc_empty[s]), kFfDrains);  // one tile's four warps of both CTAs
         }
         for (int s = 0; s < kRowInfos; ++s) {
             mbar_init(smem_u32(&info_full[s]), 1);
-            mbar_init(smem_u32(&info_empty[s]), 2 + kRowLoaders + kFfDrains);
+            mbar_init(smem_u32(&info_empty[s]), 3 + kRowLoaders + kFfDrains);  // every warp but the scout
+        }
+        for (int s = 0; s < kRowScales; ++s) {
+            mbar_init(smem_u32(&scale_full[s]), 1);
+            mbar_init(smem_u32(&scale_empty[s]), kFfDrains);
         }
         mbar_init(smem_u32(last), 1);
         *abort_flag = 0;
@@ -120,7 +246,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     griddep_wait();  // the align's outputs and x come from previous kernels
     griddep_launch_dependents();
 
-    const uint32_t ring = smem_u32(smem);  // a stage: [rows][weights]
+    const uint32_t ring = smem_u32(smem);  // a stage: [rows][64 rows of the first tile][64 of the second]
     int issued = 0;
     // A thread of the epilogue holds 128 sums: its 8 warps get registers of the
     // other 8 (256 x 64 + 256 x 192 = the 512 x 128 of the launch, which the
@@ -147,8 +273,13 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         // both CTAs' bytes complete the leader's barrier
                         if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
                         const uint32_t fb = cluster_addr(bar, 0u);
-                        if constexpr (UP) tma_load_5d_pair(to, &tm_w, kb * kFfRowBytes, nt * 4, e, fb);
-                        else tma_load_3d_pair(to, &tm_w, kb * kFfRowBytes, nt * kFfRows, e, fb);
+                        // this CTA's half of either tile: the first CTA's is the tile's first 64 rows
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int tile = (nt & ~1) + h;
+                            if constexpr (UP) tma_load_5d_pair(to + h * (kFfWBytes / 2), &tm_w, kb * kFfRowBytes, 4 * tile + 2 * (int)rank, e, fb);
+                            else tma_load_3d_pair(to + h * (kFfWBytes / 2), &tm_w, kb * kFfRowBytes, kFfRows * tile + 64 * (int)rank, e, fb);
+                        }
                     }
                     ++issued;
                     st.next(ST);
@@ -161,7 +292,12 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         } else if (warp == 1) {
             // --------------------------------------------------- MMAs ----
             const bool elected = elect_one();
-            const uint32_t idesc = idesc_e4m3(2 * kFfRows, 256);
+            // A k-block's two tiles one after the other, each into an
+            // accumulator that its own warps of the epilogue wait for: from an
+            // accumulator's last MMA to the next one's first in it the signals
+            // between the CTAs take 1100 cycles without any work in between, a
+            // tile's MMAs 256.
+            const uint32_t idesc = idesc_e4m3(2 * kFfRows, 128);
             RingPos st, iq, ac;
             bool ok = true;
             while (ok) {
@@ -174,23 +310,29 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (rank != 0) continue;
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
-                    if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
-                    tc_fence_after();
-                    const uint32_t base = ring + (uint32_t)(st.i * kRowStageBytes), acc = tmem + (uint32_t)(ac.i * 256);
-                    const uint64_t da = smem_desc_sw<128>(base), db = smem_desc_sw<128>(base + kFfWBytes);
+                    const uint32_t base = ring + (uint32_t)(st.i * kRowStageBytes);
+                    const uint64_t da = smem_desc_sw<128>(base);
                     const int steps = kb + 1 == p.num_kb ? p.last_steps : 4;
-                    if (elected) {
-                        if (steps == 4) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) tc_mma_e4m3<true>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
-                        } else {
-                            for (int kk = 0; kk < steps; ++kk) tc_mma_e4m3<true>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                    for (int h = 0; h < 2; ++h) {
+                        if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
+                        tc_fence_after();
+                        const uint32_t acc = tmem + (uint32_t)(ac.i * 128);
+                        const uint64_t db = smem_desc_sw<128>(base + kFfWBytes + h * (kFfWBytes / 2));
+                        if (elected) {
+                            if (steps == 4) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) tc_mma_e4m3<true>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                            } else {
+                                for (int kk = 0; kk < steps; ++kk) tc_mma_e4m3<true>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                            }
+                            ff_commit<true>(&acc_full[ac.i]);
                         }
-                        ff_commit<true>(&empty[st.i]);
-                        ff_commit<true>(&acc_full[ac.i]);
+                        ac.next(kRowAccs);
                     }
+                    if (!ok) break;
+                    if (elected) ff_commit<true>(&empty[st.i]);
                     st.next(ST);
-                    ac.next(kRowAccs);
                 }
             }
             // every MMA issued is done before TMEM is freed, also after an abort
@@ -200,7 +342,73 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
             }
             __syncwarp();
-        } else if (warp >= 4) {
+        } else if (warp == 3) {
+            // ------------------------------------------------- scales ----
+            // For every kFp8Group k-blocks and row the products of its scale
+            // with the weight's: with the gate's and the up rows' (the same
+            // block of 128 features for both tiles), or with either tile's. A
+            // row's are requested before the wait for the ring.
+            RingPos sc, iq;
+            bool ok = true;
+            while (ok) {
+                if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
+                const Info *inf = info + iq.i;
+                const int all = inf->n;
+                if (all >= 0) {
+                    const int n = all / 2, tile = inf->nt & ~1;
+                    int row[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) row[j] = lane + 32 * j < n ? inf->row[(int)rank * n + lane + 32 * j] : -1;
+                    // lanes 0 to 3: the first, 4 to 7: the second
+                    const int wrow = UP ? (tile >> 1) + (lane & 4 ? p.scale_rows >> 1 : 0) : min(tile + (lane >> 2 & 1), p.ntiles - 1);
+                    const float *ws = reinterpret_cast<const float *>(p.w_scales) +
+                                      ((int64_t)inf->e * p.scale_rows + wrow) * p.num_kb + (lane & 3);
+                    for (int kb = 0; kb < p.num_kb; kb += kFp8Group) {
+                        uint32_t v[4][kFp8Group];
+                        float w = 0.0f;
+                        if (lane < 8 && kb + (lane & 3) < p.num_kb) w = __ldcg(ws + kb);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t *src = reinterpret_cast<const uint32_t *>(p.x_scales) +
+                                                  (uint64_t)(uint32_t)row[j] * (uint32_t)p.num_kb + kb;
+#pragma unroll
+                            for (int q = 0; q < kFp8Group; ++q) v[j][q] = 0u;
+                            if (p.scale_bytes == 16) {
+                                ld_cg_16(v[j], src, row[j]);
+                            } else if (p.scale_bytes == 8) {
+#pragma unroll
+                                for (int q = 0; q < kFp8Group; q += 2)
+                                    ld_cg_8(v[j] + q, src + q, kb + q < p.num_kb ? row[j] : -1);
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < kFp8Group; ++q)
+                                    if (row[j] >= 0 && kb + q < p.num_kb) v[j][q] = __ldcg(src + q);
+                            }
+                        }
+                        __syncwarp();
+                        if (!(ok = warp_wait(&scale_empty[sc.i], sc.ph ^ 1u, abort_flag))) break;
+                        float2 *to = scale_ring + sc.i * (kRowScaleBytes / 8) + lane;
+#pragma unroll
+                        for (int q = 0; q < kFp8Group; ++q) {
+                            const float w0 = __shfl_sync(0xffffffffu, w, q), w1 = __shfl_sync(0xffffffffu, w, 4 + q);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float x = __uint_as_float(v[j][q]);
+                                to[q * 128 + 32 * j] = make_float2(x * w0, x * w1);
+                            }
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&scale_full[sc.i]));
+                        sc.next(kRowScales);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
+                iq.next(kRowInfos);
+                if (all < 0) break;
+            }
+            __syncwarp();
+        } else {
             // -------------------------------------------- routed rows ----
             // A warp copies 32 of the CTA's rows for every stage: eight lanes
             // a row, a lane the same chunk of eight rows, whose addresses it
@@ -273,100 +481,106 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         // ------------------------------------------------------ epilogue ----
-        // one row a thread: row q 32 + lane of the CTA's, columns [128 half, +
-        // 128): the weight tile 2 t + half, both CTAs having the same tiles.
-        // sum[32 c + j]: of a gated tile 16 gate and their 16 up values in turn
+        // one row a thread: row q 32 + lane of the CTA's, all columns of one
+        // tile: sum[32 c + j], of a gated tile 16 gate and their 16 up values
+        // in turn
         const int q = warp & 3, half = (warp - 8) >> 2;
-        RingPos iq, ac;
-        const uint32_t buffer = smem_u32(out_rows) + (uint32_t)((warp - 8) * 32 * 128);
+        RingPos iq, sc;
+        int in = 0;            // k-block of the group of scales
+        uint32_t odd = 0, ph = 0;  // the next accumulator (2 odd + half), its parity
+        const uint32_t buffer = smem_u32(out_rows) + (uint32_t)((OUT == kRowE4m3 ? q : warp - 8) * 32 * 128);
+        const uint32_t hand_back = cluster_addr(smem_u32(&acc_empty[half]), 0u);
+        const int r = q * 32 + lane;
         while (true) {
             bool ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
             const Info *inf = info + iq.i;
-            const int n = ok ? inf->n / 2 : -1;  // (-1 / 2 = 0: told apart by the next line)
-            const bool more = ok && inf->n >= 0;
+            const int num_kb = ok && inf->n >= 0 ? p.num_kb : 0;
             float sum[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
-            const int r = q * 32 + lane;
-            int slot = -1, tile = 0;
-            if (more) {
-                if (r < n) slot = inf->slot[(int)rank * n + r];
-                tile = (inf->nt & ~1) + half;
-                const int xrow = r < n ? inf->row[(int)rank * n + r] : -1;
-                const float *xs = reinterpret_cast<const float *>(p.x_scales) + (uint64_t)(uint32_t)max(xrow, 0) * (uint32_t)p.num_kb;
-                const int wrow = min(tile, p.ntiles - 1) >> (UP ? 1 : 0);
-                const float *ws = reinterpret_cast<const float *>(p.w_scales) + ((int64_t)inf->e * p.scale_rows + wrow) * p.num_kb;
-                const float *wu = ws + (int64_t)(p.scale_rows >> 1) * p.num_kb;  // (UP)
-                // this row's scales of four k-blocks, and the next four; lane l
-                // holds the tile's of k-block l of 32
-                uint32_t now[4] = {}, next[4];
-                auto request = [&](int kb, uint32_t (&v)[4]) {
-                    const uint32_t *src = reinterpret_cast<const uint32_t *>(xs) + kb;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = 0u;
-                    if (kb >= p.num_kb) return;
-                    if (p.scale_bytes == 16) {
-                        ld_cg_16(v, src, xrow);
-                    } else if (p.scale_bytes == 8) {
-                        ld_cg_8(v, src, xrow);
-                        ld_cg_8(v + 2, src + 2, kb + 2 < p.num_kb ? xrow : -1);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (xrow >= 0 && kb + j < p.num_kb) v[j] = __ldcg(src + j);
-                    }
-                };
-                float tg = 0.0f, tu = 0.0f;
-                request(0, next);
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if ((kb & 31) == 0) {
-                        if (kb + lane < p.num_kb) {
-                            tg = __ldcg(ws + kb + lane);
-                            if (UP) tu = __ldcg(wu + kb + lane);
-                        }
-                        __syncwarp();
-                    }
-                    if ((kb & 3) == 0) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) now[j] = next[j];
-                        request(kb + 4, next);
-                    }
-                    const float sx = __uint_as_float(kb & 2 ? (kb & 1 ? now[3] : now[2]) : (kb & 1 ? now[1] : now[0]));
-                    const float g = sx * __shfl_sync(0xffffffffu, tg, kb & 31);
-                    const float u = UP ? sx * __shfl_sync(0xffffffffu, tu, kb & 31) : g;
-                    if (!(ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag))) break;
-                    tc_fence_after();
-                    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * 256 + half * 128);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32_async(acc + 32 * c, v);
-                        tmem_wait_ld(v);
-                        if (c == 3) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[ac.i]), 0u));
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[32 * c + j] = fmaf(__uint_as_float(v[j]), j < 16 ? g : u, sum[32 * c + j]);
-                    }
-                    ac.next(kRowAccs);
+            for (int kb = 0; kb < num_kb; ++kb) {
+                // (after a wait that gave up the loop runs on, over whatever
+                // TMEM and the ring hold: leaving it would cost copies of the sums)
+                if (in == 0) ok &= warp_wait(&scale_full[sc.i], sc.ph, abort_flag);
+                const float2 s = scale_ring[sc.i * (kRowScaleBytes / 8) + in * 128 + r];
+                const float g = UP || half == 0 ? s.x : s.y, u = UP ? s.y : g;
+                ok &= warp_wait(&acc_full[2 * odd + half], ph, abort_flag);
+                tc_fence_after();
+                float last[32];
+                add_columns(sum, last, tmem + ((uint32_t)(q * 32) << 16) + (2 * odd + half) * 128u, g, u);
+                tc_fence_before();
+                ++in;
+                if (lane == 0) {
+                    mbar_arrive_cluster(hand_back + 16u * odd);
+                    if (in == kFp8Group || kb + 1 == num_kb) mbar_arrive(smem_u32(&scale_empty[sc.i]));
                 }
+                __syncwarp();
+                if (in == kFp8Group || kb + 1 == num_kb) {
+                    in = 0;
+                    sc.next(kRowScales);
+                }
+                ph ^= odd;
+                odd ^= 1u;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[96 + j] = fmaf(last[j], j < 16 ? g : u, sum[96 + j]);
             }
             if constexpr (OUT == kRowE4m3) ok = meet_two_if(1 + q, ok);  // both warps of a row go on, or none does
-            if (!ok || !more) break;
+            if (!ok || num_kb == 0) break;
+            const int n = inf->n / 2, tile = (inf->nt & ~1) + half;
+            const int slot = r < n ? inf->slot[(int)rank * n + r] : -1;
             if constexpr (UP) {
-                const int f = tile * 64, width = min(128, 2 * max(p.feat - f, 0));  // bytes of this tile's features in bf16
+                const int f = tile * 64;
                 uint32_t o[32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o[8 * c + j] = pack_bf16x2(swiglu(sum[32 * c + 2 * j], sum[32 * c + 16 + 2 * j]),
-                                                   swiglu(sum[32 * c + 2 * j + 1], sum[32 * c + 17 + 2 * j]));
+                    for (int j = 0; j < 16; j += 4) {
+                        const float g[4] = {sum[32 * c + j], sum[32 * c + j + 1], sum[32 * c + j + 2], sum[32 * c + j + 3]};
+                        const float u[4] = {sum[32 * c + 16 + j], sum[32 * c + 17 + j], sum[32 * c + 18 + j], sum[32 * c + 19 + j]};
+                        float a[4];
+                        swiglu4(g, u, a);
+                        o[8 * c + j / 2] = pack_bf16x2(a[0], a[1]);
+                        o[8 * c + j / 2 + 1] = pack_bf16x2(a[2], a[3]);
+                    }
                 if constexpr (OUT == kRowBf16) {
                     uint8_t *to = slot >= 0 ? static_cast<uint8_t *>(p.out) + ((int64_t)slot * p.feat + f) * 2 : nullptr;
-                    put_row_lines(buffer, o, to, width);
+                    put_row_lines(buffer, o, to, 2 * max(p.feat - f, 0));
+                } else {
+                    // the block of 128 features is both tiles': the largest
+                    // magnitude over both, then this tile's 64 codes beside
+                    // the other's, and each warp writes half of the rows
+                    uint32_t m = 0u;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) m = max(m, max(o[j] & 0x7FFFu, (o[j] >> 16) & 0x7FFFu));
+                    amax_ex[128 * half + r] = m;
+                    __syncwarp();
+                    ok = meet_two_if(1 + q, true);
+                    m = max(m, amax_ex[128 * (half ^ 1) + r]);
+                    float scale, factor;
+                    block_scale_e4m3(m, scale, factor);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint2 lo = codes8(make_uint4(o[8 * c], o[8 * c + 1], o[8 * c + 2], o[8 * c + 3]), factor);
+                        const uint2 hi = codes8(make_uint4(o[8 * c + 4], o[8 * c + 5], o[8 * c + 6], o[8 * c + 7]), factor);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                     ::"r"(buffer + (uint32_t)(lane * 128 + (((4 * half + c) ^ (lane & 7)) << 4))), "r"(lo.x),
+                                       "r"(lo.y), "r"(hi.x), "r"(hi.y) : "memory");
+                    }
+                    const int f0 = f & ~127;
+                    if (half == 0 && slot >= 0) p.out_scales[(int64_t)slot * ((p.feat + 127) >> 7) + (f0 >> 7)] = scale;
+                    __syncwarp();
+                    ok = meet_two_if(1 + q, true);
+                    uint8_t *to = slot >= 0 ? static_cast<uint8_t *>(p.out) + (int64_t)slot * p.feat + f0 : nullptr;
+                    const int c = lane & 7;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = 16 * half + 4 * i + (lane >> 3);
+                        uint4 w;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(buffer + (uint32_t)(at * 128 + ((c ^ (at & 7)) << 4))) : "memory");
+                        uint8_t *line = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), at));
+                        if (line != nullptr && 16 * c < p.feat - f0) *reinterpret_cast<uint4 *>(line + 16 * c) = w;
+                    }
                 }
             } else {
                 constexpr int kPer = OUT == kRowF32 ? 32 : 64;  // features of 128 bytes
@@ -375,9 +589,8 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     uint32_t o[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        o[j] = OUT == kRowF32 ? __float_as_uint(sum[kPer * c + (OUT == kRowF32 ? j : 0)])
-                                              : pack_bf16x2(sum[kPer * c + (OUT == kRowF32 ? 0 : 2 * j)],
-                                                            sum[kPer * c + (OUT == kRowF32 ? 0 : 2 * j + 1)]);
+                        if constexpr (OUT == kRowF32) o[j] = __float_as_uint(sum[kPer * c + j]);
+                        else o[j] = pack_bf16x2(sum[kPer * c + 2 * j], sum[kPer * c + 2 * j + 1]);
                     const int f = tile * 128 + kPer * c;
                     uint8_t *to = slot >= 0 ? static_cast<uint8_t *>(p.out) + ((int64_t)slot * p.feat + f) * (128 / kPer) : nullptr;
                     put_row_lines(buffer, o, to, max(p.feat - f, 0) * (128 / kPer));
@@ -421,6 +634,7 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
     if (const cudaError_t e = common_params(a, p)) return e;
     p.x = static_cast<const uint8_t *>(a.x);
     p.x_bytes = a.K;
+    p.out_scales = a.out_scales;
     p.x_row_bytes = (uint32_t)a.ld_x;
     p.x_scales = static_cast<const uint8_t *>(a.x_scales);
     p.w_scales = static_cast<const uint8_t *>(a.w_scales);
@@ -432,7 +646,7 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
     if (p.stages < 5) return cudaErrorNotSupported;  // (more than the loaders have under way; never with these sizes)
     const size_t smem = 1024 + (size_t)p.stages * kRowStageBytes + kRowMiscBytes;
     CUtensorMap mw;
-    if (!encode_weight(&mw, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint64_t)a.K, (cuuint64_t)a.K, kFfRowBytes))
+    if (!encode_weight(&mw, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint64_t)a.K, (cuuint64_t)a.K, kFfRowBytes, kFfRows / 2))
         return cudaErrorInvalidValue;
 
     static std::atomic<bool> configured[kMaxDevices];
@@ -469,6 +683,7 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
 }
 
 constexpr int kRowsPerExpert = 128;
+bool expert_rows_fp8(int64_t numel, int num_experts) { return numel >= (int64_t)kRowsPerExpert * num_experts; }
 
 template <bool UP, bool F32>
 static cudaError_t launch_columns(const FfnLaunch &a, int sms, cudaStream_t stream) {
@@ -478,7 +693,8 @@ static cudaError_t launch_columns(const FfnLaunch &a, int sms, cudaStream_t stre
 }
 
 cudaError_t launch_expert_product_fp8(const FfnLaunch &a, int sms, cudaStream_t stream) {
-    const bool rows = a.numel >= (int64_t)kRowsPerExpert * a.num_experts;
+    const bool rows = expert_rows_fp8(a.numel, a.num_experts);
+    if (a.out_scales) return rows && a.gated ? launch_rows<true, kRowE4m3>(a, sms, stream) : cudaErrorNotSupported;
     if (a.gated) return rows ? launch_rows<true, kRowBf16>(a, sms, stream) : launch_columns<true, false>(a, sms, stream);
     if (a.out32) return rows ? launch_rows<false, kRowF32>(a, sms, stream) : launch_columns<false, true>(a, sms, stream);
     return rows ? launch_rows<false, kRowBf16>(a, sms, stream) : launch_columns<false, false>(a, sms, stream);

@@ -215,6 +215,7 @@ struct FfnLaunch {
     const int32_t *sorted, *eids, *npp;
     void *out;
     bool out32;              // (not gated) out is fp32
+    float *out_scales;       // (gated, fp8, expert_rows_fp8) out is E4M3 with these scales
     void *hdr;               // workspace header (sticky error word)
 };
 // Whether the rows between the second product and the sum are fp32 (out32)
@@ -222,6 +223,8 @@ struct FfnLaunch {
 bool expert_rows_fp32(int64_t numel, int num_experts, int H);
 cudaError_t launch_expert_product(const FfnLaunch &a, cudaStream_t stream);
 cudaError_t launch_expert_product_fp8(const FfnLaunch &a, int sms, cudaStream_t stream);
+// Whether the E4M3 products of that many rows take the form that can write E4M3.
+bool expert_rows_fp8(int64_t numel, int num_experts);
 // Whether a product of that many rows runs on CTA pairs.
 bool expert_pairs(int64_t numel, int num_experts);
 // The word on the current device that gets every product's error bits.
