@@ -21,9 +21,10 @@ namespace smr {
 
 // A piece of work: up to 256 routed rows (blocks of one expert together) and two
 // weight tiles for a CTA pair; either CTA holds half of the rows and half of
-// each tile. 16 warps: 0 weights, 1 MMAs, 2 scout, 3 scales, 4 to 7 load the
-// routed rows (32 each), the last 8 are the epilogue, two for each quarter of
-// TMEM's lanes, one of these for either tile.
+// each tile. 16 warps: 0 and 1 issue the MMAs of either tile, 2 scout, 3
+// scales, 4 to 7 load the routed rows (32 each; 4 the weights too), the last 8
+// are the epilogue, two for each quarter of TMEM's lanes, one of these for
+// either tile.
 constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4, kRowScales = 3;
 constexpr int kRowStageBytes = 2 * kFfWBytes;
 constexpr int kRowScaleBytes = kFp8Group * 128 * 8;  // [k-block][row] (two products of scales)
@@ -36,6 +37,30 @@ constexpr int kRowMiscBytes = kRowBarBytes + kRowInfos * (int)sizeof(FfInfo<256>
                               kRowOutBytes + 2 * 128 * 4;
 
 enum RowOut : int { kRowBf16 = 0, kRowF32 = 1, kRowE4m3 = 2 };
+
+// The four MMAs of a k-block (K = 32 each), the first over what D holds.
+__device__ __forceinline__ void mma_k_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+        " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+        " setp.ne.b32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        " setp.eq.b32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, p;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, p;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, p;\n}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
+}
+// Arrivals where `yes` (no branch: a warp that splits here is late for the rest).
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool yes) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}"
+                 ::"r"(bar), "r"((uint32_t)yes) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster_if(uint32_t bar, bool yes) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}"
+                 ::"r"(bar), "r"((uint32_t)yes) : "memory");
+}
 
 // Two warps meet; both get whether both came with ok.
 __device__ __forceinline__ bool meet_two_if(int id, bool ok) {
@@ -215,7 +240,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(smem_u32(&full[s]), 1 + 2 * kRowLoaders);  // the weights' bytes, the row loaders of both CTAs
-            mbar_init(smem_u32(&empty[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 2);  // either tile's MMAs
         }
         for (int s = 0; s < kRowAccs; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
@@ -229,7 +254,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             mbar_init(smem_u32(&scale_full[s]), 1);
             mbar_init(smem_u32(&scale_empty[s]), kFfDrains);
         }
-        mbar_init(smem_u32(last), 1);
+        mbar_init(smem_u32(last), 2);
         *abort_flag = 0;
         mbar_fence_init();
         prefetch_tensormap(&tm_w);
@@ -247,56 +272,20 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     griddep_launch_dependents();
 
     const uint32_t ring = smem_u32(smem);  // a stage: [rows][64 rows of the first tile][64 of the second]
-    int issued = 0;
+    int issued = 0;  // stages whose weights were requested (warp 4)
     // A thread of the epilogue holds 128 sums: its 8 warps get registers of the
     // other 8 (256 x 64 + 256 x 192 = the 512 x 128 of the launch, which the
     // launcher makes sure of).
     if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        if (warp == 0) {
-            // ------------------------------------------------ weights ----
-            const bool elected = elect_one();
-            RingPos st, iq;
-            bool ok = true;
-            while (ok) {
-                if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
-                const volatile Info *inf = info + iq.i;
-                const int n = inf->n, nt = inf->nt, e = inf->e;
-                __syncwarp();
-                if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
-                iq.next(kRowInfos);
-                if (n < 0) break;
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
-                    const uint32_t to = ring + (uint32_t)(st.i * kRowStageBytes + kFfWBytes), bar = smem_u32(&full[st.i]);
-                    if (elected) {
-                        // both CTAs' bytes complete the leader's barrier
-                        if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
-                        const uint32_t fb = cluster_addr(bar, 0u);
-                        // this CTA's half of either tile: the first CTA's is the tile's first 64 rows
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int tile = (nt & ~1) + h;
-                            if constexpr (UP) tma_load_5d_pair(to + h * (kFfWBytes / 2), &tm_w, kb * kFfRowBytes, 4 * tile + 2 * (int)rank, e, fb);
-                            else tma_load_3d_pair(to + h * (kFfWBytes / 2), &tm_w, kb * kFfRowBytes, kFfRows * tile + 64 * (int)rank, e, fb);
-                        }
-                    }
-                    ++issued;
-                    st.next(ST);
-                }
-            }
-            __syncwarp();
-        } else if (warp == 2) {
-            ff_scout<UP, true, 256, kRowInfos, 2>(p, info, info_full, info_empty, abort_flag, rank);
-            __syncwarp();
-        } else if (warp == 1) {
+        if (warp < 2) {
             // --------------------------------------------------- MMAs ----
+            // A warp for either tile: its k-blocks in turn into two
+            // accumulators. (From an accumulator's last MMA to the next one's
+            // first in it the signals between the CTAs take 1100 cycles
+            // without any work in between, a tile's MMAs 256; and issuing four
+            // MMAs takes a warp 300.)
             const bool elected = elect_one();
-            // A k-block's two tiles one after the other, each into an
-            // accumulator that its own warps of the epilogue wait for: from an
-            // accumulator's last MMA to the next one's first in it the signals
-            // between the CTAs take 1100 cycles without any work in between, a
-            // tile's MMAs 256.
             const uint32_t idesc = idesc_e4m3(2 * kFfRows, 128);
             RingPos st, iq, ac;
             bool ok = true;
@@ -309,30 +298,24 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (n < 0) break;
                 if (rank != 0) continue;
                 for (int kb = 0; kb < p.num_kb; ++kb) {
+                    uint64_t *done = &acc_full[2 * ac.i + warp];
+                    if (!(ok = warp_wait(&acc_empty[2 * ac.i + warp], ac.ph ^ 1u, abort_flag))) break;
                     if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
-                    const uint32_t base = ring + (uint32_t)(st.i * kRowStageBytes);
-                    const uint64_t da = smem_desc_sw<128>(base);
+                    tc_fence_after();
+                    const uint32_t base = ring + (uint32_t)(st.i * kRowStageBytes), acc = tmem + (uint32_t)((2 * ac.i + warp) * 128);
+                    const uint64_t da = smem_desc_sw<128>(base), db = smem_desc_sw<128>(base + kFfWBytes + warp * (kFfWBytes / 2));
                     const int steps = kb + 1 == p.num_kb ? p.last_steps : 4;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
-                        tc_fence_after();
-                        const uint32_t acc = tmem + (uint32_t)(ac.i * 128);
-                        const uint64_t db = smem_desc_sw<128>(base + kFfWBytes + h * (kFfWBytes / 2));
-                        if (elected) {
-                            if (steps == 4) {
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) tc_mma_e4m3<true>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
-                            } else {
-                                for (int kk = 0; kk < steps; ++kk) tc_mma_e4m3<true>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
-                            }
-                            ff_commit<true>(&acc_full[ac.i]);
+                    if (elected) {
+                        if (steps == 4) {
+                            mma_k_block(acc, da, db, idesc);
+                        } else {
+                            for (int kk = 0; kk < steps; ++kk) tc_mma_e4m3<true>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
                         }
-                        ac.next(kRowAccs);
+                        ff_commit<true>(done);
+                        ff_commit<true>(&empty[st.i]);
                     }
-                    if (!ok) break;
-                    if (elected) ff_commit<true>(&empty[st.i]);
                     st.next(ST);
+                    ac.next(2);
                 }
             }
             // every MMA issued is done before TMEM is freed, also after an abort
@@ -341,6 +324,9 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 volatile int never = 0;
                 if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
             }
+            __syncwarp();
+        } else if (warp == 2) {
+            ff_scout<UP, true, 256, kRowInfos, 2>(p, info, info_full, info_empty, abort_flag, rank);
             __syncwarp();
         } else if (warp == 3) {
             // ------------------------------------------------- scales ----
@@ -416,7 +402,9 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             // ((c ^ (r & 7)) << 4), the 128-byte swizzle. Copies of as many
             // stages as are free are under way; the oldest is waited for, made
             // visible to the tensor core and announced when the next stage is
-            // not free yet, or when all are under way.
+            // not free yet, or when all are under way. The first of them
+            // requests a stage's weights too.
+            const bool weights = warp == 4 && elect_one();
             const int c = lane & 7, r0 = 32 * (warp - 4) + (lane >> 3);  // rows r0 + 4 i
             const uint32_t to0 = ring + (uint32_t)(r0 * kFfRowBytes + ((c ^ (lane >> 3)) << 4));
             const uint32_t to1 = ring + (uint32_t)(r0 * kFfRowBytes + ((c ^ (4 + (lane >> 3))) << 4));
@@ -454,10 +442,25 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         if (row >= 0) copy |= 1u << i;
                         from[i] = p.x + (uint64_t)(uint32_t)max(row, 0) * p.x_row_bytes + c * 16;
                     }
+                    const int nt = inf->nt & ~1, e = inf->e;
                     int left = p.x_bytes - c * 16;  // (pieces past the row's end are not read by the last MMA steps)
                     for (int kb = 0; kb < p.num_kb; ++kb) {
                         if (!(ok = wait_for(&empty[st.i], st.ph ^ 1u))) break;
                         const uint32_t base = (uint32_t)(st.i * kRowStageBytes);
+                        if (weights) {
+                            const uint32_t bar = smem_u32(&full[st.i]), fb = cluster_addr(bar, 0u);
+                            // both CTAs' bytes complete the leader's barrier
+                            if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
+                            // this CTA's half of either tile: the first CTA's is the tile's first 64 rows
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t to = ring + base + (uint32_t)(kFfWBytes + h * (kFfWBytes / 2));
+                                if constexpr (UP) tma_load_5d_pair(to, &tm_w, kb * kFfRowBytes, 4 * (nt + h) + 2 * (int)rank, e, fb);
+                                else tma_load_3d_pair(to, &tm_w, kb * kFfRowBytes, kFfRows * (nt + h) + 64 * (int)rank, e, fb);
+                            }
+                        }
+                        __syncwarp();
+                        ++issued;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             cp_async_16((i & 1 ? to1 : to0) + base + (uint32_t)(i * 4 * kFfRowBytes), from[i],
@@ -498,27 +501,27 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             float sum[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+            if (num_kb > 0) ok &= warp_wait(&scale_full[sc.i], sc.ph, abort_flag);
+            float2 s = scale_ring[sc.i * (kRowScaleBytes / 8) + r];
             for (int kb = 0; kb < num_kb; ++kb) {
                 // (after a wait that gave up the loop runs on, over whatever
                 // TMEM and the ring hold: leaving it would cost copies of the sums)
-                if (in == 0) ok &= warp_wait(&scale_full[sc.i], sc.ph, abort_flag);
-                const float2 s = scale_ring[sc.i * (kRowScaleBytes / 8) + in * 128 + r];
                 const float g = UP || half == 0 ? s.x : s.y, u = UP ? s.y : g;
                 ok &= warp_wait(&acc_full[2 * odd + half], ph, abort_flag);
                 tc_fence_after();
                 float last[32];
                 add_columns(sum, last, tmem + ((uint32_t)(q * 32) << 16) + (2 * odd + half) * 128u, g, u);
                 tc_fence_before();
-                ++in;
-                if (lane == 0) {
-                    mbar_arrive_cluster(hand_back + 16u * odd);
-                    if (in == kFp8Group || kb + 1 == num_kb) mbar_arrive(smem_u32(&scale_empty[sc.i]));
-                }
-                __syncwarp();
-                if (in == kFp8Group || kb + 1 == num_kb) {
+                arrive_cluster_if(hand_back + 16u * odd, lane == 0);
+                // the next k-block's scales
+                const bool group = ++in == kFp8Group || kb + 1 == num_kb;
+                if (group) {
+                    arrive_if(smem_u32(&scale_empty[sc.i]), lane == 0);
                     in = 0;
                     sc.next(kRowScales);
+                    if (kb + 1 < num_kb) ok &= warp_wait(&scale_full[sc.i], sc.ph, abort_flag);
                 }
+                s = scale_ring[sc.i * (kRowScaleBytes / 8) + in * 128 + r];
                 ph ^= odd;
                 odd ^= 1u;
 #pragma unroll
@@ -605,7 +608,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
 
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag && warp == 0 && lane == 0) {
+    if (*abort_flag && warp == 4 && lane == 0) {
         // a wait gave up: the piece's outputs are not written; weights still in
         // flight land before the CTA leaves
         ffn_error(p, kErrWaitTimeout);
