@@ -25,7 +25,7 @@ namespace smr {
 // scales, 4 to 7 load the routed rows (32 each; 4 the weights too), the last 8
 // are the epilogue, two for each quarter of TMEM's lanes, one of these for
 // either tile.
-constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4, kRowScales = 3;
+constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4, kRowScales = 4;
 constexpr int kRowStageBytes = 2 * kFfWBytes;
 constexpr int kRowScaleBytes = kFp8Group * 128 * 8;  // [k-block][row] (two products of scales)
 constexpr int kRowBars = 2 * kFfMaxStages + 2 * kRowAccs + 2 * kRowInfos + 2 * kRowScales + 1;
@@ -60,6 +60,30 @@ __device__ __forceinline__ void arrive_if(uint32_t bar, bool yes) {
 __device__ __forceinline__ void arrive_cluster_if(uint32_t bar, bool yes) {
     asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}"
                  ::"r"(bar), "r"((uint32_t)yes) : "memory");
+}
+
+// As warp_wait, by shared-memory addresses: the epilogue has no registers for
+// 64-bit ones (what it spills comes back in 270 cycles, a third of a k-block).
+__device__ __forceinline__ bool warp_wait_at(uint32_t bar, uint32_t parity, uint32_t abort_at) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) {
+        const long long t0 = clock64();
+        while (!(ok = mbar_try_wait(bar, parity))) {
+            int gone;
+            asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(gone) : "r"(abort_at) : "memory");
+            if (gone) break;
+            if (clock64() - t0 > kWaitCycles) {
+                asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort_at), "r"(1) : "memory");
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ int lds_int(uint32_t at) {
+    int v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
 // Two warps meet; both get whether both came with ok.
@@ -487,50 +511,57 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         // one row a thread: row q 32 + lane of the CTA's, all columns of one
         // tile: sum[32 c + j], of a gated tile 16 gate and their 16 up values
         // in turn
+        // Addresses are offsets from `at`, ring positions come from counts.
         const int q = warp & 3, half = (warp - 8) >> 2;
-        RingPos iq, sc;
-        int in = 0;            // k-block of the group of scales
-        uint32_t odd = 0, ph = 0;  // the next accumulator (2 odd + half), its parity
-        const uint32_t buffer = smem_u32(out_rows) + (uint32_t)((OUT == kRowE4m3 ? q : warp - 8) * 32 * 128);
-        const uint32_t hand_back = cluster_addr(smem_u32(&acc_empty[half]), 0u);
-        const int r = q * 32 + lane;
+        const uint32_t at = smem_u32(misc);
+        constexpr uint32_t kAccFull = 16 * kFfMaxStages, kAccEmpty = kAccFull + 8 * kRowAccs, kInfoFull = kAccEmpty + 8 * kRowAccs,
+                           kInfoEmpty = kInfoFull + 8 * kRowInfos, kScaleFull = kInfoEmpty + 8 * kRowInfos,
+                           kScaleEmpty = kScaleFull + 8 * kRowScales, kAbort = kScaleEmpty + 8 * kRowScales + 12,
+                           kInfo = kRowBarBytes, kScales = kInfo + kRowInfos * (uint32_t)sizeof(Info),
+                           kOutRows = kScales + kRowScales * kRowScaleBytes;
+        const uint32_t hand_back = cluster_addr(at + kAccEmpty + 8u * half, 0u);
+        const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + 128u * half, scales = at + kScales + 8u * (q * 32 + lane) + (UP ? 0u : 4u * half);
+        uint32_t items = 0, groups = 0, units = 0;
         while (true) {
-            bool ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
-            const Info *inf = info + iq.i;
-            const int num_kb = ok && inf->n >= 0 ? p.num_kb : 0;
+            bool ok = warp_wait_at(at + kInfoFull + 8 * (items & (kRowInfos - 1)), items / kRowInfos & 1u, at + kAbort);
+            const uint32_t inf = at + kInfo + (items & (kRowInfos - 1)) * (uint32_t)sizeof(Info);
+            const bool more = ok && lds_int(inf) >= 0;
             float sum[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
-            if (num_kb > 0) ok &= warp_wait(&scale_full[sc.i], sc.ph, abort_flag);
-            float2 s = scale_ring[sc.i * (kRowScaleBytes / 8) + r];
-            for (int kb = 0; kb < num_kb; ++kb) {
-                // (after a wait that gave up the loop runs on, over whatever
-                // TMEM and the ring hold: leaving it would cost copies of the sums)
-                const float g = UP || half == 0 ? s.x : s.y, u = UP ? s.y : g;
-                ok &= warp_wait(&acc_full[2 * odd + half], ph, abort_flag);
+            // (after a wait that gave up the loop runs on, over whatever TMEM
+            // and the ring hold: leaving it would cost copies of the sums)
+#pragma unroll 1
+            for (int kb = more ? 0 : p.num_kb; kb < p.num_kb; ++kb) {
+                if ((kb & (kFp8Group - 1)) == 0)
+                    ok &= warp_wait_at(at + kScaleFull + 8 * (groups & (kRowScales - 1)), groups / kRowScales & 1u, at + kAbort);
+                float g, u;
+                const uint32_t from_s = scales + (groups & (kRowScales - 1)) * kRowScaleBytes + (kb & (kFp8Group - 1)) * 1024u;
+                if constexpr (UP) {
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(g), "=f"(u) : "r"(from_s) : "memory");
+                } else {
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g) : "r"(from_s) : "memory");
+                    u = g;
+                }
+                ok &= warp_wait_at(at + kAccFull + 8u * half + 16u * (units & 1u), units >> 1 & 1u, at + kAbort);
                 tc_fence_after();
                 float last[32];
-                add_columns(sum, last, tmem + ((uint32_t)(q * 32) << 16) + (2 * odd + half) * 128u, g, u);
+                add_columns(sum, last, from + 256u * (units & 1u), g, u);
                 tc_fence_before();
-                arrive_cluster_if(hand_back + 16u * odd, lane == 0);
-                // the next k-block's scales
-                const bool group = ++in == kFp8Group || kb + 1 == num_kb;
-                if (group) {
-                    arrive_if(smem_u32(&scale_empty[sc.i]), lane == 0);
-                    in = 0;
-                    sc.next(kRowScales);
-                    if (kb + 1 < num_kb) ok &= warp_wait(&scale_full[sc.i], sc.ph, abort_flag);
+                arrive_cluster_if(hand_back + 16u * (units & 1u), lane == 0);
+                ++units;
+                if ((kb & (kFp8Group - 1)) == kFp8Group - 1 || kb + 1 == p.num_kb) {
+                    arrive_if(at + kScaleEmpty + 8 * (groups & (kRowScales - 1)), lane == 0);
+                    ++groups;
                 }
-                s = scale_ring[sc.i * (kRowScaleBytes / 8) + in * 128 + r];
-                ph ^= odd;
-                odd ^= 1u;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) sum[96 + j] = fmaf(last[j], j < 16 ? g : u, sum[96 + j]);
             }
             if constexpr (OUT == kRowE4m3) ok = meet_two_if(1 + q, ok);  // both warps of a row go on, or none does
-            if (!ok || num_kb == 0) break;
-            const int n = inf->n / 2, tile = (inf->nt & ~1) + half;
-            const int slot = r < n ? inf->slot[(int)rank * n + r] : -1;
+            if (!ok || !more) break;
+            const int r = q * 32 + lane, n = lds_int(inf) / 2, tile = (lds_int(inf + 4) & ~1) + half;
+            const int slot = r < n ? lds_int(inf + 16 + 4 * ((int)rank * n + r)) : -1;
+            const uint32_t buffer = at + kOutRows + (uint32_t)((OUT == kRowE4m3 ? q : warp - 8) * 32 * 128);
             if constexpr (UP) {
                 const int f = tile * 64;
                 uint32_t o[32];
@@ -600,8 +631,8 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
-            iq.next(kRowInfos);
+            if (lane == 0) mbar_arrive(at + kInfoEmpty + 8 * (items & (kRowInfos - 1)));
+            ++items;
         }
         __syncwarp();
     }
