@@ -28,7 +28,7 @@ namespace smr {
 constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4, kRowScales = 4;
 constexpr int kRowStageBytes = 2 * kFfWBytes;
 constexpr int kRowScaleBytes = kFp8Group * 128 * 8;  // [k-block][row] (two products of scales)
-constexpr int kRowBars = 2 * kFfMaxStages + 2 * kRowAccs + 2 * kRowInfos + 2 * kRowScales + 1;
+constexpr int kRowBars = 3 * kFfMaxStages + 2 * kRowAccs + 2 * kRowInfos + 2 * kRowScales + 1;
 constexpr int kRowBarBytes = (kRowBars * 8 + 8 + 15) / 16 * 16;
 // The epilogue's outputs leave through shared memory, 128 bytes of 32 rows a
 // warp at a time, so that rows are written in whole lines.
@@ -243,9 +243,10 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     const int ST = p.stages;
     uint8_t *misc = smem + (size_t)ST * kRowStageBytes;
     // full and acc_empty are the leader's, the others each CTA's own
-    uint64_t *full = reinterpret_cast<uint64_t *>(misc);
+    uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // the weights landed, and the other CTA's rows
     uint64_t *empty = full + kFfMaxStages;
-    uint64_t *acc_full = empty + kFfMaxStages;
+    uint64_t *rows_full = empty + kFfMaxStages;           // this CTA's rows landed
+    uint64_t *acc_full = rows_full + kFfMaxStages;
     uint64_t *acc_empty = acc_full + kRowAccs;
     uint64_t *info_full = acc_empty + kRowAccs;
     uint64_t *info_empty = info_full + kRowInfos;
@@ -263,7 +264,8 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     const uint32_t rank = cluster_ctarank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(smem_u32(&full[s]), 1 + 2 * kRowLoaders);  // the weights' bytes, the row loaders of both CTAs
+            mbar_init(smem_u32(&full[s]), 2);
+            mbar_init(smem_u32(&rows_full[s]), 32 * kRowLoaders);
             mbar_init(smem_u32(&empty[s]), 2);  // either tile's MMAs
         }
         for (int s = 0; s < kRowAccs; ++s) {
@@ -320,10 +322,23 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 if (elected) mbar_arrive(smem_u32(&info_empty[iq.i]));
                 iq.next(kRowInfos);
                 if (n < 0) break;
-                if (rank != 0) continue;
+                if (rank != 0) {
+                    // the peer's first warp passes its rows on, once the
+                    // tensor core can see them
+                    if (warp != 0) continue;
+                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                        if (!(ok = warp_wait(&rows_full[st.i], st.ph, abort_flag))) break;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        if (elected) mbar_arrive_cluster(cluster_addr(smem_u32(&full[st.i]), 0u));
+                        st.next(ST);
+                    }
+                    continue;
+                }
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     uint64_t *done = &acc_full[2 * ac.i + warp];
                     if (!(ok = warp_wait(&acc_empty[2 * ac.i + warp], ac.ph ^ 1u, abort_flag))) break;
+                    if (!(ok = warp_wait(&rows_full[st.i], st.ph, abort_flag))) break;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
                     tc_fence_after();
                     const uint32_t base = ring + (uint32_t)(st.i * kRowStageBytes), acc = tmem + (uint32_t)((2 * ac.i + warp) * 128);
@@ -423,37 +438,19 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             // A warp copies 32 of the CTA's rows for every stage: eight lanes
             // a row, a lane the same chunk of eight rows, whose addresses it
             // keeps for the whole item. Chunk c of row r lands at r * 128 +
-            // ((c ^ (r & 7)) << 4), the 128-byte swizzle. Copies of as many
-            // stages as are free are under way; the oldest is waited for, made
-            // visible to the tensor core and announced when the next stage is
-            // not free yet, or when all are under way. The first of them
+            // ((c ^ (r & 7)) << 4), the 128-byte swizzle. The copies announce
+            // themselves when they land (a warp that waited for them and made
+            // them visible to the tensor core would take 900 cycles a stage);
+            // who waits for them does the rest. The first of the warps
             // requests a stage's weights too.
             const bool weights = warp == 4 && elect_one();
             const int c = lane & 7, r0 = 32 * (warp - 4) + (lane >> 3);  // rows r0 + 4 i
             const uint32_t to0 = ring + (uint32_t)(r0 * kFfRowBytes + ((c ^ (lane >> 3)) << 4));
             const uint32_t to1 = ring + (uint32_t)(r0 * kFfRowBytes + ((c ^ (4 + (lane >> 3))) << 4));
-            RingPos st, old, iq;  // the next stage, the oldest under way
-            int pending = 0;
-            auto announce = [&] {
-                switch (pending) {  // (all but the oldest may stay under way)
-                    case 1: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-                    case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-                    case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-                    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&full[old.i]), 0u));
-                old.next(ST);
-                --pending;
-            };
-            auto wait_for = [&](uint64_t *bar, uint32_t parity) {
-                while (pending > 0 && !__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) announce();
-                return warp_wait(bar, parity, abort_flag);
-            };
+            RingPos st, iq;
             bool ok = true;
             while (ok) {
-                if (!(ok = wait_for(&info_full[iq.i], iq.ph))) break;
+                if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
                 const Info *inf = info + iq.i;
                 const int all = inf->n;
                 if (all >= 0) {
@@ -469,7 +466,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     const int nt = inf->nt & ~1, e = inf->e;
                     int left = p.x_bytes - c * 16;  // (pieces past the row's end are not read by the last MMA steps)
                     for (int kb = 0; kb < p.num_kb; ++kb) {
-                        if (!(ok = wait_for(&empty[st.i], st.ph ^ 1u))) break;
+                        if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
                         const uint32_t base = (uint32_t)(st.i * kRowStageBytes);
                         if (weights) {
                             const uint32_t bar = smem_u32(&full[st.i]), fb = cluster_addr(bar, 0u);
@@ -491,10 +488,9 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                                         left > 0 && (copy >> i & 1u) ? 0 : -1);
                             from[i] += kFfRowBytes;
                         }
-                        asm volatile("cp.async.commit_group;" ::: "memory");
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&rows_full[st.i])) : "memory");
                         left -= kFfRowBytes;
                         st.next(ST);
-                        if (++pending == 4) announce();
                     }
                 }
                 __syncwarp();
@@ -502,7 +498,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 iq.next(kRowInfos);
                 if (all < 0) break;
             }
-            while (pending > 0) announce();
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
         }
     } else {
@@ -514,7 +510,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         // Addresses are offsets from `at`, ring positions come from counts.
         const int q = warp & 3, half = (warp - 8) >> 2;
         const uint32_t at = smem_u32(misc);
-        constexpr uint32_t kAccFull = 16 * kFfMaxStages, kAccEmpty = kAccFull + 8 * kRowAccs, kInfoFull = kAccEmpty + 8 * kRowAccs,
+        constexpr uint32_t kAccFull = 24 * kFfMaxStages, kAccEmpty = kAccFull + 8 * kRowAccs, kInfoFull = kAccEmpty + 8 * kRowAccs,
                            kInfoEmpty = kInfoFull + 8 * kRowInfos, kScaleFull = kInfoEmpty + 8 * kRowInfos,
                            kScaleEmpty = kScaleFull + 8 * kRowScales, kAbort = kScaleEmpty + 8 * kRowScales + 12,
                            kInfo = kRowBarBytes, kScales = kInfo + kRowInfos * (uint32_t)sizeof(Info),
@@ -677,7 +673,6 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
     constexpr uint32_t kSmemMax = 232448;
     p.stages = (int)((kSmemMax - 1024 - kRowMiscBytes) / kRowStageBytes);
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
-    if (p.stages < 5) return cudaErrorNotSupported;  // (more than the loaders have under way; never with these sizes)
     const size_t smem = 1024 + (size_t)p.stages * kRowStageBytes + kRowMiscBytes;
     CUtensorMap mw;
     if (!encode_weight(&mw, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint64_t)a.K, (cuuint64_t)a.K, kFfRowBytes, kFfRows / 2))
