@@ -170,11 +170,11 @@ struct ScoreLaunch {
     int32_t *ids;            // [M][k + S]
     float *wts;
     uint16_t *logits_out;    // optional [M][E] copy of bf16 logits
-    int nk, log_groups, group_size;  // set by the launcher
+    int log_groups, group_size;  // set by the launcher
 };
 // Experts that a lane holds (score_places), at most.
 constexpr int kScoreMaxPlaces = 32;
-int score_places(int E, int groups, int *log_groups = nullptr);
+int score_places(int E, int groups);
 cudaError_t launch_select_experts(const ScoreLaunch &a, cudaStream_t stream);
 // A 2-D bf16 tensor map with the 128-byte swizzle (rows of row_bytes; boxes
 // of box_inner x box_outer elements); false if it cannot be encoded.
