@@ -13,7 +13,17 @@
 // from shared memory by all threads, and these reads bound the kernel (16384
 // tokens, gated product: 787 us). So here the routed rows are the MMA's rows: a
 // thread of the epilogue holds one row, its scale is one register, and a weight
-// tile's is the same for all.
+// tile's is the same for all (470 us, 1.75 PFLOP/s).
+//
+// What bounds that: the epilogue takes 1080 cycles a k-block of 256 x 256 (the
+// tensor core 512), the adds 290 of them (one an element, scheduler and cycle),
+// the loads from TMEM, the waits and the signals the rest, and 3600 an item for
+// its outputs (16 k-blocks with H = 2048). Measured and not better: sixteen
+// warps in the epilogue (491 us; the others are then short of registers),
+// packed adds of two (a pair takes two cycles), one warp issuing both tiles'
+// MMAs (531 us: three waits, the issue and two commits take a warp 1300 cycles),
+// a warp for every accumulator (536 us), copies that a warp waits for and makes
+// visible before it announces them (531 us).
 #include "smr_ffn.cuh"
 #include "smr_fp8.cuh"
 
@@ -22,7 +32,7 @@ namespace smr {
 // A piece of work: up to 256 routed rows (blocks of one expert together) and two
 // weight tiles for a CTA pair; either CTA holds half of the rows and half of
 // each tile. 16 warps: 0 and 1 issue the MMAs of either tile, 2 scout, 3
-// scales, 4 to 7 load the routed rows (32 each; 4 the weights too), the last 8
+// scales, 4 to 7 load the routed rows and the weights (two warps every other stage), the last 8
 // are the epilogue, two for each quarter of TMEM's lanes, one of these for
 // either tile.
 constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4, kRowScales = 4;
@@ -35,6 +45,9 @@ constexpr int kRowBarBytes = (kRowBars * 8 + 8 + 15) / 16 * 16;
 constexpr int kRowOutBytes = 8 * 32 * 128;
 constexpr int kRowMiscBytes = kRowBarBytes + kRowInfos * (int)sizeof(FfInfo<256>) + kRowScales * kRowScaleBytes +
                               kRowOutBytes + 2 * 128 * 4;
+
+// What a weight's load into shared memory takes, with room to spare (0.5 ms).
+constexpr long long kRowDrainCycles = 1ll << 20;
 
 enum RowOut : int { kRowBf16 = 0, kRowF32 = 1, kRowE4m3 = 2 };
 
@@ -265,7 +278,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(smem_u32(&full[s]), 2);
-            mbar_init(smem_u32(&rows_full[s]), 32 * kRowLoaders);
+            mbar_init(smem_u32(&rows_full[s]), 16 * kRowLoaders);
             mbar_init(smem_u32(&empty[s]), 2);  // either tile's MMAs
         }
         for (int s = 0; s < kRowAccs; ++s) {
@@ -298,7 +311,6 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     griddep_launch_dependents();
 
     const uint32_t ring = smem_u32(smem);  // a stage: [rows][64 rows of the first tile][64 of the second]
-    int issued = 0;  // stages whose weights were requested (warp 4)
     // A thread of the epilogue holds 128 sums: its 8 warps get registers of the
     // other 8 (256 x 64 + 256 x 192 = the 512 x 128 of the launch, which the
     // launcher makes sure of).
@@ -435,40 +447,36 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             __syncwarp();
         } else {
             // -------------------------------------------- routed rows ----
-            // A warp copies 32 of the CTA's rows for every stage: eight lanes
-            // a row, a lane the same chunk of eight rows, whose addresses it
-            // keeps for the whole item. Chunk c of row r lands at r * 128 +
-            // ((c ^ (r & 7)) << 4), the 128-byte swizzle. The copies announce
-            // themselves when they land (a warp that waited for them and made
-            // them visible to the tensor core would take 900 cycles a stage);
-            // who waits for them does the rest. The first of the warps
-            // requests a stage's weights too.
-            const bool weights = warp == 4 && elect_one();
-            const int c = lane & 7, r0 = 32 * (warp - 4) + (lane >> 3);  // rows r0 + 4 i
+            // Two warps copy the CTA's rows of a stage, 64 each, the other two
+            // those of the next: eight lanes a row, a lane the same chunk of
+            // sixteen rows, whose numbers it keeps for the whole item. Chunk c
+            // of row r lands at r * 128 + ((c ^ (r & 7)) << 4), the 128-byte
+            // swizzle. The copies announce themselves when they land (a warp
+            // that waited for them and made them visible to the tensor core
+            // would take 900 cycles a stage); who waits for them does the
+            // rest. The two request the stage's weights in turn.
+            const int c = lane & 7, r0 = 64 * (warp & 1) + (lane >> 3);  // rows r0 + 4 i
             const uint32_t to0 = ring + (uint32_t)(r0 * kFfRowBytes + ((c ^ (lane >> 3)) << 4));
             const uint32_t to1 = ring + (uint32_t)(r0 * kFfRowBytes + ((c ^ (4 + (lane >> 3))) << 4));
+            const bool elected = elect_one();
             RingPos st, iq;
-            bool ok = true;
+            int next = (warp - 4) >> 1;  // the next stage of these two, counted from the item's first
+            st.skip(next, ST);
+            bool weights = (warp & 1) == 0, ok = true;
             while (ok) {
                 if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
                 const Info *inf = info + iq.i;
                 const int all = inf->n;
                 if (all >= 0) {
                     const int n = all / 2;  // this CTA's rows of the item
-                    const uint8_t *from[8];
-                    uint32_t copy = 0u;  // a bit a row that there is
+                    int row[16];  // -1: none
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = r0 + 4 * i < n ? inf->row[(int)rank * n + r0 + 4 * i] : -1;
-                        if (row >= 0) copy |= 1u << i;
-                        from[i] = p.x + (uint64_t)(uint32_t)max(row, 0) * p.x_row_bytes + c * 16;
-                    }
+                    for (int i = 0; i < 16; ++i) row[i] = r0 + 4 * i < n ? inf->row[(int)rank * n + r0 + 4 * i] : -1;
                     const int nt = inf->nt & ~1, e = inf->e;
-                    int left = p.x_bytes - c * 16;  // (pieces past the row's end are not read by the last MMA steps)
-                    for (int kb = 0; kb < p.num_kb; ++kb) {
+                    for (; next < p.num_kb; next += 2) {
                         if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
                         const uint32_t base = (uint32_t)(st.i * kRowStageBytes);
-                        if (weights) {
+                        if (weights && elected) {
                             const uint32_t bar = smem_u32(&full[st.i]), fb = cluster_addr(bar, 0u);
                             // both CTAs' bytes complete the leader's barrier
                             if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
@@ -476,22 +484,23 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const uint32_t to = ring + base + (uint32_t)(kFfWBytes + h * (kFfWBytes / 2));
-                                if constexpr (UP) tma_load_5d_pair(to, &tm_w, kb * kFfRowBytes, 4 * (nt + h) + 2 * (int)rank, e, fb);
-                                else tma_load_3d_pair(to, &tm_w, kb * kFfRowBytes, kFfRows * (nt + h) + 64 * (int)rank, e, fb);
+                                if constexpr (UP) tma_load_5d_pair(to, &tm_w, next * kFfRowBytes, 4 * (nt + h) + 2 * (int)rank, e, fb);
+                                else tma_load_3d_pair(to, &tm_w, next * kFfRowBytes, kFfRows * (nt + h) + 64 * (int)rank, e, fb);
                             }
                         }
+                        weights = !weights;
                         __syncwarp();
-                        ++issued;
+                        const int off = next * kFfRowBytes + c * 16;
+                        const uint8_t *x = p.x + off;
+                        const bool some = off < p.x_bytes;  // (pieces past the row's end are not read by the last MMA steps)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            cp_async_16((i & 1 ? to1 : to0) + base + (uint32_t)(i * 4 * kFfRowBytes), from[i],
-                                        left > 0 && (copy >> i & 1u) ? 0 : -1);
-                            from[i] += kFfRowBytes;
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            cp_async_16((i & 1 ? to1 : to0) + base + (uint32_t)(i * 4 * kFfRowBytes),
+                                        x + (uint64_t)(uint32_t)row[i] * p.x_row_bytes, some ? row[i] : -1);
                         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&rows_full[st.i])) : "memory");
-                        left -= kFfRowBytes;
-                        st.next(ST);
+                        st.skip(2, ST);
                     }
+                    if (ok) next -= p.num_kb;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&info_empty[iq.i]));
@@ -635,15 +644,12 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
 
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag && warp == 4 && lane == 0) {
-        // a wait gave up: the piece's outputs are not written; weights still in
-        // flight land before the CTA leaves
-        ffn_error(p, kErrWaitTimeout);
-        if (rank == 0)
-            for (int j = issued - ST > 0 ? issued - ST : 0; j < issued; ++j) {
-                volatile int drain = 0;
-                mbar_wait_bounded(smem_u32(&full[j % ST]), (uint32_t)(j / ST) & 1u, &drain);
-            }
+    if (*abort_flag) {
+        // A wait gave up: the piece's outputs are not written. Weights still in
+        // flight land before the CTA leaves: after this long they have.
+        if (warp == 0 && lane == 0) ffn_error(p, kErrWaitTimeout);
+        const long long t0 = clock64();
+        while (clock64() - t0 < kRowDrainCycles) {}
     }
     // no barrier of either CTA can still be signalled, both are done with TMEM
     __syncwarp();
@@ -711,7 +717,17 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, expert_rows_kernel<UP, OUT>, mw, p);
 }
 
-constexpr int kRowsPerExpert = 128;
+// From this many rows an expert, on average, the routed rows are the MMA's rows:
+// an item then costs the same for 16 rows as for 256, but its scales are one
+// register. The gated product in us on the device, evenly spread and skewed
+// (128 experts, tokens of 8 slots; weights as rows, in pairs / routed rows):
+// 1024 tokens (64 rows) 101 and 112 / 119 and 119, 1536 tokens (96 rows) 117 and
+// 133 / 119 and 129, 2048 tokens 159 and 159 / 120 and 139, 4096 tokens 266 and
+// 256 / 166 and 179; the second product 69 and 76 / 77 and 83, 81 and 91 / 82
+// and 91, 107 and 109 / 86 and 99, 181 and 180 / 133 and 139. (Pairs against
+// single CTAs at 768 tokens, 48 rows: 91 and 101 / 92 and 111, second product
+// 62 and 68 / 60 and 72.)
+constexpr int kRowsPerExpert = 96;
 bool expert_rows_fp8(int64_t numel, int num_experts) { return numel >= (int64_t)kRowsPerExpert * num_experts; }
 
 template <bool UP, bool F32>

@@ -155,7 +155,11 @@ SHAPES = [
     (2500, 128, 96, 6, 1, 3, 64, 0.0),
     (4000, 416, 224, 5, 0, 2, 128, 0.0),  # pairs of CTAs: whole and partial tiles and k-blocks
     (3000, 288, 352, 4, 1, 1, 64, 1.1),   # pairs, an odd number of weight tiles, groups of blocks
+    (90, 640, 384, 3, 0, 2, 64, 0.0),     # pairs with the weights as rows: 48 to 96 rows an expert
+    (170, 416, 224, 5, 0, 2, 128, 0.0),
+    (230, 288, 352, 4, 1, 1, 64, 1.1),
     (2000, 1152, 768, 4, 0, 2, 128, 0.0),
+    (3000, 4224, 128, 2, 0, 1, 128, 0.0),  # 33 k-blocks
 ]
 
 
@@ -204,7 +208,7 @@ def test_down_matches_64_bits(smr, shape, fp32_rows):
     _close(out, *_ref_down(_row_values(xc, xs), _weight_values(wc, wsc, False), ids, wts))
 
 
-@pytest.mark.parametrize("shape", [s for s in SHAPES if s[2] % 32 == 0])
+@pytest.mark.parametrize("shape", SHAPES)
 def test_quantized_act_is_that_of_two_calls(smr, shape):
     T, H, I, E, S, k, A, zipf = shape
     ids, _, _, al, (xc, xs), (wc, wsc) = _up_case(smr, shape)
@@ -215,3 +219,295 @@ def test_quantized_act_is_that_of_two_calls(smr, shape):
     assert smr.get_device_error(ws) == 0
     c, s = smr.quantize_fp8(act)
     assert torch.equal(codes, c) and torch.equal(scales, s)
+
+
+# what runs for 50, 150 and 400 tokens of three slots over seven experts: single
+# CTAs, pairs with the weights as rows, pairs with the routed rows as rows
+REGIMES = [50, 150, 400]
+
+
+def _case(smr, T, H=256, I=160, E=6, S=1, k=2, seed=3):
+    ids, wts, g = _routing(T, E, k, S, 0.0, seed)
+    x, w13, w2 = _normal(g, T, H), _normal(g, E + S, 2 * I, H, std=1.5 * H ** -0.5), _normal(g, E + S, H, I, std=I ** -0.5)
+    xc, xs = smr.quantize_fp8(x)
+    w13, ws13 = smr.quantize_fp8_weight(w13, gated=True)
+    w2, ws2 = smr.quantize_fp8_weight(w2)
+    return ids, wts, smr.align(ids, E + S, 64), (xc, xs), (w13, ws13), (w2, ws2)
+
+
+def _ffn(smr, c, **kw):
+    ids, wts, al, (x, xs), (w13, ws13), (w2, ws2) = c
+    act, scales = smr.expert_up(x, w13, *al, width=ids.shape[1], block_size=64, x_scales=xs, w_scales=ws13, quantize_act=True, **kw)
+    return act, scales, smr.expert_down(act, w2, ids, wts, *al, block_size=64, x_scales=scales, w_scales=ws2, **kw)
+
+
+def _equal(a, b):
+    return all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("T", REGIMES)
+def test_layer_matches_64_bits(smr, T):
+    """Route with codes written by its launch, both products, from hidden states on."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x, gate, shared = _normal(g, T, 256), _normal(g, 6, 256, std=0.1), _normal(g, 1, 256, std=0.1)
+    codes, scales = torch.empty(T, 256, dtype=torch.uint8, device="cuda"), torch.empty(T, 2, device="cuda")
+    ids, wts, *al = smr.route_align(x, gate, shared, topk=2, block_size=64, hidden_fp8=codes, hidden_scales=scales,
+                                    scoring="sigmoid", balance_bias=torch.linspace(-0.1, 0.1, 6, device="cuda"), routed_scale=2.5)
+    _, _, _, _, w13, w2 = _case(smr, T)
+    c = (ids, wts, al, (codes, scales), w13, w2)
+    act, act_scales, out = _ffn(smr, c)
+    ref, tol = _ref_up(_row_values(codes, scales), _weight_values(*w13, True), ids, 3)
+    got = _row_values(act, act_scales)
+    # a code is off by half a step of 2^-3, and by half the smallest step, 2^-10 of the scale
+    tol = tol * 1.07 + got.abs() * 2.0 ** -4 + act_scales.double().repeat_interleave(BLOCK, -1)[:, : got.shape[1]] * 2.0 ** -10
+    assert ((got - ref).abs() <= tol).all()
+    _close(out, *_ref_down(got, _weight_values(*w2, False), ids, wts))
+
+
+@pytest.mark.parametrize("T", REGIMES)
+def test_skipped_slots(smr, T):
+    """Ids that no expert has: their rows of act, codes and scales stay as they were and they add nothing."""
+    ids, wts, _, (x, xs), (w13, ws13), (w2, ws2) = _case(smr, T)
+    ids = ids.clone()
+    ids[3, 1], ids[7, 0], ids[20] = -1, 100, 7
+    ws = smr.Workspace(256)
+    al = smr.align(ids, 7, 64, workspace=ws)
+    assert smr.get_device_error(ws) == 1
+    gone = ((ids < 0) | (ids >= 7)).reshape(-1)
+    kw = dict(width=3, block_size=64, x_scales=xs, w_scales=ws13)
+    out = torch.full((3 * T, 160), 5.0, dtype=torch.bfloat16, device="cuda")
+    smr.expert_up(x, w13, *al, out=out, **kw)
+    assert (out[gone] == 5.0).all() and gone.sum() == 5
+    ref, tol = _ref_up(_row_values(x, xs), _weight_values(w13, ws13, True), ids, 3)
+    _close(out[~gone], ref[~gone], tol[~gone])
+    codes = torch.full((3 * T, 160), 0x7F, dtype=torch.uint8, device="cuda")  # NaN
+    scales = torch.full((3 * T, 2), 7.0, device="cuda")
+    smr.expert_up(x, w13, *al, out=codes, act_scales=scales, quantize_act=True, **kw)
+    assert (codes[gone] == 0x7F).all() and (scales[gone] == 7.0).all()
+    c, s = smr.quantize_fp8(out)
+    assert torch.equal(codes[~gone], c[~gone]) and torch.equal(scales[~gone], s[~gone])
+    y = smr.expert_down(codes, w2, ids, wts, *al, block_size=64, x_scales=scales, w_scales=ws2)
+    values = torch.where(gone[:, None], torch.zeros(1, dtype=torch.float64, device="cuda"), _row_values(codes, scales))
+    _close(y, *_ref_down(values, _weight_values(w2, ws2, False), ids, wts))
+    assert (y[20] == 0).all()
+
+
+@pytest.mark.parametrize("T", REGIMES)
+def test_no_slot_at_all(smr, T):
+    ids, wts, _, (x, xs), (w13, ws13), (w2, ws2) = _case(smr, T)
+    ids = torch.full_like(ids, -1)
+    al = smr.align(ids, 7, 64, workspace=smr.Workspace(256))
+    assert int(al[2]) == 0
+    codes = torch.full((3 * T, 160), 9, dtype=torch.uint8, device="cuda")
+    scales = torch.full((3 * T, 2), 2.0, device="cuda")
+    smr.expert_up(x, w13, *al, width=3, block_size=64, x_scales=xs, w_scales=ws13, quantize_act=True, out=codes, act_scales=scales)
+    assert (codes == 9).all() and (scales == 2.0).all()
+    assert (smr.expert_down(codes, w2, ids, wts, *al, block_size=64, x_scales=scales, w_scales=ws2) == 0).all()
+
+
+@pytest.mark.parametrize("T", REGIMES)
+def test_bad_values_stay_in_their_rows(smr, T):
+    """A row of NaN codes, a NaN and an infinite scale: only their own tokens."""
+    c = _case(smr, T)
+    good = _ffn(smr, c)
+    ids, wts, al, (x, xs), w13, w2 = c
+    x, xs = x.clone(), xs.clone()
+    x[4] = 0x7F
+    xs[11, 1] = float("nan")
+    xs[30, 0] = float("inf")
+    got = _ffn(smr, (ids, wts, al, (x, xs), w13, w2))
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[[4, 11, 30]] = True
+    rows = bad.repeat_interleave(3)
+    assert torch.equal(got[0][~rows], good[0][~rows]) and torch.equal(got[1][~rows], good[1][~rows])
+    assert torch.equal(got[2][~bad], good[2][~bad])
+    assert got[2][bad].isnan().all() and got[1][rows].isnan().any(1).all()
+
+
+@pytest.mark.parametrize("T", REGIMES)
+def test_same_bits_twice_and_tail_ignored(smr, T):
+    c = _case(smr, T)
+    ref = _ffn(smr, c)
+    assert _equal(_ffn(smr, c), ref)
+    ids, wts, al, x, w13, w2 = c
+    n = int(al[2])
+    srt, eids = al[0].clone(), al[1].clone()
+    srt[n:], eids[n // 64:] = 0, 0
+    assert _equal(_ffn(smr, (ids, wts, (srt, eids, al[2]), x, w13, w2)), ref)
+
+
+@pytest.mark.parametrize("T", REGIMES)
+def test_corrupted_align_outputs(smr, T):
+    ids, wts, al, (x, xs), (w13, ws13), _ = _case(smr, T)
+    kw = dict(width=3, block_size=64, x_scales=xs, w_scales=ws13)
+    good = smr.expert_up(x, w13, *al, **kw)
+    for quantize in (False, True):
+        srt, eids = al[0].clone(), al[1].clone()
+        bad_slot = int(srt[1])
+        srt[1], srt[2] = 1 << 29, -5
+        ws = smr.Workspace(256)
+        got = smr.expert_up(x, w13, srt, eids, al[2], workspace=ws, quantize_act=quantize, **kw)
+        assert smr.get_device_error(ws) == 4
+        eids[0] = 7
+        smr.expert_up(x, w13, al[0], eids, al[2], workspace=ws, quantize_act=quantize, **kw)
+        assert smr.get_device_error(ws) == 5
+        if not quantize:
+            keep = torch.ones(3 * T, dtype=torch.bool, device="cuda")
+            keep[[bad_slot, int(al[0][2])]] = False
+            assert torch.equal(got[keep], good[keep])
+        for n in (1 << 30, -64):
+            srt, eids = al[0].clone(), al[1].clone()
+            srt[int(al[2]):], eids[int(al[2]) // 64:] = 3 * T, 0
+            out = torch.zeros(3 * T, 160, dtype=torch.uint8 if quantize else torch.bfloat16, device="cuda")
+            ws = smr.Workspace(256)
+            got = smr.expert_up(x, w13, srt, eids, torch.full_like(al[2], n), out=out, workspace=ws, quantize_act=quantize, **kw)
+            assert smr.get_device_error(ws) == 0
+            ref = good if not quantize else smr.quantize_fp8(good)[0]
+            assert torch.equal(out, ref if n > 0 else torch.zeros_like(out))
+
+
+@pytest.mark.parametrize("T", [50, 400])
+def test_captured_and_replayed(smr, T):
+    """Graphs without workspaces of their own on two streams at once, with new inputs, next to eager calls."""
+    cases = [_case(smr, T, seed=s) for s in (5, 6)]
+    eager = [_ffn(smr, c) for c in cases]
+    graphs, outs = [], []
+    for c in cases:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(_ffn(smr, c))
+        graphs.append(gr)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for gr, s in zip(graphs, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                gr.replay()
+        assert _equal(_ffn(smr, cases[0]), eager[0])
+        for s in streams:
+            torch.cuda.current_stream().wait_stream(s)
+    assert all(_equal(a, b) for a, b in zip(outs, eager))
+    cases[0][3][0].bitwise_xor_(0x80)  # the first graph's hidden states, negated
+    graphs[0].replay()
+    ref = _ffn(smr, cases[0])
+    torch.cuda.synchronize()
+    assert _equal(outs[0], ref) and not torch.equal(ref[0], eager[0][0])
+
+
+def test_other_streams(smr):
+    for T in REGIMES:
+        c = _case(smr, T)
+        ref = _ffn(smr, c)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        assert _equal(_ffn(smr, c, stream=s), ref)
+        q = smr.quantize_fp8(torch.ones(5, 96, dtype=torch.bfloat16, device="cuda"), stream=s)
+        v = smr.dequantize_fp8(*q, stream=s.cuda_stream)
+        ids, w = smr.select_experts(torch.arange(40.0, device="cuda").view(1, 40), topk=3, stream=s)
+        s.synchronize()
+        assert (v == 1).all() and ids.tolist() == [[39, 38, 37]]
+
+
+@pytest.mark.parametrize("K", [128, 256, 512, 288])
+@pytest.mark.parametrize("shift", [0, 1, 2])
+@pytest.mark.parametrize("T", [20, 150, 400])
+def test_scale_rows_of_any_alignment(smr, K, shift, T):
+    """Rows of scales that can be read 16, 8 or only 4 bytes at a time."""
+    ids, _, al, (x, xs), (w13, ws13), _ = _case(smr, T, H=K)
+    kw = dict(width=3, block_size=64)
+    ref = smr.expert_up(x, w13, *al, x_scales=xs, w_scales=ws13, **kw)
+    moved = []
+    for t in (xs, ws13):
+        buf = torch.full((t.numel() + shift,), float("nan"), device="cuda")
+        moved.append(buf[shift:].view_as(t))
+        moved[-1].copy_(t)
+    assert torch.equal(smr.expert_up(x, w13, *al, x_scales=moved[0], w_scales=moved[1], **kw), ref)
+    _close(ref, *_ref_up(_row_values(x, xs), _weight_values(w13, ws13, True), ids, 3))
+
+
+@pytest.mark.parametrize("E", [1, 1025])
+def test_offsets_past_32_bits(smr, E):
+    """Codes, outputs and rows of more than 2^31 elements with the routed rows as the MMA's
+    rows (one expert), of more than 2^31 bytes with them as its columns (95 rows an expert)."""
+    T, I, H, A = 140000 if E == 1 else 98000, 16384, 32, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.tensor([0, 1, 65535, 65536, T - 2, T - 1], device="cuda")
+    real = min(E, 4)  # experts with weights
+    if E == 1:
+        ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    else:
+        ids = torch.full((T, 1), -1, dtype=torch.int32, device="cuda")
+        ids[rows, 0] = torch.tensor([0, 3, 3, 2, 0, 3], dtype=torch.int32, device="cuda")
+    wts = torch.rand(T, 1, device="cuda", generator=g)
+    al = smr.align(ids, E, A, workspace=smr.Workspace(256))
+    x, xs = smr.quantize_fp8(_normal(g, T, H))
+    small13, smalls13 = smr.quantize_fp8_weight(_normal(g, real, 2 * I, H, std=0.5), gated=True)
+    small2, smalls2 = smr.quantize_fp8_weight(_normal(g, real, H, I, std=I ** -0.5))
+
+    def padded(t):
+        full = torch.zeros((E, *t.shape[1:]), dtype=t.dtype, device="cuda")
+        full[:real] = t
+        return full
+
+    w13, ws13, w2, ws2 = map(padded, (small13, smalls13, small2, smalls2))
+    kw = dict(width=1, block_size=A, x_scales=xs, w_scales=ws13)
+    act = smr.expert_up(x, w13, *al, **kw)[rows]
+    _close(act, *_ref_up(_row_values(x[rows], xs[rows]), _weight_values(small13, smalls13, True), ids[rows], 1))
+    codes, scales = smr.expert_up(x, w13, *al, quantize_act=True, **kw)
+    c, s = smr.quantize_fp8(act)
+    assert torch.equal(codes[rows], c) and torch.equal(scales[rows], s)
+    out = smr.expert_down(codes, w2, ids, wts, *al, block_size=A, x_scales=scales, w_scales=ws2)
+    _close(out[rows], *_ref_down(_row_values(c, s), _weight_values(small2, smalls2, False), ids[rows], wts[rows]))
+
+
+def test_empty_batch(smr):
+    al = smr.align(torch.zeros(0, 2, dtype=torch.int32, device="cuda"), 4, 64)
+    w13, ws13 = smr.quantize_fp8_weight(torch.zeros(4, 64, 64, dtype=torch.bfloat16, device="cuda"), gated=True)
+    x, xs = smr.quantize_fp8(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"))
+    assert x.shape == (0, 64) and xs.shape == (0, 1) and smr.dequantize_fp8(x, xs).shape == (0, 64)
+    act, scales = smr.expert_up(x, w13, *al, width=2, block_size=64, x_scales=xs, w_scales=ws13, quantize_act=True)
+    assert act.shape == (0, 32) and scales.shape == (0, 1) and smr.last_launch_count() == 0
+    w2, ws2 = smr.quantize_fp8_weight(torch.zeros(4, 64, 32, dtype=torch.bfloat16, device="cuda"))
+    out = smr.expert_down(act, w2, torch.zeros(0, 2, dtype=torch.int32, device="cuda"), torch.zeros(0, 2, device="cuda"),
+                          *al, block_size=64, x_scales=scales, w_scales=ws2)
+    assert out.shape == (0, 64) and smr.last_launch_count() == 0
+
+
+def test_launches_and_given_outputs(smr):
+    for T in REGIMES:
+        c = _case(smr, T)
+        ids, wts, al, (x, xs), (w13, ws13), (w2, ws2) = c
+        ref = _ffn(smr, c)
+        codes, scales = torch.empty_like(ref[0]), torch.empty_like(ref[1])
+        got = smr.expert_up(x.view(torch.float8_e4m3fn), w13.view(torch.float8_e4m3fn), *al, width=3, block_size=64,
+                            x_scales=xs, w_scales=ws13, quantize_act=True, out=codes, act_scales=scales)
+        assert got[0] is codes and got[1] is scales and smr.last_launch_count() == (1 if T == 400 else 2)
+        assert torch.equal(codes, ref[0]) and torch.equal(scales, ref[1])
+    with pytest.raises(ValueError, match="one device"):
+        smr.expert_up(x, w13, *al, width=3, block_size=64, x_scales=xs, w_scales=ws13.cpu())
+    with pytest.raises(smr.SmrUnsupported, match="64 or 128"):
+        smr.expert_up(x, w13, *al, width=3, block_size=256, x_scales=xs, w_scales=ws13)
+    with pytest.raises(smr.SmrError, match="16-byte aligned"):
+        buf = torch.zeros(x.numel() + 8, dtype=torch.uint8, device="cuda")
+        smr.expert_up(buf[8:].view_as(x), w13, *al, width=3, block_size=64, x_scales=xs, w_scales=ws13)
+
+
+def test_one_workspace_for_every_call(smr):
+    """Scored routes, both products in all forms and bf16 ones in turn on one workspace."""
+    ws = smr.Workspace()
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ref = {T: _ffn(smr, _case(smr, T)) for T in REGIMES}
+    routes = {}
+    for M in (3, 16, 40, 600):
+        x, gate = _normal(g, M, 256), _normal(g, 64, 256, std=0.1)
+        routes[M] = (x, gate, smr.route(x, gate, topk=6, scoring="sigmoid", num_groups=8, topk_groups=3),
+                     smr.route_align(x, gate, topk=6, block_size=64))
+    for _ in range(3):
+        for T in REGIMES:
+            assert _equal(_ffn(smr, _case(smr, T), workspace=ws), ref[T])
+            for M, (x, gate, scored, plain) in routes.items():
+                got = smr.route(x, gate, topk=6, scoring="sigmoid", num_groups=8, topk_groups=3, workspace=ws)
+                assert _equal(got, scored)
+                got = smr.route_align(x, gate, topk=6, block_size=64, workspace=ws)
+                assert _equal(got[:2], plain[:2]) and torch.equal(got[4], plain[4])
+    assert smr.get_device_error(ws) == 0
