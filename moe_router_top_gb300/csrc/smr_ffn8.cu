@@ -534,13 +534,11 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             float sum[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
-            // (after a wait that gave up the loop runs on, over whatever TMEM
-            // and the ring hold: leaving it would cost copies of the sums)
-#pragma unroll 1
-            for (int kb = more ? 0 : p.num_kb; kb < p.num_kb; ++kb) {
-                if ((kb & (kFp8Group - 1)) == 0)
-                    ok &= warp_wait_at(at + kScaleFull + 8 * (groups & (kRowScales - 1)), groups / kRowScales & 1u, at + kAbort);
-                float g, u;
+            // The scales of a k-block are read while the one before is added.
+            // (After a wait that gave up the loop runs on, over whatever TMEM
+            // and the ring hold: leaving it would cost copies of the sums.)
+            float g = 0.0f, u = 0.0f;
+            const auto read_scales = [&](int kb) {
                 const uint32_t from_s = scales + (groups & (kRowScales - 1)) * kRowScaleBytes + (kb & (kFp8Group - 1)) * 1024u;
                 if constexpr (UP) {
                     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(g), "=f"(u) : "r"(from_s) : "memory");
@@ -548,19 +546,31 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(g) : "r"(from_s) : "memory");
                     u = g;
                 }
+            };
+            if (more) {
+                ok &= warp_wait_at(at + kScaleFull + 8 * (groups & (kRowScales - 1)), groups / kRowScales & 1u, at + kAbort);
+                read_scales(0);
+            }
+#pragma unroll 1
+            for (int kb = more ? 0 : p.num_kb; kb < p.num_kb;) {
                 ok &= warp_wait_at(at + kAccFull + 8u * half + 16u * (units & 1u), units >> 1 & 1u, at + kAbort);
                 tc_fence_after();
                 float last[32];
-                add_columns(sum, last, from + 256u * (units & 1u), g, u);
+                const float g0 = g, u0 = u;
+                add_columns(sum, last, from + 256u * (units & 1u), g0, u0);
                 tc_fence_before();
                 arrive_cluster_if(hand_back + 16u * (units & 1u), lane == 0);
                 ++units;
-                if ((kb & (kFp8Group - 1)) == kFp8Group - 1 || kb + 1 == p.num_kb) {
+                ++kb;
+                if ((kb & (kFp8Group - 1)) == 0 || kb == p.num_kb) {
                     arrive_if(at + kScaleEmpty + 8 * (groups & (kRowScales - 1)), lane == 0);
                     ++groups;
+                    if (kb < p.num_kb)
+                        ok &= warp_wait_at(at + kScaleFull + 8 * (groups & (kRowScales - 1)), groups / kRowScales & 1u, at + kAbort);
                 }
+                read_scales(kb);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) sum[96 + j] = fmaf(last[j], j < 16 ? g : u, sum[96 + j]);
+                for (int j = 0; j < 32; ++j) sum[96 + j] = fmaf(last[j], j < 16 ? g0 : u0, sum[96 + j]);
             }
             if constexpr (OUT == kRowE4m3) ok = meet_two_if(1 + q, ok);  // both warps of a row go on, or none does
             if (!ok || !more) break;
