@@ -348,10 +348,12 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 }
                 for (int kb = 0; kb < p.num_kb; ++kb) {
                     uint64_t *done = &acc_full[2 * ac.i + warp];
-                    if (!(ok = warp_wait(&acc_empty[2 * ac.i + warp], ac.ph ^ 1u, abort_flag))) break;
+                    // (the accumulator last: it is what is waited for longest,
+                    // and each wait takes 150 cycles)
                     if (!(ok = warp_wait(&rows_full[st.i], st.ph, abort_flag))) break;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
+                    if (!(ok = warp_wait(&acc_empty[2 * ac.i + warp], ac.ph ^ 1u, abort_flag))) break;
                     tc_fence_after();
                     const uint32_t base = ring + (uint32_t)(st.i * kRowStageBytes), acc = tmem + (uint32_t)((2 * ac.i + warp) * 128);
                     const uint64_t da = smem_desc_sw<128>(base), db = smem_desc_sw<128>(base + kFfWBytes + warp * (kFfWBytes / 2));
