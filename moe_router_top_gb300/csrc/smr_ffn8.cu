@@ -13,17 +13,19 @@
 // from shared memory by all threads, and these reads bound the kernel (16384
 // tokens, gated product: 787 us). So here the routed rows are the MMA's rows: a
 // thread of the epilogue holds one row, its scale is one register, and a weight
-// tile's is the same for all (470 us, 1.75 PFLOP/s).
+// tile's is the same for all (467 us, 1.77 PFLOP/s).
 //
-// What bounds that: the epilogue takes 1080 cycles a k-block of 256 x 256 (the
-// tensor core 512), the adds 290 of them (one an element, scheduler and cycle),
-// the loads from TMEM, the waits and the signals the rest, and 3600 an item for
-// its outputs (16 k-blocks with H = 2048). Measured and not better: sixteen
-// warps in the epilogue (491 us; the others are then short of registers),
-// packed adds of two (a pair takes two cycles), one warp issuing both tiles'
-// MMAs (531 us: three waits, the issue and two commits take a warp 1300 cycles),
-// a warp for every accumulator (536 us), copies that a warp waits for and makes
-// visible before it announces them (531 us).
+// What bounds that (us for the gated product of 16384 tokens, parts taken out in
+// turn): the chain from an accumulator's MMAs over the signals between the CTAs
+// to the epilogue and back takes 305 without the adds and the outputs, of which
+// the tensor core works 200; the adds, one an element, scheduler and cycle, 100;
+// the outputs 65; the row copies 18; the loads from TMEM nothing. Measured and
+// not better: one accumulator of 256 columns a k-block (493 us), sixteen warps
+// in the epilogue (491; the others are then short of registers), packed adds of
+// two (a pair takes two cycles), one warp issuing both tiles' MMAs (531), a warp
+// for every accumulator (536), copies that a warp waits for and makes visible
+// before it announces them (531), the stages handed back by the epilogue (463,
+// the second product 25 longer).
 #include "smr_ffn.cuh"
 #include "smr_fp8.cuh"
 
@@ -321,8 +323,8 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             // A warp for either tile: its k-blocks in turn into two
             // accumulators. (From an accumulator's last MMA to the next one's
             // first in it the signals between the CTAs take 1100 cycles
-            // without any work in between, a tile's MMAs 256; and issuing four
-            // MMAs takes a warp 300.)
+            // without any work in between, a tile's MMAs 256; and a k-block's
+            // waits, issue and commits take a warp 600.)
             const bool elected = elect_one();
             const uint32_t idesc = idesc_e4m3(2 * kFfRows, 128);
             RingPos st, iq, ac;

@@ -12,35 +12,38 @@ namespace smr {
 constexpr int kFp8Threads = 256;
 constexpr int kFp8Vecs = 4;  // 16-byte vectors (8 values) a thread has in flight
 
-// Bound by memory: 2 bytes read and 1 written per value. One 16-byte load per
-// 8 values, 16 neighbouring lanes share a block; kFp8Vecs independent loads a
-// thread cover the latency. A row's last block may be short (K / 8 vectors a
-// row, whole blocks of 16 counted).
+// Bound by memory: 2 bytes read and 1 written per value. A thread takes 16
+// values, 8 neighbouring lanes a block; kFp8Pieces independent pieces a thread
+// cover the latency. A row's last block may be short (K is a multiple of 32:
+// whole pieces).
+constexpr int kFp8Pieces = 2;
 __global__ void __launch_bounds__(kFp8Threads)
-quantize_fp8_kernel(const uint16_t *__restrict__ x, int64_t ld, uint32_t row_vecs, uint32_t row_blocks, uint32_t blocks,
+quantize_fp8_kernel(const uint16_t *__restrict__ x, int64_t ld, uint32_t row_pieces, uint32_t row_blocks, uint32_t blocks,
                     uint8_t *__restrict__ codes, float *__restrict__ scales) {
     griddep_wait();
     griddep_launch_dependents();
-    const uint32_t first = blockIdx.x * (kFp8Threads / 16 * kFp8Vecs) + threadIdx.x / 16, in = threadIdx.x & 15;
-    uint4 v[kFp8Vecs];
-    int64_t at[kFp8Vecs];  // the vector among the codes, -1: none
+    const uint32_t first = blockIdx.x * (kFp8Threads / 8 * kFp8Pieces) + threadIdx.x / 8, in = threadIdx.x & 7;
+    uint4 v[kFp8Pieces][2];
+    int64_t at[kFp8Pieces];  // the piece among the codes, -1: none
 #pragma unroll
-    for (int j = 0; j < kFp8Vecs; ++j) {
-        const uint32_t b = first + j * (kFp8Threads / 16);
-        const uint32_t row = b / row_blocks, vec = (b - row * row_blocks) * 16 + in;
-        at[j] = b < blocks && vec < row_vecs ? (int64_t)row * row_vecs + vec : -1;
-        v[j] = at[j] >= 0 ? ld_stream_rows_v4(x + (int64_t)row * ld + vec * 8) : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < kFp8Pieces; ++j) {
+        const uint32_t b = first + j * (kFp8Threads / 8);
+        const uint32_t row = b / row_blocks, piece = (b - row * row_blocks) * 8 + in;
+        at[j] = b < blocks && piece < row_pieces ? (int64_t)row * row_pieces + piece : -1;
+        const uint16_t *from = x + (int64_t)row * ld + piece * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[j][h] = at[j] >= 0 ? ld_stream_rows_v4(from + 8 * h) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int j = 0; j < kFp8Vecs; ++j) {
-        uint32_t m = abs_max8(v[j]);
+    for (int j = 0; j < kFp8Pieces; ++j) {
+        uint32_t m = max(abs_max8(v[j][0]), abs_max8(v[j][1]));
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         float scale, factor;
         block_scale_e4m3(m, scale, factor);
-        const uint2 c = codes8(v[j], factor);
-        if (at[j] >= 0) reinterpret_cast<uint2 *>(codes)[at[j]] = c;
-        const uint32_t b = first + j * (kFp8Threads / 16);
+        const uint2 lo = codes8(v[j][0], factor), hi = codes8(v[j][1], factor);
+        if (at[j] >= 0) reinterpret_cast<uint4 *>(codes)[at[j]] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        const uint32_t b = first + j * (kFp8Threads / 8);
         if (in == 0 && b < blocks) scales[b] = scale;
     }
 }
@@ -169,9 +172,9 @@ cudaError_t launch_quantize_fp8(const uint16_t *x, int64_t rows, int K, int64_t 
                                 cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     const uint32_t row_blocks = (uint32_t)(K + 127) / 128, blocks = (uint32_t)(rows * row_blocks);
-    const int64_t per = kFp8Threads / 16 * kFp8Vecs;
+    const int64_t per = kFp8Threads / 8 * kFp8Pieces;
     const cudaLaunchConfig_t cfg = fp8_config((blocks + per - 1) / per, stream, attr);
-    return cudaLaunchKernelEx(&cfg, quantize_fp8_kernel, x, ld, (uint32_t)(K / 8), row_blocks, blocks, codes, scales);
+    return cudaLaunchKernelEx(&cfg, quantize_fp8_kernel, x, ld, (uint32_t)(K / 16), row_blocks, blocks, codes, scales);
 }
 
 cudaError_t launch_quantize_fp8_slots(const QuantizeRows &a, cudaStream_t stream) {
