@@ -201,9 +201,9 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
     if (row >= p.M) return;  // warp-uniform
-    const int L = 32 >> p.log_groups, gs = p.group_size, group = lane / L;
+    const int shift = 5 - p.log_groups, L = 1 << shift, gs = p.group_size, group = lane >> shift;
     // place i is expert first + (i / V) * L * V + i % V, there while that is below `end`
-    const int first = group * gs + lane % L * V, end = group < p.groups ? (group + 1) * gs : 0;
+    const int first = group * gs + (lane & (L - 1)) * V, end = group < p.groups ? (group + 1) * gs : 0;
     // (requested now: at the end it would be waited for)
     float shared = 0.0f;
     if (p.shared != nullptr && lane == p.k) shared = __ldcg(p.shared + row);
@@ -237,6 +237,11 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
         for (int i = 0; i < NK; ++i)
             if (expert(i) < end) p.logits_out[row * p.E + expert(i)] = (uint16_t)(__float_as_uint(x[i]) >> 16);
     }
+    float c[NK];  // first the balance bias, requested along with the logits
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) c[i] = expert(i) < end ? __ldcg(p.bias + expert(i)) : 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < NK; ++i) x[i] = expert(i) < end ? to_finite(x[i]) : -INFINITY;
 
@@ -262,7 +267,6 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
     const float inv = __frcp_rn(den);
 
     // choices; without a bias the logits themselves, which have their order
-    float c[NK];
     // how far a choice in 32 bits may be off, twice: 4e-7 of a sigmoid, 2e-6
     // of a softmax (its sum of up to ten roundings), half a unit of c itself
     const float slack = p.bias == nullptr ? 0.0f : (soft ? 4e-6f : 8e-7f);
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             const float s = soft ? exp2_fast((x[i] - top) * kLog2e) * inv : sigmoid_fast(x[i]);
-            c[i] = expert(i) < end ? s + load_bias(p, expert(i)) : -INFINITY;
+            c[i] = expert(i) < end ? s + to_finite(c[i]) : -INFINITY;
         }
     } else {
 #pragma unroll
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
         for (int j = 0; j < p.kept; ++j) {
             low = __reduce_max_sync(0xffffffffu, left);
             const int lane0 = __ffs(__ballot_sync(0xffffffffu, left == low)) - 1;
-            if (lane / L == lane0 / L) {
+            if (group == lane0 >> shift) {
                 stays = true;
                 left = 0u;
             }
