@@ -78,7 +78,7 @@ __device__ __forceinline__ void arrive_cluster_if(uint32_t bar, bool yes) {
 }
 
 // As warp_wait, by shared-memory addresses: the epilogue has no registers for
-// 64-bit ones (what it spills comes back in 270 cycles, a third of a k-block).
+// 64-bit ones, and what it spills is read back at every k-block.
 __device__ __forceinline__ bool warp_wait_at(uint32_t bar, uint32_t parity, uint32_t abort_at) {
     bool ok = mbar_try_wait(bar, parity);
     if (!ok) {
@@ -135,7 +135,7 @@ __device__ __forceinline__ void put_row_lines(uint32_t buffer, const uint32_t (&
 
 // A row's 128 columns times g and u (16 and 16 in turn), added to d; the last
 // 32 are left in `last`, so that the accumulator can be handed back before they
-// are added. Bound by the loads' latency (77 cycles) and by the adds (one a
+// are added. Bound by the loads' latency and by the adds (one a
 // cycle for the two warps of a scheduler): while one load's values are added the
 // next is under way, 32 columns and 16 in turn, as many as there are registers
 // for. One statement, as the order in it is what counts.

@@ -38,7 +38,9 @@ __device__ __forceinline__ float load_logit(const ScoreLaunch &p, int64_t row, i
     if constexpr (F32) return to_finite(__ldcg(static_cast<const float *>(p.logits) + row * p.ld + e));
     else return to_finite(__uint_as_float((uint32_t)__ldcg(static_cast<const uint16_t *>(p.logits) + row * p.ld + e) << 16));
 }
-__device__ __forceinline__ float load_bias(const ScoreLaunch &p, int e) { return to_finite(__ldcg(p.bias + e)); }
+// (Through the L1 cache: every row reads all of it, and 2047 rows of 256 that
+// asked L2 for its eight lines took 18 us, 11 of them in that queue.)
+__device__ __forceinline__ float load_bias(const ScoreLaunch &p, int e) { return to_finite(p.bias[e]); }
 
 // A float's bits as an unsigned number of the same order (0 below them all).
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -189,8 +191,10 @@ __device__ __noinline__ void settle_in_64_bits(const ScoreLaunch &p, int64_t row
     __syncwarp();
 }
 
-// Bound by its instructions for large batches (about 900 a row) and by latency
-// for small ones; what it reads is the logits, once, in whole sectors.
+// Bound by its instructions for large batches (1170 a row of 512 experts in 8
+// groups as ncu counts them; 16384 rows take 25.3 us) and by latency for small
+// ones (4 rows of 512: 3.5 us); what it reads is the logits, once, in whole
+// sectors.
 template <int NK, int V, bool F32>
 __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const ScoreLaunch p) {
     __shared__ __align__(16) uint32_t cand_u[kScoreWarps][32];  // choices, as unsigned numbers
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
     float c[NK];  // first the balance bias, requested along with the logits
     if (p.bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < NK; ++i) c[i] = expert(i) < end ? __ldcg(p.bias + expert(i)) : 0.0f;
+        for (int i = 0; i < NK; ++i) c[i] = expert(i) < end ? load_bias(p, expert(i)) : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < NK; ++i) x[i] = expert(i) < end ? to_finite(x[i]) : -INFINITY;
@@ -274,7 +278,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             const float s = soft ? exp2_fast((x[i] - top) * kLog2e) * inv : sigmoid_fast(x[i]);
-            c[i] = expert(i) < end ? s + to_finite(c[i]) : -INFINITY;
+            c[i] = expert(i) < end ? s + c[i] : -INFINITY;
         }
     } else {
 #pragma unroll
@@ -345,8 +349,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
     // once) is a lower bound of the want-th largest choice, and few choices
     // reach it: these are ranked against each other. (Where there are fewer
     // maxima, or more than 32 choices reach it, the largest is taken `want`
-    // times. Maxima of whole lanes are too few where few groups stay: 16384 rows
-    // of 512 experts, 3 groups of 8, 35 us instead of WWWW.)
+    // times. Maxima of whole lanes would be too few where few groups stay.)
     uint32_t *const found = cand_u[threadIdx.x >> 5];
     float *const found_x = cand_x[threadIdx.x >> 5];
     float2 *const found_at = cand_s[threadIdx.x >> 5][0], *const sorted = cand_s[threadIdx.x >> 5][1];
@@ -559,7 +562,8 @@ cudaError_t launch_select_experts(const ScoreLaunch &in, cudaStream_t stream) {
     const int single = (a.group_size + L - 1) / L;
     if (single > kScoreMaxPlaces) return cudaErrorNotSupported;
     // Four experts a load where groups and rows are made of whole aligned
-    // pieces of four (16384 x 512 in fp32: 14.2 us, one at a time 15.6).
+    // pieces of four (16384 x 512 in fp32: 25.3 us, one at a time 35.9; 2047 x
+    // 256 in bf16: 10.7 and 11.1).
     const int fours = (a.group_size + 4 * L - 1) / (4 * L) * 4, size = a.f32 ? 4 : 2;
     const bool wide = a.group_size % 4 == 0 && a.ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * size) == 0 &&
                       fours <= kScoreMaxPlaces;
