@@ -1,0 +1,334 @@
+"""Host-side checks of the scored routing and E4M3 entry points (no GPU needed):
+refusals with every reason before any device work, workspace sizes, the calls
+that launch nothing, and the Python layer's argument checks."""
+from __future__ import annotations
+
+import ctypes
+import os
+import re
+
+import pytest
+
+from moe_router_top_gb300 import _lib
+from moe_router_top_gb300._lib import (AlignArgs, ExpertDownFp8Args, ExpertUpFp8Args, RouteArgs, Scoring, SelectArgs)
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from moe_router_top_gb300 import build
+    build.build()
+    return _lib.load()
+
+
+@pytest.fixture(scope="module")
+def smr(lib):
+    import moe_router_top_gb300
+    return moe_router_top_gb300
+
+
+P = 0x10000
+INVALID, UNSUP, WORKSPACE = _lib.SMR_ERR_INVALID_ARG, _lib.SMR_ERR_UNSUPPORTED, _lib.SMR_ERR_WORKSPACE
+ROWS = 256 + 16 * 1024 * 8  # where the products' rows and a scored route's logits begin
+
+
+def _with(a, over):
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+def _up(**over):
+    return _with(ExpertUpFp8Args(4, 11, 256, 128, 65, 64, P, P, P, P, P, 44 + 65 * 63, P, P, P, None), over)
+
+
+def _down(**over):
+    return _with(ExpertDownFp8Args(4, 11, 256, 128, 65, 64, P, P, P, P, P, P, 65, 0, P, 44 + 65 * 63, P, P, P), over)
+
+
+def _scoring(**over):
+    return _with(Scoring(1, 8, 4, 2, 2.5, P), over)
+
+
+def _select(scoring=None, **over):
+    return _with(SelectArgs(P, 1, 4, 64, 64, 6, 1, 1, P, 1.0, scoring or _scoring(), P, P), over)
+
+
+def _refused(lib, status, want, *frags):
+    assert status == want
+    msg = lib.smr_last_error().decode()
+    for f in frags:
+        assert f in msg, msg
+    assert lib.smr_last_launch_count() == 0
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(Scoring) == 32 and Scoring.balance_bias.offset == 24
+    assert ctypes.sizeof(SelectArgs) == 8 + 8 + 8 + 16 + 8 + 8 + 32 + 16 and SelectArgs.scoring.offset == 56
+    assert ctypes.sizeof(ExpertUpFp8Args) == 6 * 4 + 10 * 8 and ExpertUpFp8Args.x.offset == 24
+    assert ctypes.sizeof(ExpertDownFp8Args) == 6 * 4 + 12 * 8 and ExpertDownFp8Args.fp32_rows.offset == 76
+
+
+@pytest.mark.parametrize("over,status,frag", [
+    (dict(num_tokens=-1), INVALID, "num_tokens must be >= 0"),
+    (dict(width=0), INVALID, "width must be >= 1"),
+    (dict(H=240), INVALID, "multiple of 32"),
+    (dict(H=16416), INVALID, "16384"),
+    (dict(I=8), INVALID, "multiple of 16"),
+    (dict(num_experts=0), INVALID, "num_experts must be in [1, 1025]"),
+    (dict(num_experts=1026), INVALID, "num_experts must be in [1, 1025]"),
+    (dict(block_size=32), UNSUP, "block_size must be 64 or 128"),
+    (dict(x=None), INVALID, "x must be"),
+    (dict(x=P + 8), INVALID, "x must be"),
+    (dict(w=P + 8), INVALID, "w must be"),
+    (dict(x_scales=None), INVALID, "x_scales and w_scales must be set"),
+    (dict(w_scales=None), INVALID, "x_scales and w_scales must be set"),
+    (dict(x_scales=P + 2), INVALID, "x_scales must be 4-byte aligned"),
+    (dict(w_scales=P + 2), INVALID, "w_scales must be 4-byte aligned"),
+    (dict(sorted_token_ids=None), INVALID, "must be set"),
+    (dict(expert_ids=P + 2), INVALID, "4-byte aligned"),
+    (dict(act=P + 4), INVALID, "act must be"),
+    (dict(act_scales=P + 2), INVALID, "act_scales must be 4-byte aligned"),
+    (dict(act_scales=P, I=48), INVALID, "multiple of 32 with act_scales"),
+    (dict(sorted_cap=0), INVALID, "sorted_cap"),
+    (dict(sorted_cap=1 << 31), UNSUP, "int32"),
+    (dict(num_tokens=1 << 27, width=9), UNSUP, "2^30"),
+    (dict(act_scales=P, sorted_cap=(1 << 31) - 1, I=256), UNSUP, "2^31 with act_scales"),
+])
+def test_up_refusals(lib, over, status, frag):
+    _refused(lib, lib.smr_expert_up_fp8(ctypes.byref(_up(**over)), P, 1 << 40, None), status, "smr_expert_up_fp8", frag)
+
+
+@pytest.mark.parametrize("over,status,frag", [
+    (dict(I=144), INVALID, "I must be a multiple of 32"),
+    (dict(H=40), INVALID, "H must be a multiple of 16"),
+    (dict(num_logical=0), INVALID, "num_logical must be in"),
+    (dict(topk_ids=None), INVALID, "topk_ids must be"),
+    (dict(topk_weights=P + 2), INVALID, "topk_weights must be"),
+    (dict(fp32_rows=2), INVALID, "fp32_rows must be 0 or 1"),
+    (dict(out=None), INVALID, "out must be"),
+    (dict(w_scales=None), INVALID, "must be set"),
+])
+def test_down_refusals(lib, over, status, frag):
+    _refused(lib, lib.smr_expert_down_fp8(ctypes.byref(_down(**over)), P, 1 << 40, None), status, "smr_expert_down_fp8", frag)
+
+
+def test_every_reason_is_listed(lib):
+    a = _up(num_tokens=-1, H=3, I=3, block_size=5)
+    _refused(lib, lib.smr_expert_up_fp8(ctypes.byref(a), P, 1 << 40, None), INVALID, "num_tokens", "H must be", "I must be", "block_size")
+    s = _select(_scoring(sigmoid=2, group_best=3, num_groups=7), topk=0, E=0)
+    _refused(lib, lib.smr_select_experts(ctypes.byref(s), None), INVALID, "sigmoid", "group_best", "topk must be", "E must be")
+
+
+def test_workspaces(lib):
+    size, down = lib.smr_expert_up_fp8_workspace_size, lib.smr_expert_down_fp8_workspace_size
+    assert size(None) == 0 and down(None) == 0 and size(ctypes.byref(_up())) == 256
+    # quantised activations wait in bf16 while an expert has few rows
+    assert size(ctypes.byref(_up(act_scales=P))) == ROWS + 4 * 11 * 128 * 2
+    many = 96 * 65 // 11 + 1
+    assert size(ctypes.byref(_up(act_scales=P, num_tokens=many))) == 256
+    assert size(ctypes.byref(_up(act_scales=P, num_tokens=many - 1))) == ROWS + -(-(many - 1) * 11 * 128 * 2 // 256) * 256
+    assert down(ctypes.byref(_down())) == ROWS + 4 * 11 * 256 * 4
+    assert down(ctypes.byref(_down(num_tokens=4096))) == ROWS + 4096 * 11 * 256 * 2
+    assert down(ctypes.byref(_down(num_tokens=4096, fp32_rows=1))) == ROWS + 4096 * 11 * 256 * 4
+    for fn, a, need in ((lib.smr_expert_up_fp8, _up(), 256), (lib.smr_expert_up_fp8, _up(act_scales=P), ROWS + 11264),
+                        (lib.smr_expert_down_fp8, _down(), ROWS + 45056)):
+        assert fn(ctypes.byref(a), P, need - 1, None) == WORKSPACE
+        assert fn(ctypes.byref(a), None, need, None) == WORKSPACE
+        assert fn(ctypes.byref(a), P + 128, need, None) == WORKSPACE
+
+
+def test_nothing_to_do(lib):
+    assert lib.smr_expert_up_fp8(ctypes.byref(ExpertUpFp8Args(0, 1, 32, 16, 1, 64)), None, 0, None) == _lib.SMR_OK
+    assert lib.smr_expert_down_fp8(ctypes.byref(ExpertDownFp8Args(0, 1, 16, 32, 1, 64, num_logical=1)), None, 0, None) == _lib.SMR_OK
+    empty = SelectArgs(None, 1, 0, 0, 64, 6, 0, 1, None, 1.0, Scoring(0, 1, 1, 1, 1.0, None), None, None)
+    assert lib.smr_select_experts(ctypes.byref(empty), None) == _lib.SMR_OK
+    assert lib.smr_quantize_fp8(None, 0, 64, 64, None, None, None) == _lib.SMR_OK
+    assert lib.smr_quantize_fp8_weight(None, 0, 64, 64, None, None, None) == _lib.SMR_OK
+    assert lib.smr_quantize_fp8_weight(None, 4, 0, 64, None, None, None) == _lib.SMR_OK
+    assert lib.smr_dequantize_fp8(None, None, 0, 64, None, None) == _lib.SMR_OK
+    r = RouteArgs()
+    r.M, r.H, r.E, r.topk, r.shared_scale, r.renormalize = 0, 64, 64, 6, 1.0, 1
+    s = Scoring(1, 8, 4, 2, 1.0, None)
+    assert lib.smr_route_scored(ctypes.byref(r), ctypes.byref(s), None, 0, None) == _lib.SMR_OK
+    assert lib.smr_last_launch_count() == 0
+
+
+@pytest.mark.parametrize("call,frag", [
+    (lambda lib: lib.smr_quantize_fp8(P, -1, 64, 64, P, P, None), "rows must be >= 0"),
+    (lambda lib: lib.smr_quantize_fp8(P, 1, 48, 48, P, P, None), "multiple of 32"),
+    (lambda lib: lib.smr_quantize_fp8(P, 1, 64, 60, P, P, None), "ld_x must be"),
+    (lambda lib: lib.smr_quantize_fp8(P + 8, 1, 64, 64, P, P, None), "x must be"),
+    (lambda lib: lib.smr_quantize_fp8(P, 1, 64, 64, P + 8, P, None), "codes must be"),
+    (lambda lib: lib.smr_quantize_fp8(P, 1, 64, 64, P, None, None), "scales must be"),
+    (lambda lib: lib.smr_quantize_fp8(P, 1 << 29, 64, 64, P, P, None), "2^34"),
+    (lambda lib: lib.smr_quantize_fp8_weight(P, -1, 64, 64, P, P, None), "matrices must be >= 0"),
+    (lambda lib: lib.smr_quantize_fp8_weight(P, 1 << 30, 1 << 20, 64, P, P, None), "2^40"),
+    (lambda lib: lib.smr_quantize_fp8_weight(P, 2, 64, 64, P, P + 1, None), "scales must be"),
+    (lambda lib: lib.smr_dequantize_fp8(P, P, 1, 65, P, None), "multiple of 32"),
+    (lambda lib: lib.smr_dequantize_fp8(P, P, 1, 64, P + 8, None), "out must be"),
+])
+def test_quantize_refusals(lib, call, frag):
+    assert call(lib) in (INVALID, UNSUP)
+    assert frag in lib.smr_last_error().decode() and lib.smr_last_launch_count() == 0
+
+
+@pytest.mark.parametrize("over,sover,status,frag", [
+    (dict(M=-1), {}, INVALID, "M must be >= 0"),
+    (dict(E=1025), {}, INVALID, "E must be in [1, 1024]"),
+    (dict(topk=65), {}, INVALID, "topk must be in [1, E]"),
+    (dict(topk=32), dict(topk_groups=8), UNSUP, "topk + has_shared must be <= 32"),
+    (dict(topk=40), dict(topk_groups=8), UNSUP, "topk + has_shared must be <= 32"),
+    (dict(renormalize=2), {}, INVALID, "renormalize"),
+    (dict(logits_fp32=2), {}, INVALID, "logits_fp32"),
+    (dict(has_shared=0), {}, INVALID, "shared_logits must be NULL"),
+    (dict(shared_scale=float("inf")), {}, INVALID, "shared_scale must be finite"),
+    (dict(logits=None), {}, INVALID, "logits must be"),
+    (dict(logits=P + 2), {}, INVALID, "logits must be"),
+    (dict(ld_logits=63), {}, INVALID, "ld_logits must be"),
+    (dict(topk_ids=None), {}, INVALID, "topk_ids must be"),
+    (dict(topk_weights=P + 1), {}, INVALID, "topk_weights must be"),
+    ({}, dict(sigmoid=5), INVALID, "sigmoid must be 0 or 1"),
+    ({}, dict(group_best=0), INVALID, "group_best must be 1 or 2"),
+    ({}, dict(num_groups=0), INVALID, "num_groups must be in [1, 32]"),
+    ({}, dict(num_groups=64, topk_groups=64), INVALID, "num_groups must be in [1, 32]"),
+    ({}, dict(num_groups=7), INVALID, "num_groups must divide the experts"),
+    ({}, dict(topk_groups=9), INVALID, "topk_groups must be in [1, num_groups]"),
+    (dict(topk=9), dict(topk_groups=1), INVALID, "topk must be at most topk_groups"),
+    ({}, dict(routed_scale=float("nan")), INVALID, "routed_scale must be finite"),
+    ({}, dict(balance_bias=P + 2), INVALID, "balance_bias must be 4-byte aligned"),
+    (dict(E=1020, ld_logits=1020), dict(num_groups=17, topk_groups=17), UNSUP, "num_groups of that many experts"),
+])
+def test_select_refusals(lib, over, sover, status, frag):
+    _refused(lib, lib.smr_select_experts(ctypes.byref(_select(_scoring(**sover), **over)), None), status, "smr_select_experts", frag)
+    _refused(lib, lib.smr_select_experts(None, None), INVALID, "args is NULL")
+
+
+def _route():
+    return _with(RouteArgs(), dict(M=4, H=64, E=64, topk=6, shared_scale=1.0, renormalize=1, hidden=P, ld_hidden=64,
+                                   gate_w=P, topk_ids=P, topk_weights=P))
+
+
+def test_scored_route_refusals_and_sizes(lib):
+    r, ws = _route(), 1 << 30
+    _refused(lib, lib.smr_route_scored(ctypes.byref(r), None, P, ws, None), INVALID, "scoring is NULL")
+    _refused(lib, lib.smr_route_scored(ctypes.byref(r), ctypes.byref(_scoring(num_groups=7)), P, ws, None), INVALID, "divide")
+    r.M = -1
+    _refused(lib, lib.smr_route_scored(ctypes.byref(r), ctypes.byref(_scoring(sigmoid=3)), P, ws, None), INVALID, "M must be", "sigmoid")
+    size = lib.smr_route_scored_workspace_size
+    for M in (1, 16, 17, 600):
+        r.M = M
+        assert size(ctypes.byref(r)) == ROWS + -(-M * 64 * 2 // 256) * 256 + -(-M * 4 // 256) * 256
+        assert lib.smr_route_scored(ctypes.byref(r), ctypes.byref(_scoring()), P, size(ctypes.byref(r)) - 1, None) == WORKSPACE
+    a = AlignArgs()
+    a.topk_ids, a.num_tokens, a.width, a.num_experts, a.block_size = P, 600, 6, 64, 64
+    a.sorted_token_ids, a.sorted_cap, a.expert_ids, a.expert_cap, a.num_tokens_post_padded = P, 1 << 20, P, 1 << 20, P
+    both = lib.smr_route_align_scored_workspace_size(ctypes.byref(r), ctypes.byref(a))
+    assert both > size(ctypes.byref(r))  # 3600 slots: the align's counts of tiles
+    assert lib.smr_route_align_scored(ctypes.byref(r), ctypes.byref(_scoring()), ctypes.byref(a), P, both - 1, None) == WORKSPACE
+    a.width = 7
+    _refused(lib, lib.smr_route_align_scored(ctypes.byref(r), ctypes.byref(_scoring()), ctypes.byref(a), P, ws, None), INVALID,
+             "align.width must equal")
+
+
+def _align_outputs(T, width, E, A):
+    cap = T * width + E * (A - 1)
+    i32 = torch.int32
+    return torch.zeros(cap, dtype=i32), torch.zeros(-(-cap // A), dtype=i32), torch.zeros(1, dtype=i32)
+
+
+def test_python_product_checks(smr):
+    u8, f32 = torch.uint8, torch.float32
+    al = _align_outputs(4, 2, 3, 64)
+    x, xs = torch.zeros(4, 160, dtype=u8), torch.zeros(4, 2, dtype=f32)
+    w, ws = torch.zeros(3, 64, 160, dtype=u8), torch.zeros(3, 2, 2, dtype=f32)
+    kw = dict(width=2, block_size=64)
+    for bad, match in ((dict(x_scales=xs[:, :1], w_scales=ws), "x_scales must be"), (dict(x_scales=xs, w_scales=ws[:, :1]), "w_scales must be"),
+                       (dict(x_scales=xs, w_scales=ws.to(u8)), "w_scales must be"), (dict(x_scales=xs), "both be"),
+                       (dict(x_scales=xs, w_scales=ws, act_scales=xs), "act_scales"), (dict(quantize_act=True), "quantize_act needs")):
+        with pytest.raises(ValueError, match=match):
+            smr.expert_up(x, w, *al, **bad, **kw)
+    with pytest.raises(ValueError, match="x must be"):
+        smr.expert_up(x.to(torch.bfloat16), w, *al, x_scales=xs, w_scales=ws, **kw)
+    with pytest.raises(ValueError, match="w must be"):
+        smr.expert_up(x, w.to(torch.int8), *al, x_scales=xs, w_scales=ws, **kw)
+    with pytest.raises(ValueError, match="x must be"):
+        smr.expert_up(torch.zeros(4, 320, dtype=u8)[:, ::2], w, *al, x_scales=xs, w_scales=ws, **kw)
+    with pytest.raises(ValueError, match="CUDA device"):
+        smr.expert_up(x, w, *al, x_scales=xs, w_scales=ws, **kw)
+    ids, wts = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    act, acts = torch.zeros(8, 32, dtype=u8), torch.zeros(8, 1)
+    w2, ws2 = torch.zeros(3, 160, 32, dtype=u8), torch.zeros(3, 2, 1)
+    with pytest.raises(ValueError, match="w_scales must be"):
+        smr.expert_down(act, w2, ids, wts, *al, block_size=64, x_scales=acts, w_scales=ws2[:, :1])
+    with pytest.raises(ValueError, match="CUDA device"):
+        smr.expert_down(act, w2, ids, wts, *al, block_size=64, x_scales=acts, w_scales=ws2)
+
+
+def test_python_format_and_select_checks(smr):
+    b16 = torch.bfloat16
+    for call in (lambda: smr.quantize_fp8(torch.zeros(2, 64)), lambda: smr.quantize_fp8(torch.zeros(2, 40, dtype=b16)),
+                 lambda: smr.quantize_fp8(torch.zeros(64, 64, dtype=b16).T[:, :32]), lambda: smr.quantize_fp8_weight(torch.zeros(64, 64, dtype=b16)),
+                 lambda: smr.quantize_fp8_weight(torch.zeros(2, 33, 64, dtype=b16), gated=True),
+                 lambda: smr.dequantize_fp8(torch.zeros(2, 64, dtype=torch.uint8), torch.zeros(2, 2)),
+                 lambda: smr.dequantize_fp8(torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2, 1)),
+                 lambda: smr.quantize_fp8(torch.zeros(2, 64, dtype=b16))):  # (the last: not on a CUDA device)
+        with pytest.raises(ValueError):
+            call()
+    lg = torch.zeros(3, 64)
+    for kw, match in ((dict(), "CUDA device"), (dict(shared_logits=torch.zeros(3)), "given with has_shared"),
+                      (dict(has_shared=True, shared_logits=torch.zeros(2)), "shared_logits must be")):
+        with pytest.raises(ValueError, match=match):
+            smr.select_experts(lg, topk=4, **kw)
+    with pytest.raises(ValueError, match="logits must be"):
+        smr.select_experts(lg.double(), topk=4)
+    with pytest.raises(ValueError, match="logits must be"):
+        smr.select_experts(torch.zeros(3, 128)[:, ::2], topk=4)
+    for kw, match in ((dict(scoring="max"), "scoring must be"), (dict(balance_bias=torch.zeros(3)), "balance_bias must be"),
+                      (dict(balance_bias=torch.zeros(64, dtype=b16)), "balance_bias must be"), (dict(num_groups=1 << 32), "below 2"),
+                      (dict(topk_groups=-1), "at least 0")):
+        with pytest.raises(ValueError, match=match):
+            smr._scoring(**{**dict(scoring="sigmoid", balance_bias=None, num_groups=1, topk_groups=None, group_best=1,
+                                   routed_scale=1.0, E=64, device=lg.device), **kw})
+    plain = dict(balance_bias=None, num_groups=1, topk_groups=None, group_best=1, routed_scale=1.0, E=64, device=lg.device)
+    assert smr._scoring("softmax", **plain) is None  # the route's own
+    s = smr._scoring("sigmoid", **{**plain, "num_groups": 8})
+    assert (s.sigmoid, s.num_groups, s.topk_groups, s.group_best, s.routed_scale, s.balance_bias) == (1, 8, 8, 1, 1.0, None)
+
+
+def test_disabled(smr, monkeypatch):
+    monkeypatch.setenv("SMR_DISABLE", "1")
+    b16 = torch.bfloat16
+    for call in (lambda: smr.select_experts(torch.zeros(1, 4), topk=1), lambda: smr.quantize_fp8(torch.zeros(1, 32, dtype=b16)),
+                 lambda: smr.quantize_fp8_weight(torch.zeros(1, 1, 32, dtype=b16)),
+                 lambda: smr.dequantize_fp8(torch.zeros(1, 32, dtype=torch.uint8), torch.zeros(1, 1))):
+        with pytest.raises(smr.SmrUnsupported, match="SMR_DISABLE"):
+            call()
+
+
+def test_no_read_only_loads_behind_a_programmatic_launch():
+    """These kernels start while the kernel before them may still write what they
+    read: none of it may come through the read-only path."""
+    from moe_router_top_gb300 import build
+    for name in ("smr_ffn.cuh", "smr_ffn8.cu", "smr_fp8.cu", "smr_fp8.cuh", "smr_score.cu"):
+        code = re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, name)).read())
+        for bad in (".nc", "ld_stream_v4", "__ldg"):
+            assert bad not in code, (name, bad)
+        for kernel in re.findall(r"__global__.*?\n}\n", code, re.S):
+            head, body = kernel.split("{", 1)
+            for ptr in re.findall(r"const (?:uint\w+|int\w+|float) \*__restrict__ (\w+)", head):
+                assert not re.search(rf"\b{ptr}\[", body), (name, ptr)
+
+
+def test_moved_registers_add_up():
+    """The epilogue's warps wait for registers that the others give up: the shares
+    must not exceed what the launch has (the launcher refuses a kernel that was
+    compiled with fewer)."""
+    from moe_router_top_gb300 import build
+    code = open(os.path.join(build.CSRC, "smr_ffn8.cu")).read()
+    dec, inc = int(re.search(r"setmaxnreg\.dec\S* (\d+)", code).group(1)), int(re.search(r"setmaxnreg\.inc\S* (\d+)", code).group(1))
+    threads = int(re.search(r"kRowThreads = (\d+)", code).group(1))
+    regs = int(re.search(r"at\.numRegs != (\d+)", code).group(1))
+    assert len(re.findall("setmaxnreg", code)) == 2 and threads == 512
+    assert 256 * dec + 256 * inc == threads * regs <= 65536

@@ -213,3 +213,95 @@ def test_scored_route(smr, M, E, S):
     n = int(al[2])
     assert n == int(got[4]) and torch.equal(al[0][:n], got[2][:n]) and torch.equal(al[1][: n // 64], got[3][: n // 64])
     assert smr.get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("M", [4, 16, 17, 700])
+def test_captured_and_replayed(smr, M):
+    """Graphs of a scored route and align and of a selection, replayed with new
+    inputs and on two streams at once, give what eager calls give."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    gate = (torch.randn(160, 256, device="cuda", generator=g) / 12).to(torch.bfloat16)
+    shared = (torch.randn(1, 256, device="cuda", generator=g) / 12).to(torch.bfloat16)
+    how = dict(topk=6, scoring="sigmoid", num_groups=8, topk_groups=4, group_best=2, routed_scale=2.5)
+    sets = []
+    for _ in range(2):
+        x = torch.randn(M, 256, device="cuda", generator=g).to(torch.bfloat16)
+        bias = torch.randn(160, device="cuda", generator=g) * 0.1
+        lg = torch.empty(M, 160, dtype=torch.bfloat16, device="cuda")
+        sets.append((x, bias, lg, smr.Workspace()))
+
+    def call(x, bias, lg, ws):
+        out = smr.route_align(x, gate, shared, block_size=64, balance_bias=bias, logits_out=lg, workspace=ws, **how)
+        return out + smr.select_experts(lg, balance_bias=bias, has_shared=True, shared_scale=0.5, **how)
+
+    def same(a, b):
+        n = int(b[4])
+        return int(a[4]) == n and torch.equal(a[2][:n], b[2][:n]) and torch.equal(a[3][: n // 64], b[3][: n // 64]) and all(
+            torch.equal(a[i], b[i]) for i in (0, 1, 5, 6))
+
+    eager = [call(*s) for s in sets]
+    graphs, outs = [], []
+    for s in sets:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(call(*s))
+        graphs.append(gr)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for gr, st in zip(graphs, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert all(same(a, b) for a, b in zip(outs, eager))
+    sets[0][0].neg_()
+    sets[0][1].neg_()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    new = [t.clone() for t in outs[0]]
+    ref = call(*sets[0])
+    assert same(new, ref) and not torch.equal(ref[0], eager[0][0])
+    assert all(smr.get_device_error(s[3]) == 0 for s in sets)
+
+
+def test_changed_bias_between_calls(smr):
+    """The bias that one call reads and a kernel then changes: the next call's is the new one."""
+    logits, g = _logits(300, 256, 11)
+    bias = torch.randn(256, device="cuda", generator=g)
+    for _ in range(10):
+        a = smr.select_experts(logits, topk=8, scoring="sigmoid", balance_bias=bias)
+        bias.neg_()
+        b = smr.select_experts(logits, topk=8, scoring="sigmoid", balance_bias=bias)
+        ref = smr.select_experts(logits, topk=8, scoring="sigmoid", balance_bias=bias.clone())
+        assert torch.equal(b[0], ref[0]) and torch.equal(b[1], ref[1]) and not torch.equal(a[0], b[0])
+
+
+def test_offsets_past_32_bits(smr):
+    M, E = 2_200_000, 1024
+    logits = torch.zeros(M, E, dtype=torch.bfloat16, device="cuda")
+    tail, g = _logits(60, E, 12, dtype=torch.bfloat16)
+    logits[-60:] = tail
+    ids, w = smr.select_experts(logits, topk=8, scoring="sigmoid", num_groups=8, topk_groups=4)
+    small = smr.select_experts(tail, topk=8, scoring="sigmoid", num_groups=8, topk_groups=4)
+    assert torch.equal(ids[-60:], small[0]) and torch.equal(w[-60:], small[1])
+    assert (ids[:-60] == torch.arange(8, device="cuda", dtype=torch.int32)).all() and (w[:-60] == 0.125).all()
+
+
+@pytest.mark.parametrize("M", [0, 5, 40])
+def test_scored_align_sizes(smr, M):
+    """An empty batch pads to nothing; an EPLB remap sees the scored ids."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(M, 128, device="cuda", generator=g).to(torch.bfloat16)
+    gate = (torch.randn(64, 128, device="cuda", generator=g) / 8).to(torch.bfloat16)
+    how = dict(topk=4, scoring="sigmoid", num_groups=4, topk_groups=2)
+    got = smr.route_align(x, gate, block_size=64, **how)
+    ids, w = smr.route(x, gate, **how)
+    assert torch.equal(got[0], ids) and torch.equal(got[1], w)
+    assert int(got[4]) % 64 == 0 and (int(got[4]) == 0) == (M == 0)
+    emap = torch.full((64, 2), -1, dtype=torch.int32, device="cuda")
+    emap[:, 0] = torch.arange(64, device="cuda").flip(0)
+    count = torch.ones(64, dtype=torch.int32, device="cuda")
+    mapped = smr.route_align(x, gate, block_size=64, eplb_map=emap, eplb_count=count, num_physical=64, **how)
+    plain = smr.align(63 - ids, 64, 64)
+    n = int(plain[2])
+    assert int(mapped[4]) == n and torch.equal(mapped[2][:n], plain[0][:n]) and torch.equal(mapped[3][: n // 64], plain[1][: n // 64])
