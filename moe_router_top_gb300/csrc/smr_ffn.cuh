@@ -698,13 +698,13 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                     const uint32_t idesc = idesc_e4m3(kM, n);
                     for (int kb = 0; ok && kb < p.num_kb; kb += SUB) {
                         if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
+                        if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
+                        tc_fence_after();
                         const uint32_t base = ring + (uint32_t)st.i * p.stage_bytes;
 #pragma unroll
                         for (int u = 0; u < SUB; ++u) {
                             if (SUB > 1 && kb + u >= p.num_kb) break;
-                            if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
-                            tc_fence_after();
-                            const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols);
+                            const uint32_t acc = tmem + (uint32_t)(ac.i * p.acc_cols + u * p.A);
                             const uint64_t da = smem_desc_sw<128>(base + u * kFfWBytes),
                                            db = smem_desc_sw<128>(base + x_off + u * p.b_bytes);
                             const int steps = kb + u + 1 == p.num_kb ? p.last_steps : 4;
@@ -717,12 +717,13 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                                     for (int kk = 0; kk < steps; ++kk)
                                         tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
                                 }
-                                ff_commit<PAIR>(&acc_full[ac.i]);
                             }
-                            ac.next(p.accs);
                         }
-                        if (!ok) break;
-                        if (elected) ff_commit<PAIR>(&empty[st.i]);
+                        if (elected) {
+                            ff_commit<PAIR>(&acc_full[ac.i]);
+                            ff_commit<PAIR>(&empty[st.i]);
+                        }
+                        ac.next(p.accs);
                         st.next(ST);
                     }
                     continue;
@@ -989,11 +990,12 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                                 : (uint32_t)((lane & 7) * kOutPitch<UP> + q * 64 + (lane >> 3) * 16);
         uint32_t buf = 0;
         if constexpr (FP8) {
-            // E4M3: an accumulator holds one k-block's products, which are added,
-            // times the scale of their column and of the weight tile, to the
-            // piece's sums in registers (column 16 half + 32 g and on in sum[g],
-            // in the fragments' order; fp32 outputs: 16 columns of one row).
-            constexpr int kGroups = kCols / 32;
+            // E4M3: an accumulator holds the products of a stage's k-blocks, side
+            // by side, which are added, times the scale of their column and of
+            // the weight tile, to the piece's sums in registers (column 16 half +
+            // 32 g and on in sum[g], in the fragments' order; fp32 outputs: 16
+            // columns of one row).
+            constexpr int kGroups = SUB == 2 ? 2 : kCols / 32;  // (two k-blocks a stage: blocks of 64 rows)
             RingPos sc;
             while (true) {
                 bool ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag);
@@ -1004,51 +1006,64 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 for (int g = 0; g < kGroups; ++g)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sum[g][j] = 0.0f;
-                for (int kb = 0; n >= 0 && kb < p.num_kb; ++kb) {
+                for (int kb = 0; n >= 0 && kb < p.num_kb; kb += SUB) {
                     const int in = kb & (kFp8Group - 1);
                     if (in == 0 && !(ok = warp_wait(&scale_full[sc.i], sc.ph, abort_flag))) break;
+                    const float *scales = scale_ring + sc.i * (kFp8ScaleBytes<kCols> / 4) + in * (kCols + 4) + 16 * half + (F32 ? 0 : 4 * (lane & 3));
+                    // 16 columns twice a wait for TMEM (what one costs is the same
+                    // for more): of both k-blocks, or two groups of one. Their
+                    // scales (of b: 16, or this thread's four) are read ahead.
+                    constexpr int kFour = F32 ? 4 : 1, kNext = SUB == 2 ? 0 : 32, kNextKb = SUB == 2 ? kCols + 4 : 0;
+                    const bool two = SUB == 1 || kb + 1 < p.num_kb;
+                    float4 f[2][kFour];
+                    float2 w[2];
+                    const auto read_scales = [&](int g) {
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int t = 0; t < kFour; ++t)
+                                f[b][t] = *reinterpret_cast<const float4 *>(scales + 32 * g + b * (kNext + kNextKb) + 4 * t);
+                    };
+                    read_scales(0);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        w[b] = UP ? *reinterpret_cast<const float2 *>(scales + kCols - 16 * half - 4 * (lane & 3) + b * kNextKb) : make_float2(1.0f, 1.0f);
                     if (!(ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag))) break;
                     tc_fence_after();
-                    const float *scales = scale_ring + sc.i * (kFp8ScaleBytes<kCols> / 4) + in * (kCols + 4);
-                    const float2 w = UP ? *reinterpret_cast<const float2 *>(scales + kCols) : make_float2(1.0f, 1.0f);
-                    scales += 16 * half + (F32 ? 0 : 4 * (lane & 3));
                     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.acc_cols + 16 * half);
-                    // twice 16 columns a wait: what a wait costs is the same for more
 #pragma unroll
-                    for (int g0 = 0; g0 < kGroups; g0 += 2) {
+                    for (int g0 = 0; g0 < kGroups; g0 += 3 - SUB) {
                         if (16 * half + 32 * g0 >= n) break;
                         uint32_t v[2][16];
-                        float4 f[2];
-                        const bool both = 16 * half + 32 * (g0 + 1) < n;
+                        const bool both = SUB == 2 ? two : 16 * half + 32 * (g0 + 1) < n;
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             if (b == 1 && !both) break;
-                            if constexpr (F32) tmem_ld16_async(acc + (uint32_t)(32 * (g0 + b)), v[b]);
-                            else tmem_ld_frags_async(acc + (uint32_t)(32 * (g0 + b)), v[b]);
+                            const uint32_t from = acc + (uint32_t)(32 * g0 + b * (SUB == 2 ? p.A : 32));
+                            if constexpr (F32) tmem_ld16_async(from, v[b]);
+                            else tmem_ld_frags_async(from, v[b]);
                         }
+                        if (g0 != 0) read_scales(g0);
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
                             if (b == 1 && !both) break;
-                            const int g = g0 + b;
+                            const int g = g0 + (SUB == 2 ? 0 : b);
+                            tmem_wait_ld16(v[b]);
                             if constexpr (F32) {
-                                tmem_wait_ld16(v[b]);
 #pragma unroll
                                 for (int t = 0; t < 4; ++t) {
-                                    f[b] = *reinterpret_cast<const float4 *>(scales + 32 * g + 4 * t);
 #pragma unroll
                                     for (int u = 0; u < 2; ++u) {
                                         const int j = 8 * u + 2 * t;
-                                        sum[g][j] = fmaf(__uint_as_float(v[b][j]), u ? f[b].z : f[b].x, sum[g][j]);
-                                        sum[g][j + 1] = fmaf(__uint_as_float(v[b][j + 1]), u ? f[b].w : f[b].y, sum[g][j + 1]);
+                                        sum[g][j] = fmaf(__uint_as_float(v[b][j]), u ? f[b][t].z : f[b][t].x, sum[g][j]);
+                                        sum[g][j + 1] = fmaf(__uint_as_float(v[b][j + 1]), u ? f[b][t].w : f[b][t].y, sum[g][j + 1]);
                                     }
                                 }
                             } else {
-                                f[b] = *reinterpret_cast<const float4 *>(scales + 32 * g);
-                                tmem_wait_ld16(v[b]);
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
-                                    const float wh = h == 0 ? w.x : w.y;
-                                    const float4 s = UP ? make_float4(f[b].x * wh, f[b].y * wh, f[b].z * wh, f[b].w * wh) : f[b];
+                                    const float wh = h == 0 ? w[b].x : w[b].y;
+                                    const float4 s = UP ? make_float4(f[b][0].x * wh, f[b][0].y * wh, f[b][0].z * wh, f[b][0].w * wh) : f[b][0];
 #pragma unroll
                                     for (int r = 0; r < 2; ++r) {
                                         const int j = 8 * h + 2 * r;
@@ -1066,9 +1081,9 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                     if (lane == 0) {
                         if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[ac.i]), 0u));
                         else mbar_arrive(smem_u32(&acc_empty[ac.i]));
-                        if (in == kFp8Group - 1 || kb + 1 == p.num_kb) mbar_arrive(smem_u32(&scale_empty[sc.i]));
+                        if (in + SUB == kFp8Group || kb + SUB >= p.num_kb) mbar_arrive(smem_u32(&scale_empty[sc.i]));
                     }
-                    if (in == kFp8Group - 1 || kb + 1 == p.num_kb) sc.next(kFp8Ring);
+                    if (in + SUB == kFp8Group || kb + SUB >= p.num_kb) sc.next(kFp8Ring);
                     ac.next(p.accs);
                 }
                 // the four warps go on together, or none does
@@ -1322,7 +1337,7 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     p.stages = (int)((kSmemMax - 1024 - kMisc) / p.stage_bytes);
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
     if (p.stages < kFfLoaders<SUB, FP8>) return cudaErrorNotSupported;  // (see the row loaders; never with these sizes)
-    p.acc_cols = PAIR ? kCols : a.A;
+    p.acc_cols = PAIR ? kCols : (FP8 ? SUB : 1) * a.A;
     p.accs = kFfAccs<FP8>;
     while (p.accs * p.acc_cols > 512) p.accs /= 2;
     const int cols = p.accs * p.acc_cols + (MX ? 32 : 0);
