@@ -30,6 +30,10 @@
 #include "smr_device.cuh"
 #include "smr_launch.h"
 
+#ifndef FFN_BOUNDS  // (smr_ffn8.cu gives registers outright)
+#define FFN_BOUNDS __launch_bounds__(kFfThreads<SUB, FP8>, 1)
+#endif
+
 namespace smr {
 
 // k-blocks a stage: two for blocks of 64 rows and for pairs in MXFP4, else one
@@ -68,7 +72,8 @@ struct FfInfo {
     int row[COLS];
 };
 // Accumulators in TMEM: two, one being drained under the other's MMAs. In E4M3
-// one holds a single k-block (see the epilogue), and as many as fit are used.
+// one holds the k-blocks of a single stage (see the epilogue), and as many as
+// fit are used.
 template <bool FP8>
 constexpr int kFfAccs = FP8 ? 4 : 2;
 // E4M3: scales of a piece's columns for kFp8Group k-blocks, and of the weight
@@ -541,10 +546,13 @@ __device__ __forceinline__ void ff_scout(const FfParams &p, FfInfo<COLS> *info, 
 // epilogue's registers, so that blocks of the sum fit beside a CTA).
 // FP8: E4M3 operands. Their scales change from one 128 values of K to the next
 // and are no powers of two, so the tensor core cannot apply them: a k-block is
-// one MMA chain into an accumulator of its own, which the epilogue's warps add,
-// scaled, to sums in their registers.
+// one MMA chain into columns of its own, which the epilogue's warps add,
+// scaled, to sums in their registers. What bounds that with few rows an expert
+// is the chain of signals, from the ring over the MMAs to the epilogue and back,
+// some 600 cycles a turn; so a stage's two k-blocks share a turn (512 skewed
+// tokens of H 2048, 128 experts, I 768: both products 151 us, with a turn each 180).
 template <bool MX, bool UP, bool PAIR, int SUB, bool F32, bool FP8 = false>
-__global__ void __launch_bounds__(kFfThreads<SUB, FP8>, 1)
+__global__ void FFN_BOUNDS
 expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const FfParams p) {
     constexpr int kCols = kFfCols<MX, PAIR, FP8>;
     using Info = FfInfo<kCols>;
@@ -1011,23 +1019,23 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                     if (in == 0 && !(ok = warp_wait(&scale_full[sc.i], sc.ph, abort_flag))) break;
                     const float *scales = scale_ring + sc.i * (kFp8ScaleBytes<kCols> / 4) + in * (kCols + 4) + 16 * half + (F32 ? 0 : 4 * (lane & 3));
                     // 16 columns twice a wait for TMEM (what one costs is the same
-                    // for more): of both k-blocks, or two groups of one. Their
-                    // scales (of b: 16, or this thread's four) are read ahead.
-                    constexpr int kFour = F32 ? 4 : 1, kNext = SUB == 2 ? 0 : 32, kNextKb = SUB == 2 ? kCols + 4 : 0;
+                    // for more): of both k-blocks, or two groups of one.
+                    constexpr int kNext = SUB == 2 ? kCols + 4 : 32;
                     const bool two = SUB == 1 || kb + 1 < p.num_kb;
-                    float4 f[2][kFour];
-                    float2 w[2];
+                    // (bf16 outputs: a thread's four scales are read ahead; of
+                    // fp32 ones the 16 columns', which would take registers)
+                    float4 f4[2];
+                    float2 w[2] = {make_float2(1.0f, 1.0f), make_float2(1.0f, 1.0f)};
                     const auto read_scales = [&](int g) {
+                        if constexpr (!F32)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b)
-#pragma unroll
-                            for (int t = 0; t < kFour; ++t)
-                                f[b][t] = *reinterpret_cast<const float4 *>(scales + 32 * g + b * (kNext + kNextKb) + 4 * t);
+                            for (int b = 0; b < 2; ++b) f4[b] = *reinterpret_cast<const float4 *>(scales + 32 * g + b * kNext);
                     };
                     read_scales(0);
+                    if constexpr (UP)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        w[b] = UP ? *reinterpret_cast<const float2 *>(scales + kCols - 16 * half - 4 * (lane & 3) + b * kNextKb) : make_float2(1.0f, 1.0f);
+                        for (int b = 0; b < 2; ++b)
+                            w[b] = *reinterpret_cast<const float2 *>(scales + kCols - 16 * half - 4 * (lane & 3) + (SUB == 2 ? b * kNext : 0));
                     if (!(ok = warp_wait(&acc_full[ac.i], ac.ph, abort_flag))) break;
                     tc_fence_after();
                     const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ac.i * p.acc_cols + 16 * half);
@@ -1050,20 +1058,23 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                             const int g = g0 + (SUB == 2 ? 0 : b);
                             tmem_wait_ld16(v[b]);
                             if constexpr (F32) {
+                                float4 f[4];
+#pragma unroll
+                                for (int t = 0; t < 4; ++t) f[t] = *reinterpret_cast<const float4 *>(scales + 32 * g0 + b * kNext + 4 * t);
 #pragma unroll
                                 for (int t = 0; t < 4; ++t) {
 #pragma unroll
                                     for (int u = 0; u < 2; ++u) {
                                         const int j = 8 * u + 2 * t;
-                                        sum[g][j] = fmaf(__uint_as_float(v[b][j]), u ? f[b][t].z : f[b][t].x, sum[g][j]);
-                                        sum[g][j + 1] = fmaf(__uint_as_float(v[b][j + 1]), u ? f[b][t].w : f[b][t].y, sum[g][j + 1]);
+                                        sum[g][j] = fmaf(__uint_as_float(v[b][j]), u ? f[t].z : f[t].x, sum[g][j]);
+                                        sum[g][j + 1] = fmaf(__uint_as_float(v[b][j + 1]), u ? f[t].w : f[t].y, sum[g][j + 1]);
                                     }
                                 }
                             } else {
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
                                     const float wh = h == 0 ? w[b].x : w[b].y;
-                                    const float4 s = UP ? make_float4(f[b][0].x * wh, f[b][0].y * wh, f[b][0].z * wh, f[b][0].w * wh) : f[b][0];
+                                    const float4 s = UP ? make_float4(f4[b].x * wh, f4[b].y * wh, f4[b].z * wh, f4[b].w * wh) : f4[b];
 #pragma unroll
                                     for (int r = 0; r < 2; ++r) {
                                         const int j = 8 * h + 2 * r;

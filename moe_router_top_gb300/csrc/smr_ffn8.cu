@@ -26,6 +26,12 @@
 // for every accumulator (536), copies that a warp waits for and makes visible
 // before it announces them (531), the stages handed back by the epilogue (463,
 // the second product 25 longer).
+// Registers of the kernel of the other formats. Blocks of 64 rows, 112: they
+// leave 8192 for a block of the sum or of the quantisation that follows, which
+// reads the align's outputs meanwhile (the decode shape, 8 tokens: second
+// product 35.5 us; with 128 registers 41.7, with 96, which spill, 38.2 but 512
+// tokens 62 instead of 56).
+#define FFN_BOUNDS __maxnreg__(SUB == 2 ? 112 : 128)
 #include "smr_ffn.cuh"
 #include "smr_fp8.cuh"
 

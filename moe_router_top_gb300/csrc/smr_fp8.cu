@@ -50,16 +50,18 @@ quantize_fp8_kernel(const uint16_t *__restrict__ x, int64_t ld, uint32_t row_pie
 
 // The same for the rows of the slots that an align lists (no other row is
 // written): a 16-lane group takes a block of one listed row a step. The grid
-// covers the SMs; what lies past num_tokens_post_padded costs nothing.
-__global__ void __launch_bounds__(kFp8Threads)
+// covers the SMs; what lies past num_tokens_post_padded costs nothing. The
+// align's outputs, which the product waited for before it let this launch go,
+// are read under the product: a block is small enough to be resident beside it.
+constexpr int kSlotsThreads = 128;
+__global__ void __launch_bounds__(kSlotsThreads)
 quantize_fp8_slots_kernel(const QuantizeRows p, uint32_t row_blocks) {
-    griddep_wait();
-    griddep_launch_dependents();
     const uint32_t in = threadIdx.x & 15;
     const int64_t rows = min((int64_t)max(__ldcg(p.npp), 0), p.sorted_cap);
     const uint32_t blocks = (uint32_t)(rows * row_blocks), row_vecs = (uint32_t)p.K / 8;  // (blocks < 2^31)
-    const uint32_t step = gridDim.x * (kFp8Threads / 16);
-    for (uint32_t b0 = blockIdx.x * (kFp8Threads / 16); b0 < blocks; b0 += kFp8Vecs * step) {
+    const uint32_t step = gridDim.x * (kSlotsThreads / 16);
+    bool waited = false;
+    for (uint32_t b0 = blockIdx.x * (kSlotsThreads / 16); b0 < blocks; b0 += kFp8Vecs * step) {
         uint4 v[kFp8Vecs];
         int64_t at[kFp8Vecs];   // the vector among the codes, -1: none
         int64_t sat[kFp8Vecs];  // the block among the scales, -1: none
@@ -72,6 +74,9 @@ quantize_fp8_slots_kernel(const QuantizeRows p, uint32_t row_blocks) {
             at[j] = real && vec < row_vecs ? (int64_t)slot * row_vecs + vec : -1;
             sat[j] = real && in == 0 ? (int64_t)slot * row_blocks + kb : -1;
         }
+        if (!waited) griddep_wait();
+        if (!waited) griddep_launch_dependents();
+        waited = true;
 #pragma unroll
         for (int j = 0; j < kFp8Vecs; ++j)
             v[j] = at[j] >= 0 ? ld_stream_rows_v4(p.x + at[j] * 8) : make_uint4(0u, 0u, 0u, 0u);
@@ -87,6 +92,7 @@ quantize_fp8_slots_kernel(const QuantizeRows p, uint32_t row_blocks) {
             if (sat[j] >= 0) p.scales[sat[j]] = scale;
         }
     }
+    if (!waited) griddep_wait();
 }
 
 // Weights, once: a CTA per 128 x 128 block of one of the matrices [N][K].
@@ -180,9 +186,10 @@ cudaError_t launch_quantize_fp8(const uint16_t *x, int64_t rows, int K, int64_t 
 cudaError_t launch_quantize_fp8_slots(const QuantizeRows &a, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     const uint32_t row_blocks = (uint32_t)(a.K + 127) / 128;
-    const int64_t per = kFp8Threads / 16, need = (a.sorted_cap * row_blocks + per - 1) / per;
-    const int64_t room = 8 * (int64_t)sm_count();
-    const cudaLaunchConfig_t cfg = fp8_config(need < room ? need : room, stream, attr);
+    const int64_t per = kSlotsThreads / 16, need = (a.sorted_cap * row_blocks + per - 1) / per;
+    const int64_t room = 16 * (int64_t)sm_count();
+    cudaLaunchConfig_t cfg = fp8_config(need < room ? need : room, stream, attr);
+    cfg.blockDim = dim3(kSlotsThreads, 1, 1);
     return cudaLaunchKernelEx(&cfg, quantize_fp8_slots_kernel, a, row_blocks);
 }
 

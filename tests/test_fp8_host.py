@@ -6,6 +6,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import subprocess
 
 import pytest
 
@@ -332,3 +333,28 @@ def test_moved_registers_add_up():
     regs = int(re.search(r"at\.numRegs != (\d+)", code).group(1))
     assert len(re.findall("setmaxnreg", code)) == 2 and threads == 512
     assert 256 * dec + 256 * inc == threads * regs <= 65536
+
+
+def test_what_follows_fits_beside_a_product_of_few_rows(tmp_path):
+    """By the compiler's register counts: a block of the sum, or of the
+    activations' quantisation, fits on an SM that holds a CTA of the product
+    before it; and the rows kernel has the registers that its warps share out."""
+    from moe_router_top_gb300 import build
+    used = {}
+    for name in ("smr_ffn8.cu", "smr_ffn.cu", "smr_fp8.cu"):
+        out = subprocess.run([build.nvcc()] + build.ARCH + build.FLAGS + ["-Xptxas", "-v", "-c", os.path.join(build.CSRC, name),
+                             "-o", str(tmp_path / "k.o")], check=True, capture_output=True, text=True)
+        used.update(re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", out.stdout + out.stderr, re.S))
+
+    def alloc(part, threads):  # registers are handed out to warps in units of 8 a thread
+        name = next(n for n in used if part in n)
+        return -(-int(used[name]) // 8) * 8 * threads
+
+    source = open(os.path.join(build.CSRC, "smr_ffn.cu")).read()
+    combine = int(re.search(r"kCombineThreads = (\d+);", source).group(1))
+    slots = int(re.search(r"kSlotsThreads = (\d+);", open(os.path.join(build.CSRC, "smr_fp8.cu")).read()).group(1))
+    for f32 in (0, 1):
+        assert alloc(f"expert_ffn_kernelILb0ELb0ELb0ELi2ELb{f32}ELb1E", 512) + alloc(f"expert_combine_kernelILb{f32}", combine) <= 65536
+    assert alloc("expert_ffn_kernelILb0ELb1ELb0ELi2ELb0ELb1E", 512) + alloc("quantize_fp8_slots_kernel", slots) <= 65536
+    rows = [n for n in used if "expert_rows_kernel" in n]
+    assert len(rows) == 4 and all(int(used[n]) == 128 for n in rows)
