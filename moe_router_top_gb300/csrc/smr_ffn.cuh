@@ -88,13 +88,12 @@ constexpr int kFfBars = 2 * kFfMaxStages + 2 * kFfAccs<FP8> + 2 * kFfInfos + 1 +
 template <bool FP8>
 constexpr int kFfBarBytes = (kFfBars<FP8> * 8 + 8 + 15) / 16 * 16;
 // Columns of a piece, at most. (A pair of MXFP4: 128, as two accumulators of
-// 256 columns would leave no room in TMEM for the scales. A pair of E4M3: 128,
-// as the epilogue holds the columns' sums in registers.)
-template <bool MX, bool PAIR, bool FP8 = false>
-constexpr int kFfCols = PAIR && !MX && !FP8 ? 256 : 128;
+// 256 columns would leave no room in TMEM for the scales.)
+template <bool MX, bool PAIR>
+constexpr int kFfCols = PAIR && !MX ? 256 : 128;
 template <bool MX, bool UP, bool PAIR, bool FP8 = false>
-constexpr int kFfMiscBytes = kFfBarBytes<FP8> + kFfInfos * (int)sizeof(FfInfo<kFfCols<MX, PAIR, FP8>>) +
-                             (FP8 ? kFp8Ring * kFp8ScaleBytes<kFfCols<MX, PAIR, FP8>> : 0);
+constexpr int kFfMiscBytes = kFfBarBytes<FP8> + kFfInfos * (int)sizeof(FfInfo<kFfCols<MX, PAIR>>) +
+                             (FP8 ? kFp8Ring * kFp8ScaleBytes<kFfCols<MX, PAIR>> : 0);
 
 struct FfParams {
     int num_kb, last_steps;  // k-blocks; MMA steps of the last one (4 in the others)
@@ -379,13 +378,14 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
 // gridDim-th item: a block's tiles run next to each other in time
 // (its rows stay in L2), blocks of one expert too (its weights).
 // UP: rows of x by token, else by slot. AHEAD: items whose entries are under way.
-template <bool UP, bool PAIR, int COLS, int INFOS, int AHEAD>
+// CTAS: the CTAs of an item (one can also take groups of blocks and two tiles).
+template <bool UP, bool PAIR, int COLS, int INFOS, int AHEAD, int CTAS = PAIR ? 2 : 1>
 __device__ __forceinline__ void ff_scout(const FfParams &p, FfInfo<COLS> *info, uint64_t *info_full, uint64_t *info_empty,
                                          volatile int *abort_flag, uint32_t rank) {
     const int lane = threadIdx.x & 31;
     const int A = p.A, G = PAIR ? COLS / A : 1;
     const int tiles = PAIR ? (p.ntiles + 1) / 2 : p.ntiles;
-    const int ctas = PAIR ? gridDim.x >> 1 : gridDim.x, cta = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    const int ctas = (int)gridDim.x / CTAS, cta = (int)blockIdx.x / CTAS;
     const int dgrp = ctas / tiles, dtile = ctas % tiles;
     int grp = cta / tiles, tile = cta % tiles;  // the item
     const int bo = 8 * lane / A, po = 8 * lane % A;  // this lane's 8 entries: block of the group, place in it
@@ -554,7 +554,8 @@ __device__ __forceinline__ void ff_scout(const FfParams &p, FfInfo<COLS> *info, 
 template <bool MX, bool UP, bool PAIR, int SUB, bool F32, bool FP8 = false>
 __global__ void FFN_BOUNDS
 expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_s, const FfParams p) {
-    constexpr int kCols = kFfCols<MX, PAIR, FP8>;
+    static_assert(!FP8 || (!PAIR && !MX), "E4M3: single CTAs (see smr_ffn8.cu)");
+    constexpr int kCols = kFfCols<MX, PAIR>;
     using Info = FfInfo<kCols>;
     constexpr int kLoaders = kFfLoaders<SUB, FP8>, kFirst = kFfRoles<FP8>, kAccs = kFfAccs<FP8>;
     extern __shared__ uint8_t smem_raw[];
@@ -703,7 +704,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                 if (rank != 0) continue;
                 constexpr int kM = PAIR ? 2 * kFfRows : kFfRows;
                 if constexpr (FP8) {
-                    const uint32_t idesc = idesc_e4m3(kM, n);
+                    const uint32_t idesc = idesc_e4m3(kFfRows, n);
                     for (int kb = 0; ok && kb < p.num_kb; kb += SUB) {
                         if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
                         if (!(ok = warp_wait(&acc_empty[ac.i], ac.ph ^ 1u, abort_flag))) break;
@@ -720,16 +721,16 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                                 if (steps == 4) {
 #pragma unroll
                                     for (int kk = 0; kk < 4; ++kk)
-                                        tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                                        tc_mma_e4m3<false>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
                                 } else {
                                     for (int kk = 0; kk < steps; ++kk)
-                                        tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                                        tc_mma_e4m3<false>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
                                 }
                             }
                         }
                         if (elected) {
-                            ff_commit<PAIR>(&acc_full[ac.i]);
-                            ff_commit<PAIR>(&empty[st.i]);
+                            ff_commit<false>(&acc_full[ac.i]);
+                            ff_commit<false>(&empty[st.i]);
                         }
                         ac.next(p.accs);
                         st.next(ST);
@@ -1090,8 +1091,7 @@ expert_ffn_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constan
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(smem_u32(&acc_empty[ac.i]), 0u));
-                        else mbar_arrive(smem_u32(&acc_empty[ac.i]));
+                        mbar_arrive(smem_u32(&acc_empty[ac.i]));
                         if (in + SUB == kFp8Group || kb + SUB >= p.num_kb) mbar_arrive(smem_u32(&scale_empty[sc.i]));
                     }
                     if (in + SUB == kFp8Group || kb + SUB >= p.num_kb) sc.next(kFp8Ring);
@@ -1340,7 +1340,7 @@ static cudaError_t launch_product(const FfnLaunch &a, int sms, cudaStream_t stre
     // (4 bytes of scales are 128 values of MXFP4 and of E4M3)
     const uintptr_t scales_at = reinterpret_cast<uintptr_t>(a.x_scales) | (uintptr_t)(4 * (FP8 ? p.num_kb : p.num_chunks));
     p.scale_bytes = scales_at % 16 == 0 ? 16 : (scales_at % 8 == 0 ? 8 : 4);
-    constexpr int kCols = kFfCols<MX, PAIR, FP8>;
+    constexpr int kCols = kFfCols<MX, PAIR>;
     p.b_bytes = (uint32_t)(PAIR ? kCols / 2 : a.A) * kFfRowBytes;
     p.stage_bytes = SUB * (kFfWBytes + p.b_bytes + (MX ? 4 * kSfAtom : 0));
     constexpr uint32_t kSmemMax = 232448;

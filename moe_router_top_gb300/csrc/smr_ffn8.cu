@@ -13,7 +13,7 @@
 // from shared memory by all threads, and these reads bound the kernel (16384
 // tokens, gated product: 787 us). So here the routed rows are the MMA's rows: a
 // thread of the epilogue holds one row, its scale is one register, and a weight
-// tile's is the same for all (467 us, 1.77 PFLOP/s).
+// tile's is the same for all (467 us, 1.77 PFLOP/s, in CTA pairs).
 //
 // What bounds that (us for the gated product of 16384 tokens, parts taken out in
 // turn): the chain from an accumulator's MMAs over the signals between the CTAs
@@ -26,6 +26,9 @@
 // for every accumulator (536), copies that a warp waits for and makes visible
 // before it announces them (531), the stages handed back by the epilogue (463,
 // the second product 25 longer).
+#include "smr_fp8.cuh"
+#include "smr_launch.h"
+
 // Registers of the kernel of the other formats. Blocks of 64 rows, 112: they
 // leave 8192 for a block of the sum or of the quantisation that follows, which
 // reads the align's outputs meanwhile (the decode shape, 8 tokens: second
@@ -33,26 +36,39 @@
 // tokens 62 instead of 56).
 #define FFN_BOUNDS __maxnreg__(SUB == 2 ? 112 : 128)
 #include "smr_ffn.cuh"
-#include "smr_fp8.cuh"
 
 namespace smr {
 
-// A piece of work: up to 256 routed rows (blocks of one expert together) and two
-// weight tiles for a CTA pair; either CTA holds half of the rows and half of
-// each tile. 16 warps: 0 and 1 issue the MMAs of either tile, 2 scout, 3
-// scales, 4 to 7 load the routed rows and the weights (two warps every other stage), the last 8
-// are the epilogue, two for each quarter of TMEM's lanes, one of these for
-// either tile.
-constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4, kRowScales = 4;
-constexpr int kRowStageBytes = 2 * kFfWBytes;
+// A piece of work: two weight tiles and up to 128 routed rows (blocks of one
+// expert together) for a CTA, or up to 256 for a CTA pair, where either CTA holds
+// half of the rows and half of each tile. 16 warps: 0 and 1 issue the MMAs of
+// either tile, 2 scout, 3 scales, 4 to 7 load the routed rows and the weights
+// (two warps every other stage), the last 8 are the epilogue, two for each
+// quarter of TMEM's lanes, one of these for either tile.
+constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4;
+template <bool PAIR>
+constexpr int kRowStageBytes = (PAIR ? 2 : 3) * kFfWBytes;  // [rows][the first tile, or half of it][the second]
 constexpr int kRowScaleBytes = kFp8Group * 128 * 8;  // [k-block][row] (two products of scales)
-constexpr int kRowBars = 3 * kFfMaxStages + 2 * kRowAccs + 2 * kRowInfos + 2 * kRowScales + 1;
-constexpr int kRowBarBytes = (kRowBars * 8 + 8 + 15) / 16 * 16;
 // The epilogue's outputs leave through shared memory, 128 bytes of 32 rows a
-// warp at a time, so that rows are written in whole lines.
-constexpr int kRowOutBytes = 8 * 32 * 128;
-constexpr int kRowMiscBytes = kRowBarBytes + kRowInfos * (int)sizeof(FfInfo<256>) + kRowScales * kRowScaleBytes +
-                              kRowOutBytes + 2 * 128 * 4;
+// warp at a time, so that rows are written in whole lines. Where that leaves
+// three stages only, the gated product of single CTAs, it is 16 rows, and the
+// ring of scales is half as long: four stages (4096 tokens: 152 us, with three
+// 157; the second product, with twice the outputs, takes 127 instead of 125).
+template <bool UP, bool PAIR>
+constexpr bool kRowLean = UP && !PAIR;
+template <bool UP, bool PAIR>
+constexpr int kRowScales = kRowLean<UP, PAIR> ? 2 : 4;
+template <bool UP, bool PAIR>
+constexpr int kRowOutRows = kRowLean<UP, PAIR> ? 16 : 32;
+template <bool UP, bool PAIR>
+constexpr int kRowOutBytes = 8 * kRowOutRows<UP, PAIR> * 128;
+template <bool UP, bool PAIR>
+constexpr int kRowBars = 3 * kFfMaxStages + 2 * kRowAccs + 2 * kRowInfos + 2 * kRowScales<UP, PAIR> + 1;
+template <bool UP, bool PAIR>
+constexpr int kRowBarBytes = (kRowBars<UP, PAIR> * 8 + 8 + 15) / 16 * 16;
+template <bool UP, bool PAIR>
+constexpr int kRowMiscBytes = kRowBarBytes<UP, PAIR> + kRowInfos * (int)sizeof(FfInfo<PAIR ? 256 : 128>) +
+                              kRowScales<UP, PAIR> * kRowScaleBytes + kRowOutBytes<UP, PAIR> + 2 * 128 * 4;
 
 // What a weight's load into shared memory takes, with room to spare (0.5 ms).
 constexpr long long kRowDrainCycles = 1ll << 20;
@@ -60,19 +76,24 @@ constexpr long long kRowDrainCycles = 1ll << 20;
 enum RowOut : int { kRowBf16 = 0, kRowF32 = 1, kRowE4m3 = 2 };
 
 // The four MMAs of a k-block (K = 32 each), the first over what D holds.
+#define ROW_MMAS(group)                                                              \
+    asm volatile(                                                                    \
+        "{\n .reg .pred p;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"                    \
+        " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"            \
+        " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"            \
+        " setp.ne.b32 p, 0, 0;\n"                                                    \
+        " tcgen05.mma.cta_group::" group ".kind::f8f6f4 [%0], %1, %2, %3, p;\n"      \
+        " setp.eq.b32 p, 0, 0;\n"                                                    \
+        " tcgen05.mma.cta_group::" group ".kind::f8f6f4 [%0], a1, b1, %3, p;\n"      \
+        " tcgen05.mma.cta_group::" group ".kind::f8f6f4 [%0], a2, b2, %3, p;\n"      \
+        " tcgen05.mma.cta_group::" group ".kind::f8f6f4 [%0], a3, b3, %3, p;\n}"     \
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory")
+template <bool PAIR>
 __device__ __forceinline__ void mma_k_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-    asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
-        " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
-        " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
-        " setp.ne.b32 p, 0, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        " setp.eq.b32 p, 0, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, p;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, p;\n"
-        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, p;\n}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc) : "memory");
+    if constexpr (PAIR) ROW_MMAS("2");
+    else ROW_MMAS("1");
 }
+#undef ROW_MMAS
 // Arrivals where `yes` (no branch: a warp that splits here is late for the rest).
 __device__ __forceinline__ void arrive_if(uint32_t bar, bool yes) {
     asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}"
@@ -115,28 +136,31 @@ __device__ __forceinline__ bool meet_two_if(int id, bool ok) {
     return all != 0;
 }
 
-// 128 bytes of every lane's row (8 pieces of 16) to the warp's buffer, then out
-// in whole lines: out[r] is row r's address, nullptr: none; bytes: how much of
+// 128 bytes of every lane's row (8 pieces of 16) to the warp's buffer, ROWS rows
+// at a time, then out in whole lines: out[r] is row r's address, nullptr: none; bytes: how much of
 // the 128 there is.
+template <int ROWS>
 __device__ __forceinline__ void put_row_lines(uint32_t buffer, const uint32_t (&v)[32], uint8_t *out, int bytes) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, c = lane & 7;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                     ::"r"(buffer + (uint32_t)(lane * 128 + ((c ^ (lane & 7)) << 4))), "r"(v[4 * c]), "r"(v[4 * c + 1]),
-                       "r"(v[4 * c + 2]), "r"(v[4 * c + 3]) : "memory");
-    __syncwarp();
-    const int c = lane & 7;
+    for (int from = 0; from < 32; from += ROWS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 3);
-        uint4 w;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                     : "r"(buffer + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4))) : "memory");
-        uint8_t *to = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r));
-        if (to != nullptr && 16 * c < bytes) *reinterpret_cast<uint4 *>(to + 16 * c) = w;
+        for (int i = 0; i < 8; ++i)
+            asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %5, %6;\n @p st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n}"
+                         ::"r"(buffer + (uint32_t)(lane % ROWS * 128 + ((i ^ (lane & 7)) << 4))), "r"(v[4 * i]), "r"(v[4 * i + 1]),
+                           "r"(v[4 * i + 2]), "r"(v[4 * i + 3]), "r"(lane / ROWS * ROWS), "r"(from) : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < ROWS / 4; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(buffer + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4))) : "memory");
+            uint8_t *to = reinterpret_cast<uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), from + r));
+            if (to != nullptr && 16 * c < bytes) *reinterpret_cast<uint4 *>(to + 16 * c) = w;
+        }
+        __syncwarp();
     }
-    __syncwarp();
 }
 
 // A row's 128 columns times g and u (16 and 16 in turn), added to d; the last
@@ -254,15 +278,17 @@ __device__ __forceinline__ void swiglu4(const float (&g)[4], const float (&u)[4]
     a[3] *= n[3] * (r23 * d[2]);
 }
 
-template <bool UP, int OUT>
+template <bool UP, int OUT, bool PAIR>
 __global__ void __launch_bounds__(kRowThreads, 1)
 expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
-    using Info = FfInfo<256>;
+    using Info = FfInfo<PAIR ? 256 : 128>;
+    constexpr int kCtas = PAIR ? 2 : 1, kStageBytes = kRowStageBytes<PAIR>, kTileBytes = kFfWBytes / kCtas,  // (of a weight tile here)
+                  kScaleRing = kRowScales<UP, PAIR>, kBars = kRowBarBytes<UP, PAIR>, kOutBuffer = kRowOutRows<UP, PAIR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     const int ST = p.stages;
-    uint8_t *misc = smem + (size_t)ST * kRowStageBytes;
+    uint8_t *misc = smem + (size_t)ST * kStageBytes;
     // full and acc_empty are the leader's, the others each CTA's own
     uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // the weights landed, and the other CTA's rows
     uint64_t *empty = full + kFfMaxStages;
@@ -272,32 +298,32 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     uint64_t *info_full = acc_empty + kRowAccs;
     uint64_t *info_empty = info_full + kRowInfos;
     uint64_t *scale_full = info_empty + kRowInfos;
-    uint64_t *scale_empty = scale_full + kRowScales;
-    uint64_t *last = scale_empty + kRowScales;
+    uint64_t *scale_empty = scale_full + kScaleRing;
+    uint64_t *last = scale_empty + kScaleRing;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(last + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    Info *info = reinterpret_cast<Info *>(misc + kRowBarBytes);
-    float2 *scale_ring = reinterpret_cast<float2 *>(misc + kRowBarBytes + kRowInfos * sizeof(Info));
-    uint8_t *out_rows = misc + kRowBarBytes + kRowInfos * sizeof(Info) + kRowScales * kRowScaleBytes;
-    uint32_t *amax_ex = reinterpret_cast<uint32_t *>(out_rows + kRowOutBytes);  // [2][128]
+    Info *info = reinterpret_cast<Info *>(misc + kBars);
+    float2 *scale_ring = reinterpret_cast<float2 *>(misc + kBars + kRowInfos * sizeof(Info));
+    uint8_t *out_rows = misc + kBars + kRowInfos * sizeof(Info) + kScaleRing * kRowScaleBytes;
+    uint32_t *amax_ex = reinterpret_cast<uint32_t *>(out_rows + kRowOutBytes<UP, PAIR>);  // [2][128]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(smem_u32(&full[s]), 2);
+            mbar_init(smem_u32(&full[s]), kCtas);
             mbar_init(smem_u32(&rows_full[s]), 16 * kRowLoaders);
             mbar_init(smem_u32(&empty[s]), 2);  // either tile's MMAs
         }
         for (int s = 0; s < kRowAccs; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
-            mbar_init(smem_u32(&acc_empty[s]), kFfDrains);  // one tile's four warps of both CTAs
+            mbar_init(smem_u32(&acc_empty[s]), kCtas * kFfDrains / 2);  // one tile's four warps (of both CTAs)
         }
         for (int s = 0; s < kRowInfos; ++s) {
             mbar_init(smem_u32(&info_full[s]), 1);
             mbar_init(smem_u32(&info_empty[s]), 3 + kRowLoaders + kFfDrains);  // every warp but the scout
         }
-        for (int s = 0; s < kRowScales; ++s) {
+        for (int s = 0; s < kScaleRing; ++s) {
             mbar_init(smem_u32(&scale_full[s]), 1);
             mbar_init(smem_u32(&scale_empty[s]), kFfDrains);
         }
@@ -307,18 +333,23 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         prefetch_tensormap(&tm_w);
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_u32(tmem_slot), 512u);
-        tmem_relinquish_pair();
+        if constexpr (PAIR) {
+            tmem_alloc_pair(smem_u32(tmem_slot), 512u);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_slot), 512u);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    if constexpr (PAIR) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();  // the align's outputs and x come from previous kernels
     griddep_launch_dependents();
 
-    const uint32_t ring = smem_u32(smem);  // a stage: [rows][64 rows of the first tile][64 of the second]
+    const uint32_t ring = smem_u32(smem);
     // A thread of the epilogue holds 128 sums: its 8 warps get registers of the
     // other 8 (256 x 64 + 256 x 192 = the 512 x 128 of the launch, which the
     // launcher makes sure of).
@@ -332,7 +363,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             // without any work in between, a tile's MMAs 256; and a k-block's
             // waits, issue and commits take a warp 600.)
             const bool elected = elect_one();
-            const uint32_t idesc = idesc_e4m3(2 * kFfRows, 128);
+            const uint32_t idesc = idesc_e4m3(kCtas * kFfRows, 128);
             RingPos st, iq, ac;
             bool ok = true;
             while (ok) {
@@ -363,17 +394,17 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
                     if (!(ok = warp_wait(&acc_empty[2 * ac.i + warp], ac.ph ^ 1u, abort_flag))) break;
                     tc_fence_after();
-                    const uint32_t base = ring + (uint32_t)(st.i * kRowStageBytes), acc = tmem + (uint32_t)((2 * ac.i + warp) * 128);
-                    const uint64_t da = smem_desc_sw<128>(base), db = smem_desc_sw<128>(base + kFfWBytes + warp * (kFfWBytes / 2));
+                    const uint32_t base = ring + (uint32_t)(st.i * kStageBytes), acc = tmem + (uint32_t)((2 * ac.i + warp) * 128);
+                    const uint64_t da = smem_desc_sw<128>(base), db = smem_desc_sw<128>(base + kFfWBytes + warp * kTileBytes);
                     const int steps = kb + 1 == p.num_kb ? p.last_steps : 4;
                     if (elected) {
                         if (steps == 4) {
-                            mma_k_block(acc, da, db, idesc);
+                            mma_k_block<PAIR>(acc, da, db, idesc);
                         } else {
-                            for (int kk = 0; kk < steps; ++kk) tc_mma_e4m3<true>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                            for (int kk = 0; kk < steps; ++kk) tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
                         }
-                        ff_commit<true>(done);
-                        ff_commit<true>(&empty[st.i]);
+                        ff_commit<PAIR>(done);
+                        ff_commit<PAIR>(&empty[st.i]);
                     }
                     st.next(ST);
                     ac.next(2);
@@ -381,13 +412,16 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             }
             // every MMA issued is done before TMEM is freed, also after an abort
             if (rank == 0) {
-                if (elected) tc_commit_pair(smem_u32(last), 0x1);
+                if (elected) {
+                    if constexpr (PAIR) tc_commit_pair(smem_u32(last), 0x1);
+                    else tc_commit(smem_u32(last));
+                }
                 volatile int never = 0;
                 if (!mbar_wait_bounded(smem_u32(last), 0u, &never)) *abort_flag = 1;
             }
             __syncwarp();
         } else if (warp == 2) {
-            ff_scout<UP, true, 256, kRowInfos, 2>(p, info, info_full, info_empty, abort_flag, rank);
+            ff_scout<UP, true, 128 * kCtas, kRowInfos, 2, kCtas>(p, info, info_full, info_empty, abort_flag, rank);
             __syncwarp();
         } else if (warp == 3) {
             // ------------------------------------------------- scales ----
@@ -402,7 +436,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 const Info *inf = info + iq.i;
                 const int all = inf->n;
                 if (all >= 0) {
-                    const int n = all / 2, tile = inf->nt & ~1;
+                    const int n = all / kCtas, tile = inf->nt & ~1;
                     int row[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) row[j] = lane + 32 * j < n ? inf->row[(int)rank * n + lane + 32 * j] : -1;
@@ -446,7 +480,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&scale_full[sc.i]));
-                        sc.next(kRowScales);
+                        sc.next(kScaleRing);
                     }
                 }
                 __syncwarp();
@@ -478,24 +512,30 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 const Info *inf = info + iq.i;
                 const int all = inf->n;
                 if (all >= 0) {
-                    const int n = all / 2;  // this CTA's rows of the item
+                    const int n = all / kCtas;  // this CTA's rows of the item
                     int row[16];  // -1: none
 #pragma unroll
                     for (int i = 0; i < 16; ++i) row[i] = r0 + 4 * i < n ? inf->row[(int)rank * n + r0 + 4 * i] : -1;
                     const int nt = inf->nt & ~1, e = inf->e;
                     for (; next < p.num_kb; next += 2) {
                         if (!(ok = warp_wait(&empty[st.i], st.ph ^ 1u, abort_flag))) break;
-                        const uint32_t base = (uint32_t)(st.i * kRowStageBytes);
+                        const uint32_t base = (uint32_t)(st.i * kStageBytes);
                         if (weights && elected) {
-                            const uint32_t bar = smem_u32(&full[st.i]), fb = cluster_addr(bar, 0u);
-                            // both CTAs' bytes complete the leader's barrier
+                            const uint32_t bar = smem_u32(&full[st.i]);
+                            // (both CTAs' bytes complete the leader's barrier)
                             if (rank == 0) mbar_arrive_expect_tx(bar, 2 * kFfWBytes);
-                            // this CTA's half of either tile: the first CTA's is the tile's first 64 rows
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const uint32_t to = ring + base + (uint32_t)(kFfWBytes + h * (kFfWBytes / 2));
-                                if constexpr (UP) tma_load_5d_pair(to, &tm_w, next * kFfRowBytes, 4 * (nt + h) + 2 * (int)rank, e, fb);
-                                else tma_load_3d_pair(to, &tm_w, next * kFfRowBytes, kFfRows * (nt + h) + 64 * (int)rank, e, fb);
+                                const uint32_t to = ring + base + (uint32_t)(kFfWBytes + h * kTileBytes);
+                                if constexpr (PAIR) {
+                                    // this CTA's half of either tile: the first CTA's is the tile's first 64 rows
+                                    const uint32_t fb = cluster_addr(bar, 0u);
+                                    if constexpr (UP) tma_load_5d_pair(to, &tm_w, next * kFfRowBytes, 4 * (nt + h) + 2 * (int)rank, e, fb);
+                                    else tma_load_3d_pair(to, &tm_w, next * kFfRowBytes, kFfRows * (nt + h) + 64 * (int)rank, e, fb);
+                                } else {
+                                    if constexpr (UP) tma_load_5d(to, &tm_w, next * kFfRowBytes, 4 * (nt + h), e, bar);
+                                    else tma_load_3d(to, &tm_w, next * kFfRowBytes, kFfRows * (nt + h), e, bar);
+                                }
                             }
                         }
                         weights = !weights;
@@ -531,10 +571,10 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         const uint32_t at = smem_u32(misc);
         constexpr uint32_t kAccFull = 24 * kFfMaxStages, kAccEmpty = kAccFull + 8 * kRowAccs, kInfoFull = kAccEmpty + 8 * kRowAccs,
                            kInfoEmpty = kInfoFull + 8 * kRowInfos, kScaleFull = kInfoEmpty + 8 * kRowInfos,
-                           kScaleEmpty = kScaleFull + 8 * kRowScales, kAbort = kScaleEmpty + 8 * kRowScales + 12,
-                           kInfo = kRowBarBytes, kScales = kInfo + kRowInfos * (uint32_t)sizeof(Info),
-                           kOutRows = kScales + kRowScales * kRowScaleBytes;
-        const uint32_t hand_back = cluster_addr(at + kAccEmpty + 8u * half, 0u);
+                           kScaleEmpty = kScaleFull + 8 * kScaleRing, kAbort = kScaleEmpty + 8 * kScaleRing + 12,
+                           kInfo = kBars, kScales = kInfo + kRowInfos * (uint32_t)sizeof(Info),
+                           kOutRows = kScales + kScaleRing * kRowScaleBytes;
+        const uint32_t hand_back = PAIR ? cluster_addr(at + kAccEmpty + 8u * half, 0u) : at + kAccEmpty + 8u * half;
         const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + 128u * half, scales = at + kScales + 8u * (q * 32 + lane) + (UP ? 0u : 4u * half);
         uint32_t items = 0, groups = 0, units = 0;
         while (true) {
@@ -549,7 +589,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             // and the ring hold: leaving it would cost copies of the sums.)
             float g = 0.0f, u = 0.0f;
             const auto read_scales = [&](int kb) {
-                const uint32_t from_s = scales + (groups & (kRowScales - 1)) * kRowScaleBytes + (kb & (kFp8Group - 1)) * 1024u;
+                const uint32_t from_s = scales + (groups & (kScaleRing - 1)) * kRowScaleBytes + (kb & (kFp8Group - 1)) * 1024u;
                 if constexpr (UP) {
                     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(g), "=f"(u) : "r"(from_s) : "memory");
                 } else {
@@ -558,7 +598,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 }
             };
             if (more) {
-                ok &= warp_wait_at(at + kScaleFull + 8 * (groups & (kRowScales - 1)), groups / kRowScales & 1u, at + kAbort);
+                ok &= warp_wait_at(at + kScaleFull + 8 * (groups & (kScaleRing - 1)), groups / kScaleRing & 1u, at + kAbort);
                 read_scales(0);
             }
 #pragma unroll 1
@@ -569,14 +609,15 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                 const float g0 = g, u0 = u;
                 add_columns(sum, last, from + 256u * (units & 1u), g0, u0);
                 tc_fence_before();
-                arrive_cluster_if(hand_back + 16u * (units & 1u), lane == 0);
+                if constexpr (PAIR) arrive_cluster_if(hand_back + 16u * (units & 1u), lane == 0);
+                else arrive_if(hand_back + 16u * (units & 1u), lane == 0);
                 ++units;
                 ++kb;
                 if ((kb & (kFp8Group - 1)) == 0 || kb == p.num_kb) {
-                    arrive_if(at + kScaleEmpty + 8 * (groups & (kRowScales - 1)), lane == 0);
+                    arrive_if(at + kScaleEmpty + 8 * (groups & (kScaleRing - 1)), lane == 0);
                     ++groups;
                     if (kb < p.num_kb)
-                        ok &= warp_wait_at(at + kScaleFull + 8 * (groups & (kRowScales - 1)), groups / kRowScales & 1u, at + kAbort);
+                        ok &= warp_wait_at(at + kScaleFull + 8 * (groups & (kScaleRing - 1)), groups / kScaleRing & 1u, at + kAbort);
                 }
                 read_scales(kb);
 #pragma unroll
@@ -584,9 +625,9 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             }
             if constexpr (OUT == kRowE4m3) ok = meet_two_if(1 + q, ok);  // both warps of a row go on, or none does
             if (!ok || !more) break;
-            const int r = q * 32 + lane, n = lds_int(inf) / 2, tile = (lds_int(inf + 4) & ~1) + half;
+            const int r = q * 32 + lane, n = lds_int(inf) / kCtas, tile = (lds_int(inf + 4) & ~1) + half;
             const int slot = r < n ? lds_int(inf + 16 + 4 * ((int)rank * n + r)) : -1;
-            const uint32_t buffer = at + kOutRows + (uint32_t)((OUT == kRowE4m3 ? q : warp - 8) * 32 * 128);
+            const uint32_t buffer = at + kOutRows + (uint32_t)(OUT == kRowE4m3 ? q * 32 * 128 : (warp - 8) * kOutBuffer * 128);
             if constexpr (UP) {
                 const int f = tile * 64;
                 uint32_t o[32];
@@ -603,7 +644,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     }
                 if constexpr (OUT == kRowBf16) {
                     uint8_t *to = slot >= 0 ? static_cast<uint8_t *>(p.out) + ((int64_t)slot * p.feat + f) * 2 : nullptr;
-                    put_row_lines(buffer, o, to, 2 * max(p.feat - f, 0));
+                    put_row_lines<kOutBuffer>(buffer, o, to, 2 * max(p.feat - f, 0));
                 } else {
                     // the block of 128 features is both tiles': the largest
                     // magnitude over both, then this tile's 64 codes beside
@@ -652,7 +693,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         else o[j] = pack_bf16x2(sum[kPer * c + 2 * j], sum[kPer * c + 2 * j + 1]);
                     const int f = tile * 128 + kPer * c;
                     uint8_t *to = slot >= 0 ? static_cast<uint8_t *>(p.out) + ((int64_t)slot * p.feat + f) * (128 / kPer) : nullptr;
-                    put_row_lines(buffer, o, to, max(p.feat - f, 0) * (128 / kPer));
+                    put_row_lines<kOutBuffer>(buffer, o, to, max(p.feat - f, 0) * (128 / kPer));
                 }
             }
             __syncwarp();
@@ -673,14 +714,15 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     }
     // no barrier of either CTA can still be signalled, both are done with TMEM
     __syncwarp();
-    cluster_sync();
+    if constexpr (PAIR) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 512u);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, 512u);
+        else tmem_dealloc(tmem, 512u);
     }
 }
 
-template <bool UP, int OUT>
+template <bool UP, int OUT, bool PAIR>
 static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream) {
     FfParams p{};
     p.num_kb = (a.K + 127) / 128;
@@ -697,29 +739,29 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
     const uintptr_t scales_at = reinterpret_cast<uintptr_t>(a.x_scales) | (uintptr_t)(4 * p.num_kb);
     p.scale_bytes = scales_at % 16 == 0 ? 16 : (scales_at % 8 == 0 ? 8 : 4);
     constexpr uint32_t kSmemMax = 232448;
-    p.stages = (int)((kSmemMax - 1024 - kRowMiscBytes) / kRowStageBytes);
+    p.stages = (int)((kSmemMax - 1024 - kRowMiscBytes<UP, PAIR>) / kRowStageBytes<PAIR>);
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
-    const size_t smem = 1024 + (size_t)p.stages * kRowStageBytes + kRowMiscBytes;
+    const size_t smem = 1024 + (size_t)p.stages * kRowStageBytes<PAIR> + kRowMiscBytes<UP, PAIR>;
     CUtensorMap mw;
-    if (!encode_weight(&mw, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint64_t)a.K, (cuuint64_t)a.K, kFfRowBytes, kFfRows / 2))
+    if (!encode_weight(&mw, a, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint64_t)a.K, (cuuint64_t)a.K, kFfRowBytes, PAIR ? kFfRows / 2 : kFfRows))
         return cudaErrorInvalidValue;
 
     static std::atomic<bool> configured[kMaxDevices];
     const cudaError_t e = once_per_device(configured, [](int) {
         cudaFuncAttributes at;
-        cudaError_t r = cudaFuncGetAttributes(&at, expert_rows_kernel<UP, OUT>);
+        cudaError_t r = cudaFuncGetAttributes(&at, expert_rows_kernel<UP, OUT, PAIR>);
         // (with fewer registers at launch the epilogue's wait for more would never end)
         if (r == cudaSuccess && at.numRegs != 128) r = cudaErrorNotSupported;
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(expert_rows_kernel<UP, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+            r = cudaFuncSetAttribute(expert_rows_kernel<UP, OUT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(expert_rows_kernel<UP, OUT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+            r = cudaFuncSetAttribute(expert_rows_kernel<UP, OUT, PAIR>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                      cudaSharedmemCarveoutMaxShared);
         return r;
     });
     if (e != cudaSuccess) return e;
-    const int64_t most = (int64_t)p.max_blocks * ((p.ntiles + 1) / 2 * 2);
-    const int room = sms / 2 * 2;
+    const int64_t most = (int64_t)p.max_blocks * ((p.ntiles + 1) / 2 * (PAIR ? 2 : 1));
+    const int room = PAIR ? sms / 2 * 2 : sms;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(most < room ? most : room), 1, 1);
     cfg.blockDim = dim3(kRowThreads, 1, 1);
@@ -733,36 +775,49 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, expert_rows_kernel<UP, OUT>, mw, p);
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, expert_rows_kernel<UP, OUT, PAIR>, mw, p);
 }
 
-// From this many rows an expert, on average, the routed rows are the MMA's rows:
-// an item then costs the same for 16 rows as for 256, but its scales are one
-// register. The gated product in us on the device, evenly spread and skewed
-// (128 experts, tokens of 8 slots; weights as rows, in pairs / routed rows):
-// 1024 tokens (64 rows) 101 and 112 / 119 and 119, 1536 tokens (96 rows) 117 and
-// 133 / 119 and 129, 2048 tokens 159 and 159 / 120 and 139, 4096 tokens 266 and
-// 256 / 166 and 179; the second product 69 and 76 / 77 and 83, 81 and 91 / 82
-// and 91, 107 and 109 / 86 and 99, 181 and 180 / 133 and 139. (Pairs against
-// single CTAs at 768 tokens, 48 rows: 91 and 101 / 92 and 111, second product
-// 62 and 68 / 60 and 72.)
-constexpr int kRowsPerExpert = 96;
+// From this many rows an expert, on average, the routed rows are the MMA's rows.
+// An item then costs the same for 16 rows as for 128, but its scales are one
+// register. H 2048, 128 experts, top-8, I 768; the gated product in us on the
+// device, evenly spread and skewed (weights as the MMA's rows / routed rows): 512
+// tokens (32 rows) 70 and 80 / 81 and 81, 768 tokens (48) 93 and 107 / 81 and
+// 83, 1536 tokens 125 and 140 / 86 and 103; the second product 56 and 63 / 64
+// and 68, 58 and 65 / 52 and 56, 77 and 86 / 62 and 73.
+constexpr int kRowsPerExpert = 48;
 bool expert_rows_fp8(int64_t numel, int num_experts) { return numel >= (int64_t)kRowsPerExpert * num_experts; }
+
+// And from this many a CTA pair takes up to 256 of them: each CTA then loads half
+// of the weight tiles, but pieces of 128 rows leave half of its lanes idle and
+// the signals between the CTAs take their time (pairs / single CTAs, us: the gated
+// product of 4096 tokens, 256 rows, 166 and 179 / 152 and 157, 8192 tokens 271
+// and 268 / 261 and 261, 12000 tokens 344 and 360 / 360 and 367, 16384 tokens 468
+// and 466 / 480 and 477; the second product of 4096 tokens 133 and 137 / 126 and
+// 129, 6000 tokens 175 and 175 / 169 and 172, 8192 tokens 224 and 224 / 228 and
+// 227, 16384 tokens 407 and 405 / 428 and 426).
+template <bool UP>
+constexpr int kRowPairsPerExpert = UP ? 640 : 448;
+
+template <bool UP, int OUT>
+static cudaError_t launch_rows_of(const FfnLaunch &a, int sms, cudaStream_t stream) {
+    return a.numel >= (int64_t)kRowPairsPerExpert<UP> * a.num_experts ? launch_rows<UP, OUT, true>(a, sms, stream)
+                                                                       : launch_rows<UP, OUT, false>(a, sms, stream);
+}
 
 template <bool UP, bool F32>
 static cudaError_t launch_columns(const FfnLaunch &a, int sms, cudaStream_t stream) {
-    if (expert_pairs(a.numel, a.num_experts)) return launch_product<false, UP, true, 1, F32, true>(a, sms, stream);
     return a.A == 64 ? launch_product<false, UP, false, 2, F32, true>(a, sms, stream)
                      : launch_product<false, UP, false, 1, F32, true>(a, sms, stream);
 }
 
 cudaError_t launch_expert_product_fp8(const FfnLaunch &a, int sms, cudaStream_t stream) {
     const bool rows = expert_rows_fp8(a.numel, a.num_experts);
-    if (a.out_scales) return rows && a.gated ? launch_rows<true, kRowE4m3>(a, sms, stream) : cudaErrorNotSupported;
-    if (a.gated) return rows ? launch_rows<true, kRowBf16>(a, sms, stream) : launch_columns<true, false>(a, sms, stream);
-    if (a.out32) return rows ? launch_rows<false, kRowF32>(a, sms, stream) : launch_columns<false, true>(a, sms, stream);
-    return rows ? launch_rows<false, kRowBf16>(a, sms, stream) : launch_columns<false, false>(a, sms, stream);
+    if (a.out_scales) return rows && a.gated ? launch_rows_of<true, kRowE4m3>(a, sms, stream) : cudaErrorNotSupported;
+    if (a.gated) return rows ? launch_rows_of<true, kRowBf16>(a, sms, stream) : launch_columns<true, false>(a, sms, stream);
+    if (a.out32) return rows ? launch_rows_of<false, kRowF32>(a, sms, stream) : launch_columns<false, true>(a, sms, stream);
+    return rows ? launch_rows_of<false, kRowBf16>(a, sms, stream) : launch_columns<false, false>(a, sms, stream);
 }
 
 }  // namespace smr

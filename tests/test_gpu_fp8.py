@@ -155,7 +155,7 @@ SHAPES = [
     (2500, 128, 96, 6, 1, 3, 64, 0.0),
     (4000, 416, 224, 5, 0, 2, 128, 0.0),  # pairs of CTAs: whole and partial tiles and k-blocks
     (3000, 288, 352, 4, 1, 1, 64, 1.1),   # pairs, an odd number of weight tiles, groups of blocks
-    (90, 640, 384, 3, 0, 2, 64, 0.0),     # pairs with the weights as rows: 48 to 96 rows an expert
+    (90, 640, 384, 3, 0, 2, 64, 0.0),     # routed rows as the MMA's, single CTAs
     (170, 416, 224, 5, 0, 2, 128, 0.0),
     (230, 288, 352, 4, 1, 1, 64, 1.1),
     (2000, 1152, 768, 4, 0, 2, 128, 0.0),
@@ -221,9 +221,9 @@ def test_quantized_act_is_that_of_two_calls(smr, shape):
     assert torch.equal(codes, c) and torch.equal(scales, s)
 
 
-# what runs for 50, 150 and 400 tokens of three slots over seven experts: single
-# CTAs, pairs with the weights as rows, pairs with the routed rows as rows
-REGIMES = [50, 150, 400]
+# tokens of three slots over seven experts: the routed rows as the MMA's columns,
+# as its rows (twice), the same in CTA pairs
+REGIMES = [50, 150, 400, 2000]
 
 
 def _case(smr, T, H=256, I=160, E=6, S=1, k=2, seed=3):
@@ -366,7 +366,7 @@ def test_corrupted_align_outputs(smr, T):
             assert torch.equal(out, ref if n > 0 else torch.zeros_like(out))
 
 
-@pytest.mark.parametrize("T", [50, 400])
+@pytest.mark.parametrize("T", [50, 400, 2000])
 def test_captured_and_replayed(smr, T):
     """Graphs without workspaces of their own on two streams at once, with new inputs, next to eager calls."""
     cases = [_case(smr, T, seed=s) for s in (5, 6)]
@@ -410,7 +410,7 @@ def test_other_streams(smr):
 
 @pytest.mark.parametrize("K", [128, 256, 512, 288])
 @pytest.mark.parametrize("shift", [0, 1, 2])
-@pytest.mark.parametrize("T", [20, 150, 400])
+@pytest.mark.parametrize("T", [20, 150, 400, 2000])
 def test_scale_rows_of_any_alignment(smr, K, shift, T):
     """Rows of scales that can be read 16, 8 or only 4 bytes at a time."""
     ids, _, al, (x, xs), (w13, ws13), _ = _case(smr, T, H=K)
@@ -425,13 +425,14 @@ def test_scale_rows_of_any_alignment(smr, K, shift, T):
     _close(ref, *_ref_up(_row_values(x, xs), _weight_values(w13, ws13, True), ids, 3))
 
 
-@pytest.mark.parametrize("E", [1, 1025])
-def test_offsets_past_32_bits(smr, E):
-    """Codes, outputs and rows of more than 2^31 elements with the routed rows as the MMA's
-    rows (one expert), of more than 2^31 bytes with them as its columns (95 rows an expert)."""
-    T, I, H, A = 140000 if E == 1 else 98000, 16384, 32, 128
+@pytest.mark.parametrize("E,T", [(1, 140000), (1025, 98000), (1025, 49000)])
+def test_offsets_past_32_bits(smr, E, T):
+    """With the routed rows as the MMA's rows codes and outputs of more than 2^31 elements (pairs) and
+    more than 2^31 bytes (95 rows an expert); as its columns (47) of more than 2^30 bytes."""
+    I, H, A = 16384, 32, 128
     g = torch.Generator(device="cuda").manual_seed(1)
-    rows = torch.tensor([0, 1, 65535, 65536, T - 2, T - 1], device="cuda")
+    at = min(65536, T - 3)
+    rows = torch.tensor([0, 1, at - 1, at, T - 2, T - 1], device="cuda")
     real = min(E, 4)  # experts with weights
     if E == 1:
         ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
@@ -481,7 +482,7 @@ def test_launches_and_given_outputs(smr):
         codes, scales = torch.empty_like(ref[0]), torch.empty_like(ref[1])
         got = smr.expert_up(x.view(torch.float8_e4m3fn), w13.view(torch.float8_e4m3fn), *al, width=3, block_size=64,
                             x_scales=xs, w_scales=ws13, quantize_act=True, out=codes, act_scales=scales)
-        assert got[0] is codes and got[1] is scales and smr.last_launch_count() == (1 if T == 400 else 2)
+        assert got[0] is codes and got[1] is scales and smr.last_launch_count() == (2 if T == 50 else 1)
         assert torch.equal(codes, ref[0]) and torch.equal(scales, ref[1])
     with pytest.raises(ValueError, match="one device"):
         smr.expert_up(x, w13, *al, width=3, block_size=64, x_scales=xs, w_scales=ws13.cpu())
