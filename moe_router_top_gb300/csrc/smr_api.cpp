@@ -940,7 +940,7 @@ SMR_API smr_status smr_expert_down_fp32(const smr_expert_down_args *args, void *
 // Whether quantised activations pass through the workspace in bf16: with few
 // rows an expert a block of 128 features is not one CTA's.
 static bool up_fp8_through_bf16(const smr_expert_up_fp8_args *a) {
-    return a->act_scales && !smr::expert_rows_fp8((int64_t)a->num_tokens * a->width, a->num_experts);
+    return a->act_scales && !smr::expert_rows_fp8((int64_t)a->num_tokens * a->width, a->num_experts, a->block_size);
 }
 
 SMR_API size_t smr_expert_up_fp8_workspace_size(const smr_expert_up_fp8_args *args) {

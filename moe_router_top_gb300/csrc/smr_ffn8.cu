@@ -787,7 +787,14 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
 // 83, 1536 tokens 125 and 140 / 86 and 103; the second product 56 and 63 / 64
 // and 68, 58 and 65 / 52 and 56, 77 and 86 / 62 and 73.
 constexpr int kRowsPerExpert = 48;
-bool expert_rows_fp8(int64_t numel, int num_experts) { return numel >= (int64_t)kRowsPerExpert * num_experts; }
+// In blocks of 128 rows, where a stage of two k-blocks does not fit and its
+// columns take a turn each, from fewer (both products, the activations quantised
+// between them: 512 tokens 170 and 180 / 154 and 159, 128 tokens, 8 rows, 150 /
+// 147, 8 tokens of the decode shape 121 / 126).
+constexpr int kRowsPerExpert128 = 16;
+bool expert_rows_fp8(int64_t numel, int num_experts, int A) {
+    return numel >= (int64_t)(A == 128 ? kRowsPerExpert128 : kRowsPerExpert) * num_experts;
+}
 
 // And from this many a CTA pair takes up to 256 of them: each CTA then loads half
 // of the weight tiles, but pieces of 128 rows leave half of its lanes idle and
@@ -813,7 +820,7 @@ static cudaError_t launch_columns(const FfnLaunch &a, int sms, cudaStream_t stre
 }
 
 cudaError_t launch_expert_product_fp8(const FfnLaunch &a, int sms, cudaStream_t stream) {
-    const bool rows = expert_rows_fp8(a.numel, a.num_experts);
+    const bool rows = expert_rows_fp8(a.numel, a.num_experts, a.A);
     if (a.out_scales) return rows && a.gated ? launch_rows_of<true, kRowE4m3>(a, sms, stream) : cudaErrorNotSupported;
     if (a.gated) return rows ? launch_rows_of<true, kRowBf16>(a, sms, stream) : launch_columns<true, false>(a, sms, stream);
     if (a.out32) return rows ? launch_rows_of<false, kRowF32>(a, sms, stream) : launch_columns<false, true>(a, sms, stream);

@@ -130,6 +130,9 @@ def test_workspaces(lib):
     many = 48 * 65 // 11 + 1
     assert size(ctypes.byref(_up(act_scales=P, num_tokens=many))) == 256
     assert size(ctypes.byref(_up(act_scales=P, num_tokens=many - 1))) == ROWS + -(-(many - 1) * 11 * 128 * 2 // 256) * 256
+    few = 16 * 65 // 11 + 1  # in blocks of 128 rows fewer
+    assert size(ctypes.byref(_up(act_scales=P, num_tokens=few, block_size=128))) == 256
+    assert size(ctypes.byref(_up(act_scales=P, num_tokens=few - 1, block_size=128))) > ROWS
     assert down(ctypes.byref(_down())) == ROWS + 4 * 11 * 256 * 4
     assert down(ctypes.byref(_down(num_tokens=4096))) == ROWS + 4096 * 11 * 256 * 2
     assert down(ctypes.byref(_down(num_tokens=4096, fp32_rows=1))) == ROWS + 4096 * 11 * 256 * 4
