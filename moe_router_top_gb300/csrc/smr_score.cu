@@ -15,7 +15,8 @@
 // itself is compared. With one, c is evaluated in 32 bits with a bound on its
 // error; where two choices that the bound does not tell apart would decide the
 // slots (about one row in 500), those that could be among them are evaluated
-// again in 64 bits, and where two groups would, the whole row is.
+// again in 64 bits, and where two groups would, the experts that count in their
+// values are (softmax scores beside a bias: the whole row).
 //
 // One warp per row. A group's experts lie on L lanes next to each other (groups
 // as many as the next power of two, L = 32 / groups): a lane holds pieces of V
@@ -159,6 +160,43 @@ __device__ __noinline__ int select_in_64_bits(const ScoreLaunch &p, int64_t row)
     return mine;
 }
 
+// Whether the group of this lane stays, its value in 64 bits: of the experts whose
+// choice in 32 bits reaches `from`. (2047 rows of 256 in 8 groups, sigmoids
+// beside a small bias: 7 us; with the whole row in 64 bits, which a few rows of
+// such a batch then need, 17. Not for softmax scores beside a bias, which
+// need the row's sum. Without a bias scores relative to the row's largest do.)
+template <int V, bool F32>
+__device__ __noinline__ bool group_stays_in_64_bits(const ScoreLaunch &p, int64_t row, int first, int end, float from, float top) {
+    const int lane = threadIdx.x & 31, L = 32 >> p.log_groups, g = lane / L;
+    double m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+        const int e = first + i / V * (L * V) + i % V;
+        if (e >= end) break;
+        const float x = load_logit<F32>(p, row, e), b = p.bias != nullptr ? load_bias(p, e) : 0.0f;
+        if ((p.bias != nullptr ? sigmoid_fast(x) + b : x) < from) continue;
+        const double t = exp_64(p.sigmoid ? -(double)x : (double)x - (double)top);
+        const double v = (p.sigmoid ? 1.0 / (1.0 + t) : t) + (double)b;
+        m2 = fmax(m2, fmin(m1, v));
+        m1 = fmax(m1, v);
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int o = L >> 1; o >= 1; o >>= 1) {
+        const double o1 = __shfl_xor_sync(0xffffffffu, m1, o), o2 = __shfl_xor_sync(0xffffffffu, m2, o);
+        m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+        m1 = fmax(m1, o1);
+    }
+    const double value = p.best == 2 ? m1 + m2 : m1;
+    int above = 0;
+#pragma unroll 1
+    for (int h = 0; h < p.groups; ++h) {
+        const double v = __shfl_sync(0xffffffffu, value, h * L);
+        above += v > value || (v == value && h < g);
+    }
+    return g < p.groups && above < p.kept;
+}
+
 // The order of n candidates (expert, logit; on entry in any order) in 64 bits:
 // slot j's on return in place j, for the first k of them. Rare and rolled up:
 // code that runs once a launch is fetched from far away.
@@ -192,11 +230,12 @@ __device__ __noinline__ void settle_in_64_bits(const ScoreLaunch &p, int64_t row
 }
 
 // Bound by its instructions for large batches (1170 a row of 512 experts in 8
-// groups as ncu counts them; 16384 rows take 25.3 us) and by latency for small
-// ones (4 rows of 512: 3.5 us); what it reads is the logits, once, in whole
-// sectors.
+// groups as ncu counts them; 16384 rows take 26.4 us) and by latency for small
+// ones (4 rows of 512: 3.7 us); what it reads is the logits, once, in whole
+// sectors. 16 logits a lane in pieces of four: three CTAs an SM (two, with the
+// registers that the compiler would take: 32.5 us).
 template <int NK, int V, bool F32>
-__global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const ScoreLaunch p) {
+__global__ void __launch_bounds__(32 * kScoreWarps, NK == 16 && V == 4 ? 3 : 1) select_experts_kernel(const ScoreLaunch p) {
     __shared__ __align__(16) uint32_t cand_u[kScoreWarps][32];  // choices, as unsigned numbers
     __shared__ float cand_x[kScoreWarps][32];                  // and their logits
     __shared__ float2 cand_s[kScoreWarps][2][32];              // (choice, expert) as collected; (expert, logit) in order
@@ -271,9 +310,12 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
     const float inv = __frcp_rn(den);
 
     // choices; without a bias the logits themselves, which have their order
-    // how far a choice in 32 bits may be off, twice: 4e-7 of a sigmoid, 2e-6
-    // of a softmax (its sum of up to ten roundings), half a unit of c itself
-    const float slack = p.bias == nullptr ? 0.0f : (soft ? 4e-6f : 8e-7f);
+    // How far a score in 32 bits may be off, twice: 4e-7 of a sigmoid. Of e =
+    // exp(-d), d below the row's largest, e (2^-22 + 2.5 d 2^-24), at most 3e-7;
+    // the sum's relative error is that averaged over the row (d ln N at most on
+    // average: 1.3e-6) and ten roundings, so a softmax is off by s (2.3e-6 +
+    // 1.5e-7 d), at most 2.5e-6 of the row's largest score, which is `inv`.
+    const float slack = soft ? (p.bias != nullptr ? 5e-6f * inv : 1e-6f) : 8e-7f;
     if (p.bias != nullptr) {
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
@@ -300,6 +342,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
             m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
             m1 = fmaxf(m1, o1);
         }
+        const float least_of = p.best == 2 ? m2 : m1;  // the least choice that counts
         float value = m1, mag = fabsf(m1);  // (mag: what its rounding goes by)
         if (p.best == 2) {
             if (p.bias == nullptr) {  // of logits: their scores
@@ -332,7 +375,12 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
             const uint32_t next = __reduce_max_sync(0xffffffffu, left);
             const float lo = unordered(low), hi = unordered(next);
             const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mag)));
-            unsure = next != 0u && !(lo - hi > 2.0f * (soft ? 4e-6f : 8e-7f) + 5e-7f * most);
+            unsure = next != 0u && !(lo - hi > 2.0f * slack + 5e-7f * most);
+        }
+        if (unsure && !(soft && p.bias != nullptr)) {  // (the same in all lanes)
+            unsure = false;
+            const float from = p.bias == nullptr ? least_of : least_of - (8e-7f + 2.5e-7f * fabsf(least_of));
+            stays = group_stays_in_64_bits<V, F32>(p, row, first, end, from, top);
         }
         if (!stays) {
 #pragma unroll
@@ -517,7 +565,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) select_experts_kernel(const 
     float sum = slot ? n : 0.0f;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float w = (p.renorm ? n / sum : (soft ? n / den : n)) * p.routed_scale;
+    const float w = (p.renorm ? n / sum : n * inv) * p.routed_scale;  // (inv: 1 for sigmoids)
     const int width = p.k + p.S;
     if (slot) {
         p.ids[row * width + lane] = ej;
@@ -562,8 +610,8 @@ cudaError_t launch_select_experts(const ScoreLaunch &in, cudaStream_t stream) {
     const int single = (a.group_size + L - 1) / L;
     if (single > kScoreMaxPlaces) return cudaErrorNotSupported;
     // Four experts a load where groups and rows are made of whole aligned
-    // pieces of four (16384 x 512 in fp32: 25.3 us, one at a time 35.9; 2047 x
-    // 256 in bf16: 10.7 and 11.1).
+    // pieces of four (one at a time 16384 x 512 in fp32 take 1.4 times as long,
+    // 2047 x 256 in bf16 1.04 times).
     const int fours = (a.group_size + 4 * L - 1) / (4 * L) * 4, size = a.f32 ? 4 : 2;
     const bool wide = a.group_size % 4 == 0 && a.ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * size) == 0 &&
                       fours <= kScoreMaxPlaces;
