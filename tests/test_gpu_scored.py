@@ -305,3 +305,15 @@ def test_scored_align_sizes(smr, M):
     plain = smr.align(63 - ids, 64, 64)
     n = int(plain[2])
     assert int(mapped[4]) == n and torch.equal(mapped[2][:n], plain[0][:n]) and torch.equal(mapped[3][: n // 64], plain[1][: n // 64])
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("std", [None, 0.02, 1e-5])
+def test_many_rows_in_groups(smr, scoring, std):
+    """Enough rows that groups and slots closer than the bound in 32 bits are among them."""
+    logits, g = _logits(20000, 256, 21, std=1.0, dtype=torch.bfloat16)
+    bias = None if std is None else torch.randn(256, device="cuda", generator=g) * std
+    for kept, best, renorm in ((4, 2, True), (3, 1, False)):
+        _check(smr, logits, 8, scoring, bias, 8, kept, best, renorm, 2.5)
+    _check(smr, logits[:, :255].contiguous(), 8, scoring, None if bias is None else bias[:255], 5, 3, 2)  # 51 experts a group
+    _check(smr, logits, 8, scoring, bias)
