@@ -289,10 +289,10 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                                                 ~static_cast<uintptr_t>(1023));
     const int ST = p.stages;
     uint8_t *misc = smem + (size_t)ST * kStageBytes;
-    // full and acc_empty are the leader's, the others each CTA's own
-    uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // the weights landed, and the other CTA's rows
+    // full and acc_empty are the leader's, rows_full its peer's, the others each CTA's own
+    uint64_t *full = reinterpret_cast<uint64_t *>(misc);  // the weights and the rows landed, the peer's too
     uint64_t *empty = full + kFfMaxStages;
-    uint64_t *rows_full = empty + kFfMaxStages;           // this CTA's rows landed
+    uint64_t *rows_full = empty + kFfMaxStages;           // the peer's rows landed
     uint64_t *acc_full = rows_full + kFfMaxStages;
     uint64_t *acc_empty = acc_full + kRowAccs;
     uint64_t *info_full = acc_empty + kRowAccs;
@@ -311,7 +311,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(smem_u32(&full[s]), kCtas);
+            mbar_init(smem_u32(&full[s]), 16 * kRowLoaders + kCtas);
             mbar_init(smem_u32(&rows_full[s]), 16 * kRowLoaders);
             mbar_init(smem_u32(&empty[s]), 2);  // either tile's MMAs
         }
@@ -389,9 +389,8 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     uint64_t *done = &acc_full[2 * ac.i + warp];
                     // (the accumulator last: it is what is waited for longest,
                     // and each wait takes 150 cycles)
-                    if (!(ok = warp_wait(&rows_full[st.i], st.ph, abort_flag))) break;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     if (!(ok = warp_wait(&acc_empty[2 * ac.i + warp], ac.ph ^ 1u, abort_flag))) break;
                     tc_fence_after();
                     const uint32_t base = ring + (uint32_t)(st.i * kStageBytes), acc = tmem + (uint32_t)((2 * ac.i + warp) * 128);
@@ -502,6 +501,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             const int c = lane & 7, r0 = 64 * (warp & 1) + (lane >> 3);  // rows r0 + 4 i
             const uint32_t to0 = ring + (uint32_t)(r0 * kFfRowBytes + ((c ^ (lane >> 3)) << 4));
             const uint32_t to1 = ring + (uint32_t)(r0 * kFfRowBytes + ((c ^ (4 + (lane >> 3))) << 4));
+            const uint32_t landed = smem_u32(rank == 0 ? full : rows_full);
             const bool elected = elect_one();
             RingPos st, iq;
             int next = (warp - 4) >> 1;  // the next stage of these two, counted from the item's first
@@ -547,7 +547,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                         for (int i = 0; i < 16; ++i)
                             cp_async_16((i & 1 ? to1 : to0) + base + (uint32_t)(i * 4 * kFfRowBytes),
                                         x + (uint64_t)(uint32_t)row[i] * p.x_row_bytes, some ? row[i] : -1);
-                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&rows_full[st.i])) : "memory");
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(landed + 8u * st.i) : "memory");
                         st.skip(2, ST);
                     }
                     if (ok) next -= p.num_kb;
