@@ -45,17 +45,24 @@ namespace smr {
 // either tile, 2 scout, 3 scales, 4 to 7 load the routed rows and the weights
 // (two warps every other stage), the last 8 are the epilogue, two for each
 // quarter of TMEM's lanes, one of these for either tile.
-constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 4;
+constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 2;
 template <bool PAIR>
 constexpr int kRowStageBytes = (PAIR ? 2 : 3) * kFfWBytes;  // [rows][the first tile, or half of it][the second]
 constexpr int kRowScaleBytes = kFp8Group * 128 * 8;  // [k-block][row] (two products of scales)
 // The epilogue's outputs leave through shared memory, 128 bytes of 32 rows a
-// warp at a time, so that rows are written in whole lines. Where that leaves
-// three stages only, the gated product of single CTAs, it is 16 rows, and the
-// ring of scales is half as long: four stages (4096 tokens: 152 us, with three
-// 157; the second product, with twice the outputs, takes 127 instead of 125).
+// warp at a time, so that rows are written in whole lines. Where that would leave
+// three stages only, in single CTAs, it is 16 rows, and the ring of scales is
+// half as long. Four are the least that are sound: either issuing warp, and either
+// pair of loaders, takes every other k-block, and a parity wait tells a stage's
+// last use from the one before only. Who waits for k-block j's use of a stage must
+// know that the use before, j - ST, has been filled (issuing), or the one before
+// that, j - 2 ST, consumed (loading). An issuing warp at j has issued j - 2, so the
+// epilogue handed back j - 4, and with it, in order, all before: j - ST <= j - 4. A
+// loader at j has waited for j - 2 - ST to be consumed, before which j - 4 - ST and
+// all before were handed back: j - 2 ST <= j - 4 - ST.
+constexpr int kRowLeastStages = 4;
 template <bool UP, bool PAIR>
-constexpr bool kRowLean = UP && !PAIR;
+constexpr bool kRowLean = !PAIR;
 template <bool UP, bool PAIR>
 constexpr int kRowScales = kRowLean<UP, PAIR> ? 2 : 4;
 template <bool UP, bool PAIR>
@@ -313,11 +320,11 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(smem_u32(&full[s]), 16 * kRowLoaders + kCtas);
             mbar_init(smem_u32(&rows_full[s]), 16 * kRowLoaders);
-            mbar_init(smem_u32(&empty[s]), 2);  // either tile's MMAs
+            mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int s = 0; s < kRowAccs; ++s) {
             mbar_init(smem_u32(&acc_full[s]), 1);
-            mbar_init(smem_u32(&acc_empty[s]), kCtas * kFfDrains / 2);  // one tile's four warps (of both CTAs)
+            mbar_init(smem_u32(&acc_empty[s]), kCtas * kFfDrains);
         }
         for (int s = 0; s < kRowInfos; ++s) {
             mbar_init(smem_u32(&info_full[s]), 1);
@@ -357,14 +364,15 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp < 2) {
             // --------------------------------------------------- MMAs ----
-            // A warp for either tile: its k-blocks in turn into two
-            // accumulators. (From an accumulator's last MMA to the next one's
-            // first in it the signals between the CTAs take 1100 cycles
-            // without any work in between, a tile's MMAs 256; and a k-block's
-            // waits, issue and commits take a warp 600.)
+            // The two warps take k-blocks in turn, each into accumulators of its
+            // own: what a k-block's waits, fence, issue and commits take a warp,
+            // some 600 cycles, is more than the tensor core needs.
             const bool elected = elect_one();
             const uint32_t idesc = idesc_e4m3(kCtas * kFfRows, 128);
-            RingPos st, iq, ac;
+            RingPos st, iq;
+            uint32_t turn = 1u;  // parity of the accumulators' last hand-back
+            int next = rank == 0 ? warp : 0;  // this warp's next k-block, counted from the item's first
+            st.skip(next, ST);
             bool ok = true;
             while (ok) {
                 if (!(ok = warp_wait(&info_full[iq.i], iq.ph, abort_flag))) break;
@@ -385,29 +393,32 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                     }
                     continue;
                 }
-                for (int kb = 0; kb < p.num_kb; ++kb) {
-                    uint64_t *done = &acc_full[2 * ac.i + warp];
-                    // (the accumulator last: it is what is waited for longest,
+                for (; next < p.num_kb; next += 2) {
+                    // (the accumulators last: they are what is waited for longest,
                     // and each wait takes 150 cycles)
                     if (!(ok = warp_wait(&full[st.i], st.ph, abort_flag))) break;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    if (!(ok = warp_wait(&acc_empty[2 * ac.i + warp], ac.ph ^ 1u, abort_flag))) break;
+                    if (!(ok = warp_wait(&acc_empty[warp], turn, abort_flag))) break;
                     tc_fence_after();
-                    const uint32_t base = ring + (uint32_t)(st.i * kStageBytes), acc = tmem + (uint32_t)((2 * ac.i + warp) * 128);
-                    const uint64_t da = smem_desc_sw<128>(base), db = smem_desc_sw<128>(base + kFfWBytes + warp * kTileBytes);
-                    const int steps = kb + 1 == p.num_kb ? p.last_steps : 4;
+                    const uint32_t base = ring + (uint32_t)(st.i * kStageBytes), acc = tmem + (uint32_t)(warp * 256);
+                    const uint64_t da = smem_desc_sw<128>(base), db = smem_desc_sw<128>(base + kFfWBytes),
+                                   db2 = smem_desc_sw<128>(base + kFfWBytes + kTileBytes);
+                    const int steps = next + 1 == p.num_kb ? p.last_steps : 4;
                     if (elected) {
                         if (steps == 4) {
                             mma_k_block<PAIR>(acc, da, db, idesc);
+                            mma_k_block<PAIR>(acc + 128u, da, db2, idesc);
                         } else {
                             for (int kk = 0; kk < steps; ++kk) tc_mma_e4m3<PAIR>(acc, da + 2 * kk, db + 2 * kk, idesc, kk ? 1u : 0u);
+                            for (int kk = 0; kk < steps; ++kk) tc_mma_e4m3<PAIR>(acc + 128u, da + 2 * kk, db2 + 2 * kk, idesc, kk ? 1u : 0u);
                         }
-                        ff_commit<PAIR>(done);
-                        ff_commit<PAIR>(&empty[st.i]);
+                        ff_commit<PAIR>(&empty[st.i]);  // (before the epilogue can know, see kRowLeastStages)
+                        ff_commit<PAIR>(&acc_full[warp]);
                     }
-                    st.next(ST);
-                    ac.next(2);
+                    st.skip(2, ST);
+                    turn ^= 1u;
                 }
+                if (ok) next -= p.num_kb;
             }
             // every MMA issued is done before TMEM is freed, also after an abort
             if (rank == 0) {
@@ -574,7 +585,7 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
                            kScaleEmpty = kScaleFull + 8 * kScaleRing, kAbort = kScaleEmpty + 8 * kScaleRing + 12,
                            kInfo = kBars, kScales = kInfo + kRowInfos * (uint32_t)sizeof(Info),
                            kOutRows = kScales + kScaleRing * kRowScaleBytes;
-        const uint32_t hand_back = PAIR ? cluster_addr(at + kAccEmpty + 8u * half, 0u) : at + kAccEmpty + 8u * half;
+        const uint32_t hand_back = PAIR ? cluster_addr(at + kAccEmpty, 0u) : at + kAccEmpty;
         const uint32_t from = tmem + ((uint32_t)(q * 32) << 16) + 128u * half, scales = at + kScales + 8u * (q * 32 + lane) + (UP ? 0u : 4u * half);
         uint32_t items = 0, groups = 0, units = 0;
         while (true) {
@@ -603,14 +614,14 @@ expert_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const FfParams p) {
             }
 #pragma unroll 1
             for (int kb = more ? 0 : p.num_kb; kb < p.num_kb;) {
-                ok &= warp_wait_at(at + kAccFull + 8u * half + 16u * (units & 1u), units >> 1 & 1u, at + kAbort);
+                ok &= warp_wait_at(at + kAccFull + 8u * (units & 1u), units >> 1 & 1u, at + kAbort);
                 tc_fence_after();
                 float last[32];
                 const float g0 = g, u0 = u;
                 add_columns(sum, last, from + 256u * (units & 1u), g0, u0);
                 tc_fence_before();
-                if constexpr (PAIR) arrive_cluster_if(hand_back + 16u * (units & 1u), lane == 0);
-                else arrive_if(hand_back + 16u * (units & 1u), lane == 0);
+                if constexpr (PAIR) arrive_cluster_if(hand_back + 8u * (units & 1u), lane == 0);
+                else arrive_if(hand_back + 8u * (units & 1u), lane == 0);
                 ++units;
                 ++kb;
                 if ((kb & (kFp8Group - 1)) == 0 || kb == p.num_kb) {
@@ -740,6 +751,7 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
     p.scale_bytes = scales_at % 16 == 0 ? 16 : (scales_at % 8 == 0 ? 8 : 4);
     constexpr uint32_t kSmemMax = 232448;
     p.stages = (int)((kSmemMax - 1024 - kRowMiscBytes<UP, PAIR>) / kRowStageBytes<PAIR>);
+    static_assert((kSmemMax - 1024 - kRowMiscBytes<UP, PAIR>) / kRowStageBytes<PAIR> >= kRowLeastStages, "see kRowLeastStages");
     if (p.stages > kFfMaxStages) p.stages = kFfMaxStages;
     const size_t smem = 1024 + (size_t)p.stages * kRowStageBytes<PAIR> + kRowMiscBytes<UP, PAIR>;
     CUtensorMap mw;
