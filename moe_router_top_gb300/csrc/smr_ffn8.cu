@@ -13,19 +13,21 @@
 // from shared memory by all threads, and these reads bound the kernel (16384
 // tokens, gated product: 787 us). So here the routed rows are the MMA's rows: a
 // thread of the epilogue holds one row, its scale is one register, and a weight
-// tile's is the same for all (467 us, 1.77 PFLOP/s, in CTA pairs).
+// tile's is the same for all (428 us, 1.93 PFLOP/s, in CTA pairs).
 //
 // What bounds that (us for the gated product of 16384 tokens, parts taken out in
-// turn): the chain from an accumulator's MMAs over the signals between the CTAs
-// to the epilogue and back takes 305 without the adds and the outputs, of which
-// the tensor core works 200; the adds, one an element, scheduler and cycle, 100;
-// the outputs 65; the row copies 18; the loads from TMEM nothing. Measured and
-// not better: one accumulator of 256 columns a k-block (493 us), sixteen warps
-// in the epilogue (491; the others are then short of registers), packed adds of
-// two (a pair takes two cycles), one warp issuing both tiles' MMAs (531), a warp
-// for every accumulator (536), copies that a warp waits for and makes visible
-// before it announces them (531), the stages handed back by the epilogue (463,
-// the second product 25 longer).
+// turn when it took 468 to 480): the chain of signals from an issuing warp to the
+// epilogue and back took 300 without the adds and the outputs, of which the
+// tensor core works 200; the adds, one an element, scheduler and cycle, 95; the
+// outputs 55 to 80; the row copies 18; the loads from TMEM and of the weights 10
+// each. An issuing warp's own waits, fence and commits were the longest link: one
+// wait less took the 468 to 437, two warps in turn that to 428. Measured before
+// that and not better: one accumulator of 256 columns a k-block (493 us), sixteen
+// warps in the epilogue (491; the others are then short of registers), packed
+// adds of two (a pair takes two cycles), one warp issuing all (531), a warp for
+// every accumulator (536), copies that a warp waits for and makes visible before
+// it announces them (531), the stages handed back by the epilogue (463, the
+// second product 25 longer).
 #include "smr_fp8.cuh"
 #include "smr_launch.h"
 
@@ -41,8 +43,8 @@ namespace smr {
 
 // A piece of work: two weight tiles and up to 128 routed rows (blocks of one
 // expert together) for a CTA, or up to 256 for a CTA pair, where either CTA holds
-// half of the rows and half of each tile. 16 warps: 0 and 1 issue the MMAs of
-// either tile, 2 scout, 3 scales, 4 to 7 load the routed rows and the weights
+// half of the rows and half of each tile. 16 warps: 0 and 1 issue the MMAs, every
+// other k-block, 2 scout, 3 scales, 4 to 7 load the routed rows and the weights
 // (two warps every other stage), the last 8 are the epilogue, two for each
 // quarter of TMEM's lanes, one of these for either tile.
 constexpr int kRowLoaders = 4, kRowThreads = 512, kRowInfos = 4, kRowAccs = 2;
@@ -794,10 +796,11 @@ static cudaError_t launch_rows(const FfnLaunch &a, int sms, cudaStream_t stream)
 // From this many rows an expert, on average, the routed rows are the MMA's rows.
 // An item then costs the same for 16 rows as for 128, but its scales are one
 // register. H 2048, 128 experts, top-8, I 768; the gated product in us on the
-// device, evenly spread and skewed (weights as the MMA's rows / routed rows): 512
-// tokens (32 rows) 70 and 80 / 81 and 81, 768 tokens (48) 93 and 107 / 81 and
-// 83, 1536 tokens 125 and 140 / 86 and 103; the second product 56 and 63 / 64
-// and 68, 58 and 65 / 52 and 56, 77 and 86 / 62 and 73.
+// device, evenly spread and skewed (weights as the MMA's rows / routed rows, as
+// measured before the last two steps above): 512 tokens (32 rows) 70 and 80 / 81
+// and 81, 768 tokens (48) 93 and 107 / 81 and 83, 1536 tokens 125 and 140 / 86 and
+// 103; the second product 56 and 63 / 64 and 68, 58 and 65 / 52 and 56, 77 and 86 /
+// 62 and 73.
 constexpr int kRowsPerExpert = 48;
 // In blocks of 128 rows, where a stage of two k-blocks does not fit and its
 // columns take a turn each, from fewer (both products, the activations quantised
@@ -810,7 +813,8 @@ bool expert_rows_fp8(int64_t numel, int num_experts, int A) {
 
 // And from this many a CTA pair takes up to 256 of them: each CTA then loads half
 // of the weight tiles, but pieces of 128 rows leave half of its lanes idle and
-// the signals between the CTAs take their time (pairs / single CTAs, us: the gated
+// the signals between the CTAs take their time (pairs / single CTAs, us, before the
+// last two steps: the gated
 // product of 4096 tokens, 256 rows, 166 and 179 / 152 and 157, 8192 tokens 271
 // and 268 / 261 and 261, 12000 tokens 344 and 360 / 360 and 367, 16384 tokens 468
 // and 466 / 480 and 477; the second product of 4096 tokens 133 and 137 / 126 and
